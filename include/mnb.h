@@ -731,6 +731,125 @@ MNB_API mnb_status mnb_graph_run_from_host(mnb_graph graph, const void *in_host,
 /* Frees the graph (host objects). Errors: MNB_ERR_NULL. */
 MNB_API mnb_status mnb_graph_destroy(mnb_graph graph);
 
+/*
+ * Mixture-of-experts layer on packed 4-bit weights (page "Qwen3 CPU Inference
+ * Critical Path", com.microsoft operator inventory: MoE / QMoE beside
+ * MatMulNBits; the page names the operators only, the conventions below are
+ * this library's).
+ *
+ * Token m has top_k choices among E experts. "Slot" p = m * top_k + j is its
+ * choice j: an expert index and a weight.
+ *
+ * mnb_experts describes E weights N x K of one kind, packed together by
+ * mnb_prepack_experts (HOST struct, DEVICE pointers inside).
+ */
+#define MNB_MOE_MAX_EXPERTS 1024
+#define MNB_MOE_MAX_TOP_K 32
+
+typedef struct {
+  const void *packed_b;      /* from mnb_prepack_experts                      */
+  const void *packed_scales;
+  const void *packed_zp;     /* NULL: every zero point is 8                   */
+  const float *bias;         /* [E, N] fp32 or NULL                           */
+  int64_t E, N, K;
+  int32_t block_size;
+  int32_t scale_dtype;       /* mnb_dtype                                     */
+} mnb_experts;
+
+/*
+ * Offline re-layout of a stack of E MatMulNBits weights: B [E, N, nb, bs/2],
+ * scales [E, N, nb], zero_points [E, N, ceil(nb/2)] or NULL, each expert as
+ * mnb_prepack reads one weight. Every expert's rows are padded to a whole
+ * number of 16-row tiles (zero codes and scales), so the packed stack is an
+ * ordinary packed weight of E * Np rows, Np = N rounded up to a multiple of
+ * 16: its buffers have the sizes mnb_prepacked_sizes(E * Np, K, ...) gives
+ * and its header says so (for N % 16 == 0 the bytes are those of mnb_prepack
+ * on the E * N rows). Arguments and errors as mnb_prepack; MNB_ERR_SHAPE
+ * also for E < 1 and when E * Np passes 2^31 - 1.
+ */
+MNB_API mnb_status mnb_prepack_experts(const uint8_t *B, const void *scales,
+                                       const uint8_t *zero_points, int64_t E, int64_t N,
+                                       int64_t K, int block_size, mnb_dtype scale_dtype,
+                                       void *packed_b, void *packed_scales, void *packed_zp,
+                                       mnb_stream_t stream);
+
+/*
+ * Top-k softmax router. For each row l of logits [M, E] (fp32 or bf16) the
+ * top_k largest are chosen, largest first, ties going to the lowest index;
+ * with p_e = exp(l_e - max l), choice j has the weight
+ *   normalize = 1: p_j / (sum of p over the chosen),
+ *   normalize = 0: p_j / (sum of p over all E).
+ * A logit of -inf or NaN masks its expert: it is never chosen and adds
+ * nothing to a sum. Choices for which no expert is left (all of them in a
+ * fully masked row) are expert -1 with weight 0. A logit of +inf has p = 1
+ * (shared with other +inf), finite ones beside it p = 0.
+ *  weights  fp32 [M, top_k]; experts int32 [M, top_k].
+ *  offsets, order: both NULL, or int32 [E + 1] and [M * top_k]: the slots
+ *    sorted by expert, those of expert e at order[offsets[e] ..
+ *    offsets[e+1]) in increasing order; slots without an expert come after
+ *    offsets[E].
+ *  workspace: mnb_moe_route_workspace_size(M, E, top_k) bytes of DEVICE
+ *    memory, 256-byte aligned (NULL when that is 0); its contents need no
+ *    preparation and mean nothing afterwards. Calls that may overlap on the
+ *    GPU (two streams, or graphs replayed side by side) need one each.
+ * Results are exact in the choice and bitwise reproducible.
+ * Errors: MNB_ERR_NULL (also for one of offsets and order without the
+ * other), MNB_ERR_SHAPE (M or E < 1, top_k < 1 or > E, M * top_k past
+ * 2^31 - 1, normalize not 0/1, workspace too small), MNB_ERR_DTYPE,
+ * MNB_ERR_UNSUPPORTED (E > MNB_MOE_MAX_EXPERTS, top_k > MNB_MOE_MAX_TOP_K),
+ * MNB_ERR_ALIGN, MNB_ERR_ALIAS (an output or the workspace overlaps another
+ * buffer), MNB_ERR_DEVICE, MNB_ERR_CUDA.
+ */
+MNB_API size_t mnb_moe_route_workspace_size(int64_t M, int64_t E, int top_k);
+MNB_API mnb_status mnb_moe_route(const void *logits, mnb_dtype logits_dtype, int64_t M,
+                                 int64_t E, int top_k, int normalize, float *weights,
+                                 int32_t *experts, int32_t *offsets, int32_t *order,
+                                 void *workspace, size_t workspace_bytes, mnb_stream_t stream);
+
+/*
+ * Products whose weight each slot picks from a stack of experts:
+ *   Y[m,j,:] = A[m,:] * dequant(W[e])^T + bias[e]   (a_per_slot = 0)
+ *   Y[m,j,:] = A[m,j,:] * dequant(W[e])^T + bias[e] (a_per_slot = 1)
+ * with e = experts[m,j]; an e outside 0 .. E-1 (the router's -1) names no
+ * expert and gives a row of zeros. The same expert may appear in a row more
+ * than once.
+ *  A [M, K] or [M, top_k, K] and Y [M, top_k, N] in a_dtype; experts int32
+ *  [M, top_k] DEVICE; w HOST.
+ *  workspace: as mnb_moe_route's, of mnb_matmul_experts_workspace_size
+ *  bytes (0 for arguments the call refuses).
+ * Accumulation is fp32. Errors: as mnb_matmul, and MNB_ERR_SHAPE for top_k
+ * < 1, M * top_k past 2^31 - 1 or a workspace too small,
+ * MNB_ERR_UNSUPPORTED for E > MNB_MOE_MAX_EXPERTS.
+ */
+MNB_API size_t mnb_matmul_experts_workspace_size(int64_t M, int top_k, const mnb_experts *w,
+                                                 mnb_dtype a_dtype, int a_per_slot);
+MNB_API mnb_status mnb_matmul_experts(const void *A, int a_per_slot, const mnb_experts *w,
+                                      const int32_t *experts, int64_t M, int top_k, void *Y,
+                                      mnb_dtype a_dtype, void *workspace,
+                                      size_t workspace_bytes, mnb_stream_t stream);
+
+/*
+ * The whole layer on router logits [M, E]: with the choices e_j and weights
+ * r_j of mnb_moe_route,
+ *   Y[m] = sum_j r_j * (Wd_e h_j + bd_e),
+ *   h_j  = silu(Wg_e X[m] + bg_e) * (Wu_e X[m] + bu_e),  silu(x) = x sigmoid(x).
+ *  X, Y [M, H] in a_dtype; gate, up: stacks of E weights I x H with the same
+ *  block size, scale dtype and zero-point presence; down: a stack of E
+ *  weights H x I. A token without an expert gets a row of zeros.
+ *  workspace: as mnb_moe_route's, of mnb_moe_workspace_size bytes (0 for
+ *  arguments the call refuses).
+ * Accumulation is fp32. Errors: as mnb_moe_route and mnb_matmul_experts;
+ * MNB_ERR_SHAPE when the three stacks do not fit together.
+ */
+MNB_API size_t mnb_moe_workspace_size(int64_t M, int top_k, const mnb_experts *gate,
+                                      const mnb_experts *up, const mnb_experts *down,
+                                      mnb_dtype a_dtype);
+MNB_API mnb_status mnb_moe(const void *X, const void *logits, mnb_dtype logits_dtype, int64_t M,
+                           int top_k, int normalize, const mnb_experts *gate,
+                           const mnb_experts *up, const mnb_experts *down, void *Y,
+                           mnb_dtype a_dtype, void *workspace, size_t workspace_bytes,
+                           mnb_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

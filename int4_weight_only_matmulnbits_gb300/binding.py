@@ -7,10 +7,12 @@ immediately; there is no fallback implementation.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
 from dataclasses import dataclass
+from typing import NamedTuple
 
 import torch
 
@@ -43,7 +45,10 @@ EXPORTS = ("mnb_status_string", "mnb_last_error_string", "mnb_version",
            "mnb_matmul_workspace_size", "mnb_matmul_ws", "mnb_matmul_plan",
            "mnb_packed_header_make", "mnb_packed_register", "mnb_packed_read_header",
            "mnb_packed_forget", "mnb_graph_build", "mnb_graph_info", "mnb_graph_run",
-           "mnb_graph_run_from_host", "mnb_graph_destroy", "mnb_test_wait_fault")
+           "mnb_graph_run_from_host", "mnb_graph_destroy", "mnb_test_wait_fault",
+           "mnb_prepack_experts", "mnb_moe_route_workspace_size", "mnb_moe_route",
+           "mnb_matmul_experts_workspace_size", "mnb_matmul_experts",
+           "mnb_moe_workspace_size", "mnb_moe")
 
 _lock = threading.Lock()
 _lib = None
@@ -86,6 +91,14 @@ class ChainInfoC(ctypes.Structure):
                                       "has_zero_points", "ring_stages", "k_max",
                                       "tiles_per_segment", "ctas_per_sm")] + [
         ("check", ctypes.c_uint64)]
+
+
+class ExpertsC(ctypes.Structure):
+    """mnb_experts (include/mnb.h)."""
+    _fields_ = [("packed_b", ctypes.c_void_p), ("packed_scales", ctypes.c_void_p),
+                ("packed_zp", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("E", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
+                ("block_size", ctypes.c_int32), ("scale_dtype", ctypes.c_int32)]
 
 
 class MnbError(RuntimeError):
@@ -196,6 +209,21 @@ def load(build_if_missing: bool = False):
         lib.mnb_prepack_bnb4.restype = i32
         lib.mnb_matmul_bnb4.argtypes = [p, p, p, p, p, i64, i64, i64, i32, p, i32, i32, p]
         lib.mnb_matmul_bnb4.restype = i32
+        e = ctypes.POINTER(ExpertsC)
+        lib.mnb_prepack_experts.argtypes = [p, p, p, i64, i64, i64, i32, i32, p, p, p, p]
+        lib.mnb_prepack_experts.restype = i32
+        lib.mnb_moe_route_workspace_size.argtypes = [i64, i64, i32]
+        lib.mnb_moe_route_workspace_size.restype = sz
+        lib.mnb_moe_route.argtypes = [p, i32, i64, i64, i32, i32, p, p, p, p, p, sz, p]
+        lib.mnb_moe_route.restype = i32
+        lib.mnb_matmul_experts_workspace_size.argtypes = [i64, i32, e, i32, i32]
+        lib.mnb_matmul_experts_workspace_size.restype = sz
+        lib.mnb_matmul_experts.argtypes = [p, i32, e, p, i64, i32, p, i32, p, sz, p]
+        lib.mnb_matmul_experts.restype = i32
+        lib.mnb_moe_workspace_size.argtypes = [i64, i32, e, e, e, i32]
+        lib.mnb_moe_workspace_size.restype = sz
+        lib.mnb_moe.argtypes = [p, p, i32, i64, i32, i32, e, e, e, p, i32, p, sz, p]
+        lib.mnb_moe.restype = i32
         _lib = lib
         return lib
 
@@ -717,4 +745,186 @@ def mnb_matmul_bnb4(A: torch.Tensor, w: PackedWeight, code: torch.Tensor,
                                   w.block_size, _ptr(out), _dtype_code(A.dtype),
                                   _dtype_code(w.scale_dtype), _stream(stream)),
            "mnb_matmul_bnb4")
+    return out
+
+
+# ---- mixture of experts ---------------------------------------------------------
+
+@dataclass
+class PackedExperts:
+    """Caller-owned prepacked buffers of a stack of E weights N x K."""
+    packed_b: torch.Tensor
+    packed_scales: torch.Tensor
+    packed_zp: torch.Tensor | None
+    E: int
+    N: int
+    K: int
+    block_size: int
+    scale_dtype: torch.dtype
+
+    def nbytes(self) -> int:
+        return sum(t.numel() * t.element_size() for t in
+                   (self.packed_b, self.packed_scales, self.packed_zp) if t is not None)
+
+
+class MoeRouting(NamedTuple):
+    """What mnb_moe_route returns (include/mnb.h)."""
+    weights: torch.Tensor  # fp32 [M, top_k]
+    experts: torch.Tensor  # int32 [M, top_k], -1: no expert left
+    offsets: torch.Tensor  # int32 [E + 1]
+    order: torch.Tensor    # int32 [M * top_k]: the slots m * top_k + j by expert
+
+
+def _on_gpu(name: str, t: torch.Tensor, device: torch.device | None = None) -> None:
+    """A contiguous CUDA tensor, on `device` when given."""
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the call runs on {device}")
+
+
+@contextlib.contextmanager
+def _call_on(device: torch.device, stream):
+    """Makes `device` current and yields the call's stream handle, with torch's
+    allocations (outputs, workspace) made for that stream: the caller's, or the
+    device's current one. The caller orders `stream` with the work that made
+    the inputs and that reads the outputs."""
+    with torch.cuda.device(device):
+        if stream is None:
+            yield ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+        else:
+            if stream.device != device:
+                raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+            with torch.cuda.stream(stream):
+                yield ctypes.c_void_p(stream.cuda_stream)
+
+
+def _workspace(n: int, device: torch.device) -> torch.Tensor | None:
+    """n bytes for one call. Freed on return to torch's allocator, which hands
+    the memory out again on the same stream only, after the call's kernels."""
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def _experts_struct(w: PackedExperts, bias: torch.Tensor | None, device) -> ExpertsC:
+    _on_gpu("packed_b", w.packed_b, device)
+    if bias is not None:
+        _on_gpu("bias", bias, device)
+        if bias.dtype != torch.float32 or bias.shape != (w.E, w.N):
+            raise ValueError(f"bias must be an fp32 [{w.E}, {w.N}] tensor")
+    ptr = lambda t: None if t is None else t.data_ptr()
+    return ExpertsC(w.packed_b.data_ptr(), w.packed_scales.data_ptr(), ptr(w.packed_zp),
+                    ptr(bias), w.E, w.N, w.K, w.block_size, _dtype_code(w.scale_dtype))
+
+
+def mnb_prepack_experts(B: torch.Tensor, scales: torch.Tensor,
+                        zero_points: torch.Tensor | None, N: int, K: int, block_size: int, *,
+                        stream=None) -> PackedExperts:
+    """Prepack a stack of weights in MatMulNBits layout (device tensors): B
+    [E, N, nb, bs/2], scales [E, N, nb], zero_points [E, N, ceil(nb/2)]."""
+    nb = -(-K // block_size)
+    E = B.shape[0]
+    for name, t, shape in (("B", B, (E, N, nb, block_size // 2)), ("scales", scales, (E, N, nb)),
+                           ("zero_points", zero_points, (E, N, (nb + 1) // 2))):
+        if t is not None:
+            _on_gpu(name, t, B.device)
+            if t.shape != shape or (name != "scales" and t.dtype != torch.uint8):
+                raise ValueError(f"{name} must have the shape {shape}"
+                                 + ("" if name == "scales" else " and uint8 elements"))
+    sb, ss, sz = mnb_prepacked_sizes(E * (-(-N // 16) * 16), K, block_size, scales.dtype,
+                                     zero_points is not None)
+    with _call_on(B.device, stream) as s:
+        pb, ps = (torch.empty(n, dtype=torch.uint8, device=B.device) for n in (sb, ss))
+        pz = (torch.empty(sz, dtype=torch.uint8, device=B.device)
+              if zero_points is not None else None)
+        _check(load().mnb_prepack_experts(_ptr(B), _ptr(scales), _ptr(zero_points), E, N, K,
+                                          block_size, _dtype_code(scales.dtype), _ptr(pb),
+                                          _ptr(ps), _ptr(pz), s), "mnb_prepack_experts")
+    return PackedExperts(pb, ps, pz, E, N, K, block_size, scales.dtype)
+
+
+def mnb_moe_route(logits: torch.Tensor, top_k: int, *, normalize: bool = True,
+                  stream=None) -> MoeRouting:
+    """Top-k softmax router of logits [M, E]: weights and experts [M, top_k],
+    and the slots m * top_k + j listed by expert (offsets, order). -inf and NaN
+    mask an expert; choices without one left are expert -1, weight 0."""
+    if logits.dim() != 2:
+        raise ValueError("logits must be [M, E]")
+    _on_gpu("logits", logits)
+    M, E = logits.shape
+    lib, dev = load(), logits.device
+    with _call_on(dev, stream) as s:
+        weights = torch.empty(M, top_k, dtype=torch.float32, device=dev)
+        experts = torch.empty(M, top_k, dtype=torch.int32, device=dev)
+        offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
+        order = torch.empty(M * top_k, dtype=torch.int32, device=dev)
+        n = lib.mnb_moe_route_workspace_size(M, E, top_k)
+        ws = _workspace(n, dev)
+        _check(lib.mnb_moe_route(_ptr(logits), _dtype_code(logits.dtype), M, E, top_k,
+                                 1 if normalize else 0, _ptr(weights), _ptr(experts),
+                                 _ptr(offsets), _ptr(order), _ptr(ws), n, s), "mnb_moe_route")
+    return MoeRouting(weights, experts, offsets, order)
+
+
+def mnb_matmul_experts(A: torch.Tensor, w: PackedExperts, experts: torch.Tensor,
+                       bias: torch.Tensor | None = None, *, out: torch.Tensor | None = None,
+                       stream=None) -> torch.Tensor:
+    """Y[m, j] = A[m] (or A[m, j]) @ dequant(w[experts[m, j]])^T + bias[...]:
+    A [M, K] or [M, top_k, K], experts int32 [M, top_k] (an index outside
+    0 .. E-1 names none: a row of zeros), bias fp32 [E, N]; Y [M, top_k, N]."""
+    dev = A.device
+    _on_gpu("A", A)
+    _on_gpu("experts", experts, dev)
+    if experts.dim() != 2 or experts.dtype != torch.int32:
+        raise ValueError("experts must be an int32 [M, top_k] tensor")
+    M, top_k = experts.shape
+    per_slot = A.dim() == 3
+    if A.shape != ((M, top_k, w.K) if per_slot else (M, w.K)):
+        raise ValueError(f"A must be [{M}, {w.K}] or [{M}, {top_k}, {w.K}]")
+    lib, code = load(), _dtype_code(A.dtype)
+    c = _experts_struct(w, bias, dev)
+    with _call_on(dev, stream) as s:
+        if out is None:
+            out = torch.empty(M, top_k, w.N, dtype=A.dtype, device=dev)
+        else:
+            _on_gpu("out", out, dev)
+            if out.shape != (M, top_k, w.N) or out.dtype != A.dtype:
+                raise ValueError(f"out must be a [{M}, {top_k}, {w.N}] tensor of A's dtype")
+        n = lib.mnb_matmul_experts_workspace_size(M, top_k, c, code, per_slot)
+        ws = _workspace(n, dev)
+        _check(lib.mnb_matmul_experts(_ptr(A), per_slot, c, _ptr(experts), M, top_k, _ptr(out),
+                                      code, _ptr(ws), n, s), "mnb_matmul_experts")
+    return out
+
+
+def mnb_moe(X: torch.Tensor, logits: torch.Tensor, gate: PackedExperts, up: PackedExperts,
+            down: PackedExperts, top_k: int, *, normalize: bool = True,
+            bias_gate: torch.Tensor | None = None, bias_up: torch.Tensor | None = None,
+            bias_down: torch.Tensor | None = None, out: torch.Tensor | None = None,
+            stream=None) -> torch.Tensor:
+    """The whole mixture-of-experts layer: route each token of X [M, H] by its
+    logits [M, E] (as mnb_moe_route) and return the weighted sum of its
+    experts' gated MLPs, down(silu(gate x) * (up x)), [M, H]."""
+    dev = X.device
+    _on_gpu("X", X)
+    _on_gpu("logits", logits, dev)
+    if X.dim() != 2 or X.shape[1] != gate.K:
+        raise ValueError(f"X must be [M, {gate.K}]")
+    M = X.shape[0]
+    if logits.shape != (M, gate.E):
+        raise ValueError(f"logits must be [{M}, {gate.E}]")
+    lib, code = load(), _dtype_code(X.dtype)
+    g, u, d = (_experts_struct(w, b, dev) for w, b in
+               ((gate, bias_gate), (up, bias_up), (down, bias_down)))
+    with _call_on(dev, stream) as s:
+        if out is None:
+            out = torch.empty_like(X)
+        else:
+            _on_gpu("out", out, dev)
+            if out.shape != X.shape or out.dtype != X.dtype:
+                raise ValueError(f"out must be a [{M}, {gate.K}] tensor of X's dtype")
+        n = lib.mnb_moe_workspace_size(M, top_k, g, u, d, code)
+        ws = _workspace(n, dev)
+        _check(lib.mnb_moe(_ptr(X), _ptr(logits), _dtype_code(logits.dtype), M, top_k,
+                           1 if normalize else 0, g, u, d, _ptr(out), code, _ptr(ws), n, s),
+               "mnb_moe")
     return out

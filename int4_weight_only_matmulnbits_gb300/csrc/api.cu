@@ -13,6 +13,7 @@
 #include "../../include/mnb.h"
 #include "mnb_common.cuh"
 #include "mnb_launch.h"
+#include "moe.h"
 
 namespace mnb {
 
@@ -300,6 +301,146 @@ mnb_status run_matmul(const void *A, const void *packed_b, const void *scales,
   }
   if (e != cudaSuccess) return cuda_fail(e, "mnb_matmul");
   return MNB_OK;
+}
+
+// ---- mixture of experts: checks ------------------------------------------------
+
+// Rows of one expert in a packed stack.
+int64_t padded_rows(int64_t N) { return ceil_div(N, kTileN) * kTileN; }
+
+mnb_status check_slots(int64_t M, int top_k) {
+  if (M < 1 || M > kMaxDim || top_k < 1 || M > kMaxDim / top_k) return MNB_ERR_SHAPE;
+  return MNB_OK;
+}
+
+mnb_status check_route(int64_t M, int64_t E, int top_k) {
+  const mnb_status st = check_slots(M, top_k);
+  if (st != MNB_OK) return st;
+  if (E < 1 || E > kMaxDim || top_k > E) return MNB_ERR_SHAPE;
+  if (E > kMoeMaxExperts || top_k > kMoeMaxTopK) {
+    std::snprintf(g_last_error, sizeof g_last_error,
+                  "E=%lld top_k=%d: at most %d experts and %d choices", (long long)E, top_k,
+                  kMoeMaxExperts, kMoeMaxTopK);
+    return MNB_ERR_UNSUPPORTED;
+  }
+  return MNB_OK;
+}
+
+mnb_status check_stack_shape(const mnb_experts &w) {
+  mnb_status st = check_shape(w.N, w.K, w.block_size, w.scale_dtype);
+  if (st != MNB_OK) return st;
+  if (w.E < 1 || w.E > kMaxDim / padded_rows(w.N)) return MNB_ERR_SHAPE;
+  st = check_shape(w.E * padded_rows(w.N), w.K, w.block_size, w.scale_dtype);
+  if (st != MNB_OK) return st;
+  if (w.E > kMoeMaxExperts) {
+    std::snprintf(g_last_error, sizeof g_last_error, "E=%lld: at most %d experts",
+                  (long long)w.E, kMoeMaxExperts);
+    return MNB_ERR_UNSUPPORTED;
+  }
+  return MNB_OK;
+}
+
+mnb_status check_stack(const mnb_experts &w) {
+  if (!w.packed_b || !w.packed_scales) return MNB_ERR_NULL;
+  const mnb_status st = check_stack_shape(w);
+  if (st != MNB_OK) return st;
+  if (!aligned(w.packed_b, 16) || !aligned(w.packed_scales, 16) || !aligned(w.packed_zp, 16) ||
+      !aligned(w.bias, 4))
+    return MNB_ERR_ALIGN;
+  return MNB_OK;
+}
+
+mnb_status check_stack_layout(const mnb_experts &w) {
+  return check_layout(w.packed_b, w.E * padded_rows(w.N), w.K, w.block_size, w.scale_dtype,
+                      w.packed_zp != nullptr, MNB_CODES_AFFINE);
+}
+
+// The three stacks of a layer: each well formed, and of sizes that fit.
+mnb_status check_layer(const mnb_experts &gate, const mnb_experts &up,
+                       const mnb_experts &down) {
+  for (const mnb_experts *w : {&gate, &up, &down}) {
+    const mnb_status st = check_stack_shape(*w);
+    if (st != MNB_OK) return st;
+  }
+  const char *what = gate.E != up.E || gate.E != down.E ? "E"
+                     : gate.N != up.N || gate.K != up.K ||
+                             gate.block_size != up.block_size ||
+                             gate.scale_dtype != up.scale_dtype ||
+                             !gate.packed_zp != !up.packed_zp
+                         ? "the gate and up stacks"
+                     : down.N != gate.K || down.K != gate.N ? "the down stack's N or K"
+                                                            : nullptr;
+  if (!what) return MNB_OK;
+  std::snprintf(g_last_error, sizeof g_last_error,
+                "the stacks of the layer do not fit together: %s", what);
+  return MNB_ERR_SHAPE;
+}
+
+struct Range {
+  const void *p;
+  size_t n;
+};
+
+// What a call writes against what it reads, and against each other.
+mnb_status check_disjoint(const Range *outs, int n_outs, const Range *ins, int n_ins) {
+  for (int i = 0; i < n_outs; ++i) {
+    for (int j = 0; j < n_ins; ++j)
+      if (overlap(outs[i].p, outs[i].n, ins[j].p, ins[j].n)) return MNB_ERR_ALIAS;
+    for (int j = i + 1; j < n_outs; ++j)
+      if (overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return MNB_ERR_ALIAS;
+  }
+  return MNB_OK;
+}
+
+struct StackRanges {
+  Range r[4];
+  explicit StackRanges(const mnb_experts &w) {
+    const Sizes s = packed_sizes(w.E * padded_rows(w.N), w.K, w.block_size, w.scale_dtype,
+                                 w.packed_zp != nullptr);
+    r[0] = {w.packed_b, s.b};
+    r[1] = {w.packed_scales, s.s};
+    r[2] = {w.packed_zp, s.z};
+    r[3] = {w.bias, w.bias ? size_t(w.E) * w.N * 4 : 0};
+  }
+};
+
+mnb_status check_workspace(const void *ws, size_t bytes, size_t need) {
+  if (need == 0) return MNB_OK;
+  if (!ws) return MNB_ERR_NULL;
+  if (!aligned(ws, 256)) return MNB_ERR_ALIGN;
+  if (bytes < need) {
+    std::snprintf(g_last_error, sizeof g_last_error,
+                  "the workspace has %zu bytes, the call needs %zu", bytes, need);
+    return MNB_ERR_SHAPE;
+  }
+  return MNB_OK;
+}
+
+ExpertStack expert_stack(const mnb_experts &w) {
+  return ExpertStack{w.packed_b, w.packed_scales, w.packed_zp, w.bias,
+                     static_cast<int>(w.E), static_cast<int>(w.N), static_cast<int>(w.K),
+                     w.block_size, w.scale_dtype == MNB_F32};
+}
+
+ExpertsArgs experts_args(const void *A, int a_per_slot, const mnb_experts &w,
+                         const int32_t *experts, int64_t M, int top_k, void *Y, int a_dtype) {
+  return ExpertsArgs{A, a_dtype == MNB_F32, a_per_slot != 0, expert_stack(w), experts, M,
+                     top_k, Y, nullptr, g_pdl.load() != 0};
+}
+
+MoeArgs moe_args(const void *X, const void *logits, int logits_dtype, int64_t M, int top_k,
+                 int normalize, const mnb_experts &gate, const mnb_experts &up,
+                 const mnb_experts &down, void *Y, int a_dtype) {
+  return MoeArgs{X, a_dtype == MNB_F32, logits, logits_dtype == MNB_F32, M, top_k,
+                 normalize != 0, expert_stack(gate), expert_stack(up), expert_stack(down), Y,
+                 nullptr, g_pdl.load() != 0};
+}
+
+mnb_status experts_unsupported(int64_t M, int top_k, const mnb_experts &w) {
+  std::snprintf(g_last_error, sizeof g_last_error,
+                "no kernel for M=%lld top_k=%d E=%lld N=%lld K=%lld bs=%d", (long long)M,
+                top_k, (long long)w.E, (long long)w.N, (long long)w.K, w.block_size);
+  return MNB_ERR_UNSUPPORTED;
 }
 
 // The Python binding mirrors these two structs field by field.
@@ -1226,6 +1367,177 @@ mnb_status mnb_chain_run_noalloc(const mnb_chain_op *ops, int32_t n_ops, int64_t
                        stream);
   if (st != MNB_OK) return st;
   return mnb_chain_run(scratch, &info, stream);
+}
+
+// ---- mixture of experts ------------------------------------------------------
+
+static_assert(MNB_MOE_MAX_EXPERTS == kMoeMaxExperts && MNB_MOE_MAX_TOP_K == kMoeMaxTopK, "");
+static_assert(sizeof(mnb_experts) == 64, "mnb_experts layout");
+
+mnb_status mnb_prepack_experts(const uint8_t *B, const void *scales,
+                               const uint8_t *zero_points, int64_t E, int64_t N, int64_t K,
+                               int block_size, mnb_dtype scale_dtype, void *packed_b,
+                               void *packed_scales, void *packed_zp, mnb_stream_t stream) {
+  if (!B || !scales || !packed_b || !packed_scales) return MNB_ERR_NULL;
+  if (zero_points && !packed_zp) return MNB_ERR_NULL;
+  mnb_status st = check_shape(N, K, block_size, scale_dtype);
+  if (st != MNB_OK) return st;
+  if (E < 1 || E > kMaxDim / padded_rows(N)) return MNB_ERR_SHAPE;
+  const int64_t rows = E * padded_rows(N);
+  st = check_shape(rows, K, block_size, scale_dtype);
+  if (st != MNB_OK) return st;
+  if (!aligned(packed_b, 16) || !aligned(packed_scales, 16) ||
+      (zero_points && !aligned(packed_zp, 16)) ||
+      !aligned(scales, dtype_size(scale_dtype)))
+    return MNB_ERR_ALIGN;
+  const int64_t nb = ceil_div(K, block_size);
+  const Sizes out = packed_sizes(rows, K, block_size, scale_dtype, zero_points != nullptr);
+  const void *const ins[3] = {B, scales, zero_points};
+  const size_t in_n[3] = {size_t(E) * N * nb * (block_size / 2),
+                          size_t(E) * N * nb * dtype_size(scale_dtype),
+                          zero_points ? size_t(E) * N * ((nb + 1) / 2) : 0};
+  void *const outs[3] = {packed_b, packed_scales, zero_points ? packed_zp : nullptr};
+  const size_t out_n[3] = {out.b, out.s, out.z};
+  st = check_outputs_disjoint(outs, out_n, ins, in_n);
+  if (st != MNB_OK) return st;
+  st = check_device();
+  if (st != MNB_OK) return st;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const ExpertPackArgs a{B, scales, zero_points, E, N, K, block_size,
+                         scale_dtype == MNB_F32, packed_b, packed_scales, packed_zp};
+  const mnb_packed_header h = make_header(rows, K, block_size, scale_dtype,
+                                          zero_points != nullptr, MNB_CODES_AFFINE);
+  cudaError_t e = launch_prepack_experts(a, s);
+  if (e == cudaSuccess)
+    e = launch_pack_header(h, static_cast<char *>(packed_b) + codes_bytes(rows, K), s);
+  if (e != cudaSuccess) return cuda_fail(e, "mnb_prepack_experts");
+  record_header(packed_b, h);
+  return MNB_OK;
+}
+
+size_t mnb_moe_route_workspace_size(int64_t M, int64_t E, int top_k) {
+  if (check_route(M, E, top_k) != MNB_OK) return 0;
+  return moe_route_workspace_bytes(M, static_cast<int>(E), top_k);
+}
+
+mnb_status mnb_moe_route(const void *logits, mnb_dtype logits_dtype, int64_t M, int64_t E,
+                         int top_k, int normalize, float *weights, int32_t *experts,
+                         int32_t *offsets, int32_t *order, void *workspace,
+                         size_t workspace_bytes, mnb_stream_t stream) {
+  if (!logits || !weights || !experts || !offsets != !order) return MNB_ERR_NULL;
+  mnb_status st = check_route(M, E, top_k);
+  if (st != MNB_OK) return st;
+  if (normalize != 0 && normalize != 1) return MNB_ERR_SHAPE;
+  if (!valid_dtype(logits_dtype)) return MNB_ERR_DTYPE;
+  if (!aligned(logits, dtype_size(logits_dtype)) || !aligned(weights, 4) ||
+      !aligned(experts, 4) || !aligned(offsets, 4) || !aligned(order, 4))
+    return MNB_ERR_ALIGN;
+  const size_t need = offsets ? moe_route_workspace_bytes(M, static_cast<int>(E), top_k) : 0;
+  st = check_workspace(workspace, workspace_bytes, need);
+  if (st != MNB_OK) return st;
+  const size_t P = size_t(M) * top_k;
+  const Range outs[] = {{weights, P * 4}, {experts, P * 4}, {offsets, size_t(E + 1) * 4},
+                        {order, P * 4}, {workspace, need}};
+  const Range ins[] = {{logits, size_t(M) * E * dtype_size(logits_dtype)}};
+  st = check_disjoint(outs, 5, ins, 1);
+  if (st != MNB_OK) return st;
+  st = check_device();
+  if (st != MNB_OK) return st;
+  const RouteArgs a{logits, logits_dtype == MNB_F32, M, static_cast<int>(E), top_k,
+                    normalize != 0, weights, experts, offsets, order,
+                    static_cast<unsigned char *>(workspace), g_pdl.load() != 0};
+  const cudaError_t e = launch_moe_route(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "mnb_moe_route");
+  return MNB_OK;
+}
+
+size_t mnb_matmul_experts_workspace_size(int64_t M, int top_k, const mnb_experts *w,
+                                         mnb_dtype a_dtype, int a_per_slot) {
+  if (!w || check_stack_shape(*w) != MNB_OK || check_slots(M, top_k) != MNB_OK ||
+      !valid_dtype(a_dtype))
+    return 0;
+  return matmul_experts_workspace_bytes(
+      experts_args(nullptr, a_per_slot, *w, nullptr, M, top_k, nullptr, a_dtype));
+}
+
+mnb_status mnb_matmul_experts(const void *A, int a_per_slot, const mnb_experts *w,
+                              const int32_t *experts, int64_t M, int top_k, void *Y,
+                              mnb_dtype a_dtype, void *workspace, size_t workspace_bytes,
+                              mnb_stream_t stream) {
+  if (!A || !w || !experts || !Y) return MNB_ERR_NULL;
+  if (a_per_slot != 0 && a_per_slot != 1) return MNB_ERR_SHAPE;
+  mnb_status st = check_slots(M, top_k);
+  if (st == MNB_OK) st = check_stack(*w);
+  if (st != MNB_OK) return st;
+  if (!valid_dtype(a_dtype)) return MNB_ERR_DTYPE;
+  const size_t es = dtype_size(a_dtype);
+  if (!aligned(A, es) || !aligned(Y, es) || !aligned(experts, 4)) return MNB_ERR_ALIGN;
+  const size_t P = size_t(M) * top_k;
+  ExpertsArgs a = experts_args(A, a_per_slot, *w, experts, M, top_k, Y, a_dtype);
+  const size_t need = matmul_experts_workspace_bytes(a);
+  st = check_workspace(workspace, workspace_bytes, need);
+  if (st != MNB_OK) return st;
+  const StackRanges sr(*w);
+  const Range outs[] = {{Y, P * w->N * es}, {workspace, need}};
+  const Range ins[] = {{A, (a_per_slot ? P : size_t(M)) * w->K * es}, {experts, P * 4},
+                       sr.r[0], sr.r[1], sr.r[2], sr.r[3]};
+  st = check_disjoint(outs, 2, ins, 6);
+  if (st == MNB_OK) st = check_stack_layout(*w);
+  if (st == MNB_OK) st = check_device();
+  if (st != MNB_OK) return st;
+  a.ws = static_cast<unsigned char *>(workspace);
+  const cudaError_t e = launch_matmul_experts(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e == cudaErrorNotSupported) return experts_unsupported(M, top_k, *w);
+  if (e != cudaSuccess) return cuda_fail(e, "mnb_matmul_experts");
+  return MNB_OK;
+}
+
+size_t mnb_moe_workspace_size(int64_t M, int top_k, const mnb_experts *gate,
+                              const mnb_experts *up, const mnb_experts *down,
+                              mnb_dtype a_dtype) {
+  if (!gate || !up || !down || check_layer(*gate, *up, *down) != MNB_OK ||
+      check_route(M, gate->E, top_k) != MNB_OK || !valid_dtype(a_dtype))
+    return 0;
+  return moe_workspace_bytes(
+      moe_args(nullptr, nullptr, 0, M, top_k, 0, *gate, *up, *down, nullptr, a_dtype));
+}
+
+mnb_status mnb_moe(const void *X, const void *logits, mnb_dtype logits_dtype, int64_t M,
+                   int top_k, int normalize, const mnb_experts *gate, const mnb_experts *up,
+                   const mnb_experts *down, void *Y, mnb_dtype a_dtype, void *workspace,
+                   size_t workspace_bytes, mnb_stream_t stream) {
+  if (!X || !logits || !gate || !up || !down || !Y) return MNB_ERR_NULL;
+  mnb_status st = check_layer(*gate, *up, *down);
+  for (const mnb_experts *w : {gate, up, down})
+    if (st == MNB_OK) st = check_stack(*w);
+  if (st == MNB_OK) st = check_route(M, gate->E, top_k);
+  if (st != MNB_OK) return st;
+  if (normalize != 0 && normalize != 1) return MNB_ERR_SHAPE;
+  if (!valid_dtype(logits_dtype) || !valid_dtype(a_dtype)) return MNB_ERR_DTYPE;
+  const size_t es = dtype_size(a_dtype);
+  if (!aligned(X, es) || !aligned(Y, es) || !aligned(logits, dtype_size(logits_dtype)))
+    return MNB_ERR_ALIGN;
+  MoeArgs a = moe_args(X, logits, logits_dtype, M, top_k, normalize, *gate, *up, *down, Y,
+                       a_dtype);
+  const size_t need = moe_workspace_bytes(a);
+  st = check_workspace(workspace, workspace_bytes, need);
+  if (st != MNB_OK) return st;
+  const StackRanges sg(*gate), su(*up), sd(*down);
+  const size_t xy = size_t(M) * gate->K * es;
+  const Range outs[] = {{Y, xy}, {workspace, need}};
+  const Range ins[] = {{X, xy}, {logits, size_t(M) * gate->E * dtype_size(logits_dtype)},
+                       sg.r[0], sg.r[1], sg.r[2], sg.r[3], su.r[0], su.r[1], su.r[2],
+                       su.r[3], sd.r[0], sd.r[1], sd.r[2], sd.r[3]};
+  st = check_disjoint(outs, 2, ins, 14);
+  for (const mnb_experts *w : {gate, up, down})
+    if (st == MNB_OK) st = check_stack_layout(*w);
+  if (st == MNB_OK) st = check_device();
+  if (st != MNB_OK) return st;
+  a.ws = static_cast<unsigned char *>(workspace);
+  const cudaError_t e = launch_moe(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e == cudaErrorNotSupported) return experts_unsupported(M, top_k, *gate);
+  if (e != cudaSuccess) return cuda_fail(e, "mnb_moe");
+  return MNB_OK;
 }
 
 }  // extern "C"

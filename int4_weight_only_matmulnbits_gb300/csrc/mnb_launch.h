@@ -104,6 +104,8 @@ GemmPlanInfo gemm_plan_info(const MatmulArgs &a, int sms);
 size_t gemm_workspace_bytes();
 
 cudaError_t launch_prepack(const PrepackArgs &a, cudaStream_t stream);
+// The kernel that ends every prepack call: writes the header, nothing else.
+cudaError_t launch_pack_header(const mnb_packed_header &h, void *dst, cudaStream_t stream);
 // Test-only failure injection for the decode kernel (mnb_test_wait_fault).
 void gemv_set_wait_fault(int stop_stage);
 cudaError_t launch_unprepack(const UnprepackArgs &a, cudaStream_t stream);

@@ -1,0 +1,94 @@
+// The top-k softmax router for one row of logits, by one warp.
+//
+// For a row l[0..E): p_e = exp(l_e - max l). The k largest l_e are chosen,
+// largest first, ties going to the lowest index; choice j has the weight
+// p_j / sum (over the chosen when normalizing, over all experts otherwise).
+// -inf and NaN mask an expert: it is never chosen and adds nothing. When
+// fewer than k experts are left, the remaining choices are expert -1 with
+// weight 0. +inf counts as the maximum: it has p = 1, finite logits beside
+// it p = 0.
+//
+// Selection compares 32-bit keys whose unsigned order is the order of the
+// logits, so the same integer reductions serve fp32 and bf16 logits and the
+// choice is exact; sums and weights are fp32.
+#pragma once
+
+#include <cstdint>
+
+#include "mnb_common.cuh"
+
+namespace mnb {
+
+// Order-preserving key of a logit: 0 for -inf and NaN (masked), otherwise
+// larger for larger values; -0 and +0 share a key.
+__device__ __forceinline__ uint32_t logit_key(float x) {
+  if (!(x > -INFINITY)) return 0u;
+  const uint32_t u = __float_as_uint(x + 0.f);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float key_logit(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
+}
+// exp(l - max), with exp(inf - inf) = 1.
+__device__ __forceinline__ float logit_exp(float l, float top) {
+  return l == top ? 1.f : expf(l - top);
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Lane j < top_k returns choice j of row m: expert (or -1) and weight.
+// keys: E words of shared memory of this warp.
+__device__ __forceinline__ void route_row(const void *logits, bool f32, int64_t m, int E,
+                                          int top_k, bool normalize, uint32_t *keys,
+                                          int &expert, float &weight) {
+  const int lane = threadIdx.x & 31;
+  uint32_t best = 0;
+  int bi = 0;
+  for (int i = lane; i < E; i += 32) {
+    const float x =
+        f32 ? static_cast<const float *>(logits)[m * E + i]
+            : bf16_bits_to_f32(static_cast<const uint16_t *>(logits)[m * E + i]);
+    const uint32_t k = logit_key(x);
+    keys[i] = k;
+    if (k > best) {
+      best = k;
+      bi = i;
+    }
+  }
+  const float top = key_logit(__reduce_max_sync(0xffffffffu, best));
+  float all = 0.f;
+  if (!normalize) {
+    for (int i = lane; i < E; i += 32)
+      if (keys[i]) all += logit_exp(key_logit(keys[i]), top);
+    all = warp_sum(all);
+  }
+  expert = -1;
+  float p = 0.f;
+  for (int j = 0; j < top_k; ++j) {
+    const uint32_t win = __reduce_max_sync(0xffffffffu, best);
+    if (win == 0) break;  // every expert left is masked
+    const int at = static_cast<int>(
+        __reduce_min_sync(0xffffffffu, best == win ? static_cast<uint32_t>(bi) : 0xFFFFFFFFu));
+    if (lane == j) {
+      expert = at;
+      p = logit_exp(key_logit(win), top);
+    }
+    if ((at & 31) == lane) {  // this lane's next best
+      keys[at] = 0;
+      best = 0;
+      for (int i = lane; i < E; i += 32)
+        if (keys[i] > best) {
+          best = keys[i];
+          bi = i;
+        }
+    }
+  }
+  const float chosen = warp_sum(p);
+  weight = expert < 0 ? 0.f : p / (normalize ? chosen : all);
+}
+
+}  // namespace mnb

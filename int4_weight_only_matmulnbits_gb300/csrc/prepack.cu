@@ -258,6 +258,11 @@ cudaError_t launch_prepack(const PrepackArgs &a, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
+cudaError_t launch_pack_header(const mnb_packed_header &h, void *dst, cudaStream_t stream) {
+  prepack_fence_kernel<<<1, 32, 0, stream>>>(h, static_cast<uint64_t *>(dst));
+  return cudaGetLastError();
+}
+
 cudaError_t launch_unprepack(const UnprepackArgs &a, cudaStream_t stream) {
   const int64_t nb = ceil_div(a.K, a.bs);
   const int64_t K64 = ceil_div(a.K, kChunkK);

@@ -1,0 +1,397 @@
+"""GPU parity of the mixture-of-experts operators (mnb_moe_route, mnb_matmul_experts, mnb_moe)
+against their definition in 64 bits (moe_reference.py)."""
+import math
+
+import pytest
+import torch
+
+import int4_weight_only_matmulnbits_gb300 as mnb
+
+from . import moe_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def dev():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    mnb.build_library()
+    mnb.load()
+    return torch.device("cuda:0")
+
+
+def stack(g, E, N, K, bs, sdt, zp, bias):
+    """(B, scales, zero points, bias) of E seeded weights, on the CPU."""
+    nb = -(-K // bs)
+    B = torch.randint(0, 256, (E, N, nb, bs // 2), generator=g, dtype=torch.uint8)
+    s = (torch.rand(E, N, nb, generator=g) * 0.015 + 0.005).to(sdt)
+    z = (torch.randint(0, 256, (E, N, (nb + 1) // 2), generator=g, dtype=torch.uint8)
+         if zp else None)
+    b = torch.randn(E, N, generator=g) * 0.05 if bias else None
+    return B, s, z, b
+
+
+def to(dev, *ts):
+    return [None if t is None else t.to(dev) for t in ts]
+
+
+def pack(dev, w, N, K, bs):
+    B, s, z, b = to(dev, *w)
+    return mnb.mnb_prepack_experts(B, s, z, N, K, bs), b, ref.dequant(B, s, z, K)
+
+
+# ---- packing -------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("bs", [16, 32, 256])
+@pytest.mark.parametrize("E,N,K", [(1, 1, 1), (3, 16, 64), (2, 33, 130), (5, 48, 257)])
+@pytest.mark.parametrize("zp", [False, True])
+def test_pack_is_the_padded_stack(dev, bs, E, N, K, zp):
+    """The packed stack is mnb_prepack's of the E * Np rows with zero padding."""
+    g = torch.Generator().manual_seed(bs + N)
+    B, s, z, _ = to(dev, *stack(g, E, N, K, bs, F32, zp, False))
+    w = mnb.mnb_prepack_experts(B, s, z, N, K, bs)
+    Np = -(-N // 16) * 16
+    pad = lambda t: None if t is None else torch.nn.functional.pad(
+        t, (0, 0) * (t.dim() - 2) + (0, Np - N)).reshape(E * Np, *t.shape[2:]).contiguous()
+    plain = mnb.mnb_prepack(pad(B), pad(s), pad(z), E * Np, K, bs)
+    assert torch.equal(w.packed_scales, plain.packed_scales)
+    assert torch.equal(w.packed_b, plain.packed_b)
+    assert (z is None) == (w.packed_zp is None)
+    if zp:
+        assert torch.equal(w.packed_zp, plain.packed_zp)
+
+
+# ---- router --------------------------------------------------------------------------------
+
+def check_route(logits, k, normalize):
+    r = mnb.mnb_moe_route(logits, k, normalize=normalize)
+    w, e, off, order = ref.route(logits, k, normalize)
+    assert torch.equal(r.experts.cpu().long(), e)
+    assert torch.equal(r.offsets.cpu().long(), off)
+    assert torch.equal(r.order.cpu().long(), order)
+    # exp within 2 steps, a sum of E terms, a division: (E + 8) 2^-24.
+    E = logits.shape[1]
+    assert ((r.weights.cpu().double() - w).abs() <= (E + 8) * 2.0 ** -24 * w + 1e-37).all()
+    return r
+
+
+@pytest.mark.parametrize("M,E,k", [(1, 1, 1), (1, 128, 8), (2, 7, 7), (5, 33, 4), (31, 64, 6),
+                                   (32, 128, 8), (33, 8, 2), (100, 256, 8), (257, 60, 5),
+                                   (3, 1024, 32), (700, 16, 3)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("normalize", [True, False])
+def test_route(dev, M, E, k, dtype, normalize):
+    g = torch.Generator().manual_seed(M * 7 + E)
+    check_route(torch.randn(M, E, generator=g).to(dtype).to(dev), k, normalize)
+
+
+@pytest.mark.parametrize("M", [4, 300])
+@pytest.mark.parametrize("normalize", [True, False])
+def test_route_ties(dev, M, normalize):
+    """Few distinct values, both zeros among them: the lowest index wins."""
+    g = torch.Generator().manual_seed(5)
+    values = torch.tensor([-1.0, -0.0, 0.0, 0.5])
+    x = values[torch.randint(0, 4, (M, 48), generator=g)]
+    check_route(x.to(dev), 6, normalize)
+    check_route(x.to(BF16).to(dev), 6, normalize)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("normalize", [True, False])
+def test_route_masks_and_extremes(dev, dtype, normalize):
+    """-inf and NaN are masked (some, all but few, all), the lowest finite value is not;
+    +inf takes the whole weight."""
+    E, k = 40, 5
+    x = torch.randn(8, E, generator=torch.Generator().manual_seed(3)).to(dtype)
+    x[0, ::2] = -math.inf
+    x[1, 1:] = math.nan
+    x[2] = -math.inf
+    x[3, 3:] = -math.inf
+    x[3, 1] = math.nan
+    x[4] = torch.finfo(dtype).min
+    x[5, 7] = x[5, 30] = math.inf
+    x[6] = torch.finfo(dtype).max
+    r = check_route(x.to(dev), k, normalize)
+    assert (r.experts[2] == -1).all() and (r.weights[2] == 0).all()
+    assert r.experts[1].tolist() == [0, -1, -1, -1, -1]
+    assert r.experts[5, :2].tolist() == [7, 30] and r.weights[5, :2].tolist() == [0.5, 0.5]
+
+
+@pytest.mark.parametrize("M,E,k", [(4099, 128, 8), (20000, 64, 2), (9000, 256, 8)])
+def test_route_many_rows(dev, M, E, k):
+    """Long inputs against torch's stable sort (the choice is exact)."""
+    g = torch.Generator().manual_seed(M)
+    x = torch.randn(M, E, generator=g).to(BF16).to(dev)
+    x[::17, : E // 2] = -math.inf
+    x[5::1000] = -math.inf
+    r = mnb.mnb_moe_route(x, k)
+    top, idx = torch.sort(x.double(), dim=1, descending=True, stable=True)
+    idx = torch.where(top > -math.inf, idx, -1)[:, :k]
+    assert torch.equal(r.experts.long(), idx)
+    p = torch.exp(top[:, :k] - top[:, :1]).nan_to_num(0.0)
+    w = (p / p.sum(1, keepdim=True)).nan_to_num(0.0)
+    assert ((r.weights.double() - w).abs() <= (E + 8) * 2.0 ** -24 * w + 1e-37).all()
+    key = torch.where(idx < 0, E, idx).flatten()
+    assert torch.equal(r.order.long(), torch.sort(key, stable=True).indices)
+    assert torch.equal(r.offsets.long(),
+                       torch.searchsorted(torch.sort(key).values, torch.arange(E + 1, device=dev)))
+    again = mnb.mnb_moe_route(x, k)
+    assert all(torch.equal(a, b) for a, b in zip(r, again))
+
+
+# ---- products --------------------------------------------------------------------------------
+
+def run_experts(dev, M, E, k, N, K, bs, dtype, *, sdt=None, zp=False, bias=False,
+                per_slot=False, table=None, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    w, b, W = pack(dev, stack(g, E, N, K, bs, sdt or dtype, zp, bias), N, K, bs)
+    A = torch.randn(*((M, k, K) if per_slot else (M, K)), generator=g).to(dtype).to(dev)
+    if table is None:
+        table = torch.randint(0, E, (M, k), generator=g, dtype=torch.int32)
+    table = table.to(dev)
+    room = torch.full((M + 1, k, N), 77.0, dtype=dtype, device=dev)
+    Y = mnb.mnb_matmul_experts(A, w, table, b, out=room[:M])
+    assert (room[M:] == 77.0).all()
+    a = A.double() if per_slot else A.double().unsqueeze(1).expand(M, k, K)
+    R, err = ref.products(a, W, table, b, dtype)
+    what = f"M{M} E{E} k{k} N{N} K{K} bs{bs}"
+    ref.check(Y, R, err, what)
+    none = (table < 0) | (table >= E)
+    assert (Y[none] == 0).all()
+    assert torch.equal(Y, mnb.mnb_matmul_experts(A, w, table, b)), "not reproducible"
+    return Y
+
+
+@pytest.mark.parametrize("bs", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("zp", [False, True])
+def test_experts_tails(dev, bs, dtype, zp):
+    """Ragged N and K, one expert to many, few slots to many, both row forms."""
+    i = 0
+    for N, K in ((1, 1), (7, bs + 1), (33, 72), (129, 257), (80, 640)):
+        for M, k, E in ((1, 1, 1), (1, 8, 12), (3, 2, 5), (17, 4, 6), (70, 3, 4)):
+            i += 1
+            run_experts(dev, M, E, k, N, K, bs, dtype, zp=zp, bias=i % 2 == 0,
+                        per_slot=i % 3 == 0, seed=100 * bs + i)
+
+
+@pytest.mark.parametrize("adt,sdt", [(F32, BF16), (BF16, F32)])
+@pytest.mark.parametrize("M", [2, 90])
+def test_experts_mixed_scale_types(dev, adt, sdt, M):
+    for bs, zp in ((16, True), (32, False), (64, True)):
+        run_experts(dev, M, 3, 2, 96, 512, bs, adt, sdt=sdt, zp=zp, bias=True, seed=bs + M)
+
+
+@pytest.mark.parametrize("M", [6, 150])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_experts_empty_and_repeated(dev, M, dtype):
+    """Rows without an expert (-1 and other indices outside), one expert named twice in a row,
+    experts nobody names, and tables that are all empty or all one expert."""
+    E, k = 9, 4
+    g = torch.Generator().manual_seed(M)
+    t = torch.randint(0, E, (M, k), generator=g, dtype=torch.int32)
+    t[t == 3] = 4
+    t[1] = -1
+    t[2] = torch.tensor([5, 5, 5, -7], dtype=torch.int32)
+    t[3, 1], t[4, 2] = E, 2 ** 31 - 1
+    for per_slot in (False, True):
+        run_experts(dev, M, E, k, 70, 320, 32, dtype, bias=True, table=t, per_slot=per_slot)
+        run_experts(dev, M, E, k, 70, 320, 32, dtype, table=torch.full_like(t, -1),
+                    per_slot=per_slot)
+        run_experts(dev, M, E, k, 70, 320, 32, dtype, table=torch.full_like(t, 6),
+                    per_slot=per_slot)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("M,k,E,N,K", [(1, 8, 64, 768, 2560), (9, 2, 8, 512, 1024),
+                                       (40, 6, 24, 208, 1111), (400, 4, 16, 264, 704),
+                                       (700, 8, 5, 136, 2048), (33, 1, 1, 1000, 4096)])
+def test_experts_larger(dev, M, k, E, N, K, dtype):
+    run_experts(dev, M, E, k, N, K, 32, dtype, zp=N % 3 == 0, bias=M > 8, per_slot=k % 2 == 0,
+                seed=M)
+
+
+def test_experts_wide_magnitudes(dev):
+    """Rows of very different size, values beyond the range of fp16, zeros and one large value
+    among small ones: each row is as exact as the others."""
+    for M, dtype in ((5, F32), (5, BF16), (130, F32), (130, BF16)):
+        g = torch.Generator().manual_seed(M)
+        E, k, N, K, bs = 4, 2, 64, 512, 32
+        w, _, W = pack(dev, stack(g, E, N, K, bs, F32, True, False), N, K, bs)
+        A = torch.randn(M, K, generator=g) * 10.0 ** torch.randint(-20, 15, (M, 1), generator=g)
+        A[1] = 0
+        A[2] = torch.randn(K, generator=g) * 1e-3
+        A[2, 17] = 3e6
+        A = A.to(dtype).to(dev)
+        t = torch.randint(0, E, (M, k), generator=g, dtype=torch.int32).to(dev)
+        R, err = ref.products(A.double().unsqueeze(1).expand(M, k, K), W, t, None, dtype)
+        ref.check(mnb.mnb_matmul_experts(A, w, t), R, err, f"M{M} {dtype}")
+
+
+# ---- the layer ---------------------------------------------------------------------------------
+
+def layer_inputs(dev, M, E, k, H, I, bs, dtype, *, sdt=None, zp=False, bias=False, seed=0,
+                 bs_down=None):
+    g = torch.Generator().manual_seed(seed)
+    ws = [pack(dev, stack(g, E, N, K, b, sdt or dtype, zp, bias), N, K, b)
+          for N, K, b in ((I, H, bs), (I, H, bs), (H, I, bs_down or bs))]
+    X = torch.randn(M, H, generator=g).to(dtype).to(dev)
+    logits = torch.randn(M, E, generator=g).to(dev)
+    return X, logits, ws
+
+
+def run_layer(dev, X, logits, ws, k, normalize=True, what=""):
+    (wg, bg, Wg), (wu, bu, Wu), (wd, bd, Wd) = ws
+    M, H = X.shape
+    room = torch.full((M + 1, H), 77.0, dtype=X.dtype, device=dev)
+    kw = dict(normalize=normalize, bias_gate=bg, bias_up=bu, bias_down=bd)
+    Y = mnb.mnb_moe(X, logits, wg, wu, wd, k, out=room[:M], **kw)
+    assert (room[M:] == 77.0).all()
+    weights, experts, _, _ = ref.route(logits, k, normalize)
+    R, err = ref.layer(X, weights, experts.to(dev), Wg, Wu, Wd, bg, bu, bd, X.dtype)
+    ref.check(Y, R, err, what)
+    assert torch.equal(Y, mnb.mnb_moe(X, logits, wg, wu, wd, k, **kw)), "not reproducible"
+    return Y
+
+
+@pytest.mark.parametrize("bs", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("zp", [False, True])
+def test_layer_tails(dev, bs, dtype, zp):
+    i = 0
+    for H, I in ((1, 1), (bs + 1, 7), (130, 72), (200, 257)):
+        for M, k, E in ((1, 1, 1), (1, 4, 9), (5, 2, 3), (20, 3, 6), (65, 2, 4)):
+            i += 1
+            x = layer_inputs(dev, M, E, k, H, I, bs, dtype, zp=zp, bias=i % 2 == 0, seed=bs + i)
+            run_layer(dev, *x, k, normalize=i % 3 != 0, what=f"M{M} E{E} k{k} H{H} I{I} bs{bs}")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("M,k,E,H,I,bs", [(1, 8, 128, 1024, 512, 32), (16, 8, 64, 512, 768, 32),
+                                          (33, 4, 20, 1000, 520, 64), (150, 6, 16, 640, 352, 128),
+                                          (600, 8, 8, 512, 256, 32), (300, 2, 40, 264, 136, 16)])
+def test_layer_larger(dev, M, k, E, H, I, bs, dtype):
+    x = layer_inputs(dev, M, E, k, H, I, bs, dtype, zp=M % 2 == 0, bias=M > 100, seed=M,
+                     bs_down=32)
+    run_layer(dev, *x, k, what=f"M{M}")
+
+
+@pytest.mark.parametrize("M", [3, 12, 140])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_layer_masked_tokens(dev, M, dtype):
+    """Tokens with fewer experts than choices, with none at all, and a batch without any."""
+    X, logits, ws = layer_inputs(dev, M, 10, 4, 96, 160, 32, dtype, bias=True, seed=M)
+    logits[0] = -math.inf
+    logits[1, 2:] = -math.inf
+    logits[2, ::2] = math.nan
+    Y = run_layer(dev, X, logits, ws, 4, what="masked")
+    assert (Y[0] == 0).all()
+    Y = run_layer(dev, X, torch.full_like(logits, -math.inf), ws, 4, what="all masked")
+    assert (Y == 0).all()
+
+
+@pytest.mark.parametrize("M", [4, 140])
+def test_layer_all_tokens_one_expert(dev, M):
+    X, logits, ws = layer_inputs(dev, M, 6, 2, 128, 192, 32, BF16, seed=M)
+    logits[:, 4] += 50
+    logits[:, 1] += 40
+    run_layer(dev, X, logits, ws, 2, what="skewed")
+
+
+@pytest.mark.parametrize("M", [1, 7, 140])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_layer_is_its_parts(dev, M, dtype):
+    """The operators together: router, gate and up products, SiLU in torch, down product and
+    weighted sum give the layer's result."""
+    E, k, H, I = 12, 3, 256, 320
+    X, logits, ((wg, bg, _), (wu, bu, _), (wd, bd, _)) = layer_inputs(
+        dev, M, E, k, H, I, 32, dtype, bias=True, seed=M)
+    r = mnb.mnb_moe_route(logits.to(BF16).float(), k)
+    g = mnb.mnb_matmul_experts(X, wg, r.experts, bg).float()
+    u = mnb.mnb_matmul_experts(X, wu, r.experts, bu).float()
+    h = (torch.nn.functional.silu(g) * u).to(dtype)
+    y = mnb.mnb_matmul_experts(h, wd, r.experts, bd).float()
+    Y = mnb.mnb_moe(X, logits.to(BF16), wg, wu, wd, k, bias_gate=bg, bias_up=bu, bias_down=bd)
+    parts = (r.weights.unsqueeze(2) * y).sum(1)
+    # Both are within a few roundings of the activations' type of the exact layer.
+    u = {F32: 1e-5, BF16: 2.0 ** -6}[dtype]
+    assert (Y.float() - parts).norm() <= u * parts.norm()
+
+
+@pytest.mark.parametrize("M", [2, 140])
+def test_layer_rows_do_not_mix(dev, M):
+    """A token with infinite or NaN activations spoils its own row only."""
+    X, logits, ((wg, _, _), (wu, _, _), (wd, _, _)) = layer_inputs(
+        dev, M, 5, 2, 128, 96, 32, BF16, seed=M)
+    Y = mnb.mnb_moe(X, logits, wg, wu, wd, 2)
+    bad = X.clone()
+    bad[0, 3] = math.inf
+    bad[0, 9] = math.nan
+    Z = mnb.mnb_moe(bad, logits, wg, wu, wd, 2)
+    assert not torch.isfinite(Z[0]).any()
+    assert torch.equal(Y[1:], Z[1:])
+
+
+# ---- streams and graphs --------------------------------------------------------------------------
+
+@pytest.mark.parametrize("M", [1, 12, 140])
+def test_captured_and_replayed(dev, M):
+    """Captured once, replayed on new inputs, two graphs on two streams at a time."""
+    k = 4
+    made = []
+    for i in range(2):
+        X, logits, ws = layer_inputs(dev, M, 16, k, 256, 192, 32, BF16, seed=M + i)
+        packed = [w for w, _, _ in ws]
+        mnb.mnb_moe(X, logits, *packed, k)
+        torch.cuda.synchronize()
+        graph, st = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        with torch.cuda.graph(graph, stream=st):
+            Y = mnb.mnb_moe(X, logits, *packed, k)
+            r = mnb.mnb_moe_route(logits, k)
+            P = mnb.mnb_matmul_experts(X, packed[0], r.experts)
+        made.append((X, logits, packed, graph, st, Y, r, P))
+    for turn in range(3):
+        for X, logits, *_ in made:
+            X.copy_(torch.randn_like(X))
+            logits.copy_(torch.randn_like(logits))
+        torch.cuda.synchronize()
+        for *_, graph, st, Y, r, P in made:
+            with torch.cuda.stream(st):
+                for _ in range(5):
+                    graph.replay()
+        torch.cuda.synchronize()
+        for X, logits, packed, graph, st, Y, r, P in made:
+            assert torch.equal(Y, mnb.mnb_moe(X, logits, *packed, k))
+            now = mnb.mnb_moe_route(logits, k)
+            assert all(torch.equal(a, b) for a, b in zip(r, now))
+            assert torch.equal(P, mnb.mnb_matmul_experts(X, packed[0], now.experts))
+
+
+@pytest.mark.parametrize("M", [2, 140])
+def test_other_stream(dev, M):
+    k = 2
+    X, logits, ws = layer_inputs(dev, M, 8, k, 256, 192, 32, BF16, seed=M)
+    packed = [w for w, _, _ in ws]
+    Y = mnb.mnb_moe(X, logits, *packed, k)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    outs = [mnb.mnb_moe(X, logits, *packed, k, stream=st) for _ in range(8)]
+    st.synchronize()
+    assert all(torch.equal(o, Y) for o in outs)
+
+
+def test_programmatic_launch_off(dev):
+    X, logits, ws = layer_inputs(dev, 3, 8, 2, 256, 192, 32, BF16)
+    packed = [w for w, _, _ in ws]
+    Y = mnb.mnb_moe(X, logits, *packed, 2)
+    mnb.mnb_set_programmatic_launch(False)
+    try:
+        assert torch.equal(mnb.mnb_moe(X, logits, *packed, 2), Y)
+    finally:
+        mnb.mnb_set_programmatic_launch(True)
+
+
+def test_no_faults_recorded(dev):
+    assert mnb.mnb_fault_status() == 0
