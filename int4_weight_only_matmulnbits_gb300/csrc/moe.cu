@@ -16,7 +16,9 @@
 #include "mnb_common.cuh"
 #include "mnb_launch.h"
 #include "moe.h"
+#include "moe_lists.cuh"
 #include "moe_route.cuh"
+#include "moe_stream.h"
 
 namespace mnb {
 namespace {
@@ -24,10 +26,6 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 
-__device__ __forceinline__ float load_f(const void *p, bool f32, int64_t i) {
-  return f32 ? static_cast<const float *>(p)[i]
-             : bf16_bits_to_f32(static_cast<const uint16_t *>(p)[i]);
-}
 __device__ __forceinline__ void store_f(void *p, bool f32, int64_t i, float v) {
   if (f32) static_cast<float *>(p)[i] = v;
   else static_cast<uint16_t *>(p)[i] = static_cast<uint16_t>(bf16_bits(v));
@@ -106,6 +104,8 @@ __global__ void __launch_bounds__(kThreads)
                  float *weights, int32_t *experts) {
   extern __shared__ uint32_t keys_all[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  grid_dependency_wait();
+  grid_dependents_launch();
   for (int64_t m = blockIdx.x * (int64_t)kWarps + warp; m < M; m += (int64_t)gridDim.x * kWarps) {
     int e;
     float r;
@@ -126,6 +126,8 @@ __global__ void __launch_bounds__(kListWarps * 32)
   extern __shared__ int32_t cnt[];  // [kListWarps][E + 1], then [E + 1]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int32_t *mine = cnt + warp * (E + 1), *start = cnt + kListWarps * (E + 1);
+  grid_dependency_wait();
+  grid_dependents_launch();
   for (int i = threadIdx.x; i < kListWarps * (E + 1); i += blockDim.x) cnt[i] = 0;
   __syncthreads();
   const int64_t per = ceil_div(P, kListWarps), lo = warp * per, hi = lo + per < P ? lo + per : P;
@@ -177,112 +179,62 @@ __global__ void __launch_bounds__(kListWarps * 32)
   }
 }
 
-// ---- products ---------------------------------------------------------------------
-
-// One warp forms one 16-row tile of one slot: lane (g, t) holds rows g and
-// g + 8 and, of every 16 k, the elements 4t .. 4t+3 of the packed word.
-__device__ __forceinline__ void tile_dot(const ExpertStack &w, int64_t tile, const void *a,
-                                         bool a_f32, int64_t a0, float (&acc)[2]) {
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int K64 = static_cast<int>(ceil_div(w.K, kChunkK));
-  const int64_t nb = ceil_div(w.K, w.bs), nbz = ceil_div(nb, 2) * 2;
-  acc[0] = acc[1] = 0.f;
-  for (int c = 0; c < K64; ++c) {
-    const uint4 v = reinterpret_cast<const uint4 *>(w.b)[(tile * K64 + c) * 32 + lane];
-    const uint32_t words[4] = {v.x, v.y, v.z, v.w};
-    for (int j = 0; j < 4; ++j) {
-      const int k0 = c * kChunkK + 16 * j + 4 * t;
-      if (k0 >= w.K) break;
-      const int64_t b = k0 / w.bs;
-      float d[2] = {0.f, 0.f};
-      uint64_t zw = 0x8888888888888888ull;
-      if (w.z) zw = static_cast<const uint64_t *>(w.z)[tile * nbz + b];
-      for (int o = 0; o < 4 && k0 + o < w.K; ++o) {
-        const float x = load_f(a, a_f32, a0 + k0 + o);
-        for (int h = 0; h < 2; ++h) {
-          const int q = (words[j] >> code_shift(o, h)) & 15;
-          const int z = static_cast<int>(zw >> (4 * (g + 8 * h))) & 15;
-          d[h] = fmaf(static_cast<float>(q - z), x, d[h]);
-        }
-      }
-      for (int h = 0; h < 2; ++h)
-        acc[h] = fmaf(load_f(w.s, w.s_f32, (tile * nb + b) * kTileN + g + 8 * h), d[h], acc[h]);
+// Router and lists of a few slots in one block.
+__global__ void __launch_bounds__(kThreads) route_few_kernel(RouteArgs a) {
+  extern __shared__ __align__(16) int few_smem[];
+  const int P = static_cast<int>(a.M) * a.top_k;
+  const SlotLists L = slot_lists(few_smem, P, a.E);
+  uint32_t *keys = reinterpret_cast<uint32_t *>(few_smem + slot_lists_ints(P, a.E));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  grid_dependency_wait();
+  grid_dependents_launch();
+  for (int m = warp; m < a.M; m += kWarps) {
+    int e;
+    float r;
+    route_row(a.logits, a.logits_f32, m, a.E, a.top_k, a.normalize, keys + warp * a.E, e, r);
+    if (lane < a.top_k) {
+      a.experts[m * a.top_k + lane] = e;
+      a.weights[m * a.top_k + lane] = r;
+      L.e[m * a.top_k + lane] = e < 0 ? a.E : e;
     }
   }
-  for (int h = 0; h < 2; ++h) {
-    acc[h] += __shfl_xor_sync(0xffffffffu, acc[h], 1);
-    acc[h] += __shfl_xor_sync(0xffffffffu, acc[h], 2);
-  }
+  __syncthreads();
+  build_lists(L, P, a.E, 1);
+  for (int i = threadIdx.x; i <= a.E; i += kThreads) a.offsets[i] = L.off[i];
+  for (int i = threadIdx.x; i < P; i += kThreads) a.order[i] = L.order[i];
 }
 
-__global__ void __launch_bounds__(kThreads) product_kernel(ExpertsArgs a) {
-  const int lane = threadIdx.x & 31, g = lane >> 2;
-  const int64_t N16 = ceil_div(a.w.N, kTileN), items = a.M * a.top_k * N16;
-  for (int64_t it = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5; it < items;
-       it += ((int64_t)gridDim.x * blockDim.x) >> 5) {
-    const int64_t p = it / N16, nt = it % N16;
-    const int e = a.experts[p];
-    const bool some = e >= 0 && e < a.w.E;
-    float acc[2] = {0.f, 0.f};
-    if (some)
-      tile_dot(a.w, e * N16 + nt, a.A, a.a_f32, (a.per_slot ? p : p / a.top_k) * a.w.K, acc);
-    for (int h = 0; h < 2; ++h) {
-      const int64_t n = nt * kTileN + g + 8 * h;
-      if ((lane & 3) || n >= a.w.N) continue;
-      if (some && a.w.bias) acc[h] += a.w.bias[int64_t(e) * a.w.N + n];
-      store_f(a.Y, a.a_f32, p * a.w.N + n, acc[h]);
-    }
-  }
-}
-
+// Sum of each token's down partials, in slot order (long inputs).
 __global__ void __launch_bounds__(kThreads)
-    gate_up_kernel(MoeArgs a, const int32_t *experts, float *hidden) {
-  const int lane = threadIdx.x & 31, g = lane >> 2;
-  const int64_t N16 = ceil_div(a.gate.N, kTileN), items = a.M * a.top_k * N16;
-  for (int64_t it = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5; it < items;
-       it += ((int64_t)gridDim.x * blockDim.x) >> 5) {
-    const int64_t p = it / N16, nt = it % N16;
-    const int e = experts[p];
-    if (e < 0) continue;
-    float vg[2], vu[2];
-    tile_dot(a.gate, e * N16 + nt, a.X, a.a_f32, p / a.top_k * a.gate.K, vg);
-    tile_dot(a.up, e * N16 + nt, a.X, a.a_f32, p / a.top_k * a.gate.K, vu);
-    for (int h = 0; h < 2; ++h) {
-      const int64_t n = nt * kTileN + g + 8 * h;
-      if ((lane & 3) || n >= a.gate.N) continue;
-      if (a.gate.bias) vg[h] += a.gate.bias[int64_t(e) * a.gate.N + n];
-      if (a.up.bias) vu[h] += a.up.bias[int64_t(e) * a.up.N + n];
-      hidden[p * a.gate.N + n] = vg[h] / (1.f + expf(-vg[h])) * vu[h];
-    }
+    combine_kernel(const float *part, const int32_t *experts, int64_t M, int top_k, int N,
+                   void *Y, bool f32) {
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int64_t total = M * N;
+  for (int64_t i = blockIdx.x * int64_t(kThreads) + threadIdx.x; i < total;
+       i += int64_t(gridDim.x) * kThreads) {
+    const int64_t m = i / N;
+    float y = 0.f;
+    for (int j = 0; j < top_k; ++j)
+      if (experts[m * top_k + j] >= 0) y += part[(m * top_k + j) * N + (i - m * N)];
+    store_f(Y, f32, i, y);
   }
 }
 
-__global__ void __launch_bounds__(kThreads)
-    down_kernel(MoeArgs a, const int32_t *experts, const float *weights, const float *hidden) {
-  const int lane = threadIdx.x & 31, g = lane >> 2;
-  const int64_t N16 = ceil_div(a.down.N, kTileN), items = a.M * N16;
-  for (int64_t it = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5; it < items;
-       it += ((int64_t)gridDim.x * blockDim.x) >> 5) {
-    const int64_t m = it / N16, nt = it % N16;
-    float y[2] = {0.f, 0.f};
-    for (int j = 0; j < a.top_k; ++j) {
-      const int64_t p = m * a.top_k + j;
-      const int e = experts[p];
-      if (e < 0) continue;
-      float v[2];
-      tile_dot(a.down, e * N16 + nt, hidden, true, p * a.down.K, v);
-      for (int h = 0; h < 2; ++h) {
-        const int64_t n = nt * kTileN + g + 8 * h;
-        if (n >= a.down.N) continue;
-        if (a.down.bias) v[h] += a.down.bias[int64_t(e) * a.down.N + n];
-        y[h] = fmaf(weights[p], v[h], y[h]);
-      }
-    }
-    for (int h = 0; h < 2; ++h) {
-      const int64_t n = nt * kTileN + g + 8 * h;
-      if (!(lane & 3) && n < a.down.N) store_f(a.Y, a.a_f32, m * a.down.N + n, y[h]);
-    }
-  }
+template <typename... P, typename... A>
+cudaError_t launch_pdl(void (*kernel)(P...), unsigned grid, int block, size_t smem, bool pdl,
+                       cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
 }
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -310,49 +262,262 @@ cudaError_t launch_prepack_experts(const ExpertPackArgs &a, cudaStream_t stream)
   return cudaGetLastError();
 }
 
-cudaError_t launch_moe_route(const RouteArgs &a, cudaStream_t stream) {
-  const size_t keys = size_t(kWarps) * a.E * 4;
-  route_kernel<<<grid_of(a.M, kWarps), kThreads, keys, stream>>>(
-      a.logits, a.logits_f32, a.M, a.E, a.top_k, a.normalize, a.weights, a.experts);
-  if (a.order) {
-    static std::atomic<unsigned long long> done{0};
-    const int bytes = (kListWarps + 1) * (kMoeMaxExperts + 1) * 4;
-    const cudaError_t e = ensure_smem_limit(lists_kernel, bytes, done);
-    if (e != cudaSuccess) return e;
-    lists_kernel<<<1, kListWarps * 32, size_t(kListWarps + 1) * (a.E + 1) * 4, stream>>>(
-        a.experts, a.M * a.top_k, a.E, a.offsets, a.order);
+
+namespace {
+
+int ilog2(int x) {
+  int r = 0;
+  while ((1 << r) < x) ++r;
+  return r;
+}
+
+// Fills the geometry of a weight-streaming launch. `lists_p`: slots listed in
+// shared memory (0: ready lists); `per_expert`: the most slots an expert can
+// have. false: not even one activation row fits.
+struct StreamPlan {
+  StreamParams p{};
+  int terms = 1, grid = 1, smem = 0;
+  bool zp = false, sf32 = false;
+};
+bool plan_stream(StreamPlan &pl, const ExpertStack &w, int mode, int terms, int64_t P,
+                 int64_t M, int top_k, bool few, int64_t per_expert, bool keys) {
+  StreamParams &p = pl.p;
+  pl.terms = terms;
+  pl.zp = w.z != nullptr;
+  pl.sf32 = w.s_f32;
+  p.mode = mode;
+  p.E = w.E;
+  p.N = w.N;
+  p.K = w.K;
+  p.N16 = static_cast<int>(ceil_div(w.N, kTileN));
+  p.K64 = static_cast<int>(ceil_div(w.K, kChunkK));
+  p.nb = static_cast<int>(ceil_div(w.K, w.bs));
+  p.nbz = (p.nb + 1) / 2 * 2;
+  p.bs_log2 = ilog2(w.bs);
+  p.P = static_cast<int>(P);
+  p.M = static_cast<int>(M);
+  p.top_k = top_k;
+  const int nmat = mode == kStreamGateUp ? 2 : 1, es = w.s_f32 ? 4 : 2;
+  // k ranges of at least three chunks per warp.
+  p.ksplit = 8;
+  while (p.ksplit > 1 && p.K64 / p.ksplit < 3) p.ksplit /= 2;
+  p.tpu = 8 / p.ksplit;
+  p.ns = static_cast<int>(ceil_div(p.N16, p.tpu));
+  const int range = static_cast<int>(ceil_div(p.K64, p.ksplit));
+  p.kc = static_cast<int>(ceil_div(range, ceil_div(range, 4)));
+  const int nblk = (p.kc * kChunkK + w.bs - 1) / w.bs + 1;
+  p.st_scale = p.kc * kChunkBytes;
+  p.st_zp = p.st_scale + (nblk * kTileN * es + 15) / 16 * 16;
+  p.st_bytes = (p.st_zp + (pl.zp ? (nblk / 2 + 1) * 16 : 0) + 127) / 128 * 128;
+  const int64_t krow = int64_t(p.K64) * kChunkK + 16;
+  const int64_t lists =
+      (int64_t(slot_lists_ints(few ? p.P : 0, p.E)) * 4 + (few ? p.P * 4 : 0) + 127) / 128 * 128;
+  const int red = 2 * 8 * nmat * kTileN * 8 * 4;
+  const int64_t ring =
+      std::max<int64_t>(8 * 4 * p.st_bytes, keys ? int64_t(8) * p.E * 4 : 0);
+  // Slots per group: about twice the mean list, so that few experts need a
+  // second pass over their weights, within what two CTAs per SM leave (one
+  // CTA per SM when that is not enough for the mean).
+  const int64_t mean = ceil_div(P, w.E);
+  int want = 1;
+  while (want < 8 && want < 2 * mean && want < per_expert) want *= 2;
+  constexpr int64_t kHalf = 113 * 1024, kFull = 226 * 1024;
+  auto bytes = [&](int gt) { return lists + red + ring + int64_t(terms) * gt * krow * 2; };
+  int gt = want;
+  while (gt > 1 && bytes(gt) > kHalf && gt > mean) gt /= 2;
+  while (gt > 1 && bytes(gt) > kFull) gt /= 2;
+  if (bytes(gt) > kFull) return false;
+  p.gt = gt;
+  p.krow = static_cast<int>(krow);
+  p.off_lists = 0;
+  p.off_keys = slot_lists_ints(few ? p.P : 0, p.E) * 4;
+  p.off_red = static_cast<int>(lists);
+  p.off_ring = p.off_red + red;
+  p.off_x = static_cast<int>(p.off_ring + ring);
+  pl.smem = static_cast<int>(bytes(gt));
+  const int64_t most = P * p.ns, slots = int64_t(sm_count()) * (pl.smem <= kHalf ? 2 : 1);
+  if (most > (int64_t(1) << 31) - 1) return false;
+  pl.grid = static_cast<int>(std::min(most, slots));
+  return true;
+}
+
+cudaError_t run_stream(const StreamPlan &pl, bool pdl, cudaStream_t stream) {
+  const int bs = 1 << pl.p.bs_log2;
+  auto *fn = bs == 16 ? launch_stream<1> : bs == 32 ? launch_stream<2> : launch_stream<4>;
+  return fn(pl.p, pl.zp, pl.sf32, pl.terms, pl.grid, pl.smem, pdl, stream);
+}
+
+StreamMat stream_mat(const ExpertStack &w) {
+  return StreamMat{static_cast<const uint4 *>(w.b), static_cast<const unsigned char *>(w.s),
+                   static_cast<const unsigned char *>(w.z), w.bias};
+}
+
+bool vec_rows(const void *a, int64_t K, size_t es) {
+  return reinterpret_cast<uintptr_t>(a) % 16 == 0 && K * es % 16 == 0;
+}
+
+// Carves a workspace into 256-byte aligned pieces; with a null base it only
+// adds up the bytes.
+struct Carve {
+  unsigned char *base;
+  size_t used = 0;
+  template <typename T>
+  T *take(size_t n) {
+    T *r = base ? reinterpret_cast<T *>(base + used) : nullptr;
+    used += align256(n * sizeof(T));
+    return r;
   }
-  return cudaGetLastError();
+};
+
+// The lists of many slots in global memory.
+struct Lists {
+  float *weights = nullptr;
+  int32_t *experts = nullptr, *offsets = nullptr, *order = nullptr;
+};
+
+cudaError_t launch_lists(const int32_t *experts, int64_t P, int E, int32_t *offsets,
+                         int32_t *order, bool pdl, cudaStream_t stream) {
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = ensure_smem_limit(
+      lists_kernel, (kListWarps + 1) * (kMoeMaxExperts + 1) * 4, done);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(lists_kernel, 1, kListWarps * 32, size_t(kListWarps + 1) * (E + 1) * 4, pdl,
+                    stream, experts, P, E, offsets, order);
+}
+
+struct MoeSpace {
+  Lists l;
+  uint16_t *hidden;
+  float *part;
+  unsigned *counters;
+  size_t bytes;
+};
+MoeSpace moe_space(const MoeArgs &a) {
+  const size_t P = size_t(a.M) * a.top_k;
+  Carve c{a.ws};
+  MoeSpace s{};
+  if (P > kFewSlots) {
+    s.l.weights = c.take<float>(P);
+    s.l.experts = c.take<int32_t>(P);
+    s.l.offsets = c.take<int32_t>(a.gate.E + 1);
+    s.l.order = c.take<int32_t>(P);
+  } else {
+    s.counters = c.take<unsigned>(ceil_div(a.down.N, kTileN));
+  }
+  const size_t ldh = ceil_div(a.gate.N, 8) * 8;
+  s.hidden = c.take<uint16_t>((a.a_f32 ? 3 : 2) * P * ldh);
+  s.part = c.take<float>(P * a.down.N);
+  s.bytes = c.used;
+  return s;
+}
+
+}  // namespace
+
+size_t moe_route_workspace_bytes(int64_t, int, int) { return 0; }
+
+cudaError_t launch_moe_route(const RouteArgs &a, cudaStream_t stream) {
+  const int64_t P = a.M * a.top_k;
+  if (a.order && P <= kFewSlots) {
+    const size_t smem = size_t(slot_lists_ints(static_cast<int>(P), a.E) + kWarps * a.E) * 4;
+    return launch_pdl(route_few_kernel, 1, kThreads, smem, a.pdl, stream, a);
+  }
+  cudaError_t e = launch_pdl(route_kernel, grid_of(a.M, kWarps), kThreads,
+                             size_t(kWarps) * a.E * 4, a.pdl, stream, a.logits, a.logits_f32,
+                             a.M, a.E, a.top_k, a.normalize, a.weights, a.experts);
+  if (e == cudaSuccess && a.order)
+    e = launch_lists(a.experts, P, a.E, a.offsets, a.order, a.pdl, stream);
+  return e;
+}
+
+size_t matmul_experts_workspace_bytes(const ExpertsArgs &a) {
+  const size_t P = size_t(a.M) * a.top_k;
+  if (P <= kFewSlots) return 0;
+  return align256(size_t(a.w.E + 1) * 4) + align256(P * 4);
 }
 
 cudaError_t launch_matmul_experts(const ExpertsArgs &a, cudaStream_t stream) {
-  const int64_t items = a.M * a.top_k * ceil_div(a.w.N, kTileN);
-  product_kernel<<<grid_of(items, kWarps), kThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  const int64_t P = a.M * a.top_k;
+  const bool few = P <= kFewSlots;
+  StreamPlan pl;
+  if (!plan_stream(pl, a.w, kStreamProduct, a.a_f32 ? 3 : 1, P, a.M, a.top_k, few, P, false))
+    return cudaErrorNotSupported;
+  Lists l;
+  if (!few) {
+    Carve c{a.ws};
+    l.offsets = c.take<int32_t>(a.w.E + 1);
+    l.order = c.take<int32_t>(P);
+    const cudaError_t e =
+        launch_lists(a.experts, P, a.w.E, l.offsets, l.order, a.pdl, stream);
+    if (e != cudaSuccess) return e;
+  }
+  StreamParams &p = pl.p;
+  p.w[0] = stream_mat(a.w);
+  p.A = a.A;
+  p.a_vec = vec_rows(a.A, a.w.K, a.a_f32 ? 4 : 2);
+  p.per_slot = a.per_slot;
+  p.table = a.experts;
+  p.offsets = l.offsets;
+  p.order = l.order;
+  p.Y = a.Y;
+  p.y_f32 = a.a_f32;
+  return run_stream(pl, a.pdl, stream);
 }
 
-size_t moe_route_workspace_bytes(int64_t, int, int) { return 0; }
-size_t matmul_experts_workspace_bytes(const ExpertsArgs &) { return 0; }
-
 size_t moe_workspace_bytes(const MoeArgs &a) {
-  const size_t P = size_t(a.M) * a.top_k;
-  return 2 * align256(P * 4) + align256(P * a.gate.N * 4);
+  MoeArgs b = a;
+  b.ws = nullptr;
+  return moe_space(b).bytes;
 }
 
 cudaError_t launch_moe(const MoeArgs &a, cudaStream_t stream) {
-  const size_t P = size_t(a.M) * a.top_k;
-  float *weights = reinterpret_cast<float *>(a.ws);
-  int32_t *experts = reinterpret_cast<int32_t *>(a.ws + align256(P * 4));
-  float *hidden = reinterpret_cast<float *>(a.ws + 2 * align256(P * 4));
-  RouteArgs r{a.logits, a.logits_f32, a.M, a.gate.E, a.top_k, a.normalize, weights, experts,
-              nullptr, nullptr, nullptr, a.pdl};
-  const cudaError_t e = launch_moe_route(r, stream);
+  const int64_t P = a.M * a.top_k;
+  const bool few = P <= kFewSlots;
+  const MoeSpace s = moe_space(a);
+  StreamPlan up, down;
+  if (!plan_stream(up, a.gate, kStreamGateUp, a.a_f32 ? 3 : 1, P, a.M, a.top_k, few, a.M, few) ||
+      !plan_stream(down, a.down, kStreamDown, a.a_f32 ? 3 : 2, P, a.M, a.top_k, few, a.M, few))
+    return cudaErrorNotSupported;
+  if (!few) {
+    const RouteArgs r{a.logits, a.logits_f32, a.M, a.gate.E, a.top_k, a.normalize, s.l.weights,
+                      s.l.experts, s.l.offsets, s.l.order, nullptr, a.pdl};
+    const cudaError_t e = launch_moe_route(r, stream);
+    if (e != cudaSuccess) return e;
+  }
+  for (StreamParams *p : {&up.p, &down.p}) {
+    if (few) {
+      p->logits = a.logits;
+      p->logits_f32 = a.logits_f32;
+      p->normalize = a.normalize;
+    } else {
+      p->offsets = s.l.offsets;
+      p->order = s.l.order;
+      p->weights = s.l.weights;
+      p->experts = s.l.experts;
+    }
+    p->y_f32 = a.a_f32;
+    p->plane = P * (ceil_div(a.gate.N, 8) * 8);
+    p->ldh = static_cast<int>(ceil_div(a.gate.N, 8) * 8);
+    p->counters = s.counters;
+  }
+  up.p.w[0] = stream_mat(a.gate);
+  up.p.w[1] = stream_mat(a.up);
+  up.p.A = a.X;
+  up.p.a_vec = vec_rows(a.X, a.gate.K, a.a_f32 ? 4 : 2);
+  up.p.hidden = s.hidden;
+  up.p.h_planes = a.a_f32 ? 3 : 2;
+  up.p.n_counters = few ? down.p.ns : 0;
+  cudaError_t e = run_stream(up, a.pdl, stream);
   if (e != cudaSuccess) return e;
-  gate_up_kernel<<<grid_of(P * ceil_div(a.gate.N, kTileN), kWarps), kThreads, 0, stream>>>(
-      a, experts, hidden);
-  down_kernel<<<grid_of(a.M * ceil_div(a.down.N, kTileN), kWarps), kThreads, 0, stream>>>(
-      a, experts, weights, hidden);
-  return cudaGetLastError();
+  down.p.w[0] = stream_mat(a.down);
+  down.p.A = s.hidden;
+  down.p.a_vec = 1;
+  down.p.part = s.part;
+  down.p.Y = a.Y;
+  down.p.early = few;
+  e = run_stream(down, a.pdl, stream);
+  if (e != cudaSuccess || few) return e;
+  return launch_pdl(combine_kernel, grid_of(a.M * a.down.N, kThreads), kThreads, 0, a.pdl,
+                    stream, s.part, s.l.experts, a.M, a.top_k, a.down.N, a.Y, a.a_f32);
 }
 
 }  // namespace mnb
