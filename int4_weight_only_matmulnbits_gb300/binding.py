@@ -7,7 +7,6 @@ immediately; there is no fallback implementation.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import threading
@@ -783,37 +782,49 @@ def _on_gpu(name: str, t: torch.Tensor, device: torch.device | None = None) -> N
         raise ValueError(f"{name} is on {t.device}, the call runs on {device}")
 
 
-@contextlib.contextmanager
-def _call_on(device: torch.device, stream):
-    """Makes `device` current and yields the call's stream handle, with torch's
+def _call_on(device: torch.device, stream, call):
+    """call(handle) with `device` current, the call's stream handle, and torch's
     allocations (outputs, workspace) made for that stream: the caller's, or the
     device's current one. The caller orders `stream` with the work that made
     the inputs and that reads the outputs."""
-    with torch.cuda.device(device):
-        if stream is None:
-            yield ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
-        else:
-            if stream.device != device:
-                raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-            with torch.cuda.stream(stream):
-                yield ctypes.c_void_p(stream.cuda_stream)
+    if stream is None:
+        if device.index == torch.cuda.current_device():  # nothing to switch
+            return call(torch.cuda.current_stream().cuda_stream)
+        with torch.cuda.device(device):
+            return call(torch.cuda.current_stream().cuda_stream)
+    if stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        return call(stream.cuda_stream)
 
 
-def _workspace(n: int, device: torch.device) -> torch.Tensor | None:
-    """n bytes for one call. Freed on return to torch's allocator, which hands
-    the memory out again on the same stream only, after the call's kernels."""
-    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+def _workspace(n: int, device: torch.device):
+    """(tensor, address) of n bytes for one call. Freed on return to torch's
+    allocator, which hands the memory out again on the same stream only, after
+    the call's kernels."""
+    if n == 0:
+        return None, None
+    t = torch.empty(n, dtype=torch.uint8, device=device)
+    return t, t.data_ptr()
 
 
 def _experts_struct(w: PackedExperts, bias: torch.Tensor | None, device) -> ExpertsC:
+    """mnb_experts of w; the struct of the last bias is kept with w."""
+    key = (None if bias is None else bias.data_ptr(), device)
+    kept = w.__dict__.get("_struct")
+    if bias is None and kept is not None and kept[0] == key:
+        return kept[1]
     _on_gpu("packed_b", w.packed_b, device)
     if bias is not None:
         _on_gpu("bias", bias, device)
         if bias.dtype != torch.float32 or bias.shape != (w.E, w.N):
             raise ValueError(f"bias must be an fp32 [{w.E}, {w.N}] tensor")
     ptr = lambda t: None if t is None else t.data_ptr()
-    return ExpertsC(w.packed_b.data_ptr(), w.packed_scales.data_ptr(), ptr(w.packed_zp),
-                    ptr(bias), w.E, w.N, w.K, w.block_size, _dtype_code(w.scale_dtype))
+    c = ExpertsC(w.packed_b.data_ptr(), w.packed_scales.data_ptr(), ptr(w.packed_zp), ptr(bias),
+                 w.E, w.N, w.K, w.block_size, _dtype_code(w.scale_dtype))
+    if bias is None:
+        w.__dict__["_struct"] = (key, c)
+    return c
 
 
 def mnb_prepack_experts(B: torch.Tensor, scales: torch.Tensor,
@@ -832,14 +843,16 @@ def mnb_prepack_experts(B: torch.Tensor, scales: torch.Tensor,
                                  + ("" if name == "scales" else " and uint8 elements"))
     sb, ss, sz = mnb_prepacked_sizes(E * (-(-N // 16) * 16), K, block_size, scales.dtype,
                                      zero_points is not None)
-    with _call_on(B.device, stream) as s:
+
+    def call(s):
         pb, ps = (torch.empty(n, dtype=torch.uint8, device=B.device) for n in (sb, ss))
         pz = (torch.empty(sz, dtype=torch.uint8, device=B.device)
               if zero_points is not None else None)
         _check(load().mnb_prepack_experts(_ptr(B), _ptr(scales), _ptr(zero_points), E, N, K,
                                           block_size, _dtype_code(scales.dtype), _ptr(pb),
                                           _ptr(ps), _ptr(pz), s), "mnb_prepack_experts")
-    return PackedExperts(pb, ps, pz, E, N, K, block_size, scales.dtype)
+        return PackedExperts(pb, ps, pz, E, N, K, block_size, scales.dtype)
+    return _call_on(B.device, stream, call)
 
 
 def mnb_moe_route(logits: torch.Tensor, top_k: int, *, normalize: bool = True,
@@ -851,18 +864,20 @@ def mnb_moe_route(logits: torch.Tensor, top_k: int, *, normalize: bool = True,
         raise ValueError("logits must be [M, E]")
     _on_gpu("logits", logits)
     M, E = logits.shape
-    lib, dev = load(), logits.device
-    with _call_on(dev, stream) as s:
+    lib, dev, code = _lib or load(), logits.device, _dtype_code(logits.dtype)
+
+    def call(s):
         weights = torch.empty(M, top_k, dtype=torch.float32, device=dev)
         experts = torch.empty(M, top_k, dtype=torch.int32, device=dev)
         offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
         order = torch.empty(M * top_k, dtype=torch.int32, device=dev)
         n = lib.mnb_moe_route_workspace_size(M, E, top_k)
-        ws = _workspace(n, dev)
-        _check(lib.mnb_moe_route(_ptr(logits), _dtype_code(logits.dtype), M, E, top_k,
-                                 1 if normalize else 0, _ptr(weights), _ptr(experts),
-                                 _ptr(offsets), _ptr(order), _ptr(ws), n, s), "mnb_moe_route")
-    return MoeRouting(weights, experts, offsets, order)
+        ws, wp = _workspace(n, dev)
+        _check(lib.mnb_moe_route(logits.data_ptr(), code, M, E, top_k, 1 if normalize else 0,
+                                 weights.data_ptr(), experts.data_ptr(), offsets.data_ptr(),
+                                 order.data_ptr(), wp, n, s), "mnb_moe_route")
+        return MoeRouting(weights, experts, offsets, order)
+    return _call_on(dev, stream, call)
 
 
 def mnb_matmul_experts(A: torch.Tensor, w: PackedExperts, experts: torch.Tensor,
@@ -880,20 +895,21 @@ def mnb_matmul_experts(A: torch.Tensor, w: PackedExperts, experts: torch.Tensor,
     per_slot = A.dim() == 3
     if A.shape != ((M, top_k, w.K) if per_slot else (M, w.K)):
         raise ValueError(f"A must be [{M}, {w.K}] or [{M}, {top_k}, {w.K}]")
-    lib, code = load(), _dtype_code(A.dtype)
+    if out is not None:
+        _on_gpu("out", out, dev)
+        if out.shape != (M, top_k, w.N) or out.dtype != A.dtype:
+            raise ValueError(f"out must be a [{M}, {top_k}, {w.N}] tensor of A's dtype")
+    lib, code = _lib or load(), _dtype_code(A.dtype)
     c = _experts_struct(w, bias, dev)
-    with _call_on(dev, stream) as s:
-        if out is None:
-            out = torch.empty(M, top_k, w.N, dtype=A.dtype, device=dev)
-        else:
-            _on_gpu("out", out, dev)
-            if out.shape != (M, top_k, w.N) or out.dtype != A.dtype:
-                raise ValueError(f"out must be a [{M}, {top_k}, {w.N}] tensor of A's dtype")
+
+    def call(s):
+        Y = torch.empty(M, top_k, w.N, dtype=A.dtype, device=dev) if out is None else out
         n = lib.mnb_matmul_experts_workspace_size(M, top_k, c, code, per_slot)
-        ws = _workspace(n, dev)
-        _check(lib.mnb_matmul_experts(_ptr(A), per_slot, c, _ptr(experts), M, top_k, _ptr(out),
-                                      code, _ptr(ws), n, s), "mnb_matmul_experts")
-    return out
+        ws, wp = _workspace(n, dev)
+        _check(lib.mnb_matmul_experts(A.data_ptr(), per_slot, c, experts.data_ptr(), M, top_k,
+                                      Y.data_ptr(), code, wp, n, s), "mnb_matmul_experts")
+        return Y
+    return _call_on(dev, stream, call)
 
 
 def mnb_moe(X: torch.Tensor, logits: torch.Tensor, gate: PackedExperts, up: PackedExperts,
@@ -912,19 +928,20 @@ def mnb_moe(X: torch.Tensor, logits: torch.Tensor, gate: PackedExperts, up: Pack
     M = X.shape[0]
     if logits.shape != (M, gate.E):
         raise ValueError(f"logits must be [{M}, {gate.E}]")
-    lib, code = load(), _dtype_code(X.dtype)
-    g, u, d = (_experts_struct(w, b, dev) for w, b in
-               ((gate, bias_gate), (up, bias_up), (down, bias_down)))
-    with _call_on(dev, stream) as s:
-        if out is None:
-            out = torch.empty_like(X)
-        else:
-            _on_gpu("out", out, dev)
-            if out.shape != X.shape or out.dtype != X.dtype:
-                raise ValueError(f"out must be a [{M}, {gate.K}] tensor of X's dtype")
+    if out is not None:
+        _on_gpu("out", out, dev)
+        if out.shape != X.shape or out.dtype != X.dtype:
+            raise ValueError(f"out must be a [{M}, {gate.K}] tensor of X's dtype")
+    lib, code, lcode = _lib or load(), _dtype_code(X.dtype), _dtype_code(logits.dtype)
+    g, u, d = (_experts_struct(gate, bias_gate, dev), _experts_struct(up, bias_up, dev),
+               _experts_struct(down, bias_down, dev))
+
+    def call(s):
+        Y = torch.empty_like(X) if out is None else out
         n = lib.mnb_moe_workspace_size(M, top_k, g, u, d, code)
-        ws = _workspace(n, dev)
-        _check(lib.mnb_moe(_ptr(X), _ptr(logits), _dtype_code(logits.dtype), M, top_k,
-                           1 if normalize else 0, g, u, d, _ptr(out), code, _ptr(ws), n, s),
+        ws, wp = _workspace(n, dev)
+        _check(lib.mnb_moe(X.data_ptr(), logits.data_ptr(), lcode, M, top_k,
+                           1 if normalize else 0, g, u, d, Y.data_ptr(), code, wp, n, s),
                "mnb_moe")
-    return out
+        return Y
+    return _call_on(dev, stream, call)

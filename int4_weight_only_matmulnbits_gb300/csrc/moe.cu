@@ -12,6 +12,8 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
+#include <utility>
 
 #include "mnb_common.cuh"
 #include "mnb_launch.h"
@@ -25,6 +27,8 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
+constexpr int kPrepWarps = 32;  // a warp per token of a short input
+constexpr int kPrepThreads = kPrepWarps * 32;
 
 __device__ __forceinline__ void store_f(void *p, bool f32, int64_t i, float v) {
   if (f32) static_cast<float *>(p)[i] = v;
@@ -119,13 +123,15 @@ __global__ void __launch_bounds__(kThreads)
 
 // Slots by expert (one block): a stable counting sort. Each warp owns a
 // contiguous range of slots and a row of counters; slots without an expert
-// count as expert E.
+// count as expert E. Also the groups of up to 2^gt_log2 slots, when asked for.
 constexpr int kListWarps = 16;
 __global__ void __launch_bounds__(kListWarps * 32)
-    lists_kernel(const int32_t *experts, int64_t P, int E, int32_t *offsets, int32_t *order) {
-  extern __shared__ int32_t cnt[];  // [kListWarps][E + 1], then [E + 1]
+    lists_kernel(const int32_t *experts, int64_t P, int E, int32_t *offsets, int32_t *order,
+                 SlotGroup *groups, int32_t *n_groups, int gt_log2) {
+  extern __shared__ int32_t cnt[];  // [kListWarps][E + 1], then [E + 1] twice
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int32_t *mine = cnt + warp * (E + 1), *start = cnt + kListWarps * (E + 1);
+  int32_t *gstart = start + E + 1;
   grid_dependency_wait();
   grid_dependents_launch();
   for (int i = threadIdx.x; i < kListWarps * (E + 1); i += blockDim.x) cnt[i] = 0;
@@ -146,26 +152,34 @@ __global__ void __launch_bounds__(kListWarps * 32)
       sum += c;
     }
     start[e] = sum;
+    gstart[e] = e < E ? (sum + (1 << gt_log2) - 1) >> gt_log2 : 0;
   }
   __syncthreads();
-  if (warp == 0) {  // exclusive prefix over the experts
+  if (warp < 2) {  // exclusive prefixes over the experts: slots, groups
+    int32_t *v = warp ? gstart : start;
     int base = 0;
-    for (int i = 0; i <= E; i += 32) {
-      const int v = i + lane <= E ? start[i + lane] : 0;
-      int x = v;
+    for (int i = lane; i - lane <= E; i += 32) {
+      const int own = i <= E ? v[i] : 0;
+      int x = own;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
       }
-      if (i + lane <= E) {
-        start[i + lane] = base + x - v;
-        offsets[i + lane] = base + x - v;
-      }
+      if (i <= E) v[i] = base + x - own;
       base += __shfl_sync(0xffffffffu, x, 31);
     }
   }
   __syncthreads();
+  for (int e = threadIdx.x; e <= E; e += blockDim.x) {
+    offsets[e] = start[e];
+    if (groups && e < E) {
+      const int first = start[e], n = start[e + 1] - first, gt = 1 << gt_log2;
+      SlotGroup *g = groups + gstart[e];
+      for (int k = 0; k < n; k += gt) *g++ = SlotGroup{e, first + k, min(gt, n - k)};
+    }
+  }
+  if (groups && threadIdx.x == 0) *n_groups = gstart[E];
   for (int64_t p0 = lo; p0 < hi; p0 += 32) {
     const int64_t p = p0 + lane;
     const bool ok = p < hi;
@@ -179,29 +193,122 @@ __global__ void __launch_bounds__(kListWarps * 32)
   }
 }
 
-// Router and lists of a few slots in one block.
-__global__ void __launch_bounds__(kThreads) route_few_kernel(RouteArgs a) {
-  extern __shared__ __align__(16) int few_smem[];
-  const int P = static_cast<int>(a.M) * a.top_k;
-  const SlotLists L = slot_lists(few_smem, P, a.E);
-  uint32_t *keys = reinterpret_cast<uint32_t *>(few_smem + slot_lists_ints(P, a.E));
+// Bits of the largest magnitude of row `row` of A [.., K], by one block.
+__device__ __forceinline__ uint32_t row_top(const void *A, bool f32, bool vec, int64_t row,
+                                            int K, uint32_t *scratch) {
+  uint32_t top = 0;
+  const int64_t at = row * K;
+  if (vec) {
+    const uint4 *a = reinterpret_cast<const uint4 *>(static_cast<const char *>(A) +
+                                                     at * (f32 ? 4 : 2));
+    const int n = K / (f32 ? 4 : 8);
+#pragma unroll 2
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+      const uint4 x = a[i];
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        top = max(top, w[q] & (f32 ? 0x7FFFFFFFu : 0x7FFF0000u));
+        if (!f32) top = max(top, (w[q] << 16) & 0x7FFF0000u);
+      }
+    }
+  } else {
+    for (int i = threadIdx.x; i < K; i += blockDim.x)
+      top = max(top, (f32 ? static_cast<const uint32_t *>(A)[at + i]
+                          : uint32_t(static_cast<const uint16_t *>(A)[at + i]) << 16) &
+                         0x7FFFFFFFu);
+  }
+  top = __reduce_max_sync(0xffffffffu, top);
+  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = top;
+  __syncthreads();
+  const int lane = threadIdx.x & 31;
+  top = lane < blockDim.x >> 5 ? scratch[lane] : 0;
+  top = __reduce_max_sync(0xffffffffu, top);
+  return top;
+}
+
+// What the products need ahead, for a few slots, in one launch. Block 0: the
+// router (or a table of experts) and the lists; the blocks after it: the
+// largest magnitude of an activation row each, and cleared counters.
+struct PrepArgs {
+  const void *logits;    // the router, or null:
+  const int32_t *table;  // experts of the slots
+  int logits_f32, normalize;
+  int M, E, top_k, gt_log2;
+  float *weights;
+  int32_t *experts, *offsets, *order, *n_groups;  // weights, experts: router only
+  SlotGroup *groups;                              // and n_groups: may be null
+  const void *A;
+  int a_f32, a_vec, K, rows;
+  uint32_t *tops;
+  uint32_t *clear;  // words to clear
+  int n_clear;
+};
+__global__ void __launch_bounds__(kPrepThreads) prep_kernel(const PrepArgs a) {
+  extern __shared__ __align__(16) int prep_smem[];
+  __shared__ uint32_t scratch[kPrepWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int P = a.M * a.top_k;
+  const SlotLists L = slot_lists(prep_smem, P, a.E);
+  if (blockIdx.x == 0) clear_lists(L, a.E);
   grid_dependency_wait();
   grid_dependents_launch();
-  for (int m = warp; m < a.M; m += kWarps) {
-    int e;
-    float r;
-    route_row(a.logits, a.logits_f32, m, a.E, a.top_k, a.normalize, keys + warp * a.E, e, r);
-    if (lane < a.top_k) {
-      a.experts[m * a.top_k + lane] = e;
-      a.weights[m * a.top_k + lane] = r;
-      L.e[m * a.top_k + lane] = e < 0 ? a.E : e;
+  if (blockIdx.x > 0) {
+    if (blockIdx.x == 1)
+      for (int i = threadIdx.x; i < a.n_clear; i += kPrepThreads) a.clear[i] = 0;
+    const int64_t row = blockIdx.x - 1;
+    const uint32_t top = row_top(a.A, a.a_f32, a.a_vec, row, a.K, scratch);
+    if (threadIdx.x == 0) a.tops[row] = top;
+    return;
+  }
+  if (a.logits) {
+    uint32_t *keys = reinterpret_cast<uint32_t *>(prep_smem + slot_lists_ints(P, a.E)) + warp * a.E;
+#pragma unroll 1
+    for (int m = warp; m < a.M; m += kPrepWarps) {
+      int e;
+      float r;
+      route_row(a.logits, a.logits_f32, m, a.E, a.top_k, a.normalize, keys, e, r);
+      if (lane < a.top_k) {
+        const int q = m * a.top_k + lane;
+        a.experts[q] = e;
+        a.weights[q] = r;
+        L.e[q] = e < 0 ? a.E : e;
+      }
+    }
+  } else {
+    for (int i = threadIdx.x; i < P; i += kPrepThreads) {
+      const int e = a.table[i];
+      L.e[i] = e >= 0 && e < a.E ? e : a.E;
     }
   }
   __syncthreads();
-  build_lists(L, P, a.E, 1);
-  for (int i = threadIdx.x; i <= a.E; i += kThreads) a.offsets[i] = L.off[i];
-  for (int i = threadIdx.x; i < P; i += kThreads) a.order[i] = L.order[i];
+  build_lists(L, P, a.E, a.gt_log2);
+#pragma unroll 1
+  for (int i = threadIdx.x; i <= a.E; i += kPrepThreads) a.offsets[i] = L.off[i];
+#pragma unroll 1
+  for (int i = threadIdx.x; i < P; i += kPrepThreads) a.order[i] = L.order[i];
+  if (a.groups) {
+#pragma unroll 1
+    for (int i = threadIdx.x; i < *L.ngrp; i += kPrepThreads) a.groups[i] = L.grp[i];
+    if (threadIdx.x == 0) *a.n_groups = *L.ngrp;
+  }
+}
+
+// The row magnitudes of many rows, and cleared words.
+__global__ void __launch_bounds__(kThreads)
+    row_tops_kernel(const void *A, bool f32, bool vec, int64_t rows, int K, uint32_t *tops,
+                    uint32_t *clear, int64_t n_clear) {
+  __shared__ uint32_t scratch[kWarps];
+  grid_dependency_wait();
+  grid_dependents_launch();
+  for (int64_t i = blockIdx.x * int64_t(kThreads) + threadIdx.x; i < n_clear;
+       i += int64_t(gridDim.x) * kThreads)
+    clear[i] = 0;
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+    const uint32_t top = row_top(A, f32, vec, row, K, scratch);
+    if (threadIdx.x == 0) tops[row] = top;
+    __syncthreads();
+  }
 }
 
 // Sum of each token's down partials, in slot order (long inputs).
@@ -271,16 +378,15 @@ int ilog2(int x) {
   return r;
 }
 
-// Fills the geometry of a weight-streaming launch. `lists_p`: slots listed in
-// shared memory (0: ready lists); `per_expert`: the most slots an expert can
-// have. false: not even one activation row fits.
+// Fills the geometry of a weight-streaming launch. `per_expert`: the most
+// slots an expert can have. false: not even one activation row fits.
 struct StreamPlan {
   StreamParams p{};
   int terms = 1, grid = 1, smem = 0;
   bool zp = false, sf32 = false;
 };
 bool plan_stream(StreamPlan &pl, const ExpertStack &w, int mode, int terms, int64_t P,
-                 int64_t M, int top_k, bool few, int64_t per_expert, bool keys) {
+                 int64_t M, int top_k, int64_t per_expert) {
   StreamParams &p = pl.p;
   pl.terms = terms;
   pl.zp = w.z != nullptr;
@@ -294,48 +400,68 @@ bool plan_stream(StreamPlan &pl, const ExpertStack &w, int mode, int terms, int6
   p.nb = static_cast<int>(ceil_div(w.K, w.bs));
   p.nbz = (p.nb + 1) / 2 * 2;
   p.bs_log2 = ilog2(w.bs);
+  p.npair = mode == kStreamGateUp ? p.N16 : (p.N16 + 1) / 2;
   p.P = static_cast<int>(P);
   p.M = static_cast<int>(M);
   p.top_k = top_k;
-  const int nmat = mode == kStreamGateUp ? 2 : 1, es = w.s_f32 ? 4 : 2;
-  // k ranges of at least three chunks per warp.
-  p.ksplit = 8;
-  while (p.ksplit > 1 && p.K64 / p.ksplit < 3) p.ksplit /= 2;
+  const int es = w.s_f32 ? 4 : 2;
+  // Warps per pair: what makes the longest run of work shortest, in chunks,
+  // with the distinct experts that P random slots name; a step costs a warp
+  // that has its pair to itself about five chunks more (it stores alone),
+  // otherwise one and half a chunk per warp that meets. Measured on 16 tokens
+  // of 8 out of 128 experts, 2560 -> 768 -> 2560: 109 us for 4 and 2 warps
+  // (this rule's choice), 126 for 8 and 1.
+  const double E = w.E, distinct = E * (1 - std::pow(1 - 1 / E, double(P)));
+  const int64_t groups = std::max<int64_t>(1, std::max<int64_t>(std::llround(distinct), P / 8));
+  double best = 0;
+  for (int ks = 1; ks <= 8 && ks <= p.K64; ks *= 2) {
+    const int64_t steps = groups * ceil_div(p.npair, 8 / ks);
+    const double cost = double(ceil_div(steps, kStreamCtas * sm_count())) *
+                        (ceil_div(p.K64, ks) + (ks == 1 ? 5 : 1 + ks / 2));
+    if (ks == 1 || cost < best) {
+      best = cost;
+      p.ksplit = ks;
+    }
+  }
   p.tpu = 8 / p.ksplit;
-  p.ns = static_cast<int>(ceil_div(p.N16, p.tpu));
-  const int range = static_cast<int>(ceil_div(p.K64, p.ksplit));
-  p.kc = static_cast<int>(ceil_div(range, ceil_div(range, 4)));
-  const int nblk = (p.kc * kChunkK + w.bs - 1) / w.bs + 1;
-  p.st_scale = p.kc * kChunkBytes;
-  p.st_zp = p.st_scale + (nblk * kTileN * es + 15) / 16 * 16;
-  p.st_bytes = (p.st_zp + (pl.zp ? (nblk / 2 + 1) * 16 : 0) + 127) / 128 * 128;
+  p.tpu_log2 = ilog2(p.tpu);
+  p.ns = static_cast<int>(ceil_div(p.npair, p.tpu));
+  // Scale blocks a stage can touch (blocks of up to 64 codes lie inside chunks).
+  const int nblk = w.bs <= kChunkK ? kStreamChunks * kChunkK / w.bs
+                                   : (kStreamChunks * kChunkK - 1) / w.bs + 2;
+  p.st_scale = kStreamChunks * kChunkBytes;
+  p.st_zp = p.st_scale + nblk * kTileN * es;
+  p.st_tile = p.st_zp + (pl.zp ? (nblk / 2 + 1) * 16 : 0);
+  p.st_bytes = 2 * p.st_tile;
   const int64_t krow = int64_t(p.K64) * kChunkK + 16;
-  const int64_t lists =
-      (int64_t(slot_lists_ints(few ? p.P : 0, p.E)) * 4 + (few ? p.P * 4 : 0) + 127) / 128 * 128;
-  const int red = 2 * 8 * nmat * kTileN * 8 * 4;
-  const int64_t ring =
-      std::max<int64_t>(8 * 4 * p.st_bytes, keys ? int64_t(8) * p.E * 4 : 0);
+  const int64_t sums = terms == 1 ? int64_t(p.K64) * std::max(1, kChunkK / w.bs) * 64 : 0;
+  const int64_t ring = 8 * kStreamStages * p.st_bytes;
   // Slots per group: about twice the mean list, so that few experts need a
   // second pass over their weights, within what two CTAs per SM leave (one
   // CTA per SM when that is not enough for the mean).
   const int64_t mean = ceil_div(P, w.E);
   int want = 1;
   while (want < 8 && want < 2 * mean && want < per_expert) want *= 2;
-  constexpr int64_t kHalf = 113 * 1024, kFull = 226 * 1024;
-  auto bytes = [&](int gt) { return lists + red + ring + int64_t(terms) * gt * krow * 2; };
+  // Shared memory that lets n CTAs share an SM (1 KB of each is the system's).
+  constexpr int64_t kTotal = 228 * 1024, kStatic = 1536;
+  auto room = [&](int n) { return kTotal / n - kStatic; };
+  auto bytes = [&](int gt) {
+    return sums + ring + 2 * 2 * 8 * kTileN * gt * 4 + (int64_t(terms) * gt * krow * 2 + 127) / 128 * 128;
+  };
   int gt = want;
-  while (gt > 1 && bytes(gt) > kHalf && gt > mean) gt /= 2;
-  while (gt > 1 && bytes(gt) > kFull) gt /= 2;
-  if (bytes(gt) > kFull) return false;
-  p.gt = gt;
+  while (gt > 1 && bytes(gt) > room(kStreamCtas) && gt > mean) gt /= 2;
+  while (gt > 1 && bytes(gt) > room(1)) gt /= 2;
+  if (bytes(gt) > room(1)) return false;
+  p.gt_log2 = ilog2(gt);
   p.krow = static_cast<int>(krow);
-  p.off_lists = 0;
-  p.off_keys = slot_lists_ints(few ? p.P : 0, p.E) * 4;
-  p.off_red = static_cast<int>(lists);
-  p.off_ring = p.off_red + red;
+  p.off_red = 0;
+  p.off_sums = 2 * 2 * 8 * kTileN * gt * 4;
+  p.off_ring = static_cast<int>(p.off_sums + sums);
   p.off_x = static_cast<int>(p.off_ring + ring);
   pl.smem = static_cast<int>(bytes(gt));
-  const int64_t most = P * p.ns, slots = int64_t(sm_count()) * (pl.smem <= kHalf ? 2 : 1);
+  int ctas = kStreamCtas;
+  while (pl.smem > room(ctas)) --ctas;
+  const int64_t most = P * p.ns, slots = int64_t(sm_count()) * ctas;
   if (most > (int64_t(1) << 31) - 1) return false;
   pl.grid = static_cast<int>(std::min(most, slots));
   return true;
@@ -372,43 +498,109 @@ struct Carve {
 // The lists of many slots in global memory.
 struct Lists {
   float *weights = nullptr;
-  int32_t *experts = nullptr, *offsets = nullptr, *order = nullptr;
+  int32_t *experts = nullptr, *offsets = nullptr, *order = nullptr, *n_groups = nullptr;
+  SlotGroup *groups = nullptr;
 };
 
-cudaError_t launch_lists(const int32_t *experts, int64_t P, int E, int32_t *offsets,
-                         int32_t *order, bool pdl, cudaStream_t stream) {
+// Groups of P slots at most: every expert may leave one partly filled.
+size_t max_groups(int64_t P, int E, int gt_log2) {
+  return std::min<int64_t>(P, (P >> gt_log2) + E);
+}
+
+cudaError_t launch_lists(const int32_t *experts, int64_t P, int E, const Lists &l, int gt_log2,
+                         bool pdl, cudaStream_t stream) {
   static std::atomic<unsigned long long> done{0};
   const cudaError_t e = ensure_smem_limit(
-      lists_kernel, (kListWarps + 1) * (kMoeMaxExperts + 1) * 4, done);
+      lists_kernel, (kListWarps + 2) * (kMoeMaxExperts + 1) * 4, done);
   if (e != cudaSuccess) return e;
-  return launch_pdl(lists_kernel, 1, kListWarps * 32, size_t(kListWarps + 1) * (E + 1) * 4, pdl,
-                    stream, experts, P, E, offsets, order);
+  return launch_pdl(lists_kernel, 1, kListWarps * 32, size_t(kListWarps + 2) * (E + 1) * 4, pdl,
+                    stream, experts, P, E, l.offsets, l.order, l.groups, l.n_groups, gt_log2);
+}
+
+// Slots that one block lists by itself (prep_kernel); more take the router,
+// the lists and the row magnitudes as kernels of their own.
+constexpr int kFewSlots = 256;
+
+Lists take_lists(Carve &c, int64_t P, int E, bool routed) {
+  Lists l;
+  if (routed) {
+    l.weights = c.take<float>(P);
+    l.experts = c.take<int32_t>(P);
+  }
+  l.offsets = c.take<int32_t>(E + 1);
+  l.order = c.take<int32_t>(P);
+  l.n_groups = c.take<int32_t>(1);
+  l.groups = c.take<SlotGroup>(max_groups(P, E, 0));
+  return l;
 }
 
 struct MoeSpace {
   Lists l;
-  uint16_t *hidden;
-  float *part;
-  unsigned *counters;
+  uint32_t *tops, *clear;  // clear: hidden tops [P], then the counters
+  float *hidden, *part;
   size_t bytes;
 };
+// Hidden rows start on 16 bytes.
+size_t hidden_ld(const MoeArgs &a) { return ceil_div(a.gate.N, 4) * 4; }
+size_t moe_clear_words(const MoeArgs &a) {
+  return size_t(a.M) * a.top_k + ceil_div(a.down.N, kTileN);
+}
+
 MoeSpace moe_space(const MoeArgs &a) {
   const size_t P = size_t(a.M) * a.top_k;
   Carve c{a.ws};
   MoeSpace s{};
-  if (P > kFewSlots) {
-    s.l.weights = c.take<float>(P);
-    s.l.experts = c.take<int32_t>(P);
-    s.l.offsets = c.take<int32_t>(a.gate.E + 1);
-    s.l.order = c.take<int32_t>(P);
-  } else {
-    s.counters = c.take<unsigned>(ceil_div(a.down.N, kTileN));
-  }
-  const size_t ldh = ceil_div(a.gate.N, 8) * 8;
-  s.hidden = c.take<uint16_t>((a.a_f32 ? 3 : 2) * P * ldh);
+  s.l = take_lists(c, P, a.gate.E, true);
+  s.tops = c.take<uint32_t>(a.M);
+  s.clear = c.take<uint32_t>(moe_clear_words(a));
+  s.hidden = c.take<float>(P * hidden_ld(a));
   s.part = c.take<float>(P * a.down.N);
   s.bytes = c.used;
   return s;
+}
+
+struct ExpertsSpace {
+  Lists l;
+  uint32_t *tops;
+  size_t bytes;
+};
+ExpertsSpace experts_space(const ExpertsArgs &a) {
+  const size_t P = size_t(a.M) * a.top_k;
+  Carve c{a.ws};
+  ExpertsSpace s{};
+  s.l = take_lists(c, P, a.w.E, false);
+  s.tops = c.take<uint32_t>(a.per_slot ? P : a.M);
+  s.bytes = c.used;
+  return s;
+}
+
+cudaError_t launch_prep(const PrepArgs &a, bool pdl, cudaStream_t stream) {
+  const int P = a.M * a.top_k;
+  // Keys in shared memory for more experts than registers hold.
+  const size_t smem =
+      size_t(slot_lists_ints(P, a.E) + (a.logits && a.E > 256 ? kPrepWarps * a.E : 0)) * 4;
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = ensure_smem_limit(
+      prep_kernel, (slot_lists_ints(kFewSlots, kMoeMaxExperts) + kPrepWarps * kMoeMaxExperts) * 4,
+      done);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(prep_kernel, 1 + a.rows, kPrepThreads, smem, pdl, stream, a);
+}
+
+cudaError_t launch_row_tops(const void *A, bool f32, bool vec, int64_t rows, int K,
+                            uint32_t *tops, uint32_t *clear, int64_t n_clear, bool pdl,
+                            cudaStream_t stream) {
+  return launch_pdl(row_tops_kernel, grid_of(rows, 1), kThreads, 0, pdl, stream, A, f32, vec,
+                    rows, K, tops, clear, n_clear);
+}
+
+void set_lists(StreamParams &p, const Lists &l) {
+  p.offsets = l.offsets;
+  p.order = l.order;
+  p.n_groups = l.n_groups;
+  p.groups = l.groups;
+  p.experts = l.experts;
+  p.weights = l.weights;
 }
 
 }  // namespace
@@ -418,46 +610,78 @@ size_t moe_route_workspace_bytes(int64_t, int, int) { return 0; }
 cudaError_t launch_moe_route(const RouteArgs &a, cudaStream_t stream) {
   const int64_t P = a.M * a.top_k;
   if (a.order && P <= kFewSlots) {
-    const size_t smem = size_t(slot_lists_ints(static_cast<int>(P), a.E) + kWarps * a.E) * 4;
-    return launch_pdl(route_few_kernel, 1, kThreads, smem, a.pdl, stream, a);
+    PrepArgs r{};
+    r.logits = a.logits;
+    r.logits_f32 = a.logits_f32;
+    r.normalize = a.normalize;
+    r.M = static_cast<int>(a.M);
+    r.E = a.E;
+    r.top_k = a.top_k;
+    r.weights = a.weights;
+    r.experts = a.experts;
+    r.offsets = a.offsets;
+    r.order = a.order;
+    return launch_prep(r, a.pdl, stream);
   }
   cudaError_t e = launch_pdl(route_kernel, grid_of(a.M, kWarps), kThreads,
                              size_t(kWarps) * a.E * 4, a.pdl, stream, a.logits, a.logits_f32,
                              a.M, a.E, a.top_k, a.normalize, a.weights, a.experts);
-  if (e == cudaSuccess && a.order)
-    e = launch_lists(a.experts, P, a.E, a.offsets, a.order, a.pdl, stream);
+  if (e == cudaSuccess && a.order) {
+    Lists l;
+    l.offsets = a.offsets;
+    l.order = a.order;
+    e = launch_lists(a.experts, P, a.E, l, 0, a.pdl, stream);
+  }
   return e;
 }
 
 size_t matmul_experts_workspace_bytes(const ExpertsArgs &a) {
-  const size_t P = size_t(a.M) * a.top_k;
-  if (P <= kFewSlots) return 0;
-  return align256(size_t(a.w.E + 1) * 4) + align256(P * 4);
+  ExpertsArgs b = a;
+  b.ws = nullptr;
+  return experts_space(b).bytes;
 }
 
 cudaError_t launch_matmul_experts(const ExpertsArgs &a, cudaStream_t stream) {
-  const int64_t P = a.M * a.top_k;
-  const bool few = P <= kFewSlots;
+  const int64_t P = a.M * a.top_k, rows = a.per_slot ? P : a.M;
   StreamPlan pl;
-  if (!plan_stream(pl, a.w, kStreamProduct, a.a_f32 ? 3 : 1, P, a.M, a.top_k, few, P, false))
+  if (!plan_stream(pl, a.w, kStreamProduct, a.a_f32 ? 2 : 1, P, a.M, a.top_k, P))
     return cudaErrorNotSupported;
-  Lists l;
-  if (!few) {
-    Carve c{a.ws};
-    l.offsets = c.take<int32_t>(a.w.E + 1);
-    l.order = c.take<int32_t>(P);
-    const cudaError_t e =
-        launch_lists(a.experts, P, a.w.E, l.offsets, l.order, a.pdl, stream);
-    if (e != cudaSuccess) return e;
+  const ExpertsSpace s = experts_space(a);
+  const bool vec = vec_rows(a.A, a.w.K, a.a_f32 ? 4 : 2);
+  cudaError_t e;
+  if (P <= kFewSlots) {
+    PrepArgs r{};
+    r.table = a.experts;
+    r.M = static_cast<int>(a.M);
+    r.E = a.w.E;
+    r.top_k = a.top_k;
+    r.gt_log2 = pl.p.gt_log2;
+    r.offsets = s.l.offsets;
+    r.order = s.l.order;
+    r.n_groups = s.l.n_groups;
+    r.groups = s.l.groups;
+    r.A = a.A;
+    r.a_f32 = a.a_f32;
+    r.a_vec = vec;
+    r.K = a.w.K;
+    r.rows = static_cast<int>(rows);
+    r.tops = s.tops;
+    e = launch_prep(r, a.pdl, stream);
+  } else {
+    e = launch_lists(a.experts, P, a.w.E, s.l, pl.p.gt_log2, a.pdl, stream);
+    if (e == cudaSuccess)
+      e = launch_row_tops(a.A, a.a_f32, vec, rows, a.w.K, s.tops, nullptr, 0, a.pdl, stream);
   }
+  if (e != cudaSuccess) return e;
   StreamParams &p = pl.p;
-  p.w[0] = stream_mat(a.w);
+  set_lists(p, s.l);
+  p.w[0] = p.w[1] = stream_mat(a.w);
   p.A = a.A;
-  p.a_vec = vec_rows(a.A, a.w.K, a.a_f32 ? 4 : 2);
+  p.a_vec = vec;
+  p.a_f32 = a.a_f32;
   p.per_slot = a.per_slot;
-  p.table = a.experts;
-  p.offsets = l.offsets;
-  p.order = l.order;
+  p.ld = a.w.K;
+  p.tops = s.tops;
   p.Y = a.Y;
   p.y_f32 = a.a_f32;
   return run_stream(pl, a.pdl, stream);
@@ -474,46 +698,74 @@ cudaError_t launch_moe(const MoeArgs &a, cudaStream_t stream) {
   const bool few = P <= kFewSlots;
   const MoeSpace s = moe_space(a);
   StreamPlan up, down;
-  if (!plan_stream(up, a.gate, kStreamGateUp, a.a_f32 ? 3 : 1, P, a.M, a.top_k, few, a.M, few) ||
-      !plan_stream(down, a.down, kStreamDown, a.a_f32 ? 3 : 2, P, a.M, a.top_k, few, a.M, few))
+  const int terms = a.a_f32 ? 2 : 1;
+  if (!plan_stream(up, a.gate, kStreamGateUp, terms, P, a.M, a.top_k, a.M) ||
+      !plan_stream(down, a.down, kStreamDown, terms, P, a.M, a.top_k, a.M))
     return cudaErrorNotSupported;
-  if (!few) {
+  // Both launches use the lists: groups of the size that fits both.
+  up.p.gt_log2 = down.p.gt_log2 = std::min(up.p.gt_log2, down.p.gt_log2);
+  const bool vec = vec_rows(a.X, a.gate.K, a.a_f32 ? 4 : 2);
+  const int64_t n_clear = moe_clear_words(a);
+  cudaError_t e;
+  if (few) {
+    PrepArgs r{};
+    r.logits = a.logits;
+    r.logits_f32 = a.logits_f32;
+    r.normalize = a.normalize;
+    r.M = static_cast<int>(a.M);
+    r.E = a.gate.E;
+    r.top_k = a.top_k;
+    r.gt_log2 = up.p.gt_log2;
+    r.weights = s.l.weights;
+    r.experts = s.l.experts;
+    r.offsets = s.l.offsets;
+    r.order = s.l.order;
+    r.n_groups = s.l.n_groups;
+    r.groups = s.l.groups;
+    r.A = a.X;
+    r.a_f32 = a.a_f32;
+    r.a_vec = vec;
+    r.K = a.gate.K;
+    r.rows = static_cast<int>(a.M);
+    r.tops = s.tops;
+    r.clear = s.clear;
+    r.n_clear = static_cast<int>(n_clear);
+    e = launch_prep(r, a.pdl, stream);
+  } else {
     const RouteArgs r{a.logits, a.logits_f32, a.M, a.gate.E, a.top_k, a.normalize, s.l.weights,
-                      s.l.experts, s.l.offsets, s.l.order, nullptr, a.pdl};
-    const cudaError_t e = launch_moe_route(r, stream);
-    if (e != cudaSuccess) return e;
+                      s.l.experts, nullptr, nullptr, nullptr, a.pdl};
+    e = launch_moe_route(r, stream);
+    if (e == cudaSuccess)
+      e = launch_lists(s.l.experts, P, a.gate.E, s.l, up.p.gt_log2, a.pdl, stream);
+    if (e == cudaSuccess)
+      e = launch_row_tops(a.X, a.a_f32, vec, a.M, a.gate.K, s.tops, s.clear, n_clear, a.pdl,
+                          stream);
   }
-  for (StreamParams *p : {&up.p, &down.p}) {
-    if (few) {
-      p->logits = a.logits;
-      p->logits_f32 = a.logits_f32;
-      p->normalize = a.normalize;
-    } else {
-      p->offsets = s.l.offsets;
-      p->order = s.l.order;
-      p->weights = s.l.weights;
-      p->experts = s.l.experts;
-    }
-    p->y_f32 = a.a_f32;
-    p->plane = P * (ceil_div(a.gate.N, 8) * 8);
-    p->ldh = static_cast<int>(ceil_div(a.gate.N, 8) * 8);
-    p->counters = s.counters;
-  }
+  if (e != cudaSuccess) return e;
+  set_lists(up.p, s.l);
   up.p.w[0] = stream_mat(a.gate);
   up.p.w[1] = stream_mat(a.up);
   up.p.A = a.X;
-  up.p.a_vec = vec_rows(a.X, a.gate.K, a.a_f32 ? 4 : 2);
+  up.p.a_vec = vec;
+  up.p.a_f32 = a.a_f32;
+  up.p.ld = a.gate.K;
+  up.p.tops = s.tops;
   up.p.hidden = s.hidden;
-  up.p.h_planes = a.a_f32 ? 3 : 2;
-  up.p.n_counters = few ? down.p.ns : 0;
-  cudaError_t e = run_stream(up, a.pdl, stream);
+  up.p.hidden_tops = s.clear;
+  up.p.ldh = hidden_ld(a);
+  e = run_stream(up, a.pdl, stream);
   if (e != cudaSuccess) return e;
-  down.p.w[0] = stream_mat(a.down);
+  set_lists(down.p, s.l);
+  down.p.w[0] = down.p.w[1] = stream_mat(a.down);
   down.p.A = s.hidden;
-  down.p.a_vec = 1;
+  down.p.a_f32 = down.p.a_vec = down.p.per_slot = 1;
+  down.p.ld = hidden_ld(a);
+  down.p.tops = s.clear;
   down.p.part = s.part;
   down.p.Y = a.Y;
-  down.p.early = few;
+  down.p.y_f32 = a.a_f32;
+  down.p.counters = few ? s.clear + P : nullptr;
+  down.p.early = a.pdl;
   e = run_stream(down, a.pdl, stream);
   if (e != cudaSuccess || few) return e;
   return launch_pdl(combine_kernel, grid_of(a.M * a.down.N, kThreads), kThreads, 0, a.pdl,

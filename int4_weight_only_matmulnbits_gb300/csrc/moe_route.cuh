@@ -40,9 +40,64 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// Lane j < top_k returns choice j of row m: expert (or -1) and weight.
-// keys: E words of shared memory of this warp.
-__device__ __forceinline__ void route_row(const void *logits, bool f32, int64_t m, int E,
+// Lane j < top_k gets choice j of row m: expert (or -1) and weight. Lane l
+// holds the keys of experts l, l + 32, ... in KPL registers (32 KPL >= E).
+template <int KPL>
+__device__ __forceinline__ void route_row_regs(const void *logits, bool f32, int64_t m, int E,
+                                               int top_k, bool normalize, int &expert,
+                                               float &weight) {
+  const int lane = threadIdx.x & 31;
+  uint32_t key[KPL];
+#pragma unroll
+  for (int q = 0; q < KPL; ++q) {
+    const int i = lane + 32 * q;
+    float x = -INFINITY;
+    if (i < E)
+      x = f32 ? static_cast<const float *>(logits)[m * E + i]
+              : bf16_bits_to_f32(static_cast<const uint16_t *>(logits)[m * E + i]);
+    key[q] = logit_key(x);
+  }
+  uint32_t first = 0, mine = 0;
+  expert = -1;
+  float all = 0.f;
+#pragma unroll 1
+  for (int j = 0; j < top_k; ++j) {
+    uint32_t best = key[0];
+    int bi = lane;
+#pragma unroll
+    for (int q = 1; q < KPL; ++q)
+      if (key[q] > best) {
+        best = key[q];
+        bi = lane + 32 * q;
+      }
+    const uint32_t win = __reduce_max_sync(0xffffffffu, best);
+    if (win == 0) break;  // every expert left is masked
+    const int at = static_cast<int>(
+        __reduce_min_sync(0xffffffffu, best == win ? static_cast<uint32_t>(bi) : 0xFFFFFFFFu));
+    if (j == 0) {
+      first = win;
+      if (!normalize) {
+#pragma unroll
+        for (int q = 0; q < KPL; ++q)
+          if (key[q]) all += logit_exp(key_logit(key[q]), key_logit(win));
+        all = warp_sum(all);
+      }
+    }
+    if (lane == j) {
+      expert = at;
+      mine = win;
+    }
+#pragma unroll
+    for (int q = 0; q < KPL; ++q)
+      if (at == lane + 32 * q) key[q] = 0;
+  }
+  const float p = expert < 0 ? 0.f : logit_exp(key_logit(mine), key_logit(first));
+  const float chosen = warp_sum(p);
+  weight = expert < 0 ? 0.f : p / (normalize ? chosen : all);
+}
+
+// The same with the keys in E words of shared memory of this warp (any E).
+__device__ __forceinline__ void route_row_shared(const void *logits, bool f32, int64_t m, int E,
                                           int top_k, bool normalize, uint32_t *keys,
                                           int &expert, float &weight) {
   const int lane = threadIdx.x & 31;
@@ -89,6 +144,16 @@ __device__ __forceinline__ void route_row(const void *logits, bool f32, int64_t 
   }
   const float chosen = warp_sum(p);
   weight = expert < 0 ? 0.f : p / (normalize ? chosen : all);
+}
+
+// keys: E words of shared memory of this warp (used when E > 256).
+__device__ __forceinline__ void route_row(const void *logits, bool f32, int64_t m, int E,
+                                          int top_k, bool normalize, uint32_t *keys,
+                                          int &expert, float &weight) {
+  if (E <= 64) route_row_regs<2>(logits, f32, m, E, top_k, normalize, expert, weight);
+  else if (E <= 128) route_row_regs<4>(logits, f32, m, E, top_k, normalize, expert, weight);
+  else if (E <= 256) route_row_regs<8>(logits, f32, m, E, top_k, normalize, expert, weight);
+  else route_row_shared(logits, f32, m, E, top_k, normalize, keys, expert, weight);
 }
 
 }  // namespace mnb

@@ -6,42 +6,50 @@
 //   product     Y[p]    = W_e a_p + b_e
 //   gate + up   h[p]    = r_p * silu(Wg_e x + bg) * (Wu_e x + bu)
 //   down        Y[m]    = sum over the slots of m of (Wd_e h[p] + r_p bd)
-// Every weight byte is read once per group, 24 bytes a cycle and SM at full
-// memory bandwidth, while a 512-byte chunk (64 k of 16 rows) costs a warp
-// about 80 instructions: memory bounds it, with little to spare, as long as
-// enough bytes are in flight.
+// Every weight byte is read once per group. At full memory bandwidth an SM
+// receives 24 bytes a cycle, so a 512-byte chunk (64 k of 16 rows) may take
+// it about 24 cycles, some 60 to 70 issued instructions: the unpacking, not
+// the products, is what competes with the memory.
 //
-//  * Warps are autonomous: each streams its own sequence of (tile, k range)
-//    pieces through a private ring of shared-memory stages filled by
-//    asynchronous 16-byte copies, across steps, tiles and experts. No
-//    barrier is needed to refill a stage, and a lane reads back the very
-//    16 bytes it copied.
-//  * A step is `tpu` tiles of one group; `ksplit` warps share a tile's k and
-//    meet in shared memory, in fixed order, once per step. CTAs take equal
-//    contiguous runs of steps, so a group's activations are staged about
-//    once per CTA.
-//  * Codes become bf16 q - z exactly (128 + q by one logic operation per
-//    pair, minus 128 + z), the products with bf16 activations are exact in
-//    fp32, and a block's scale is applied to its fp32 sum: no weight is
-//    rounded. fp32 activations enter as three bf16 parts by truncation
-//    (8 + 8 + 8 bits: their sum is the value), hidden values as two (bf16
-//    activations, 2^-16) or three.
-//  * The layer takes two launches. Both run the router for themselves, so
-//    the second needs nothing from the first but the hidden rows: it routes
-//    and fills its rings before it waits for the first kernel to finish.
-//    Down partials go to a workspace; the CTA that completes a column
-//    group, by an arrival counter, adds them in slot order, so the result
-//    does not depend on which CTA that is.
+//  * Activations become fp16, each row scaled by a power of two so that its
+//    largest magnitude lies in 2^14 .. 2^15 (bf16 values are then exact down
+//    to 2^-28 of it); fp32 activations become two fp16 parts, 22 bits.
+//  * A code becomes an fp16 by one logic operation per pair: 1024 + q for
+//    the low nibble of a byte (tile rows 0-7), 1024 + 16 q for the high one
+//    (rows 8-15, whose sums are 16 times too large until the end); one shift
+//    per eight codes. For one-part activations the offset comes off a block
+//    as a whole: the MMA sums of a block start at minus the offset times the
+//    block's sum of activations (staged beside them). That costs rounding of
+//    2^-24 of some 200 times the result, far below a bf16 result's; two-part
+//    activations (fp32 results) take it off every code exactly.
+//  * A block's scale is applied to its fp32 sums: no weight is rounded.
+//  * Warps are autonomous: each streams its own sequence of (tile pair, k
+//    range) pieces through a private ring of shared-memory stages filled by
+//    asynchronous 16-byte copies, across tiles and experts. No barrier is
+//    needed to refill a stage, and a lane reads back the very 16 bytes of
+//    codes it copied. A warp works on two tiles at a time (gate and up of
+//    the same rows, or two neighbours), which share the activation loads.
+//  * A step is `tpu` pairs of one group; `ksplit` warps share a pair's k and
+//    meet in shared memory, in fixed order (ksplit 1: no meeting, no
+//    barrier). CTAs take equal contiguous runs of steps, so a group's
+//    activations are staged about once per CTA.
+//  * The lists and the rows' largest magnitudes come from a small kernel
+//    ahead (moe.cu); the layer is two launches of this one. The second needs
+//    nothing from the first but the hidden rows and their magnitudes: it
+//    fills its rings before it waits for the first to finish. Down partials
+//    go to a workspace; whoever completes a column range, by an arrival
+//    counter, adds them in slot order, so the result does not depend on who
+//    that is.
+//  * What runs once per launch is kept short and rolled up: fetching
+//    instructions is most of the time of a call for one token.
 #pragma once
 
-#include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include <atomic>
 
 #include "mnb_common.cuh"
 #include "mnb_launch.h"
-#include "moe_lists.cuh"
-#include "moe_route.cuh"
 #include "moe_stream.h"
 
 namespace mnb {
@@ -49,8 +57,9 @@ namespace stream {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kCols = 8;    // slots per group at most
-constexpr int kStages = 4;  // ring depth per warp
+constexpr int kCols = 8;  // slots per group at most
+constexpr int kStages = kStreamStages;
+constexpr int kChunks = kStreamChunks;  // chunks per stage and tile
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src) {
   asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src)
@@ -62,366 +71,487 @@ __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-__device__ __forceinline__ uint32_t bf16x2_sub(uint32_t a, uint32_t b) {
+// D += A * B, m16n8k16, fp16 inputs, fp32 accumulate.
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint2 b) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b.x), "r"(b.y));
+}
+
+// D = A * B + C.
+__device__ __forceinline__ void mma_f16_from(float (&d)[4], const uint32_t (&a)[4], uint2 b,
+                                             float c0, float c1, float c2, float c3) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b.x), "r"(b.y), "f"(c0), "f"(c1),
+        "f"(c2), "f"(c3));
+}
+
+// Eight codes: pairs of 1024 + q (rows g: r[0], r[2]) and of 1024 + 16 q
+// (rows g + 8: r[1], r[3]).
+__device__ __forceinline__ void codes_to_f16x2(uint32_t w, uint32_t (&r)[4]) {
+  constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u, kMagic = 0x64006400u;
+  r[0] = lop3_and_or(w, kLow, kMagic);
+  r[1] = lop3_and_or(w, kHigh, kMagic);
+  w >>= 8;
+  r[2] = lop3_and_or(w, kLow, kMagic);
+  r[3] = lop3_and_or(w, kHigh, kMagic);
+}
+__device__ __forceinline__ uint32_t f16x2_sub(uint32_t a, uint32_t b) {
   uint32_t d;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
+}
+__device__ __forceinline__ uint32_t f16x2_fma(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+// The power of two that brings a row whose largest magnitude has the bits
+// `top` into 2^14 .. 2^15 (1 for rows of zeros and rows that are not finite;
+// at most 2^126), as an exponent.
+__device__ __forceinline__ int row_shift(uint32_t top) {
+  const int e = static_cast<int>(top >> 23);
+  if (top == 0u || e == 255) return 0;
+  return min(14 - (e - 127), 126);
+}
+__device__ __forceinline__ float exp2i(int k) {  // 2^k, |k| <= 126
+  return __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
+}
+
+// Eight consecutive activations from element k of a row, zeros past K.
+__device__ __forceinline__ void load8(const void *A, bool f32, bool vec, int64_t row, int k,
+                                      int K, float (&v)[8]) {
+  if (vec && k + 8 <= K) {
+    if (f32) {
+      const float4 *a = reinterpret_cast<const float4 *>(static_cast<const float *>(A) + row + k);
+      const float4 x = a[0], y = a[1];
+      v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+      v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
+    } else {
+      const uint4 x =
+          *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(A) + row + k);
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        v[2 * q] = __uint_as_float(w[q] << 16);
+        v[2 * q + 1] = __uint_as_float(w[q] & 0xFFFF0000u);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      v[q] = 0.f;
+      if (k + q < K)
+        v[q] = f32 ? static_cast<const float *>(A)[row + k + q]
+                   : bf16_bits_to_f32(static_cast<const uint16_t *>(A)[row + k + q]);
+    }
+  }
 }
 
 // Where a warp stands in its sequence of stages.
 struct Cursor {
   int step, e, group, nstep;  // step; its group's expert, id and column step
-  int mat, c;                 // matrix and first chunk of the stage
+  int c;                      // first chunk of the stage
 };
 
 template <int SPB, bool ZP, bool SF32, int TERMS>
-__global__ void __launch_bounds__(kThreads, 2) stream_kernel(const StreamParams p) {
+__global__ void __launch_bounds__(kThreads, kStreamCtas) stream_kernel(const StreamParams p) {
   constexpr int kEs = SF32 ? 4 : 2;
+  constexpr int kBlocks = 4 / SPB;       // scale blocks (or parts of one) per chunk
+  constexpr bool kSums = TERMS == 1;     // the codes' offset goes by the blocks' sums
   extern __shared__ __align__(128) unsigned char smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
-  const bool ready = p.offsets != nullptr;  // lists in global memory
-  const SlotLists L = slot_lists(reinterpret_cast<int *>(smem + p.off_lists), ready ? 0 : p.P, p.E);
-  float *s_w = reinterpret_cast<float *>(smem + p.off_keys);  // weights [P] (few slots)
   __shared__ int s_last;
+  __shared__ float s_unscale[kCols];  // what undoes a column's row scale
 
   if (!p.early) {
     grid_dependency_wait();
     grid_dependents_launch();
   }
-  // ---- lists --------------------------------------------------------------------
-  if (ready) {
-    for (int i = tid; i <= p.E; i += kThreads) L.off[i] = p.offsets[i];
-    __syncthreads();
-    if (warp == 0) {
-      const int n = warp_prefix(
-          p.E, [&](int i) { return (L.off[i + 1] - L.off[i] + p.gt - 1) / p.gt; },
-          [&](int i, int v) { L.gpre[i] = v; });
-      if (lane == 0) L.gpre[p.E] = n;
-    }
-    __syncthreads();
-  } else {
-    if (p.logits) {
-      uint32_t *keys = reinterpret_cast<uint32_t *>(smem + p.off_ring) + warp * p.E;
-      for (int m = warp; m < p.M; m += kWarps) {
-        int e;
-        float r;
-        route_row(p.logits, p.logits_f32 != 0, m, p.E, p.top_k, p.normalize != 0, keys, e, r);
-        if (lane < p.top_k) {
-          L.e[m * p.top_k + lane] = e < 0 ? p.E : e;
-          s_w[m * p.top_k + lane] = r;
-        }
-      }
-    } else {
-      for (int i = tid; i < p.P; i += kThreads) {
-        const int e = p.table[i];
-        L.e[i] = e >= 0 && e < p.E ? e : p.E;
-      }
-    }
-    __syncthreads();
-    build_lists(L, p.P, p.E, p.gt);
-  }
-  const int32_t *order = ready ? p.order : L.order;
-  const float *weights = ready ? p.weights : s_w;
-  const int routed = L.off[p.E];
-
   // ---- this CTA's steps ------------------------------------------------------------
-  const int groups = L.gpre[p.E];
+  const int32_t *order = p.order;
+  const SlotGroup *grp = p.groups;
+  const int groups = *p.n_groups;
   const int64_t total = int64_t(groups) * p.ns;
   const int lo = static_cast<int>(total * blockIdx.x / gridDim.x);
   const int hi = static_cast<int>(total * (blockIdx.x + 1) / gridDim.x);
-  const int nmat = p.mode == kStreamGateUp ? 2 : 1;
+  const bool gate_up = p.mode == kStreamGateUp;
   const int ks = warp % p.ksplit, tl = warp / p.ksplit;
   const int c0 = p.K64 * ks / p.ksplit, c1 = p.K64 * (ks + 1) / p.ksplit;
   unsigned char *ring = smem + p.off_ring + warp * (kStages * p.st_bytes);
   const uint32_t ring_u = smem_addr(ring);
 
-  auto expert_of = [&](int e, int group) {
-    while (L.gpre[e + 1] <= group) ++e;
-    return e;
-  };
-  auto has_tile = [&](const Cursor &q) { return q.nstep * p.tpu + tl < p.N16; };
+  auto has_pair = [&](const Cursor &q) { return q.nstep * p.tpu + tl < p.npair; };
+  // The tile of matrix `mat` in pair i of an expert (a pair past an odd
+  // number of tiles repeats the last one).
+  auto tile_of = [&](int i, int mat) { return gate_up ? i : min(2 * i + mat, p.N16 - 1); };
   auto next_step = [&](Cursor &q) {
     ++q.step;
     if (++q.nstep == p.ns) {
       q.nstep = 0;
       ++q.group;
-      if (q.step < hi) q.e = expert_of(q.e, q.group);
+      if (q.step < hi) q.e = grp[q.group].e;
     }
   };
   Cursor pre;  // next stage to fetch
   pre.step = lo;
   pre.group = lo / p.ns;
   pre.nstep = lo - pre.group * p.ns;
-  pre.e = lo < hi ? expert_of(0, pre.group) : 0;
-  pre.mat = 0;
+  pre.e = lo < hi ? grp[pre.group].e : 0;
   pre.c = c0;
   Cursor cur = pre;
-  while (pre.step < hi && !has_tile(pre)) next_step(pre);
+  while (pre.step < hi && !has_pair(pre)) next_step(pre);
 
+  // Sources of the pair being fetched, from the start of its k; lane l copies
+  // the 16-byte pieces l of the codes of a chunk, and of a stage's scales and
+  // zero points (at most 32 each).
+  const uint4 *fw[2];
+  const unsigned char *fs[2], *fz[2];
+  auto aim = [&] {
+#pragma unroll
+    for (int mat = 0; mat < 2; ++mat) {
+      const int64_t tile = int64_t(pre.e) * p.N16 + tile_of(pre.nstep * p.tpu + tl, mat);
+      fw[mat] = p.w[mat].b + tile * p.K64 * 32 + lane;
+      fs[mat] = p.w[mat].s + tile * p.nb * (kTileN * kEs) + lane * 16;
+      if (ZP) fz[mat] = p.w[mat].z + tile * p.nbz * 8 + lane * 16;
+    }
+  };
+  // First block of the stage at chunk c, and the one past its last.
+  auto block_lo = [&](int c) { return SPB == 4 ? (c * kChunkK) >> p.bs_log2 : c * kBlocks; };
+  auto block_hi = [&](int c) {
+    return SPB == 4 ? ((c * kChunkK - 1) >> p.bs_log2) + 1 : c * kBlocks;
+  };
+  if (pre.step < hi) aim();
   auto fetch = [&](int slot) {
     if (pre.step < hi) {
-      const int64_t tile = int64_t(pre.e) * p.N16 + pre.nstep * p.tpu + tl;
-      const int n = min(p.kc, c1 - pre.c);
-      const uint32_t dst = ring_u + slot * p.st_bytes + lane * 16;
-      const uint4 *src = p.w[pre.mat].b + (tile * p.K64 + pre.c) * 32 + lane;
-      for (int i = 0; i < n; ++i) cp16(dst + i * kChunkBytes, src + i * 32);
-      const int b0 = (pre.c * kChunkK) >> p.bs_log2;
-      const int b1 = min(p.nb, (((pre.c + n) * kChunkK - 1) >> p.bs_log2) + 1);
-      const unsigned char *ss = p.w[pre.mat].s + (tile * p.nb + b0) * (kTileN * kEs);
-      for (int i = lane; i < (b1 - b0) * kEs; i += 32)
-        cp16(ring_u + slot * p.st_bytes + p.st_scale + i * 16, ss + i * 16);
-      if (ZP) {
-        // Pairs of words from an even block on.
-        const unsigned char *zz = p.w[pre.mat].z + (tile * p.nbz + (b0 & ~1)) * 8;
-        for (int i = lane; i < (b1 + 1) / 2 - b0 / 2; i += 32)
-          cp16(ring_u + slot * p.st_bytes + p.st_zp + i * 16, zz + i * 16);
+      const int c = pre.c, n = min(kChunks, c1 - c);
+      const int b0 = block_lo(c), need = block_hi(c + n), b1 = min(p.nb, need);
+#pragma unroll
+      for (int mat = 0; mat < 2; ++mat) {
+        const uint32_t dst = ring_u + slot * p.st_bytes + mat * p.st_tile + lane * 16;
+        const uint4 *src = fw[mat] + c * 32;
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i)
+          if (i < n) cp16(dst + i * kChunkBytes, src + i * 32);
+        if (lane < (b1 - b0) * kEs)
+          cp16(dst + p.st_scale, fs[mat] + b0 * (kTileN * kEs));
+        if (ZP)  // pairs of words from an even block on
+          if (lane < (b1 + 1) / 2 - b0 / 2) cp16(dst + p.st_zp, fz[mat] + (b0 / 2) * 16);
       }
-      pre.c += p.kc;
+      // Blocks past the last hold only k >= K, whose activations are zero;
+      // their scales are zeros, so that nothing stale meets them.
+      if (b1 < need && lane >= (b1 - b0) * kEs && lane < (need - b0) * kEs)
+        for (int mat = 0; mat < 2; ++mat)
+          *reinterpret_cast<uint4 *>(ring + slot * p.st_bytes + mat * p.st_tile + p.st_scale +
+                                     lane * 16) = make_uint4(0, 0, 0, 0);
+      pre.c = c + kChunks;
       if (pre.c >= c1) {
         pre.c = c0;
-        if (++pre.mat == nmat) {
-          pre.mat = 0;
-          do next_step(pre);
-          while (pre.step < hi && !has_tile(pre));
-        }
+        do next_step(pre);
+        while (pre.step < hi && !has_pair(pre));
+        if (pre.step < hi) aim();
       }
     }
     cp_commit();
   };
-  // (The routers' keys lay in the rings; building the lists ended with a barrier.)
-#pragma unroll
+#pragma unroll 1
   for (int i = 0; i < kStages - 1; ++i) fetch(i);
 
   if (p.early) grid_dependency_wait();
-  if (p.mode == kStreamGateUp && blockIdx.x == 0)
-    for (int i = tid; i < p.n_counters; i += kThreads) p.counters[i] = 0;
-
   // Rows that no step writes: slots without an expert (product), every token
   // when nothing is routed (down).
+  auto store = [&](int64_t i, float v) {
+    if (p.y_f32) static_cast<float *>(p.Y)[i] = v;
+    else static_cast<uint16_t *>(p.Y)[i] = static_cast<uint16_t>(bf16_bits(v));
+  };
   if (p.mode == kStreamProduct) {
-    for (int i = routed + blockIdx.x; i < p.P; i += gridDim.x) {
+    for (int i = p.offsets[p.E] + blockIdx.x; i < p.P; i += gridDim.x) {
       const int64_t row = int64_t(order[i]) * p.N;
-      for (int n = tid; n < p.N; n += kThreads) {
-        if (p.y_f32) static_cast<float *>(p.Y)[row + n] = 0.f;
-        else static_cast<uint16_t *>(p.Y)[row + n] = 0;
-      }
+      for (int n = tid; n < p.N; n += kThreads) store(row + n, 0.f);
     }
-  } else if (p.mode == kStreamDown && groups == 0) {
+  } else if (p.mode == kStreamDown && groups == 0 && p.counters) {
     const int64_t n = int64_t(p.M) * p.N;
-    for (int64_t i = blockIdx.x * int64_t(kThreads) + tid; i < n; i += int64_t(gridDim.x) * kThreads) {
-      if (p.y_f32) static_cast<float *>(p.Y)[i] = 0.f;
-      else static_cast<uint16_t *>(p.Y)[i] = 0;
-    }
+    for (int64_t i = blockIdx.x * int64_t(kThreads) + tid; i < n; i += int64_t(gridDim.x) * kThreads)
+      store(i, 0.f);
   }
 
   uint16_t *sx = reinterpret_cast<uint16_t *>(smem + p.off_x);
-  const int xterm = p.gt * p.krow;  // elements between the parts
+  const int xterm = p.krow << p.gt_log2;  // elements between the parts
+  // Per block and pair of columns 2t, 2t+1: what the MMAs start from, or (ZP)
+  // what it is made of: -1024 S and -S.
+  float4 *sums = reinterpret_cast<float4 *>(smem + p.off_sums);  // [K64 * kBlocks][4]
   float *red = reinterpret_cast<float *>(smem + p.off_red);
   int slot = 0, staged = -1, cols = 0, first = 0;
 
   for (; cur.step < hi; next_step(cur)) {
     if (cur.group != staged) {
       // ---- stage the group's activation rows ------------------------------------
-      first = L.off[cur.e] + (cur.group - L.gpre[cur.e]) * p.gt;
-      cols = min(p.gt, L.off[cur.e + 1] - first);
-      // (Every warp is done with the rows before: the last join had a barrier.)
+      first = grp[cur.group].first;
+      cols = grp[cur.group].cols;
+      if (staged >= 0) __syncthreads();  // every warp is done with the rows before
       staged = cur.group;
       const int pieces = p.K64 * (kChunkK / 8);
-      const int planes = p.mode == kStreamDown ? TERMS : 1;
-      for (int i = tid; i < planes * cols * pieces; i += kThreads) {
-        const int row = i / pieces, k = (i - row * pieces) * 8;
-        const int plane = row / cols, col = row - plane * cols;
-        const int slot_id = order[first + col];
-        uint16_t *dst = sx + col * p.krow + k;
-        if (TERMS == 3 && p.mode != kStreamDown) {
-          const float *a = static_cast<const float *>(p.A) +
-                           int64_t(p.per_slot ? slot_id : slot_id / p.top_k) * p.K;
+#pragma unroll 1
+      for (int col = 0; col < cols; ++col) {
+        int row = order[first + col];
+        if (!p.per_slot) row /= p.top_k;
+        const int shift = row_shift(__ldcg(p.tops + row));
+        const float f = exp2i(shift);
+        if (tid == 0) s_unscale[col] = exp2i(-shift);
+        // Whole warps go round: pieces are a multiple of 8, a block's sum is
+        // formed by up to 8 neighbouring lanes.
+#pragma unroll 1
+        for (int i0 = warp * 32; i0 < pieces; i0 += kThreads) {
+          const int i = i0 + lane, k = i * 8;
           float v[8];
-          if (p.a_vec && k + 8 <= p.K) {
-            const float4 x = *reinterpret_cast<const float4 *>(a + k);
-            const float4 y = *reinterpret_cast<const float4 *>(a + k + 4);
-            v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-            v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
-          } else {
+          load8(p.A, p.a_f32, p.a_vec, row * p.ld, k, p.K, v);  // zeros past K
+          uint32_t hi4[4], lo4[4];
+          float sum = 0.f;
 #pragma unroll
-            for (int q = 0; q < 8; ++q) v[q] = k + q < p.K ? a[k + q] : 0.f;
+          for (int q = 0; q < 4; ++q) {
+            const float x = v[2 * q] * f, y = v[2 * q + 1] * f;
+            hi4[q] = pack_f16x2(x, y);
+            const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&hi4[q]));
+            if (kSums) sum += h.x + h.y;
+            else lo4[q] = pack_f16x2(x - h.x, y - h.y);
           }
+          uint16_t *dst = sx + col * p.krow + k;
+          if (i < pieces) {
+            *reinterpret_cast<uint4 *>(dst) = make_uint4(hi4[0], hi4[1], hi4[2], hi4[3]);
+            if (!kSums)
+              *reinterpret_cast<uint4 *>(dst + xterm) = make_uint4(lo4[0], lo4[1], lo4[2], lo4[3]);
+          }
+          if (kSums) {
+            constexpr int kLanes = kChunkK / kBlocks / 8;  // lanes per block
 #pragma unroll
-          for (int part = 0; part < 3; ++part) {
-            uint32_t w[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const uint32_t x = __float_as_uint(v[2 * q]) & 0xFFFF0000u;
-              const uint32_t y = __float_as_uint(v[2 * q + 1]) & 0xFFFF0000u;
-              v[2 * q] -= __uint_as_float(x);
-              v[2 * q + 1] -= __uint_as_float(y);
-              w[q] = (x >> 16) | y;
+            for (int o = 1; o < kLanes; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (i < pieces && lane % kLanes == 0) {
+              // Offsets 1024 + z (rows g) and 1024 + 16 z (rows g + 8), z = 8.
+              float *q = reinterpret_cast<float *>(sums) + (i / kLanes) * 16 + (col >> 1) * 4 +
+                         (col & 1);
+              q[0] = (ZP ? -1024.f : -1032.f) * sum;
+              q[2] = (ZP ? -1.f : -1152.f) * sum;
             }
-            *reinterpret_cast<uint4 *>(dst + part * xterm) = make_uint4(w[0], w[1], w[2], w[3]);
           }
-        } else {
-          const int64_t row0 = p.mode == kStreamDown
-                                   ? plane * p.plane + int64_t(slot_id) * p.ldh
-                                   : int64_t(p.per_slot ? slot_id : slot_id / p.top_k) * p.K;
-          const uint16_t *a = static_cast<const uint16_t *>(p.A) + row0;
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (p.a_vec && k + 8 <= p.K) {
-            v = __ldcg(reinterpret_cast<const uint4 *>(a + k));
-          } else {
-            uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-              if (k + q < p.K) w[q >> 1] |= uint32_t(__ldcg(a + k + q)) << (16 * (q & 1));
-            v = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-          *reinterpret_cast<uint4 *>(dst + plane * xterm) = v;
         }
       }
       __syncthreads();
     }
 
-    // ---- the warp's part of its tile --------------------------------------------
+    // ---- the warp's part of its pair --------------------------------------------
     float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-    if (has_tile(cur)) {
-      const bool have = g < cols;
-      const uint16_t *xrow = sx + (have ? g : 0) * p.krow + 4 * t;
-#pragma unroll
-      for (int mat = 0; mat < 2; ++mat) {
-        if (mat >= nmat) break;
-        for (int c = c0; c < c1; c += p.kc) {
-          cp_wait<kStages - 2>();
-          __syncwarp();  // the stage is there, and every lane is done with the one before
-          fetch(slot == 0 ? kStages - 1 : slot - 1);
-          const unsigned char *st = ring + slot * p.st_bytes;
-          const int n = min(p.kc, c1 - c);
-          const int b0 = (c * kChunkK) >> p.bs_log2;
-          const unsigned char *sc = st + p.st_scale + g * kEs;
-          const unsigned char *sz = st + p.st_zp + (b0 & 1) * 8;
+    if (has_pair(cur)) {
+      // Lanes of columns past the group's slots read its first row: their
+      // sums are never looked at.
+      const uint16_t *xrow = sx + (g < cols ? g : 0) * p.krow + 4 * t;
+      for (int c = c0; c < c1; c += kChunks) {
+        cp_wait<kStages - 2>();
+        __syncwarp();  // the stage is there, and every lane is done with the one before
+        fetch(slot == 0 ? kStages - 1 : slot - 1);
+        const unsigned char *st = ring + slot * p.st_bytes;
+        const unsigned char *wp = st + lane * 16;
+        const int n = min(kChunks, c1 - c);
+        const int b0 = block_lo(c);
+        const unsigned char *sc = st + p.st_scale + g * kEs;
+        const unsigned char *sz = st + p.st_zp + (b0 & 1) * 8;
+        const uint16_t *xk = xrow + c * kChunkK;
+        const float4 *sk = sums + c * (kBlocks * 4) + t;
 #pragma unroll 1
-          for (int i = 0; i < n; ++i) {
-            const uint4 w4 = *reinterpret_cast<const uint4 *>(st + i * kChunkBytes + lane * 16);
-            const uint32_t wv[4] = {w4.x, w4.y, w4.z, w4.w};
-            const uint16_t *xk = xrow + (c + i) * kChunkK;
-            constexpr int kBlocks = 4 / SPB;  // scale blocks a chunk touches
-            // Blocks past the last hold only k >= K, whose activations are
-            // zero: any finite scale serves.
-            const int bc = ((c + i) * kChunkK) >> p.bs_log2;
+        for (int i = 0; i < n; ++i, wp += kChunkBytes, xk += kChunkK, sk += kBlocks * 4) {
+          uint32_t wv[2][4];
 #pragma unroll
-            for (int bb = 0; bb < kBlocks; ++bb) {
-              const int bi = min(bc + bb, p.nb - 1) - b0;
-              float s0, s1;
-              if (SF32) {
-                s0 = *reinterpret_cast<const float *>(sc + bi * (kTileN * 4));
-                s1 = *reinterpret_cast<const float *>(sc + bi * (kTileN * 4) + 32);
-              } else {
-                s0 = bf16_bits_to_f32(*reinterpret_cast<const uint16_t *>(sc + bi * (kTileN * 2)));
-                s1 = bf16_bits_to_f32(
-                    *reinterpret_cast<const uint16_t *>(sc + bi * (kTileN * 2) + 16));
-              }
-              uint32_t z0 = 0x43084308u, z1 = z0;  // 128 + 8
+          for (int mat = 0; mat < 2; ++mat) {
+            const uint4 w4 = *reinterpret_cast<const uint4 *>(wp + mat * p.st_tile);
+            wv[mat][0] = w4.x; wv[mat][1] = w4.y; wv[mat][2] = w4.z; wv[mat][3] = w4.w;
+          }
+          const int bi = SPB == 4 ? (((c + i) * kChunkK) >> p.bs_log2) - b0 : i * kBlocks;
+          const unsigned char *scb = sc + bi * (kTileN * kEs);
+          const unsigned char *szb = sz + bi * 8;
+#pragma unroll
+          for (int bb = 0; bb < kBlocks; ++bb) {
+            float d[2][4];
+            uint32_t z0[2], z1[2], y1[2];
+            float4 sv;
+            if (kSums) sv = sk[bb * 4];
+#pragma unroll
+            for (int mat = 0; mat < 2; ++mat) {
+              uint32_t q0 = 8, q1 = 8;
               if (ZP) {
-                const uint2 zw = *reinterpret_cast<const uint2 *>(sz + bi * 8);
-                z0 = 0x43004300u | (((zw.x >> (4 * g)) & 15u) * 0x10001u);
-                z1 = 0x43004300u | (((zw.y >> (4 * g)) & 15u) * 0x10001u);
+                const uint2 zw =
+                    *reinterpret_cast<const uint2 *>(szb + mat * p.st_tile + bb * 8);
+                q0 = (zw.x >> (4 * g)) & 15u;
+                q1 = (zw.y >> (4 * g)) & 15u;
               }
-              float d[4];
+              if (kSums && ZP) {
+                // z and 16 z as floats: 2^23 + n in bits, less 2^23.
+                const float f0 = __uint_as_float(0x4B000000u | q0) - 8388608.f;
+                const float f1 = __uint_as_float(0x4B000000u | (q1 << 4)) - 8388608.f;
+                d[mat][0] = fmaf(f0, sv.z, sv.x);
+                d[mat][1] = fmaf(f0, sv.w, sv.y);
+                d[mat][2] = fmaf(f1, sv.z, sv.x);
+                d[mat][3] = fmaf(f1, sv.w, sv.y);
+              } else if (!kSums) {
+                // 1024 + z, and -(64 + z) for the sixteenth of 1024 + 16 q.
+                z0[mat] = 0x64006400u | (q0 * 0x10001u);
+                z1[mat] = f16x2_sub(0x64006400u | (q1 * 0x10001u), 0x63806380u);  // 64 + z
+                y1[mat] = z1[mat] ^ 0x80008000u;
+                d[mat][0] = d[mat][1] = d[mat][2] = d[mat][3] = 0.f;
+              }
+            }
 #pragma unroll
-              for (int jj = 0; jj < SPB; ++jj) {
-                const int j = bb * SPB + jj;
+            for (int jj = 0; jj < SPB; ++jj) {
+              const int j = bb * SPB + jj;
+              uint2 xb[TERMS];
+#pragma unroll
+              for (int part = 0; part < TERMS; ++part)
+                xb[part] = *reinterpret_cast<const uint2 *>(xk + part * xterm + 16 * j);
+#pragma unroll
+              for (int mat = 0; mat < 2; ++mat) {
                 uint32_t wf[4];
-                codes_to_bf16x2(wv[j], wf);
-                wf[0] = bf16x2_sub(wf[0], z0);
-                wf[1] = bf16x2_sub(wf[1], z1);
-                wf[2] = bf16x2_sub(wf[2], z0);
-                wf[3] = bf16x2_sub(wf[3], z1);
+                codes_to_f16x2(wv[mat][j], wf);
+                if (!kSums) {
+                  constexpr uint32_t kSixteenth = 0x2C002C00u;  // 2^-4
+                  wf[0] = f16x2_sub(wf[0], z0[mat]);
+                  wf[1] = f16x2_fma(wf[1], kSixteenth, y1[mat]);
+                  wf[2] = f16x2_sub(wf[2], z0[mat]);
+                  wf[3] = f16x2_fma(wf[3], kSixteenth, y1[mat]);
+                }
 #pragma unroll
                 for (int part = 0; part < TERMS; ++part) {
-                  uint2 b = make_uint2(0, 0);
-                  if (have) b = *reinterpret_cast<const uint2 *>(xk + part * xterm + 16 * j);
-                  if (jj == 0 && part == 0) mma_bf16_16816_zero(d, wf, b.x, b.y);
-                  else mma_bf16_16816(d, wf, b.x, b.y);
+                  if (kSums && !ZP && jj == 0)
+                    mma_f16_from(d[mat], wf, xb[part], sv.x, sv.y, sv.z, sv.w);
+                  else
+                    mma_f16(d[mat], wf, xb[part]);
                 }
               }
-              acc[mat][0] = fmaf(s0, d[0], acc[mat][0]);
-              acc[mat][1] = fmaf(s0, d[1], acc[mat][1]);
-              acc[mat][2] = fmaf(s1, d[2], acc[mat][2]);
-              acc[mat][3] = fmaf(s1, d[3], acc[mat][3]);
+            }
+#pragma unroll
+            for (int mat = 0; mat < 2; ++mat) {
+              const unsigned char *sm = scb + mat * p.st_tile + bb * (kTileN * kEs);
+              float s0, s1;
+              if (SF32) {
+                s0 = *reinterpret_cast<const float *>(sm);
+                s1 = *reinterpret_cast<const float *>(sm + 32);
+              } else {
+                s0 = bf16_bits_to_f32(*reinterpret_cast<const uint16_t *>(sm));
+                s1 = bf16_bits_to_f32(*reinterpret_cast<const uint16_t *>(sm + 16));
+              }
+              acc[mat][0] = fmaf(s0, d[mat][0], acc[mat][0]);
+              acc[mat][1] = fmaf(s0, d[mat][1], acc[mat][1]);
+              acc[mat][2] = fmaf(s1, d[mat][2], acc[mat][2]);
+              acc[mat][3] = fmaf(s1, d[mat][3], acc[mat][3]);
             }
           }
-          slot = slot == kStages - 1 ? 0 : slot + 1;
         }
+        slot = slot == kStages - 1 ? 0 : slot + 1;
       }
     }
 
-    // ---- join the k ranges and store -----------------------------------------------
-    // Two buffers by turns: a buffer is written again only after the barrier
-    // of the step in between.
-    float *rb = red + ((cur.step - lo) & 1) * (kWarps * nmat * kTileN * kCols);
+    // ---- store ---------------------------------------------------------------------
+    // The warps of a pair meet in shared memory, a warp that has its pair to
+    // itself meets its own lanes there. Two buffers by turns: a buffer is
+    // written again only after the barrier of the step in between.
+    constexpr float kUpper = kSums ? 0.0625f : 1.f;  // rows 8-15 of a tile
+    const bool alone = p.ksplit == 1;
+    const int gt = 1 << p.gt_log2;
+    float *rb = red + (((cur.step - lo) & 1) * 2 * kWarps << p.gt_log2) * kTileN;
 #pragma unroll
     for (int mat = 0; mat < 2; ++mat) {
-      if (mat >= nmat) break;
-      float *r = rb + (mat * kWarps + warp) * (kTileN * kCols) + 2 * t;
-      *reinterpret_cast<float2 *>(r + g * kCols) = make_float2(acc[mat][0], acc[mat][1]);
-      *reinterpret_cast<float2 *>(r + (g + 8) * kCols) = make_float2(acc[mat][2], acc[mat][3]);
-    }
-    __syncthreads();
-    const int rows = p.tpu * kTileN, n0 = cur.nstep * rows;
-    for (int i = tid; i < rows * cols; i += kThreads) {
-      const int col = i / rows, r = i - col * rows, n = n0 + r;
-      if (n >= p.N) continue;
-      const int slot_id = order[first + col];
-      const float *rr = rb + ((r >> 4) * p.ksplit * kTileN + (r & 15)) * kCols + col;
-      float v[2] = {0.f, 0.f};
+      float *r = rb + ((mat * kWarps + warp) * kTileN + g) * gt;
 #pragma unroll
-      for (int mat = 0; mat < 2; ++mat) {
-        if (mat >= nmat) break;
-        for (int k2 = 0; k2 < p.ksplit; ++k2)
-          v[mat] += rr[(mat * kWarps + k2) * (kTileN * kCols)];
-      }
-      const int64_t bn = int64_t(cur.e) * p.N + n;
-      if (p.mode == kStreamProduct) {
-        const float y = p.w[0].bias ? v[0] + p.w[0].bias[bn] : v[0];
-        const int64_t o = int64_t(slot_id) * p.N + n;
-        if (p.y_f32) static_cast<float *>(p.Y)[o] = y;
-        else static_cast<uint16_t *>(p.Y)[o] = static_cast<uint16_t>(bf16_bits(y));
-      } else if (p.mode == kStreamGateUp) {
-        const float a = p.w[0].bias ? v[0] + p.w[0].bias[bn] : v[0];
-        const float u = p.w[1].bias ? v[1] + p.w[1].bias[bn] : v[1];
-        float h = a / (1.f + expf(-a)) * u * weights[slot_id];
-        for (int pl = 0; pl < p.h_planes; ++pl) {  // parts by truncation
-          const uint32_t x = __float_as_uint(h) & 0xFFFF0000u;
-          p.hidden[pl * p.plane + int64_t(slot_id) * p.ldh + n] = static_cast<uint16_t>(x >> 16);
-          h -= __uint_as_float(x);
+      for (int o = 0; o < 2; ++o)
+        if (2 * t + o < cols) {
+          r[2 * t + o] = acc[mat][o];
+          r[8 * gt + 2 * t + o] = acc[mat][2 + o] * kUpper;
         }
-      } else {
-        p.part[int64_t(slot_id) * p.N + n] =
-            p.w[0].bias ? fmaf(weights[slot_id], p.w[0].bias[bn], v[0]) : v[0];
+    }
+    if (alone) __syncwarp();
+    else __syncthreads();
+    // Columns of a pair: 16 (of both matrices) for gate and up, else 32. Item
+    // i: row r of the step (of the warp's pair), column `col`.
+    const int wide_log2 = gate_up ? 4 : 5;
+    const int rows_log2 = alone ? wide_log2 : wide_log2 + p.tpu_log2, rows = 1 << rows_log2;
+    const int part0 = cur.nstep * p.tpu + (alone ? warp : 0), n0 = part0 << wide_log2;
+#pragma unroll 1
+    for (int i0 = alone ? 0 : warp * 32; i0 < cols << rows_log2; i0 += alone ? 32 : kThreads) {
+      const int i = i0 + lane, col = i >> rows_log2, r = i & (rows - 1), n = n0 + r;
+      uint32_t top = 0;  // hidden value's magnitude
+      int id = 0;
+      if (col < cols && n < p.N) {
+        const int w0 = alone ? warp : (r >> wide_log2) * p.ksplit;
+        const float *rr =
+            rb + (((gate_up ? 0 : (r >> 4) & 1) * kWarps + w0) * kTileN + (r & 15)) * gt + col;
+        float v0 = 0.f, v1 = 0.f;
+#pragma unroll 1
+        for (int k2 = 0; k2 < p.ksplit; ++k2, rr += kTileN * gt) {
+          v0 += rr[0];
+          if (gate_up) v1 += rr[kWarps * kTileN * gt];
+        }
+        const float f = s_unscale[col];
+        id = order[first + col];
+        const int64_t bn = int64_t(cur.e) * p.N + n;
+        v0 *= f;
+        const float b0 = p.w[0].bias ? p.w[0].bias[bn] : 0.f;
+        if (gate_up) {
+          v0 += b0;
+          v1 *= f;
+          if (p.w[1].bias) v1 += p.w[1].bias[bn];
+          const float h = v0 / (1.f + expf(-v0)) * v1 * p.weights[id];
+          p.hidden[id * p.ldh + n] = h;
+          top = __float_as_uint(h) & 0x7FFFFFFFu;
+        } else if (p.mode == kStreamProduct) {
+          store(int64_t(id) * p.N + n, v0 + b0);
+        } else {
+          p.part[int64_t(id) * p.N + n] = b0 != 0.f ? fmaf(p.weights[id], b0, v0) : v0;
+        }
+      }
+      if (gate_up) {  // 16 lanes share a column
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        if ((lane & 15) == 0 && top) atomicMax(p.hidden_tops + id, top);
       }
     }
-    if (p.mode == kStreamDown && p.counters) {
-      // The last group of this column range adds the partials of each token.
-      __syncthreads();
-      if (tid == 0) {
+    if (p.mode == kStreamDown && p.counters && n0 < p.N) {
+      // Whoever completes this column range adds the partials of each token,
+      // in slot order.
+      int last = 0;
+      if (alone) __syncwarp();
+      else __syncthreads();
+      if (alone ? lane == 0 : tid == 0) {
         __threadfence();
-        s_last = atomicAdd(p.counters + cur.nstep, 1u) == static_cast<unsigned>(groups - 1);
+        last = atomicAdd(p.counters + part0, 1u) == static_cast<unsigned>(groups - 1);
         __threadfence();
+        s_last = last;
       }
-      __syncthreads();
-      if (s_last) {
-        const int width = min(rows, p.N - n0);
-        for (int i = tid; i < p.M * width; i += kThreads) {
-          const int m = i / width, n = n0 + i - m * width;
+      if (alone) {
+        last = __shfl_sync(0xffffffffu, last, 0);
+        __syncwarp();
+      } else {
+        __syncthreads();
+        last = s_last;
+      }
+      if (last)
+#pragma unroll 1
+        for (int i = alone ? lane : tid; i < p.M << rows_log2; i += alone ? 32 : kThreads) {
+          const int m = i >> rows_log2, n = n0 + (i & (rows - 1));
+          if (n >= p.N) continue;
           float y = 0.f;
           for (int j = 0; j < p.top_k; ++j) {
             const int q = m * p.top_k + j;
-            if (L.e[q] < p.E) y += __ldcg(p.part + int64_t(q) * p.N + n);
+            if (p.experts[q] >= 0) y += __ldcg(p.part + int64_t(q) * p.N + n);
           }
-          const int64_t o = int64_t(m) * p.N + n;
-          if (p.y_f32) static_cast<float *>(p.Y)[o] = y;
-          else static_cast<uint16_t *>(p.Y)[o] = static_cast<uint16_t>(bf16_bits(y));
+          store(int64_t(m) * p.N + n, y);
         }
-      }
     }
   }
   cp_wait<0>();
@@ -431,7 +561,7 @@ template <int SPB, bool ZP, bool SF32, int TERMS>
 cudaError_t launch_one(const StreamParams &p, int grid, int smem, bool pdl, cudaStream_t stream) {
   static std::atomic<unsigned long long> done{0};
   auto *kernel = stream_kernel<SPB, ZP, SF32, TERMS>;
-  const cudaError_t e = ensure_smem_limit(kernel, 227 * 1024 - 1024, done);
+  const cudaError_t e = ensure_smem_limit(kernel, 226 * 1024 + 512, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);
@@ -446,25 +576,18 @@ cudaError_t launch_one(const StreamParams &p, int grid, int smem, bool pdl, cuda
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-template <int SPB, bool ZP, bool SF32>
-cudaError_t launch_terms(const StreamParams &p, int terms, int grid, int smem, bool pdl,
-                         cudaStream_t stream) {
-  return terms == 1   ? launch_one<SPB, ZP, SF32, 1>(p, grid, smem, pdl, stream)
-         : terms == 2 ? launch_one<SPB, ZP, SF32, 2>(p, grid, smem, pdl, stream)
-                      : launch_one<SPB, ZP, SF32, 3>(p, grid, smem, pdl, stream);
-}
-
 }  // namespace stream
 
 template <int SPB>
 cudaError_t launch_stream(const StreamParams &p, bool zp, bool sf32, int terms, int grid,
                           int smem, bool pdl, cudaStream_t s) {
   using namespace stream;
-  if (zp)
-    return sf32 ? launch_terms<SPB, true, true>(p, terms, grid, smem, pdl, s)
-                : launch_terms<SPB, true, false>(p, terms, grid, smem, pdl, s);
-  return sf32 ? launch_terms<SPB, false, true>(p, terms, grid, smem, pdl, s)
-              : launch_terms<SPB, false, false>(p, terms, grid, smem, pdl, s);
+  auto one = [&](auto *fn) { return fn(p, grid, smem, pdl, s); };
+  if (terms == 1)
+    return zp ? one(sf32 ? launch_one<SPB, true, true, 1> : launch_one<SPB, true, false, 1>)
+              : one(sf32 ? launch_one<SPB, false, true, 1> : launch_one<SPB, false, false, 1>);
+  return zp ? one(sf32 ? launch_one<SPB, true, true, 2> : launch_one<SPB, true, false, 2>)
+            : one(sf32 ? launch_one<SPB, false, true, 2> : launch_one<SPB, false, false, 2>);
 }
 
 }  // namespace mnb

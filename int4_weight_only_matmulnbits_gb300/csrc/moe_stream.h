@@ -7,11 +7,16 @@
 
 namespace mnb {
 
+// A run of slots that share an expert: their places in the order of slots.
+struct SlotGroup {
+  int e, first, cols;
+};
+
 enum StreamMode { kStreamProduct = 0, kStreamGateUp = 1, kStreamDown = 2 };
 
-// Slots the kernel lists for itself in shared memory (every CTA builds the
-// lists); longer inputs come with lists in global memory.
-constexpr int kFewSlots = 256;
+constexpr int kStreamStages = 3;  // ring stages per warp
+constexpr int kStreamChunks = 2;  // chunks per stage and tile
+constexpr int kStreamCtas = 3;    // CTAs per SM the registers allow
 
 struct StreamMat {
   const uint4 *b;
@@ -21,38 +26,37 @@ struct StreamMat {
 
 struct StreamParams {
   int mode;
-  StreamMat w[2];  // gate and up, or one matrix
+  StreamMat w[2];  // gate and up, or one matrix twice
   int E, N, N16, K, K64, nb, nbz, bs_log2;
-  // Activations: rows of A (row p / top_k, or p when per_slot), or planes of
-  // bf16 rows whose sum is the hidden row of slot p (mode down).
+  // Activations, fp32 or bf16: row p / top_k of A for slot p, or row p when
+  // per_slot; rows ld elements apart.
   const void *A;
-  int a_vec;  // rows of A are 16-byte aligned
+  int a_f32, a_vec;  // a_vec: rows are 16-byte aligned
   int per_slot;
-  int64_t plane;  // elements between planes
+  int64_t ld;
   int P, M, top_k;
-  // Lists: from logits, from a table of experts, or ready in global memory.
-  const void *logits;
-  int logits_f32, normalize;
-  const int32_t *table;
-  const int32_t *offsets, *order;
-  const float *weights;  // [P] with the ready lists
-  const int32_t *experts;  // [P] with the ready lists (mode down)
-  // Outputs: Y [P, N] (product), bf16 planes [P, ldh] (gate and up), fp32
-  // partials [P, N] and Y [M, N] (down).
+  const uint32_t *tops;  // bits of the largest magnitude of each row
+  // Lists.
+  const int32_t *offsets, *order, *n_groups, *experts;
+  const SlotGroup *groups;
+  const float *weights;  // [P] (gate and up, down)
+  // Outputs: Y [P, N] (product), hidden rows [P, ldh] (gate and up), partials
+  // [P, N] and Y [M, N] (down).
   void *Y;
   int y_f32;
-  uint16_t *hidden;
-  int ldh, h_planes;
+  float *hidden;
+  uint32_t *hidden_tops;  // [P], zeros before
+  int64_t ldh;
   float *part;
-  unsigned *counters;  // [n steps] arrivals per column group; gate and up clears them
-  int n_counters;
+  unsigned *counters;  // arrivals per column range, zeros before; or null
   // Geometry.
-  int gt;               // slots per group (<= 8)
-  int ksplit, tpu, ns;  // warps per tile, tiles per step, steps per group
-  int kc, st_bytes, st_scale, st_zp;  // chunks per stage; stage layout
+  int gt_log2;          // slots per group: 2^gt_log2 <= 8
+  int npair;            // tile pairs of an expert
+  int ksplit, tpu, tpu_log2, ns;  // warps per pair, pairs per step, steps per group
+  int st_tile, st_bytes, st_scale, st_zp;  // stage layout
   int krow;             // staged activation row, in elements
-  int off_lists, off_keys, off_x, off_red, off_ring;
-  int early;            // down: the router runs, and weights load, ahead of the dependency wait
+  int off_x, off_sums, off_red, off_ring;
+  int early;  // down: weights load ahead of the dependency wait
 };
 
 template <int SPB>

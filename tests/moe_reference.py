@@ -10,18 +10,32 @@ choose:
   * fp32 activations: weights and activations enter exactly up to 2^-22 of each (the parts of a
     split), so a product is within (2 n + 16) 2^-23 mag + 2^-22 mag;
   * bf16 activations: a weight may be rounded to fp16 (2^-11) and so may a hidden value
-    (2^-11); a result is rounded to bf16 (2^-8). fp16 activations are scaled by a power of two
-    so that a bound of the row (its largest magnitude; for a hidden row, the product of the
-    bounds of its gate and up sums) lies in 2^14 .. 2^15: they are exact down to 2^-14 and
-    within 2^-25 below that, at most FLOOR = 2^-39 of the row's bound.
+    (2^-11); a result is rounded to bf16 (2^-8). fp16 activations (for fp32 ones, the parts
+    they are split into) are scaled by a power of two so that a bound of the row (its largest
+    magnitude; for a hidden row, the product of the bounds of its gate and up sums) lies in
+    2^14 .. 2^15: they are exact down to 2^-14 and within 2^-25 below that, at most
+    FLOOR = 2^-39 of the row's bound. The offset of the codes
+    may be taken off a block as a whole: codes of 1024 + r q carry an offset of 1024 + r z (r is
+    1 or 16, divided out again at the end), and (1024 + r z) s / r times the sum of a block's
+    activations comes off. That sum has at most 64 terms; it and the products it comes off are
+    each within 64 2^-24 of (1024 + r z) s / r times the activations' magnitudes, at most
+    OFFSET = 2 * 64 * 1039 * 2^-24 of the sum of |a| s in all (r = 1, z = 15).
 """
 import torch
 
 U_W = {torch.float32: 2.0 ** -22, torch.bfloat16: 2.0 ** -11}
 U_H = {torch.float32: 2.0 ** -22, torch.bfloat16: 2.0 ** -11}
 U_OUT = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8}
-FLOOR = {torch.float32: 0.0, torch.bfloat16: 2.0 ** -39}
+FLOOR = {torch.float32: 2.0 ** -39, torch.bfloat16: 2.0 ** -39}
+OFFSET = {torch.float32: 0.0, torch.bfloat16: 2 * 64 * 1039 * 2.0 ** -24}
 TINY = 1e-30
+
+
+class Stack:
+    """Weights [E, N, K] and their scales, spread over K, in float64."""
+
+    def __init__(self, W, S):
+        self.W, self.S = W, S
 
 
 def sum_u(n):
@@ -29,14 +43,15 @@ def sum_u(n):
 
 
 def dequant(B, s, z, K):
-    """[E, N, K] float64 of a stack in MatMulNBits storage."""
+    """The Stack of a MatMulNBits storage."""
     E, N, nb, half = B.shape
     i = torch.arange(K, device=B.device)
     b = i // (2 * half)
     byte = B.reshape(E, N, -1)[:, :, i // 2].long()
     q = (byte >> (4 * (i % 2))) & 15
     zp = 8 if z is None else (z.long()[:, :, b // 2] >> (4 * (b % 2))) & 15
-    return (q - zp).double() * s.double()[:, :, b]
+    S = s.double()[:, :, b]
+    return Stack((q - zp).double() * S, S)
 
 
 def route(logits, k, normalize):
@@ -76,6 +91,7 @@ def products(A, W, experts, bias, dtype, cap=None):
     """(Y [M, k, N] float64, bound without the output's rounding) for A [M, k, K] float64.
     cap [M, k]: the bound of each row (default: its largest magnitude)."""
     cap = A.abs().amax(2) if cap is None else cap
+    W, S = W.W, W.S
     M, k, K = A.shape
     Y = torch.zeros(M, k, W.shape[1], dtype=torch.float64, device=A.device)
     err = torch.zeros_like(Y)
@@ -90,7 +106,8 @@ def products(A, W, experts, bias, dtype, cap=None):
                 mag = mag + bias[e].double().abs()
             Y[m, j] = y
             low = FLOOR[dtype] * cap[m, j].unsqueeze(1) * W[e].abs().sum(1)
-            err[m, j] = (sum_u(K) + U_W[dtype]) * mag + low
+            off = OFFSET[dtype] * (a.abs() @ S[e].abs().T)
+            err[m, j] = (sum_u(K) + U_W[dtype]) * mag + low + off
     return Y, err
 
 
@@ -107,14 +124,14 @@ def layer(X, weights, experts, Wg, Wu, Wd, bg, bu, bd, dtype):
     eh = eh + (U_H[dtype] + 2.0 ** -20) * (h.abs() + eh)
     # Bounds of the hidden rows: largest weight times the row's 1-norm, plus the bias.
     cap = torch.zeros(M, k, dtype=torch.float64, device=X.device)
-    for e in range(Wg.shape[0]):
+    for e in range(Wg.W.shape[0]):
         m, j = torch.nonzero(experts == e, as_tuple=True)
-        one = lambda W, b: (32 * W[e].abs().max() * x[m, j].abs().sum(1)  # noqa: E731
+        one = lambda W, b: (32 * W.W[e].abs().max() * x[m, j].abs().sum(1)  # noqa: E731
                             + (0 if b is None else b[e].double().abs().max()))
         cap[m, j] = one(Wg, bg) * one(Wu, bu)
     y, ey = products(h, Wd, experts, bd, dtype, cap)
-    Wabs = Wd.abs()
-    for e in range(Wd.shape[0]):
+    Wabs = Wd.W.abs()
+    for e in range(Wabs.shape[0]):
         m, j = torch.nonzero(experts == e, as_tuple=True)
         if len(m):
             ey[m, j] += eh[m, j] @ Wabs[e].T * 1.01
