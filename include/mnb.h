@@ -449,7 +449,7 @@ MNB_API void mnb_set_programmatic_launch(int enable);
  * exits instead of hanging. This call waits for the current device to be
  * idle, returns the fault bits seen since the last call in *fault_bits
  * (HOST; 0 = none; 1 = decode kernel, 2 = a tensor-core kernel, 4 = decode
- * chain) and clears
+ * chain, 8 = expert layer's tensor-core kernel) and clears
  * them. Errors: MNB_ERR_NULL, MNB_ERR_CUDA.
  */
 MNB_API mnb_status mnb_fault_status(unsigned int *fault_bits);

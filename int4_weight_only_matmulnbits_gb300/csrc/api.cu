@@ -543,8 +543,10 @@ mnb_status mnb_fault_status(unsigned int *fault_bits) {
   unsigned int c = 0, d = 0;
   if (e == cudaSuccess) e = chain_take_fault(&c);
   if (e == cudaSuccess) e = pair_take_fault(&d);
+  unsigned int f = 0;
+  if (e == cudaSuccess) e = moe_take_fault(&f);
   if (e != cudaSuccess) return cuda_fail(e, "mnb_fault_status");
-  *fault_bits = a | b | c | d;
+  *fault_bits = a | b | c | d | f;
   return MNB_OK;
 }
 

@@ -18,9 +18,11 @@
 #include "mnb_common.cuh"
 #include "mnb_launch.h"
 #include "moe.h"
+#include "moe_half.cuh"
 #include "moe_lists.cuh"
 #include "moe_route.cuh"
 #include "moe_stream.h"
+#include "moe_tile.h"
 
 namespace mnb {
 namespace {
@@ -311,6 +313,316 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
+// ---- many slots, bf16: lists over several blocks, fp16 rows, scales ----------
+
+// The stable counting sort of lists_kernel over many blocks of kSortSlots
+// slots. First launch: each block's slots per expert, [blocks][E + 1].
+constexpr int kSortSlots = 1024;
+__global__ void __launch_bounds__(kThreads)
+    count_kernel(const int32_t *experts, int64_t P, int E, int32_t *counts, uint32_t *clear,
+                 int n_clear) {
+  extern __shared__ int32_t cnt[];  // [E + 1]
+  for (int i = threadIdx.x; i <= E; i += kThreads) cnt[i] = 0;
+  grid_dependency_wait();
+  grid_dependents_launch();
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i < n_clear; i += kThreads) clear[i] = 0;
+  __syncthreads();
+  const int64_t lo = int64_t(blockIdx.x) * kSortSlots;
+  const int n = static_cast<int>(P - lo < kSortSlots ? P - lo : kSortSlots);
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const int e = experts[lo + i];
+    atomicAdd(cnt + (e >= 0 && e < E ? e : E), 1);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i <= E; i += kThreads) counts[int64_t(blockIdx.x) * (E + 1) + i] = cnt[i];
+}
+
+// Second launch: places. Each block adds up the counts of the blocks before
+// it and of all, scans the experts, and places its slots in order; block 0
+// writes the offsets and the groups. place[p]: where slot p stands in the
+// order, counting from 0; slots without an expert come last.
+__global__ void __launch_bounds__(kThreads)
+    place_kernel(const int32_t *experts, int64_t P, int E, const int32_t *counts, int32_t *offsets,
+                 int32_t *order, int32_t *place, SlotGroup *groups, int32_t *n_groups,
+                 int gt_log2) {
+  extern __shared__ int32_t mem[];
+  int32_t *start = mem, *gstart = mem + E + 1;        // [E + 1] each
+  int32_t *cnt = mem + 2 * (E + 1);                   // [kWarps][E + 1]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int64_t lo = int64_t(blockIdx.x) * kSortSlots;
+  const int n = static_cast<int>(P - lo < kSortSlots ? P - lo : kSortSlots);
+  for (int i = threadIdx.x; i < kWarps * (E + 1); i += kThreads) cnt[i] = 0;
+  __syncthreads();
+  constexpr int kPer = kSortSlots / kWarps;
+  auto key_of = [&](int i) {
+    const int e = experts[lo + i];
+    return e >= 0 && e < E ? e : E;
+  };
+  int32_t *mine = cnt + warp * (E + 1);
+  for (int i = warp * kPer + lane; i < min(n, (warp + 1) * kPer); i += 32)
+    atomicAdd(mine + key_of(i), 1);
+  // Totals, and the part of them in the blocks before; two threads per
+  // expert where there are that many.
+  __syncthreads();
+  for (int e = threadIdx.x; e <= E; e += kThreads) {
+    int all = 0, before = 0;
+#pragma unroll 8
+    for (int b = 0; b < gridDim.x; ++b) {
+      const int c = counts[int64_t(b) * (E + 1) + e];
+      all += c;
+      if (b < blockIdx.x) before += c;
+    }
+    start[e] = all;
+    gstart[e] = e < E ? (all + (1 << gt_log2) - 1) >> gt_log2 : 0;
+    for (int w = 0; w < kWarps; ++w) {  // where each warp's first slot goes, less start
+      const int c = cnt[w * (E + 1) + e];
+      cnt[w * (E + 1) + e] = before;
+      before += c;
+    }
+  }
+  __syncthreads();
+  if (warp < 2) {  // exclusive prefixes over the experts: slots, groups
+    int32_t *v = warp ? gstart : start;
+    int base = 0;
+    for (int i = lane; i - lane <= E; i += 32) {
+      const int own = i <= E ? v[i] : 0;
+      int x = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (i <= E) v[i] = base + x - own;
+      base += __shfl_sync(0xffffffffu, x, 31);
+    }
+  }
+  __syncthreads();
+  if (blockIdx.x == 0) {
+    for (int e = threadIdx.x; e <= E; e += kThreads) {
+      offsets[e] = start[e];
+      if (groups && e < E) {
+        const int first = start[e], c = start[e + 1] - first, gt = 1 << gt_log2;
+        SlotGroup *g = groups + gstart[e];
+        for (int k = 0; k < c; k += gt) *g++ = SlotGroup{e, first + k, min(gt, c - k)};
+      }
+    }
+    if (groups && threadIdx.x == 0) *n_groups = gstart[E];
+  }
+  for (int i0 = warp * kPer; i0 < min(n, (warp + 1) * kPer); i0 += 32) {
+    const int i = i0 + lane;
+    const bool ok = i < n;
+    const int e = ok ? key_of(i) : -1;
+    const unsigned same = __match_any_sync(0xffffffffu, e);
+    const int rank = __popc(same & ((1u << lane) - 1));
+    if (ok) {
+      const int at = start[e] + mine[e] + rank;
+      order[at] = static_cast<int32_t>(lo + i);
+      if (place) place[lo + i] = at;
+    }
+    __syncwarp();
+    if (ok && rank == 0) mine[e] += __popc(same);
+    __syncwarp();
+  }
+}
+
+// bf16 activation rows as fp16, one copy for each routed slot, at the slot's
+// place: row m of A [M, K] for slots m * copies .. (copies = top_k, or 1
+// with a row per slot). A block per row. Also per place: what undoes the
+// row's scale, and (norm1 given) a bound of the row's 1-norm. Rows of Y of
+// slots without an expert are cleared (Y given), and so are the columns
+// hidden_n .. hidden_ld of the hidden rows.
+struct ConvertArgs {
+  const uint16_t *A;
+  int a_vec, K, Kp, copies;
+  const int32_t *place, *offsets;
+  int E;
+  uint16_t *out;
+  float *unscale, *norm1;
+  uint16_t *Y;
+  int N;
+  uint16_t *hidden;
+  int hidden_n, hidden_ld;
+};
+__global__ void __launch_bounds__(kThreads) convert_kernel(const ConvertArgs a) {
+  __shared__ uint32_t tops[kWarps];
+  __shared__ float sums[kWarps];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int64_t m = blockIdx.x;
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int routed = a.offsets[a.E];
+  uint32_t top = 0;
+  float sum = 0.f;
+  for (int k = tid * 8; k < a.Kp; k += kThreads * 8) {
+    float v[8];
+    load8(a.A, false, a.a_vec, m * a.K, k, a.K, v);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      top = max(top, __float_as_uint(v[q]) & 0x7FFFFFFFu);
+      sum += fabsf(v[q]);
+    }
+  }
+  top = __reduce_max_sync(0xffffffffu, top);
+  sum = warp_sum(sum);
+  if (lane == 0) {
+    tops[warp] = top;
+    sums[warp] = sum;
+  }
+  __syncthreads();
+  sum = 0.f;
+  for (int w = 0; w < kWarps; ++w) {
+    top = max(top, tops[w]);
+    sum += sums[w];
+  }
+  const int shift = row_shift(top);
+  const float f = exp2i(shift);
+  for (int j = 0; j < a.copies; ++j) {
+    const int64_t slot = m * a.copies + j;
+    const int at = a.place[slot];
+    if (at < routed) {
+      if (tid == 0) {
+        a.unscale[at] = exp2i(-shift);
+        if (a.norm1) a.norm1[at] = sum * 1.01f;  // above the exact sum for any K < 2^17
+      }
+      if (a.hidden)
+        for (int k = a.hidden_n + tid; k < a.hidden_ld; k += kThreads)
+          a.hidden[int64_t(at) * a.hidden_ld + k] = 0;
+    } else if (a.Y) {
+      for (int n = tid; n < a.N; n += kThreads) a.Y[slot * a.N + n] = 0;
+    }
+  }
+  for (int k = tid * 8; k < a.Kp; k += kThreads * 8) {
+    float v[8];
+    load8(a.A, false, a.a_vec, m * a.K, k, a.K, v);
+    uint4 h;
+    h.x = pack_f16x2(v[0] * f, v[1] * f);
+    h.y = pack_f16x2(v[2] * f, v[3] * f);
+    h.z = pack_f16x2(v[4] * f, v[5] * f);
+    h.w = pack_f16x2(v[6] * f, v[7] * f);
+    for (int j = 0; j < a.copies; ++j) {
+      const int at = a.place[m * a.copies + j];
+      if (at < routed) *reinterpret_cast<uint4 *>(a.out + int64_t(at) * a.Kp + k) = h;
+    }
+  }
+}
+
+// Per packed row of a stack: the power of two that brings its largest |scale|
+// into 2^9 .. 2^10; per expert: the bits of the largest |scale| and |bias|
+// (cleared before). A warp per 16-row tile; the tile's scales are contiguous
+// and go by 16-byte pieces, whose rows depend on the lane alone.
+struct ScaleArgs {
+  const unsigned char *s[3];
+  const float *bias[3];
+  float *fac[3];
+  uint32_t *smax[3], *bmax[3];
+  int64_t tiles_end[3];  // running sums of the stacks' tiles
+  int N[3], N16[3], nb[3], f32[3];
+  int count;
+};
+__global__ void __launch_bounds__(kThreads) tile_scales_kernel(const ScaleArgs a) {
+  const int lane = threadIdx.x & 31;
+  grid_dependency_wait();
+  grid_dependents_launch();
+  int64_t tile = blockIdx.x * int64_t(kWarps) + (threadIdx.x >> 5);
+  int i = 0;
+  while (i < a.count && tile >= a.tiles_end[i]) ++i;
+  if (i == a.count) return;
+  if (i > 0) tile -= a.tiles_end[i - 1];
+  const int per = a.f32[i] ? 4 : 8;  // scales per piece
+  const int pieces = a.nb[i] * 16 / per;
+  const uint4 *src = reinterpret_cast<const uint4 *>(
+      a.s[i] + tile * a.nb[i] * (16 * (a.f32[i] ? 4 : 2)));
+  uint32_t top[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 4
+  for (int q = lane; q < pieces; q += 32) {
+    const uint4 x = src[q];
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int o = 0; o < 4; ++o) {
+      if (a.f32[i]) {
+        top[o] = max(top[o], w[o] & 0x7FFFFFFFu);
+      } else {
+        top[2 * o] = max(top[2 * o], (w[o] << 16) & 0x7FFF0000u);
+        top[2 * o + 1] = max(top[2 * o + 1], w[o] & 0x7FFF0000u);
+      }
+    }
+  }
+  // Lanes with the same piece of a block: equal modulo 2 (bf16) or 4 (fp32).
+#pragma unroll
+  for (int o = 2; o < 32; o <<= 1)
+#pragma unroll
+    for (int r = 0; r < 8; ++r)
+      if (o >= 4 || !a.f32[i]) top[r] = max(top[r], __shfl_xor_sync(0xffffffffu, top[r], o));
+  uint32_t most = 0;
+#pragma unroll
+  for (int r = 0; r < 8; ++r) {
+    if (r >= per) break;
+    most = max(most, top[r]);
+    if (lane < 16 / per) a.fac[i][tile * kTileN + lane * per + r] = exp2i(row_shift(top[r]) - 5);
+  }
+  most = __reduce_max_sync(0xffffffffu, most);
+  const int e = static_cast<int>(tile / a.N16[i]);
+  uint32_t b = 0;
+  const int n = static_cast<int>(tile % a.N16[i]) * kTileN + lane;
+  if (a.bias[i] && lane < kTileN && n < a.N[i])
+    b = __float_as_uint(a.bias[i][int64_t(e) * a.N[i] + n]) & 0x7FFFFFFFu;
+  b = __reduce_max_sync(0xffffffffu, b);
+  if (lane == 0) {
+    atomicMax(a.smax[i] + e, most);
+    if (b) atomicMax(a.bmax[i] + e, b);
+  }
+}
+
+// Sum of each token's fp16 partials, in slot order.
+__global__ void __launch_bounds__(kThreads)
+    combine_half_kernel(const uint16_t *part, const float *unscale, const int32_t *place,
+                        const int32_t *offsets, int E, int64_t M, int top_k, int N, uint16_t *Y) {
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int routed = offsets[E];
+  const int64_t m = blockIdx.x;
+  const bool vec = N % 8 == 0;  // rows of partials and of Y start on 16 bytes
+  const bool yvec = vec && reinterpret_cast<uintptr_t>(Y) % 16 == 0;
+  for (int n = threadIdx.x * 8; n < N; n += kThreads * 8) {
+    float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < top_k; ++j) {
+      const int at = place[m * top_k + j];
+      if (at >= routed) continue;
+      const float f = unscale[at];
+      const uint16_t *src = part + int64_t(at) * N + n;
+      uint32_t w[4];
+      if (vec) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(src);
+        w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          w[q] = (n + 2 * q < N ? src[2 * q] : 0) |
+                 (n + 2 * q + 1 < N ? uint32_t(src[2 * q + 1]) << 16 : 0);
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&w[q]));
+        y[2 * q] = fmaf(v.x, f, y[2 * q]);
+        y[2 * q + 1] = fmaf(v.y, f, y[2 * q + 1]);
+      }
+    }
+    uint16_t *dst = Y + m * N + n;
+    if (yvec) {
+      uint32_t w[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) w[q] = bf16_bits(y[2 * q]) | (bf16_bits(y[2 * q + 1]) << 16);
+      *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+      for (int q = 0; q < 8; ++q)
+        if (n + q < N) dst[q] = static_cast<uint16_t>(bf16_bits(y[q]));
+    }
+  }
+}
+
 // Sum of each token's down partials, in slot order (long inputs).
 __global__ void __launch_bounds__(kThreads)
     combine_kernel(const float *part, const int32_t *experts, int64_t M, int top_k, int N,
@@ -574,6 +886,201 @@ ExpertsSpace experts_space(const ExpertsArgs &a) {
   return s;
 }
 
+// ---- tensor-core path: bf16 activations, many slots ---------------------------
+
+// From this many slots on; fewer stream the weights past groups of 8 slots.
+constexpr int kTileMinSlots = 257;
+bool tile_path(bool a_f32, int64_t P) { return !a_f32 && P >= kTileMinSlots; }
+
+int64_t k_pad(int64_t K) { return ceil_div(K, kChunkK) * kChunkK; }
+
+struct TileSpace {
+  Lists l;
+  int32_t *counts, *place;
+  uint32_t *clear;  // per stack: smax [E], bmax [E]
+  float *fac[3];
+  uint16_t *rows;   // fp16 activations by place
+  float *unscale, *norm1;
+  // The layer's.
+  uint16_t *hidden, *part;
+  float *h_unscale, *p_unscale;
+  int32_t *h_shift;
+  size_t bytes;
+};
+TileSpace tile_space(unsigned char *ws, int64_t P, const ExpertStack *const *w, int stacks,
+                     bool layer) {
+  Carve c{ws};
+  TileSpace s{};
+  const int E = w[0]->E;
+  if (layer) {
+    s.l.weights = c.take<float>(P);
+    s.l.experts = c.take<int32_t>(P);
+  }
+  s.l.offsets = c.take<int32_t>(E + 1);
+  s.l.order = c.take<int32_t>(P);
+  s.l.n_groups = c.take<int32_t>(1);
+  s.l.groups = c.take<SlotGroup>(max_groups(P, E, kTileSlotsLog2));
+  s.counts = c.take<int32_t>(ceil_div(P, kSortSlots) * (E + 1));
+  s.place = c.take<int32_t>(P);
+  s.clear = c.take<uint32_t>(size_t(stacks) * 2 * E);
+  for (int i = 0; i < stacks; ++i)
+    s.fac[i] = c.take<float>(size_t(E) * ceil_div(w[i]->N, kTileN) * kTileN);
+  s.rows = c.take<uint16_t>(size_t(P) * k_pad(w[0]->K));
+  s.unscale = c.take<float>(P);
+  if (layer) {
+    s.norm1 = c.take<float>(P);
+    s.hidden = c.take<uint16_t>(size_t(P) * k_pad(w[2]->K));
+    s.part = c.take<uint16_t>(size_t(P) * w[2]->N);
+    s.h_unscale = c.take<float>(P);
+    s.p_unscale = c.take<float>(P);
+    s.h_shift = c.take<int32_t>(P);
+  }
+  s.bytes = c.used;
+  return s;
+}
+
+// Lists by place, and the stacks' scale factors.
+cudaError_t launch_tile_lists(const TileSpace &s, const int32_t *experts, int64_t P,
+                              const ExpertStack *const *w, int stacks, bool pdl,
+                              cudaStream_t stream) {
+  const int E = w[0]->E;
+  const unsigned blocks = static_cast<unsigned>(ceil_div(P, kSortSlots));
+  cudaError_t e = launch_pdl(count_kernel, blocks, kThreads, size_t(E + 1) * 4, pdl, stream,
+                             experts, P, E, s.counts, s.clear, stacks * 2 * E);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(place_kernel, blocks, kThreads, size_t(2 + kWarps) * (E + 1) * 4, pdl, stream,
+                 experts, P, E, s.counts, s.l.offsets, s.l.order, s.place, s.l.groups,
+                 s.l.n_groups, kTileSlotsLog2);
+  if (e != cudaSuccess) return e;
+  ScaleArgs a{};
+  a.count = stacks;
+  int64_t end = 0;
+  for (int i = 0; i < stacks; ++i) {
+    a.s[i] = static_cast<const unsigned char *>(w[i]->s);
+    a.bias[i] = w[i]->bias;
+    a.fac[i] = s.fac[i];
+    a.smax[i] = s.clear + (2 * i) * E;
+    a.bmax[i] = s.clear + (2 * i + 1) * E;
+    a.N[i] = w[i]->N;
+    a.N16[i] = static_cast<int>(ceil_div(w[i]->N, kTileN));
+    a.nb[i] = static_cast<int>(ceil_div(w[i]->K, w[i]->bs));
+    a.f32[i] = w[i]->s_f32;
+    end += int64_t(E) * a.N16[i];
+    a.tiles_end[i] = end;
+  }
+  return launch_pdl(tile_scales_kernel, static_cast<unsigned>(ceil_div(end, kWarps)), kThreads, 0,
+                    pdl, stream, a);
+}
+
+cudaError_t fill_tile(TileParams &p, int mode, const ExpertStack *const *w, int first,
+                      const TileSpace &s, const uint16_t *rows, int64_t P) {
+  const ExpertStack &w0 = *w[first];
+  p.mode = mode;
+  for (int m = 0; m < 2; ++m) {
+    const int i = mode == kStreamGateUp ? first + m : first;
+    p.w[m] = stream_mat(*w[i]);
+    p.ts[m] = TileScales{s.fac[i], s.clear + 2 * i * w0.E, s.clear + (2 * i + 1) * w0.E};
+  }
+  p.E = w0.E;
+  p.N = w0.N;
+  p.N16 = static_cast<int>(ceil_div(w0.N, kTileN));
+  p.K64 = static_cast<int>(ceil_div(w0.K, kChunkK));
+  p.nb = static_cast<int>(ceil_div(w0.K, w0.bs));
+  p.nbz = (p.nb + 1) / 2 * 2;
+  p.bs_log2 = ilog2(w0.bs);
+  p.ntile = static_cast<int>(ceil_div(w0.N, mode == kStreamGateUp ? 64 : 128));
+  p.order = s.l.order;
+  p.n_groups = s.l.n_groups;
+  p.groups = s.l.groups;
+  p.weights = s.l.weights;
+  const uint64_t dims[2] = {static_cast<uint64_t>(p.K64) * kChunkK, static_cast<uint64_t>(P)};
+  const uint64_t strides[1] = {dims[0] * 2};
+  const uint32_t box[2] = {kChunkK, kTileBox};
+  return make_tmap(&p.tmb, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, rows, dims, strides, box,
+                   CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+cudaError_t launch_experts_tile(const ExpertsArgs &a, cudaStream_t stream) {
+  const int64_t P = a.M * a.top_k;
+  const ExpertStack *w[1] = {&a.w};
+  const TileSpace s = tile_space(a.ws, P, w, 1, false);
+  cudaError_t e = launch_tile_lists(s, a.experts, P, w, 1, a.pdl, stream);
+  if (e != cudaSuccess) return e;
+  ConvertArgs c{};
+  c.A = static_cast<const uint16_t *>(a.A);
+  c.a_vec = vec_rows(a.A, a.w.K, 2);
+  c.K = a.w.K;
+  c.Kp = static_cast<int>(k_pad(a.w.K));
+  c.copies = a.per_slot ? 1 : a.top_k;
+  c.place = s.place;
+  c.offsets = s.l.offsets;
+  c.E = a.w.E;
+  c.out = s.rows;
+  c.unscale = s.unscale;
+  c.Y = static_cast<uint16_t *>(a.Y);
+  c.N = a.w.N;
+  e = launch_pdl(convert_kernel, static_cast<unsigned>(a.per_slot ? P : a.M), kThreads, 0, a.pdl,
+                 stream, c);
+  if (e != cudaSuccess) return e;
+  TileParams p{};
+  e = fill_tile(p, kStreamProduct, w, 0, s, s.rows, P);
+  if (e != cudaSuccess) return e;
+  p.unscale = s.unscale;
+  p.Y = static_cast<uint16_t *>(a.Y);
+  return launch_tile(p, a.w.z != nullptr, a.w.s_f32, a.w.bs, a.pdl, stream);
+}
+
+cudaError_t launch_moe_tile(const MoeArgs &a, cudaStream_t stream) {
+  const int64_t P = a.M * a.top_k;
+  const ExpertStack *w[3] = {&a.gate, &a.up, &a.down};
+  const TileSpace s = tile_space(a.ws, P, w, 3, true);
+  cudaError_t e = launch_pdl(route_kernel, grid_of(a.M, kWarps), kThreads,
+                             size_t(kWarps) * a.gate.E * 4, a.pdl, stream, a.logits,
+                             a.logits_f32, a.M, a.gate.E, a.top_k, a.normalize, s.l.weights,
+                             s.l.experts);
+  if (e == cudaSuccess) e = launch_tile_lists(s, s.l.experts, P, w, 3, a.pdl, stream);
+  if (e != cudaSuccess) return e;
+  ConvertArgs c{};
+  c.A = static_cast<const uint16_t *>(a.X);
+  c.a_vec = vec_rows(a.X, a.gate.K, 2);
+  c.K = a.gate.K;
+  c.Kp = static_cast<int>(k_pad(a.gate.K));
+  c.copies = a.top_k;
+  c.place = s.place;
+  c.offsets = s.l.offsets;
+  c.E = a.gate.E;
+  c.out = s.rows;
+  c.unscale = s.unscale;
+  c.norm1 = s.norm1;
+  c.hidden = s.hidden;
+  c.hidden_n = a.gate.N;
+  c.hidden_ld = static_cast<int>(k_pad(a.gate.N));
+  e = launch_pdl(convert_kernel, static_cast<unsigned>(a.M), kThreads, 0, a.pdl, stream, c);
+  if (e != cudaSuccess) return e;
+  TileParams up{}, down{};
+  e = fill_tile(up, kStreamGateUp, w, 0, s, s.rows, P);
+  if (e != cudaSuccess) return e;
+  up.unscale = s.unscale;
+  up.norm1 = s.norm1;
+  up.hidden = s.hidden;
+  up.ldh = c.hidden_ld;
+  up.out_unscale = s.h_unscale;
+  up.out_shift = s.h_shift;
+  e = launch_tile(up, a.gate.z != nullptr, a.gate.s_f32, a.gate.bs, a.pdl, stream);
+  if (e != cudaSuccess) return e;
+  e = fill_tile(down, kStreamDown, w, 2, s, s.hidden, P);
+  if (e != cudaSuccess) return e;
+  down.unscale = s.h_unscale;
+  down.shift = s.h_shift;
+  down.part = s.part;
+  down.out_unscale = s.p_unscale;
+  e = launch_tile(down, a.down.z != nullptr, a.down.s_f32, a.down.bs, a.pdl, stream);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(combine_half_kernel, static_cast<unsigned>(a.M), kThreads, 0, a.pdl, stream,
+                    s.part, s.p_unscale, s.place, s.l.offsets, a.gate.E, a.M, a.top_k, a.down.N,
+                    static_cast<uint16_t *>(a.Y));
+}
+
 cudaError_t launch_prep(const PrepArgs &a, bool pdl, cudaStream_t stream) {
   const int P = a.M * a.top_k;
   // Keys in shared memory for more experts than registers hold.
@@ -638,11 +1145,16 @@ cudaError_t launch_moe_route(const RouteArgs &a, cudaStream_t stream) {
 size_t matmul_experts_workspace_bytes(const ExpertsArgs &a) {
   ExpertsArgs b = a;
   b.ws = nullptr;
+  if (tile_path(a.a_f32, a.M * a.top_k)) {
+    const ExpertStack *w[1] = {&a.w};
+    return tile_space(nullptr, a.M * a.top_k, w, 1, false).bytes;
+  }
   return experts_space(b).bytes;
 }
 
 cudaError_t launch_matmul_experts(const ExpertsArgs &a, cudaStream_t stream) {
   const int64_t P = a.M * a.top_k, rows = a.per_slot ? P : a.M;
+  if (tile_path(a.a_f32, P)) return launch_experts_tile(a, stream);
   StreamPlan pl;
   if (!plan_stream(pl, a.w, kStreamProduct, a.a_f32 ? 2 : 1, P, a.M, a.top_k, P))
     return cudaErrorNotSupported;
@@ -690,12 +1202,17 @@ cudaError_t launch_matmul_experts(const ExpertsArgs &a, cudaStream_t stream) {
 size_t moe_workspace_bytes(const MoeArgs &a) {
   MoeArgs b = a;
   b.ws = nullptr;
+  if (tile_path(a.a_f32, a.M * a.top_k)) {
+    const ExpertStack *w[3] = {&a.gate, &a.up, &a.down};
+    return tile_space(nullptr, a.M * a.top_k, w, 3, true).bytes;
+  }
   return moe_space(b).bytes;
 }
 
 cudaError_t launch_moe(const MoeArgs &a, cudaStream_t stream) {
   const int64_t P = a.M * a.top_k;
   const bool few = P <= kFewSlots;
+  if (tile_path(a.a_f32, P)) return launch_moe_tile(a, stream);
   const MoeSpace s = moe_space(a);
   StreamPlan up, down;
   const int terms = a.a_f32 ? 2 : 1;

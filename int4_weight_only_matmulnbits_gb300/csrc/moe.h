@@ -81,4 +81,7 @@ struct MoeArgs {
 size_t moe_workspace_bytes(const MoeArgs &a);
 cudaError_t launch_moe(const MoeArgs &a, cudaStream_t stream);
 
+// Reads and clears the fault word of the tensor-core kernel.
+cudaError_t moe_take_fault(unsigned int *out);
+
 }  // namespace mnb

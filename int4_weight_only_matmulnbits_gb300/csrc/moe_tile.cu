@@ -1,0 +1,493 @@
+// Tensor-core (tcgen05 / TMEM) kernel of the expert layer, for many slots.
+//
+// One unit of work is a group of up to 128 slots that share an expert times
+// a column tile of the expert's weight: 128 weight rows (64 of gate and the
+// same 64 of up, or 128 of one matrix). The weight rows are the MMA's A
+// operand (M = 128), the slots its columns (N = slots rounded up to 16), so
+// ragged lists cost no tensor work beyond 15 columns:
+//   D[row, slot] = sum_k w[row, k] x[slot, k]
+//
+//  * A comes from TMEM. A lane's 16 fp16 pairs of a packed 16 x 64 chunk are
+//    exactly the registers of a 16x256b TMEM store, so the unpacking warps
+//    write each dequantised chunk with one store, without shared memory,
+//    swizzles or a proxy fence: 32 TMEM columns per 64-wide k stage, four
+//    stages, beside the accumulator's 128 columns. 256 columns per CTA: two
+//    CTAs share an SM, one's epilogue under the other's main loop.
+//  * Weights are fp16, w' = (q - z) * s with each row's scales brought to
+//    2^9 .. 2^10 by a power of two that the epilogue undoes. q - z is exact,
+//    and so is a bf16 scale; the product has 12 bits, fp16 keeps 11: one
+//    rounding of 2^-11 at most, an eighth of a bf16 weight's.
+//  * B are fp16 activation rows, scaled by a power of two per row, in the
+//    order of the lists: TMA tiles of 32 rows x 64 k, 128-byte swizzle.
+//  * Hidden values leave as fp16, the row scaled so that a bound of it (15 s
+//    times the 1-norm of x, for gate and for up) fits: typical values then
+//    lie 15 or so octaves above fp16's smallest normal. Down partials
+//    likewise; they are added per token by a kernel that follows.
+//  * Warps 0-7 unpack, then do the epilogue; each streams its own tile's
+//    codes and scales through a private ring of asynchronous copies. Warp 8
+//    issues the TMA loads, warp 9 the MMAs.
+// Unpacking costs a chunk (64 k of 16 rows) about 85 instructions, 700 per
+// stage and CTA; a stage of 128 slots keeps the tensor core busy for 256
+// cycles. Below some 90 slots per group the unpacking bounds the kernel, at
+// about the rate memory delivers the weights.
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "mnb_common.cuh"
+#include "mnb_launch.h"
+#include "moe.h"
+#include "moe_half.cuh"
+#include "moe_tile.h"
+#include "umma.cuh"
+
+namespace mnb {
+
+__device__ unsigned int g_fault_moe = 0;
+
+namespace {
+
+constexpr int kDqWarps = 8;
+constexpr int kThreads = 32 * (kDqWarps + 2);
+constexpr int kAStages = 4;   // TMEM A stages (32 columns each)
+constexpr int kBStages = 4;   // activation stages
+constexpr int kRing = 6;      // weight chunks per warp in flight
+constexpr int kBStageBytes = kTileSlots * 128;
+constexpr int kTmemCols = 256;
+constexpr int kBarDq = 1;     // named barrier of the unpacking warps
+
+__host__ __device__ constexpr uint32_t idesc_f16(int n) {  // D fp32, A and B fp16, K-major, M = 128
+  return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
+}
+
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                        bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(static_cast<int>(accumulate))
+      : "memory");
+}
+__device__ __forceinline__ void umma_commit(uint64_t *bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+          smem_addr(bar))
+      : "memory");
+}
+// 16 lanes x 32 columns: lane (g, t) writes, for j < 4, columns 8j + 2t and
+// 8j + 2t + 1 of TMEM lanes g (r[4j], r[4j+1]) and g + 8 (r[4j+2], r[4j+3]).
+__device__ __forceinline__ void tmem_st_16x64(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15])
+      : "memory");
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+struct Layout {  // shared memory, from a 1024-byte aligned base
+  int ring_bytes, scale, zp, chunk_bytes;
+  int off_ring, off_col, off_bar, total;
+};
+// Per column of a unit, for the epilogue: two buffers by turns.
+struct Column {
+  float unscale;  // undoes the activation row's scale (times the output's scale)
+  float weight;
+  int out;        // slot (product) or place
+  float scale;    // output scale (gate and up, down)
+};
+
+template <int BS, bool SF32, bool ZP>
+__host__ __device__ constexpr Layout make_layout() {
+  Layout l{};
+  constexpr int kBlk = BS < kChunkK ? kChunkK / BS : 1;
+  l.scale = kChunkBytes;
+  l.zp = l.scale + kBlk * kTileN * (SF32 ? 4 : 2);
+  l.chunk_bytes = l.zp + (ZP ? (kBlk == 1 ? 16 : kBlk * 8) : 0);
+  l.ring_bytes = kRing * l.chunk_bytes;
+  l.off_ring = kBStages * kBStageBytes;
+  l.off_col = l.off_ring + kDqWarps * l.ring_bytes;
+  l.off_bar = l.off_col + 2 * kTileSlots * static_cast<int>(sizeof(Column));
+  l.total = l.off_bar + 256;
+  return l;
+}
+
+// Smallest e with x < 2^e, for x >= 0 (0: a very small one; not finite: 128).
+__device__ __forceinline__ int expo(float x) {
+  return static_cast<int>(__float_as_uint(x) >> 23) - 126;
+}
+
+template <int BS, bool ZP, bool SF32>
+__global__ void __launch_bounds__(kThreads, 2) tile_kernel(const __grid_constant__ TileParams p) {
+  constexpr Layout kL = make_layout<BS, SF32, ZP>();
+  constexpr int kEs = SF32 ? 4 : 2;
+  constexpr int kBlk = BS < kChunkK ? kChunkK / BS : 1;  // blocks per chunk
+  constexpr int kSpb = 4 / kBlk;                         // 16-wide steps per block
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+  uint64_t *afull = reinterpret_cast<uint64_t *>(smem + kL.off_bar);
+  uint64_t *aempty = afull + kAStages;
+  uint64_t *bfull = aempty + kAStages;
+  uint64_t *bempty = bfull + kBStages;
+  uint64_t *dfull = bempty + kBStages;
+  uint64_t *dempty = dfull + 1;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(dempty + 1);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < kAStages; ++i) {
+      mbar_init(afull + i, kDqWarps);
+      mbar_init(aempty + i, 1);
+    }
+    for (int i = 0; i < kBStages; ++i) {
+      mbar_init(bfull + i, 1);
+      mbar_init(bempty + i, 1);
+    }
+    mbar_init(dfull, 1);
+    mbar_init(dempty, kDqWarps);
+    fence_barrier_init();
+  }
+  if (warp == kDqWarps + 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_addr(tmem_slot)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_a = *tmem_slot, tmem_d = tmem_a + kAStages * 32;
+
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int units = *p.n_groups * p.ntile;
+  const bool gate_up = p.mode == kStreamGateUp;
+
+  if (warp == kDqWarps) {
+    if (lane == 0) {  // ---- TMA: activation rows ----------------------------------
+      int it = 0;
+      bool ok = true;
+      for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+        const SlotGroup sg = p.groups[u / p.ntile];
+        const int boxes = (sg.cols + kTileBox - 1) / kTileBox;
+        for (int kb = 0; kb < p.K64; ++kb, ++it) {
+          const int s = it % kBStages;
+          if (it >= kBStages && !mbar_wait(bempty + s, (it / kBStages - 1) & 1)) {
+            record_fault(&g_fault_moe, kFaultMoeWait);
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(bfull + s, boxes * kTileBox * 128);
+          for (int b = 0; b < boxes; ++b)
+            tma_load_2d(smem + s * kBStageBytes + b * kTileBox * 128, &p.tmb, kb * kChunkK,
+                        sg.first + b * kTileBox, bfull + s);
+        }
+      }
+    }
+  } else if (warp == kDqWarps + 1) {
+    if (lane == 0) {  // ---- MMA ------------------------------------------------------
+      int it = 0, n = 0;
+      bool ok = true;
+      for (int u = blockIdx.x; u < units && ok; u += gridDim.x, ++n) {
+        const uint32_t idesc = idesc_f16((p.groups[u / p.ntile].cols + 15) & ~15);
+        if (n > 0 && !mbar_wait(dempty, (n - 1) & 1)) ok = false;
+        tc_fence_after();
+        for (int kb = 0; kb < p.K64 && ok; ++kb, ++it) {
+          const int a = it % kAStages, b = it % kBStages;
+          if (!mbar_wait(bfull + b, (it / kBStages) & 1) ||
+              !mbar_wait(afull + a, (it / kAStages) & 1)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t b_base = smem_addr(smem + b * kBStageBytes);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_ts(tmem_d, tmem_a + a * 32 + kk * 8, smem_desc_sw128(b_base + kk * 32), idesc,
+                    kb > 0 || kk > 0);
+          umma_commit(aempty + a);
+          umma_commit(bempty + b);
+        }
+        if (ok) umma_commit(dfull);
+        else record_fault(&g_fault_moe, kFaultMoeWait);
+      }
+    }
+  } else {
+    // ---- unpacking and epilogue ---------------------------------------------------
+    const int g = lane >> 2;
+    const int quarter = warp & 3, half = warp >> 2;  // TMEM lanes 32 quarter + 16 half ..
+    unsigned char *ring = smem + kL.off_ring + warp * kL.ring_bytes;
+    const uint32_t ring_u = smem_addr(ring);
+    Column *cols2 = reinterpret_cast<Column *>(smem + kL.off_col);
+    const int mat = gate_up ? half : 0;
+    // The tile of a unit this warp unpacks (past the last: the last again,
+    // its rows are never stored).
+    auto tile_of = [&](int u) {
+      const SlotGroup *sg = p.groups + u / p.ntile;
+      const int nt = u % p.ntile;
+      const int i = gate_up ? 4 * nt + quarter : 8 * nt + 2 * quarter + half;
+      return int64_t(sg->e) * p.N16 + min(i, p.N16 - 1);
+    };
+    // Fetch cursor.
+    int fu = blockIdx.x, fc = 0, fslot = 0;
+    const uint4 *fw = nullptr;
+    const unsigned char *fs = nullptr, *fz = nullptr;
+    auto aim = [&] {
+      const int64_t tile = tile_of(fu);
+      fw = p.w[mat].b + tile * p.K64 * 32 + lane;
+      fs = p.w[mat].s + tile * p.nb * (kTileN * kEs) + lane * 16;
+      if (ZP) fz = p.w[mat].z + tile * p.nbz * 8 + lane * 16;
+    };
+    if (fu < units) aim();
+    auto fetch = [&] {
+      if (fu < units) {
+        const uint32_t dst = ring_u + fslot * kL.chunk_bytes + lane * 16;
+        cp16(dst, fw + fc * 32);
+        const int b0 = BS > kChunkK ? (fc * kChunkK) / BS : fc * kBlk;
+        const int n = min(kBlk, p.nb - b0);  // the rest of the chunk has k >= K
+        if (lane < n * kEs) cp16(dst + kL.scale, fs + b0 * (kTileN * kEs));
+        else if (lane < kBlk * kEs)
+          *reinterpret_cast<uint4 *>(ring + fslot * kL.chunk_bytes + kL.scale + lane * 16) =
+              make_uint4(0, 0, 0, 0);
+        if (ZP && lane < (kBlk + 1) / 2 && 2 * lane < p.nbz - (b0 & ~1))
+          cp16(dst + kL.zp, fz + (b0 / 2) * 16);
+        fslot = fslot == kRing - 1 ? 0 : fslot + 1;
+        if (++fc == p.K64) {
+          fc = 0;
+          fu += gridDim.x;
+          if (fu < units) aim();
+        }
+      }
+      cp_commit();
+    };
+    for (int i = 0; i < kRing - 1; ++i) fetch();
+
+    int it = 0, slot = 0, n = 0;
+    bool ok = true;
+    for (int u = blockIdx.x; u < units && ok; u += gridDim.x, ++n) {
+      const SlotGroup sg = p.groups[u / p.ntile];
+      const int nt = u % p.ntile;
+      const int64_t tile = tile_of(u);
+      const float f0 = p.ts[mat].fac[tile * kTileN + g];
+      const float f1 = p.ts[mat].fac[tile * kTileN + g + 8] * 0.0625f;  // high nibbles: 16 q
+      // Column data of the unit.
+      Column *col = cols2 + (n & 1) * kTileSlots;
+      if (tid < sg.cols) {
+        const int place = sg.first + tid, id = p.order[place];
+        Column c;
+        c.unscale = p.unscale[place];
+        c.weight = gate_up || p.mode == kStreamDown ? p.weights[id] : 1.f;
+        c.out = p.mode == kStreamProduct ? id : place;
+        c.scale = 1.f;
+        auto bits = [&](const uint32_t *v) { return __uint_as_float(v[sg.e]); };
+        if (gate_up) {
+          // |h| <= (15 s |x|_1 + |b|) for gate times the same for up.
+          const float x1 = p.norm1[place];
+          int e = 0;
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+            e += expo(15.f * bits(p.ts[m].smax) * x1 + bits(p.ts[m].bmax));
+          const int shift = max(-126, min(126, 15 - e));
+          c.scale = exp2i(shift);
+          if (nt == 0) {
+            p.out_unscale[place] = exp2i(-shift);
+            p.out_shift[place] = shift;
+          }
+        } else if (p.mode == kStreamDown) {
+          // |sum| <= 15 s K 2^15 / 2^shift, and the bias.
+          const int e = max(expo(15.f * bits(p.ts[0].smax) * static_cast<float>(p.K64 * kChunkK)) +
+                                15 - p.shift[place],
+                            expo(bits(p.ts[0].bmax))) + 1;
+          const int shift = max(-126, min(126, 15 - e));
+          c.scale = exp2i(shift);
+          if (nt == 0) p.out_unscale[place] = exp2i(-shift);
+        }
+        col[tid] = c;
+      }
+      for (int kb = 0; kb < p.K64; ++kb, ++it) {
+        const int a = it % kAStages;
+        cp_wait<kRing - 2>();
+        __syncwarp();  // the chunk is there, and every lane is done with the one before
+        fetch();
+        const unsigned char *st = ring + slot * kL.chunk_bytes;
+        slot = slot == kRing - 1 ? 0 : slot + 1;
+        const uint4 w4 = *reinterpret_cast<const uint4 *>(st + lane * 16);
+        const uint32_t wv[4] = {w4.x, w4.y, w4.z, w4.w};
+        uint32_t r[16];
+#pragma unroll
+        for (int bb = 0; bb < kBlk; ++bb) {
+          float s0, s1;
+          if (SF32) {
+            const float *sc = reinterpret_cast<const float *>(st + kL.scale) + bb * kTileN + g;
+            s0 = sc[0];
+            s1 = sc[8];
+          } else {
+            const uint16_t *sc =
+                reinterpret_cast<const uint16_t *>(st + kL.scale) + bb * kTileN + g;
+            s0 = bf16_bits_to_f32(sc[0]);
+            s1 = bf16_bits_to_f32(sc[8]);
+          }
+          s0 *= f0;
+          s1 *= f1;
+          uint32_t z0 = 0x64086408u, z1 = 0x64806480u;  // 1024 + 8, 1024 + 16 * 8
+          if (ZP) {
+            const int b0 = BS > kChunkK ? (kb * kChunkK) / BS : kb * kBlk;
+            const uint2 zw =
+                *reinterpret_cast<const uint2 *>(st + kL.zp + (bb + (b0 & 1)) * 8);
+            z0 = 0x64006400u | (((zw.x >> (4 * g)) & 15u) * 0x10001u);
+            z1 = 0x64006400u | (((zw.y >> (4 * g)) & 15u) * 0x100010u);
+          }
+          const uint32_t h0 = pack_f16x2(s0, s0), h1 = pack_f16x2(s1, s1);
+          auto scaled = [&](uint32_t c, uint32_t z, uint32_t h, float s) {
+            const uint32_t d = f16x2_sub(c, z);  // q - z, or 16 (q - z): exact
+            if (!SF32) return f16x2_mul(d, h);
+            const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&d));
+            return pack_f16x2(v.x * s, v.y * s);
+          };
+#pragma unroll
+          for (int jj = 0; jj < kSpb; ++jj) {
+            const int j = bb * kSpb + jj;
+            uint32_t c[4];
+            codes_to_f16x2(wv[j], c);
+            r[4 * j] = scaled(c[0], z0, h0, s0);
+            r[4 * j + 1] = scaled(c[2], z0, h0, s0);
+            r[4 * j + 2] = scaled(c[1], z1, h1, s1);
+            r[4 * j + 3] = scaled(c[3], z1, h1, s1);
+          }
+        }
+        if (it >= kAStages && !mbar_wait(aempty + a, (it / kAStages - 1) & 1)) {
+          record_fault(&g_fault_moe, kFaultMoeWait);
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        tmem_st_16x64(tmem_a + a * 32 + (static_cast<uint32_t>(32 * quarter + 16 * half) << 16), r);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(afull + a);
+      }
+      // Every unpacking warp meets here, whether or not its waits held.
+      named_barrier_sync(kBarDq, 32 * kDqWarps);  // the columns' data
+      if (ok && !mbar_wait(dfull, n & 1)) {
+        record_fault(&g_fault_moe, kFaultMoeWait);
+        ok = false;
+      }
+      if (!ok) break;
+      tc_fence_after();
+      // ---- epilogue: this warp's TMEM lanes, columns 64 half .. -----------------
+      // TMEM lane of a thread: gate rows 0-15 and up rows 16-31 of a quarter,
+      // or row 32 quarter + lane of the tile.
+      const int row = gate_up ? 64 * nt + 16 * quarter + (lane & 15)
+                              : 128 * nt + 32 * quarter + lane;
+      const bool live = row < p.N;
+      const int m = gate_up ? lane >> 4 : 0;
+      const int64_t srow = int64_t(sg.e) * p.N16 * kTileN + (live ? row : 0);
+      // The inverse of a power of two.
+      const float rinv = __uint_as_float((254u << 23) - __float_as_uint(p.ts[m].fac[srow]));
+      const float bias =
+          p.w[m].bias && live ? p.w[m].bias[int64_t(sg.e) * p.N + row] : 0.f;
+      const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
+      for (int c0 = 64 * half; c0 < 64 * half + 64 && c0 < sg.cols; c0 += 32) {
+        float v[32];
+        tmem_ld32(tmem_d + lanes + c0, v);
+        if (gate_up) {
+          // Lanes below 16 take columns 0-15, the others 16-31: each sends
+          // what the other half-warp lacks.
+          const bool up = lane >= 16;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const Column &mine = col[min(c0 + i, sg.cols - 1)];
+            const Column &theirs = col[min(c0 + 16 + i, sg.cols - 1)];
+            const float lo = v[i] * rinv * mine.unscale + bias;
+            const float hi = v[16 + i] * rinv * theirs.unscale + bias;
+            const float got = __shfl_xor_sync(0xffffffffu, up ? lo : hi, 16);
+            const float gv = up ? got : lo, uv = up ? hi : got;
+            const Column &c = up ? theirs : mine;
+            const int cc = c0 + i + (up ? 16 : 0);
+            const float h = gv / (1.f + __expf(-gv)) * uv * c.weight * c.scale;
+            if (live && cc < sg.cols)
+              p.hidden[c.out * p.ldh + row] = __half_as_ushort(__float2half_rn(h));
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            if (c0 + i >= sg.cols) break;
+            const Column &c = col[c0 + i];
+            const int64_t o = int64_t(c.out) * p.N + row;
+            const float y = v[i] * rinv * c.unscale;
+            if (!live) continue;
+            if (p.mode == kStreamProduct)
+              p.Y[o] = static_cast<uint16_t>(bf16_bits(y + bias));
+            else
+              p.part[o] =
+                  __half_as_ushort(__float2half_rn((bias != 0.f ? fmaf(c.weight, bias, y) : y) * c.scale));
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(dempty);
+    }
+    cp_wait<0>();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kDqWarps + 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_a),
+                 "r"(kTmemCols)
+                 : "memory");
+  }
+}
+
+template <int BS, bool ZP, bool SF32>
+cudaError_t launch_one(const TileParams &p, bool pdl, cudaStream_t stream) {
+  constexpr int kSmem = make_layout<BS, SF32, ZP>().total + 1024;
+  static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs per SM");
+  static std::atomic<unsigned long long> done{0};
+  auto *kernel = tile_kernel<BS, ZP, SF32>;
+  const cudaError_t e = ensure_smem_limit(kernel, kSmem, done);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(2 * sm_count());
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <int BS>
+cudaError_t launch_bs(const TileParams &p, bool zp, bool sf32, bool pdl, cudaStream_t s) {
+  if (zp) return sf32 ? launch_one<BS, true, true>(p, pdl, s) : launch_one<BS, true, false>(p, pdl, s);
+  return sf32 ? launch_one<BS, false, true>(p, pdl, s) : launch_one<BS, false, false>(p, pdl, s);
+}
+
+}  // namespace
+
+cudaError_t launch_tile(const TileParams &p, bool zp, bool sf32, int bs, bool pdl,
+                        cudaStream_t stream) {
+  switch (bs) {
+    case 16: return launch_bs<16>(p, zp, sf32, pdl, stream);
+    case 32: return launch_bs<32>(p, zp, sf32, pdl, stream);
+    case 64: return launch_bs<64>(p, zp, sf32, pdl, stream);
+    case 128: return launch_bs<128>(p, zp, sf32, pdl, stream);
+    default: return launch_bs<256>(p, zp, sf32, pdl, stream);
+  }
+}
+
+cudaError_t moe_take_fault(unsigned int *out) {
+  cudaError_t e = cudaMemcpyFromSymbol(out, g_fault_moe, sizeof(unsigned int));
+  if (e != cudaSuccess) return e;
+  const unsigned int zero = 0;
+  return cudaMemcpyToSymbol(g_fault_moe, &zero, sizeof zero);
+}
+
+}  // namespace mnb

@@ -1,0 +1,51 @@
+// Launch interface of the expert layer's tensor-core kernel (moe_tile.cu),
+// for many slots per expert with bf16 activations.
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "moe_stream.h"
+
+namespace mnb {
+
+constexpr int kTileSlots = 128;  // slots per group (columns of an accumulator)
+constexpr int kTileSlotsLog2 = 7;
+constexpr int kTileBox = 32;     // activation rows per TMA box
+
+// What the weights' scales of a stack are brought to (tile_scales_kernel).
+struct TileScales {
+  const float *fac;      // [E * N16 * 16] power of two per row
+  const uint32_t *smax;  // [E] bits of the largest |scale|
+  const uint32_t *bmax;  // [E] bits of the largest |bias|
+};
+
+struct TileParams {
+  CUtensorMap tmb;  // activation rows: {64 K64, rows} fp16, box {64, 32}, 128-byte swizzle
+  int mode;
+  StreamMat w[2];
+  TileScales ts[2];
+  int E, N, N16, K64, nb, nbz, bs_log2;
+  int ntile;  // column tiles of an expert: 64 columns (gate and up) or 128
+  // Lists: slots by expert; places count along the order.
+  const int32_t *order, *n_groups;
+  const SlotGroup *groups;
+  const float *weights;  // [P] by slot (gate and up, down)
+  // By place: what undoes the activation row's scale, and its 1-norm (gate
+  // and up) or scale exponent (down).
+  const float *unscale, *norm1;
+  const int32_t *shift;
+  // Outputs: Y [P, N] bf16 by slot (product); hidden fp16 rows [P, ldh] and
+  // their undo factors and exponents, by place (gate and up); fp16 partials
+  // [P, N] and their undo factors, by place (down).
+  uint16_t *Y, *hidden, *part;
+  int64_t ldh;
+  float *out_unscale;
+  int32_t *out_shift;
+};
+
+cudaError_t launch_tile(const TileParams &p, bool zp, bool sf32, int bs, bool pdl,
+                        cudaStream_t stream);
+
+}  // namespace mnb

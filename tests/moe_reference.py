@@ -19,7 +19,10 @@ choose:
     1 or 16, divided out again at the end), and (1024 + r z) s / r times the sum of a block's
     activations comes off. That sum has at most 64 terms; it and the products it comes off are
     each within 64 2^-24 of (1024 + r z) s / r times the activations' magnitudes, at most
-    OFFSET = 2 * 64 * 1039 * 2^-24 of the sum of |a| s in all (r = 1, z = 15).
+    OFFSET = 2 * 64 * 1039 * 2^-24 of the sum of |a| s in all (r = 1, z = 15). The layer's
+    down sums may leave as fp16 before they are added (2^-11), scaled by a bound of theirs: at
+    most 2^-25 of 2^e / 2^15, where 2^e is at most four times twice the bound 15 s K' times the
+    hidden bound (K' = K rounded up to 64) or the bias.
 """
 import torch
 
@@ -122,12 +125,13 @@ def layer(X, weights, experts, Wg, Wu, Wd, bg, bu, bd, dtype):
     # |d silu| <= 1.1; the product, exp and division in fp32 cost a few roundings.
     eh = 1.1 * eg * (u.abs() + eu) + (silu.abs() + 1.1 * eg) * eu
     eh = eh + (U_H[dtype] + 2.0 ** -20) * (h.abs() + eh)
-    # Bounds of the hidden rows: largest weight times the row's 1-norm, plus the bias.
+    # Bounds of the hidden rows: 15 times the largest scale times the row's 1-norm, plus the
+    # bias, for gate and for up; each is rounded up to a power of two (a factor of 2).
     cap = torch.zeros(M, k, dtype=torch.float64, device=X.device)
     for e in range(Wg.W.shape[0]):
         m, j = torch.nonzero(experts == e, as_tuple=True)
-        one = lambda W, b: (32 * W.W[e].abs().max() * x[m, j].abs().sum(1)  # noqa: E731
-                            + (0 if b is None else b[e].double().abs().max()))
+        one = lambda W, b: 2 * (16 * W.S[e].abs().max() * x[m, j].abs().sum(1)  # noqa: E731
+                                + (0 if b is None else b[e].double().abs().max()))
         cap[m, j] = one(Wg, bg) * one(Wu, bu)
     y, ey = products(h, Wd, experts, bd, dtype, cap)
     Wabs = Wd.W.abs()
@@ -135,6 +139,10 @@ def layer(X, weights, experts, Wg, Wu, Wd, bg, bu, bd, dtype):
         m, j = torch.nonzero(experts == e, as_tuple=True)
         if len(m):
             ey[m, j] += eh[m, j] @ Wabs[e].T * 1.01
+            if dtype == torch.bfloat16:
+                most = 8 * (16 * Wd.S[e].abs().max() * (Wabs.shape[2] + 63) * cap[m, j]
+                            + (0 if bd is None else bd[e].double().abs().max()))
+                ey[m, j] += 2.0 ** -11 * (y[m, j].abs() + ey[m, j]) + 2.0 ** -40 * most.unsqueeze(1)
     w = weights.to(y.device).unsqueeze(2)
     Y = (w * y).sum(1)
     err = (w * ey).sum(1) + (2.0 ** -20 + k * 2.0 ** -23) * (w * y.abs()).sum(1)
