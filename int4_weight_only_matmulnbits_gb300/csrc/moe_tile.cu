@@ -10,9 +10,9 @@
 //  * A comes from TMEM. A lane's 16 fp16 pairs of a packed 16 x 64 chunk are
 //    exactly the registers of a 16x256b TMEM store, so the unpacking warps
 //    write each dequantised chunk with one store, without shared memory,
-//    swizzles or a proxy fence: 32 TMEM columns per 64-wide k stage, four
-//    stages, beside the accumulator's 128 columns. 256 columns per CTA: two
-//    CTAs share an SM, one's epilogue under the other's main loop.
+//    swizzles or a proxy fence: 64 TMEM columns per stage of two chunks (128
+//    k), two stages, beside the accumulator's 128 columns. 256 columns per
+//    CTA: two CTAs share an SM, one's epilogue under the other's main loop.
 //  * Weights are fp16, w' = (q - z) * s with each row's scales brought to
 //    2^9 .. 2^10 by a power of two that the epilogue undoes. q - z is exact,
 //    and so is a bf16 scale; the product has 12 bits, fp16 keeps 11: one
@@ -25,11 +25,8 @@
 //    likewise; they are added per token by a kernel that follows.
 //  * Warps 0-7 unpack, then do the epilogue; each streams its own tile's
 //    codes and scales through a private ring of asynchronous copies. Warp 8
-//    issues the TMA loads, warp 9 the MMAs.
-// Unpacking costs a chunk (64 k of 16 rows) about 85 instructions, 700 per
-// stage and CTA; a stage of 128 slots keeps the tensor core busy for 256
-// cycles. Below some 90 slots per group the unpacking bounds the kernel, at
-// about the rate memory delivers the weights.
+//    issues the TMA loads, warp 9 the MMAs, warp 10 gathers what the epilogue
+//    needs of a unit's columns.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -48,13 +45,14 @@ __device__ unsigned int g_fault_moe = 0;
 namespace {
 
 constexpr int kDqWarps = 8;
-constexpr int kThreads = 32 * (kDqWarps + 2);
-constexpr int kAStages = 4;   // TMEM A stages (32 columns each)
-constexpr int kBStages = 4;   // activation stages
-constexpr int kRing = 6;      // weight chunks per warp in flight
-constexpr int kBStageBytes = kTileSlots * 128;
+constexpr int kThreads = 32 * (kDqWarps + 3);
+constexpr int kChunks = 2;    // 64-wide k chunks per stage
+constexpr int kAStages = 2;   // TMEM A stages (64 columns each)
+constexpr int kBStages = 2;   // activation stages
+constexpr int kRing = 3;      // weight stages per warp in flight
+constexpr int kBChunkBytes = kTileSlots * 128;
+constexpr int kBStageBytes = kChunks * kBChunkBytes;
 constexpr int kTmemCols = 256;
-constexpr int kBarDq = 1;     // named barrier of the unpacking warps
 
 __host__ __device__ constexpr uint32_t idesc_f16(int n) {  // D fp32, A and B fp16, K-major, M = 128
   return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
@@ -84,32 +82,37 @@ __device__ __forceinline__ void tmem_st_16x64(uint32_t taddr, const uint32_t (&r
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
       "r"(r[15])
       : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
 struct Layout {  // shared memory, from a 1024-byte aligned base
-  int ring_bytes, scale, zp, chunk_bytes;
+  int scale, zp, stage_bytes;  // a warp's weight stage
   int off_ring, off_col, off_bar, total;
 };
-// Per column of a unit, for the epilogue: two buffers by turns.
-struct Column {
-  float unscale;  // undoes the activation row's scale (times the output's scale)
-  float weight;
-  int out;        // slot (product) or place
-  float scale;    // output scale (gate and up, down)
+// What the epilogue needs of a column: a undoes the activation row's scale
+// (down: and applies the output's); b is the slot's weight times the output's
+// scale; out the slot (product).
+struct Columns {
+  float2 ab[kTileSlots];
+  int out[kTileSlots];
 };
+
+// Scale blocks a stage touches (blocks of up to 64 codes lie inside chunks).
+template <int BS>
+constexpr int kStageBlocks = BS <= kChunkK ? kChunks * kChunkK / BS
+                                           : (kChunks * kChunkK - 1) / BS + 2;
 
 template <int BS, bool SF32, bool ZP>
 __host__ __device__ constexpr Layout make_layout() {
   Layout l{};
-  constexpr int kBlk = BS < kChunkK ? kChunkK / BS : 1;
-  l.scale = kChunkBytes;
-  l.zp = l.scale + kBlk * kTileN * (SF32 ? 4 : 2);
-  l.chunk_bytes = l.zp + (ZP ? (kBlk == 1 ? 16 : kBlk * 8) : 0);
-  l.ring_bytes = kRing * l.chunk_bytes;
+  l.scale = kChunks * kChunkBytes;
+  l.zp = l.scale + kStageBlocks<BS> * kTileN * (SF32 ? 4 : 2);
+  l.stage_bytes = l.zp + (ZP ? (kStageBlocks<BS> / 2 + 1) * 16 : 0);
   l.off_ring = kBStages * kBStageBytes;
-  l.off_col = l.off_ring + kDqWarps * l.ring_bytes;
-  l.off_bar = l.off_col + 2 * kTileSlots * static_cast<int>(sizeof(Column));
+  l.off_col = l.off_ring + kDqWarps * kRing * l.stage_bytes;
+  l.off_bar = l.off_col + 2 * static_cast<int>(sizeof(Columns));
   l.total = l.off_bar + 256;
   return l;
 }
@@ -131,9 +134,12 @@ __global__ void __launch_bounds__(kThreads, 2) tile_kernel(const __grid_constant
   uint64_t *aempty = afull + kAStages;
   uint64_t *bfull = aempty + kAStages;
   uint64_t *bempty = bfull + kBStages;
-  uint64_t *dfull = bempty + kBStages;
+  uint64_t *cfull = bempty + kBStages;
+  uint64_t *cempty = cfull + 2;
+  uint64_t *dfull = cempty + 2;
   uint64_t *dempty = dfull + 1;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(dempty + 1);
+  Columns *cols2 = reinterpret_cast<Columns *>(smem + kL.off_col);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -144,6 +150,10 @@ __global__ void __launch_bounds__(kThreads, 2) tile_kernel(const __grid_constant
     for (int i = 0; i < kBStages; ++i) {
       mbar_init(bfull + i, 1);
       mbar_init(bempty + i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(cfull + i, 1);
+      mbar_init(cempty + i, kDqWarps);
     }
     mbar_init(dfull, 1);
     mbar_init(dempty, kDqWarps);
@@ -159,12 +169,13 @@ __global__ void __launch_bounds__(kThreads, 2) tile_kernel(const __grid_constant
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem_a = *tmem_slot, tmem_d = tmem_a + kAStages * 32;
+  const uint32_t tmem_a = *tmem_slot, tmem_d = tmem_a + kAStages * kChunks * 32;
 
   grid_dependency_wait();
   grid_dependents_launch();
   const int units = *p.n_groups * p.ntile;
   const bool gate_up = p.mode == kStreamGateUp;
+  const int stages = (p.K64 + kChunks - 1) / kChunks;  // per unit
 
   if (warp == kDqWarps) {
     if (lane == 0) {  // ---- TMA: activation rows ----------------------------------
@@ -173,17 +184,18 @@ __global__ void __launch_bounds__(kThreads, 2) tile_kernel(const __grid_constant
       for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
         const SlotGroup sg = p.groups[u / p.ntile];
         const int boxes = (sg.cols + kTileBox - 1) / kTileBox;
-        for (int kb = 0; kb < p.K64; ++kb, ++it) {
-          const int s = it % kBStages;
+        for (int kb = 0; kb < p.K64; kb += kChunks, ++it) {
+          const int s = it % kBStages, nc = min(kChunks, p.K64 - kb);
           if (it >= kBStages && !mbar_wait(bempty + s, (it / kBStages - 1) & 1)) {
             record_fault(&g_fault_moe, kFaultMoeWait);
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(bfull + s, boxes * kTileBox * 128);
-          for (int b = 0; b < boxes; ++b)
-            tma_load_2d(smem + s * kBStageBytes + b * kTileBox * 128, &p.tmb, kb * kChunkK,
-                        sg.first + b * kTileBox, bfull + s);
+          mbar_arrive_expect_tx(bfull + s, nc * boxes * kTileBox * 128);
+          for (int c = 0; c < nc; ++c)
+            for (int b = 0; b < boxes; ++b)
+              tma_load_2d(smem + s * kBStageBytes + c * kBChunkBytes + b * kTileBox * 128, &p.tmb,
+                          (kb + c) * kChunkK, sg.first + b * kTileBox, bfull + s);
         }
       }
     }
@@ -195,8 +207,8 @@ __global__ void __launch_bounds__(kThreads, 2) tile_kernel(const __grid_constant
         const uint32_t idesc = idesc_f16((p.groups[u / p.ntile].cols + 15) & ~15);
         if (n > 0 && !mbar_wait(dempty, (n - 1) & 1)) ok = false;
         tc_fence_after();
-        for (int kb = 0; kb < p.K64 && ok; ++kb, ++it) {
-          const int a = it % kAStages, b = it % kBStages;
+        for (int kb = 0; kb < p.K64 && ok; kb += kChunks, ++it) {
+          const int a = it % kAStages, b = it % kBStages, nc = min(kChunks, p.K64 - kb);
           if (!mbar_wait(bfull + b, (it / kBStages) & 1) ||
               !mbar_wait(afull + a, (it / kAStages) & 1)) {
             ok = false;
@@ -204,10 +216,12 @@ __global__ void __launch_bounds__(kThreads, 2) tile_kernel(const __grid_constant
           }
           tc_fence_after();
           const uint32_t b_base = smem_addr(smem + b * kBStageBytes);
+          for (int c = 0; c < nc; ++c)
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma_ts(tmem_d, tmem_a + a * 32 + kk * 8, smem_desc_sw128(b_base + kk * 32), idesc,
-                    kb > 0 || kk > 0);
+            for (int kk = 0; kk < 4; ++kk)
+              umma_ts(tmem_d, tmem_a + (a * kChunks + c) * 32 + kk * 8,
+                      smem_desc_sw128(b_base + c * kBChunkBytes + kk * 32), idesc,
+                      kb + c > 0 || kk > 0);
           umma_commit(aempty + a);
           umma_commit(bempty + b);
         }
@@ -215,74 +229,20 @@ __global__ void __launch_bounds__(kThreads, 2) tile_kernel(const __grid_constant
         else record_fault(&g_fault_moe, kFaultMoeWait);
       }
     }
-  } else {
-    // ---- unpacking and epilogue ---------------------------------------------------
-    const int g = lane >> 2;
-    const int quarter = warp & 3, half = warp >> 2;  // TMEM lanes 32 quarter + 16 half ..
-    unsigned char *ring = smem + kL.off_ring + warp * kL.ring_bytes;
-    const uint32_t ring_u = smem_addr(ring);
-    Column *cols2 = reinterpret_cast<Column *>(smem + kL.off_col);
-    const int mat = gate_up ? half : 0;
-    // The tile of a unit this warp unpacks (past the last: the last again,
-    // its rows are never stored).
-    auto tile_of = [&](int u) {
-      const SlotGroup *sg = p.groups + u / p.ntile;
-      const int nt = u % p.ntile;
-      const int i = gate_up ? 4 * nt + quarter : 8 * nt + 2 * quarter + half;
-      return int64_t(sg->e) * p.N16 + min(i, p.N16 - 1);
-    };
-    // Fetch cursor.
-    int fu = blockIdx.x, fc = 0, fslot = 0;
-    const uint4 *fw = nullptr;
-    const unsigned char *fs = nullptr, *fz = nullptr;
-    auto aim = [&] {
-      const int64_t tile = tile_of(fu);
-      fw = p.w[mat].b + tile * p.K64 * 32 + lane;
-      fs = p.w[mat].s + tile * p.nb * (kTileN * kEs) + lane * 16;
-      if (ZP) fz = p.w[mat].z + tile * p.nbz * 8 + lane * 16;
-    };
-    if (fu < units) aim();
-    auto fetch = [&] {
-      if (fu < units) {
-        const uint32_t dst = ring_u + fslot * kL.chunk_bytes + lane * 16;
-        cp16(dst, fw + fc * 32);
-        const int b0 = BS > kChunkK ? (fc * kChunkK) / BS : fc * kBlk;
-        const int n = min(kBlk, p.nb - b0);  // the rest of the chunk has k >= K
-        if (lane < n * kEs) cp16(dst + kL.scale, fs + b0 * (kTileN * kEs));
-        else if (lane < kBlk * kEs)
-          *reinterpret_cast<uint4 *>(ring + fslot * kL.chunk_bytes + kL.scale + lane * 16) =
-              make_uint4(0, 0, 0, 0);
-        if (ZP && lane < (kBlk + 1) / 2 && 2 * lane < p.nbz - (b0 & ~1))
-          cp16(dst + kL.zp, fz + (b0 / 2) * 16);
-        fslot = fslot == kRing - 1 ? 0 : fslot + 1;
-        if (++fc == p.K64) {
-          fc = 0;
-          fu += gridDim.x;
-          if (fu < units) aim();
-        }
+  } else if (warp == kDqWarps + 2) {
+    // ---- columns ------------------------------------------------------------------
+    int n = 0;
+    for (int u = blockIdx.x; u < units; u += gridDim.x, ++n) {
+      if (n >= 2 && !mbar_wait(cempty + (n & 1), (n / 2 - 1) & 1)) {
+        if (lane == 0) record_fault(&g_fault_moe, kFaultMoeWait);
+        break;
       }
-      cp_commit();
-    };
-    for (int i = 0; i < kRing - 1; ++i) fetch();
-
-    int it = 0, slot = 0, n = 0;
-    bool ok = true;
-    for (int u = blockIdx.x; u < units && ok; u += gridDim.x, ++n) {
       const SlotGroup sg = p.groups[u / p.ntile];
-      const int nt = u % p.ntile;
-      const int64_t tile = tile_of(u);
-      const float f0 = p.ts[mat].fac[tile * kTileN + g];
-      const float f1 = p.ts[mat].fac[tile * kTileN + g + 8] * 0.0625f;  // high nibbles: 16 q
-      // Column data of the unit.
-      Column *col = cols2 + (n & 1) * kTileSlots;
-      if (tid < sg.cols) {
-        const int place = sg.first + tid, id = p.order[place];
-        Column c;
-        c.unscale = p.unscale[place];
-        c.weight = gate_up || p.mode == kStreamDown ? p.weights[id] : 1.f;
-        c.out = p.mode == kStreamProduct ? id : place;
-        c.scale = 1.f;
-        auto bits = [&](const uint32_t *v) { return __uint_as_float(v[sg.e]); };
+      Columns &cl = cols2[n & 1];
+      auto bits = [&](const uint32_t *v) { return __uint_as_float(v[sg.e]); };
+      for (int c = lane; c < sg.cols; c += 32) {
+        const int place = sg.first + c, id = p.order[place];
+        float a = p.unscale[place], b = 1.f;
         if (gate_up) {
           // |h| <= (15 s |x|_1 + |b|) for gate times the same for up.
           const float x1 = p.norm1[place];
@@ -291,8 +251,8 @@ __global__ void __launch_bounds__(kThreads, 2) tile_kernel(const __grid_constant
           for (int m = 0; m < 2; ++m)
             e += expo(15.f * bits(p.ts[m].smax) * x1 + bits(p.ts[m].bmax));
           const int shift = max(-126, min(126, 15 - e));
-          c.scale = exp2i(shift);
-          if (nt == 0) {
+          b = p.weights[id] * exp2i(shift);
+          if (u % p.ntile == 0) {
             p.out_unscale[place] = exp2i(-shift);
             p.out_shift[place] = shift;
           }
@@ -302,76 +262,166 @@ __global__ void __launch_bounds__(kThreads, 2) tile_kernel(const __grid_constant
                                 15 - p.shift[place],
                             expo(bits(p.ts[0].bmax))) + 1;
           const int shift = max(-126, min(126, 15 - e));
-          c.scale = exp2i(shift);
-          if (nt == 0) p.out_unscale[place] = exp2i(-shift);
+          a *= exp2i(shift);
+          b = p.weights[id] * exp2i(shift);
+          if (u % p.ntile == 0) p.out_unscale[place] = exp2i(-shift);
         }
-        col[tid] = c;
+        cl.ab[c] = make_float2(a, b);
+        cl.out[c] = id;
       }
-      for (int kb = 0; kb < p.K64; ++kb, ++it) {
-        const int a = it % kAStages;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(cfull + (n & 1));
+    }
+  } else {
+    // ---- unpacking and epilogue ---------------------------------------------------
+    const int g = lane >> 2;
+    const int quarter = warp & 3, half = warp >> 2;  // TMEM lanes 32 quarter + 16 half ..
+    unsigned char *ring = smem + kL.off_ring + warp * (kRing * kL.stage_bytes);
+    const uint32_t ring_u = smem_addr(ring);
+    const int mat = gate_up ? half : 0;
+    // The tile of a unit this warp unpacks (past the last: the last again,
+    // its rows are never stored).
+    auto tile_of = [&](int e, int nt) {
+      const int i = gate_up ? 4 * nt + quarter : 8 * nt + 2 * quarter + half;
+      return int64_t(e) * p.N16 + min(i, p.N16 - 1);
+    };
+    // Fetch cursor; the expert of the unit after its own is loaded a unit
+    // ahead, the row factors of the unit it is in as it enters.
+    int fu = blockIdx.x, fc = 0, fslot = 0, ne = 0;
+    float nf0 = 0.f, nf1 = 0.f;
+    const uint4 *fw = nullptr;
+    const unsigned char *fs = nullptr, *fz = nullptr;
+    auto aim = [&] {
+      const int64_t tile = tile_of(ne, fu % p.ntile);
+      fw = p.w[mat].b + tile * p.K64 * 32 + lane;
+      fs = p.w[mat].s + tile * p.nb * (kTileN * kEs) + lane * 16;
+      if (ZP) fz = p.w[mat].z + tile * p.nbz * 8 + lane * 16;
+      nf0 = p.ts[mat].fac[tile * kTileN + g];
+      nf1 = p.ts[mat].fac[tile * kTileN + g + 8] * 0.0625f;  // high nibbles: 16 q
+      const int next = fu + gridDim.x;
+      if (next < units) ne = p.groups[next / p.ntile].e;
+    };
+    auto block_lo = [&](int c) { return BS > kChunkK ? (c * kChunkK) / BS : c * kBlk; };
+    auto block_hi = [&](int c) { return BS > kChunkK ? (c * kChunkK - 1) / BS + 1 : c * kBlk; };
+    auto fetch = [&] {
+      if (fu < units) {
+        const uint32_t dst = ring_u + fslot * kL.stage_bytes + lane * 16;
+        const int nc = min(kChunks, p.K64 - fc);
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
+          if (c < nc) cp16(dst + c * kChunkBytes, fw + (fc + c) * 32);
+        const int b0 = block_lo(fc), need = block_hi(fc + nc), b1 = min(p.nb, need);
+        if (lane < (b1 - b0) * kEs) cp16(dst + kL.scale, fs + b0 * (kTileN * kEs));
+        else if (lane < (need - b0) * kEs)  // blocks past the last: k >= K, finite scales
+          *reinterpret_cast<uint4 *>(ring + fslot * kL.stage_bytes + kL.scale + lane * 16) =
+              make_uint4(0, 0, 0, 0);
+        if (ZP && lane < (b1 + 1) / 2 - b0 / 2) cp16(dst + kL.zp, fz + (b0 / 2) * 16);
+        fslot = fslot == kRing - 1 ? 0 : fslot + 1;
+        fc += kChunks;
+        if (fc >= p.K64) {
+          fc = 0;
+          fu += gridDim.x;
+          if (fu < units) aim();
+        }
+      }
+      cp_commit();
+    };
+    if (fu < units) {
+      ne = p.groups[fu / p.ntile].e;
+      aim();
+    }
+    // The factors of the unit being unpacked. The cursor runs kRing - 1 stages
+    // ahead: at the end of a unit it is in the next one, unless units are
+    // shorter than that.
+    float f0 = nf0, f1 = nf1;
+    for (int i = 0; i < kRing - 1; ++i) fetch();
+
+    int it = 0, slot = 0, n = 0;
+    bool ok = true;
+    for (int u = blockIdx.x; u < units && ok; u += gridDim.x, ++n) {
+      const SlotGroup sg = p.groups[u / p.ntile];
+      const int nt = u % p.ntile;
+      if (stages < kRing) {
+        const float *fac = p.ts[mat].fac + tile_of(sg.e, nt) * kTileN + g;
+        f0 = fac[0];
+        f1 = fac[8] * 0.0625f;
+      }
+      for (int kb = 0; kb < p.K64; kb += kChunks, ++it) {
+        const int a = it % kAStages, nc = min(kChunks, p.K64 - kb);
         cp_wait<kRing - 2>();
-        __syncwarp();  // the chunk is there, and every lane is done with the one before
+        __syncwarp();  // the stage is there, and every lane is done with the one before
         fetch();
-        const unsigned char *st = ring + slot * kL.chunk_bytes;
+        const unsigned char *st = ring + slot * kL.stage_bytes;
         slot = slot == kRing - 1 ? 0 : slot + 1;
-        const uint4 w4 = *reinterpret_cast<const uint4 *>(st + lane * 16);
-        const uint32_t wv[4] = {w4.x, w4.y, w4.z, w4.w};
-        uint32_t r[16];
+        const int b0 = block_lo(kb);
 #pragma unroll
-        for (int bb = 0; bb < kBlk; ++bb) {
-          float s0, s1;
-          if (SF32) {
-            const float *sc = reinterpret_cast<const float *>(st + kL.scale) + bb * kTileN + g;
-            s0 = sc[0];
-            s1 = sc[8];
-          } else {
-            const uint16_t *sc =
-                reinterpret_cast<const uint16_t *>(st + kL.scale) + bb * kTileN + g;
-            s0 = bf16_bits_to_f32(sc[0]);
-            s1 = bf16_bits_to_f32(sc[8]);
-          }
-          s0 *= f0;
-          s1 *= f1;
-          uint32_t z0 = 0x64086408u, z1 = 0x64806480u;  // 1024 + 8, 1024 + 16 * 8
-          if (ZP) {
-            const int b0 = BS > kChunkK ? (kb * kChunkK) / BS : kb * kBlk;
-            const uint2 zw =
-                *reinterpret_cast<const uint2 *>(st + kL.zp + (bb + (b0 & 1)) * 8);
-            z0 = 0x64006400u | (((zw.x >> (4 * g)) & 15u) * 0x10001u);
-            z1 = 0x64006400u | (((zw.y >> (4 * g)) & 15u) * 0x100010u);
-          }
-          const uint32_t h0 = pack_f16x2(s0, s0), h1 = pack_f16x2(s1, s1);
-          auto scaled = [&](uint32_t c, uint32_t z, uint32_t h, float s) {
-            const uint32_t d = f16x2_sub(c, z);  // q - z, or 16 (q - z): exact
-            if (!SF32) return f16x2_mul(d, h);
-            const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&d));
-            return pack_f16x2(v.x * s, v.y * s);
-          };
+        for (int cc = 0; cc < kChunks; ++cc) {
+          if (cc >= nc) break;
+          const uint4 w4 = *reinterpret_cast<const uint4 *>(st + cc * kChunkBytes + lane * 16);
+          const uint32_t wv[4] = {w4.x, w4.y, w4.z, w4.w};
+          uint32_t r[16];
 #pragma unroll
-          for (int jj = 0; jj < kSpb; ++jj) {
-            const int j = bb * kSpb + jj;
-            uint32_t c[4];
-            codes_to_f16x2(wv[j], c);
-            r[4 * j] = scaled(c[0], z0, h0, s0);
-            r[4 * j + 1] = scaled(c[2], z0, h0, s0);
-            r[4 * j + 2] = scaled(c[1], z1, h1, s1);
-            r[4 * j + 3] = scaled(c[3], z1, h1, s1);
+          for (int bb = 0; bb < kBlk; ++bb) {
+            // The block's place in the stage.
+            const int bi = BS > kChunkK ? block_lo(kb + cc) - b0 : cc * kBlk + bb;
+            float s0, s1;
+            if (SF32) {
+              const float *sc = reinterpret_cast<const float *>(st + kL.scale) + bi * kTileN + g;
+              s0 = sc[0];
+              s1 = sc[8];
+            } else {
+              const uint16_t *sc =
+                  reinterpret_cast<const uint16_t *>(st + kL.scale) + bi * kTileN + g;
+              s0 = bf16_bits_to_f32(sc[0]);
+              s1 = bf16_bits_to_f32(sc[8]);
+            }
+            s0 *= f0;
+            s1 *= f1;
+            uint32_t z0 = 0x64086408u, z1 = 0x64806480u;  // 1024 + 8, 1024 + 16 * 8
+            if (ZP) {
+              const uint2 zw = *reinterpret_cast<const uint2 *>(st + kL.zp + (bi + (b0 & 1)) * 8);
+              z0 = 0x64006400u | (((zw.x >> (4 * g)) & 15u) * 0x10001u);
+              z1 = 0x64006400u | (((zw.y >> (4 * g)) & 15u) * 0x100010u);
+            }
+            const uint32_t h0 = pack_f16x2(s0, s0), h1 = pack_f16x2(s1, s1);
+            auto scaled = [&](uint32_t c, uint32_t z, uint32_t h, float s) {
+              const uint32_t d = f16x2_sub(c, z);  // q - z, or 16 (q - z): exact
+              if (!SF32) return f16x2_mul(d, h);
+              const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&d));
+              return pack_f16x2(v.x * s, v.y * s);
+            };
+#pragma unroll
+            for (int jj = 0; jj < kSpb; ++jj) {
+              const int j = bb * kSpb + jj;
+              uint32_t c[4];
+              codes_to_f16x2(wv[j], c);
+              r[4 * j] = scaled(c[0], z0, h0, s0);
+              r[4 * j + 1] = scaled(c[2], z0, h0, s0);
+              r[4 * j + 2] = scaled(c[1], z1, h1, s1);
+              r[4 * j + 3] = scaled(c[3], z1, h1, s1);
+            }
           }
+          if (cc == 0) {
+            if (it >= kAStages && !mbar_wait(aempty + a, (it / kAStages - 1) & 1)) {
+              record_fault(&g_fault_moe, kFaultMoeWait);
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+          }
+          tmem_st_16x64(tmem_a + (a * kChunks + cc) * 32 +
+                            (static_cast<uint32_t>(32 * quarter + 16 * half) << 16),
+                        r);
         }
-        if (it >= kAStages && !mbar_wait(aempty + a, (it / kAStages - 1) & 1)) {
-          record_fault(&g_fault_moe, kFaultMoeWait);
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        tmem_st_16x64(tmem_a + a * 32 + (static_cast<uint32_t>(32 * quarter + 16 * half) << 16), r);
+        if (!ok) break;
+        tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(afull + a);
       }
-      // Every unpacking warp meets here, whether or not its waits held.
-      named_barrier_sync(kBarDq, 32 * kDqWarps);  // the columns' data
-      if (ok && !mbar_wait(dfull, n & 1)) {
+      f0 = nf0;
+      f1 = nf1;
+      if (ok && (!mbar_wait(cfull + (n & 1), (n / 2) & 1) || !mbar_wait(dfull, n & 1))) {
         record_fault(&g_fault_moe, kFaultMoeWait);
         ok = false;
       }
@@ -380,10 +430,11 @@ __global__ void __launch_bounds__(kThreads, 2) tile_kernel(const __grid_constant
       // ---- epilogue: this warp's TMEM lanes, columns 64 half .. -----------------
       // TMEM lane of a thread: gate rows 0-15 and up rows 16-31 of a quarter,
       // or row 32 quarter + lane of the tile.
+      const Columns &cl = cols2[n & 1];
       const int row = gate_up ? 64 * nt + 16 * quarter + (lane & 15)
                               : 128 * nt + 32 * quarter + lane;
-      const bool live = row < p.N;
-      const int m = gate_up ? lane >> 4 : 0;
+      const bool live = row < p.N, up = gate_up && lane >= 16;
+      const int m = up ? 1 : 0;
       const int64_t srow = int64_t(sg.e) * p.N16 * kTileN + (live ? row : 0);
       // The inverse of a power of two.
       const float rinv = __uint_as_float((254u << 23) - __float_as_uint(p.ts[m].fac[srow]));
@@ -396,40 +447,46 @@ __global__ void __launch_bounds__(kThreads, 2) tile_kernel(const __grid_constant
         if (gate_up) {
           // Lanes below 16 take columns 0-15, the others 16-31: each sends
           // what the other half-warp lacks.
-          const bool up = lane >= 16;
+          const int mine0 = c0 + (up ? 16 : 0);
+          uint16_t *dst = p.hidden + int64_t(sg.first + mine0) * p.ldh + row;
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const Column &mine = col[min(c0 + i, sg.cols - 1)];
-            const Column &theirs = col[min(c0 + 16 + i, sg.cols - 1)];
-            const float lo = v[i] * rinv * mine.unscale + bias;
-            const float hi = v[16 + i] * rinv * theirs.unscale + bias;
-            const float got = __shfl_xor_sync(0xffffffffu, up ? lo : hi, 16);
-            const float gv = up ? got : lo, uv = up ? hi : got;
-            const Column &c = up ? theirs : mine;
-            const int cc = c0 + i + (up ? 16 : 0);
-            const float h = gv / (1.f + __expf(-gv)) * uv * c.weight * c.scale;
-            if (live && cc < sg.cols)
-              p.hidden[c.out * p.ldh + row] = __half_as_ushort(__float2half_rn(h));
+            const float keep = up ? v[16 + i] : v[i], send = up ? v[i] : v[16 + i];
+            const float2 ck = cl.ab[mine0 + i];
+            const float as = cl.ab[c0 + i + (up ? 0 : 16)].x;
+            const float k = fmaf(keep * rinv, ck.x, bias);
+            const float got = __shfl_xor_sync(0xffffffffu, fmaf(send * rinv, as, bias), 16);
+            const float gv = up ? got : k, uv = up ? k : got;
+            const float h = __fdividef(gv * uv, 1.f + __expf(-gv)) * ck.y;
+            // exp overflows for gv < -88: the quotient is then -0 or, where
+            // __fdividef's divisor passes 2^126, 0 as well.
+            if (live && mine0 + i < sg.cols)
+              dst[i * p.ldh] = __half_as_ushort(__float2half_rn(h));
           }
-        } else {
+        } else if (p.mode == kStreamProduct) {
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            if (c0 + i >= sg.cols) break;
-            const Column &c = col[c0 + i];
-            const int64_t o = int64_t(c.out) * p.N + row;
-            const float y = v[i] * rinv * c.unscale;
-            if (!live) continue;
-            if (p.mode == kStreamProduct)
-              p.Y[o] = static_cast<uint16_t>(bf16_bits(y + bias));
-            else
-              p.part[o] =
-                  __half_as_ushort(__float2half_rn((bias != 0.f ? fmaf(c.weight, bias, y) : y) * c.scale));
+            const float y = fmaf(v[i] * rinv, cl.ab[c0 + i].x, bias);
+            if (live && c0 + i < sg.cols)
+              p.Y[int64_t(cl.out[c0 + i]) * p.N + row] = static_cast<uint16_t>(bf16_bits(y));
+          }
+        } else {
+          uint16_t *dst = p.part + int64_t(sg.first + c0) * p.N + row;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float2 c = cl.ab[c0 + i];
+            const float y = fmaf(v[i] * rinv, c.x, bias * c.y);
+            if (live && c0 + i < sg.cols)
+              dst[int64_t(i) * p.N] = __half_as_ushort(__float2half_rn(y));
           }
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(dempty);
+      if (lane == 0) {
+        mbar_arrive(dempty);
+        mbar_arrive(cempty + (n & 1));
+      }
     }
     cp_wait<0>();
   }
