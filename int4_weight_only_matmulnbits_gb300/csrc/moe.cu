@@ -338,6 +338,13 @@ __global__ void __launch_bounds__(kThreads)
   for (int i = threadIdx.x; i <= E; i += kThreads) counts[int64_t(blockIdx.x) * (E + 1) + i] = cnt[i];
 }
 
+// Slots per group of an expert's c slots: as even as whole columns of 16 let
+// them be, at most gt (a multiple of 16).
+__device__ __forceinline__ int group_size(int c, int gt) {
+  const int n = (c + gt - 1) / gt;
+  return n ? (c + 16 * n - 1) / (16 * n) * 16 : gt;
+}
+
 // Second launch: places. Each block adds up the counts of the blocks before
 // it and of all, scans the experts, and places its slots in order; block 0
 // writes the offsets and the groups. place[p]: where slot p stands in the
@@ -345,7 +352,7 @@ __global__ void __launch_bounds__(kThreads)
 __global__ void __launch_bounds__(kThreads)
     place_kernel(const int32_t *experts, int64_t P, int E, const int32_t *counts, int32_t *offsets,
                  int32_t *order, int32_t *place, SlotGroup *groups, int32_t *n_groups,
-                 int gt_log2) {
+                 int gt) {
   extern __shared__ int32_t mem[];
   int32_t *start = mem, *gstart = mem + E + 1;        // [E + 1] each
   int32_t *cnt = mem + 2 * (E + 1);                   // [kWarps][E + 1]
@@ -376,7 +383,8 @@ __global__ void __launch_bounds__(kThreads)
       if (b < blockIdx.x) before += c;
     }
     start[e] = all;
-    gstart[e] = e < E ? (all + (1 << gt_log2) - 1) >> gt_log2 : 0;
+    const int size = group_size(all, gt);
+    gstart[e] = e < E ? (all + size - 1) / size : 0;
     for (int w = 0; w < kWarps; ++w) {  // where each warp's first slot goes, less start
       const int c = cnt[w * (E + 1) + e];
       cnt[w * (E + 1) + e] = before;
@@ -404,9 +412,11 @@ __global__ void __launch_bounds__(kThreads)
     for (int e = threadIdx.x; e <= E; e += kThreads) {
       offsets[e] = start[e];
       if (groups && e < E) {
-        const int first = start[e], c = start[e + 1] - first, gt = 1 << gt_log2;
+        const int first = start[e], c = start[e + 1] - first, n = gstart[e + 1] - gstart[e];
         SlotGroup *g = groups + gstart[e];
-        for (int k = 0; k < c; k += gt) *g++ = SlotGroup{e, first + k, min(gt, c - k)};
+        const int size = group_size(c, gt);
+        for (int k = 0; k < n; ++k)
+          g[k] = SlotGroup{e, first + k * size, min(size, c - k * size)};
       }
     }
     if (groups && threadIdx.x == 0) *n_groups = gstart[E];
@@ -919,7 +929,7 @@ TileSpace tile_space(unsigned char *ws, int64_t P, const ExpertStack *const *w, 
   s.l.offsets = c.take<int32_t>(E + 1);
   s.l.order = c.take<int32_t>(P);
   s.l.n_groups = c.take<int32_t>(1);
-  s.l.groups = c.take<SlotGroup>(max_groups(P, E, kTileSlotsLog2));
+  s.l.groups = c.take<SlotGroup>(P / kTileSlots + E);
   s.counts = c.take<int32_t>(ceil_div(P, kSortSlots) * (E + 1));
   s.place = c.take<int32_t>(P);
   s.clear = c.take<uint32_t>(size_t(stacks) * 2 * E);
@@ -950,7 +960,7 @@ cudaError_t launch_tile_lists(const TileSpace &s, const int32_t *experts, int64_
   if (e != cudaSuccess) return e;
   e = launch_pdl(place_kernel, blocks, kThreads, size_t(2 + kWarps) * (E + 1) * 4, pdl, stream,
                  experts, P, E, s.counts, s.l.offsets, s.l.order, s.place, s.l.groups,
-                 s.l.n_groups, kTileSlotsLog2);
+                 s.l.n_groups, kTileSlots);
   if (e != cudaSuccess) return e;
   ScaleArgs a{};
   a.count = stacks;

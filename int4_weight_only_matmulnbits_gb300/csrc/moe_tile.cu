@@ -1,6 +1,6 @@
 // Tensor-core (tcgen05 / TMEM) kernel of the expert layer, for many slots.
 //
-// One unit of work is a group of up to 128 slots that share an expert times
+// One unit of work is a group of up to 192 slots that share an expert times
 // a column tile of the expert's weight: 128 weight rows (64 of gate and the
 // same 64 of up, or 128 of one matrix). The weight rows are the MMA's A
 // operand (M = 128), the slots its columns (N = slots rounded up to 16), so
@@ -11,8 +11,8 @@
 //    exactly the registers of a 16x256b TMEM store, so the unpacking warps
 //    write each dequantised chunk with one store, without shared memory,
 //    swizzles or a proxy fence: 64 TMEM columns per stage of two chunks (128
-//    k), two stages, beside the accumulator's 128 columns. 256 columns per
-//    CTA: two CTAs share an SM, one's epilogue under the other's main loop.
+//    k), two stages. The other 384 columns are two accumulators: a unit is
+//    stored while the next one is computed. One CTA per SM.
 //  * Weights are fp16, w' = (q - z) * s with each row's scales brought to
 //    2^9 .. 2^10 by a power of two that the epilogue undoes. q - z is exact,
 //    and so is a bf16 scale; the product has 12 bits, fp16 keeps 11: one
@@ -23,10 +23,10 @@
 //    times the 1-norm of x, for gate and for up) fits: typical values then
 //    lie 15 or so octaves above fp16's smallest normal. Down partials
 //    likewise; they are added per token by a kernel that follows.
-//  * Warps 0-7 unpack, then do the epilogue; each streams its own tile's
-//    codes and scales through a private ring of asynchronous copies. Warp 8
-//    issues the TMA loads, warp 9 the MMAs, warp 10 gathers what the epilogue
-//    needs of a unit's columns.
+//  * Warps 0-7 unpack, each its own tile's codes and scales from a private
+//    ring of asynchronous copies; warps 8-15 store; one warp each issues the
+//    TMA loads, issues the MMAs, and gathers what a unit's columns need for
+//    the epilogue.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -44,15 +44,18 @@ __device__ unsigned int g_fault_moe = 0;
 
 namespace {
 
-constexpr int kDqWarps = 8;
-constexpr int kThreads = 32 * (kDqWarps + 3);
+constexpr int kDqWarps = 8;   // warps 0-7 unpack
+constexpr int kEpWarps = 8;   // warps 8-15 store
+constexpr int kTmaWarp = kDqWarps + kEpWarps, kMmaWarp = kTmaWarp + 1, kColWarp = kTmaWarp + 2;
+constexpr int kThreads = 32 * (kTmaWarp + 3);
 constexpr int kChunks = 2;    // 64-wide k chunks per stage
 constexpr int kAStages = 2;   // TMEM A stages (64 columns each)
-constexpr int kBStages = 2;   // activation stages
-constexpr int kRing = 3;      // weight stages per warp in flight
+constexpr int kBStages = 3;   // activation stages
+constexpr int kRing = 5;      // weight stages per warp in flight
 constexpr int kBChunkBytes = kTileSlots * 128;
 constexpr int kBStageBytes = kChunks * kBChunkBytes;
-constexpr int kTmemCols = 256;
+constexpr int kTmemCols = 512;  // A, and two accumulators of kTileSlots columns
+static_assert(kAStages * kChunks * 32 + 2 * kTileSlots == kTmemCols, "all of TMEM");
 
 __host__ __device__ constexpr uint32_t idesc_f16(int n) {  // D fp32, A and B fp16, K-major, M = 128
   return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
@@ -123,7 +126,7 @@ __device__ __forceinline__ int expo(float x) {
 }
 
 template <int BS, bool ZP, bool SF32>
-__global__ void __launch_bounds__(kThreads, 2) tile_kernel(const __grid_constant__ TileParams p) {
+__global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant__ TileParams p) {
   constexpr Layout kL = make_layout<BS, SF32, ZP>();
   constexpr int kEs = SF32 ? 4 : 2;
   constexpr int kBlk = BS < kChunkK ? kChunkK / BS : 1;  // blocks per chunk
@@ -137,8 +140,8 @@ __global__ void __launch_bounds__(kThreads, 2) tile_kernel(const __grid_constant
   uint64_t *cfull = bempty + kBStages;
   uint64_t *cempty = cfull + 2;
   uint64_t *dfull = cempty + 2;
-  uint64_t *dempty = dfull + 1;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(dempty + 1);
+  uint64_t *dempty = dfull + 2;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(dempty + 2);
   Columns *cols2 = reinterpret_cast<Columns *>(smem + kL.off_col);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -153,13 +156,13 @@ __global__ void __launch_bounds__(kThreads, 2) tile_kernel(const __grid_constant
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(cfull + i, 1);
-      mbar_init(cempty + i, kDqWarps);
+      mbar_init(cempty + i, kEpWarps);
+      mbar_init(dfull + i, 1);
+      mbar_init(dempty + i, kEpWarps);
     }
-    mbar_init(dfull, 1);
-    mbar_init(dempty, kDqWarps);
     fence_barrier_init();
   }
-  if (warp == kDqWarps + 1) {
+  if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_addr(tmem_slot)),
                  "r"(kTmemCols)
@@ -177,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, 2) tile_kernel(const __grid_constant
   const bool gate_up = p.mode == kStreamGateUp;
   const int stages = (p.K64 + kChunks - 1) / kChunks;  // per unit
 
-  if (warp == kDqWarps) {
+  if (warp == kTmaWarp) {
     if (lane == 0) {  // ---- TMA: activation rows ----------------------------------
       int it = 0;
       bool ok = true;
@@ -199,13 +202,15 @@ __global__ void __launch_bounds__(kThreads, 2) tile_kernel(const __grid_constant
         }
       }
     }
-  } else if (warp == kDqWarps + 1) {
+  } else if (warp == kMmaWarp) {
     if (lane == 0) {  // ---- MMA ------------------------------------------------------
       int it = 0, n = 0;
       bool ok = true;
+      int ncols = blockIdx.x < units ? p.groups[blockIdx.x / p.ntile].cols : 0;
       for (int u = blockIdx.x; u < units && ok; u += gridDim.x, ++n) {
-        const uint32_t idesc = idesc_f16((p.groups[u / p.ntile].cols + 15) & ~15);
-        if (n > 0 && !mbar_wait(dempty, (n - 1) & 1)) ok = false;
+        const uint32_t idesc = idesc_f16((ncols + 15) & ~15), d = tmem_d + (n & 1) * kTileSlots;
+        if (u + gridDim.x < units) ncols = p.groups[(u + gridDim.x) / p.ntile].cols;
+        if (n >= 2 && !mbar_wait(dempty + (n & 1), (n / 2 - 1) & 1)) ok = false;
         tc_fence_after();
         for (int kb = 0; kb < p.K64 && ok; kb += kChunks, ++it) {
           const int a = it % kAStages, b = it % kBStages, nc = min(kChunks, p.K64 - kb);
@@ -219,17 +224,17 @@ __global__ void __launch_bounds__(kThreads, 2) tile_kernel(const __grid_constant
           for (int c = 0; c < nc; ++c)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              umma_ts(tmem_d, tmem_a + (a * kChunks + c) * 32 + kk * 8,
+              umma_ts(d, tmem_a + (a * kChunks + c) * 32 + kk * 8,
                       smem_desc_sw128(b_base + c * kBChunkBytes + kk * 32), idesc,
                       kb + c > 0 || kk > 0);
           umma_commit(aempty + a);
           umma_commit(bempty + b);
         }
-        if (ok) umma_commit(dfull);
+        if (ok) umma_commit(dfull + (n & 1));
         else record_fault(&g_fault_moe, kFaultMoeWait);
       }
     }
-  } else if (warp == kDqWarps + 2) {
+  } else if (warp == kColWarp) {
     // ---- columns ------------------------------------------------------------------
     int n = 0;
     for (int u = blockIdx.x; u < units; u += gridDim.x, ++n) {
@@ -272,8 +277,8 @@ __global__ void __launch_bounds__(kThreads, 2) tile_kernel(const __grid_constant
       __syncwarp();
       if (lane == 0) mbar_arrive(cfull + (n & 1));
     }
-  } else {
-    // ---- unpacking and epilogue ---------------------------------------------------
+  } else if (warp < kDqWarps) {
+    // ---- unpacking ------------------------------------------------------------------
     const int g = lane >> 2;
     const int quarter = warp & 3, half = warp >> 2;  // TMEM lanes 32 quarter + 16 half ..
     unsigned char *ring = smem + kL.off_ring + warp * (kRing * kL.stage_bytes);
@@ -336,13 +341,12 @@ __global__ void __launch_bounds__(kThreads, 2) tile_kernel(const __grid_constant
     float f0 = nf0, f1 = nf1;
     for (int i = 0; i < kRing - 1; ++i) fetch();
 
-    int it = 0, slot = 0, n = 0;
+    int it = 0, slot = 0;
     bool ok = true;
-    for (int u = blockIdx.x; u < units && ok; u += gridDim.x, ++n) {
-      const SlotGroup sg = p.groups[u / p.ntile];
-      const int nt = u % p.ntile;
+    for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
       if (stages < kRing) {
-        const float *fac = p.ts[mat].fac + tile_of(sg.e, nt) * kTileN + g;
+        const float *fac =
+            p.ts[mat].fac + tile_of(p.groups[u / p.ntile].e, u % p.ntile) * kTileN + g;
         f0 = fac[0];
         f1 = fac[8] * 0.0625f;
       }
@@ -421,13 +425,15 @@ __global__ void __launch_bounds__(kThreads, 2) tile_kernel(const __grid_constant
       }
       f0 = nf0;
       f1 = nf1;
-      if (ok && (!mbar_wait(cfull + (n & 1), (n / 2) & 1) || !mbar_wait(dfull, n & 1))) {
-        record_fault(&g_fault_moe, kFaultMoeWait);
-        ok = false;
-      }
-      if (!ok) break;
-      tc_fence_after();
-      // ---- epilogue: this warp's TMEM lanes, columns 64 half .. -----------------
+    }
+    cp_wait<0>();
+  } else {
+    // ---- epilogue: TMEM lanes of a quarter, half of the columns ---------------------
+    const int quarter = warp & 3, half = (warp - kDqWarps) >> 2;
+    int n = 0;
+    for (int u = blockIdx.x; u < units; u += gridDim.x, ++n) {
+      const SlotGroup sg = p.groups[u / p.ntile];
+      const int nt = u % p.ntile;
       // TMEM lane of a thread: gate rows 0-15 and up rows 16-31 of a quarter,
       // or row 32 quarter + lane of the tile.
       const Columns &cl = cols2[n & 1];
@@ -440,10 +446,16 @@ __global__ void __launch_bounds__(kThreads, 2) tile_kernel(const __grid_constant
       const float rinv = __uint_as_float((254u << 23) - __float_as_uint(p.ts[m].fac[srow]));
       const float bias =
           p.w[m].bias && live ? p.w[m].bias[int64_t(sg.e) * p.N + row] : 0.f;
-      const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
-      for (int c0 = 64 * half; c0 < 64 * half + 64 && c0 < sg.cols; c0 += 32) {
+      const uint32_t d = tmem_d + (n & 1) * kTileSlots + (static_cast<uint32_t>(32 * quarter) << 16);
+      if (!mbar_wait(cfull + (n & 1), (n / 2) & 1) || !mbar_wait(dfull + (n & 1), (n / 2) & 1)) {
+        record_fault(&g_fault_moe, kFaultMoeWait);
+        break;
+      }
+      tc_fence_after();
+      const int share = (sg.cols + 63) / 64 * 32;  // columns per half
+      for (int c0 = share * half; c0 < share * (half + 1) && c0 < sg.cols; c0 += 32) {
         float v[32];
-        tmem_ld32(tmem_d + lanes + c0, v);
+        tmem_ld32(d + c0, v);
         if (gate_up) {
           // Lanes below 16 take columns 0-15, the others 16-31: each sends
           // what the other half-warp lacks.
@@ -484,15 +496,14 @@ __global__ void __launch_bounds__(kThreads, 2) tile_kernel(const __grid_constant
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(dempty);
+        mbar_arrive(dempty + (n & 1));
         mbar_arrive(cempty + (n & 1));
       }
     }
-    cp_wait<0>();
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kDqWarps + 1) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_a),
                  "r"(kTmemCols)
@@ -503,13 +514,13 @@ __global__ void __launch_bounds__(kThreads, 2) tile_kernel(const __grid_constant
 template <int BS, bool ZP, bool SF32>
 cudaError_t launch_one(const TileParams &p, bool pdl, cudaStream_t stream) {
   constexpr int kSmem = make_layout<BS, SF32, ZP>().total + 1024;
-  static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs per SM");
+  static_assert(kSmem <= 227 * 1024, "shared memory");
   static std::atomic<unsigned long long> done{0};
   auto *kernel = tile_kernel<BS, ZP, SF32>;
   const cudaError_t e = ensure_smem_limit(kernel, kSmem, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(2 * sm_count());
+  cfg.gridDim = dim3(sm_count());
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = stream;

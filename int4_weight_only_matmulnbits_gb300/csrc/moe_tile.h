@@ -10,8 +10,7 @@
 
 namespace mnb {
 
-constexpr int kTileSlots = 128;  // slots per group (columns of an accumulator)
-constexpr int kTileSlotsLog2 = 7;
+constexpr int kTileSlots = 192;  // slots per group (columns of an accumulator)
 constexpr int kTileBox = 32;     // activation rows per TMA box
 
 // What the weights' scales of a stack are brought to (tile_scales_kernel).
