@@ -1,10 +1,10 @@
 // Tensor-core (tcgen05 / TMEM) kernel of the expert layer, for many slots.
 //
 // One unit of work is a group of up to 192 slots that share an expert times
-// a column tile of the expert's weight: 128 weight rows (64 of gate and the
-// same 64 of up, or 128 of one matrix). The weight rows are the MMA's A
-// operand (M = 128), the slots its columns (N = slots rounded up to 16), so
-// ragged lists cost no tensor work beyond 15 columns:
+// two column tiles of the expert's weight, one for each CTA of a pair: 128
+// weight rows each (64 of gate and the same 64 of up, or 128 of one matrix).
+// The weight rows are the MMA's A operand (cta_group::2, M = 256), the slots
+// its columns (N = slots rounded up to 32), so ragged lists cost little:
 //   D[row, slot] = sum_k w[row, k] x[slot, k]
 //
 //  * A comes from TMEM. A lane's 16 fp16 pairs of a packed 16 x 64 chunk are
@@ -18,7 +18,11 @@
 //    and so is a bf16 scale; the product has 12 bits, fp16 keeps 11: one
 //    rounding of 2^-11 at most, an eighth of a bf16 weight's.
 //  * B are fp16 activation rows, scaled by a power of two per row, in the
-//    order of the lists: TMA tiles of 32 rows x 64 k, 128-byte swizzle.
+//    order of the lists: TMA tiles of 32 rows x 64 k, 128-byte swizzle. Each
+//    CTA loads half of a group's rows: with 128 weight rows a CTA and all of
+//    the slots, activations would take 64 bytes a cycle and SM, more than L2
+//    gives (measured: 593 us instead of 476 for 4096 tokens of 8 out of 128
+//    experts, 2560 -> 768 -> 2560).
 //  * Hidden values leave as fp16, the row scaled so that a bound of it (15 s
 //    times the 1-norm of x, for gate and for up) fits: typical values then
 //    lie 15 or so octaves above fp16's smallest normal. Down partials
@@ -50,29 +54,54 @@ constexpr int kTmaWarp = kDqWarps + kEpWarps, kMmaWarp = kTmaWarp + 1, kColWarp 
 constexpr int kThreads = 32 * (kTmaWarp + 3);
 constexpr int kChunks = 2;    // 64-wide k chunks per stage
 constexpr int kAStages = 2;   // TMEM A stages (64 columns each)
-constexpr int kBStages = 3;   // activation stages
+constexpr int kBStages = 5;   // activation stages
 constexpr int kRing = 5;      // weight stages per warp in flight
-constexpr int kBChunkBytes = kTileSlots * 128;
+constexpr int kBChunkBytes = kTileSlots / 2 * 128;  // a CTA's half of the slots
 constexpr int kBStageBytes = kChunks * kBChunkBytes;
 constexpr int kTmemCols = 512;  // A, and two accumulators of kTileSlots columns
 static_assert(kAStages * kChunks * 32 + 2 * kTileSlots == kTmemCols, "all of TMEM");
 
-__host__ __device__ constexpr uint32_t idesc_f16(int n) {  // D fp32, A and B fp16, K-major, M = 128
-  return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
+// D fp32, A and B fp16, K-major, M = 256 over the pair.
+__host__ __device__ constexpr uint32_t idesc_f16(int n) {
+  return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (16u << 24);
+}
+__device__ __forceinline__ int columns_of(int slots) { return (slots + 31) & ~31; }
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// Address of this CTA's shared variable `p` in CTA `rank` of the pair.
+__device__ __forceinline__ uint32_t cluster_addr(const void *p, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_addr(p)), "r"(rank));
+  return r;
+}
+// Arrival on a barrier of either CTA. What it publishes lies in tensor memory
+// (stores waited for and fenced before it) or in shared memory that TMA
+// wrote: nothing a cluster-scope release of this thread's writes would add.
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 
+// D += A x B^T over the pair: each CTA's 128 rows of A in its tensor memory,
+// each CTA's half of B's rows in its shared memory, at the same offsets.
 __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                        bool accumulate) {
+                                        uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(static_cast<int>(accumulate))
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-__device__ __forceinline__ void umma_commit(uint64_t *bar) {
+// Arrival, once the MMAs issued so far are complete, on the barrier at `bar`'s
+// offset in each CTA of `mask`.
+__device__ __forceinline__ void umma_commit(uint64_t *bar, uint16_t mask) {
   asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-          smem_addr(bar))
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+      "[%0], %1;" ::"r"(smem_addr(bar)),
+      "h"(mask)
       : "memory");
 }
 // 16 lanes x 32 columns: lane (g, t) writes, for j < 4, columns 8j + 2t and
@@ -141,42 +170,48 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
   uint64_t *cempty = cfull + 2;
   uint64_t *dfull = cempty + 2;
   uint64_t *dempty = dfull + 2;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(dempty + 2);
+  uint64_t *done = dempty + 2;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
   Columns *cols2 = reinterpret_cast<Columns *>(smem + kL.off_col);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_rank();
   if (tid == 0) {
     for (int i = 0; i < kAStages; ++i) {
-      mbar_init(afull + i, kDqWarps);
+      mbar_init(afull + i, 2 * kDqWarps);  // both CTAs' warps, at CTA 0
       mbar_init(aempty + i, 1);
     }
     for (int i = 0; i < kBStages; ++i) {
-      mbar_init(bfull + i, 1);
+      mbar_init(bfull + i, rank == 0 ? 2 : 1);  // at CTA 0, CTA 1's half as well
       mbar_init(bempty + i, 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(cfull + i, 1);
       mbar_init(cempty + i, kEpWarps);
       mbar_init(dfull + i, 1);
-      mbar_init(dempty + i, kEpWarps);
+      mbar_init(dempty + i, 2 * kEpWarps);  // both CTAs' warps, at CTA 0
     }
+    mbar_init(done, 1);
     fence_barrier_init();
   }
   if (warp == kMmaWarp) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_addr(tmem_slot)),
                  "r"(kTmemCols)
                  : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync_all();  // both CTAs' barriers exist before any remote arrival
   tc_fence_after();
   const uint32_t tmem_a = *tmem_slot, tmem_d = tmem_a + kAStages * kChunks * 32;
 
   grid_dependency_wait();
   grid_dependents_launch();
-  const int units = *p.n_groups * p.ntile;
+  // A pair of CTAs takes two neighbouring column tiles of a group.
+  const int np = (p.ntile + 1) / 2, units = *p.n_groups * np;
+  const int u0 = blockIdx.x >> 1, du = gridDim.x >> 1;
   const bool gate_up = p.mode == kStreamGateUp;
   const int stages = (p.K64 + kChunks - 1) / kChunks;  // per unit
 
@@ -184,9 +219,10 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     if (lane == 0) {  // ---- TMA: activation rows ----------------------------------
       int it = 0;
       bool ok = true;
-      for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-        const SlotGroup sg = p.groups[u / p.ntile];
-        const int boxes = (sg.cols + kTileBox - 1) / kTileBox;
+      for (int u = u0; u < units && ok; u += du) {
+        const SlotGroup sg = p.groups[u / np];
+        const int half = columns_of(sg.cols) / 2, first = sg.first + static_cast<int>(rank) * half;
+        const int boxes = (half + kTileBox - 1) / kTileBox;
         for (int kb = 0; kb < p.K64; kb += kChunks, ++it) {
           const int s = it % kBStages, nc = min(kChunks, p.K64 - kb);
           if (it >= kBStages && !mbar_wait(bempty + s, (it / kBStages - 1) & 1)) {
@@ -198,51 +234,78 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
           for (int c = 0; c < nc; ++c)
             for (int b = 0; b < boxes; ++b)
               tma_load_2d(smem + s * kBStageBytes + c * kBChunkBytes + b * kTileBox * 128, &p.tmb,
-                          (kb + c) * kChunkK, sg.first + b * kTileBox, bfull + s);
+                          (kb + c) * kChunkK, first + b * kTileBox, bfull + s);
         }
       }
     }
   } else if (warp == kMmaWarp) {
-    if (lane == 0) {  // ---- MMA ------------------------------------------------------
-      int it = 0, n = 0;
-      bool ok = true;
-      int ncols = blockIdx.x < units ? p.groups[blockIdx.x / p.ntile].cols : 0;
-      for (int u = blockIdx.x; u < units && ok; u += gridDim.x, ++n) {
-        const uint32_t idesc = idesc_f16((ncols + 15) & ~15), d = tmem_d + (n & 1) * kTileSlots;
-        if (u + gridDim.x < units) ncols = p.groups[(u + gridDim.x) / p.ntile].cols;
+    bool ok = true;
+    int n = 0;
+    if (lane == 0 && rank == 0) {  // ---- MMAs of the pair -------------------------------
+      int slots = u0 < units ? p.groups[u0 / np].cols : 0, as = 0, bs = 0;
+      uint32_t aphase = 0, bphase = 0;
+      const uint64_t desc0 = smem_desc_sw128(smem_addr(smem));
+      for (int u = u0; u < units && ok; u += du, ++n) {
+        const uint32_t idesc = idesc_f16(columns_of(slots)), d = tmem_d + (n & 1) * kTileSlots;
+        if (u + du < units) slots = p.groups[(u + du) / np].cols;
         if (n >= 2 && !mbar_wait(dempty + (n & 1), (n / 2 - 1) & 1)) ok = false;
         tc_fence_after();
-        for (int kb = 0; kb < p.K64 && ok; kb += kChunks, ++it) {
-          const int a = it % kAStages, b = it % kBStages, nc = min(kChunks, p.K64 - kb);
-          if (!mbar_wait(bfull + b, (it / kBStages) & 1) ||
-              !mbar_wait(afull + a, (it / kAStages) & 1)) {
+        // One thread feeds the pair's tensor cores, in the few issue slots that
+        // 18 other warps leave it: the loop is kept short. A chunk's MMAs step
+        // A by 8 columns and B's descriptor by 32 bytes.
+        for (int kb = 0; kb < p.K64; kb += kChunks) {
+          if (!mbar_wait(bfull + bs, bphase) || !mbar_wait(afull + as, aphase)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t b_base = smem_addr(smem + b * kBStageBytes);
-          for (int c = 0; c < nc; ++c)
+          const uint32_t ta = tmem_a + as * (kChunks * 32);
+          const uint64_t desc = desc0 + bs * (kBStageBytes >> 4);
+          umma_ts(d, ta, desc, idesc, kb);
+#pragma unroll
+          for (int kk = 1; kk < 4; ++kk) umma_ts(d, ta + kk * 8, desc + kk * 2, idesc, 1);
+          if (kb + 1 < p.K64)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              umma_ts(d, tmem_a + (a * kChunks + c) * 32 + kk * 8,
-                      smem_desc_sw128(b_base + c * kBChunkBytes + kk * 32), idesc,
-                      kb + c > 0 || kk > 0);
-          umma_commit(aempty + a);
-          umma_commit(bempty + b);
+              umma_ts(d, ta + 32 + kk * 8, desc + (kBChunkBytes >> 4) + kk * 2, idesc, 1);
+          umma_commit(aempty + as, 3);
+          umma_commit(bempty + bs, 3);
+          if (++as == kAStages) {
+            as = 0;
+            aphase ^= 1;
+          }
+          if (++bs == kBStages) {
+            bs = 0;
+            bphase ^= 1;
+          }
         }
-        if (ok) umma_commit(dfull + (n & 1));
-        else record_fault(&g_fault_moe, kFaultMoeWait);
+        if (ok) umma_commit(dfull + (n & 1), 3);
       }
+      // Every MMA issued is complete before the tensor memory is released.
+      umma_commit(done, 1);
+      if (!mbar_wait(done, 0) || !ok) record_fault(&g_fault_moe, kFaultMoeWait);
+    } else if (lane == 0) {  // ---- CTA 1: tells CTA 0 that its half has landed -----------
+      const uint32_t peer = cluster_addr(bfull, 0);
+      int it = 0;
+      for (int u = u0; u < units && ok; u += du)
+        for (int kb = 0; kb < p.K64; kb += kChunks, ++it) {
+          if (!mbar_wait(bfull + it % kBStages, (it / kBStages) & 1)) {
+            record_fault(&g_fault_moe, kFaultMoeWait);
+            ok = false;
+            break;
+          }
+          mbar_arrive_cluster(peer + 8 * (it % kBStages));
+        }
     }
   } else if (warp == kColWarp) {
     // ---- columns ------------------------------------------------------------------
     int n = 0;
-    for (int u = blockIdx.x; u < units; u += gridDim.x, ++n) {
+    for (int u = u0; u < units; u += du, ++n) {
       if (n >= 2 && !mbar_wait(cempty + (n & 1), (n / 2 - 1) & 1)) {
         if (lane == 0) record_fault(&g_fault_moe, kFaultMoeWait);
         break;
       }
-      const SlotGroup sg = p.groups[u / p.ntile];
+      const SlotGroup sg = p.groups[u / np];
       Columns &cl = cols2[n & 1];
       auto bits = [&](const uint32_t *v) { return __uint_as_float(v[sg.e]); };
       for (int c = lane; c < sg.cols; c += 32) {
@@ -257,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
             e += expo(15.f * bits(p.ts[m].smax) * x1 + bits(p.ts[m].bmax));
           const int shift = max(-126, min(126, 15 - e));
           b = p.weights[id] * exp2i(shift);
-          if (u % p.ntile == 0) {
+          if (u % np == 0 && rank == 0) {
             p.out_unscale[place] = exp2i(-shift);
             p.out_shift[place] = shift;
           }
@@ -269,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
           const int shift = max(-126, min(126, 15 - e));
           a *= exp2i(shift);
           b = p.weights[id] * exp2i(shift);
-          if (u % p.ntile == 0) p.out_unscale[place] = exp2i(-shift);
+          if (u % np == 0 && rank == 0) p.out_unscale[place] = exp2i(-shift);
         }
         cl.ab[c] = make_float2(a, b);
         cl.out[c] = id;
@@ -286,25 +349,25 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     const int mat = gate_up ? half : 0;
     // The tile of a unit this warp unpacks (past the last: the last again,
     // its rows are never stored).
-    auto tile_of = [&](int e, int nt) {
+    auto tile_of = [&](int e, int pair) {
+      const int nt = 2 * pair + static_cast<int>(rank);
       const int i = gate_up ? 4 * nt + quarter : 8 * nt + 2 * quarter + half;
       return int64_t(e) * p.N16 + min(i, p.N16 - 1);
     };
     // Fetch cursor; the expert of the unit after its own is loaded a unit
     // ahead, the row factors of the unit it is in as it enters.
-    int fu = blockIdx.x, fc = 0, fslot = 0, ne = 0;
+    int fu = u0, fc = 0, fslot = 0, ne = 0;
     float nf0 = 0.f, nf1 = 0.f;
     const uint4 *fw = nullptr;
     const unsigned char *fs = nullptr, *fz = nullptr;
     auto aim = [&] {
-      const int64_t tile = tile_of(ne, fu % p.ntile);
+      const int64_t tile = tile_of(ne, fu % np);
       fw = p.w[mat].b + tile * p.K64 * 32 + lane;
       fs = p.w[mat].s + tile * p.nb * (kTileN * kEs) + lane * 16;
       if (ZP) fz = p.w[mat].z + tile * p.nbz * 8 + lane * 16;
       nf0 = p.ts[mat].fac[tile * kTileN + g];
       nf1 = p.ts[mat].fac[tile * kTileN + g + 8] * 0.0625f;  // high nibbles: 16 q
-      const int next = fu + gridDim.x;
-      if (next < units) ne = p.groups[next / p.ntile].e;
+      if (fu + du < units) ne = p.groups[(fu + du) / np].e;
     };
     auto block_lo = [&](int c) { return BS > kChunkK ? (c * kChunkK) / BS : c * kBlk; };
     auto block_hi = [&](int c) { return BS > kChunkK ? (c * kChunkK - 1) / BS + 1 : c * kBlk; };
@@ -325,14 +388,14 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         fc += kChunks;
         if (fc >= p.K64) {
           fc = 0;
-          fu += gridDim.x;
+          fu += du;
           if (fu < units) aim();
         }
       }
       cp_commit();
     };
     if (fu < units) {
-      ne = p.groups[fu / p.ntile].e;
+      ne = p.groups[fu / np].e;
       aim();
     }
     // The factors of the unit being unpacked. The cursor runs kRing - 1 stages
@@ -341,12 +404,13 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     float f0 = nf0, f1 = nf1;
     for (int i = 0; i < kRing - 1; ++i) fetch();
 
+    const uint32_t afull0 = cluster_addr(afull, 0);
     int it = 0, slot = 0;
     bool ok = true;
-    for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+    for (int u = u0; u < units && ok; u += du) {
       if (stages < kRing) {
         const float *fac =
-            p.ts[mat].fac + tile_of(p.groups[u / p.ntile].e, u % p.ntile) * kTileN + g;
+            p.ts[mat].fac + tile_of(p.groups[u / np].e, u % np) * kTileN + g;
         f0 = fac[0];
         f1 = fac[8] * 0.0625f;
       }
@@ -358,12 +422,9 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         const unsigned char *st = ring + slot * kL.stage_bytes;
         slot = slot == kRing - 1 ? 0 : slot + 1;
         const int b0 = block_lo(kb);
-#pragma unroll
-        for (int cc = 0; cc < kChunks; ++cc) {
-          if (cc >= nc) break;
+        auto unpack = [&](int cc, uint32_t (&r)[16]) {
           const uint4 w4 = *reinterpret_cast<const uint4 *>(st + cc * kChunkBytes + lane * 16);
           const uint32_t wv[4] = {w4.x, w4.y, w4.z, w4.w};
-          uint32_t r[16];
 #pragma unroll
           for (int bb = 0; bb < kBlk; ++bb) {
             // The block's place in the stage.
@@ -405,23 +466,26 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
               r[4 * j + 3] = scaled(c[3], z1, h1, s1);
             }
           }
-          if (cc == 0) {
-            if (it >= kAStages && !mbar_wait(aempty + a, (it / kAStages - 1) & 1)) {
-              record_fault(&g_fault_moe, kFaultMoeWait);
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-          }
-          tmem_st_16x64(tmem_a + (a * kChunks + cc) * 32 +
-                            (static_cast<uint32_t>(32 * quarter + 16 * half) << 16),
-                        r);
+        };
+        // Both chunks without a branch: their instructions interleave. (An odd
+        // last chunk's partner is whatever the stage held, and is not stored.)
+        uint32_t r0[16], r1[16];
+        unpack(0, r0);
+        unpack(1, r1);
+        if (it >= kAStages && !mbar_wait(aempty + a, (it / kAStages - 1) & 1)) {
+          record_fault(&g_fault_moe, kFaultMoeWait);
+          ok = false;
+          break;
         }
-        if (!ok) break;
+        tc_fence_after();
+        const uint32_t ta = tmem_a + a * (kChunks * 32) +
+                            (static_cast<uint32_t>(32 * quarter + 16 * half) << 16);
+        tmem_st_16x64(ta, r0);
+        if (nc > 1) tmem_st_16x64(ta + 32, r1);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(afull + a);
+        if (lane == 0) mbar_arrive_cluster(afull0 + 8 * a);
       }
       f0 = nf0;
       f1 = nf1;
@@ -430,10 +494,11 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
   } else {
     // ---- epilogue: TMEM lanes of a quarter, half of the columns ---------------------
     const int quarter = warp & 3, half = (warp - kDqWarps) >> 2;
+    const uint32_t dempty0 = cluster_addr(dempty, 0);
     int n = 0;
-    for (int u = blockIdx.x; u < units; u += gridDim.x, ++n) {
-      const SlotGroup sg = p.groups[u / p.ntile];
-      const int nt = u % p.ntile;
+    for (int u = u0; u < units; u += du, ++n) {
+      const SlotGroup sg = p.groups[u / np];
+      const int nt = 2 * (u % np) + static_cast<int>(rank);
       // TMEM lane of a thread: gate rows 0-15 and up rows 16-31 of a quarter,
       // or row 32 quarter + lane of the tile.
       const Columns &cl = cols2[n & 1];
@@ -496,16 +561,17 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(dempty + (n & 1));
+        mbar_arrive_cluster(dempty0 + 8 * (n & 1));
         mbar_arrive(cempty + (n & 1));
       }
     }
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync_all();  // neither CTA releases the tensor memory while the pair uses it
   if (warp == kMmaWarp) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_a),
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_a),
                  "r"(kTmemCols)
                  : "memory");
   }
@@ -520,15 +586,19 @@ cudaError_t launch_one(const TileParams &p, bool pdl, cudaStream_t stream) {
   const cudaError_t e = ensure_smem_limit(kernel, kSmem, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(sm_count());
+  cfg.gridDim = dim3(sm_count() & ~1);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = pdl ? 1 : 0;
+  cfg.numAttrs = pdl ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
