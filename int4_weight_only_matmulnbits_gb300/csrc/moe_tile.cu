@@ -85,6 +85,15 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok));
+  return ok != 0;
+}
+
 // D += A x B^T over the pair: each CTA's 128 rows of A in its tensor memory,
 // each CTA's half of B's rows in its shared memory, at the same offsets.
 __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
@@ -240,36 +249,39 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     }
   } else if (warp == kMmaWarp) {
     bool ok = true;
-    int n = 0;
-    if (lane == 0 && rank == 0) {  // ---- MMAs of the pair -------------------------------
-      int slots = u0 < units ? p.groups[u0 / np].cols : 0, as = 0, bs = 0;
+    if (rank == 0) {  // ---- MMAs of the pair ---------------------------------------------
+      // The whole warp goes round and one elected lane issues, so that the
+      // instructions' operands stay in uniform registers: moving them there
+      // for every MMA took a thread on its own 100 cycles each.
+      int as = 0, bs = 0, n = 0;
       uint32_t aphase = 0, bphase = 0;
       const uint64_t desc0 = smem_desc_sw128(smem_addr(smem));
+      int slots = u0 < units ? p.groups[u0 / np].cols : 0;
       for (int u = u0; u < units && ok; u += du, ++n) {
-        const uint32_t idesc = idesc_f16(columns_of(slots)), d = tmem_d + (n & 1) * kTileSlots;
+        const uint32_t idesc = idesc_f16(columns_of(__shfl_sync(0xffffffffu, slots, 0)));
+        const uint32_t d = tmem_d + (n & 1) * kTileSlots;
         if (u + du < units) slots = p.groups[(u + du) / np].cols;
-        if (n >= 2 && !mbar_wait(dempty + (n & 1), (n / 2 - 1) & 1)) ok = false;
+        if (n >= 2) ok = __all_sync(0xffffffffu, mbar_wait(dempty + (n & 1), (n / 2 - 1) & 1));
         tc_fence_after();
-        // One thread feeds the pair's tensor cores, in the few issue slots that
-        // 18 other warps leave it: the loop is kept short. A chunk's MMAs step
-        // A by 8 columns and B's descriptor by 32 bytes.
-        for (int kb = 0; kb < p.K64; kb += kChunks) {
-          if (!mbar_wait(bfull + bs, bphase) || !mbar_wait(afull + as, aphase)) {
-            ok = false;
-            break;
-          }
+        for (int kb = 0; kb < p.K64 && ok; kb += kChunks) {
+          ok = mbar_wait(bfull + bs, bphase) && mbar_wait(afull + as, aphase);
+          ok = __all_sync(0xffffffffu, ok);
           tc_fence_after();
           const uint32_t ta = tmem_a + as * (kChunks * 32);
           const uint64_t desc = desc0 + bs * (kBStageBytes >> 4);
-          umma_ts(d, ta, desc, idesc, kb);
+          if (ok && elect_one()) {
+            // A chunk's MMAs step A by 8 columns and B's descriptor by 32 bytes.
+            umma_ts(d, ta, desc, idesc, kb);
 #pragma unroll
-          for (int kk = 1; kk < 4; ++kk) umma_ts(d, ta + kk * 8, desc + kk * 2, idesc, 1);
-          if (kb + 1 < p.K64)
+            for (int kk = 1; kk < 4; ++kk) umma_ts(d, ta + kk * 8, desc + kk * 2, idesc, 1);
+            if (kb + 1 < p.K64)
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              umma_ts(d, ta + 32 + kk * 8, desc + (kBChunkBytes >> 4) + kk * 2, idesc, 1);
-          umma_commit(aempty + as, 3);
-          umma_commit(bempty + bs, 3);
+              for (int kk = 0; kk < 4; ++kk)
+                umma_ts(d, ta + 32 + kk * 8, desc + (kBChunkBytes >> 4) + kk * 2, idesc, 1);
+            umma_commit(aempty + as, 3);
+            umma_commit(bempty + bs, 3);
+          }
+          __syncwarp();
           if (++as == kAStages) {
             as = 0;
             aphase ^= 1;
@@ -279,11 +291,14 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
             bphase ^= 1;
           }
         }
-        if (ok) umma_commit(dfull + (n & 1), 3);
+        if (ok && elect_one()) umma_commit(dfull + (n & 1), 3);
+        __syncwarp();
       }
       // Every MMA issued is complete before the tensor memory is released.
-      umma_commit(done, 1);
-      if (!mbar_wait(done, 0) || !ok) record_fault(&g_fault_moe, kFaultMoeWait);
+      if (elect_one()) umma_commit(done, 1);
+      __syncwarp();
+      if (!__all_sync(0xffffffffu, mbar_wait(done, 0)) || !ok)
+        if (lane == 0) record_fault(&g_fault_moe, kFaultMoeWait);
     } else if (lane == 0) {  // ---- CTA 1: tells CTA 0 that its half has landed -----------
       const uint32_t peer = cluster_addr(bfull, 0);
       int it = 0;
