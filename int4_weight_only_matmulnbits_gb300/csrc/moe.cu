@@ -520,7 +520,7 @@ __global__ void __launch_bounds__(kThreads) convert_kernel(const ConvertArgs a) 
 }
 
 // Per packed row of a stack: the power of two that brings its largest |scale|
-// into 2^9 .. 2^10; per expert: the bits of the largest |scale| and |bias|
+// into 2^14 .. 2^15; per expert: the bits of the largest |scale| and |bias|
 // (cleared before). A warp per 16-row tile; the tile's scales are contiguous
 // and go by 16-byte pieces, whose rows depend on the lane alone.
 struct ScaleArgs {
@@ -571,7 +571,7 @@ __global__ void __launch_bounds__(kThreads) tile_scales_kernel(const ScaleArgs a
   for (int r = 0; r < 8; ++r) {
     if (r >= per) break;
     most = max(most, top[r]);
-    if (lane < 16 / per) a.fac[i][tile * kTileN + lane * per + r] = exp2i(row_shift(top[r]) - 5);
+    if (lane < 16 / per) a.fac[i][tile * kTileN + lane * per + r] = exp2i(row_shift(top[r]));
   }
   most = __reduce_max_sync(0xffffffffu, most);
   const int e = static_cast<int>(tile / a.N16[i]);

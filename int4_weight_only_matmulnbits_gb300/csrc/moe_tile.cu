@@ -13,10 +13,11 @@
 //    swizzles or a proxy fence: 64 TMEM columns per stage of two chunks (128
 //    k), two stages. The other 384 columns are two accumulators: a unit is
 //    stored while the next one is computed. One CTA per SM.
-//  * Weights are fp16, w' = (q - z) * s with each row's scales brought to
-//    2^9 .. 2^10 by a power of two that the epilogue undoes. q - z is exact,
-//    and so is a bf16 scale; the product has 12 bits, fp16 keeps 11: one
-//    rounding of 2^-11 at most, an eighth of a bf16 weight's.
+//  * Weights are fp16, w' = (q - z) s' 2^-24, with each row's scales brought
+//    to at most 2^15 by a power of two that the epilogue undoes: one rounding
+//    of 2^-11 of the weight, or 2^-15 of its row's largest scale where that
+//    is more, and for odd z above 8 one of z s' beside it: an eighth of a
+//    bf16 weight's. A code's fp16 form costs one mask (see the unpacking).
 //  * B are fp16 activation rows, scaled by a power of two per row, in the
 //    order of the lists: TMA tiles of 32 rows x 64 k, 128-byte swizzle. Each
 //    CTA loads half of a group's rows: with 128 weight rows a CTA and all of
@@ -27,10 +28,10 @@
 //    times the 1-norm of x, for gate and for up) fits: typical values then
 //    lie 15 or so octaves above fp16's smallest normal. Down partials
 //    likewise; they are added per token by a kernel that follows.
-//  * Warps 0-7 unpack, each its own tile's codes and scales from a private
-//    ring of asynchronous copies; warps 8-15 store; one warp each issues the
-//    TMA loads, issues the MMAs, and gathers what a unit's columns need for
-//    the epilogue.
+//  * Warps 0-15 unpack, each its own tile's codes and scales from a private
+//    ring of asynchronous copies, in two groups that alternate stages; warps
+//    16-23 store; one warp each issues the TMA loads, issues the MMAs, and
+//    gathers what a unit's columns need for the epilogue.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -48,14 +49,16 @@ __device__ unsigned int g_fault_moe = 0;
 
 namespace {
 
-constexpr int kDqWarps = 8;   // warps 0-7 unpack
-constexpr int kEpWarps = 8;   // warps 8-15 store
+constexpr int kDqGroups = 2;  // groups of unpacking warps: group i takes the stages i, i + 2, ..
+constexpr int kDqGroupWarps = 8;
+constexpr int kDqWarps = kDqGroups * kDqGroupWarps;  // warps 0-15 unpack
+constexpr int kEpWarps = 8;                          // warps 16-23 store
 constexpr int kTmaWarp = kDqWarps + kEpWarps, kMmaWarp = kTmaWarp + 1, kColWarp = kTmaWarp + 2;
 constexpr int kThreads = 32 * (kTmaWarp + 3);
 constexpr int kChunks = 2;    // 64-wide k chunks per stage
-constexpr int kAStages = 2;   // TMEM A stages (64 columns each)
+constexpr int kAStages = kDqGroups;  // TMEM A stages (64 columns each), one per group
 constexpr int kBStages = 5;   // activation stages
-constexpr int kRing = 5;      // weight stages per warp in flight
+constexpr int kRing = 3;      // weight stages per warp in flight
 constexpr int kBChunkBytes = kTileSlots / 2 * 128;  // a CTA's half of the slots
 constexpr int kBStageBytes = kChunks * kBChunkBytes;
 constexpr int kTmemCols = 512;  // A, and two accumulators of kTileSlots columns
@@ -129,7 +132,7 @@ __device__ __forceinline__ void tmem_st_wait() {
 }
 
 struct Layout {  // shared memory, from a 1024-byte aligned base
-  int scale, zp, stage_bytes;  // a warp's weight stage
+  int scale, zp, fac, stage_bytes;  // a warp's weight stage
   int off_ring, off_col, off_bar, total;
 };
 // What the epilogue needs of a column: a undoes the activation row's scale
@@ -150,7 +153,8 @@ __host__ __device__ constexpr Layout make_layout() {
   Layout l{};
   l.scale = kChunks * kChunkBytes;
   l.zp = l.scale + kStageBlocks<BS> * kTileN * (SF32 ? 4 : 2);
-  l.stage_bytes = l.zp + (ZP ? (kStageBlocks<BS> / 2 + 1) * 16 : 0);
+  l.fac = l.zp + (ZP ? (kStageBlocks<BS> / 2 + 1) * 16 : 0);
+  l.stage_bytes = l.fac + 8 * 8;
   l.off_ring = kBStages * kBStageBytes;
   l.off_col = l.off_ring + kDqWarps * kRing * l.stage_bytes;
   l.off_bar = l.off_col + 2 * static_cast<int>(sizeof(Columns));
@@ -187,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
   const uint32_t rank = cluster_rank();
   if (tid == 0) {
     for (int i = 0; i < kAStages; ++i) {
-      mbar_init(afull + i, 2 * kDqWarps);  // both CTAs' warps, at CTA 0
+      mbar_init(afull + i, 2 * kDqGroupWarps);  // both CTAs' warps, at CTA 0
       mbar_init(aempty + i, 1);
     }
     for (int i = 0; i < kBStages; ++i) {
@@ -225,25 +229,33 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
   const int stages = (p.K64 + kChunks - 1) / kChunks;  // per unit
 
   if (warp == kTmaWarp) {
-    if (lane == 0) {  // ---- TMA: activation rows ----------------------------------
-      int it = 0;
-      bool ok = true;
-      for (int u = u0; u < units && ok; u += du) {
-        const SlotGroup sg = p.groups[u / np];
-        const int half = columns_of(sg.cols) / 2, first = sg.first + static_cast<int>(rank) * half;
-        const int boxes = (half + kTileBox - 1) / kTileBox;
-        for (int kb = 0; kb < p.K64; kb += kChunks, ++it) {
-          const int s = it % kBStages, nc = min(kChunks, p.K64 - kb);
-          if (it >= kBStages && !mbar_wait(bempty + s, (it / kBStages - 1) & 1)) {
-            record_fault(&g_fault_moe, kFaultMoeWait);
-            ok = false;
-            break;
-          }
+    // ---- TMA: activation rows (issued as the MMAs are, below) ---------------------
+    int s = 0, it = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int u = u0; u < units && ok; u += du) {
+      const SlotGroup sg = p.groups[u / np];
+      const int cols = __shfl_sync(0xffffffffu, sg.cols, 0), half = columns_of(cols) / 2;
+      const int first = __shfl_sync(0xffffffffu, sg.first, 0) + static_cast<int>(rank) * half;
+      const int boxes = (half + kTileBox - 1) / kTileBox;
+      for (int kb = 0; kb < p.K64; kb += kChunks, ++it) {
+        if (it >= kBStages) ok = __all_sync(0xffffffffu, mbar_wait(bempty + s, phase ^ 1));
+        if (!ok) {
+          if (lane == 0) record_fault(&g_fault_moe, kFaultMoeWait);
+          break;
+        }
+        const int nc = min(kChunks, p.K64 - kb);
+        if (elect_one()) {
           mbar_arrive_expect_tx(bfull + s, nc * boxes * kTileBox * 128);
           for (int c = 0; c < nc; ++c)
             for (int b = 0; b < boxes; ++b)
               tma_load_2d(smem + s * kBStageBytes + c * kBChunkBytes + b * kTileBox * 128, &p.tmb,
                           (kb + c) * kChunkK, first + b * kTileBox, bfull + s);
+        }
+        __syncwarp();
+        if (++s == kBStages) {
+          s = 0;
+          phase ^= 1;
         }
       }
     }
@@ -357,8 +369,9 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     }
   } else if (warp < kDqWarps) {
     // ---- unpacking ------------------------------------------------------------------
-    const int g = lane >> 2;
-    const int quarter = warp & 3, half = warp >> 2;  // TMEM lanes 32 quarter + 16 half ..
+    const int g = lane >> 2, grp = warp / kDqGroupWarps;
+    // TMEM lanes 32 quarter + 16 half ..
+    const int quarter = warp & 3, half = (warp % kDqGroupWarps) >> 2;
     unsigned char *ring = smem + kL.off_ring + warp * (kRing * kL.stage_bytes);
     const uint32_t ring_u = smem_addr(ring);
     const int mat = gate_up ? half : 0;
@@ -369,9 +382,9 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
       const int i = gate_up ? 4 * nt + quarter : 8 * nt + 2 * quarter + half;
       return int64_t(e) * p.N16 + min(i, p.N16 - 1);
     };
-    // Fetch cursor; the expert of the unit after its own is loaded a unit
-    // ahead, the row factors of the unit it is in as it enters.
-    int fu = u0, fc = 0, fslot = 0, ne = 0;
+    // Fetch cursor: unit, stage in it, ring slot; the expert of the unit after
+    // its own is loaded a unit ahead, the row factors as it enters a unit.
+    int fu = u0, fj = grp, fslot = 0, ne = 0;
     float nf0 = 0.f, nf1 = 0.f;
     const uint4 *fw = nullptr;
     const unsigned char *fs = nullptr, *fz = nullptr;
@@ -384,59 +397,59 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
       nf1 = p.ts[mat].fac[tile * kTileN + g + 8] * 0.0625f;  // high nibbles: 16 q
       if (fu + du < units) ne = p.groups[(fu + du) / np].e;
     };
+    // Into the unit that holds the stage fj counts past this one's end.
+    auto settle = [&] {
+      bool moved = false;
+      while (fj >= stages && fu < units) {
+        fj -= stages;
+        fu += du;
+        if (moved && fu < units) ne = p.groups[fu / np].e;  // (units of one stage)
+        moved = true;
+      }
+      if (moved && fu < units) aim();
+    };
     auto block_lo = [&](int c) { return BS > kChunkK ? (c * kChunkK) / BS : c * kBlk; };
     auto block_hi = [&](int c) { return BS > kChunkK ? (c * kChunkK - 1) / BS + 1 : c * kBlk; };
     auto fetch = [&] {
       if (fu < units) {
-        const uint32_t dst = ring_u + fslot * kL.stage_bytes + lane * 16;
-        const int nc = min(kChunks, p.K64 - fc);
+        const uint32_t off = fslot * kL.stage_bytes, dst = ring_u + off + lane * 16;
+        const int fc = fj * kChunks, nc = min(kChunks, p.K64 - fc);
 #pragma unroll
         for (int c = 0; c < kChunks; ++c)
           if (c < nc) cp16(dst + c * kChunkBytes, fw + (fc + c) * 32);
         const int b0 = block_lo(fc), need = block_hi(fc + nc), b1 = min(p.nb, need);
         if (lane < (b1 - b0) * kEs) cp16(dst + kL.scale, fs + b0 * (kTileN * kEs));
         else if (lane < (need - b0) * kEs)  // blocks past the last: k >= K, finite scales
-          *reinterpret_cast<uint4 *>(ring + fslot * kL.stage_bytes + kL.scale + lane * 16) =
-              make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4 *>(ring + off + kL.scale + lane * 16) = make_uint4(0, 0, 0, 0);
         if (ZP && lane < (b1 + 1) / 2 - b0 / 2) cp16(dst + kL.zp, fz + (b0 / 2) * 16);
+        if ((lane & 3) == 0)
+          *reinterpret_cast<float2 *>(ring + off + kL.fac + g * 8) = make_float2(nf0, nf1);
         fslot = fslot == kRing - 1 ? 0 : fslot + 1;
-        fc += kChunks;
-        if (fc >= p.K64) {
-          fc = 0;
-          fu += du;
-          if (fu < units) aim();
-        }
+        fj += kDqGroups;
+        if (fj >= stages) settle();
       }
       cp_commit();
     };
     if (fu < units) {
       ne = p.groups[fu / np].e;
       aim();
+      if (fj >= stages) settle();
     }
-    // The factors of the unit being unpacked. The cursor runs kRing - 1 stages
-    // ahead: at the end of a unit it is in the next one, unless units are
-    // shorter than that.
-    float f0 = nf0, f1 = nf1;
     for (int i = 0; i < kRing - 1; ++i) fetch();
 
     const uint32_t afull0 = cluster_addr(afull, 0);
-    int it = 0, slot = 0;
+    int slot = 0, j = grp, use = 0;  // use: of this group's TMEM stage
     bool ok = true;
-    for (int u = u0; u < units && ok; u += du) {
-      if (stages < kRing) {
-        const float *fac =
-            p.ts[mat].fac + tile_of(p.groups[u / np].e, u % np) * kTileN + g;
-        f0 = fac[0];
-        f1 = fac[8] * 0.0625f;
-      }
-      for (int kb = 0; kb < p.K64; kb += kChunks, ++it) {
-        const int a = it % kAStages, nc = min(kChunks, p.K64 - kb);
+    for (int u = u0; u < units && ok; u += du, j -= stages) {
+      for (; j < stages; j += kDqGroups, ++use) {
+        const int kb = j * kChunks, nc = min(kChunks, p.K64 - kb);
         cp_wait<kRing - 2>();
         __syncwarp();  // the stage is there, and every lane is done with the one before
         fetch();
         const unsigned char *st = ring + slot * kL.stage_bytes;
         slot = slot == kRing - 1 ? 0 : slot + 1;
         const int b0 = block_lo(kb);
+        const float2 f = *reinterpret_cast<const float2 *>(st + kL.fac + g * 8);
         auto unpack = [&](int cc, uint32_t (&r)[16]) {
           const uint4 w4 = *reinterpret_cast<const uint4 *>(st + cc * kChunkBytes + lane * 16);
           const uint32_t wv[4] = {w4.x, w4.y, w4.z, w4.w};
@@ -455,30 +468,44 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
               s0 = bf16_bits_to_f32(sc[0]);
               s1 = bf16_bits_to_f32(sc[8]);
             }
-            s0 *= f0;
-            s1 *= f1;
-            uint32_t z0 = 0x64086408u, z1 = 0x64806480u;  // 1024 + 8, 1024 + 16 * 8
+            s0 *= f.x;
+            s1 *= f.y;
+            // s' = s times the row's factor, at most 2^15. A code under its mask
+            // is the fp16 subnormal q 2^-24 (high nibbles: q 2^-20 with s' / 16),
+            // so that one fused multiply-add gives (q - z) s' 2^-24, rounded
+            // once. z s' is exact for z up to 8 and even z (bf16 scales).
+            const uint32_t h0 = pack_f16x2(s0, s0), h1 = pack_f16x2(s1, s1);
+            uint32_t z0, z1;
             if (ZP) {
               const uint2 zw = *reinterpret_cast<const uint2 *>(st + kL.zp + (bi + (b0 & 1)) * 8);
-              z0 = 0x64006400u | (((zw.x >> (4 * g)) & 15u) * 0x10001u);
-              z1 = 0x64006400u | (((zw.y >> (4 * g)) & 15u) * 0x100010u);
+              // -z 2^-24 as a pair; for rows g + 8, -z 2^-20.
+              z0 = f16x2_mul(h0, 0x80008000u | (((zw.x >> (4 * g)) & 15u) * 0x10001u));
+              z1 = f16x2_mul(h1, 0x80008000u | (((zw.y >> (4 * g)) & 15u) * 0x100010u));
+            } else {
+              z0 = f16x2_mul(h0, 0x80088008u);
+              z1 = f16x2_mul(h1, 0x80808080u);
             }
-            const uint32_t h0 = pack_f16x2(s0, s0), h1 = pack_f16x2(s1, s1);
-            auto scaled = [&](uint32_t c, uint32_t z, uint32_t h, float s) {
-              const uint32_t d = f16x2_sub(c, z);  // q - z, or 16 (q - z): exact
-              if (!SF32) return f16x2_mul(d, h);
-              const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&d));
-              return pack_f16x2(v.x * s, v.y * s);
+            auto scaled = [&](uint32_t c, uint32_t z, uint32_t h, float s, uint32_t zs) {
+              if (!SF32) return f16x2_fma(c, h, z);
+              // fp32 scales: from exact q - z, rounded once as well.
+              const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&c));
+              const float2 n = __half22float2(*reinterpret_cast<const __half2 *>(&zs));
+              return pack_f16x2((v.x + n.x) * s, (v.y + n.y) * s);
             };
+            uint32_t n0 = 0x80088008u, n1 = 0x80808080u;  // -z as the codes are held
+            if (SF32 && ZP) {
+              const uint2 zw = *reinterpret_cast<const uint2 *>(st + kL.zp + (bi + (b0 & 1)) * 8);
+              n0 = 0x80008000u | (((zw.x >> (4 * g)) & 15u) * 0x10001u);
+              n1 = 0x80008000u | (((zw.y >> (4 * g)) & 15u) * 0x100010u);
+            }
 #pragma unroll
             for (int jj = 0; jj < kSpb; ++jj) {
               const int j = bb * kSpb + jj;
-              uint32_t c[4];
-              codes_to_f16x2(wv[j], c);
-              r[4 * j] = scaled(c[0], z0, h0, s0);
-              r[4 * j + 1] = scaled(c[2], z0, h0, s0);
-              r[4 * j + 2] = scaled(c[1], z1, h1, s1);
-              r[4 * j + 3] = scaled(c[3], z1, h1, s1);
+              const uint32_t w = wv[j], v = w >> 8;
+              r[4 * j] = scaled(w & 0x000F000Fu, z0, h0, s0, n0);
+              r[4 * j + 1] = scaled(v & 0x000F000Fu, z0, h0, s0, n0);
+              r[4 * j + 2] = scaled(w & 0x00F000F0u, z1, h1, s1, n1);
+              r[4 * j + 3] = scaled(v & 0x00F000F0u, z1, h1, s1, n1);
             }
           }
         };
@@ -487,23 +514,21 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         uint32_t r0[16], r1[16];
         unpack(0, r0);
         unpack(1, r1);
-        if (it >= kAStages && !mbar_wait(aempty + a, (it / kAStages - 1) & 1)) {
+        if (use > 0 && !mbar_wait(aempty + grp, (use - 1) & 1)) {
           record_fault(&g_fault_moe, kFaultMoeWait);
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t ta = tmem_a + a * (kChunks * 32) +
+        const uint32_t ta = tmem_a + grp * (kChunks * 32) +
                             (static_cast<uint32_t>(32 * quarter + 16 * half) << 16);
         tmem_st_16x64(ta, r0);
         if (nc > 1) tmem_st_16x64(ta + 32, r1);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(afull0 + 8 * a);
+        if (lane == 0) mbar_arrive_cluster(afull0 + 8 * grp);
       }
-      f0 = nf0;
-      f1 = nf1;
     }
     cp_wait<0>();
   } else {
@@ -522,8 +547,9 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
       const bool live = row < p.N, up = gate_up && lane >= 16;
       const int m = up ? 1 : 0;
       const int64_t srow = int64_t(sg.e) * p.N16 * kTileN + (live ? row : 0);
-      // The inverse of a power of two.
-      const float rinv = __uint_as_float((254u << 23) - __float_as_uint(p.ts[m].fac[srow]));
+      // The inverse of a power of two, and the 2^-24 that the codes carry.
+      const float rinv =
+          __uint_as_float((254u << 23) - __float_as_uint(p.ts[m].fac[srow])) * 16777216.f;
       const float bias =
           p.w[m].bias && live ? p.w[m].bias[int64_t(sg.e) * p.N + row] : 0.f;
       const uint32_t d = tmem_d + (n & 1) * kTileSlots + (static_cast<uint32_t>(32 * quarter) << 16);

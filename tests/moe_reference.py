@@ -19,7 +19,10 @@ choose:
     1 or 16, divided out again at the end), and (1024 + r z) s / r times the sum of a block's
     activations comes off. That sum has at most 64 terms; it and the products it comes off are
     each within 64 2^-24 of (1024 + r z) s / r times the activations' magnitudes, at most
-    OFFSET = 2 * 64 * 1039 * 2^-24 of the sum of |a| s in all (r = 1, z = 15). The layer's
+    OFFSET = 2 * 64 * 1039 * 2^-24 of the sum of |a| s in all (r = 1, z = 15); or z s may be
+    rounded to fp16 before it comes off a code, at most 15 2^-12 s for each |a|, which is less.
+    An fp16 weight's row is scaled so that its largest scale lies in 2^-10 .. 2^-9: a weight
+    below 2^-14 there is within 2^-25, at most ROW = 2^-15 of the row's largest scale. The layer's
     down sums may leave as fp16 before they are added (2^-11), scaled by a bound of theirs: at
     most 2^-25 of 2^e / 2^15, where 2^e is at most four times twice the bound 15 s K' times the
     hidden bound (K' = K rounded up to 64) or the bias.
@@ -31,6 +34,7 @@ U_H = {torch.float32: 2.0 ** -22, torch.bfloat16: 2.0 ** -11}
 U_OUT = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8}
 FLOOR = {torch.float32: 2.0 ** -39, torch.bfloat16: 2.0 ** -39}
 OFFSET = {torch.float32: 0.0, torch.bfloat16: 2 * 64 * 1039 * 2.0 ** -24}
+ROW = {torch.float32: 0.0, torch.bfloat16: 2.0 ** -15}
 TINY = 1e-30
 
 
@@ -110,7 +114,8 @@ def products(A, W, experts, bias, dtype, cap=None):
             Y[m, j] = y
             low = FLOOR[dtype] * cap[m, j].unsqueeze(1) * W[e].abs().sum(1)
             off = OFFSET[dtype] * (a.abs() @ S[e].abs().T)
-            err[m, j] = (sum_u(K) + U_W[dtype]) * mag + low + off
+            row = ROW[dtype] * a.abs().sum(1, keepdim=True) * S[e].abs().amax(1)
+            err[m, j] = (sum_u(K) + U_W[dtype]) * mag + low + off + row
     return Y, err
 
 
