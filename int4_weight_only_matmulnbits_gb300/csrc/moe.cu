@@ -586,33 +586,26 @@ __global__ void __launch_bounds__(kThreads) tile_scales_kernel(const ScaleArgs a
   }
 }
 
-// Sum of each token's fp16 partials, in slot order.
+// Sum of each token's fp16 partials (rows of ld, a multiple of 8), in slot
+// order.
 __global__ void __launch_bounds__(kThreads)
-    combine_half_kernel(const uint16_t *part, const float *unscale, const int32_t *place,
-                        const int32_t *offsets, int E, int64_t M, int top_k, int N, uint16_t *Y) {
+    combine_half_kernel(const uint16_t *part, int64_t ld, const float *unscale,
+                        const int32_t *place, const int32_t *offsets, int E, int64_t M, int top_k,
+                        int N, uint16_t *Y) {
   grid_dependency_wait();
   grid_dependents_launch();
   const int routed = offsets[E];
   const int64_t m = blockIdx.x;
-  const bool vec = N % 8 == 0;  // rows of partials and of Y start on 16 bytes
-  const bool yvec = vec && reinterpret_cast<uintptr_t>(Y) % 16 == 0;
+  const bool yvec = N % 8 == 0 && reinterpret_cast<uintptr_t>(Y) % 16 == 0;
   for (int n = threadIdx.x * 8; n < N; n += kThreads * 8) {
     float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
     for (int j = 0; j < top_k; ++j) {
       const int at = place[m * top_k + j];
       if (at >= routed) continue;
       const float f = unscale[at];
-      const uint16_t *src = part + int64_t(at) * N + n;
-      uint32_t w[4];
-      if (vec) {
-        const uint4 x = *reinterpret_cast<const uint4 *>(src);
-        w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
-      } else {
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          w[q] = (n + 2 * q < N ? src[2 * q] : 0) |
-                 (n + 2 * q + 1 < N ? uint32_t(src[2 * q + 1]) << 16 : 0);
-      }
+      const uint4 x = *reinterpret_cast<const uint4 *>(part + int64_t(at) * ld + n);
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&w[q]));
@@ -902,6 +895,8 @@ ExpertsSpace experts_space(const ExpertsArgs &a) {
 constexpr int kTileMinSlots = 257;
 bool tile_path(bool a_f32, int64_t P) { return !a_f32 && P >= kTileMinSlots; }
 
+// Rows of partials start on 16 bytes.
+int64_t part_ld(int64_t N) { return ceil_div(N, 8) * 8; }
 int64_t k_pad(int64_t K) { return ceil_div(K, kChunkK) * kChunkK; }
 
 struct TileSpace {
@@ -940,7 +935,7 @@ TileSpace tile_space(unsigned char *ws, int64_t P, const ExpertStack *const *w, 
   if (layer) {
     s.norm1 = c.take<float>(P);
     s.hidden = c.take<uint16_t>(size_t(P) * k_pad(w[2]->K));
-    s.part = c.take<uint16_t>(size_t(P) * w[2]->N);
+    s.part = c.take<uint16_t>(size_t(P) * part_ld(w[2]->N));
     s.h_unscale = c.take<float>(P);
     s.p_unscale = c.take<float>(P);
     s.h_shift = c.take<int32_t>(P);
@@ -1037,6 +1032,7 @@ cudaError_t launch_experts_tile(const ExpertsArgs &a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   p.unscale = s.unscale;
   p.Y = static_cast<uint16_t *>(a.Y);
+  p.y_pairs = a.w.N % 2 == 0 && reinterpret_cast<uintptr_t>(a.Y) % 4 == 0;
   return launch_tile(p, a.w.z != nullptr, a.w.s_f32, a.w.bs, a.pdl, stream);
 }
 
@@ -1083,11 +1079,12 @@ cudaError_t launch_moe_tile(const MoeArgs &a, cudaStream_t stream) {
   down.unscale = s.h_unscale;
   down.shift = s.h_shift;
   down.part = s.part;
+  down.ldp = part_ld(a.down.N);
   down.out_unscale = s.p_unscale;
   e = launch_tile(down, a.down.z != nullptr, a.down.s_f32, a.down.bs, a.pdl, stream);
   if (e != cudaSuccess) return e;
   return launch_pdl(combine_half_kernel, static_cast<unsigned>(a.M), kThreads, 0, a.pdl, stream,
-                    s.part, s.p_unscale, s.place, s.l.offsets, a.gate.E, a.M, a.top_k, a.down.N,
+                    s.part, part_ld(a.down.N), s.p_unscale, s.place, s.l.offsets, a.gate.E, a.M, a.top_k, a.down.N,
                     static_cast<uint16_t *>(a.Y));
 }
 

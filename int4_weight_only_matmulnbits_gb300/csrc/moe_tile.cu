@@ -143,10 +143,10 @@ struct Columns {
   int out[kTileSlots];
 };
 
-// Scale blocks a stage touches (blocks of up to 64 codes lie inside chunks).
+// Scale blocks of a stage (128 k; stages start at multiples of it), and of a
+// step of all groups.
 template <int BS>
-constexpr int kStageBlocks = BS <= kChunkK ? kChunks * kChunkK / BS
-                                           : (kChunks * kChunkK - 1) / BS + 2;
+constexpr int kStageBlocks = BS <= kChunks * kChunkK ? kChunks * kChunkK / BS : 1;
 
 template <int BS, bool SF32, bool ZP>
 __host__ __device__ constexpr Layout make_layout() {
@@ -382,16 +382,19 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
       const int i = gate_up ? 4 * nt + quarter : 8 * nt + 2 * quarter + half;
       return int64_t(e) * p.N16 + min(i, p.N16 - 1);
     };
-    // Fetch cursor: unit, stage in it, ring slot; the expert of the unit after
-    // its own is loaded a unit ahead, the row factors as it enters a unit.
+    // Fetch cursor: unit, stage in it, ring slot, sources; the expert of the
+    // unit after its own is loaded a unit ahead, the row factors as it enters
+    // a unit. Lane l copies the 16-byte pieces l of a chunk's codes, and of a
+    // stage's scales and zero points (at most 32 each).
     int fu = u0, fj = grp, fslot = 0, ne = 0;
     float nf0 = 0.f, nf1 = 0.f;
     const uint4 *fw = nullptr;
     const unsigned char *fs = nullptr, *fz = nullptr;
+    auto block_of = [&](int j) { return j * (kChunks * kChunkK) / BS; };
     auto aim = [&] {
       const int64_t tile = tile_of(ne, fu % np);
-      fw = p.w[mat].b + tile * p.K64 * 32 + lane;
-      fs = p.w[mat].s + tile * p.nb * (kTileN * kEs) + lane * 16;
+      fw = p.w[mat].b + (tile * p.K64 + fj * kChunks) * 32 + lane;
+      fs = p.w[mat].s + (tile * p.nb + block_of(fj)) * (kTileN * kEs) + lane * 16;
       if (ZP) fz = p.w[mat].z + tile * p.nbz * 8 + lane * 16;
       nf0 = p.ts[mat].fac[tile * kTileN + g];
       nf1 = p.ts[mat].fac[tile * kTileN + g + 8] * 0.0625f;  // high nibbles: 16 q
@@ -408,28 +411,38 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
       }
       if (moved && fu < units) aim();
     };
-    auto block_lo = [&](int c) { return BS > kChunkK ? (c * kChunkK) / BS : c * kBlk; };
-    auto block_hi = [&](int c) { return BS > kChunkK ? (c * kChunkK - 1) / BS + 1 : c * kBlk; };
     auto fetch = [&] {
       if (fu < units) {
         const uint32_t off = fslot * kL.stage_bytes, dst = ring_u + off + lane * 16;
-        const int fc = fj * kChunks, nc = min(kChunks, p.K64 - fc);
-#pragma unroll
-        for (int c = 0; c < kChunks; ++c)
-          if (c < nc) cp16(dst + c * kChunkBytes, fw + (fc + c) * 32);
-        const int b0 = block_lo(fc), need = block_hi(fc + nc), b1 = min(p.nb, need);
-        if (lane < (b1 - b0) * kEs) cp16(dst + kL.scale, fs + b0 * (kTileN * kEs));
-        else if (lane < (need - b0) * kEs)  // blocks past the last: k >= K, finite scales
-          *reinterpret_cast<uint4 *>(ring + off + kL.scale + lane * 16) = make_uint4(0, 0, 0, 0);
-        if (ZP && lane < (b1 + 1) / 2 - b0 / 2) cp16(dst + kL.zp, fz + (b0 / 2) * 16);
+        cp16(dst, fw);
+        const int b0 = block_of(fj);
+        if (fj + 1 < stages) {
+          cp16(dst + kChunkBytes, fw + 32);
+          if (lane < kStageBlocks<BS> * kEs) cp16(dst + kL.scale, fs);
+        } else {
+          // The last stage may have one chunk, and blocks past the last: those
+          // hold only k >= K, whose activations are zero, and get scales 0.
+          if (fj * kChunks + 1 < p.K64) cp16(dst + kChunkBytes, fw + 32);
+          const int b1 = min(p.nb - b0, kStageBlocks<BS>);
+          if (lane < b1 * kEs) cp16(dst + kL.scale, fs);
+          else if (lane < kStageBlocks<BS> * kEs)
+            *reinterpret_cast<uint4 *>(ring + off + kL.scale + lane * 16) =
+                make_uint4(0, 0, 0, 0);
+        }
+        // Pairs of zero-point words from an even block on.
+        if (ZP && lane < (min(p.nb, b0 + kStageBlocks<BS>) + 1) / 2 - b0 / 2)
+          cp16(dst + kL.zp, fz + (b0 / 2) * 16);
         if ((lane & 3) == 0)
           *reinterpret_cast<float2 *>(ring + off + kL.fac + g * 8) = make_float2(nf0, nf1);
         fslot = fslot == kRing - 1 ? 0 : fslot + 1;
+        fw += kDqGroups * kChunks * 32;
+        fs += kDqGroups * kChunks * kChunkK / BS * (kTileN * kEs);
         fj += kDqGroups;
         if (fj >= stages) settle();
       }
       cp_commit();
     };
+    static_assert(kDqGroups * kChunks * kChunkK % BS == 0, "whole blocks per step");
     if (fu < units) {
       ne = p.groups[fu / np].e;
       aim();
@@ -442,13 +455,12 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     bool ok = true;
     for (int u = u0; u < units && ok; u += du, j -= stages) {
       for (; j < stages; j += kDqGroups, ++use) {
-        const int kb = j * kChunks, nc = min(kChunks, p.K64 - kb);
         cp_wait<kRing - 2>();
         __syncwarp();  // the stage is there, and every lane is done with the one before
         fetch();
         const unsigned char *st = ring + slot * kL.stage_bytes;
         slot = slot == kRing - 1 ? 0 : slot + 1;
-        const int b0 = block_lo(kb);
+        const int odd = ZP ? block_of(j) & 1 : 0;  // the first word of its pair, or the second
         const float2 f = *reinterpret_cast<const float2 *>(st + kL.fac + g * 8);
         auto unpack = [&](int cc, uint32_t (&r)[16]) {
           const uint4 w4 = *reinterpret_cast<const uint4 *>(st + cc * kChunkBytes + lane * 16);
@@ -456,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
 #pragma unroll
           for (int bb = 0; bb < kBlk; ++bb) {
             // The block's place in the stage.
-            const int bi = BS > kChunkK ? block_lo(kb + cc) - b0 : cc * kBlk + bb;
+            const int bi = BS > kChunkK ? 0 : cc * kBlk + bb;
             float s0, s1;
             if (SF32) {
               const float *sc = reinterpret_cast<const float *>(st + kL.scale) + bi * kTileN + g;
@@ -477,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
             const uint32_t h0 = pack_f16x2(s0, s0), h1 = pack_f16x2(s1, s1);
             uint32_t z0, z1;
             if (ZP) {
-              const uint2 zw = *reinterpret_cast<const uint2 *>(st + kL.zp + (bi + (b0 & 1)) * 8);
+              const uint2 zw = *reinterpret_cast<const uint2 *>(st + kL.zp + (bi + odd) * 8);
               // -z 2^-24 as a pair; for rows g + 8, -z 2^-20.
               z0 = f16x2_mul(h0, 0x80008000u | (((zw.x >> (4 * g)) & 15u) * 0x10001u));
               z1 = f16x2_mul(h1, 0x80008000u | (((zw.y >> (4 * g)) & 15u) * 0x100010u));
@@ -494,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
             };
             uint32_t n0 = 0x80088008u, n1 = 0x80808080u;  // -z as the codes are held
             if (SF32 && ZP) {
-              const uint2 zw = *reinterpret_cast<const uint2 *>(st + kL.zp + (bi + (b0 & 1)) * 8);
+              const uint2 zw = *reinterpret_cast<const uint2 *>(st + kL.zp + (bi + odd) * 8);
               n0 = 0x80008000u | (((zw.x >> (4 * g)) & 15u) * 0x10001u);
               n1 = 0x80008000u | (((zw.y >> (4 * g)) & 15u) * 0x100010u);
             }
@@ -509,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
             }
           }
         };
-        // Both chunks without a branch: their instructions interleave. (An odd
+        // Both chunks without a branch: their instructions interleave. (A lone
         // last chunk's partner is whatever the stage held, and is not stored.)
         uint32_t r0[16], r1[16];
         unpack(0, r0);
@@ -523,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         const uint32_t ta = tmem_a + grp * (kChunks * 32) +
                             (static_cast<uint32_t>(32 * quarter + 16 * half) << 16);
         tmem_st_16x64(ta, r0);
-        if (nc > 1) tmem_st_16x64(ta + 32, r1);
+        if (j * kChunks + 1 < p.K64) tmem_st_16x64(ta + 32, r1);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -562,40 +574,64 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
       for (int c0 = share * half; c0 < share * (half + 1) && c0 < sg.cols; c0 += 32) {
         float v[32];
         tmem_ld32(d + c0, v);
+        // Lanes of neighbouring rows exchange, so that each stores two rows of
+        // every other column: a pair of columns (c, c + 1) in `u`, own row.
+        auto pair_rows = [&](uint32_t u) {
+          const uint32_t w = __shfl_xor_sync(0xffffffffu, u, 1);
+          return __byte_perm(u, w, lane & 1 ? 0x3276 : 0x5410);
+        };
         if (gate_up) {
           // Lanes below 16 take columns 0-15, the others 16-31: each sends
           // what the other half-warp lacks.
           const int mine0 = c0 + (up ? 16 : 0);
-          uint16_t *dst = p.hidden + int64_t(sg.first + mine0) * p.ldh + row;
+          uint16_t *dst = p.hidden + int64_t(sg.first + mine0 + (lane & 1)) * p.ldh + (row & ~1);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float keep = up ? v[16 + i] : v[i], send = up ? v[i] : v[16 + i];
-            const float2 ck = cl.ab[mine0 + i];
-            const float as = cl.ab[c0 + i + (up ? 0 : 16)].x;
-            const float k = fmaf(keep * rinv, ck.x, bias);
-            const float got = __shfl_xor_sync(0xffffffffu, fmaf(send * rinv, as, bias), 16);
-            const float gv = up ? got : k, uv = up ? k : got;
-            const float h = __fdividef(gv * uv, 1.f + __expf(-gv)) * ck.y;
-            // exp overflows for gv < -88: the quotient is then -0 or, where
-            // __fdividef's divisor passes 2^126, 0 as well.
-            if (live && mine0 + i < sg.cols)
-              dst[i * p.ldh] = __half_as_ushort(__float2half_rn(h));
+          for (int i = 0; i < 16; i += 2) {
+            const float4 ck = *reinterpret_cast<const float4 *>(&cl.ab[mine0 + i]);
+            const float4 cs = *reinterpret_cast<const float4 *>(&cl.ab[c0 + i + (up ? 0 : 16)]);
+            float h[2];
+#pragma unroll
+            for (int o = 0; o < 2; ++o) {
+              const float keep = up ? v[16 + i + o] : v[i + o];
+              const float send = up ? v[i + o] : v[16 + i + o];
+              const float k = fmaf(keep * rinv, o ? ck.z : ck.x, bias);
+              const float got = __shfl_xor_sync(
+                  0xffffffffu, fmaf(send * rinv, o ? cs.z : cs.x, bias), 16);
+              const float gv = up ? got : k, uv = up ? k : got;
+              // exp overflows for gv < -88: the quotient is then 0.
+              h[o] = __fdividef(gv * uv, 1.f + __expf(-gv)) * (o ? ck.w : ck.y);
+            }
+            const uint32_t w = pair_rows(pack_f16x2(h[0], h[1]));
+            if ((row & ~1) < p.N && mine0 + i + (lane & 1) < sg.cols)
+              *reinterpret_cast<uint32_t *>(dst + i * p.ldh) = w;
           }
         } else if (p.mode == kStreamProduct) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float y = fmaf(v[i] * rinv, cl.ab[c0 + i].x, bias);
-            if (live && c0 + i < sg.cols)
-              p.Y[int64_t(cl.out[c0 + i]) * p.N + row] = static_cast<uint16_t>(bf16_bits(y));
+          for (int i = 0; i < 32; i += 2) {
+            const float4 ck = *reinterpret_cast<const float4 *>(&cl.ab[c0 + i]);
+            const uint32_t u = f32x2_to_bf16x2(fmaf(v[i] * rinv, ck.x, bias),
+                                               fmaf(v[i + 1] * rinv, ck.z, bias));
+            if (p.y_pairs) {
+              const uint32_t w = pair_rows(u);
+              const int c = c0 + i + (lane & 1);
+              if ((row & ~1) < p.N && c < sg.cols)
+                *reinterpret_cast<uint32_t *>(p.Y + int64_t(cl.out[c]) * p.N + (row & ~1)) = w;
+            } else if (live) {
+              if (c0 + i < sg.cols)
+                p.Y[int64_t(cl.out[c0 + i]) * p.N + row] = static_cast<uint16_t>(u);
+              if (c0 + i + 1 < sg.cols)
+                p.Y[int64_t(cl.out[c0 + i + 1]) * p.N + row] = static_cast<uint16_t>(u >> 16);
+            }
           }
         } else {
-          uint16_t *dst = p.part + int64_t(sg.first + c0) * p.N + row;
+          uint16_t *dst = p.part + int64_t(sg.first + c0 + (lane & 1)) * p.ldp + (row & ~1);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float2 c = cl.ab[c0 + i];
-            const float y = fmaf(v[i] * rinv, c.x, bias * c.y);
-            if (live && c0 + i < sg.cols)
-              dst[int64_t(i) * p.N] = __half_as_ushort(__float2half_rn(y));
+          for (int i = 0; i < 32; i += 2) {
+            const float4 ck = *reinterpret_cast<const float4 *>(&cl.ab[c0 + i]);
+            const uint32_t w = pair_rows(pack_f16x2(fmaf(v[i] * rinv, ck.x, bias * ck.y),
+                                                    fmaf(v[i + 1] * rinv, ck.z, bias * ck.w)));
+            if ((row & ~1) < p.N && c0 + i + (lane & 1) < sg.cols)
+              *reinterpret_cast<uint32_t *>(dst + i * p.ldp) = w;
           }
         }
       }

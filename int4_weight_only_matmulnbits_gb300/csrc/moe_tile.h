@@ -37,9 +37,10 @@ struct TileParams {
   const int32_t *shift;
   // Outputs: Y [P, N] bf16 by slot (product); hidden fp16 rows [P, ldh] and
   // their undo factors and exponents, by place (gate and up); fp16 partials
-  // [P, N] and their undo factors, by place (down).
+  // [P, ldp] and their undo factors, by place (down). ldh and ldp are even.
   uint16_t *Y, *hidden, *part;
-  int64_t ldh;
+  int64_t ldh, ldp;
+  int y_pairs;  // rows of Y start on 4 bytes
   float *out_unscale;
   int32_t *out_shift;
 };
