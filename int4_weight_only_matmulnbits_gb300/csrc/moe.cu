@@ -123,78 +123,6 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// Slots by expert (one block): a stable counting sort. Each warp owns a
-// contiguous range of slots and a row of counters; slots without an expert
-// count as expert E. Also the groups of up to 2^gt_log2 slots, when asked for.
-constexpr int kListWarps = 16;
-__global__ void __launch_bounds__(kListWarps * 32)
-    lists_kernel(const int32_t *experts, int64_t P, int E, int32_t *offsets, int32_t *order,
-                 SlotGroup *groups, int32_t *n_groups, int gt_log2) {
-  extern __shared__ int32_t cnt[];  // [kListWarps][E + 1], then [E + 1] twice
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int32_t *mine = cnt + warp * (E + 1), *start = cnt + kListWarps * (E + 1);
-  int32_t *gstart = start + E + 1;
-  grid_dependency_wait();
-  grid_dependents_launch();
-  for (int i = threadIdx.x; i < kListWarps * (E + 1); i += blockDim.x) cnt[i] = 0;
-  __syncthreads();
-  const int64_t per = ceil_div(P, kListWarps), lo = warp * per, hi = lo + per < P ? lo + per : P;
-  auto key_of = [&](int64_t p) {
-    const int e = experts[p];
-    return e >= 0 && e < E ? e : E;
-  };
-  for (int64_t p = lo + lane; p < hi; p += 32) atomicAdd(mine + key_of(p), 1);
-  __syncthreads();
-  // Per expert: exclusive prefix over the warps; the totals go to start.
-  for (int e = threadIdx.x; e <= E; e += blockDim.x) {
-    int sum = 0;
-    for (int w = 0; w < kListWarps; ++w) {
-      const int c = cnt[w * (E + 1) + e];
-      cnt[w * (E + 1) + e] = sum;
-      sum += c;
-    }
-    start[e] = sum;
-    gstart[e] = e < E ? (sum + (1 << gt_log2) - 1) >> gt_log2 : 0;
-  }
-  __syncthreads();
-  if (warp < 2) {  // exclusive prefixes over the experts: slots, groups
-    int32_t *v = warp ? gstart : start;
-    int base = 0;
-    for (int i = lane; i - lane <= E; i += 32) {
-      const int own = i <= E ? v[i] : 0;
-      int x = own;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      if (i <= E) v[i] = base + x - own;
-      base += __shfl_sync(0xffffffffu, x, 31);
-    }
-  }
-  __syncthreads();
-  for (int e = threadIdx.x; e <= E; e += blockDim.x) {
-    offsets[e] = start[e];
-    if (groups && e < E) {
-      const int first = start[e], n = start[e + 1] - first, gt = 1 << gt_log2;
-      SlotGroup *g = groups + gstart[e];
-      for (int k = 0; k < n; k += gt) *g++ = SlotGroup{e, first + k, min(gt, n - k)};
-    }
-  }
-  if (groups && threadIdx.x == 0) *n_groups = gstart[E];
-  for (int64_t p0 = lo; p0 < hi; p0 += 32) {
-    const int64_t p = p0 + lane;
-    const bool ok = p < hi;
-    const int e = ok ? key_of(p) : -1;
-    const unsigned same = __match_any_sync(0xffffffffu, e);
-    const int rank = __popc(same & ((1u << lane) - 1));
-    if (ok) order[start[e] + mine[e] + rank] = static_cast<int32_t>(p);
-    __syncwarp();
-    if (ok && rank == 0) mine[e] += __popc(same);
-    __syncwarp();
-  }
-}
-
 // Bits of the largest magnitude of row `row` of A [.., K], by one block.
 __device__ __forceinline__ uint32_t row_top(const void *A, bool f32, bool vec, int64_t row,
                                             int K, uint32_t *scratch) {
@@ -315,8 +243,9 @@ __global__ void __launch_bounds__(kThreads)
 
 // ---- many slots, bf16: lists over several blocks, fp16 rows, scales ----------
 
-// The stable counting sort of lists_kernel over many blocks of kSortSlots
-// slots. First launch: each block's slots per expert, [blocks][E + 1].
+// Slots by expert over many blocks of kSortSlots slots: a stable counting
+// sort. First launch: each block's slots per expert, [blocks][E + 1] (slots
+// without an expert count as expert E).
 constexpr int kSortSlots = 1024;
 __global__ void __launch_bounds__(kThreads)
     count_kernel(const int32_t *experts, int64_t P, int E, int32_t *counts, uint32_t *clear,
@@ -330,66 +259,83 @@ __global__ void __launch_bounds__(kThreads)
   __syncthreads();
   const int64_t lo = int64_t(blockIdx.x) * kSortSlots;
   const int n = static_cast<int>(P - lo < kSortSlots ? P - lo : kSortSlots);
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const int e = experts[lo + i];
-    atomicAdd(cnt + (e >= 0 && e < E ? e : E), 1);
-  }
+#pragma unroll
+  for (int i = threadIdx.x; i < kSortSlots; i += kThreads)
+    if (i < n) {
+      const int e = experts[lo + i];
+      atomicAdd(cnt + (e >= 0 && e < E ? e : E), 1);
+    }
   __syncthreads();
   for (int i = threadIdx.x; i <= E; i += kThreads) counts[int64_t(blockIdx.x) * (E + 1) + i] = cnt[i];
 }
 
-// Slots per group of an expert's c slots: as even as whole columns of 16 let
-// them be, at most gt (a multiple of 16).
-__device__ __forceinline__ int group_size(int c, int gt) {
+// Slots per group of an expert's c slots: as even as whole runs of `unit` let
+// them be, at most gt (a multiple of unit).
+__device__ __forceinline__ int group_size(int c, int gt, int unit) {
   const int n = (c + gt - 1) / gt;
-  return n ? (c + 16 * n - 1) / (16 * n) * 16 : gt;
+  return n ? (c + unit * n - 1) / (unit * n) * unit : gt;
 }
 
 // Second launch: places. Each block adds up the counts of the blocks before
 // it and of all, scans the experts, and places its slots in order; block 0
 // writes the offsets and the groups. place[p]: where slot p stands in the
 // order, counting from 0; slots without an expert come last.
-__global__ void __launch_bounds__(kThreads)
+constexpr int kPlaceThreads = 512;
+constexpr int kPlaceWarps = kPlaceThreads / 32;
+__global__ void __launch_bounds__(kPlaceThreads)
     place_kernel(const int32_t *experts, int64_t P, int E, const int32_t *counts, int32_t *offsets,
-                 int32_t *order, int32_t *place, SlotGroup *groups, int32_t *n_groups,
-                 int gt) {
+                 int32_t *order, int32_t *place, SlotGroup *groups, int32_t *n_groups, int gt,
+                 int unit) {
   extern __shared__ int32_t mem[];
-  int32_t *start = mem, *gstart = mem + E + 1;        // [E + 1] each
-  int32_t *cnt = mem + 2 * (E + 1);                   // [kWarps][E + 1]
+  int32_t *start = mem, *gstart = mem + E + 1;  // [E + 1] each
+  int32_t *cnt = mem + 2 * (E + 1);             // [kPlaceWarps][E + 1]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int i = threadIdx.x; i < kPlaceWarps * (E + 1); i += kPlaceThreads) cnt[i] = 0;
+  for (int i = threadIdx.x; i < 2 * (E + 1); i += kPlaceThreads) mem[i] = 0;
   grid_dependency_wait();
   grid_dependents_launch();
-  const int64_t lo = int64_t(blockIdx.x) * kSortSlots;
-  const int n = static_cast<int>(P - lo < kSortSlots ? P - lo : kSortSlots);
-  for (int i = threadIdx.x; i < kWarps * (E + 1); i += kThreads) cnt[i] = 0;
+  constexpr int kPer = kSortSlots / kPlaceWarps, kEach = kPer / 32;
+  const int64_t lo = int64_t(blockIdx.x) * kSortSlots + warp * kPer + lane;
+  int key[kEach];  // experts of the warp's slots, 32 at a time; -1: past the end
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    key[i] = -1;
+    if (lo + 32 * i < P) {
+      const int e = experts[lo + 32 * i];
+      key[i] = e >= 0 && e < E ? e : E;
+    }
+  }
   __syncthreads();
-  constexpr int kPer = kSortSlots / kWarps;
-  auto key_of = [&](int i) {
-    const int e = experts[lo + i];
-    return e >= 0 && e < E ? e : E;
-  };
   int32_t *mine = cnt + warp * (E + 1);
-  for (int i = warp * kPer + lane; i < min(n, (warp + 1) * kPer); i += 32)
-    atomicAdd(mine + key_of(i), 1);
-  // Totals, and the part of them in the blocks before; two threads per
-  // expert where there are that many.
-  __syncthreads();
-  for (int e = threadIdx.x; e <= E; e += kThreads) {
+#pragma unroll
+  for (int i = 0; i < kEach; ++i)
+    if (key[i] >= 0) atomicAdd(mine + key[i], 1);
+  // Totals, and the part of them in the blocks before, by all threads: a few
+  // blocks' counts of an expert each.
+  for (int i = threadIdx.x; i < (E + 1) * kPlaceWarps; i += kPlaceThreads) {
+    const int e = i % (E + 1);
     int all = 0, before = 0;
-#pragma unroll 8
-    for (int b = 0; b < gridDim.x; ++b) {
+#pragma unroll 4
+    for (int b = i / (E + 1); b < gridDim.x; b += kPlaceWarps) {
       const int c = counts[int64_t(b) * (E + 1) + e];
       all += c;
       if (b < blockIdx.x) before += c;
     }
-    start[e] = all;
-    const int size = group_size(all, gt);
-    gstart[e] = e < E ? (all + size - 1) / size : 0;
-    for (int w = 0; w < kWarps; ++w) {  // where each warp's first slot goes, less start
+    if (all) {  // gstart holds the part before until the scan
+      atomicAdd(start + e, all);
+      if (before) atomicAdd(gstart + e, before);
+    }
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e <= E; e += kPlaceThreads) {
+    int before = gstart[e];
+    for (int w = 0; w < kPlaceWarps; ++w) {  // where each warp's first slot goes, less start
       const int c = cnt[w * (E + 1) + e];
       cnt[w * (E + 1) + e] = before;
       before += c;
     }
+    const int all = start[e], size = group_size(all, gt, unit);
+    gstart[e] = e < E ? (all + size - 1) / size : 0;
   }
   __syncthreads();
   if (warp < 2) {  // exclusive prefixes over the experts: slots, groups
@@ -409,31 +355,29 @@ __global__ void __launch_bounds__(kThreads)
   }
   __syncthreads();
   if (blockIdx.x == 0) {
-    for (int e = threadIdx.x; e <= E; e += kThreads) {
+    for (int e = threadIdx.x; e <= E; e += kPlaceThreads) {
       offsets[e] = start[e];
       if (groups && e < E) {
         const int first = start[e], c = start[e + 1] - first, n = gstart[e + 1] - gstart[e];
         SlotGroup *g = groups + gstart[e];
-        const int size = group_size(c, gt);
+        const int size = group_size(c, gt, unit);
         for (int k = 0; k < n; ++k)
           g[k] = SlotGroup{e, first + k * size, min(size, c - k * size)};
       }
     }
     if (groups && threadIdx.x == 0) *n_groups = gstart[E];
   }
-  for (int i0 = warp * kPer; i0 < min(n, (warp + 1) * kPer); i0 += 32) {
-    const int i = i0 + lane;
-    const bool ok = i < n;
-    const int e = ok ? key_of(i) : -1;
-    const unsigned same = __match_any_sync(0xffffffffu, e);
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const unsigned same = __match_any_sync(0xffffffffu, key[i]);
     const int rank = __popc(same & ((1u << lane) - 1));
-    if (ok) {
-      const int at = start[e] + mine[e] + rank;
-      order[at] = static_cast<int32_t>(lo + i);
-      if (place) place[lo + i] = at;
+    if (key[i] >= 0) {
+      const int at = start[key[i]] + mine[key[i]] + rank;
+      order[at] = static_cast<int32_t>(lo + 32 * i);
+      if (place) place[lo + 32 * i] = at;
     }
     __syncwarp();
-    if (ok && rank == 0) mine[e] += __popc(same);
+    if (key[i] >= 0 && rank == 0) mine[key[i]] += __popc(same);
     __syncwarp();
   }
 }
@@ -456,17 +400,21 @@ struct ConvertArgs {
   uint16_t *hidden;
   int hidden_n, hidden_ld;
 };
-__global__ void __launch_bounds__(kThreads) convert_kernel(const ConvertArgs a) {
-  __shared__ uint32_t tops[kWarps];
-  __shared__ float sums[kWarps];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+// A block of about a thread per 8 columns, for either kernel of rows.
+int row_threads(int64_t n) {
+  return static_cast<int>(std::min<int64_t>(1024, ceil_div(ceil_div(n, 8), 32) * 32));
+}
+__global__ void __launch_bounds__(1024) convert_kernel(const ConvertArgs a) {
+  __shared__ uint32_t tops[32];
+  __shared__ float sums[32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, threads = blockDim.x;
   const int64_t m = blockIdx.x;
   grid_dependency_wait();
   grid_dependents_launch();
   const int routed = a.offsets[a.E];
   uint32_t top = 0;
   float sum = 0.f;
-  for (int k = tid * 8; k < a.Kp; k += kThreads * 8) {
+  for (int k = tid * 8; k < a.Kp; k += threads * 8) {
     float v[8];
     load8(a.A, false, a.a_vec, m * a.K, k, a.K, v);
 #pragma unroll
@@ -483,7 +431,7 @@ __global__ void __launch_bounds__(kThreads) convert_kernel(const ConvertArgs a) 
   }
   __syncthreads();
   sum = 0.f;
-  for (int w = 0; w < kWarps; ++w) {
+  for (int w = 0; w < threads >> 5; ++w) {
     top = max(top, tops[w]);
     sum += sums[w];
   }
@@ -498,13 +446,13 @@ __global__ void __launch_bounds__(kThreads) convert_kernel(const ConvertArgs a) 
         if (a.norm1) a.norm1[at] = sum * 1.01f;  // above the exact sum for any K < 2^17
       }
       if (a.hidden)
-        for (int k = a.hidden_n + tid; k < a.hidden_ld; k += kThreads)
+        for (int k = a.hidden_n + tid; k < a.hidden_ld; k += threads)
           a.hidden[int64_t(at) * a.hidden_ld + k] = 0;
     } else if (a.Y) {
-      for (int n = tid; n < a.N; n += kThreads) a.Y[slot * a.N + n] = 0;
+      for (int n = tid; n < a.N; n += threads) a.Y[slot * a.N + n] = 0;
     }
   }
-  for (int k = tid * 8; k < a.Kp; k += kThreads * 8) {
+  for (int k = tid * 8; k < a.Kp; k += threads * 8) {
     float v[8];
     load8(a.A, false, a.a_vec, m * a.K, k, a.K, v);
     uint4 h;
@@ -528,57 +476,56 @@ struct ScaleArgs {
   const float *bias[3];
   float *fac[3];
   uint32_t *smax[3], *bmax[3];
-  int64_t tiles_end[3];  // running sums of the stacks' tiles
   int N[3], N16[3], nb[3], f32[3];
-  int count;
 };
+// blockIdx: (tiles of an expert, expert, stack).
 __global__ void __launch_bounds__(kThreads) tile_scales_kernel(const ScaleArgs a) {
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, i = blockIdx.z, e = blockIdx.y;
+  const int nt = blockIdx.x * kWarps + (threadIdx.x >> 5);
   grid_dependency_wait();
   grid_dependents_launch();
-  int64_t tile = blockIdx.x * int64_t(kWarps) + (threadIdx.x >> 5);
-  int i = 0;
-  while (i < a.count && tile >= a.tiles_end[i]) ++i;
-  if (i == a.count) return;
-  if (i > 0) tile -= a.tiles_end[i - 1];
-  const int per = a.f32[i] ? 4 : 8;  // scales per piece
+  if (nt >= a.N16[i]) return;
+  const bool f32 = a.f32[i];
+  const int64_t tile = int64_t(e) * a.N16[i] + nt;
+  const int n = nt * kTileN + lane;
+  uint32_t b = 0;
+  if (a.bias[i] && lane < kTileN && n < a.N[i])
+    b = __float_as_uint(a.bias[i][int64_t(e) * a.N[i] + n]) & 0x7FFFFFFFu;
+  const int per = f32 ? 4 : 8;  // scales per piece
   const int pieces = a.nb[i] * 16 / per;
-  const uint4 *src = reinterpret_cast<const uint4 *>(
-      a.s[i] + tile * a.nb[i] * (16 * (a.f32[i] ? 4 : 2)));
-  uint32_t top[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  const uint4 *src =
+      reinterpret_cast<const uint4 *>(a.s[i] + tile * a.nb[i] * (16 * (f32 ? 4 : 2)));
+  // fp32: a word per row; bf16: two rows to a word.
+  uint32_t top[4] = {0, 0, 0, 0};
 #pragma unroll 4
   for (int q = lane; q < pieces; q += 32) {
     const uint4 x = src[q];
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-    for (int o = 0; o < 4; ++o) {
-      if (a.f32[i]) {
-        top[o] = max(top[o], w[o] & 0x7FFFFFFFu);
-      } else {
-        top[2 * o] = max(top[2 * o], (w[o] << 16) & 0x7FFF0000u);
-        top[2 * o + 1] = max(top[2 * o + 1], w[o] & 0x7FFF0000u);
-      }
-    }
+    for (int o = 0; o < 4; ++o)
+      top[o] = f32 ? max(top[o], w[o] & 0x7FFFFFFFu) : __vmaxu2(top[o], w[o] & 0x7FFF7FFFu);
   }
   // Lanes with the same piece of a block: equal modulo 2 (bf16) or 4 (fp32).
 #pragma unroll
   for (int o = 2; o < 32; o <<= 1)
+    if (o >= 4 || !f32)
 #pragma unroll
-    for (int r = 0; r < 8; ++r)
-      if (o >= 4 || !a.f32[i]) top[r] = max(top[r], __shfl_xor_sync(0xffffffffu, top[r], o));
+      for (int r = 0; r < 4; ++r) {
+        const uint32_t v = __shfl_xor_sync(0xffffffffu, top[r], o);
+        top[r] = f32 ? max(top[r], v) : __vmaxu2(top[r], v);
+      }
   uint32_t most = 0;
+  float *fac = a.fac[i] + tile * kTileN + lane * per;
 #pragma unroll
-  for (int r = 0; r < 8; ++r) {
-    if (r >= per) break;
-    most = max(most, top[r]);
-    if (lane < 16 / per) a.fac[i][tile * kTileN + lane * per + r] = exp2i(row_shift(top[r]));
+  for (int r = 0; r < 4; ++r) {
+    const uint32_t t0 = f32 ? top[r] : top[r] << 16, t1 = f32 ? 0 : top[r] & 0xFFFF0000u;
+    most = max(most, max(t0, t1));
+    if (lane < 16 / per) {
+      fac[f32 ? r : 2 * r] = exp2i(row_shift(t0));
+      if (!f32) fac[2 * r + 1] = exp2i(row_shift(t1));
+    }
   }
   most = __reduce_max_sync(0xffffffffu, most);
-  const int e = static_cast<int>(tile / a.N16[i]);
-  uint32_t b = 0;
-  const int n = static_cast<int>(tile % a.N16[i]) * kTileN + lane;
-  if (a.bias[i] && lane < kTileN && n < a.N[i])
-    b = __float_as_uint(a.bias[i][int64_t(e) * a.N[i] + n]) & 0x7FFFFFFFu;
   b = __reduce_max_sync(0xffffffffu, b);
   if (lane == 0) {
     atomicMax(a.smax[i] + e, most);
@@ -588,7 +535,7 @@ __global__ void __launch_bounds__(kThreads) tile_scales_kernel(const ScaleArgs a
 
 // Sum of each token's fp16 partials (rows of ld, a multiple of 8), in slot
 // order.
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(1024)
     combine_half_kernel(const uint16_t *part, int64_t ld, const float *unscale,
                         const int32_t *place, const int32_t *offsets, int E, int64_t M, int top_k,
                         int N, uint16_t *Y) {
@@ -597,9 +544,9 @@ __global__ void __launch_bounds__(kThreads)
   const int routed = offsets[E];
   const int64_t m = blockIdx.x;
   const bool yvec = N % 8 == 0 && reinterpret_cast<uintptr_t>(Y) % 16 == 0;
-  for (int n = threadIdx.x * 8; n < N; n += kThreads * 8) {
+  for (int n = threadIdx.x * 8; n < N; n += blockDim.x * 8) {
     float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
+#pragma unroll 8
     for (int j = 0; j < top_k; ++j) {
       const int at = place[m * top_k + j];
       if (at >= routed) continue;
@@ -644,10 +591,10 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 template <typename... P, typename... A>
-cudaError_t launch_pdl(void (*kernel)(P...), unsigned grid, int block, size_t smem, bool pdl,
+cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, int block, size_t smem, bool pdl,
                        cudaStream_t stream, A... args) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(block);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -818,18 +765,27 @@ struct Lists {
 };
 
 // Groups of P slots at most: every expert may leave one partly filled.
-size_t max_groups(int64_t P, int E, int gt_log2) {
-  return std::min<int64_t>(P, (P >> gt_log2) + E);
+size_t max_groups(int64_t P, int E, int gt) {
+  return static_cast<size_t>(std::min<int64_t>(P, P / gt + E));
 }
+size_t count_words(int64_t P, int E) { return ceil_div(P, kSortSlots) * (E + 1); }
 
-cudaError_t launch_lists(const int32_t *experts, int64_t P, int E, const Lists &l, int gt_log2,
-                         bool pdl, cudaStream_t stream) {
+// The lists of many slots: counts is workspace, `clear` words are cleared by
+// the first launch; place, and the groups of up to gt slots, when asked for.
+cudaError_t launch_lists(const int32_t *experts, int64_t P, int E, const Lists &l,
+                         int32_t *counts, int32_t *place, int gt, int unit, uint32_t *clear,
+                         int n_clear, bool pdl, cudaStream_t stream) {
   static std::atomic<unsigned long long> done{0};
-  const cudaError_t e = ensure_smem_limit(
-      lists_kernel, (kListWarps + 2) * (kMoeMaxExperts + 1) * 4, done);
+  cudaError_t e =
+      ensure_smem_limit(place_kernel, (2 + kPlaceWarps) * (kMoeMaxExperts + 1) * 4, done);
   if (e != cudaSuccess) return e;
-  return launch_pdl(lists_kernel, 1, kListWarps * 32, size_t(kListWarps + 2) * (E + 1) * 4, pdl,
-                    stream, experts, P, E, l.offsets, l.order, l.groups, l.n_groups, gt_log2);
+  const unsigned blocks = static_cast<unsigned>(ceil_div(P, kSortSlots));
+  e = launch_pdl(count_kernel, blocks, kThreads, size_t(E + 1) * 4, pdl, stream, experts, P, E,
+                 counts, clear, n_clear);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(place_kernel, blocks, kPlaceThreads, size_t(2 + kPlaceWarps) * (E + 1) * 4,
+                    pdl, stream, experts, P, E, counts, l.offsets, l.order, place, l.groups,
+                    l.n_groups, gt, unit);
 }
 
 // Slots that one block lists by itself (prep_kernel); more take the router,
@@ -845,12 +801,13 @@ Lists take_lists(Carve &c, int64_t P, int E, bool routed) {
   l.offsets = c.take<int32_t>(E + 1);
   l.order = c.take<int32_t>(P);
   l.n_groups = c.take<int32_t>(1);
-  l.groups = c.take<SlotGroup>(max_groups(P, E, 0));
+  l.groups = c.take<SlotGroup>(max_groups(P, E, 1));
   return l;
 }
 
 struct MoeSpace {
   Lists l;
+  int32_t *counts;
   uint32_t *tops, *clear;  // clear: hidden tops [P], then the counters
   float *hidden, *part;
   size_t bytes;
@@ -866,6 +823,7 @@ MoeSpace moe_space(const MoeArgs &a) {
   Carve c{a.ws};
   MoeSpace s{};
   s.l = take_lists(c, P, a.gate.E, true);
+  s.counts = P > kFewSlots ? c.take<int32_t>(count_words(P, a.gate.E)) : nullptr;
   s.tops = c.take<uint32_t>(a.M);
   s.clear = c.take<uint32_t>(moe_clear_words(a));
   s.hidden = c.take<float>(P * hidden_ld(a));
@@ -876,6 +834,7 @@ MoeSpace moe_space(const MoeArgs &a) {
 
 struct ExpertsSpace {
   Lists l;
+  int32_t *counts;
   uint32_t *tops;
   size_t bytes;
 };
@@ -884,6 +843,7 @@ ExpertsSpace experts_space(const ExpertsArgs &a) {
   Carve c{a.ws};
   ExpertsSpace s{};
   s.l = take_lists(c, P, a.w.E, false);
+  s.counts = P > kFewSlots ? c.take<int32_t>(count_words(P, a.w.E)) : nullptr;
   s.tops = c.take<uint32_t>(a.per_slot ? P : a.M);
   s.bytes = c.used;
   return s;
@@ -924,8 +884,8 @@ TileSpace tile_space(unsigned char *ws, int64_t P, const ExpertStack *const *w, 
   s.l.offsets = c.take<int32_t>(E + 1);
   s.l.order = c.take<int32_t>(P);
   s.l.n_groups = c.take<int32_t>(1);
-  s.l.groups = c.take<SlotGroup>(P / kTileSlots + E);
-  s.counts = c.take<int32_t>(ceil_div(P, kSortSlots) * (E + 1));
+  s.l.groups = c.take<SlotGroup>(max_groups(P, E, kTileSlots));
+  s.counts = c.take<int32_t>(count_words(P, E));
   s.place = c.take<int32_t>(P);
   s.clear = c.take<uint32_t>(size_t(stacks) * 2 * E);
   for (int i = 0; i < stacks; ++i)
@@ -949,17 +909,11 @@ cudaError_t launch_tile_lists(const TileSpace &s, const int32_t *experts, int64_
                               const ExpertStack *const *w, int stacks, bool pdl,
                               cudaStream_t stream) {
   const int E = w[0]->E;
-  const unsigned blocks = static_cast<unsigned>(ceil_div(P, kSortSlots));
-  cudaError_t e = launch_pdl(count_kernel, blocks, kThreads, size_t(E + 1) * 4, pdl, stream,
-                             experts, P, E, s.counts, s.clear, stacks * 2 * E);
-  if (e != cudaSuccess) return e;
-  e = launch_pdl(place_kernel, blocks, kThreads, size_t(2 + kWarps) * (E + 1) * 4, pdl, stream,
-                 experts, P, E, s.counts, s.l.offsets, s.l.order, s.place, s.l.groups,
-                 s.l.n_groups, kTileSlots);
+  const cudaError_t e = launch_lists(experts, P, E, s.l, s.counts, s.place, kTileSlots, 16,
+                                     s.clear, stacks * 2 * E, pdl, stream);
   if (e != cudaSuccess) return e;
   ScaleArgs a{};
-  a.count = stacks;
-  int64_t end = 0;
+  int most = 0;
   for (int i = 0; i < stacks; ++i) {
     a.s[i] = static_cast<const unsigned char *>(w[i]->s);
     a.bias[i] = w[i]->bias;
@@ -970,10 +924,10 @@ cudaError_t launch_tile_lists(const TileSpace &s, const int32_t *experts, int64_
     a.N16[i] = static_cast<int>(ceil_div(w[i]->N, kTileN));
     a.nb[i] = static_cast<int>(ceil_div(w[i]->K, w[i]->bs));
     a.f32[i] = w[i]->s_f32;
-    end += int64_t(E) * a.N16[i];
-    a.tiles_end[i] = end;
+    most = std::max(most, a.N16[i]);
   }
-  return launch_pdl(tile_scales_kernel, static_cast<unsigned>(ceil_div(end, kWarps)), kThreads, 0,
+  return launch_pdl(tile_scales_kernel,
+                    dim3(static_cast<unsigned>(ceil_div(most, kWarps)), E, stacks), kThreads, 0,
                     pdl, stream, a);
 }
 
@@ -1024,8 +978,8 @@ cudaError_t launch_experts_tile(const ExpertsArgs &a, cudaStream_t stream) {
   c.unscale = s.unscale;
   c.Y = static_cast<uint16_t *>(a.Y);
   c.N = a.w.N;
-  e = launch_pdl(convert_kernel, static_cast<unsigned>(a.per_slot ? P : a.M), kThreads, 0, a.pdl,
-                 stream, c);
+  e = launch_pdl(convert_kernel, static_cast<unsigned>(a.per_slot ? P : a.M), row_threads(c.Kp), 0,
+                 a.pdl, stream, c);
   if (e != cudaSuccess) return e;
   TileParams p{};
   e = fill_tile(p, kStreamProduct, w, 0, s, s.rows, P);
@@ -1061,7 +1015,7 @@ cudaError_t launch_moe_tile(const MoeArgs &a, cudaStream_t stream) {
   c.hidden = s.hidden;
   c.hidden_n = a.gate.N;
   c.hidden_ld = static_cast<int>(k_pad(a.gate.N));
-  e = launch_pdl(convert_kernel, static_cast<unsigned>(a.M), kThreads, 0, a.pdl, stream, c);
+  e = launch_pdl(convert_kernel, static_cast<unsigned>(a.M), row_threads(c.Kp), 0, a.pdl, stream, c);
   if (e != cudaSuccess) return e;
   TileParams up{}, down{};
   e = fill_tile(up, kStreamGateUp, w, 0, s, s.rows, P);
@@ -1083,7 +1037,8 @@ cudaError_t launch_moe_tile(const MoeArgs &a, cudaStream_t stream) {
   down.out_unscale = s.p_unscale;
   e = launch_tile(down, a.down.z != nullptr, a.down.s_f32, a.down.bs, a.pdl, stream);
   if (e != cudaSuccess) return e;
-  return launch_pdl(combine_half_kernel, static_cast<unsigned>(a.M), kThreads, 0, a.pdl, stream,
+  return launch_pdl(combine_half_kernel, static_cast<unsigned>(a.M), row_threads(a.down.N), 0,
+                    a.pdl, stream,
                     s.part, part_ld(a.down.N), s.p_unscale, s.place, s.l.offsets, a.gate.E, a.M, a.top_k, a.down.N,
                     static_cast<uint16_t *>(a.Y));
 }
@@ -1119,7 +1074,10 @@ void set_lists(StreamParams &p, const Lists &l) {
 
 }  // namespace
 
-size_t moe_route_workspace_bytes(int64_t, int, int) { return 0; }
+size_t moe_route_workspace_bytes(int64_t M, int E, int top_k) {
+  const int64_t P = M * top_k;
+  return P > kFewSlots ? align256(count_words(P, E) * 4) : 0;
+}
 
 cudaError_t launch_moe_route(const RouteArgs &a, cudaStream_t stream) {
   const int64_t P = a.M * a.top_k;
@@ -1144,7 +1102,8 @@ cudaError_t launch_moe_route(const RouteArgs &a, cudaStream_t stream) {
     Lists l;
     l.offsets = a.offsets;
     l.order = a.order;
-    e = launch_lists(a.experts, P, a.E, l, 0, a.pdl, stream);
+    e = launch_lists(a.experts, P, a.E, l, reinterpret_cast<int32_t *>(a.ws), nullptr, 1, 1,
+                     nullptr, 0, a.pdl, stream);
   }
   return e;
 }
@@ -1187,7 +1146,8 @@ cudaError_t launch_matmul_experts(const ExpertsArgs &a, cudaStream_t stream) {
     r.tops = s.tops;
     e = launch_prep(r, a.pdl, stream);
   } else {
-    e = launch_lists(a.experts, P, a.w.E, s.l, pl.p.gt_log2, a.pdl, stream);
+    e = launch_lists(a.experts, P, a.w.E, s.l, s.counts, nullptr, 1 << pl.p.gt_log2, 1, nullptr,
+                     0, a.pdl, stream);
     if (e == cudaSuccess)
       e = launch_row_tops(a.A, a.a_f32, vec, rows, a.w.K, s.tops, nullptr, 0, a.pdl, stream);
   }
@@ -1260,7 +1220,8 @@ cudaError_t launch_moe(const MoeArgs &a, cudaStream_t stream) {
                       s.l.experts, nullptr, nullptr, nullptr, a.pdl};
     e = launch_moe_route(r, stream);
     if (e == cudaSuccess)
-      e = launch_lists(s.l.experts, P, a.gate.E, s.l, up.p.gt_log2, a.pdl, stream);
+      e = launch_lists(s.l.experts, P, a.gate.E, s.l, s.counts, nullptr, 1 << up.p.gt_log2, 1,
+                       nullptr, 0, a.pdl, stream);
     if (e == cudaSuccess)
       e = launch_row_tops(a.X, a.a_f32, vec, a.M, a.gate.K, s.tops, s.clear, n_clear, a.pdl,
                           stream);
