@@ -88,6 +88,23 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 
+// Bounded wait that sleeps in the hardware for up to 50 us at a time: a warp
+// that polls takes issue slots from the unpacking. At most about a second.
+__device__ __forceinline__ bool mbar_sleep(uint64_t *bar, uint32_t parity) {
+  for (uint32_t i = 0; i < 20000u; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(50000u)
+        : "memory");
+    if (ok) return true;
+  }
+  return false;
+}
+
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t ok;
@@ -239,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
       const int first = __shfl_sync(0xffffffffu, sg.first, 0) + static_cast<int>(rank) * half;
       const int boxes = (half + kTileBox - 1) / kTileBox;
       for (int kb = 0; kb < p.K64; kb += kChunks, ++it) {
-        if (it >= kBStages) ok = __all_sync(0xffffffffu, mbar_wait(bempty + s, phase ^ 1));
+        if (it >= kBStages) ok = __all_sync(0xffffffffu, mbar_sleep(bempty + s, phase ^ 1));
         if (!ok) {
           if (lane == 0) record_fault(&g_fault_moe, kFaultMoeWait);
           break;
@@ -273,10 +290,10 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         const uint32_t idesc = idesc_f16(columns_of(__shfl_sync(0xffffffffu, slots, 0)));
         const uint32_t d = tmem_d + (n & 1) * kTileSlots;
         if (u + du < units) slots = p.groups[(u + du) / np].cols;
-        if (n >= 2) ok = __all_sync(0xffffffffu, mbar_wait(dempty + (n & 1), (n / 2 - 1) & 1));
+        if (n >= 2) ok = __all_sync(0xffffffffu, mbar_sleep(dempty + (n & 1), (n / 2 - 1) & 1));
         tc_fence_after();
         for (int kb = 0; kb < p.K64 && ok; kb += kChunks) {
-          ok = mbar_wait(bfull + bs, bphase) && mbar_wait(afull + as, aphase);
+          ok = mbar_sleep(bfull + bs, bphase) && mbar_sleep(afull + as, aphase);
           ok = __all_sync(0xffffffffu, ok);
           tc_fence_after();
           const uint32_t ta = tmem_a + as * (kChunks * 32);
@@ -309,14 +326,14 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
       // Every MMA issued is complete before the tensor memory is released.
       if (elect_one()) umma_commit(done, 1);
       __syncwarp();
-      if (!__all_sync(0xffffffffu, mbar_wait(done, 0)) || !ok)
+      if (!__all_sync(0xffffffffu, mbar_sleep(done, 0)) || !ok)
         if (lane == 0) record_fault(&g_fault_moe, kFaultMoeWait);
     } else if (lane == 0) {  // ---- CTA 1: tells CTA 0 that its half has landed -----------
       const uint32_t peer = cluster_addr(bfull, 0);
       int it = 0;
       for (int u = u0; u < units && ok; u += du)
         for (int kb = 0; kb < p.K64; kb += kChunks, ++it) {
-          if (!mbar_wait(bfull + it % kBStages, (it / kBStages) & 1)) {
+          if (!mbar_sleep(bfull + it % kBStages, (it / kBStages) & 1)) {
             record_fault(&g_fault_moe, kFaultMoeWait);
             ok = false;
             break;
@@ -328,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     // ---- columns ------------------------------------------------------------------
     int n = 0;
     for (int u = u0; u < units; u += du, ++n) {
-      if (n >= 2 && !mbar_wait(cempty + (n & 1), (n / 2 - 1) & 1)) {
+      if (n >= 2 && !mbar_sleep(cempty + (n & 1), (n / 2 - 1) & 1)) {
         if (lane == 0) record_fault(&g_fault_moe, kFaultMoeWait);
         break;
       }
@@ -523,10 +540,9 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         };
         // Both chunks without a branch: their instructions interleave. (A lone
         // last chunk's partner is whatever the stage held, and is not stored.)
-        uint32_t r0[16], r1[16];
+        uint32_t r0[16];
         unpack(0, r0);
-        unpack(1, r1);
-        if (use > 0 && !mbar_wait(aempty + grp, (use - 1) & 1)) {
+        if (use > 0 && !mbar_sleep(aempty + grp, (use - 1) & 1)) {
           record_fault(&g_fault_moe, kFaultMoeWait);
           ok = false;
           break;
@@ -535,7 +551,10 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         const uint32_t ta = tmem_a + grp * (kChunks * 32) +
                             (static_cast<uint32_t>(32 * quarter + 16 * half) << 16);
         tmem_st_16x64(ta, r0);
-        if (j * kChunks + 1 < p.K64) tmem_st_16x64(ta + 32, r1);
+        if (j * kChunks + 1 < p.K64) {
+          unpack(1, r0);
+          tmem_st_16x64(ta + 32, r0);
+        }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -565,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
       const float bias =
           p.w[m].bias && live ? p.w[m].bias[int64_t(sg.e) * p.N + row] : 0.f;
       const uint32_t d = tmem_d + (n & 1) * kTileSlots + (static_cast<uint32_t>(32 * quarter) << 16);
-      if (!mbar_wait(cfull + (n & 1), (n / 2) & 1) || !mbar_wait(dfull + (n & 1), (n / 2) & 1)) {
+      if (!mbar_sleep(cfull + (n & 1), (n / 2) & 1) || !mbar_sleep(dfull + (n & 1), (n / 2) & 1)) {
         record_fault(&g_fault_moe, kFaultMoeWait);
         break;
       }
