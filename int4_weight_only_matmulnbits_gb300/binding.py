@@ -788,10 +788,11 @@ def _call_on(device: torch.device, stream, call):
     device's current one. The caller orders `stream` with the work that made
     the inputs and that reads the outputs."""
     if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(device.index)
         if device.index == torch.cuda.current_device():  # nothing to switch
-            return call(torch.cuda.current_stream().cuda_stream)
+            return call(raw)
         with torch.cuda.device(device):
-            return call(torch.cuda.current_stream().cuda_stream)
+            return call(raw)
     if stream.device != device:
         raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
     with torch.cuda.device(device), torch.cuda.stream(stream):
@@ -809,21 +810,24 @@ def _workspace(n: int, device: torch.device):
 
 
 def _experts_struct(w: PackedExperts, bias: torch.Tensor | None, device) -> ExpertsC:
-    """mnb_experts of w; the struct of the last bias is kept with w."""
-    key = (None if bias is None else bias.data_ptr(), device)
-    kept = w.__dict__.get("_struct")
-    if bias is None and kept is not None and kept[0] == key:
-        return kept[1]
-    _on_gpu("packed_b", w.packed_b, device)
-    if bias is not None:
-        _on_gpu("bias", bias, device)
-        if bias.dtype != torch.float32 or bias.shape != (w.E, w.N):
-            raise ValueError(f"bias must be an fp32 [{w.E}, {w.N}] tensor")
-    ptr = lambda t: None if t is None else t.data_ptr()
-    c = ExpertsC(w.packed_b.data_ptr(), w.packed_scales.data_ptr(), ptr(w.packed_zp), ptr(bias),
-                 w.E, w.N, w.K, w.block_size, _dtype_code(w.scale_dtype))
+    """mnb_experts of w and a bias. The struct without a bias is made once for
+    w's buffers and never changed; one with a bias is a copy of it."""
+    pb = w.packed_b.data_ptr()
+    c = w.__dict__.get("_struct")
+    if c is None or c.packed_b != pb:
+        ptr = lambda t: None if t is None else t.data_ptr()
+        c = ExpertsC(pb, w.packed_scales.data_ptr(), ptr(w.packed_zp), None, w.E, w.N, w.K,
+                     w.block_size, _dtype_code(w.scale_dtype))
+        w.__dict__["_struct"] = c
+    if w.packed_b.device != device:
+        raise ValueError(f"the weights are on {w.packed_b.device}, the call runs on {device}")
     if bias is None:
-        w.__dict__["_struct"] = (key, c)
+        return c
+    _on_gpu("bias", bias, device)
+    if bias.dtype != torch.float32 or bias.shape != (w.E, w.N):
+        raise ValueError(f"bias must be an fp32 [{w.E}, {w.N}] tensor")
+    c = ExpertsC.from_buffer_copy(c)
+    c.bias = bias.data_ptr()
     return c
 
 
