@@ -573,20 +573,42 @@ __global__ void __launch_bounds__(1024)
   }
 }
 
-// Sum of each token's down partials, in slot order (long inputs).
-__global__ void __launch_bounds__(kThreads)
-    combine_kernel(const float *part, const int32_t *experts, int64_t M, int top_k, int N,
-                   void *Y, bool f32) {
+// Sum of each token's fp32 partials, in slot order: a block per token, eight
+// slots' loads at a time.
+__global__ void __launch_bounds__(1024)
+    combine_kernel(const float *part, const int32_t *experts, int top_k, int N, void *Y,
+                   bool f32) {
   grid_dependency_wait();
   grid_dependents_launch();
-  const int64_t total = M * N;
-  for (int64_t i = blockIdx.x * int64_t(kThreads) + threadIdx.x; i < total;
-       i += int64_t(gridDim.x) * kThreads) {
-    const int64_t m = i / N;
-    float y = 0.f;
-    for (int j = 0; j < top_k; ++j)
-      if (experts[m * top_k + j] >= 0) y += part[(m * top_k + j) * N + (i - m * N)];
-    store_f(Y, f32, i, y);
+  const int64_t m = blockIdx.x, q0 = m * top_k;
+  const bool vec = N % 4 == 0;  // rows of partials start on 16 bytes
+  for (int n = threadIdx.x * 4; n < N; n += blockDim.x * 4) {
+    float y[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int j0 = 0; j0 < top_k; j0 += 8) {
+      float v[8][4];
+      bool some[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        some[j] = j0 + j < top_k && experts[q0 + j0 + j] >= 0;
+        if (j0 + j >= top_k) continue;
+        const float *src = part + (q0 + j0 + j) * N + n;
+        if (vec) {
+          const float4 x = *reinterpret_cast<const float4 *>(src);
+          v[j][0] = x.x; v[j][1] = x.y; v[j][2] = x.z; v[j][3] = x.w;
+        } else {
+#pragma unroll
+          for (int o = 0; o < 4; ++o) v[j][o] = n + o < N ? src[o] : 0.f;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (some[j])
+#pragma unroll
+          for (int o = 0; o < 4; ++o) y[o] += v[j][o];
+    }
+#pragma unroll
+    for (int o = 0; o < 4; ++o)
+      if (n + o < N) store_f(Y, f32, m * N + n + o, y[o]);
   }
 }
 
@@ -1249,12 +1271,19 @@ cudaError_t launch_moe(const MoeArgs &a, cudaStream_t stream) {
   down.p.part = s.part;
   down.p.Y = a.Y;
   down.p.y_f32 = a.a_f32;
-  down.p.counters = few ? s.clear + P : nullptr;
+  // One token: whoever completes a column range adds its partials (moe_one
+  // ... us, with the launch that follows ... us). More: the last steps are
+  // all of one group, so a few CTAs would do all of the adding (16 tokens
+  // of 8 out of 128 experts: 100 us, with a launch of its own ... us).
+  const bool join = a.M == 1;
+  down.p.counters = join ? s.clear + P : nullptr;
   down.p.early = a.pdl;
   e = run_stream(down, a.pdl, stream);
-  if (e != cudaSuccess || few) return e;
-  return launch_pdl(combine_kernel, grid_of(a.M * a.down.N, kThreads), kThreads, 0, a.pdl,
-                    stream, s.part, s.l.experts, a.M, a.top_k, a.down.N, a.Y, a.a_f32);
+  if (e != cudaSuccess || join) return e;
+  const int threads =
+      static_cast<int>(std::min<int64_t>(1024, ceil_div(ceil_div(a.down.N, 4), 32) * 32));
+  return launch_pdl(combine_kernel, static_cast<unsigned>(a.M), threads, 0, a.pdl, stream, s.part,
+                    s.l.experts, a.top_k, a.down.N, a.Y, a.a_f32);
 }
 
 }  // namespace mnb

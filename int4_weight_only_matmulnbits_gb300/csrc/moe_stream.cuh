@@ -135,48 +135,56 @@ __global__ void __launch_bounds__(kThreads, kStreamCtas) stream_kernel(const Str
   Cursor cur = pre;
   while (pre.step < hi && !has_pair(pre)) next_step(pre);
 
-  // Sources of the pair being fetched, from the start of its k; lane l copies
-  // the 16-byte pieces l of the codes of a chunk, and of a stage's scales and
-  // zero points (at most 32 each).
+  // Sources of the next stage; lane l copies the 16-byte pieces l of the
+  // codes of a chunk, and of a stage's scales and zero points (at most 32).
   const uint4 *fw[2];
   const unsigned char *fs[2], *fz[2];
-  auto aim = [&] {
-#pragma unroll
-    for (int mat = 0; mat < 2; ++mat) {
-      const int64_t tile = int64_t(pre.e) * p.N16 + tile_of(pre.nstep * p.tpu + tl, mat);
-      fw[mat] = p.w[mat].b + tile * p.K64 * 32 + lane;
-      fs[mat] = p.w[mat].s + tile * p.nb * (kTileN * kEs) + lane * 16;
-      if (ZP) fz[mat] = p.w[mat].z + tile * p.nbz * 8 + lane * 16;
-    }
-  };
   // First block of the stage at chunk c, and the one past its last.
   auto block_lo = [&](int c) { return SPB == 4 ? (c * kChunkK) >> p.bs_log2 : c * kBlocks; };
   auto block_hi = [&](int c) {
     return SPB == 4 ? ((c * kChunkK - 1) >> p.bs_log2) + 1 : c * kBlocks;
   };
+  auto aim = [&] {
+#pragma unroll
+    for (int mat = 0; mat < 2; ++mat) {
+      const int64_t tile = int64_t(pre.e) * p.N16 + tile_of(pre.nstep * p.tpu + tl, mat);
+      fw[mat] = p.w[mat].b + (tile * p.K64 + c0) * 32 + lane;
+      // Blocks of 64 and more codes: from the tile's start on.
+      fs[mat] = p.w[mat].s + (tile * p.nb + (SPB == 4 ? 0 : c0 * kBlocks)) * (kTileN * kEs) +
+                lane * 16;
+      if (ZP) fz[mat] = p.w[mat].z + tile * p.nbz * 8 + lane * 16;
+    }
+  };
   if (pre.step < hi) aim();
-  auto fetch = [&](int slot) {
+  uint32_t fdst = ring_u + lane * 16;
+  auto fetch = [&] {
     if (pre.step < hi) {
-      const int c = pre.c, n = min(kChunks, c1 - c);
-      const int b0 = block_lo(c), need = block_hi(c + n), b1 = min(p.nb, need);
+      const int c = pre.c, b0 = block_lo(c);
+      const bool two = c + 1 < c1;
+      const int need = SPB == 4 ? block_hi(c + (two ? 2 : 1)) - b0 : (two ? 2 : 1) * kBlocks;
+      const int have = min(p.nb - b0, need);
 #pragma unroll
       for (int mat = 0; mat < 2; ++mat) {
-        const uint32_t dst = ring_u + slot * p.st_bytes + mat * p.st_tile + lane * 16;
-        const uint4 *src = fw[mat] + c * 32;
-#pragma unroll
-        for (int i = 0; i < kChunks; ++i)
-          if (i < n) cp16(dst + i * kChunkBytes, src + i * 32);
-        if (lane < (b1 - b0) * kEs)
-          cp16(dst + p.st_scale, fs[mat] + b0 * (kTileN * kEs));
+        const uint32_t dst = fdst + mat * p.st_tile;
+        cp16(dst, fw[mat]);
+        if (two) cp16(dst + kChunkBytes, fw[mat] + 32);
+        if (lane < have * kEs)
+          cp16(dst + p.st_scale, SPB == 4 ? fs[mat] + b0 * (kTileN * kEs) : fs[mat]);
         if (ZP)  // pairs of words from an even block on
-          if (lane < (b1 + 1) / 2 - b0 / 2) cp16(dst + p.st_zp, fz[mat] + (b0 / 2) * 16);
+          if (lane < (b0 + have + 1) / 2 - b0 / 2) cp16(dst + p.st_zp, fz[mat] + (b0 / 2) * 16);
+        fw[mat] += kChunks * 32;
+        if (SPB < 4) fs[mat] += kChunks * kBlocks * (kTileN * kEs);
       }
       // Blocks past the last hold only k >= K, whose activations are zero;
       // their scales are zeros, so that nothing stale meets them.
-      if (b1 < need && lane >= (b1 - b0) * kEs && lane < (need - b0) * kEs)
+      if (have < need && lane >= have * kEs && lane < need * kEs)
         for (int mat = 0; mat < 2; ++mat)
-          *reinterpret_cast<uint4 *>(ring + slot * p.st_bytes + mat * p.st_tile + p.st_scale +
-                                     lane * 16) = make_uint4(0, 0, 0, 0);
+          asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(fdst + mat * p.st_tile +
+                                                                      p.st_scale),
+                       "r"(0)
+                       : "memory");
+      fdst += p.st_bytes;
+      if (fdst == ring_u + lane * 16 + kStages * p.st_bytes) fdst = ring_u + lane * 16;
       pre.c = c + kChunks;
       if (pre.c >= c1) {
         pre.c = c0;
@@ -188,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, kStreamCtas) stream_kernel(const Str
     cp_commit();
   };
 #pragma unroll 1
-  for (int i = 0; i < kStages - 1; ++i) fetch(i);
+  for (int i = 0; i < kStages - 1; ++i) fetch();
 
   if (p.early) grid_dependency_wait();
   // Rows that no step writes: slots without an expert (product), every token
@@ -280,17 +288,17 @@ __global__ void __launch_bounds__(kThreads, kStreamCtas) stream_kernel(const Str
       for (int c = c0; c < c1; c += kChunks) {
         cp_wait<kStages - 2>();
         __syncwarp();  // the stage is there, and every lane is done with the one before
-        fetch(slot == 0 ? kStages - 1 : slot - 1);
+        fetch();
         const unsigned char *st = ring + slot * p.st_bytes;
-        const unsigned char *wp = st + lane * 16;
-        const int n = min(kChunks, c1 - c);
         const int b0 = block_lo(c);
         const unsigned char *sc = st + p.st_scale + g * kEs;
         const unsigned char *sz = st + p.st_zp + (b0 & 1) * 8;
-        const uint16_t *xk = xrow + c * kChunkK;
-        const float4 *sk = sums + c * (kBlocks * 4) + t;
-#pragma unroll 1
-        for (int i = 0; i < n; ++i, wp += kChunkBytes, xk += kChunkK, sk += kBlocks * 4) {
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+          if (i > 0 && c + i >= c1) break;
+          const unsigned char *wp = st + lane * 16 + i * kChunkBytes;
+          const uint16_t *xk = xrow + (c + i) * kChunkK;
+          const float4 *sk = sums + (c + i) * (kBlocks * 4) + t;
           uint32_t wv[2][4];
 #pragma unroll
           for (int mat = 0; mat < 2; ++mat) {
@@ -468,10 +476,20 @@ __global__ void __launch_bounds__(kThreads, kStreamCtas) stream_kernel(const Str
         for (int i = alone ? lane : tid; i < p.M << rows_log2; i += alone ? 32 : kThreads) {
           const int m = i >> rows_log2, n = n0 + (i & (rows - 1));
           if (n >= p.N) continue;
+          // Eight slots' loads at a time, added in order.
           float y = 0.f;
-          for (int j = 0; j < p.top_k; ++j) {
-            const int q = m * p.top_k + j;
-            if (p.experts[q] >= 0) y += __ldcg(p.part + int64_t(q) * p.N + n);
+          for (int j0 = 0; j0 < p.top_k; j0 += 8) {
+            const int64_t q = int64_t(m) * p.top_k + j0;
+            float v[8];
+            bool some[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              some[j] = j0 + j < p.top_k && p.experts[q + j] >= 0;
+              v[j] = j0 + j < p.top_k ? __ldcg(p.part + (q + j) * p.N + n) : 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (some[j]) y += v[j];
           }
           store(int64_t(m) * p.N + n, y);
         }
