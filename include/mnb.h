@@ -750,6 +750,7 @@ typedef struct {
   const void *packed_b;      /* from mnb_prepack_experts                      */
   const void *packed_scales;
   const void *packed_zp;     /* NULL: every zero point is 8                   */
+  const float *packed_rows;  /* [E * Np + E] from mnb_prepack_experts         */
   const float *bias;         /* [E, N] fp32 or NULL                           */
   int64_t E, N, K;
   int32_t block_size;
@@ -764,14 +765,17 @@ typedef struct {
  * ordinary packed weight of E * Np rows, Np = N rounded up to a multiple of
  * 16: its buffers have the sizes mnb_prepacked_sizes(E * Np, K, ...) gives
  * and its header says so (for N % 16 == 0 the bytes are those of mnb_prepack
- * on the E * N rows). Arguments and errors as mnb_prepack; MNB_ERR_SHAPE
- * also for E < 1 and when E * Np passes 2^31 - 1.
+ * on the E * N rows). packed_rows (fp32 [E * Np + E], 16-byte aligned)
+ * receives, for each packed row, the power of two that brings its largest
+ * |scale| into 2^14 .. 2^15, then each expert's largest |scale|. Arguments
+ * and errors as mnb_prepack; MNB_ERR_SHAPE also for E < 1 and when E * Np
+ * passes 2^31 - 1.
  */
 MNB_API mnb_status mnb_prepack_experts(const uint8_t *B, const void *scales,
                                        const uint8_t *zero_points, int64_t E, int64_t N,
                                        int64_t K, int block_size, mnb_dtype scale_dtype,
                                        void *packed_b, void *packed_scales, void *packed_zp,
-                                       mnb_stream_t stream);
+                                       float *packed_rows, mnb_stream_t stream);
 
 /*
  * Top-k softmax router. For each row l of logits [M, E] (fp32 or bf16) the

@@ -95,8 +95,8 @@ class ChainInfoC(ctypes.Structure):
 class ExpertsC(ctypes.Structure):
     """mnb_experts (include/mnb.h)."""
     _fields_ = [("packed_b", ctypes.c_void_p), ("packed_scales", ctypes.c_void_p),
-                ("packed_zp", ctypes.c_void_p), ("bias", ctypes.c_void_p),
-                ("E", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
+                ("packed_zp", ctypes.c_void_p), ("packed_rows", ctypes.c_void_p),
+                ("bias", ctypes.c_void_p), ("E", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
                 ("block_size", ctypes.c_int32), ("scale_dtype", ctypes.c_int32)]
 
 
@@ -209,7 +209,7 @@ def load(build_if_missing: bool = False):
         lib.mnb_matmul_bnb4.argtypes = [p, p, p, p, p, i64, i64, i64, i32, p, i32, i32, p]
         lib.mnb_matmul_bnb4.restype = i32
         e = ctypes.POINTER(ExpertsC)
-        lib.mnb_prepack_experts.argtypes = [p, p, p, i64, i64, i64, i32, i32, p, p, p, p]
+        lib.mnb_prepack_experts.argtypes = [p, p, p, i64, i64, i64, i32, i32, p, p, p, p, p]
         lib.mnb_prepack_experts.restype = i32
         lib.mnb_moe_route_workspace_size.argtypes = [i64, i64, i32]
         lib.mnb_moe_route_workspace_size.restype = sz
@@ -755,6 +755,7 @@ class PackedExperts:
     packed_b: torch.Tensor
     packed_scales: torch.Tensor
     packed_zp: torch.Tensor | None
+    packed_rows: torch.Tensor
     E: int
     N: int
     K: int
@@ -763,7 +764,8 @@ class PackedExperts:
 
     def nbytes(self) -> int:
         return sum(t.numel() * t.element_size() for t in
-                   (self.packed_b, self.packed_scales, self.packed_zp) if t is not None)
+                   (self.packed_b, self.packed_scales, self.packed_zp, self.packed_rows)
+                   if t is not None)
 
 
 class MoeRouting(NamedTuple):
@@ -816,8 +818,8 @@ def _experts_struct(w: PackedExperts, bias: torch.Tensor | None, device) -> Expe
     c = w.__dict__.get("_struct")
     if c is None or c.packed_b != pb:
         ptr = lambda t: None if t is None else t.data_ptr()
-        c = ExpertsC(pb, w.packed_scales.data_ptr(), ptr(w.packed_zp), None, w.E, w.N, w.K,
-                     w.block_size, _dtype_code(w.scale_dtype))
+        c = ExpertsC(pb, w.packed_scales.data_ptr(), ptr(w.packed_zp), w.packed_rows.data_ptr(),
+                     None, w.E, w.N, w.K, w.block_size, _dtype_code(w.scale_dtype))
         w.__dict__["_struct"] = c
     if w.packed_b.device != device:
         raise ValueError(f"the weights are on {w.packed_b.device}, the call runs on {device}")
@@ -845,17 +847,19 @@ def mnb_prepack_experts(B: torch.Tensor, scales: torch.Tensor,
             if t.shape != shape or (name != "scales" and t.dtype != torch.uint8):
                 raise ValueError(f"{name} must have the shape {shape}"
                                  + ("" if name == "scales" else " and uint8 elements"))
-    sb, ss, sz = mnb_prepacked_sizes(E * (-(-N // 16) * 16), K, block_size, scales.dtype,
-                                     zero_points is not None)
+    rows = E * (-(-N // 16) * 16)
+    sb, ss, sz = mnb_prepacked_sizes(rows, K, block_size, scales.dtype, zero_points is not None)
 
     def call(s):
         pb, ps = (torch.empty(n, dtype=torch.uint8, device=B.device) for n in (sb, ss))
         pz = (torch.empty(sz, dtype=torch.uint8, device=B.device)
               if zero_points is not None else None)
+        pr = torch.empty(rows + E, dtype=torch.float32, device=B.device)
         _check(load().mnb_prepack_experts(_ptr(B), _ptr(scales), _ptr(zero_points), E, N, K,
                                           block_size, _dtype_code(scales.dtype), _ptr(pb),
-                                          _ptr(ps), _ptr(pz), s), "mnb_prepack_experts")
-        return PackedExperts(pb, ps, pz, E, N, K, block_size, scales.dtype)
+                                          _ptr(ps), _ptr(pz), _ptr(pr), s),
+               "mnb_prepack_experts")
+        return PackedExperts(pb, ps, pz, pr, E, N, K, block_size, scales.dtype)
     return _call_on(B.device, stream, call)
 
 

@@ -341,11 +341,11 @@ mnb_status check_stack_shape(const mnb_experts &w) {
 }
 
 mnb_status check_stack(const mnb_experts &w) {
-  if (!w.packed_b || !w.packed_scales) return MNB_ERR_NULL;
+  if (!w.packed_b || !w.packed_scales || !w.packed_rows) return MNB_ERR_NULL;
   const mnb_status st = check_stack_shape(w);
   if (st != MNB_OK) return st;
   if (!aligned(w.packed_b, 16) || !aligned(w.packed_scales, 16) || !aligned(w.packed_zp, 16) ||
-      !aligned(w.bias, 4))
+      !aligned(w.packed_rows, 16) || !aligned(w.bias, 4))
     return MNB_ERR_ALIGN;
   return MNB_OK;
 }
@@ -393,7 +393,7 @@ mnb_status check_disjoint(const Range *outs, int n_outs, const Range *ins, int n
 }
 
 struct StackRanges {
-  Range r[4];
+  Range r[5];
   explicit StackRanges(const mnb_experts &w) {
     const Sizes s = packed_sizes(w.E * padded_rows(w.N), w.K, w.block_size, w.scale_dtype,
                                  w.packed_zp != nullptr);
@@ -401,6 +401,7 @@ struct StackRanges {
     r[1] = {w.packed_scales, s.s};
     r[2] = {w.packed_zp, s.z};
     r[3] = {w.bias, w.bias ? size_t(w.E) * w.N * 4 : 0};
+    r[4] = {w.packed_rows, size_t(w.E * padded_rows(w.N) + w.E) * 4};
   }
 };
 
@@ -417,7 +418,7 @@ mnb_status check_workspace(const void *ws, size_t bytes, size_t need) {
 }
 
 ExpertStack expert_stack(const mnb_experts &w) {
-  return ExpertStack{w.packed_b, w.packed_scales, w.packed_zp, w.bias,
+  return ExpertStack{w.packed_b, w.packed_scales, w.packed_zp, w.packed_rows, w.bias,
                      static_cast<int>(w.E), static_cast<int>(w.N), static_cast<int>(w.K),
                      w.block_size, w.scale_dtype == MNB_F32};
 }
@@ -1374,13 +1375,14 @@ mnb_status mnb_chain_run_noalloc(const mnb_chain_op *ops, int32_t n_ops, int64_t
 // ---- mixture of experts ------------------------------------------------------
 
 static_assert(MNB_MOE_MAX_EXPERTS == kMoeMaxExperts && MNB_MOE_MAX_TOP_K == kMoeMaxTopK, "");
-static_assert(sizeof(mnb_experts) == 64, "mnb_experts layout");
+static_assert(sizeof(mnb_experts) == 72, "mnb_experts layout");
 
 mnb_status mnb_prepack_experts(const uint8_t *B, const void *scales,
                                const uint8_t *zero_points, int64_t E, int64_t N, int64_t K,
                                int block_size, mnb_dtype scale_dtype, void *packed_b,
-                               void *packed_scales, void *packed_zp, mnb_stream_t stream) {
-  if (!B || !scales || !packed_b || !packed_scales) return MNB_ERR_NULL;
+                               void *packed_scales, void *packed_zp, float *packed_rows,
+                               mnb_stream_t stream) {
+  if (!B || !scales || !packed_b || !packed_scales || !packed_rows) return MNB_ERR_NULL;
   if (zero_points && !packed_zp) return MNB_ERR_NULL;
   mnb_status st = check_shape(N, K, block_size, scale_dtype);
   if (st != MNB_OK) return st;
@@ -1388,25 +1390,26 @@ mnb_status mnb_prepack_experts(const uint8_t *B, const void *scales,
   const int64_t rows = E * padded_rows(N);
   st = check_shape(rows, K, block_size, scale_dtype);
   if (st != MNB_OK) return st;
-  if (!aligned(packed_b, 16) || !aligned(packed_scales, 16) ||
+  if (!aligned(packed_b, 16) || !aligned(packed_scales, 16) || !aligned(packed_rows, 16) ||
       (zero_points && !aligned(packed_zp, 16)) ||
       !aligned(scales, dtype_size(scale_dtype)))
     return MNB_ERR_ALIGN;
   const int64_t nb = ceil_div(K, block_size);
   const Sizes out = packed_sizes(rows, K, block_size, scale_dtype, zero_points != nullptr);
-  const void *const ins[3] = {B, scales, zero_points};
-  const size_t in_n[3] = {size_t(E) * N * nb * (block_size / 2),
-                          size_t(E) * N * nb * dtype_size(scale_dtype),
-                          zero_points ? size_t(E) * N * ((nb + 1) / 2) : 0};
-  void *const outs[3] = {packed_b, packed_scales, zero_points ? packed_zp : nullptr};
-  const size_t out_n[3] = {out.b, out.s, out.z};
-  st = check_outputs_disjoint(outs, out_n, ins, in_n);
+  const Range ins[] = {{B, size_t(E) * N * nb * (block_size / 2)},
+                       {scales, size_t(E) * N * nb * dtype_size(scale_dtype)},
+                       {zero_points, zero_points ? size_t(E) * N * ((nb + 1) / 2) : 0}};
+  const Range outs[] = {{packed_b, out.b}, {packed_scales, out.s},
+                        {zero_points ? packed_zp : nullptr, out.z},
+                        {packed_rows, size_t(rows + E) * 4}};
+  st = check_disjoint(outs, 4, ins, 3);
   if (st != MNB_OK) return st;
   st = check_device();
   if (st != MNB_OK) return st;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const ExpertPackArgs a{B, scales, zero_points, E, N, K, block_size,
-                         scale_dtype == MNB_F32, packed_b, packed_scales, packed_zp};
+                         scale_dtype == MNB_F32, packed_b, packed_scales, packed_zp,
+                         packed_rows};
   const mnb_packed_header h = make_header(rows, K, block_size, scale_dtype,
                                           zero_points != nullptr, MNB_CODES_AFFINE);
   cudaError_t e = launch_prepack_experts(a, s);
@@ -1482,8 +1485,8 @@ mnb_status mnb_matmul_experts(const void *A, int a_per_slot, const mnb_experts *
   const StackRanges sr(*w);
   const Range outs[] = {{Y, P * w->N * es}, {workspace, need}};
   const Range ins[] = {{A, (a_per_slot ? P : size_t(M)) * w->K * es}, {experts, P * 4},
-                       sr.r[0], sr.r[1], sr.r[2], sr.r[3]};
-  st = check_disjoint(outs, 2, ins, 6);
+                       sr.r[0], sr.r[1], sr.r[2], sr.r[3], sr.r[4]};
+  st = check_disjoint(outs, 2, ins, 7);
   if (st == MNB_OK) st = check_stack_layout(*w);
   if (st == MNB_OK) st = check_device();
   if (st != MNB_OK) return st;
@@ -1528,9 +1531,10 @@ mnb_status mnb_moe(const void *X, const void *logits, mnb_dtype logits_dtype, in
   const size_t xy = size_t(M) * gate->K * es;
   const Range outs[] = {{Y, xy}, {workspace, need}};
   const Range ins[] = {{X, xy}, {logits, size_t(M) * gate->E * dtype_size(logits_dtype)},
-                       sg.r[0], sg.r[1], sg.r[2], sg.r[3], su.r[0], su.r[1], su.r[2],
-                       su.r[3], sd.r[0], sd.r[1], sd.r[2], sd.r[3]};
-  st = check_disjoint(outs, 2, ins, 14);
+                       sg.r[0], sg.r[1], sg.r[2], sg.r[3], sg.r[4], su.r[0], su.r[1],
+                       su.r[2], su.r[3], su.r[4], sd.r[0], sd.r[1], sd.r[2], sd.r[3],
+                       sd.r[4]};
+  st = check_disjoint(outs, 2, ins, 17);
   for (const mnb_experts *w : {gate, up, down})
     if (st == MNB_OK) st = check_stack_layout(*w);
   if (st == MNB_OK) st = check_device();

@@ -97,6 +97,29 @@ __global__ void pack_expert_zp_kernel(const uint8_t *__restrict__ zp,
   }
 }
 
+// Per packed row: the power of two that brings its largest |scale| into
+// 2^14 .. 2^15; per expert: the largest |scale| (bits, cleared before). A warp
+// per 16-row tile.
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+    row_scales_kernel(const T *__restrict__ s, float *__restrict__ rows, uint32_t *smax, int64_t E,
+                      int64_t N16, int64_t nb) {
+  const int lane = threadIdx.x & 31, r = lane & 15;
+  for (int64_t tile = blockIdx.x * int64_t(kWarps) + (threadIdx.x >> 5); tile < E * N16;
+       tile += int64_t(gridDim.x) * kWarps) {
+    uint32_t top = 0;
+    for (int64_t b = lane >> 4; b < nb; b += 2) {
+      const T v = s[(tile * nb + b) * kTileN + r];
+      const uint32_t u = sizeof(T) == 4 ? __float_as_uint(v) : uint32_t(v) << 16;
+      top = max(top, u & 0x7FFFFFFFu);
+    }
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));
+    if (lane < 16) rows[tile * kTileN + r] = exp2i(row_shift(top));
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (lane == 0) atomicMax(smax + tile / N16, top);
+  }
+}
+
 inline unsigned grid_of(int64_t total, int per) {
   return static_cast<unsigned>(
       std::max<int64_t>(1, std::min<int64_t>(ceil_div(total, per), 1 << 20)));
@@ -248,14 +271,11 @@ __global__ void __launch_bounds__(kThreads)
 // without an expert count as expert E).
 constexpr int kSortSlots = 1024;
 __global__ void __launch_bounds__(kThreads)
-    count_kernel(const int32_t *experts, int64_t P, int E, int32_t *counts, uint32_t *clear,
-                 int n_clear) {
+    count_kernel(const int32_t *experts, int64_t P, int E, int32_t *counts) {
   extern __shared__ int32_t cnt[];  // [E + 1]
   for (int i = threadIdx.x; i <= E; i += kThreads) cnt[i] = 0;
   grid_dependency_wait();
   grid_dependents_launch();
-  if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i < n_clear; i += kThreads) clear[i] = 0;
   __syncthreads();
   const int64_t lo = int64_t(blockIdx.x) * kSortSlots;
   const int n = static_cast<int>(P - lo < kSortSlots ? P - lo : kSortSlots);
@@ -467,69 +487,27 @@ __global__ void __launch_bounds__(1024) convert_kernel(const ConvertArgs a) {
   }
 }
 
-// Per packed row of a stack: the power of two that brings its largest |scale|
-// into 2^14 .. 2^15; per expert: the bits of the largest |scale| and |bias|
-// (cleared before). A warp per 16-row tile; the tile's scales are contiguous
-// and go by 16-byte pieces, whose rows depend on the lane alone.
-struct ScaleArgs {
-  const unsigned char *s[3];
+// Largest |bias| of each expert of up to three stacks: blockIdx (expert, stack).
+struct BiasArgs {
   const float *bias[3];
-  float *fac[3];
-  uint32_t *smax[3], *bmax[3];
-  int N[3], N16[3], nb[3], f32[3];
+  float *bmax[3];
+  int N[3];
 };
-// blockIdx: (tiles of an expert, expert, stack).
-__global__ void __launch_bounds__(kThreads) tile_scales_kernel(const ScaleArgs a) {
-  const int lane = threadIdx.x & 31, i = blockIdx.z, e = blockIdx.y;
-  const int nt = blockIdx.x * kWarps + (threadIdx.x >> 5);
+__global__ void __launch_bounds__(kThreads) bias_max_kernel(const BiasArgs a) {
+  __shared__ uint32_t scratch[kWarps];
+  const int e = blockIdx.x, i = blockIdx.y;
   grid_dependency_wait();
   grid_dependents_launch();
-  if (nt >= a.N16[i]) return;
-  const bool f32 = a.f32[i];
-  const int64_t tile = int64_t(e) * a.N16[i] + nt;
-  const int n = nt * kTileN + lane;
-  uint32_t b = 0;
-  if (a.bias[i] && lane < kTileN && n < a.N[i])
-    b = __float_as_uint(a.bias[i][int64_t(e) * a.N[i] + n]) & 0x7FFFFFFFu;
-  const int per = f32 ? 4 : 8;  // scales per piece
-  const int pieces = a.nb[i] * 16 / per;
-  const uint4 *src =
-      reinterpret_cast<const uint4 *>(a.s[i] + tile * a.nb[i] * (16 * (f32 ? 4 : 2)));
-  // fp32: a word per row; bf16: two rows to a word.
-  uint32_t top[4] = {0, 0, 0, 0};
-#pragma unroll 4
-  for (int q = lane; q < pieces; q += 32) {
-    const uint4 x = src[q];
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int o = 0; o < 4; ++o)
-      top[o] = f32 ? max(top[o], w[o] & 0x7FFFFFFFu) : __vmaxu2(top[o], w[o] & 0x7FFF7FFFu);
-  }
-  // Lanes with the same piece of a block: equal modulo 2 (bf16) or 4 (fp32).
-#pragma unroll
-  for (int o = 2; o < 32; o <<= 1)
-    if (o >= 4 || !f32)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const uint32_t v = __shfl_xor_sync(0xffffffffu, top[r], o);
-        top[r] = f32 ? max(top[r], v) : __vmaxu2(top[r], v);
-      }
-  uint32_t most = 0;
-  float *fac = a.fac[i] + tile * kTileN + lane * per;
-#pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const uint32_t t0 = f32 ? top[r] : top[r] << 16, t1 = f32 ? 0 : top[r] & 0xFFFF0000u;
-    most = max(most, max(t0, t1));
-    if (lane < 16 / per) {
-      fac[f32 ? r : 2 * r] = exp2i(row_shift(t0));
-      if (!f32) fac[2 * r + 1] = exp2i(row_shift(t1));
-    }
-  }
-  most = __reduce_max_sync(0xffffffffu, most);
-  b = __reduce_max_sync(0xffffffffu, b);
-  if (lane == 0) {
-    atomicMax(a.smax[i] + e, most);
-    if (b) atomicMax(a.bmax[i] + e, b);
+  if (!a.bias[i]) return;
+  uint32_t top = 0;
+  for (int n = threadIdx.x; n < a.N[i]; n += kThreads)
+    top = max(top, __float_as_uint(a.bias[i][int64_t(e) * a.N[i] + n]) & 0x7FFFFFFFu);
+  top = __reduce_max_sync(0xffffffffu, top);
+  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = top;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 0; w < kWarps; ++w) top = max(top, scratch[w]);
+    a.bmax[i][e] = __uint_as_float(top);
   }
 }
 
@@ -650,6 +628,15 @@ cudaError_t launch_prepack_experts(const ExpertPackArgs &a, cudaStream_t stream)
   if (a.zp)
     pack_expert_zp_kernel<<<grid_of(tiles * nbz, 256), 256, 0, stream>>>(
         a.zp, static_cast<uint64_t *>(a.packed_zp), a.N, Np, nb, nbz, tiles * nbz);
+  uint32_t *smax = reinterpret_cast<uint32_t *>(a.packed_rows + a.E * Np);
+  const cudaError_t e = cudaMemsetAsync(smax, 0, size_t(a.E) * 4, stream);
+  if (e != cudaSuccess) return e;
+  if (a.scale_f32)
+    row_scales_kernel<float><<<grid_of(tiles, kWarps), kThreads, 0, stream>>>(
+        static_cast<const float *>(a.packed_scales), a.packed_rows, smax, a.E, Np / kTileN, nb);
+  else
+    row_scales_kernel<uint16_t><<<grid_of(tiles, kWarps), kThreads, 0, stream>>>(
+        static_cast<const uint16_t *>(a.packed_scales), a.packed_rows, smax, a.E, Np / kTileN, nb);
   return cudaGetLastError();
 }
 
@@ -792,18 +779,18 @@ size_t max_groups(int64_t P, int E, int gt) {
 }
 size_t count_words(int64_t P, int E) { return ceil_div(P, kSortSlots) * (E + 1); }
 
-// The lists of many slots: counts is workspace, `clear` words are cleared by
-// the first launch; place, and the groups of up to gt slots, when asked for.
+// The lists of many slots: counts is workspace; place, and the groups of up to
+// gt slots (sizes in whole `unit`s), when asked for.
 cudaError_t launch_lists(const int32_t *experts, int64_t P, int E, const Lists &l,
-                         int32_t *counts, int32_t *place, int gt, int unit, uint32_t *clear,
-                         int n_clear, bool pdl, cudaStream_t stream) {
+                         int32_t *counts, int32_t *place, int gt, int unit, bool pdl,
+                         cudaStream_t stream) {
   static std::atomic<unsigned long long> done{0};
   cudaError_t e =
       ensure_smem_limit(place_kernel, (2 + kPlaceWarps) * (kMoeMaxExperts + 1) * 4, done);
   if (e != cudaSuccess) return e;
   const unsigned blocks = static_cast<unsigned>(ceil_div(P, kSortSlots));
   e = launch_pdl(count_kernel, blocks, kThreads, size_t(E + 1) * 4, pdl, stream, experts, P, E,
-                 counts, clear, n_clear);
+                 counts);
   if (e != cudaSuccess) return e;
   return launch_pdl(place_kernel, blocks, kPlaceThreads, size_t(2 + kPlaceWarps) * (E + 1) * 4,
                     pdl, stream, experts, P, E, counts, l.offsets, l.order, place, l.groups,
@@ -873,9 +860,10 @@ ExpertsSpace experts_space(const ExpertsArgs &a) {
 
 // ---- tensor-core path: bf16 activations, many slots ---------------------------
 
-// From this many slots on; fewer stream the weights past groups of 8 slots.
-constexpr int kTileMinSlots = 257;
-bool tile_path(bool a_f32, int64_t P) { return !a_f32 && P >= kTileMinSlots; }
+// From a mean of this many slots per expert on; fewer stream the weights past
+// groups of up to 8 slots.
+constexpr int kTileMeanSlots = 5;
+bool tile_path(bool a_f32, int64_t P, int E) { return !a_f32 && P >= int64_t(kTileMeanSlots) * E; }
 
 // Rows of partials start on 16 bytes.
 int64_t part_ld(int64_t N) { return ceil_div(N, 8) * 8; }
@@ -884,8 +872,7 @@ int64_t k_pad(int64_t K) { return ceil_div(K, kChunkK) * kChunkK; }
 struct TileSpace {
   Lists l;
   int32_t *counts, *place;
-  uint32_t *clear;  // per stack: smax [E], bmax [E]
-  float *fac[3];
+  float *bmax[3];   // [E] per stack with a bias, else null
   uint16_t *rows;   // fp16 activations by place
   float *unscale, *norm1;
   // The layer's.
@@ -909,9 +896,7 @@ TileSpace tile_space(unsigned char *ws, int64_t P, const ExpertStack *const *w, 
   s.l.groups = c.take<SlotGroup>(max_groups(P, E, kTileSlots));
   s.counts = c.take<int32_t>(count_words(P, E));
   s.place = c.take<int32_t>(P);
-  s.clear = c.take<uint32_t>(size_t(stacks) * 2 * E);
-  for (int i = 0; i < stacks; ++i)
-    s.fac[i] = c.take<float>(size_t(E) * ceil_div(w[i]->N, kTileN) * kTileN);
+  for (int i = 0; i < stacks; ++i) s.bmax[i] = w[i]->bias ? c.take<float>(E) : nullptr;
   s.rows = c.take<uint16_t>(size_t(P) * k_pad(w[0]->K));
   s.unscale = c.take<float>(P);
   if (layer) {
@@ -926,31 +911,23 @@ TileSpace tile_space(unsigned char *ws, int64_t P, const ExpertStack *const *w, 
   return s;
 }
 
-// Lists by place, and the stacks' scale factors.
+// Lists by place, and (the layer's bounds need them) the stacks' largest biases.
 cudaError_t launch_tile_lists(const TileSpace &s, const int32_t *experts, int64_t P,
                               const ExpertStack *const *w, int stacks, bool pdl,
                               cudaStream_t stream) {
   const int E = w[0]->E;
-  const cudaError_t e = launch_lists(experts, P, E, s.l, s.counts, s.place, kTileSlots, 16,
-                                     s.clear, stacks * 2 * E, pdl, stream);
-  if (e != cudaSuccess) return e;
-  ScaleArgs a{};
-  int most = 0;
+  cudaError_t e = launch_lists(experts, P, E, s.l, s.counts, s.place, kTileSlots, 16, pdl, stream);
+  BiasArgs a{};
+  bool any = false;
   for (int i = 0; i < stacks; ++i) {
-    a.s[i] = static_cast<const unsigned char *>(w[i]->s);
     a.bias[i] = w[i]->bias;
-    a.fac[i] = s.fac[i];
-    a.smax[i] = s.clear + (2 * i) * E;
-    a.bmax[i] = s.clear + (2 * i + 1) * E;
+    a.bmax[i] = s.bmax[i];
     a.N[i] = w[i]->N;
-    a.N16[i] = static_cast<int>(ceil_div(w[i]->N, kTileN));
-    a.nb[i] = static_cast<int>(ceil_div(w[i]->K, w[i]->bs));
-    a.f32[i] = w[i]->s_f32;
-    most = std::max(most, a.N16[i]);
+    any = any || w[i]->bias;
   }
-  return launch_pdl(tile_scales_kernel,
-                    dim3(static_cast<unsigned>(ceil_div(most, kWarps)), E, stacks), kThreads, 0,
-                    pdl, stream, a);
+  if (e == cudaSuccess && any && stacks > 1)
+    e = launch_pdl(bias_max_kernel, dim3(E, stacks), kThreads, 0, pdl, stream, a);
+  return e;
 }
 
 cudaError_t fill_tile(TileParams &p, int mode, const ExpertStack *const *w, int first,
@@ -960,7 +937,8 @@ cudaError_t fill_tile(TileParams &p, int mode, const ExpertStack *const *w, int 
   for (int m = 0; m < 2; ++m) {
     const int i = mode == kStreamGateUp ? first + m : first;
     p.w[m] = stream_mat(*w[i]);
-    p.ts[m] = TileScales{s.fac[i], s.clear + 2 * i * w0.E, s.clear + (2 * i + 1) * w0.E};
+    p.ts[m] = TileScales{
+        w[i]->rows, w[i]->rows + int64_t(w[i]->E) * ceil_div(w[i]->N, kTileN) * kTileN, s.bmax[i]};
   }
   p.E = w0.E;
   p.N = w0.N;
@@ -1125,7 +1103,7 @@ cudaError_t launch_moe_route(const RouteArgs &a, cudaStream_t stream) {
     l.offsets = a.offsets;
     l.order = a.order;
     e = launch_lists(a.experts, P, a.E, l, reinterpret_cast<int32_t *>(a.ws), nullptr, 1, 1,
-                     nullptr, 0, a.pdl, stream);
+                     a.pdl, stream);
   }
   return e;
 }
@@ -1133,7 +1111,7 @@ cudaError_t launch_moe_route(const RouteArgs &a, cudaStream_t stream) {
 size_t matmul_experts_workspace_bytes(const ExpertsArgs &a) {
   ExpertsArgs b = a;
   b.ws = nullptr;
-  if (tile_path(a.a_f32, a.M * a.top_k)) {
+  if (tile_path(a.a_f32, a.M * a.top_k, a.w.E)) {
     const ExpertStack *w[1] = {&a.w};
     return tile_space(nullptr, a.M * a.top_k, w, 1, false).bytes;
   }
@@ -1142,7 +1120,7 @@ size_t matmul_experts_workspace_bytes(const ExpertsArgs &a) {
 
 cudaError_t launch_matmul_experts(const ExpertsArgs &a, cudaStream_t stream) {
   const int64_t P = a.M * a.top_k, rows = a.per_slot ? P : a.M;
-  if (tile_path(a.a_f32, P)) return launch_experts_tile(a, stream);
+  if (tile_path(a.a_f32, P, a.w.E)) return launch_experts_tile(a, stream);
   StreamPlan pl;
   if (!plan_stream(pl, a.w, kStreamProduct, a.a_f32 ? 2 : 1, P, a.M, a.top_k, P))
     return cudaErrorNotSupported;
@@ -1168,8 +1146,7 @@ cudaError_t launch_matmul_experts(const ExpertsArgs &a, cudaStream_t stream) {
     r.tops = s.tops;
     e = launch_prep(r, a.pdl, stream);
   } else {
-    e = launch_lists(a.experts, P, a.w.E, s.l, s.counts, nullptr, 1 << pl.p.gt_log2, 1, nullptr,
-                     0, a.pdl, stream);
+    e = launch_lists(a.experts, P, a.w.E, s.l, s.counts, nullptr, 1 << pl.p.gt_log2, 1, a.pdl, stream);
     if (e == cudaSuccess)
       e = launch_row_tops(a.A, a.a_f32, vec, rows, a.w.K, s.tops, nullptr, 0, a.pdl, stream);
   }
@@ -1191,7 +1168,7 @@ cudaError_t launch_matmul_experts(const ExpertsArgs &a, cudaStream_t stream) {
 size_t moe_workspace_bytes(const MoeArgs &a) {
   MoeArgs b = a;
   b.ws = nullptr;
-  if (tile_path(a.a_f32, a.M * a.top_k)) {
+  if (tile_path(a.a_f32, a.M * a.top_k, a.gate.E)) {
     const ExpertStack *w[3] = {&a.gate, &a.up, &a.down};
     return tile_space(nullptr, a.M * a.top_k, w, 3, true).bytes;
   }
@@ -1201,7 +1178,7 @@ size_t moe_workspace_bytes(const MoeArgs &a) {
 cudaError_t launch_moe(const MoeArgs &a, cudaStream_t stream) {
   const int64_t P = a.M * a.top_k;
   const bool few = P <= kFewSlots;
-  if (tile_path(a.a_f32, P)) return launch_moe_tile(a, stream);
+  if (tile_path(a.a_f32, P, a.gate.E)) return launch_moe_tile(a, stream);
   const MoeSpace s = moe_space(a);
   StreamPlan up, down;
   const int terms = a.a_f32 ? 2 : 1;
@@ -1242,8 +1219,7 @@ cudaError_t launch_moe(const MoeArgs &a, cudaStream_t stream) {
                       s.l.experts, nullptr, nullptr, nullptr, a.pdl};
     e = launch_moe_route(r, stream);
     if (e == cudaSuccess)
-      e = launch_lists(s.l.experts, P, a.gate.E, s.l, s.counts, nullptr, 1 << up.p.gt_log2, 1,
-                       nullptr, 0, a.pdl, stream);
+      e = launch_lists(s.l.experts, P, a.gate.E, s.l, s.counts, nullptr, 1 << up.p.gt_log2, 1, a.pdl, stream);
     if (e == cudaSuccess)
       e = launch_row_tops(a.X, a.a_f32, vec, a.M, a.gate.K, s.tops, s.clear, n_clear, a.pdl,
                           stream);

@@ -33,6 +33,7 @@ cudaError_t launch_moe_route(const RouteArgs &a, cudaStream_t stream);
 // 16-row tiles (N16 tiles per expert).
 struct ExpertStack {
   const void *b, *s, *z;  // z may be null (every zero point is 8)
+  const float *rows;      // [E * 16 N16] row factors, then [E] largest |scale|
   const float *bias;      // [E, N] or null
   int E, N, K, bs;
   bool s_f32;
@@ -46,6 +47,7 @@ struct ExpertPackArgs {
   int bs;
   bool scale_f32;
   void *packed_b, *packed_scales, *packed_zp;
+  float *packed_rows;
 };
 // Re-layout of a stack; the header is written by the caller's last kernel.
 cudaError_t launch_prepack_experts(const ExpertPackArgs &a, cudaStream_t stream);

@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
       }
       const SlotGroup sg = p.groups[u / np];
       Columns &cl = cols2[n & 1];
-      auto bits = [&](const uint32_t *v) { return __uint_as_float(v[sg.e]); };
+      auto most = [&](const float *v) { return v ? v[sg.e] : 0.f; };
       for (int c = lane; c < sg.cols; c += 32) {
         const int place = sg.first + c, id = p.order[place];
         float a = p.unscale[place], b = 1.f;
@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
           int e = 0;
 #pragma unroll
           for (int m = 0; m < 2; ++m)
-            e += expo(15.f * bits(p.ts[m].smax) * x1 + bits(p.ts[m].bmax));
+            e += expo(15.f * most(p.ts[m].smax) * x1 + most(p.ts[m].bmax));
           const int shift = max(-126, min(126, 15 - e));
           b = p.weights[id] * exp2i(shift);
           if (u % np == 0 && rank == 0) {
@@ -370,9 +370,9 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
           }
         } else if (p.mode == kStreamDown) {
           // |sum| <= 15 s K 2^15 / 2^shift, and the bias.
-          const int e = max(expo(15.f * bits(p.ts[0].smax) * static_cast<float>(p.K64 * kChunkK)) +
+          const int e = max(expo(15.f * most(p.ts[0].smax) * static_cast<float>(p.K64 * kChunkK)) +
                                 15 - p.shift[place],
-                            expo(bits(p.ts[0].bmax))) + 1;
+                            expo(most(p.ts[0].bmax))) + 1;
           const int shift = max(-126, min(126, 15 - e));
           a *= exp2i(shift);
           b = p.weights[id] * exp2i(shift);

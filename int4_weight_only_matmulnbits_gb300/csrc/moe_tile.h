@@ -13,11 +13,11 @@ namespace mnb {
 constexpr int kTileSlots = 192;  // slots per group (columns of an accumulator)
 constexpr int kTileBox = 32;     // activation rows per TMA box
 
-// What the weights' scales of a stack are brought to (tile_scales_kernel).
+// What the kernel needs of a stack's scales and biases.
 struct TileScales {
-  const float *fac;      // [E * N16 * 16] power of two per row
-  const uint32_t *smax;  // [E] bits of the largest |scale|
-  const uint32_t *bmax;  // [E] bits of the largest |bias|
+  const float *fac;   // [E * N16 * 16] power of two per row (moe.cu, row_scales_kernel)
+  const float *smax;  // [E] largest |scale|
+  const float *bmax;  // [E] largest |bias|, or null
 };
 
 struct TileParams {

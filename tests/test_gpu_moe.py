@@ -61,6 +61,12 @@ def test_pack_is_the_padded_stack(dev, bs, E, N, K, zp):
     assert (z is None) == (w.packed_zp is None)
     if zp:
         assert torch.equal(w.packed_zp, plain.packed_zp)
+    # Row factors: powers of two that bring the largest scale into 2^14 .. 2^15.
+    fac, most = w.packed_rows[:-E].view(E, Np), w.packed_rows[-E:]
+    assert torch.equal(most, s.abs().amax((1, 2)))
+    assert (torch.frexp(fac).mantissa == 0.5).all()
+    top = s.abs().amax(2) * fac[:, :N]
+    assert ((top >= 2.0 ** 14) & (top < 2.0 ** 15)).all()
 
 
 # ---- router --------------------------------------------------------------------------------

@@ -32,7 +32,8 @@ def stack(i=0, *, E=8, N=64, K=128, bs=32, sdt=BF16, zp=False, bias=False, regis
           packed_as=None):
     base = 0x7200_0000_0000 + i * (1 << 36)
     s = b.ExpertsC(base, base + (1 << 34), base + (2 << 34) if zp else None,
-                   base + (3 << 34) if bias else None, E, N, K, bs, sdt)
+                   base + (1 << 35) + (1 << 34) + (1 << 33), base + (3 << 34) if bias else None,
+                   E, N, K, bs, sdt)
     if register:
         e, n, k = packed_as or (E, N, K)
         h = mnb.mnb_packed_header_make(e * (-(-n // 16) * 16), k, bs,
@@ -94,7 +95,7 @@ def test_stack_refusals(lib, change, status):
 
 
 def test_stack_pointers(lib):
-    for field in ("packed_b", "packed_scales"):
+    for field in ("packed_b", "packed_scales", "packed_rows"):
         w = stack()
         setattr(w, field, None)
         assert experts(lib, w=w) == b.MNB_ERR_NULL
@@ -110,6 +111,7 @@ def test_stack_pointers(lib):
     w = stack()
     assert experts(lib, w=w, y=w.packed_b + 64) == b.MNB_ERR_ALIAS
     assert experts(lib, w=w, y=w.packed_scales + 64) == b.MNB_ERR_ALIAS
+    assert experts(lib, w=w, y=w.packed_rows + 64) == b.MNB_ERR_ALIAS
 
 
 def test_stack_headers(lib):
@@ -156,9 +158,9 @@ def test_layer_stacks_must_fit(lib):
     assert moe(lib, down=stack(2, N=128, K=64, packed_as=(8, 112, 64))) == b.MNB_ERR_LAYOUT
 
 
-def prepack(lib, B=A, s=LOG, z=0, E=4, N=20, K=100, bs=32, dt=BF16, pb=EXP, ps=WEI, pz=0):
+def prepack(lib, B=A, s=LOG, z=0, E=4, N=20, K=100, bs=32, dt=BF16, pb=EXP, ps=WEI, pz=0, pr=Y):
     return lib.mnb_prepack_experts(vp(B), vp(s), vp(z), E, N, K, bs, dt, vp(pb), vp(ps), vp(pz),
-                                   None)
+                                   vp(pr), None)
 
 
 @pytest.mark.parametrize("change,status", [
@@ -169,7 +171,8 @@ def prepack(lib, B=A, s=LOG, z=0, E=4, N=20, K=100, bs=32, dt=BF16, pb=EXP, ps=W
     (dict(dt=3), b.MNB_ERR_DTYPE), (dict(pb=EXP + 4), b.MNB_ERR_ALIGN),
     (dict(ps=WEI + 8), b.MNB_ERR_ALIGN), (dict(s=LOG + 1), b.MNB_ERR_ALIGN),
     (dict(z=OFF, pz=ORD + 8), b.MNB_ERR_ALIGN), (dict(pb=A), b.MNB_ERR_ALIAS),
-    (dict(ps=EXP + 256), b.MNB_ERR_ALIAS)])
+    (dict(ps=EXP + 256), b.MNB_ERR_ALIAS), (dict(pr=0), b.MNB_ERR_NULL),
+    (dict(pr=Y + 8), b.MNB_ERR_ALIGN), (dict(pr=WEI + 16), b.MNB_ERR_ALIAS)])
 def test_prepack_experts_refusals(lib, change, status):
     assert prepack(lib, **change) == status
 
@@ -200,7 +203,7 @@ def test_workspace_sizes(lib):
 
 def test_binding_refusals(lib):
     x = torch.zeros(4, 128, dtype=torch.bfloat16)
-    w = mnb.PackedExperts(x, x, None, 8, 64, 128, 32, torch.bfloat16)
+    w = mnb.PackedExperts(x, x, None, x, 8, 64, 128, 32, torch.bfloat16)
     with pytest.raises(ValueError, match="CUDA"):
         mnb.mnb_moe_route(torch.zeros(4, 8), 2)
     with pytest.raises(ValueError, match=r"\[M, E\]"):
