@@ -817,15 +817,12 @@ Lists take_lists(Carve &c, int64_t P, int E, bool routed) {
 struct MoeSpace {
   Lists l;
   int32_t *counts;
-  uint32_t *tops, *clear;  // clear: hidden tops [P], then the counters
+  uint32_t *tops, *hidden_tops;
   float *hidden, *part;
   size_t bytes;
 };
 // Hidden rows start on 16 bytes.
 size_t hidden_ld(const MoeArgs &a) { return ceil_div(a.gate.N, 4) * 4; }
-size_t moe_clear_words(const MoeArgs &a) {
-  return size_t(a.M) * a.top_k + ceil_div(a.down.N, kTileN);
-}
 
 MoeSpace moe_space(const MoeArgs &a) {
   const size_t P = size_t(a.M) * a.top_k;
@@ -834,7 +831,7 @@ MoeSpace moe_space(const MoeArgs &a) {
   s.l = take_lists(c, P, a.gate.E, true);
   s.counts = P > kFewSlots ? c.take<int32_t>(count_words(P, a.gate.E)) : nullptr;
   s.tops = c.take<uint32_t>(a.M);
-  s.clear = c.take<uint32_t>(moe_clear_words(a));
+  s.hidden_tops = c.take<uint32_t>(P);
   s.hidden = c.take<float>(P * hidden_ld(a));
   s.part = c.take<float>(P * a.down.N);
   s.bytes = c.used;
@@ -1188,7 +1185,6 @@ cudaError_t launch_moe(const MoeArgs &a, cudaStream_t stream) {
   // Both launches use the lists: groups of the size that fits both.
   up.p.gt_log2 = down.p.gt_log2 = std::min(up.p.gt_log2, down.p.gt_log2);
   const bool vec = vec_rows(a.X, a.gate.K, a.a_f32 ? 4 : 2);
-  const int64_t n_clear = moe_clear_words(a);
   cudaError_t e;
   if (few) {
     PrepArgs r{};
@@ -1211,8 +1207,8 @@ cudaError_t launch_moe(const MoeArgs &a, cudaStream_t stream) {
     r.K = a.gate.K;
     r.rows = static_cast<int>(a.M);
     r.tops = s.tops;
-    r.clear = s.clear;
-    r.n_clear = static_cast<int>(n_clear);
+    r.clear = s.hidden_tops;
+    r.n_clear = static_cast<int>(P);
     e = launch_prep(r, a.pdl, stream);
   } else {
     const RouteArgs r{a.logits, a.logits_f32, a.M, a.gate.E, a.top_k, a.normalize, s.l.weights,
@@ -1221,8 +1217,7 @@ cudaError_t launch_moe(const MoeArgs &a, cudaStream_t stream) {
     if (e == cudaSuccess)
       e = launch_lists(s.l.experts, P, a.gate.E, s.l, s.counts, nullptr, 1 << up.p.gt_log2, 1, a.pdl, stream);
     if (e == cudaSuccess)
-      e = launch_row_tops(a.X, a.a_f32, vec, a.M, a.gate.K, s.tops, s.clear, n_clear, a.pdl,
-                          stream);
+      e = launch_row_tops(a.X, a.a_f32, vec, a.M, a.gate.K, s.tops, s.hidden_tops, P, a.pdl, stream);
   }
   if (e != cudaSuccess) return e;
   set_lists(up.p, s.l);
@@ -1234,7 +1229,7 @@ cudaError_t launch_moe(const MoeArgs &a, cudaStream_t stream) {
   up.p.ld = a.gate.K;
   up.p.tops = s.tops;
   up.p.hidden = s.hidden;
-  up.p.hidden_tops = s.clear;
+  up.p.hidden_tops = s.hidden_tops;
   up.p.ldh = hidden_ld(a);
   e = run_stream(up, a.pdl, stream);
   if (e != cudaSuccess) return e;
@@ -1243,19 +1238,11 @@ cudaError_t launch_moe(const MoeArgs &a, cudaStream_t stream) {
   down.p.A = s.hidden;
   down.p.a_f32 = down.p.a_vec = down.p.per_slot = 1;
   down.p.ld = hidden_ld(a);
-  down.p.tops = s.clear;
+  down.p.tops = s.hidden_tops;
   down.p.part = s.part;
-  down.p.Y = a.Y;
-  down.p.y_f32 = a.a_f32;
-  // One token: whoever completes a column range adds its partials (moe_one
-  // ... us, with the launch that follows ... us). More: the last steps are
-  // all of one group, so a few CTAs would do all of the adding (16 tokens
-  // of 8 out of 128 experts: 100 us, with a launch of its own ... us).
-  const bool join = a.M == 1;
-  down.p.counters = join ? s.clear + P : nullptr;
   down.p.early = a.pdl;
   e = run_stream(down, a.pdl, stream);
-  if (e != cudaSuccess || join) return e;
+  if (e != cudaSuccess) return e;
   const int threads =
       static_cast<int>(std::min<int64_t>(1024, ceil_div(ceil_div(a.down.N, 4), 32) * 32));
   return launch_pdl(combine_kernel, static_cast<unsigned>(a.M), threads, 0, a.pdl, stream, s.part,

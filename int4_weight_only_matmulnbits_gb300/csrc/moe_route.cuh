@@ -14,6 +14,7 @@
 #pragma once
 
 #include <cstdint>
+#include <type_traits>
 
 #include "mnb_common.cuh"
 
@@ -29,6 +30,11 @@ __device__ __forceinline__ uint32_t logit_key(float x) {
 __device__ __forceinline__ float key_logit(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
 }
+// The key of a bf16 logit from its upper half: the lower one is zeros for
+// positive values and ones for negative ones.
+__device__ __forceinline__ uint32_t bf16_key(uint32_t k) {
+  return (k & 0x80000000u) ? (k & 0xFFFF0000u) : (k | 0xFFFFu);
+}
 // exp(l - max), with exp(inf - inf) = 1.
 __device__ __forceinline__ float logit_exp(float l, float top) {
   return l == top ? 1.f : expf(l - top);
@@ -41,57 +47,79 @@ __device__ __forceinline__ float warp_sum(float v) {
 }
 
 // Lane j < top_k gets choice j of row m: expert (or -1) and weight. Lane l
-// holds the keys of experts l, l + 32, ... in KPL registers (32 KPL >= E).
-template <int KPL>
-__device__ __forceinline__ void route_row_regs(const void *logits, bool f32, int64_t m, int E,
-                                               int top_k, bool normalize, int &expert,
-                                               float &weight) {
+// holds experts l, l + 32, ... (KPL of them, 32 KPL >= E) as a list sorted by
+// key, then index, whose head it offers; the winner's lane moves on. bf16
+// logits fit 16 bits: key and inverted index share a word, one reduction a
+// choice; fp32 logits take a second one for the index.
+template <int KPL, bool F32>
+__device__ __forceinline__ void route_row_regs(const void *logits, int64_t m, int E, int top_k,
+                                               bool normalize, int &expert, float &weight) {
   const int lane = threadIdx.x & 31;
   uint32_t key[KPL];
+  int at[KPL];
 #pragma unroll
   for (int q = 0; q < KPL; ++q) {
     const int i = lane + 32 * q;
     float x = -INFINITY;
     if (i < E)
-      x = f32 ? static_cast<const float *>(logits)[m * E + i]
+      x = F32 ? static_cast<const float *>(logits)[m * E + i]
               : bf16_bits_to_f32(static_cast<const uint16_t *>(logits)[m * E + i]);
     key[q] = logit_key(x);
+    at[q] = i;
+    if (!F32 && key[q]) key[q] = (key[q] & 0xFFFF0000u) | (0xFFFFu - i);
   }
+  // The logit behind a key.
+  auto value = [](uint32_t k) { return key_logit(F32 ? k : bf16_key(k)); };
+  float all = 0.f;
+  if (!normalize) {
+    uint32_t best = key[0];
+#pragma unroll
+    for (int q = 1; q < KPL; ++q) best = max(best, key[q]);
+    best = __reduce_max_sync(0xffffffffu, best);
+#pragma unroll
+    for (int q = 0; q < KPL; ++q)
+      if (key[q]) all += logit_exp(value(key[q]), value(best));
+    all = warp_sum(all);
+  }
+#pragma unroll
+  for (int i = 0; i < KPL - 1; ++i)  // larger keys first; equal ones stay in order
+#pragma unroll
+    for (int q = 0; q < KPL - 1 - i; ++q)
+      if (key[q + 1] > key[q]) {
+        const uint32_t k = key[q];
+        key[q] = key[q + 1];
+        key[q + 1] = k;
+        if (F32) {
+          const int t = at[q];
+          at[q] = at[q + 1];
+          at[q + 1] = t;
+        }
+      }
   uint32_t first = 0, mine = 0;
   expert = -1;
-  float all = 0.f;
 #pragma unroll 1
   for (int j = 0; j < top_k; ++j) {
-    uint32_t best = key[0];
-    int bi = lane;
-#pragma unroll
-    for (int q = 1; q < KPL; ++q)
-      if (key[q] > best) {
-        best = key[q];
-        bi = lane + 32 * q;
-      }
-    const uint32_t win = __reduce_max_sync(0xffffffffu, best);
+    const uint32_t win = __reduce_max_sync(0xffffffffu, key[0]);
     if (win == 0) break;  // every expert left is masked
-    const int at = static_cast<int>(
-        __reduce_min_sync(0xffffffffu, best == win ? static_cast<uint32_t>(bi) : 0xFFFFFFFFu));
-    if (j == 0) {
-      first = win;
-      if (!normalize) {
-#pragma unroll
-        for (int q = 0; q < KPL; ++q)
-          if (key[q]) all += logit_exp(key_logit(key[q]), key_logit(win));
-        all = warp_sum(all);
-      }
+    int e = static_cast<int>(0xFFFFu - (win & 0xFFFFu));
+    bool own = key[0] == win;
+    if (F32) {
+      e = static_cast<int>(
+          __reduce_min_sync(0xffffffffu, own ? static_cast<uint32_t>(at[0]) : 0xFFFFFFFFu));
+      own = own && at[0] == e;
     }
+    if (j == 0) first = win;
     if (lane == j) {
-      expert = at;
+      expert = e;
       mine = win;
     }
 #pragma unroll
-    for (int q = 0; q < KPL; ++q)
-      if (at == lane + 32 * q) key[q] = 0;
+    for (int q = 0; q < KPL; ++q) {
+      key[q] = own ? (q + 1 < KPL ? key[q + 1] : 0u) : key[q];
+      if (F32 && q + 1 < KPL) at[q] = own ? at[q + 1] : at[q];
+    }
   }
-  const float p = expert < 0 ? 0.f : logit_exp(key_logit(mine), key_logit(first));
+  const float p = expert < 0 ? 0.f : logit_exp(value(mine), value(first));
   const float chosen = warp_sum(p);
   weight = expert < 0 ? 0.f : p / (normalize ? chosen : all);
 }
@@ -150,9 +178,13 @@ __device__ __forceinline__ void route_row_shared(const void *logits, bool f32, i
 __device__ __forceinline__ void route_row(const void *logits, bool f32, int64_t m, int E,
                                           int top_k, bool normalize, uint32_t *keys,
                                           int &expert, float &weight) {
-  if (E <= 64) route_row_regs<2>(logits, f32, m, E, top_k, normalize, expert, weight);
-  else if (E <= 128) route_row_regs<4>(logits, f32, m, E, top_k, normalize, expert, weight);
-  else if (E <= 256) route_row_regs<8>(logits, f32, m, E, top_k, normalize, expert, weight);
+  auto regs = [&](auto kpl) {
+    if (f32) route_row_regs<kpl.value, true>(logits, m, E, top_k, normalize, expert, weight);
+    else route_row_regs<kpl.value, false>(logits, m, E, top_k, normalize, expert, weight);
+  };
+  if (E <= 64) regs(std::integral_constant<int, 2>());
+  else if (E <= 128) regs(std::integral_constant<int, 4>());
+  else if (E <= 256) regs(std::integral_constant<int, 8>());
   else route_row_shared(logits, f32, m, E, top_k, normalize, keys, expert, weight);
 }
 

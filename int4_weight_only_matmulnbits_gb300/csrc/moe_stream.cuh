@@ -37,9 +37,7 @@
 //    ahead (moe.cu); the layer is two launches of this one. The second needs
 //    nothing from the first but the hidden rows and their magnitudes: it
 //    fills its rings before it waits for the first to finish. Down partials
-//    go to a workspace; whoever completes a column range, by an arrival
-//    counter, adds them in slot order, so the result does not depend on who
-//    that is.
+//    go to a workspace, and a launch of its own adds a token's in slot order.
 //  * What runs once per launch is kept short and rolled up: fetching
 //    instructions is most of the time of a call for one token.
 #pragma once
@@ -94,7 +92,6 @@ __global__ void __launch_bounds__(kThreads, kStreamCtas) stream_kernel(const Str
   extern __shared__ __align__(128) unsigned char smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
-  __shared__ int s_last;
   __shared__ float s_unscale[kCols];  // what undoes a column's row scale
 
   if (!p.early) {
@@ -199,8 +196,7 @@ __global__ void __launch_bounds__(kThreads, kStreamCtas) stream_kernel(const Str
   for (int i = 0; i < kStages - 1; ++i) fetch();
 
   if (p.early) grid_dependency_wait();
-  // Rows that no step writes: slots without an expert (product), every token
-  // when nothing is routed (down).
+  // Rows that no step writes: slots without an expert (product).
   auto store = [&](int64_t i, float v) {
     if (p.y_f32) static_cast<float *>(p.Y)[i] = v;
     else static_cast<uint16_t *>(p.Y)[i] = static_cast<uint16_t>(bf16_bits(v));
@@ -210,10 +206,6 @@ __global__ void __launch_bounds__(kThreads, kStreamCtas) stream_kernel(const Str
       const int64_t row = int64_t(order[i]) * p.N;
       for (int n = tid; n < p.N; n += kThreads) store(row + n, 0.f);
     }
-  } else if (p.mode == kStreamDown && groups == 0 && p.counters) {
-    const int64_t n = int64_t(p.M) * p.N;
-    for (int64_t i = blockIdx.x * int64_t(kThreads) + tid; i < n; i += int64_t(gridDim.x) * kThreads)
-      store(i, 0.f);
   }
 
   uint16_t *sx = reinterpret_cast<uint16_t *>(smem + p.off_x);
@@ -232,17 +224,20 @@ __global__ void __launch_bounds__(kThreads, kStreamCtas) stream_kernel(const Str
       if (staged >= 0) __syncthreads();  // every warp is done with the rows before
       staged = cur.group;
       const int pieces = p.K64 * (kChunkK / 8);
-#pragma unroll 1
-      for (int col = 0; col < cols; ++col) {
+      // The warps share the rows out, so that all rows' loads overlap: 8, 4, 2
+      // warps or one to a row.
+      const int share_log2 = cols == 1 ? 3 : cols == 2 ? 2 : cols <= 4 ? 1 : 0;
+      const int col = warp >> share_log2, part = warp - (col << share_log2);
+      if (col < cols) {
         int row = order[first + col];
         if (!p.per_slot) row /= p.top_k;
         const int shift = row_shift(__ldcg(p.tops + row));
         const float f = exp2i(shift);
-        if (tid == 0) s_unscale[col] = exp2i(-shift);
-        // Whole warps go round: pieces are a multiple of 8, a block's sum is
-        // formed by up to 8 neighbouring lanes.
+        if (part == 0 && lane == 0) s_unscale[col] = exp2i(-shift);
+        // Pieces are a multiple of 8; a block's sum is formed by up to 8
+        // neighbouring lanes.
 #pragma unroll 1
-        for (int i0 = warp * 32; i0 < pieces; i0 += kThreads) {
+        for (int i0 = part * 32; i0 < pieces; i0 += 32 << share_log2) {
           const int i = i0 + lane, k = i * 8;
           float v[8];
           load8(p.A, p.a_f32, p.a_vec, row * p.ld, k, p.K, v);  // zeros past K
@@ -451,48 +446,6 @@ __global__ void __launch_bounds__(kThreads, kStreamCtas) stream_kernel(const Str
         for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
         if ((lane & 15) == 0 && top) atomicMax(p.hidden_tops + id, top);
       }
-    }
-    if (p.mode == kStreamDown && p.counters && n0 < p.N) {
-      // Whoever completes this column range adds the partials of each token,
-      // in slot order.
-      int last = 0;
-      if (alone) __syncwarp();
-      else __syncthreads();
-      if (alone ? lane == 0 : tid == 0) {
-        __threadfence();
-        last = atomicAdd(p.counters + part0, 1u) == static_cast<unsigned>(groups - 1);
-        __threadfence();
-        s_last = last;
-      }
-      if (alone) {
-        last = __shfl_sync(0xffffffffu, last, 0);
-        __syncwarp();
-      } else {
-        __syncthreads();
-        last = s_last;
-      }
-      if (last)
-#pragma unroll 1
-        for (int i = alone ? lane : tid; i < p.M << rows_log2; i += alone ? 32 : kThreads) {
-          const int m = i >> rows_log2, n = n0 + (i & (rows - 1));
-          if (n >= p.N) continue;
-          // Eight slots' loads at a time, added in order.
-          float y = 0.f;
-          for (int j0 = 0; j0 < p.top_k; j0 += 8) {
-            const int64_t q = int64_t(m) * p.top_k + j0;
-            float v[8];
-            bool some[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              some[j] = j0 + j < p.top_k && p.experts[q + j] >= 0;
-              v[j] = j0 + j < p.top_k ? __ldcg(p.part + (q + j) * p.N + n) : 0.f;
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (some[j]) y += v[j];
-          }
-          store(int64_t(m) * p.N + n, y);
-        }
     }
   }
   cp_wait<0>();

@@ -41,14 +41,13 @@ struct StreamParams {
   const SlotGroup *groups;
   const float *weights;  // [P] (gate and up, down)
   // Outputs: Y [P, N] (product), hidden rows [P, ldh] (gate and up), partials
-  // [P, N] and Y [M, N] (down).
+  // [P, N] (down).
   void *Y;
   int y_f32;
   float *hidden;
   uint32_t *hidden_tops;  // [P], zeros before
   int64_t ldh;
   float *part;
-  unsigned *counters;  // arrivals per column range, zeros before; or null
   // Geometry.
   int gt_log2;          // slots per group: 2^gt_log2 <= 8
   int npair;            // tile pairs of an expert
