@@ -96,7 +96,8 @@ class ExpertsC(ctypes.Structure):
     """mnb_experts (include/mnb.h)."""
     _fields_ = [("packed_b", ctypes.c_void_p), ("packed_scales", ctypes.c_void_p),
                 ("packed_zp", ctypes.c_void_p), ("packed_rows", ctypes.c_void_p),
-                ("bias", ctypes.c_void_p), ("E", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
+                ("bias", ctypes.c_void_p), ("E", ctypes.c_int64), ("N", ctypes.c_int64),
+                ("K", ctypes.c_int64),
                 ("block_size", ctypes.c_int32), ("scale_dtype", ctypes.c_int32)]
 
 
@@ -749,7 +750,7 @@ def mnb_matmul_bnb4(A: torch.Tensor, w: PackedWeight, code: torch.Tensor,
 
 # ---- mixture of experts ---------------------------------------------------------
 
-@dataclass
+@dataclass(frozen=True)
 class PackedExperts:
     """Caller-owned prepacked buffers of a stack of E weights N x K."""
     packed_b: torch.Tensor
@@ -766,6 +767,10 @@ class PackedExperts:
         return sum(t.numel() * t.element_size() for t in
                    (self.packed_b, self.packed_scales, self.packed_zp, self.packed_rows)
                    if t is not None)
+
+    def __getstate__(self):
+        """Copied and pickled without the argument struct (addresses)."""
+        return {k: v for k, v in self.__dict__.items() if k != "_struct"}
 
 
 class MoeRouting(NamedTuple):
@@ -812,15 +817,16 @@ def _workspace(n: int, device: torch.device):
 
 
 def _experts_struct(w: PackedExperts, bias: torch.Tensor | None, device) -> ExpertsC:
-    """mnb_experts of w and a bias. The struct without a bias is made once for
-    w's buffers and never changed; one with a bias is a copy of it."""
-    pb = w.packed_b.data_ptr()
-    c = w.__dict__.get("_struct")
-    if c is None or c.packed_b != pb:
-        ptr = lambda t: None if t is None else t.data_ptr()
-        c = ExpertsC(pb, w.packed_scales.data_ptr(), ptr(w.packed_zp), w.packed_rows.data_ptr(),
-                     None, w.E, w.N, w.K, w.block_size, _dtype_code(w.scale_dtype))
-        w.__dict__["_struct"] = c
+    """mnb_experts of w and a bias. The struct without a bias is kept with w,
+    for as long as its buffers are where they were; one with a bias is a copy."""
+    at = (w.packed_b.data_ptr(), w.packed_scales.data_ptr(),
+          None if w.packed_zp is None else w.packed_zp.data_ptr(), w.packed_rows.data_ptr())
+    kept = w.__dict__.get("_struct")
+    if kept is None or kept[0] != at:
+        kept = (at, ExpertsC(*at, None, w.E, w.N, w.K, w.block_size,
+                             _dtype_code(w.scale_dtype)))
+        w.__dict__["_struct"] = kept
+    c = kept[1]
     if w.packed_b.device != device:
         raise ValueError(f"the weights are on {w.packed_b.device}, the call runs on {device}")
     if bias is None:

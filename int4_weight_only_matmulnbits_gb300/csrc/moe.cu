@@ -13,6 +13,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
+#include <initializer_list>
 #include <utility>
 
 #include "mnb_common.cuh"
@@ -182,7 +183,7 @@ __device__ __forceinline__ uint32_t row_top(const void *A, bool f32, bool vec, i
 
 // What the products need ahead, for a few slots, in one launch. Block 0: the
 // router (or a table of experts) and the lists; the blocks after it: the
-// largest magnitude of an activation row each, and cleared counters.
+// largest magnitude of an activation row each, and cleared words.
 struct PrepArgs {
   const void *logits;    // the router, or null:
   const int32_t *table;  // experts of the slots
@@ -463,7 +464,7 @@ __global__ void __launch_bounds__(1024) convert_kernel(const ConvertArgs a) {
     if (at < routed) {
       if (tid == 0) {
         a.unscale[at] = exp2i(-shift);
-        if (a.norm1) a.norm1[at] = sum * 1.01f;  // above the exact sum for any K < 2^17
+        if (a.norm1) a.norm1[at] = sum * 1.01f;  // above the exact sum for any K < 2^26
       }
       if (a.hidden)
         for (int k = a.hidden_n + tid; k < a.hidden_ld; k += threads)
@@ -649,6 +650,38 @@ int ilog2(int x) {
   return r;
 }
 
+// Shared memory of a weight-streaming CTA: stage layout, and bytes of its
+// parts for groups of gt slots.
+struct StreamSmem {
+  int st_scale, st_zp, st_tile;
+  int64_t krow, sums, ring, terms;
+  int64_t red(int gt) const { return int64_t(2 * 2 * 8 * kTileN * 4) * gt; }
+  int64_t bytes(int gt) const {
+    return red(gt) + sums + ring + ceil_div(terms * gt * krow * 2, 128) * 128;
+  }
+};
+StreamSmem stream_smem(const ExpertStack &w, int terms) {
+  StreamSmem s{};
+  const int es = w.s_f32 ? 4 : 2;
+  const int64_t K64 = ceil_div(w.K, kChunkK);
+  // Scale blocks a stage can touch (blocks of up to 64 codes lie inside chunks).
+  const int nblk = w.bs <= kChunkK ? kStreamChunks * kChunkK / w.bs
+                                   : (kStreamChunks * kChunkK - 1) / w.bs + 2;
+  s.st_scale = kStreamChunks * kChunkBytes;
+  s.st_zp = s.st_scale + nblk * kTileN * es;
+  s.st_tile = s.st_zp + (w.z ? (nblk / 2 + 1) * 16 : 0);
+  s.krow = K64 * kChunkK + 16;
+  s.sums = terms == 1 ? K64 * std::max(1, kChunkK / w.bs) * 64 : 0;
+  s.ring = int64_t(8) * kStreamStages * 2 * s.st_tile;
+  s.terms = terms;
+  return s;
+}
+// Shared memory that lets n CTAs share an SM (1 KB of each is the system's).
+int64_t stream_room(int n) { return 228 * 1024 / n - 1536; }
+bool stream_fits(const ExpertStack &w, int terms) {
+  return stream_smem(w, terms).bytes(1) <= stream_room(1);
+}
+
 // Fills the geometry of a weight-streaming launch. `per_expert`: the most
 // slots an expert can have. false: not even one activation row fits.
 struct StreamPlan {
@@ -657,7 +690,7 @@ struct StreamPlan {
   bool zp = false, sf32 = false;
 };
 bool plan_stream(StreamPlan &pl, const ExpertStack &w, int mode, int terms, int64_t P,
-                 int64_t M, int top_k, int64_t per_expert) {
+                 int top_k, int64_t per_expert) {
   StreamParams &p = pl.p;
   pl.terms = terms;
   pl.zp = w.z != nullptr;
@@ -673,9 +706,7 @@ bool plan_stream(StreamPlan &pl, const ExpertStack &w, int mode, int terms, int6
   p.bs_log2 = ilog2(w.bs);
   p.npair = mode == kStreamGateUp ? p.N16 : (p.N16 + 1) / 2;
   p.P = static_cast<int>(P);
-  p.M = static_cast<int>(M);
   p.top_k = top_k;
-  const int es = w.s_f32 ? 4 : 2;
   // Warps per pair: what makes the longest run of work shortest, in chunks,
   // with the distinct experts that P random slots name; a step costs a warp
   // that has its pair to itself about five chunks more (it stores alone),
@@ -697,41 +728,30 @@ bool plan_stream(StreamPlan &pl, const ExpertStack &w, int mode, int terms, int6
   p.tpu = 8 / p.ksplit;
   p.tpu_log2 = ilog2(p.tpu);
   p.ns = static_cast<int>(ceil_div(p.npair, p.tpu));
-  // Scale blocks a stage can touch (blocks of up to 64 codes lie inside chunks).
-  const int nblk = w.bs <= kChunkK ? kStreamChunks * kChunkK / w.bs
-                                   : (kStreamChunks * kChunkK - 1) / w.bs + 2;
-  p.st_scale = kStreamChunks * kChunkBytes;
-  p.st_zp = p.st_scale + nblk * kTileN * es;
-  p.st_tile = p.st_zp + (pl.zp ? (nblk / 2 + 1) * 16 : 0);
+  const StreamSmem sm = stream_smem(w, terms);
+  p.st_scale = sm.st_scale;
+  p.st_zp = sm.st_zp;
+  p.st_tile = sm.st_tile;
   p.st_bytes = 2 * p.st_tile;
-  const int64_t krow = int64_t(p.K64) * kChunkK + 16;
-  const int64_t sums = terms == 1 ? int64_t(p.K64) * std::max(1, kChunkK / w.bs) * 64 : 0;
-  const int64_t ring = 8 * kStreamStages * p.st_bytes;
   // Slots per group: about twice the mean list, so that few experts need a
   // second pass over their weights, within what two CTAs per SM leave (one
   // CTA per SM when that is not enough for the mean).
   const int64_t mean = ceil_div(P, w.E);
   int want = 1;
   while (want < 8 && want < 2 * mean && want < per_expert) want *= 2;
-  // Shared memory that lets n CTAs share an SM (1 KB of each is the system's).
-  constexpr int64_t kTotal = 228 * 1024, kStatic = 1536;
-  auto room = [&](int n) { return kTotal / n - kStatic; };
-  auto bytes = [&](int gt) {
-    return sums + ring + 2 * 2 * 8 * kTileN * gt * 4 + (int64_t(terms) * gt * krow * 2 + 127) / 128 * 128;
-  };
   int gt = want;
-  while (gt > 1 && bytes(gt) > room(kStreamCtas) && gt > mean) gt /= 2;
-  while (gt > 1 && bytes(gt) > room(1)) gt /= 2;
-  if (bytes(gt) > room(1)) return false;
+  while (gt > 1 && sm.bytes(gt) > stream_room(kStreamCtas) && gt > mean) gt /= 2;
+  while (gt > 1 && sm.bytes(gt) > stream_room(1)) gt /= 2;
+  if (sm.bytes(gt) > stream_room(1)) return false;
   p.gt_log2 = ilog2(gt);
-  p.krow = static_cast<int>(krow);
+  p.krow = static_cast<int>(sm.krow);
   p.off_red = 0;
-  p.off_sums = 2 * 2 * 8 * kTileN * gt * 4;
-  p.off_ring = static_cast<int>(p.off_sums + sums);
-  p.off_x = static_cast<int>(p.off_ring + ring);
-  pl.smem = static_cast<int>(bytes(gt));
+  p.off_sums = static_cast<int>(sm.red(gt));
+  p.off_ring = static_cast<int>(p.off_sums + sm.sums);
+  p.off_x = static_cast<int>(p.off_ring + sm.ring);
+  pl.smem = static_cast<int>(sm.bytes(gt));
   int ctas = kStreamCtas;
-  while (pl.smem > room(ctas)) --ctas;
+  while (pl.smem > stream_room(ctas)) --ctas;
   const int64_t most = P * p.ns, slots = int64_t(sm_count()) * ctas;
   if (most > (int64_t(1) << 31) - 1) return false;
   pl.grid = static_cast<int>(std::min(most, slots));
@@ -858,9 +878,21 @@ ExpertsSpace experts_space(const ExpertsArgs &a) {
 // ---- tensor-core path: bf16 activations, many slots ---------------------------
 
 // From a mean of this many slots per expert on; fewer stream the weights past
-// groups of up to 8 slots.
+// groups of up to 8 slots. Both measured, streaming and tensor-core path, us:
+//   experts, top_k       mean 4              mean 8
+//   8, 2             25.6    31.1        37.9    31.6
+//   16, 4            21.6    24.1        36.1    24.7
+//   32, 4            75.8    84.8       100.5    89.2
+//   128, 8          151.2   165.8       221     172
+// A row too long for the streaming kernel's shared memory (K beyond some
+// 30 000) takes the tensor-core path as well.
 constexpr int kTileMeanSlots = 5;
-bool tile_path(bool a_f32, int64_t P, int E) { return !a_f32 && P >= int64_t(kTileMeanSlots) * E; }
+bool tile_path(bool a_f32, int64_t P, std::initializer_list<const ExpertStack *> w) {
+  if (a_f32) return false;
+  for (const ExpertStack *x : w)
+    if (P >= int64_t(kTileMeanSlots) * x->E || !stream_fits(*x, 1)) return true;
+  return false;
+}
 
 // Rows of partials start on 16 bytes.
 int64_t part_ld(int64_t N) { return ceil_div(N, 8) * 8; }
@@ -937,13 +969,11 @@ cudaError_t fill_tile(TileParams &p, int mode, const ExpertStack *const *w, int 
     p.ts[m] = TileScales{
         w[i]->rows, w[i]->rows + int64_t(w[i]->E) * ceil_div(w[i]->N, kTileN) * kTileN, s.bmax[i]};
   }
-  p.E = w0.E;
   p.N = w0.N;
   p.N16 = static_cast<int>(ceil_div(w0.N, kTileN));
   p.K64 = static_cast<int>(ceil_div(w0.K, kChunkK));
   p.nb = static_cast<int>(ceil_div(w0.K, w0.bs));
   p.nbz = (p.nb + 1) / 2 * 2;
-  p.bs_log2 = ilog2(w0.bs);
   p.ntile = static_cast<int>(ceil_div(w0.N, mode == kStreamGateUp ? 64 : 128));
   p.order = s.l.order;
   p.n_groups = s.l.n_groups;
@@ -1065,7 +1095,6 @@ void set_lists(StreamParams &p, const Lists &l) {
   p.order = l.order;
   p.n_groups = l.n_groups;
   p.groups = l.groups;
-  p.experts = l.experts;
   p.weights = l.weights;
 }
 
@@ -1108,7 +1137,7 @@ cudaError_t launch_moe_route(const RouteArgs &a, cudaStream_t stream) {
 size_t matmul_experts_workspace_bytes(const ExpertsArgs &a) {
   ExpertsArgs b = a;
   b.ws = nullptr;
-  if (tile_path(a.a_f32, a.M * a.top_k, a.w.E)) {
+  if (tile_path(a.a_f32, a.M * a.top_k, {&a.w})) {
     const ExpertStack *w[1] = {&a.w};
     return tile_space(nullptr, a.M * a.top_k, w, 1, false).bytes;
   }
@@ -1117,9 +1146,9 @@ size_t matmul_experts_workspace_bytes(const ExpertsArgs &a) {
 
 cudaError_t launch_matmul_experts(const ExpertsArgs &a, cudaStream_t stream) {
   const int64_t P = a.M * a.top_k, rows = a.per_slot ? P : a.M;
-  if (tile_path(a.a_f32, P, a.w.E)) return launch_experts_tile(a, stream);
+  if (tile_path(a.a_f32, P, {&a.w})) return launch_experts_tile(a, stream);
   StreamPlan pl;
-  if (!plan_stream(pl, a.w, kStreamProduct, a.a_f32 ? 2 : 1, P, a.M, a.top_k, P))
+  if (!plan_stream(pl, a.w, kStreamProduct, a.a_f32 ? 2 : 1, P, a.top_k, P))
     return cudaErrorNotSupported;
   const ExpertsSpace s = experts_space(a);
   const bool vec = vec_rows(a.A, a.w.K, a.a_f32 ? 4 : 2);
@@ -1165,7 +1194,7 @@ cudaError_t launch_matmul_experts(const ExpertsArgs &a, cudaStream_t stream) {
 size_t moe_workspace_bytes(const MoeArgs &a) {
   MoeArgs b = a;
   b.ws = nullptr;
-  if (tile_path(a.a_f32, a.M * a.top_k, a.gate.E)) {
+  if (tile_path(a.a_f32, a.M * a.top_k, {&a.gate, &a.down})) {
     const ExpertStack *w[3] = {&a.gate, &a.up, &a.down};
     return tile_space(nullptr, a.M * a.top_k, w, 3, true).bytes;
   }
@@ -1175,12 +1204,12 @@ size_t moe_workspace_bytes(const MoeArgs &a) {
 cudaError_t launch_moe(const MoeArgs &a, cudaStream_t stream) {
   const int64_t P = a.M * a.top_k;
   const bool few = P <= kFewSlots;
-  if (tile_path(a.a_f32, P, a.gate.E)) return launch_moe_tile(a, stream);
+  if (tile_path(a.a_f32, P, {&a.gate, &a.down})) return launch_moe_tile(a, stream);
   const MoeSpace s = moe_space(a);
   StreamPlan up, down;
   const int terms = a.a_f32 ? 2 : 1;
-  if (!plan_stream(up, a.gate, kStreamGateUp, terms, P, a.M, a.top_k, a.M) ||
-      !plan_stream(down, a.down, kStreamDown, terms, P, a.M, a.top_k, a.M))
+  if (!plan_stream(up, a.gate, kStreamGateUp, terms, P, a.top_k, a.M) ||
+      !plan_stream(down, a.down, kStreamDown, terms, P, a.top_k, a.M))
     return cudaErrorNotSupported;
   // Both launches use the lists: groups of the size that fits both.
   up.p.gt_log2 = down.p.gt_log2 = std::min(up.p.gt_log2, down.p.gt_log2);

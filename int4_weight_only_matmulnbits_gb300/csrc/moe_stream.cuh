@@ -202,7 +202,8 @@ __global__ void __launch_bounds__(kThreads, kStreamCtas) stream_kernel(const Str
     else static_cast<uint16_t *>(p.Y)[i] = static_cast<uint16_t>(bf16_bits(v));
   };
   if (p.mode == kStreamProduct) {
-    for (int i = p.offsets[p.E] + blockIdx.x; i < p.P; i += gridDim.x) {
+    // (Unsigned: the last step may pass 2^31.)
+    for (unsigned i = p.offsets[p.E] + blockIdx.x; i < unsigned(p.P); i += gridDim.x) {
       const int64_t row = int64_t(order[i]) * p.N;
       for (int n = tid; n < p.N; n += kThreads) store(row + n, 0.f);
     }

@@ -34,10 +34,10 @@ struct StreamParams {
   int a_f32, a_vec;  // a_vec: rows are 16-byte aligned
   int per_slot;
   int64_t ld;
-  int P, M, top_k;
+  int P, top_k;
   const uint32_t *tops;  // bits of the largest magnitude of each row
   // Lists.
-  const int32_t *offsets, *order, *n_groups, *experts;
+  const int32_t *offsets, *order, *n_groups;
   const SlotGroup *groups;
   const float *weights;  // [P] (gate and up, down)
   // Outputs: Y [P, N] (product), hidden rows [P, ldh] (gate and up), partials

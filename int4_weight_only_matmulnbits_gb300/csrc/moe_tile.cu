@@ -276,6 +276,10 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         }
       }
     }
+    // Given up: the copies in flight land before the CTA leaves.
+    if (!ok)
+      for (int i = max(0, it - kBStages); i < it; ++i)
+        mbar_sleep(bfull + i % kBStages, (i / kBStages) & 1);
   } else if (warp == kMmaWarp) {
     bool ok = true;
     if (rank == 0) {  // ---- MMAs of the pair ---------------------------------------------

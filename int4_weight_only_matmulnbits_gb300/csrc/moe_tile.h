@@ -25,7 +25,7 @@ struct TileParams {
   int mode;
   StreamMat w[2];
   TileScales ts[2];
-  int E, N, N16, K64, nb, nbz, bs_log2;
+  int N, N16, K64, nb, nbz;
   int ntile;  // column tiles of an expert: 64 columns (gate and up) or 128
   // Lists: slots by expert; places count along the order.
   const int32_t *order, *n_groups;

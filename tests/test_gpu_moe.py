@@ -1,11 +1,15 @@
 """GPU parity of the mixture-of-experts operators (mnb_moe_route, mnb_matmul_experts, mnb_moe)
 against their definition in 64 bits (moe_reference.py)."""
+import copy
+import dataclasses
 import math
+import threading
 
 import pytest
 import torch
 
 import int4_weight_only_matmulnbits_gb300 as mnb
+from int4_weight_only_matmulnbits_gb300 import binding
 
 from . import moe_reference as ref
 
@@ -306,6 +310,36 @@ def test_layer_all_tokens_one_expert(dev, M):
     run_layer(dev, X, logits, ws, 2, what="skewed")
 
 
+@pytest.mark.parametrize("M", [1, 9, 170])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_layer_many_experts(dev, M, dtype):
+    """As many choices as the operators take, of nearly as many experts."""
+    X, logits, ws = layer_inputs(dev, M, 1000, 32, 72, 40, 32, dtype, seed=M)
+    run_layer(dev, X, logits, ws, 32, what=f"M{M}")
+
+
+@pytest.mark.parametrize("M", [1, 7])
+def test_long_rows(dev, M):
+    """Rows too long for the streaming kernel's shared memory: bf16 ones go to the tensor cores
+    at any number of slots, fp32 ones are refused."""
+    K, N, bs = 66000, 20, 32
+    g = torch.Generator().manual_seed(M)
+    w, _, W = pack(dev, stack(g, 2, N, K, bs, BF16, False, False), N, K, bs)
+    A = torch.randn(M, K, generator=g).to(BF16).to(dev)
+    t = torch.randint(0, 2, (M, 1), generator=g, dtype=torch.int32).to(dev)
+    R, err = ref.products(A.double().unsqueeze(1), W, t, None, BF16)
+    ref.check(mnb.mnb_matmul_experts(A, w, t), R, err, "product")
+    with pytest.raises(mnb.MnbError) as e:
+        mnb.mnb_matmul_experts(A.float(), w, t)
+    assert e.value.status == binding.MNB_ERR_UNSUPPORTED
+    X, logits, ws = layer_inputs(dev, M, 2, 1, 24, K, bs, BF16, seed=M)
+    run_layer(dev, X, logits, ws, 1, what="layer")
+    packed = [w for w, _, _ in ws]
+    with pytest.raises(mnb.MnbError) as e:
+        mnb.mnb_moe(X.float(), logits, *packed, 1)
+    assert e.value.status == binding.MNB_ERR_UNSUPPORTED
+
+
 @pytest.mark.parametrize("M", [1, 7, 140])
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_layer_is_its_parts(dev, M, dtype):
@@ -386,6 +420,57 @@ def test_other_stream(dev, M):
     outs = [mnb.mnb_moe(X, logits, *packed, k, stream=st) for _ in range(8)]
     st.synchronize()
     assert all(torch.equal(o, Y) for o in outs)
+
+
+def test_calls_at_once(dev):
+    """Two threads, each on a stream of its own, with calls of either kernel in flight."""
+    k = 2
+    X, logits, ws = layer_inputs(dev, 140, 8, k, 256, 192, 32, BF16)
+    packed = [w for w, _, _ in ws]
+    want = {M: mnb.mnb_moe(X[:M], logits[:M], *packed, k) for M in (1, 7, 140)}
+    torch.cuda.synchronize()
+    got, errors = [], []
+
+    def work(sizes):
+        try:
+            st = torch.cuda.Stream()
+            outs = [(M, mnb.mnb_moe(X[:M], logits[:M], *packed, k, stream=st))
+                    for _ in range(20) for M in sizes]
+            st.synchronize()
+            got.extend(outs)
+        except Exception as e:  # noqa: BLE001 (reported below)
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(s,)) for s in ((1, 140), (140, 7))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors and len(got) == 80
+    assert all(torch.equal(Y, want[M]) for M, Y in got)
+
+
+def test_copied_and_replaced_stacks(dev):
+    """A copy of a packed stack is a packed weight of its own (its header has to be registered,
+    as any restored weight's), and a stack keeps what it was made with."""
+    g = torch.Generator().manual_seed(1)
+    (a, _, Wa), (b, _, Wb) = (pack(dev, stack(g, 3, 32, 64, 32, F32, True, False), 32, 64, 32)
+                              for _ in range(2))
+    A = torch.randn(4, 64, generator=g).to(dev)
+    t = torch.randint(0, 3, (4, 2), generator=g, dtype=torch.int32).to(dev)
+    Ya, Yb = mnb.mnb_matmul_experts(A, a, t), mnb.mnb_matmul_experts(A, b, t)
+    other = copy.deepcopy(a)
+    with pytest.raises(mnb.MnbError) as e:
+        mnb.mnb_matmul_experts(A, other, t)
+    assert e.value.status == binding.MNB_ERR_LAYOUT
+    mnb.mnb_packed_register(other.packed_b, mnb.mnb_packed_read_header(other.packed_b))
+    assert torch.equal(mnb.mnb_matmul_experts(A, other, t), Ya)
+    mnb.mnb_packed_forget(other.packed_b)
+    with pytest.raises(dataclasses.FrozenInstanceError):
+        a.packed_scales = b.packed_scales
+    c = dataclasses.replace(a, packed_b=b.packed_b, packed_scales=b.packed_scales,
+                            packed_zp=b.packed_zp, packed_rows=b.packed_rows)
+    assert torch.equal(mnb.mnb_matmul_experts(A, c, t), Yb)
 
 
 def test_programmatic_launch_off(dev):
