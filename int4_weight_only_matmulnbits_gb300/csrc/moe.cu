@@ -880,13 +880,13 @@ ExpertsSpace experts_space(const ExpertsArgs &a) {
 // From a mean of this many slots per expert on; fewer stream the weights past
 // groups of up to 8 slots. Both measured, streaming and tensor-core path, us:
 //   experts, top_k       mean 4              mean 8
-//   8, 2             25.6    31.1        37.9    31.6
-//   16, 4            21.6    24.1        36.1    24.7
-//   32, 4            75.8    84.8       100.5    89.2
-//   128, 8          151.2   165.8       221     172
+//   8, 2             23.3    31.4        31.9    31.8
+//   16, 4            17.4    24.3        24.1    25.1
+//   32, 4            69.2    84.4        88.3    89.4
+//   128, 8          143.5   165.5       204.2   171.3
 // A row too long for the streaming kernel's shared memory (K beyond some
 // 30 000) takes the tensor-core path as well.
-constexpr int kTileMeanSlots = 5;
+constexpr int kTileMeanSlots = 6;
 bool tile_path(bool a_f32, int64_t P, std::initializer_list<const ExpertStack *> w) {
   if (a_f32) return false;
   for (const ExpertStack *x : w)
