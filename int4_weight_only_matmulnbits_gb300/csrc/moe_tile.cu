@@ -20,10 +20,8 @@
 //    bf16 weight's. A code's fp16 form costs one mask (see the unpacking).
 //  * B are fp16 activation rows, scaled by a power of two per row, in the
 //    order of the lists: TMA tiles of 32 rows x 64 k, 128-byte swizzle. Each
-//    CTA loads half of a group's rows: with 128 weight rows a CTA and all of
-//    the slots, activations would take 64 bytes a cycle and SM, more than L2
-//    gives (measured: 593 us instead of 476 for 4096 tokens of 8 out of 128
-//    experts, 2560 -> 768 -> 2560).
+//    CTA of a pair loads half of a group's rows: alone, with 128 weight rows
+//    and all of the slots, it would take 64 bytes of activations a cycle.
 //  * Hidden values leave as fp16, the row scaled so that a bound of it (15 s
 //    times the 1-norm of x, for gate and for up) fits: typical values then
 //    lie 15 or so octaves above fp16's smallest normal. Down partials
@@ -32,6 +30,16 @@
 //    ring of asynchronous copies, in two groups that alternate stages; warps
 //    16-23 store; one warp each issues the TMA loads, issues the MMAs, and
 //    gathers what a unit's columns need for the epilogue.
+//  * What bounds it is issue slots: per 16 x 64 chunk a warp takes about 117
+//    instructions (23 to fetch, 48 to unpack, 20 of them for the scales, the
+//    rest for a stage's waits, store and arrival; 140 with zero points), and
+//    57 % of the slots are taken, four unpacking warps a scheduler leaving
+//    gaps. Measured, 8 out of 128 experts, 2560 -> 768 -> 2560, 4096 tokens:
+//    gate and up 205 us = 1260 TFLOP/s, tensor pipe 60 % busy, down 142 us =
+//    910; 6 out of 64, 2560 -> 1408 -> 2560, 192 tokens: 101 us = 2.4 TB/s of
+//    weights, and 56. Groups of 64 slots with 6 TMEM stages and 8 activation
+//    stages, for few slots per expert, were no faster (166.6 against 165.5 us
+//    for the layer at a mean of 4, 183.0 against 181.0 at 16).
 #include <cuda_fp16.h>
 
 #include <algorithm>
