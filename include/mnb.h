@@ -821,9 +821,19 @@ MNB_API mnb_status mnb_moe_route(const void *logits, mnb_dtype logits_dtype, int
  *  [M, top_k] DEVICE; w HOST.
  *  workspace: as mnb_moe_route's, of mnb_matmul_experts_workspace_size
  *  bytes (0 for arguments the call refuses).
- * Accumulation is fp32. Errors: as mnb_matmul, and MNB_ERR_SHAPE for top_k
- * < 1, M * top_k past 2^31 - 1 or a workspace too small,
- * MNB_ERR_UNSUPPORTED for E > MNB_MOE_MAX_EXPERTS.
+ * Accumulation is fp32. Precision: activation rows are scaled by a power of
+ * two and taken to fp16, fp32 ones in two parts (22 bits), bf16 ones exactly
+ * down to 2^-28 of the row's largest magnitude. Weights are exact, but for
+ * bf16 activations and six or more slots per expert on average they are
+ * rounded once to fp16 (2^-11; small scales to 2^-15 of their row's largest).
+ * Magnitudes of scales up to 2^100. An infinity or NaN in a row of A makes
+ * the outputs of its slots non-finite (not always as an exact sum would be)
+ * and touches no other.
+ * fp32 activations stream the weights for every eight slots: meant for decode
+ * and small batches.
+ * Errors: as mnb_matmul, and MNB_ERR_SHAPE for top_k < 1, M * top_k past
+ * 2^31 - 1 or a workspace too small, MNB_ERR_UNSUPPORTED for E >
+ * MNB_MOE_MAX_EXPERTS and for fp32 rows beyond some 40 000 elements.
  */
 MNB_API size_t mnb_matmul_experts_workspace_size(int64_t M, int top_k, const mnb_experts *w,
                                                  mnb_dtype a_dtype, int a_per_slot);
@@ -842,7 +852,11 @@ MNB_API mnb_status mnb_matmul_experts(const void *A, int a_per_slot, const mnb_e
  *  weights H x I. A token without an expert gets a row of zeros.
  *  workspace: as mnb_moe_route's, of mnb_moe_workspace_size bytes (0 for
  *  arguments the call refuses).
- * Accumulation is fp32. Errors: as mnb_moe_route and mnb_matmul_experts;
+ * Accumulation and SiLU are fp32. Hidden rows are held in fp32, or (bf16 X,
+ * six or more slots per expert on average) in fp16 relative to a bound of the
+ * row: (15 max|s| |x|_1 + max|bg|) for gate times the same for up; values
+ * more than 2^29 below it lose bits. Errors: as mnb_moe_route and
+ * mnb_matmul_experts, for either width of the layer;
  * MNB_ERR_SHAPE when the three stacks do not fit together.
  */
 MNB_API size_t mnb_moe_workspace_size(int64_t M, int top_k, const mnb_experts *gate,
