@@ -97,6 +97,20 @@ def test_route(dev, M, E, k, dtype, normalize):
     check_route(torch.randn(M, E, generator=g).to(dtype).to(dev), k, normalize)
 
 
+@pytest.mark.parametrize("E", [4, 60, 64, 96, 128, 200, 256])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_route_alignment(dev, E, dtype):
+    """Rows that start off the piece a lane loads give what aligned ones do, ties included."""
+    g = torch.Generator().manual_seed(E)
+    x = (torch.randint(-8, 8, (9, E), generator=g) / 4).to(dtype).to(dev)
+    want = check_route(x, 4, True)
+    for off in (1, 2, 4):
+        room = torch.zeros(9 * E + off, dtype=dtype, device=dev)
+        y = room[off:].view(9, E)
+        y.copy_(x)
+        assert all(torch.equal(a, b) for a, b in zip(want, mnb.mnb_moe_route(y, 4)))
+
+
 @pytest.mark.parametrize("M", [4, 300])
 @pytest.mark.parametrize("normalize", [True, False])
 def test_route_ties(dev, M, normalize):
