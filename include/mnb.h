@@ -855,7 +855,8 @@ MNB_API mnb_status mnb_matmul_experts(const void *A, int a_per_slot, const mnb_e
  * Accumulation and SiLU are fp32. Hidden rows are held in fp32, or (bf16 X,
  * six or more slots per expert on average) in fp16 relative to a bound of the
  * row: (15 max|s| |x|_1 + max|bg|) for gate times the same for up; values
- * more than 2^29 below it lose bits. Errors: as mnb_moe_route and
+ * more than 2^29 below it lose bits; the down sums of a slot are then fp16
+ * relative to 15 max|s| I max|h| of its hidden row. Errors: as mnb_moe_route and
  * mnb_matmul_experts, for either width of the layer;
  * MNB_ERR_SHAPE when the three stacks do not fit together.
  */

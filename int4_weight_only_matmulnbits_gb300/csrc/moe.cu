@@ -426,6 +426,7 @@ struct ConvertArgs {
   int N;
   uint16_t *hidden;
   int hidden_n, hidden_ld;
+  uint32_t *hidden_max;  // cleared by place (hidden given)
 };
 // A block of about a thread per 8 columns, for either kernel of rows.
 int row_threads(int64_t n) {
@@ -472,6 +473,7 @@ __global__ void __launch_bounds__(1024) convert_kernel(const ConvertArgs a) {
         a.unscale[at] = exp2i(-shift);
         if (a.norm1) a.norm1[at] = sum * 1.01f;  // above the exact sum for any K < 2^26
       }
+      if (a.hidden && tid == 0) a.hidden_max[at] = 0;
       if (a.hidden)
         for (int k = a.hidden_n + tid; k < a.hidden_ld; k += threads)
           a.hidden[int64_t(at) * a.hidden_ld + k] = 0;
@@ -919,6 +921,7 @@ struct TileSpace {
   uint16_t *hidden, *part;
   float *h_unscale, *p_unscale;
   int32_t *h_shift;
+  uint32_t *h_max;
   size_t bytes;
 };
 TileSpace tile_space(unsigned char *ws, int64_t P, const ExpertStack *const *w, int stacks,
@@ -946,6 +949,7 @@ TileSpace tile_space(unsigned char *ws, int64_t P, const ExpertStack *const *w, 
     s.h_unscale = c.take<float>(P);
     s.p_unscale = c.take<float>(P);
     s.h_shift = c.take<int32_t>(P);
+    s.h_max = c.take<uint32_t>(P);
   }
   s.bytes = c.used;
   return s;
@@ -1053,6 +1057,7 @@ cudaError_t launch_moe_tile(const MoeArgs &a, cudaStream_t stream) {
   c.hidden = s.hidden;
   c.hidden_n = a.gate.N;
   c.hidden_ld = static_cast<int>(k_pad(a.gate.N));
+  c.hidden_max = s.h_max;
   e = launch_pdl(convert_kernel, static_cast<unsigned>(a.M), row_threads(c.Kp), 0, a.pdl, stream, c);
   if (e != cudaSuccess) return e;
   TileParams up{}, down{};
@@ -1064,12 +1069,14 @@ cudaError_t launch_moe_tile(const MoeArgs &a, cudaStream_t stream) {
   up.ldh = c.hidden_ld;
   up.out_unscale = s.h_unscale;
   up.out_shift = s.h_shift;
+  up.hidden_max = s.h_max;
   e = launch_tile(up, a.gate.z != nullptr, a.gate.s_f32, a.gate.bs, a.pdl, stream);
   if (e != cudaSuccess) return e;
   e = fill_tile(down, kStreamDown, w, 2, s, s.hidden, P);
   if (e != cudaSuccess) return e;
   down.unscale = s.h_unscale;
   down.shift = s.h_shift;
+  down.hidden_max = s.h_max;
   down.part = s.part;
   down.ldp = part_ld(a.down.N);
   down.out_unscale = s.p_unscale;

@@ -24,8 +24,9 @@
 //    and all of the slots, it would take 64 bytes of activations a cycle.
 //  * Hidden values leave as fp16, the row scaled so that a bound of it (15 s
 //    times the 1-norm of x, for gate and for up) fits: typical values then
-//    lie 15 or so octaves above fp16's smallest normal. Down partials
-//    likewise; they are added per token by a kernel that follows.
+//    lie 15 or so octaves above fp16's smallest normal. Down partials are
+//    fp16 too, scaled by a bound from their hidden row's largest value (15 s
+//    K max|h|); they are added per token by a kernel that follows.
 //  * Warps 0-15 unpack, each its own tile's codes and scales from a private
 //    ring of asynchronous copies, in two groups that alternate stages; warps
 //    16-23 store; one warp each issues the TMA loads, issues the MMAs, and
@@ -381,9 +382,11 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
             p.out_shift[place] = shift;
           }
         } else if (p.mode == kStreamDown) {
-          // |sum| <= 15 s K 2^15 / 2^shift, and the bias.
-          const int e = max(expo(15.f * most(p.ts[0].smax) * static_cast<float>(p.K64 * kChunkK)) +
-                                15 - p.shift[place],
+          // |sum| <= 15 s K max|h| / 2^shift, and the bias.
+          const float h = __half2float(
+              __ushort_as_half(static_cast<unsigned short>(p.hidden_max[place])));
+          const int e = max(expo(15.01f * most(p.ts[0].smax) *
+                                 static_cast<float>(p.K64 * kChunkK) * h) - p.shift[place],
                             expo(most(p.ts[0].bmax))) + 1;
           const int shift = max(-126, min(126, 15 - e));
           a *= exp2i(shift);
@@ -616,6 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
           // what the other half-warp lacks.
           const int mine0 = c0 + (up ? 16 : 0);
           uint16_t *dst = p.hidden + int64_t(sg.first + mine0 + (lane & 1)) * p.ldh + (row & ~1);
+          uint32_t top[8];  // magnitudes: two rows of every other column
 #pragma unroll
           for (int i = 0; i < 16; i += 2) {
             const float4 ck = *reinterpret_cast<const float4 *>(&cl.ab[mine0 + i]);
@@ -635,7 +639,23 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
             const uint32_t w = pair_rows(pack_f16x2(h[0], h[1]));
             if ((row & ~1) < p.N && mine0 + i + (lane & 1) < sg.cols)
               *reinterpret_cast<uint32_t *>(dst + i * p.ldh) = w;
+            top[i / 2] = (row & ~1) < p.N ? w & 0x7FFF7FFFu : 0u;
           }
+          // Each column's largest over the 16 rows: at each step a lane sends
+          // the half of its columns that the other lane goes on with.
+#pragma unroll
+          for (int n2 = 4; n2 >= 1; n2 /= 2) {
+            const bool high = lane & (2 * n2);
+#pragma unroll
+            for (int q = 0; q < n2; ++q) {
+              const uint32_t got =
+                  __shfl_xor_sync(0xffffffffu, high ? top[q] : top[n2 + q], 2 * n2);
+              top[q] = f16x2_max(high ? top[n2 + q] : top[q], got);
+            }
+          }
+          const int c = mine0 + (lane & 15);
+          const uint32_t most = max(top[0] & 0xFFFFu, top[0] >> 16);
+          if (c < sg.cols && most) atomicMax(p.hidden_max + sg.first + c, most);
         } else if (p.mode == kStreamProduct) {
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {

@@ -43,6 +43,9 @@ struct TileParams {
   int y_pairs;  // rows of Y start on 4 bytes
   float *out_unscale;
   int32_t *out_shift;
+  // Largest magnitude of each hidden row as stored (fp16 bits), by place: raised
+  // by gate and up (zeros before), read by down.
+  uint32_t *hidden_max;
 };
 
 cudaError_t launch_tile(const TileParams &p, bool zp, bool sf32, int bs, bool pdl,

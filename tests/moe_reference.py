@@ -25,7 +25,7 @@ choose:
     below 2^-14 there is within 2^-25, at most ROW = 2^-15 of the row's largest scale. The layer's
     down sums may leave as fp16 before they are added (2^-11), scaled by a bound of theirs: at
     most 2^-25 of 2^e / 2^15, where 2^e is at most four times twice the bound 15 s K' times the
-    hidden bound (K' = K rounded up to 64) or the bias.
+    hidden row's largest value (K' = K rounded up to 64) or the bias.
 """
 import torch
 
@@ -139,13 +139,14 @@ def layer(X, weights, experts, Wg, Wu, Wd, bg, bu, bd, dtype):
                                 + (0 if b is None else b[e].double().abs().max()))
         cap[m, j] = one(Wg, bg) * one(Wu, bu)
     y, ey = products(h, Wd, experts, bd, dtype, cap)
+    top = (h.abs() + eh).amax(2)
     Wabs = Wd.W.abs()
     for e in range(Wabs.shape[0]):
         m, j = torch.nonzero(experts == e, as_tuple=True)
         if len(m):
             ey[m, j] += eh[m, j] @ Wabs[e].T * 1.01
             if dtype == torch.bfloat16:
-                most = 8 * (16 * Wd.S[e].abs().max() * (Wabs.shape[2] + 63) * cap[m, j]
+                most = 8 * (16 * Wd.S[e].abs().max() * (Wabs.shape[2] + 63) * top[m, j]
                             + (0 if bd is None else bd[e].double().abs().max()))
                 ey[m, j] += 2.0 ** -11 * (y[m, j].abs() + ey[m, j]) + 2.0 ** -40 * most.unsqueeze(1)
     w = weights.to(y.device).unsqueeze(2)

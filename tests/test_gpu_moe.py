@@ -302,6 +302,24 @@ def test_layer_larger(dev, M, k, E, H, I, bs, dtype):
     run_layer(dev, *x, k, what=f"M{M}")
 
 
+@pytest.mark.parametrize("M", [3, 140])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_layer_scale_outliers(dev, M, dtype):
+    """One block of each expert's three weights is 64 times as large as the others, and small
+    activations with one large one: the bounds that values are scaled by lie far above them."""
+    E, k, H, I, bs = 6, 2, 320, 256, 32
+    g = torch.Generator().manual_seed(M)
+    ws = []
+    for N, K in ((I, H), (I, H), (H, I)):
+        B, s, z, b = stack(g, E, N, K, bs, dtype, False, False)
+        s[:, N // 3, 1] *= 64
+        ws.append(pack(dev, (B, s, z, b), N, K, bs))
+    X = torch.randn(M, H, generator=g) * 0.05
+    X[:, 7] = 20
+    logits = torch.randn(M, E, generator=g).to(dev)
+    run_layer(dev, X.to(dtype).to(dev), logits, ws, k, what="outliers")
+
+
 @pytest.mark.parametrize("M", [3, 12, 140])
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_layer_masked_tokens(dev, M, dtype):
