@@ -320,6 +320,30 @@ def test_layer_scale_outliers(dev, M, dtype):
     run_layer(dev, X.to(dtype).to(dev), logits, ws, k, what="outliers")
 
 
+@pytest.mark.parametrize("M", [3, 140])
+@pytest.mark.parametrize("factor", [1, 16])
+def test_layer_outliers_cost_no_bits(dev, M, factor):
+    """Scales of a block `factor` times the others, met by zero activations: what is left keeps
+    its precision. Norm-wise: the output's rounding to bf16 is at most 2^-8 of each element; the
+    roundings of weights and hidden values (2^-11 each, twice) have random signs and grow no
+    more than what they belong to: 2^-8 + 4 2^-11 of the result's norm."""
+    E, k, H, I, bs = 6, 2, 1024, 768, 32
+    g = torch.Generator().manual_seed(M)
+    ws = []
+    for N, K in ((I, H), (I, H), (H, I)):
+        B, s, z, b = stack(g, E, N, K, bs, BF16, False, False)
+        s[:, N // 3, 1] *= factor
+        ws.append(pack(dev, (B, s, z, b), N, K, bs))
+    X = (torch.randn(M, H, generator=g) * 0.05).to(BF16).to(dev)
+    X[:, 32:64] = 0
+    logits = torch.randn(M, E, generator=g).to(dev)
+    weights, experts, _, _ = ref.route(logits, k, True)
+    R, _ = ref.layer(X, weights, experts.to(dev), *[W for _, _, W in ws], None, None, None, BF16)
+    err = mnb.mnb_moe(X, logits, *[w for w, _, _ in ws], k).double() - R
+    plain = torch.arange(H, device=dev) != H // 3  # the row with the large scale has its own size
+    assert err[:, plain].norm() <= (2.0 ** -8 + 4 * 2.0 ** -11) * R[:, plain].norm()
+
+
 @pytest.mark.parametrize("M", [3, 12, 140])
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_layer_masked_tokens(dev, M, dtype):
