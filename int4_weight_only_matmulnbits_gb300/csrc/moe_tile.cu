@@ -388,7 +388,9 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
           const int e = max(expo(15.01f * most(p.ts[0].smax) *
                                  static_cast<float>(p.K64 * kChunkK) * h) - p.shift[place],
                             expo(most(p.ts[0].bmax))) + 1;
-          const int shift = max(-126, min(126, 15 - e));
+          // a = 2^(shift - p.shift) stays finite: a hidden row of zeros, or an
+          // expert of zero scales, has a bound of 0, and 0 * inf would be NaN.
+          const int shift = max(-126, min(min(126, 126 + p.shift[place]), 15 - e));
           a *= exp2i(shift);
           b = p.weights[id] * exp2i(shift);
           if (u % np == 0 && rank == 0) p.out_unscale[place] = exp2i(-shift);

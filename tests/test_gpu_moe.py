@@ -366,6 +366,47 @@ def test_layer_all_tokens_one_expert(dev, M):
     run_layer(dev, X, logits, ws, 2, what="skewed")
 
 
+@pytest.mark.parametrize("M", [9, 140])
+@pytest.mark.parametrize("H", [128, 2560])
+@pytest.mark.parametrize("gap", [20.0, 60.0, 150.0, math.inf])
+@pytest.mark.parametrize("normalize", [True, False])
+def test_layer_negligible_weights(dev, M, H, gap, normalize):
+    """Chosen experts whose weight is tiny, underflows, or is exactly 0 beside a logit of +inf
+    add (next to) nothing: their weighted hidden rows vanish, the tokens' rows do not."""
+    X, logits, ws = layer_inputs(dev, M, 6, 2, H, 192, 32, BF16, seed=M + H)
+    logits[:, 4] += gap
+    run_layer(dev, X, logits, ws, 2, normalize, what=f"H{H} gap {gap}")
+
+
+@pytest.mark.parametrize("M", [9, 140])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("H", [128, 2560])
+@pytest.mark.parametrize("bias", [False, True])
+def test_layer_zero_experts(dev, M, dtype, H, bias):
+    """Experts whose scales are all zero in one of the three weights, or in all of them."""
+    E, k, I, bs = 6, 2, 192, 32
+    g = torch.Generator().manual_seed(M + H)
+    ws = []
+    for i, (N, K) in enumerate(((I, H), (I, H), (H, I))):
+        B, s, z, b = stack(g, E, N, K, bs, dtype, False, bias)
+        s[i] = s[4] = 0
+        ws.append(pack(dev, (B, s, z, b), N, K, bs))
+    X = torch.randn(M, H, generator=g).to(dtype).to(dev)
+    run_layer(dev, X, torch.randn(M, E, generator=g).to(dev), ws, k, what=f"H{H}")
+
+
+@pytest.mark.parametrize("M", [9, 140])
+@pytest.mark.parametrize("H", [128, 2560])
+@pytest.mark.parametrize("bias_down", [False, True])
+def test_layer_hidden_rows_vanish(dev, M, H, bias_down):
+    """Gates so negative that SiLU underflows: hidden rows of zeros under ordinary weights."""
+    X, logits, ws = layer_inputs(dev, M, 6, 2, H, 192, 32, BF16, bias=True, seed=M + H)
+    (wg, bg, Wg), (wu, bu, Wu), (wd, bd, Wd) = ws
+    bg[1::2] = -400.0
+    run_layer(dev, X, logits, ((wg, bg, Wg), (wu, bu, Wu), (wd, bd if bias_down else None, Wd)),
+              2, what=f"H{H}")
+
+
 @pytest.mark.parametrize("M", [1, 9, 170])
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_layer_many_experts(dev, M, dtype):
