@@ -824,8 +824,10 @@ MNB_API mnb_status mnb_moe_route(const void *logits, mnb_dtype logits_dtype, int
  * Accumulation is fp32. Precision: activation rows are scaled by a power of
  * two and taken to fp16, fp32 ones in two parts (22 bits), bf16 ones exactly
  * down to 2^-28 of the row's largest magnitude. Weights are exact, but for
- * bf16 activations and six or more slots per expert on average they are
- * rounded once to fp16 (2^-11; small scales to 2^-15 of their row's largest).
+ * bf16 activations and six or more slots per expert on average, or rows too
+ * long for the kernel of fewer slots (25 000 to 59 000 elements, by block size
+ * and scale type), they are rounded once to fp16 (2^-11; small scales to 2^-15
+ * of their row's largest).
  * Magnitudes of scales up to 2^100. An infinity or NaN in a row of A makes
  * the outputs of its slots non-finite (not always as an exact sum would be)
  * and touches no other.
@@ -852,12 +854,14 @@ MNB_API mnb_status mnb_matmul_experts(const void *A, int a_per_slot, const mnb_e
  *  weights H x I. A token without an expert gets a row of zeros.
  *  workspace: as mnb_moe_route's, of mnb_moe_workspace_size bytes (0 for
  *  arguments the call refuses).
- * Accumulation and SiLU are fp32. Hidden rows are held in fp32, or (bf16 X,
- * six or more slots per expert on average) in fp16 relative to a bound of the
- * row: (15 max|s| |x|_1 + max|bg|) for gate times the same for up; values
- * more than 2^29 below it lose bits; the down sums of a slot are then fp16
- * relative to 15 max|s| I max|h| of its hidden row. Errors: as mnb_moe_route and
- * mnb_matmul_experts, for either width of the layer;
+ * Accumulation and SiLU are fp32. Weighted hidden rows r_j h_j are stored in
+ * fp32; the down product scales each by its own largest value and takes it
+ * in two fp16 parts (fp32 X) or one (bf16 X: one rounding of 2^-11). Where
+ * mnb_matmul_experts rounds weights to fp16, so does the layer, and a slot's
+ * down sums are held in fp16 (2^-11 each; small ones to 2^-37 of
+ * 15 max|s| I max|r_j h_j| + r_j max|bd|) until they are added in fp32.
+ * Errors: as mnb_moe_route and mnb_matmul_experts, for either width of the
+ * layer;
  * MNB_ERR_SHAPE when the three stacks do not fit together.
  */
 MNB_API size_t mnb_moe_workspace_size(int64_t M, int top_k, const mnb_experts *gate,

@@ -410,9 +410,8 @@ __global__ void __launch_bounds__(kPlaceThreads)
 // bf16 activation rows as fp16, one copy for each routed slot, at the slot's
 // place: row m of A [M, K] for slots m * copies .. (copies = top_k, or 1
 // with a row per slot). A block per row. Also per place: what undoes the
-// row's scale, and (norm1 given) a bound of the row's 1-norm. Rows of Y of
-// slots without an expert are cleared (Y given), and so are the columns
-// hidden_n .. hidden_ld of the hidden rows. Bound by the copies' writes: 4096
+// row's scale. Rows of Y of slots without an expert are cleared (Y given).
+// Bound by the copies' writes: 4096
 // rows of 2560, 8 copies, 189 MB in 32 us = 5.9 TB/s. (Copies, so that a
 // group's rows are one TMA tile: a gather by row would issue 8 times as many.)
 struct ConvertArgs {
@@ -421,62 +420,52 @@ struct ConvertArgs {
   const int32_t *place, *offsets;
   int E;
   uint16_t *out;
-  float *unscale, *norm1;
+  float *unscale;
   uint16_t *Y;
   int N;
-  uint16_t *hidden;
-  int hidden_n, hidden_ld;
-  uint32_t *hidden_max;  // cleared by place (hidden given)
 };
 // A block of about a thread per 8 columns, for either kernel of rows.
 int row_threads(int64_t n) {
   return static_cast<int>(std::min<int64_t>(1024, ceil_div(ceil_div(n, 8), 32) * 32));
 }
+// The largest of the threads' values, by a block of up to 1024.
+__device__ __forceinline__ uint32_t block_max(uint32_t top, uint32_t (&scratch)[32]) {
+  top = __reduce_max_sync(0xffffffffu, top);
+  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = top;
+  __syncthreads();
+  for (int w = 0; w < blockDim.x >> 5; ++w) top = max(top, scratch[w]);
+  return top;
+}
+__device__ __forceinline__ uint32_t top_of(const float (&v)[8]) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) top = max(top, __float_as_uint(v[q]) & 0x7FFFFFFFu);
+  return top;
+}
+__device__ __forceinline__ uint4 half8(const float (&v)[8], float f) {
+  return make_uint4(pack_f16x2(v[0] * f, v[1] * f), pack_f16x2(v[2] * f, v[3] * f),
+                    pack_f16x2(v[4] * f, v[5] * f), pack_f16x2(v[6] * f, v[7] * f));
+}
 __global__ void __launch_bounds__(1024) convert_kernel(const ConvertArgs a) {
   __shared__ uint32_t tops[32];
-  __shared__ float sums[32];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, threads = blockDim.x;
+  const int tid = threadIdx.x, threads = blockDim.x;
   const int64_t m = blockIdx.x;
   grid_dependency_wait();
   grid_dependents_launch();
   const int routed = a.offsets[a.E];
   uint32_t top = 0;
-  float sum = 0.f;
   for (int k = tid * 8; k < a.Kp; k += threads * 8) {
     float v[8];
     load8(a.A, false, a.a_vec, m * a.K, k, a.K, v);
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      top = max(top, __float_as_uint(v[q]) & 0x7FFFFFFFu);
-      sum += fabsf(v[q]);
-    }
+    top = max(top, top_of(v));
   }
-  top = __reduce_max_sync(0xffffffffu, top);
-  sum = warp_sum(sum);
-  if (lane == 0) {
-    tops[warp] = top;
-    sums[warp] = sum;
-  }
-  __syncthreads();
-  sum = 0.f;
-  for (int w = 0; w < threads >> 5; ++w) {
-    top = max(top, tops[w]);
-    sum += sums[w];
-  }
-  const int shift = row_shift(top);
+  const int shift = row_shift(block_max(top, tops));
   const float f = exp2i(shift);
   for (int j = 0; j < a.copies; ++j) {
     const int64_t slot = m * a.copies + j;
     const int at = a.place[slot];
     if (at < routed) {
-      if (tid == 0) {
-        a.unscale[at] = exp2i(-shift);
-        if (a.norm1) a.norm1[at] = sum * 1.01f;  // above the exact sum for any K < 2^26
-      }
-      if (a.hidden && tid == 0) a.hidden_max[at] = 0;
-      if (a.hidden)
-        for (int k = a.hidden_n + tid; k < a.hidden_ld; k += threads)
-          a.hidden[int64_t(at) * a.hidden_ld + k] = 0;
+      if (tid == 0) a.unscale[at] = exp2i(-shift);
     } else if (a.Y) {
       for (int n = tid; n < a.N; n += threads) a.Y[slot * a.N + n] = 0;
     }
@@ -484,11 +473,7 @@ __global__ void __launch_bounds__(1024) convert_kernel(const ConvertArgs a) {
   for (int k = tid * 8; k < a.Kp; k += threads * 8) {
     float v[8];
     load8(a.A, false, a.a_vec, m * a.K, k, a.K, v);
-    uint4 h;
-    h.x = pack_f16x2(v[0] * f, v[1] * f);
-    h.y = pack_f16x2(v[2] * f, v[3] * f);
-    h.z = pack_f16x2(v[4] * f, v[5] * f);
-    h.w = pack_f16x2(v[6] * f, v[7] * f);
+    const uint4 h = half8(v, f);
     for (int j = 0; j < a.copies; ++j) {
       const int at = a.place[m * a.copies + j];
       if (at < routed) *reinterpret_cast<uint4 *>(a.out + int64_t(at) * a.Kp + k) = h;
@@ -496,28 +481,52 @@ __global__ void __launch_bounds__(1024) convert_kernel(const ConvertArgs a) {
   }
 }
 
-// Largest |bias| of each expert of up to three stacks: blockIdx (expert, stack).
-struct BiasArgs {
-  const float *bias[3];
-  float *bmax[3];
-  int N[3];
-};
-__global__ void __launch_bounds__(kThreads) bias_max_kernel(const BiasArgs a) {
-  __shared__ uint32_t scratch[kWarps];
-  const int e = blockIdx.x, i = blockIdx.y;
+// Hidden rows [places, ld] in fp32 as fp16 rows [places, Kp], zeros past K, each
+// scaled by its own largest value; what undoes the scale, and its exponent
+// (126, the largest, for a row of zeros). A block per place.
+__global__ void __launch_bounds__(1024)
+    hidden_half_kernel(const float *hidden, int64_t ld, int K, int Kp, const int32_t *offsets,
+                       int E, uint16_t *out, float *unscale, int32_t *shifts) {
+  __shared__ uint32_t tops[32];
+  const int tid = threadIdx.x, step = blockDim.x * 8;
+  const int64_t at = blockIdx.x;
   grid_dependency_wait();
   grid_dependents_launch();
-  if (!a.bias[i]) return;
-  uint32_t top = 0;
-  for (int n = threadIdx.x; n < a.N[i]; n += kThreads)
-    top = max(top, __float_as_uint(a.bias[i][int64_t(e) * a.N[i] + n]) & 0x7FFFFFFFu);
-  top = __reduce_max_sync(0xffffffffu, top);
-  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = top;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 0; w < kWarps; ++w) top = max(top, scratch[w]);
-    a.bmax[i][e] = __uint_as_float(top);
+  if (at >= offsets[E]) return;
+  float v[8], u[8];  // (most rows are one step long: they are read once)
+  load8(hidden, true, true, at * ld, tid * 8, K, v);
+  uint32_t top = top_of(v);
+  for (int k = tid * 8 + step; k < K; k += step) {
+    load8(hidden, true, true, at * ld, k, K, u);
+    top = max(top, top_of(u));
   }
+  top = block_max(top, tops);
+  const int shift = top ? row_shift(top) : 126;
+  const float f = exp2i(shift);
+  if (tid == 0) {
+    unscale[at] = exp2i(-shift);
+    shifts[at] = shift;
+  }
+  uint16_t *dst = out + at * Kp;
+  if (tid * 8 < Kp) *reinterpret_cast<uint4 *>(dst + tid * 8) = half8(v, f);
+  for (int k = tid * 8 + step; k < Kp; k += step) {
+    load8(hidden, true, true, at * ld, k, K, u);
+    *reinterpret_cast<uint4 *>(dst + k) = half8(u, f);
+  }
+}
+
+// Largest |bias| of each expert.
+__global__ void __launch_bounds__(kThreads)
+    bias_max_kernel(const float *bias, int N, float *bmax) {
+  __shared__ uint32_t scratch[32];
+  const int e = blockIdx.x;
+  grid_dependency_wait();
+  grid_dependents_launch();
+  uint32_t top = 0;
+  for (int n = threadIdx.x; n < N; n += kThreads)
+    top = max(top, __float_as_uint(bias[int64_t(e) * N + n]) & 0x7FFFFFFFu);
+  top = block_max(top, scratch);
+  if (threadIdx.x == 0) bmax[e] = __uint_as_float(top);
 }
 
 // Sum of each token's fp16 partials (rows of ld, a multiple of 8), in slot
@@ -854,8 +863,8 @@ struct MoeSpace {
   float *hidden, *part;
   size_t bytes;
 };
-// Hidden rows start on 16 bytes.
-size_t hidden_ld(const MoeArgs &a) { return ceil_div(a.gate.N, 4) * 4; }
+// fp32 hidden rows start on 16 bytes.
+size_t hidden_ld(const ExpertStack &gate) { return ceil_div(gate.N, 4) * 4; }
 
 MoeSpace moe_space(const MoeArgs &a) {
   const size_t P = size_t(a.M) * a.top_k;
@@ -865,7 +874,7 @@ MoeSpace moe_space(const MoeArgs &a) {
   s.counts = P > kFewSlots ? c.take<int32_t>(count_words(P, a.gate.E)) : nullptr;
   s.tops = c.take<uint32_t>(a.M);
   s.hidden_tops = c.take<uint32_t>(P);
-  s.hidden = c.take<float>(P * hidden_ld(a));
+  s.hidden = c.take<float>(P * hidden_ld(a.gate));
   s.part = c.take<float>(P * a.down.N);
   s.bytes = c.used;
   return s;
@@ -897,8 +906,8 @@ ExpertsSpace experts_space(const ExpertsArgs &a) {
 //   16, 4            17.4    24.3        24.1    25.1
 //   32, 4            69.2    84.4        88.3    89.4
 //   128, 8          143.5   165.5       204.2   171.3
-// A row too long for the streaming kernel's shared memory (K beyond some
-// 30 000) takes the tensor-core path as well.
+// A row too long for the streaming kernel's shared memory (K beyond 25 000 to
+// 59 000, by block size and scale type) takes the tensor-core path as well.
 constexpr int kTileMeanSlots = 6;
 bool tile_path(bool a_f32, int64_t P, std::initializer_list<const ExpertStack *> w) {
   if (a_f32) return false;
@@ -914,21 +923,23 @@ int64_t k_pad(int64_t K) { return ceil_div(K, kChunkK) * kChunkK; }
 struct TileSpace {
   Lists l;
   int32_t *counts, *place;
-  float *bmax[3];   // [E] per stack with a bias, else null
-  uint16_t *rows;   // fp16 activations by place
-  float *unscale, *norm1;
-  // The layer's.
-  uint16_t *hidden, *part;
+  uint16_t *rows;  // fp16 activations by place
+  float *unscale;
+  // The layer's. Each of two pieces is used twice: fp16 hidden rows take the
+  // place of the activations, partials that of the fp32 hidden rows.
+  float *hidden;
+  uint16_t *hidden_rows, *part;
   float *h_unscale, *p_unscale;
   int32_t *h_shift;
-  uint32_t *h_max;
+  float *bmax;  // [E] of down, null without a bias
   size_t bytes;
 };
-TileSpace tile_space(unsigned char *ws, int64_t P, const ExpertStack *const *w, int stacks,
-                     bool layer) {
+// Of a product with w, or of the layer with gate = w and down.
+TileSpace tile_space(unsigned char *ws, int64_t P, const ExpertStack &w, const ExpertStack *down) {
   Carve c{ws};
   TileSpace s{};
-  const int E = w[0]->E;
+  const int E = w.E;
+  const bool layer = down != nullptr;
   if (layer) {
     s.l.weights = c.take<float>(P);
     s.l.experts = c.take<int32_t>(P);
@@ -939,50 +950,30 @@ TileSpace tile_space(unsigned char *ws, int64_t P, const ExpertStack *const *w, 
   s.l.groups = c.take<SlotGroup>(max_groups(P, E, kTileSlots));
   s.counts = c.take<int32_t>(count_words(P, E));
   s.place = c.take<int32_t>(P);
-  for (int i = 0; i < stacks; ++i) s.bmax[i] = w[i]->bias ? c.take<float>(E) : nullptr;
-  s.rows = c.take<uint16_t>(size_t(P) * k_pad(w[0]->K));
+  s.rows = c.take<uint16_t>(size_t(P) * std::max(k_pad(w.K), layer ? k_pad(down->K) : 0));
   s.unscale = c.take<float>(P);
   if (layer) {
-    s.norm1 = c.take<float>(P);
-    s.hidden = c.take<uint16_t>(size_t(P) * k_pad(w[2]->K));
-    s.part = c.take<uint16_t>(size_t(P) * part_ld(w[2]->N));
+    s.hidden_rows = s.rows;
+    s.hidden = c.take<float>(size_t(P) *
+                             std::max<size_t>(hidden_ld(w), ceil_div(part_ld(down->N), 2)));
+    s.part = reinterpret_cast<uint16_t *>(s.hidden);
     s.h_unscale = c.take<float>(P);
     s.p_unscale = c.take<float>(P);
     s.h_shift = c.take<int32_t>(P);
-    s.h_max = c.take<uint32_t>(P);
+    s.bmax = down->bias ? c.take<float>(E) : nullptr;
   }
   s.bytes = c.used;
   return s;
 }
 
-// Lists by place, and (the layer's bounds need them) the stacks' largest biases.
-cudaError_t launch_tile_lists(const TileSpace &s, const int32_t *experts, int64_t P,
-                              const ExpertStack *const *w, int stacks, bool pdl,
-                              cudaStream_t stream) {
-  const int E = w[0]->E;
-  cudaError_t e = launch_lists(experts, P, E, s.l, s.counts, s.place, kTileSlots, 16, pdl, stream);
-  BiasArgs a{};
-  bool any = false;
-  for (int i = 0; i < stacks; ++i) {
-    a.bias[i] = w[i]->bias;
-    a.bmax[i] = s.bmax[i];
-    a.N[i] = w[i]->N;
-    any = any || w[i]->bias;
-  }
-  if (e == cudaSuccess && any && stacks > 1)
-    e = launch_pdl(bias_max_kernel, dim3(E, stacks), kThreads, 0, pdl, stream, a);
-  return e;
-}
-
-cudaError_t fill_tile(TileParams &p, int mode, const ExpertStack *const *w, int first,
+// w0 and w1: gate and up, or one matrix twice.
+cudaError_t fill_tile(TileParams &p, int mode, const ExpertStack &w0, const ExpertStack &w1,
                       const TileSpace &s, const uint16_t *rows, int64_t P) {
-  const ExpertStack &w0 = *w[first];
   p.mode = mode;
   for (int m = 0; m < 2; ++m) {
-    const int i = mode == kStreamGateUp ? first + m : first;
-    p.w[m] = stream_mat(*w[i]);
-    p.ts[m] = TileScales{
-        w[i]->rows, w[i]->rows + int64_t(w[i]->E) * ceil_div(w[i]->N, kTileN) * kTileN, s.bmax[i]};
+    const ExpertStack &w = m ? w1 : w0;
+    p.w[m] = stream_mat(w);
+    p.ts[m] = TileScales{w.rows, w.rows + int64_t(w.E) * ceil_div(w.N, kTileN) * kTileN, s.bmax};
   }
   p.N = w0.N;
   p.N16 = static_cast<int>(ceil_div(w0.N, kTileN));
@@ -1003,9 +994,9 @@ cudaError_t fill_tile(TileParams &p, int mode, const ExpertStack *const *w, int 
 
 cudaError_t launch_experts_tile(const ExpertsArgs &a, cudaStream_t stream) {
   const int64_t P = a.M * a.top_k;
-  const ExpertStack *w[1] = {&a.w};
-  const TileSpace s = tile_space(a.ws, P, w, 1, false);
-  cudaError_t e = launch_tile_lists(s, a.experts, P, w, 1, a.pdl, stream);
+  const TileSpace s = tile_space(a.ws, P, a.w, nullptr);
+  cudaError_t e = launch_lists(a.experts, P, a.w.E, s.l, s.counts, s.place, kTileSlots, 16, a.pdl,
+                               stream);
   if (e != cudaSuccess) return e;
   ConvertArgs c{};
   c.A = static_cast<const uint16_t *>(a.A);
@@ -1024,7 +1015,7 @@ cudaError_t launch_experts_tile(const ExpertsArgs &a, cudaStream_t stream) {
                  a.pdl, stream, c);
   if (e != cudaSuccess) return e;
   TileParams p{};
-  e = fill_tile(p, kStreamProduct, w, 0, s, s.rows, P);
+  e = fill_tile(p, kStreamProduct, a.w, a.w, s, s.rows, P);
   if (e != cudaSuccess) return e;
   p.unscale = s.unscale;
   p.Y = static_cast<uint16_t *>(a.Y);
@@ -1034,13 +1025,17 @@ cudaError_t launch_experts_tile(const ExpertsArgs &a, cudaStream_t stream) {
 
 cudaError_t launch_moe_tile(const MoeArgs &a, cudaStream_t stream) {
   const int64_t P = a.M * a.top_k;
-  const ExpertStack *w[3] = {&a.gate, &a.up, &a.down};
-  const TileSpace s = tile_space(a.ws, P, w, 3, true);
+  const TileSpace s = tile_space(a.ws, P, a.gate, &a.down);
   cudaError_t e = launch_pdl(route_kernel, grid_of(a.M, kWarps), kThreads,
                              size_t(kWarps) * a.gate.E * 4, a.pdl, stream, a.logits,
                              a.logits_f32, a.M, a.gate.E, a.top_k, a.normalize, s.l.weights,
                              s.l.experts);
-  if (e == cudaSuccess) e = launch_tile_lists(s, s.l.experts, P, w, 3, a.pdl, stream);
+  if (e == cudaSuccess)
+    e = launch_lists(s.l.experts, P, a.gate.E, s.l, s.counts, s.place, kTileSlots, 16, a.pdl,
+                     stream);
+  if (e == cudaSuccess && s.bmax)
+    e = launch_pdl(bias_max_kernel, a.down.E, kThreads, 0, a.pdl, stream, a.down.bias, a.down.N,
+                   s.bmax);
   if (e != cudaSuccess) return e;
   ConvertArgs c{};
   c.A = static_cast<const uint16_t *>(a.X);
@@ -1053,30 +1048,25 @@ cudaError_t launch_moe_tile(const MoeArgs &a, cudaStream_t stream) {
   c.E = a.gate.E;
   c.out = s.rows;
   c.unscale = s.unscale;
-  c.norm1 = s.norm1;
-  c.hidden = s.hidden;
-  c.hidden_n = a.gate.N;
-  c.hidden_ld = static_cast<int>(k_pad(a.gate.N));
-  c.hidden_max = s.h_max;
   e = launch_pdl(convert_kernel, static_cast<unsigned>(a.M), row_threads(c.Kp), 0, a.pdl, stream, c);
   if (e != cudaSuccess) return e;
   TileParams up{}, down{};
-  e = fill_tile(up, kStreamGateUp, w, 0, s, s.rows, P);
+  e = fill_tile(up, kStreamGateUp, a.gate, a.up, s, s.rows, P);
   if (e != cudaSuccess) return e;
   up.unscale = s.unscale;
-  up.norm1 = s.norm1;
   up.hidden = s.hidden;
-  up.ldh = c.hidden_ld;
-  up.out_unscale = s.h_unscale;
-  up.out_shift = s.h_shift;
-  up.hidden_max = s.h_max;
+  up.ldh = hidden_ld(a.gate);
   e = launch_tile(up, a.gate.z != nullptr, a.gate.s_f32, a.gate.bs, a.pdl, stream);
   if (e != cudaSuccess) return e;
-  e = fill_tile(down, kStreamDown, w, 2, s, s.hidden, P);
+  const int Ip = static_cast<int>(k_pad(a.down.K));
+  e = launch_pdl(hidden_half_kernel, static_cast<unsigned>(P), row_threads(Ip), 0, a.pdl, stream,
+                 s.hidden, up.ldh, a.down.K, Ip, s.l.offsets, a.down.E, s.hidden_rows, s.h_unscale,
+                 s.h_shift);
+  if (e != cudaSuccess) return e;
+  e = fill_tile(down, kStreamDown, a.down, a.down, s, s.hidden_rows, P);
   if (e != cudaSuccess) return e;
   down.unscale = s.h_unscale;
   down.shift = s.h_shift;
-  down.hidden_max = s.h_max;
   down.part = s.part;
   down.ldp = part_ld(a.down.N);
   down.out_unscale = s.p_unscale;
@@ -1155,10 +1145,8 @@ cudaError_t launch_moe_route(const RouteArgs &a, cudaStream_t stream) {
 size_t matmul_experts_workspace_bytes(const ExpertsArgs &a) {
   ExpertsArgs b = a;
   b.ws = nullptr;
-  if (tile_path(a.a_f32, a.M * a.top_k, {&a.w})) {
-    const ExpertStack *w[1] = {&a.w};
-    return tile_space(nullptr, a.M * a.top_k, w, 1, false).bytes;
-  }
+  if (tile_path(a.a_f32, a.M * a.top_k, {&a.w}))
+    return tile_space(nullptr, a.M * a.top_k, a.w, nullptr).bytes;
   return experts_space(b).bytes;
 }
 
@@ -1212,10 +1200,8 @@ cudaError_t launch_matmul_experts(const ExpertsArgs &a, cudaStream_t stream) {
 size_t moe_workspace_bytes(const MoeArgs &a) {
   MoeArgs b = a;
   b.ws = nullptr;
-  if (tile_path(a.a_f32, a.M * a.top_k, {&a.gate, &a.down})) {
-    const ExpertStack *w[3] = {&a.gate, &a.up, &a.down};
-    return tile_space(nullptr, a.M * a.top_k, w, 3, true).bytes;
-  }
+  if (tile_path(a.a_f32, a.M * a.top_k, {&a.gate, &a.down}))
+    return tile_space(nullptr, a.M * a.top_k, a.gate, &a.down).bytes;
   return moe_space(b).bytes;
 }
 
@@ -1277,14 +1263,14 @@ cudaError_t launch_moe(const MoeArgs &a, cudaStream_t stream) {
   up.p.tops = s.tops;
   up.p.hidden = s.hidden;
   up.p.hidden_tops = s.hidden_tops;
-  up.p.ldh = hidden_ld(a);
+  up.p.ldh = hidden_ld(a.gate);
   e = run_stream(up, a.pdl, stream);
   if (e != cudaSuccess) return e;
   set_lists(down.p, s.l);
   down.p.w[0] = down.p.w[1] = stream_mat(a.down);
   down.p.A = s.hidden;
   down.p.a_f32 = down.p.a_vec = down.p.per_slot = 1;
-  down.p.ld = hidden_ld(a);
+  down.p.ld = hidden_ld(a.gate);
   down.p.tops = s.hidden_tops;
   down.p.part = s.part;
   down.p.early = a.pdl;

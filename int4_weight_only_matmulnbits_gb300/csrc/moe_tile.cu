@@ -22,11 +22,13 @@
 //    order of the lists: TMA tiles of 32 rows x 64 k, 128-byte swizzle. Each
 //    CTA of a pair loads half of a group's rows: alone, with 128 weight rows
 //    and all of the slots, it would take 64 bytes of activations a cycle.
-//  * Hidden values leave as fp16, the row scaled so that a bound of it (15 s
-//    times the 1-norm of x, for gate and for up) fits: typical values then
-//    lie 15 or so octaves above fp16's smallest normal. Down partials are
-//    fp16 too, scaled by a bound from their hidden row's largest value (15 s
-//    K max|h|); they are added per token by a kernel that follows.
+//  * Hidden values leave as fp32, the router's weight applied; a small kernel
+//    makes them fp16 rows scaled by their own largest value, as the streaming
+//    kernel does. (A scale from a bound known ahead, such as 15 s |x|_1 for
+//    gate and for up, saves that kernel, but rows far below their bound lose
+//    their bits: all of them where SiLU makes a row 2^-40 of it.) Down partials
+//    are fp16, scaled by the bound 15 s K max|h| of their hidden row; they are
+//    added per token by a kernel that follows.
 //  * Warps 0-15 unpack, each its own tile's codes and scales from a private
 //    ring of asynchronous copies, in two groups that alternate stages; warps
 //    16-23 store; one warp each issues the TMA loads, issues the MMAs, and
@@ -163,7 +165,7 @@ struct Layout {  // shared memory, from a 1024-byte aligned base
 };
 // What the epilogue needs of a column: a undoes the activation row's scale
 // (down: and applies the output's); b is the slot's weight times the output's
-// scale; out the slot (product).
+// scale (down); out the slot (product).
 struct Columns {
   float2 ab[kTileSlots];
   int out[kTileSlots];
@@ -368,31 +370,18 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
       for (int c = lane; c < sg.cols; c += 32) {
         const int place = sg.first + c, id = p.order[place];
         float a = p.unscale[place], b = 1.f;
-        if (gate_up) {
-          // |h| <= (15 s |x|_1 + |b|) for gate times the same for up.
-          const float x1 = p.norm1[place];
-          int e = 0;
-#pragma unroll
-          for (int m = 0; m < 2; ++m)
-            e += expo(15.f * most(p.ts[m].smax) * x1 + most(p.ts[m].bmax));
-          const int shift = max(-126, min(126, 15 - e));
-          b = p.weights[id] * exp2i(shift);
-          if (u % np == 0 && rank == 0) {
-            p.out_unscale[place] = exp2i(-shift);
-            p.out_shift[place] = shift;
-          }
-        } else if (p.mode == kStreamDown) {
-          // |sum| <= 15 s K max|h| / 2^shift, and the bias.
-          const float h = __half2float(
-              __ushort_as_half(static_cast<unsigned short>(p.hidden_max[place])));
+        if (p.mode != kStreamProduct) b = p.weights[id];
+        if (p.mode == kStreamDown) {
+          // |sum| <= 15 s K max|h|, and the bias; a hidden row's largest value
+          // is below 2^(15 - p.shift).
           const int e = max(expo(15.01f * most(p.ts[0].smax) *
-                                 static_cast<float>(p.K64 * kChunkK) * h) - p.shift[place],
-                            expo(most(p.ts[0].bmax))) + 1;
-          // a = 2^(shift - p.shift) stays finite: a hidden row of zeros, or an
-          // expert of zero scales, has a bound of 0, and 0 * inf would be NaN.
+                                 static_cast<float>(p.K64 * kChunkK) * 32768.f) - p.shift[place],
+                            expo(most(p.ts[0].bmax) * b)) + 1;
+          // a = 2^(shift - p.shift) stays finite: an expert of zero scales has
+          // a bound of 0, and 0 * inf would be NaN.
           const int shift = max(-126, min(min(126, 126 + p.shift[place]), 15 - e));
           a *= exp2i(shift);
-          b = p.weights[id] * exp2i(shift);
+          b *= exp2i(shift);
           if (u % np == 0 && rank == 0) p.out_unscale[place] = exp2i(-shift);
         }
         cl.ab[c] = make_float2(a, b);
@@ -620,13 +609,11 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
           // Lanes below 16 take columns 0-15, the others 16-31: each sends
           // what the other half-warp lacks.
           const int mine0 = c0 + (up ? 16 : 0);
-          uint16_t *dst = p.hidden + int64_t(sg.first + mine0 + (lane & 1)) * p.ldh + (row & ~1);
-          uint32_t top[8];  // magnitudes: two rows of every other column
+          float *dst = p.hidden + int64_t(sg.first + mine0) * p.ldh + row;
 #pragma unroll
           for (int i = 0; i < 16; i += 2) {
             const float4 ck = *reinterpret_cast<const float4 *>(&cl.ab[mine0 + i]);
             const float4 cs = *reinterpret_cast<const float4 *>(&cl.ab[c0 + i + (up ? 0 : 16)]);
-            float h[2];
 #pragma unroll
             for (int o = 0; o < 2; ++o) {
               const float keep = up ? v[16 + i + o] : v[i + o];
@@ -636,28 +623,10 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                   0xffffffffu, fmaf(send * rinv, o ? cs.z : cs.x, bias), 16);
               const float gv = up ? got : k, uv = up ? k : got;
               // exp overflows for gv < -88: the quotient is then 0.
-              h[o] = __fdividef(gv * uv, 1.f + __expf(-gv)) * (o ? ck.w : ck.y);
-            }
-            const uint32_t w = pair_rows(pack_f16x2(h[0], h[1]));
-            if ((row & ~1) < p.N && mine0 + i + (lane & 1) < sg.cols)
-              *reinterpret_cast<uint32_t *>(dst + i * p.ldh) = w;
-            top[i / 2] = (row & ~1) < p.N ? w & 0x7FFF7FFFu : 0u;
-          }
-          // Each column's largest over the 16 rows: at each step a lane sends
-          // the half of its columns that the other lane goes on with.
-#pragma unroll
-          for (int n2 = 4; n2 >= 1; n2 /= 2) {
-            const bool high = lane & (2 * n2);
-#pragma unroll
-            for (int q = 0; q < n2; ++q) {
-              const uint32_t got =
-                  __shfl_xor_sync(0xffffffffu, high ? top[q] : top[n2 + q], 2 * n2);
-              top[q] = f16x2_max(high ? top[n2 + q] : top[q], got);
+              const float h = __fdividef(gv * uv, 1.f + __expf(-gv)) * (o ? ck.w : ck.y);
+              if (live && mine0 + i + o < sg.cols) dst[(i + o) * p.ldh] = h;
             }
           }
-          const int c = mine0 + (lane & 15);
-          const uint32_t most = max(top[0] & 0xFFFFu, top[0] >> 16);
-          if (c < sg.cols && most) atomicMax(p.hidden_max + sg.first + c, most);
         } else if (p.mode == kStreamProduct) {
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {

@@ -16,8 +16,8 @@ constexpr int kTileBox = 32;     // activation rows per TMA box
 // What the kernel needs of a stack's scales and biases.
 struct TileScales {
   const float *fac;   // [E * N16 * 16] power of two per row (moe.cu, row_scales_kernel)
-  const float *smax;  // [E] largest |scale|
-  const float *bmax;  // [E] largest |bias|, or null
+  const float *smax;  // [E] largest |scale| (down)
+  const float *bmax;  // [E] largest |bias|, or null (down)
 };
 
 struct TileParams {
@@ -31,21 +31,18 @@ struct TileParams {
   const int32_t *order, *n_groups;
   const SlotGroup *groups;
   const float *weights;  // [P] by slot (gate and up, down)
-  // By place: what undoes the activation row's scale, and its 1-norm (gate
-  // and up) or scale exponent (down).
-  const float *unscale, *norm1;
+  // By place: what undoes the activation row's scale, and that scale's
+  // exponent (down).
+  const float *unscale;
   const int32_t *shift;
-  // Outputs: Y [P, N] bf16 by slot (product); hidden fp16 rows [P, ldh] and
-  // their undo factors and exponents, by place (gate and up); fp16 partials
-  // [P, ldp] and their undo factors, by place (down). ldh and ldp are even.
-  uint16_t *Y, *hidden, *part;
+  // Outputs: Y [P, N] bf16 by slot (product); hidden rows [P, ldh] in fp32, by
+  // place (gate and up); fp16 partials [P, ldp] and their undo factors, by place
+  // (down). ldp is even.
+  uint16_t *Y, *part;
+  float *hidden;
   int64_t ldh, ldp;
   int y_pairs;  // rows of Y start on 4 bytes
   float *out_unscale;
-  int32_t *out_shift;
-  // Largest magnitude of each hidden row as stored (fp16 bits), by place: raised
-  // by gate and up (zeros before), read by down.
-  uint32_t *hidden_max;
 };
 
 cudaError_t launch_tile(const TileParams &p, bool zp, bool sf32, int bs, bool pdl,

@@ -344,6 +344,46 @@ def test_layer_outliers_cost_no_bits(dev, M, factor):
     assert err[:, plain].norm() <= (2.0 ** -8 + 4 * 2.0 ** -11) * R[:, plain].norm()
 
 
+@pytest.mark.parametrize("M", [3, 140])
+@pytest.mark.parametrize("factor", [64, 256, 1024])
+def test_layer_large_outliers_cost_no_bits(dev, M, factor):
+    """The same with larger blocks, at the width of a real layer."""
+    E, k, H, I, bs = 6, 2, 2560, 768, 32
+    g = torch.Generator().manual_seed(M)
+    ws = []
+    for N, K in ((I, H), (I, H), (H, I)):
+        B, s, z, b = stack(g, E, N, K, bs, BF16, False, False)
+        s[:, N // 3, 1] *= factor
+        ws.append(pack(dev, (B, s, z, b), N, K, bs))
+    X = (torch.randn(M, H, generator=g) * 0.05).to(BF16).to(dev)
+    X[:, 32:64] = 0
+    logits = torch.randn(M, E, generator=g).to(dev)
+    weights, experts, _, _ = ref.route(logits, k, True)
+    R, _ = ref.layer(X, weights, experts.to(dev), *[W for _, _, W in ws], None, None, None, BF16)
+    err = mnb.mnb_moe(X, logits, *[w for w, _, _ in ws], k).double() - R
+    plain = torch.arange(H, device=dev) != H // 3
+    assert err[:, plain].norm() <= (2.0 ** -8 + 4 * 2.0 ** -11) * R[:, plain].norm()
+
+
+@pytest.mark.parametrize("M", [3, 140])
+@pytest.mark.parametrize("gate", [-10.0, -20.0, -40.0])
+def test_layer_small_hidden_rows_keep_their_bits(dev, M, gate):
+    """Gates far below zero: SiLU makes every hidden value, and with it the result, up to 2^52
+    times smaller, and no less precise. Norm-wise as above, and a rounding of the gate sums (at
+    most 2^-11 of some 0.1, of random sign) moves SiLU by as much of itself."""
+    E, k, H, I, bs = 6, 2, 1024, 768, 32
+    g = torch.Generator().manual_seed(M)
+    ws = [pack(dev, stack(g, E, N, K, bs, BF16, False, False), N, K, bs)
+          for N, K in ((I, H), (I, H), (H, I))]
+    X = (torch.randn(M, H, generator=g) * 0.05).to(BF16).to(dev)
+    logits = torch.randn(M, E, generator=g).to(dev)
+    bg = torch.full((E, I), gate, device=dev)
+    weights, experts, _, _ = ref.route(logits, k, True)
+    R, _ = ref.layer(X, weights, experts.to(dev), *[W for _, _, W in ws], bg, None, None, BF16)
+    err = mnb.mnb_moe(X, logits, *[w for w, _, _ in ws], k, bias_gate=bg).double() - R
+    assert err.norm() <= (2.0 ** -8 + 5 * 2.0 ** -11) * R.norm()
+
+
 @pytest.mark.parametrize("M", [3, 12, 140])
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_layer_masked_tokens(dev, M, dtype):
