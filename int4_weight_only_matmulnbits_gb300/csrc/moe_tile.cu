@@ -622,8 +622,11 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
               const float got = __shfl_xor_sync(
                   0xffffffffu, fmaf(send * rinv, o ? cs.z : cs.x, bias), 16);
               const float gv = up ? got : k, uv = up ? k : got;
-              // exp overflows for gv < -88: the quotient is then 0.
-              const float h = __fdividef(gv * uv, 1.f + __expf(-gv)) * (o ? ck.w : ck.y);
+              // silu(g) = g / (1 + e^-g), for g < 0 as g e^g / (1 + e^g): neither the
+              // divisor nor a factor of the product overflows on the way.
+              const float ex = __expf(-fabsf(gv));
+              const float h = __fdividef(gv < 0.f ? gv * ex : gv, 1.f + ex) * uv *
+                              (o ? ck.w : ck.y);
               if (live && mine0 + i + o < sg.cols) dst[(i + o) * p.ldh] = h;
             }
           }

@@ -447,6 +447,24 @@ def test_layer_hidden_rows_vanish(dev, M, H, bias_down):
               2, what=f"H{H}")
 
 
+@pytest.mark.parametrize("M", [3, 140])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("gate,up", [(-50.0, 1e38), (50.0, 1e36), (-85.0, 1e37), (1e36, 50.0)])
+def test_layer_range_of_the_gated_product(dev, M, dtype, gate, up):
+    """gate * up is beyond fp32, or near its end, where silu(gate) * up is not."""
+    X, logits, ((wg, bg, Wg), (wu, bu, Wu), (wd, bd, Wd)) = layer_inputs(
+        dev, M, 5, 2, 128, 96, 32, dtype, bias=True, seed=M)
+    bg[:] = gate
+    bu[:] = up
+    Y = run_layer(dev, X, logits, ((wg, bg, Wg), (wu, bu, Wu), (wd, bd, Wd)), 2,
+                  what=f"{gate} {up}")
+    # Norm-wise: 2^-8 of the output, four roundings of 2^-11 as above, and SiLU moved by a
+    # rounding of the gate sums (2^-11 of some 0.7).
+    weights, experts, _, _ = ref.route(logits, 2, True)
+    R, _ = ref.layer(X, weights, experts.to(dev), Wg, Wu, Wd, bg, bu, bd, dtype)
+    assert (Y.double() - R).norm() <= (2.0 ** -8 + 5 * 2.0 ** -11) * R.norm()
+
+
 @pytest.mark.parametrize("M", [1, 9, 170])
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_layer_many_experts(dev, M, dtype):
