@@ -767,9 +767,13 @@ typedef struct {
  * and its header says so (for N % 16 == 0 the bytes are those of mnb_prepack
  * on the E * N rows). packed_rows (fp32 [E * Np + E], 16-byte aligned)
  * receives, for each packed row, the power of two that brings its largest
- * |scale| into 2^14 .. 2^15, then each expert's largest |scale|. Arguments
- * and errors as mnb_prepack; MNB_ERR_SHAPE also for E < 1 and when E * Np
- * passes 2^31 - 1.
+ * |scale| into 2^14 .. 2^15, then each expert's largest |scale|. Beside the
+ * header the library records E and N: calls that describe the stack otherwise,
+ * or that pass a single weight as a stack, return MNB_ERR_LAYOUT. (A stack
+ * restored from storage is known by its registered header alone, which has
+ * the rows in all: its E and N are taken on the caller's word.) Arguments and
+ * errors as mnb_prepack; MNB_ERR_SHAPE also for E < 1 and when E * Np passes
+ * 2^31 - 1.
  */
 MNB_API mnb_status mnb_prepack_experts(const uint8_t *B, const void *scales,
                                        const uint8_t *zero_points, int64_t E, int64_t N,

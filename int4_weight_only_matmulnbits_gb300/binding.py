@@ -823,6 +823,11 @@ def _experts_struct(w: PackedExperts, bias: torch.Tensor | None, device) -> Expe
           None if w.packed_zp is None else w.packed_zp.data_ptr(), w.packed_rows.data_ptr())
     kept = w.__dict__.get("_struct")
     if kept is None or kept[0] != at:
+        # E of a stack follows from its rows in all and this size.
+        rows = w.E * (-(-w.N // 16) * 16) + w.E
+        if w.packed_rows.numel() != rows or w.packed_rows.dtype != torch.float32:
+            raise ValueError(f"packed_rows of {w.E} experts of {w.N} rows must be an fp32 "
+                             f"[{rows}] tensor")
         kept = (at, ExpertsC(*at, None, w.E, w.N, w.K, w.block_size,
                              _dtype_code(w.scale_dtype)))
         w.__dict__["_struct"] = kept

@@ -136,12 +136,21 @@ mnb_status header_valid(const mnb_packed_header &h) {
   return MNB_OK;
 }
 
+// What the library knows of a packed weight: its header and, beyond it, what
+// it was packed as. E: 0 unknown (a registered header), kPlainWeight, or the
+// experts of a stack, of N rows each.
+constexpr int64_t kPlainWeight = -1;
+struct PackedRecord {
+  mnb_packed_header h;
+  int64_t E, N;
+};
 std::mutex g_headers_mu;
-std::unordered_map<uintptr_t, mnb_packed_header> g_headers;
+std::unordered_map<uintptr_t, PackedRecord> g_headers;
 
-void record_header(const void *packed_b, const mnb_packed_header &h) {
+void record_header(const void *packed_b, const mnb_packed_header &h, int64_t E = kPlainWeight,
+                   int64_t N = 0) {
   std::lock_guard<std::mutex> lock(g_headers_mu);
-  g_headers[reinterpret_cast<uintptr_t>(packed_b)] = h;
+  g_headers[reinterpret_cast<uintptr_t>(packed_b)] = PackedRecord{h, E, N};
 }
 
 const char *dtype_name(int d) { return d == MNB_F32 ? "fp32" : "bf16"; }
@@ -160,7 +169,7 @@ mnb_status check_layout(const void *packed_b, int64_t N, int64_t K, int bs, int 
                     packed_b);
       return MNB_ERR_LAYOUT;
     }
-    h = it->second;
+    h = it->second.h;
   }
   const char *field = h.N != N                             ? "N"
                       : h.K != K                           ? "K"
@@ -350,9 +359,32 @@ mnb_status check_stack(const mnb_experts &w) {
   return MNB_OK;
 }
 
+// The header knows the E * Np rows of a stack, not how they divide; a wrong
+// division would read packed_rows past its end.
 mnb_status check_stack_layout(const mnb_experts &w) {
-  return check_layout(w.packed_b, w.E * padded_rows(w.N), w.K, w.block_size, w.scale_dtype,
-                      w.packed_zp != nullptr, MNB_CODES_AFFINE);
+  const mnb_status st = check_layout(w.packed_b, w.E * padded_rows(w.N), w.K, w.block_size,
+                                     w.scale_dtype, w.packed_zp != nullptr, MNB_CODES_AFFINE);
+  if (st != MNB_OK) return st;
+  int64_t E = 0, N = 0;
+  {
+    std::lock_guard<std::mutex> lock(g_headers_mu);
+    const auto it = g_headers.find(reinterpret_cast<uintptr_t>(w.packed_b));
+    if (it != g_headers.end()) {
+      E = it->second.E;
+      N = it->second.N;
+    }
+  }
+  if (E == 0 || (E == w.E && N == w.N)) return MNB_OK;
+  if (E == kPlainWeight)
+    std::snprintf(g_last_error, sizeof g_last_error,
+                  "packed weight %p is a single weight, not a stack of mnb_prepack_experts",
+                  w.packed_b);
+  else
+    std::snprintf(g_last_error, sizeof g_last_error,
+                  "packed stack %p differs in E or N: packed as E=%lld N=%lld, called with "
+                  "E=%lld N=%lld",
+                  w.packed_b, (long long)E, (long long)N, (long long)w.E, (long long)w.N);
+  return MNB_ERR_LAYOUT;
 }
 
 // The three stacks of a layer: each well formed, and of sizes that fit.
@@ -567,7 +599,7 @@ mnb_status mnb_packed_register(const void *packed_b, const mnb_packed_header *he
   if (!packed_b || !header) return MNB_ERR_NULL;
   const mnb_status st = header_valid(*header);
   if (st != MNB_OK) return st;
-  record_header(packed_b, *header);
+  record_header(packed_b, *header, 0);
   return MNB_OK;
 }
 
@@ -1416,7 +1448,7 @@ mnb_status mnb_prepack_experts(const uint8_t *B, const void *scales,
   if (e == cudaSuccess)
     e = launch_pack_header(h, static_cast<char *>(packed_b) + codes_bytes(rows, K), s);
   if (e != cudaSuccess) return cuda_fail(e, "mnb_prepack_experts");
-  record_header(packed_b, h);
+  record_header(packed_b, h, E, N);
   return MNB_OK;
 }
 

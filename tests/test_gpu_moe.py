@@ -628,6 +628,43 @@ def test_copied_and_replaced_stacks(dev):
     assert torch.equal(mnb.mnb_matmul_experts(A, c, t), Yb)
 
 
+def test_wrong_descriptions_are_refused(dev):
+    """A stack described with another division of its rows, a single weight passed as a stack
+    and a stack of another N are turned down on the host; a stack as the single weight that its
+    header says it is, and one known by a registered header, are taken."""
+    E, N, K, bs = 8, 64, 128, 32
+    g = torch.Generator().manual_seed(2)
+    B, s, _, _ = to(dev, *stack(g, E, N, K, bs, F32, False, False))
+    w = mnb.mnb_prepack_experts(B, s, None, N, K, bs)
+    plain = mnb.mnb_prepack(B.view(1, E * N, -1, bs // 2), s.view(E * N, -1), None, E * N, K, bs)
+    A = torch.randn(2, K, generator=g).to(dev)
+    t = torch.zeros(2, 1, dtype=torch.int32, device=dev)
+    Y = torch.zeros(2, 1, 2 * N, device=dev)
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device=dev)
+    lib = mnb.load()
+
+    def call(c):
+        return lib.mnb_matmul_experts(A.data_ptr(), 0, c, t.data_ptr(), 2, 1, Y.data_ptr(),
+                                      binding.MNB_F32, ws.data_ptr(), ws.numel(), None)
+
+    def described(packed, E, N):
+        return binding.ExpertsC(packed.packed_b.data_ptr(), packed.packed_scales.data_ptr(), None,
+                                w.packed_rows.data_ptr(), None, E, N, K, bs, binding.MNB_F32)
+
+    for packed, e, n in ((w, 16, 32), (w, 4, 128), (w, 1, 512), (w, 8, 60), (plain, 8, 64),
+                         (plain, 1, 512)):
+        assert call(described(packed, e, n)) == binding.MNB_ERR_LAYOUT, (e, n)
+        assert b"stack" in lib.mnb_last_error_string()
+    assert call(described(w, 8, 64)) == 0
+    whole = mnb.PackedWeight(w.packed_b, w.packed_scales, None, E * N, K, bs, F32)
+    assert torch.equal(mnb.mnb_matmul(A, whole), mnb.mnb_matmul(A, plain))
+    want = mnb.mnb_matmul_experts(A, w, t)
+    mnb.mnb_packed_register(w.packed_b, mnb.mnb_packed_read_header(w.packed_b))
+    assert torch.equal(mnb.mnb_matmul_experts(A, w, t), want)
+    with pytest.raises(ValueError, match="packed_rows"):
+        mnb.mnb_matmul_experts(A, dataclasses.replace(w, E=16, N=32), t)
+
+
 def test_programmatic_launch_off(dev):
     X, logits, ws = layer_inputs(dev, 3, 8, 2, 256, 192, 32, BF16)
     packed = [w for w, _, _ in ws]

@@ -126,6 +126,21 @@ def test_stack_headers(lib):
     assert b"zero points" in lib.mnb_last_error_string()
 
 
+def test_binding_refuses_a_wrong_division():
+    """8 experts of 64 rows described as 16 of 32 or 4 of 128: the same rows in all."""
+    buf = torch.zeros(512, dtype=torch.uint8)
+    rows = torch.zeros(8 * 64 + 8)
+    b._experts_struct(mnb.PackedExperts(buf, buf, None, rows, 8, 64, 128, 32, torch.bfloat16),
+                      None, buf.device)
+    for E, N in ((16, 32), (4, 128), (8, 80), (9, 64)):
+        w = mnb.PackedExperts(buf, buf, None, rows, E, N, 128, 32, torch.bfloat16)
+        with pytest.raises(ValueError, match="packed_rows"):
+            b._experts_struct(w, None, buf.device)
+    w = mnb.PackedExperts(buf, buf, None, rows.double(), 8, 64, 128, 32, torch.bfloat16)
+    with pytest.raises(ValueError, match="packed_rows"):
+        b._experts_struct(w, None, buf.device)
+
+
 def moe(lib, x=A, logits=LOG, ldt=F32, M=4, k=2, norm=1, gate=None, up=None, down=None, y=Y,
         dt=BF16, ws=WS, ws_bytes=1 << 40):
     gate = gate if gate is not None else stack(0)
