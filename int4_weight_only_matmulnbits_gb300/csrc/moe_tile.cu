@@ -348,13 +348,17 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
       int it = 0;
       for (int u = u0; u < units && ok; u += du)
         for (int kb = 0; kb < p.K64; kb += kChunks, ++it) {
-          if (!mbar_sleep(bfull + it % kBStages, (it / kBStages) & 1)) {
-            record_fault(&g_fault_moe, kFaultMoeWait);
-            ok = false;
-            break;
-          }
+          ok = mbar_sleep(bfull + it % kBStages, (it / kBStages) & 1);
+          if (!ok) break;
           mbar_arrive_cluster(peer + 8 * (it % kBStages));
         }
+      // CTA 0's commits arrive on this CTA's barriers as well, and nothing here
+      // waits for the last of them: this CTA must not be gone when they land.
+      for (int i = max(0, it - kBStages); i < it && ok; ++i)
+        ok = mbar_sleep(bempty + i % kBStages, (i / kBStages) & 1);
+      for (int i = max(0, it - kAStages); i < it && ok; ++i)
+        ok = mbar_sleep(aempty + i % kAStages, (i / kAStages) & 1);
+      if (!ok) record_fault(&g_fault_moe, kFaultMoeWait);
     }
   } else if (warp == kColWarp) {
     // ---- columns ------------------------------------------------------------------

@@ -676,5 +676,15 @@ def test_programmatic_launch_off(dev):
         mnb.mnb_set_programmatic_launch(True)
 
 
+@pytest.mark.parametrize("K", [1, 64, 65, 128, 192, 256, 640, 704])
+@pytest.mark.parametrize("N", [16, 520])
+def test_few_stages_and_units(dev, N, K):
+    """Tensor-core kernel with fewer stages than its rings hold, on pairs of CTAs with no work
+    item, one or several: every wait at its end is met (at once, and with no fault recorded)."""
+    for M, E in ((6, 1), (12, 2), (700, 60), (30000, 200)):
+        run_experts(dev, M, E, 1, N, K, 32, BF16, seed=M + K)
+    assert mnb.mnb_fault_status() == 0
+
+
 def test_no_faults_recorded(dev):
     assert mnb.mnb_fault_status() == 0
