@@ -351,6 +351,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           }
           mbar_arrive_cluster(peer_apeer + 8 * s);
         }
+      // CTA 0's commits arrive on this CTA's barriers as well, and nothing here
+      // waits for the last of them: this CTA must not be gone when they land.
+      for (int i = it > AS ? it - AS : 0; i < it && !fault; ++i)
+        fault = !mbar_wait(aempty + i % AS, (i / AS) & 1);
+      for (int i = it > BST ? it - BST : 0; i < it && !fault; ++i)
+        fault = !mbar_wait(bempty + i % BST, (i / BST) & 1);
     }
   } else if (warp >= kWarpEpi && warp < kWarpDq) {
     // ---- epilogue: TMEM -> registers -> Y ----------------------------------

@@ -73,6 +73,20 @@ def test_pair_tiles_and_tails(dev, bs, with_zp, scale_f32):
     assert mnb.mnb_fault_status() == 0
 
 
+@pytest.mark.parametrize("K", [8, 64, 72, 128, 192, 320])
+def test_pair_few_stages(dev, K):
+    """Fewer k stages than the rings hold, on one pair and on all of them: the waits at a CTA's
+    end are met, and no fault is recorded."""
+    for M, N in ((40, 48), (1100, 5000)):
+        prob = make_problem(M, N, K, 32, dtype=torch.bfloat16, zero_points=True, bias=True,
+                            seed=M + K)
+        Y = run(prob, dev)
+        rows, cols = sample(M, 40, K, (0, M - 1)), sample(N, 60, K, (0, N - 1))
+        R, mag = ref(prob, rows, cols)
+        check(Y[rows][:, cols], R, mag, f"pair M{M} N{N} K{K}")
+    assert mnb.mnb_fault_status() == 0
+
+
 @pytest.mark.parametrize("N", [1024, 2560, 4096, 9728, 4100])
 def test_pair_several_tiles_per_pair(dev, N):
     """More tiles than CTA pairs (each pair runs several tiles through both
