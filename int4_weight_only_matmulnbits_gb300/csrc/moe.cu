@@ -297,20 +297,51 @@ __device__ __forceinline__ int group_size(int c, int gt, int unit) {
   return n ? (c + unit * n - 1) / (unit * n) * unit : gt;
 }
 
-// Second launch: places. Each block adds up the counts of the blocks before
-// it and of all, scans the experts, and places its slots in order; block 0
-// writes the offsets and the groups. place[p]: where slot p stands in the
-// order, counting from 0; slots without an expert come last. 262 144 slots
-// of 128 experts: 16 us, and 5 for the counts; each block reads all blocks'
-// counts (33 000 words from L2), which costs less than another launch to add
-// them up. Blocks of 2048 slots are no faster there (router and lists 31.1 us
-// against 30.2) and slower for 3000 slots (9.1 against 7.4).
+// Between them, for many blocks: each expert's counts become sums over the
+// blocks before, in place, and row `blocks` the sum of all. A block for 32
+// experts, each warp a run of the rows.
+__global__ void __launch_bounds__(1024) scan_counts_kernel(int32_t *counts, int64_t blocks, int E) {
+  __shared__ int32_t sums[32][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e = blockIdx.x * 32 + lane;
+  const int64_t lo = blocks * warp / 32, hi = blocks * (warp + 1) / 32;
+  grid_dependency_wait();
+  grid_dependents_launch();
+  int32_t *c = counts + e;
+  int sum = 0;
+  if (e <= E) {
+#pragma unroll 8
+    for (int64_t b = lo; b < hi; ++b) sum += c[b * (E + 1)];
+  }
+  sums[warp][lane] = sum;
+  __syncthreads();
+  int at = 0;
+  for (int w = 0; w < warp; ++w) at += sums[w][lane];
+  if (e > E) return;
+  for (int64_t b0 = lo; b0 < hi; b0 += 8) {
+    int v[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[q] = b0 + q < hi ? c[(b0 + q) * (E + 1)] : 0;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      if (b0 + q < hi) c[(b0 + q) * (E + 1)] = at;
+      at += v[q];
+    }
+  }
+  if (warp == 31) c[blocks * (E + 1)] = at;
+}
+
+// Last launch: places. Each block learns how many slots of each expert stand
+// before it and in all (from scan_counts_kernel, or by adding up the counts),
+// scans the experts, and places its slots in order; block 0 writes the offsets
+// and the groups. place[p]: where slot p stands in the order, counting from 0;
+// slots without an expert come last. Blocks of 2048 slots are slower for 3000
+// slots (router and lists 9.1 us against 7.4).
 constexpr int kPlaceThreads = 512;
 constexpr int kPlaceWarps = kPlaceThreads / 32;
 __global__ void __launch_bounds__(kPlaceThreads)
-    place_kernel(const int32_t *experts, int64_t P, int E, const int32_t *counts, int32_t *offsets,
-                 int32_t *order, int32_t *place, SlotGroup *groups, int32_t *n_groups, int gt,
-                 int unit) {
+    place_kernel(const int32_t *experts, int64_t P, int E, const int32_t *counts, bool scanned,
+                 int32_t *offsets, int32_t *order, int32_t *place, SlotGroup *groups,
+                 int32_t *n_groups, int gt, int unit) {
   extern __shared__ int32_t mem[];
   int32_t *start = mem, *gstart = mem + E + 1;  // [E + 1] each
   int32_t *cnt = mem + 2 * (E + 1);             // [kPlaceWarps][E + 1]
@@ -335,9 +366,13 @@ __global__ void __launch_bounds__(kPlaceThreads)
 #pragma unroll
   for (int i = 0; i < kEach; ++i)
     if (key[i] >= 0) atomicAdd(mine + key[i], 1);
-  // Totals, and the part of them in the blocks before, by all threads: a few
-  // blocks' counts of an expert each.
-  for (int i = threadIdx.x; i < (E + 1) * kPlaceWarps; i += kPlaceThreads) {
+  // Totals, and the part of them in the blocks before (gstart until the scan):
+  // read, or added up by all threads, a few blocks' counts of an expert each.
+  for (int e = threadIdx.x; scanned && e <= E; e += kPlaceThreads) {
+    start[e] = counts[int64_t(gridDim.x) * (E + 1) + e];
+    gstart[e] = counts[int64_t(blockIdx.x) * (E + 1) + e];
+  }
+  for (int i = scanned ? (E + 1) * kPlaceWarps : threadIdx.x; i < (E + 1) * kPlaceWarps; i += kPlaceThreads) {
     const int e = i % (E + 1);
     int all = 0, before = 0;
 #pragma unroll 4
@@ -346,7 +381,7 @@ __global__ void __launch_bounds__(kPlaceThreads)
       all += c;
       if (b < blockIdx.x) before += c;
     }
-    if (all) {  // gstart holds the part before until the scan
+    if (all) {
       atomicAdd(start + e, all);
       if (before) atomicAdd(gstart + e, before);
     }
@@ -816,7 +851,17 @@ struct Lists {
 size_t max_groups(int64_t P, int E, int gt) {
   return static_cast<size_t>(std::min<int64_t>(P, P / gt + E));
 }
-size_t count_words(int64_t P, int E) { return ceil_div(P, kSortSlots) * (E + 1); }
+// Counts (blocks times experts) from which on a launch of its own sums them.
+// Fewer are added up by every block that places: a launch less, but work that
+// grows with the square of the slots. Router and lists, 8 choices, us, added up
+// by every block and by the launch:
+//   experts    65 536 slots   131 072        262 144        4 M
+//   64          10.9   12.9   15.9   16.8    23.3   22.8     668   266
+//   128         13.0   14.1   19.4   18.5    29.5   25.8    1120   310
+//   256         17.5   16.3   26.9   22.2    42.5   32.3    2041   406
+//   1000        49.5   36.2   79.0   57.4   141.1   95.0    7769  1358
+constexpr int64_t kScanCounts = 12288;
+size_t count_words(int64_t P, int E) { return (ceil_div(P, kSortSlots) + 1) * (E + 1); }
 
 // The lists of many slots: counts is workspace; place, and the groups of up to
 // gt slots (sizes in whole `unit`s), when asked for.
@@ -830,9 +875,13 @@ cudaError_t launch_lists(const int32_t *experts, int64_t P, int E, const Lists &
   const unsigned blocks = static_cast<unsigned>(ceil_div(P, kSortSlots));
   e = launch_pdl(count_kernel, blocks, kThreads, size_t(E + 1) * 4, pdl, stream, experts, P, E,
                  counts);
+  const bool scanned = int64_t(blocks) * (E + 1) >= kScanCounts;
+  if (e == cudaSuccess && scanned)
+    e = launch_pdl(scan_counts_kernel, static_cast<unsigned>(ceil_div(E + 1, 32)), 1024, 0, pdl,
+                   stream, counts, blocks, E);
   if (e != cudaSuccess) return e;
   return launch_pdl(place_kernel, blocks, kPlaceThreads, size_t(2 + kPlaceWarps) * (E + 1) * 4,
-                    pdl, stream, experts, P, E, counts, l.offsets, l.order, place, l.groups,
+                    pdl, stream, experts, P, E, counts, scanned, l.offsets, l.order, place, l.groups,
                     l.n_groups, gt, unit);
 }
 

@@ -165,6 +165,26 @@ def test_route_many_rows(dev, M, E, k):
     assert all(torch.equal(a, b) for a, b in zip(r, again))
 
 
+@pytest.mark.parametrize("M,E,k", [(12160, 128, 8), (12300, 128, 8), (400000, 64, 8),
+                                   (24000, 64, 8), (1400, 1000, 8), (1600, 1000, 8),
+                                   (130, 1024, 32), (3000, 1024, 32), (3200000, 3, 1)])
+@pytest.mark.parametrize("masked", [False, True])
+def test_route_lists_of_many_slots(dev, M, E, k, masked):
+    """Either way of summing the sort's counts, on both sides of where the choice changes;
+    slots without an expert come last."""
+    g = torch.Generator(device=dev).manual_seed(M)
+    x = torch.randn(M, E, generator=g, device=dev).to(BF16)
+    if masked:
+        x[:, E // 2:] = -math.inf
+        x[3::7] = -math.inf
+    r = mnb.mnb_moe_route(x, k)
+    key = torch.where(r.experts < 0, E, r.experts).flatten()
+    assert torch.equal(r.order.long(), torch.sort(key, stable=True).indices)
+    assert torch.equal(r.offsets.long(), torch.searchsorted(
+        torch.sort(key).values, torch.arange(E + 1, device=dev, dtype=torch.int32)))
+    assert ((r.experts < 0) == (r.weights == 0)).all()
+
+
 # ---- products --------------------------------------------------------------------------------
 
 def run_experts(dev, M, E, k, N, K, bs, dtype, *, sdt=None, zp=False, bias=False,
@@ -471,6 +491,14 @@ def test_layer_many_experts(dev, M, dtype):
     """As many choices as the operators take, of nearly as many experts."""
     X, logits, ws = layer_inputs(dev, M, 1000, 32, 72, 40, 32, dtype, seed=M)
     run_layer(dev, X, logits, ws, 32, what=f"M{M}")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_layer_many_counts(dev, dtype):
+    """Enough slots and experts for the sort's counts to be summed by a launch of their own."""
+    X, logits, ws = layer_inputs(dev, 420, 1000, 32, 72, 40, 32, dtype, seed=1)
+    logits[5] = -math.inf
+    run_layer(dev, X, logits, ws, 32, what="many counts")
 
 
 @pytest.mark.parametrize("M", [1, 7])
