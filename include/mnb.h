@@ -832,7 +832,9 @@ MNB_API mnb_status mnb_moe_route(const void *logits, mnb_dtype logits_dtype, int
  * long for the kernel of fewer slots (25 000 to 59 000 elements, by block size
  * and scale type), they are rounded once to fp16 (2^-11; small scales to 2^-15
  * of their row's largest).
- * Magnitudes of scales up to 2^100. An infinity or NaN in a row of A makes
+ * Magnitudes of scales up to 2^104 / K, at most 2^80: sums are formed for
+ * activations brought to 2^15, and 16 times too large for half of the rows.
+ * An infinity or NaN in a row of A makes
  * the outputs of its slots non-finite (not always as an exact sum would be)
  * and touches no other.
  * fp32 activations stream the weights for every eight slots: meant for decode

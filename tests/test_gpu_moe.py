@@ -274,6 +274,26 @@ def test_experts_wide_magnitudes(dev):
         ref.check(mnb.mnb_matmul_experts(A, w, t), R, err, f"M{M} {dtype}")
 
 
+@pytest.mark.parametrize("M", [3, 140])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("size", [1.0, 2.0 ** -60, 2.0 ** 20])
+@pytest.mark.parametrize("code", [0x00, 0xFF])
+def test_experts_largest_scales(dev, M, dtype, size, code):
+    """Scales of 2^80, the largest that the products take, with every term of one sign and
+    every code at its end: no sum on the way overflows, whatever the activations' size."""
+    E, k, N = 3, 2, 40
+    for K, bs in ((2560, 32), (16384, 128)):
+        B = torch.full((E, N, K // bs, bs // 2), code, dtype=torch.uint8)
+        z = torch.full((E, N, (K // bs + 1) // 2), 0xFF - code, dtype=torch.uint8)
+        s = torch.full((E, N, K // bs), 2.0 ** 80, dtype=dtype)
+        for zp in (None, z):
+            w, _, W = pack(dev, (B, s, zp, None), N, K, bs)
+            A = torch.full((M, K), size, dtype=dtype, device=dev)
+            t = torch.randint(0, E, (M, k), dtype=torch.int32).to(dev)
+            R, err = ref.products(A.double().unsqueeze(1).expand(M, k, K), W, t, None, dtype)
+            ref.check(mnb.mnb_matmul_experts(A, w, t), R, err, f"K{K}")
+
+
 # ---- the layer ---------------------------------------------------------------------------------
 
 def layer_inputs(dev, M, E, k, H, I, bs, dtype, *, sdt=None, zp=False, bias=False, seed=0,
