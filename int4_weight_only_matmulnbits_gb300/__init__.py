@@ -25,6 +25,7 @@ __all__ = ["EXPORTS", "MNB_CODES_AFFINE", "MNB_CODES_CODEBOOK", "ChainOp", "MnbC
            "mnb_matmul_experts", "mnb_matmul_gate_up", "mnb_matmul_grouped", "mnb_matmul_plan", "mnb_matmul_rmsnorm",
            "mnb_matmul_workspace", "mnb_moe", "mnb_moe_route", "mnb_packed_forget", "mnb_packed_header_make",
            "mnb_packed_read_header", "mnb_packed_register", "mnb_prepack", "mnb_prepack_bnb4",
+           "mnb_prepack_experts",
            "mnb_prepack_qdq", "mnb_prepacked_sizes", "mnb_set_programmatic_launch",
            "mnb_test_wait_fault",
            "mnb_unprepack", "mnb_version", "status_string"]

@@ -44,6 +44,12 @@ def stack(i=0, *, E=8, N=64, K=128, bs=32, sdt=BF16, zp=False, bias=False, regis
     return s
 
 
+def test_public_names():
+    """Every call of the package is among the names that it exports."""
+    calls = {n for n in dir(mnb) if n.startswith("mnb_")}
+    assert calls <= set(mnb.__all__) and all(hasattr(mnb, n) for n in mnb.__all__)
+
+
 def route(lib, logits=LOG, dt=F32, M=4, E=8, k=2, norm=1, w=WEI, e=EXP, off=OFF, order=ORD,
           ws=WS, ws_bytes=1 << 30):
     return lib.mnb_moe_route(vp(logits), dt, M, E, k, norm, vp(w), vp(e), vp(off), vp(order),
