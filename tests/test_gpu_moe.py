@@ -577,6 +577,68 @@ def test_layer_rows_do_not_mix(dev, M):
     assert torch.equal(Y[1:], Z[1:])
 
 
+@pytest.mark.parametrize("dtype,per_slot", [(BF16, True), (BF16, False), (F32, True)])
+def test_experts_offsets_past_32_bits(dev, dtype, per_slot):
+    """More than 2^31 elements of activations by slot, and of outputs: sampled rows."""
+    M, k, E, bs = 70000, 8, 12, 32
+    g = torch.Generator().manual_seed(1)
+    gd = torch.Generator(device=dev).manual_seed(1)
+    t = torch.randint(-1, E, (M, k), generator=gd, device=dev, dtype=torch.int32)
+    for N, K in ((16, 4096), (4096, 64)):
+        w, b, W = pack(dev, stack(g, E, N, K, bs, dtype, False, True), N, K, bs)
+        A = torch.randn(*((M, k, K) if per_slot else (M, K)), generator=gd, device=dev,
+                        dtype=dtype)
+        Y = mnb.mnb_matmul_experts(A, w, t, b)
+        m = torch.tensor([0, 1, 33333, 65535, 65536, M - 2, M - 1], device=dev)
+        a = A[m].double() if per_slot else A[m].double().unsqueeze(1).expand(len(m), k, K)
+        R, err = ref.products(a, W, t[m], b, dtype)
+        ref.check(Y[m], R, err, f"N{N} K{K}")
+        del A, Y
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_layer_offsets_past_32_bits(dev, dtype):
+    """More than 2^31 hidden values, and as many down sums: sampled tokens."""
+    M, k, E, bs = 70000, 8, 12, 32
+    for H, I in ((64, 4096), (4096, 64)):
+        _, _, ws = layer_inputs(dev, 1, E, k, H, I, bs, dtype, bias=True, seed=H)
+        gd = torch.Generator(device=dev).manual_seed(H)
+        X = torch.randn(M, H, generator=gd, device=dev, dtype=dtype)
+        logits = torch.randn(M, E, generator=gd, device=dev)
+        logits[33333, 3:] = -math.inf
+        (wg, bg, Wg), (wu, bu, Wu), (wd, bd, Wd) = ws
+        Y = mnb.mnb_moe(X, logits, wg, wu, wd, k, bias_gate=bg, bias_up=bu, bias_down=bd)
+        m = torch.tensor([0, 1, 33333, 65535, 65536, M - 2, M - 1], device=dev)
+        weights, experts, _, _ = ref.route(logits[m], k, True)
+        R, err = ref.layer(X[m], weights, experts.to(dev), Wg, Wu, Wd, bg, bu, bd, dtype)
+        ref.check(Y[m], R, err, f"H{H} I{I}")
+        del X, Y
+
+
+@pytest.mark.parametrize("M", [5, 140])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("off", [1, 2, 3])
+def test_rows_off_alignment(dev, M, dtype, off):
+    """Activations, logits and outputs that start off the 16 bytes (and off pairs) that whole
+    tensors start on give what aligned ones do."""
+    E, k, H, I = 9, 3, 128, 96
+    X, logits, ws = layer_inputs(dev, M, E, k, H, I, 32, dtype, seed=M)
+    packed = [w for w, _, _ in ws]
+
+    def shifted(t):
+        y = torch.empty(t.numel() + off, dtype=t.dtype, device=dev)[off:].view(t.shape)
+        return y.copy_(t)
+
+    r = mnb.mnb_moe_route(logits, k)
+    Y = mnb.mnb_moe(X, logits, *packed, k)
+    P = mnb.mnb_matmul_experts(X, packed[0], r.experts)
+    out = shifted(torch.zeros_like(Y))
+    assert torch.equal(mnb.mnb_moe(shifted(X), shifted(logits), *packed, k, out=out), Y)
+    out = shifted(torch.zeros_like(P))
+    assert torch.equal(
+        mnb.mnb_matmul_experts(shifted(X), packed[0], shifted(r.experts), out=out), P)
+
+
 # ---- streams and graphs --------------------------------------------------------------------------
 
 @pytest.mark.parametrize("M", [1, 12, 140])
