@@ -43,9 +43,12 @@
 //  * Measured, 8 out of 128 experts, 2560 -> 768 -> 2560, blocks of 32: 16
 //    tokens 47 us for gate and up (171 MB, 3.6 TB/s, 54 % of the issue slots)
 //    and 28 for down (85 MB, 3.0 TB/s); one token 11 and 9 us, of which the
-//    weights (17 and 9 MB) are 4. What bounds the first is some 75
-//    instructions per chunk (the MMAs of 8 columns take a quarter of the
-//    tensor pipe); the second the launches and chains of dependent loads.
+//    weights (17 and 9 MB) are 4. The first takes some 75 instructions per
+//    chunk, 54 % of the issue slots (the MMAs of 8 columns take a quarter of
+//    the tensor pipe), and loses a third to the division of work: whole steps
+//    over 456 CTAs are 65 chunk times by the rule's own cost (moe.cu) where an
+//    even share is 43 (down: 32 and 21). The second is bound by the launches
+//    and chains of dependent loads.
 #pragma once
 
 #include <cuda_fp16.h>

@@ -33,14 +33,16 @@
 //    ring of asynchronous copies, in two groups that alternate stages; warps
 //    16-23 store; one warp each issues the TMA loads, issues the MMAs, and
 //    gathers what a unit's columns need for the epilogue.
-//  * What bounds it is issue slots: per 16 x 64 chunk a warp takes about 117
+//  * What bounds it is the unpacking: per 16 x 64 chunk a warp takes about 117
 //    instructions (23 to fetch, 48 to unpack, 20 of them for the scales, the
-//    rest for a stage's waits, store and arrival; 140 with zero points), and
-//    57 % of the slots are taken, four unpacking warps a scheduler leaving
-//    gaps. Measured, 8 out of 128 experts, 2560 -> 768 -> 2560, 4096 tokens:
-//    gate and up 205 us = 1260 TFLOP/s, tensor pipe 60 % busy, down 142 us =
-//    910; 6 out of 64, 2560 -> 1408 -> 2560, 192 tokens: 101 us = 2.4 TB/s of
-//    weights, and 56. Groups of 64 slots with 6 TMEM stages and 8 activation
+//    rest for a stage's waits, store and arrival; 140 with zero points). They
+//    take 52 to 59 % of the issue slots: a stage's two chunks follow one
+//    another through one set of registers, and four unpacking warps a
+//    scheduler do not fill the gaps. Lists above 192 slots take several
+//    groups, and every group unpacks the weights again. Measured, 8 out of 128
+//    experts, 2560 -> 768 -> 2560, 4096 tokens: gate and up 207 us = 1250
+//    TFLOP/s, tensor pipe 59 % busy, down 139 us = 930; 6 out of 64, 2560 ->
+//    1408 -> 2560, 192 tokens: 102 us = 2.4 TB/s of weights, and 56. Groups of 64 slots with 6 TMEM stages and 8 activation
 //    stages, for few slots per expert, were no faster (166.6 against 165.5 us
 //    for the layer at a mean of 4, 183.0 against 181.0 at 16).
 #include <cuda_fp16.h>
@@ -548,8 +550,9 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
             }
           }
         };
-        // Both chunks without a branch: their instructions interleave. (A lone
-        // last chunk's partner is whatever the stage held, and is not stored.)
+        // One chunk after the other through the same registers: at 72 a thread
+        // there is no room for two sets, so the second is unpacked behind the
+        // first one's store.
         uint32_t r0[16];
         unpack(0, r0);
         if (use > 0 && !mbar_sleep(aempty + grp, (use - 1) & 1)) {

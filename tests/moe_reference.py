@@ -12,8 +12,8 @@ choose:
   * bf16 activations: a weight may be rounded to fp16 (2^-11) and so may a hidden value
     (2^-11); a result is rounded to bf16 (2^-8). fp16 activations (for fp32 ones, the parts
     they are split into) are scaled by a power of two so that a bound of the row (its largest
-    magnitude; for a hidden row, the product of the bounds of its gate and up sums) lies in
-    2^14 .. 2^15: they are exact down to 2^-14 and within 2^-25 below that, at most
+    magnitude; for a hidden row, at most the product of the bounds of its gate and up sums, which
+    is what is allowed here) lies in 2^14 .. 2^15: they are exact down to 2^-14 and within 2^-25 below that, at most
     FLOOR = 2^-39 of the row's bound. The offset of the codes
     may be taken off a block as a whole: codes of 1024 + r q carry an offset of 1024 + r z (r is
     1 or 16, divided out again at the end), and (1024 + r z) s / r times the sum of a block's
