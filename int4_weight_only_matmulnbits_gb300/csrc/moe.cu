@@ -368,22 +368,25 @@ __global__ void __launch_bounds__(kPlaceThreads)
     if (key[i] >= 0) atomicAdd(mine + key[i], 1);
   // Totals, and the part of them in the blocks before (gstart until the scan):
   // read, or added up by all threads, a few blocks' counts of an expert each.
-  for (int e = threadIdx.x; scanned && e <= E; e += kPlaceThreads) {
-    start[e] = counts[int64_t(gridDim.x) * (E + 1) + e];
-    gstart[e] = counts[int64_t(blockIdx.x) * (E + 1) + e];
-  }
-  for (int i = scanned ? (E + 1) * kPlaceWarps : threadIdx.x; i < (E + 1) * kPlaceWarps; i += kPlaceThreads) {
-    const int e = i % (E + 1);
-    int all = 0, before = 0;
-#pragma unroll 4
-    for (int b = i / (E + 1); b < gridDim.x; b += kPlaceWarps) {
-      const int c = counts[int64_t(b) * (E + 1) + e];
-      all += c;
-      if (b < blockIdx.x) before += c;
+  if (scanned) {
+    for (int e = threadIdx.x; e <= E; e += kPlaceThreads) {
+      start[e] = counts[int64_t(gridDim.x) * (E + 1) + e];
+      gstart[e] = counts[int64_t(blockIdx.x) * (E + 1) + e];
     }
-    if (all) {
-      atomicAdd(start + e, all);
-      if (before) atomicAdd(gstart + e, before);
+  } else {
+    for (int i = threadIdx.x; i < (E + 1) * kPlaceWarps; i += kPlaceThreads) {
+      const int e = i % (E + 1);
+      int all = 0, before = 0;
+#pragma unroll 4
+      for (int b = i / (E + 1); b < gridDim.x; b += kPlaceWarps) {
+        const int c = counts[int64_t(b) * (E + 1) + e];
+        all += c;
+        if (b < blockIdx.x) before += c;
+      }
+      if (all) {
+        atomicAdd(start + e, all);
+        if (before) atomicAdd(gstart + e, before);
+      }
     }
   }
   __syncthreads();
@@ -950,12 +953,13 @@ ExpertsSpace experts_space(const ExpertsArgs &a) {
 // ---- tensor-core path: bf16 activations, many slots ---------------------------
 
 // From a mean of this many slots per expert on; fewer stream the weights past
-// groups of up to 8 slots. Both measured, streaming and tensor-core path, us:
-//   experts, top_k       mean 4              mean 8
-//   8, 2             23.3    31.4        31.9    31.8
-//   16, 4            17.4    24.3        24.1    25.1
-//   32, 4            69.2    84.4        88.3    89.4
-//   128, 8          143.5   165.5       204.2   171.3
+// groups of up to 8 slots. The layer, blocks of 32, streaming and tensor-core
+// path, us:
+//   experts, top_k, H, I       mean 4          mean 6          mean 8
+//   8, 2, 1024, 2048        25.3    33.8    29.7    34.2    32.3    34.3
+//   16, 4, 1024, 512        17.2    26.0    22.5    26.3    25.7    26.9
+//   32, 4, 2560, 1408       74.6    95.0    96.7    95.2   104.2    95.0
+//   128, 8, 2560, 768      140.0   171.7   187.4   180.3   195.0   181.3
 // A row too long for the streaming kernel's shared memory (K beyond 25 000 to
 // 59 000, by block size and scale type) takes the tensor-core path as well.
 constexpr int kTileMeanSlots = 6;

@@ -42,9 +42,10 @@
 //    groups, and every group unpacks the weights again. Measured, 8 out of 128
 //    experts, 2560 -> 768 -> 2560, 4096 tokens: gate and up 207 us = 1250
 //    TFLOP/s, tensor pipe 59 % busy, down 139 us = 930; 6 out of 64, 2560 ->
-//    1408 -> 2560, 192 tokens: 102 us = 2.4 TB/s of weights, and 56. Groups of 64 slots with 6 TMEM stages and 8 activation
-//    stages, for few slots per expert, were no faster (166.6 against 165.5 us
-//    for the layer at a mean of 4, 183.0 against 181.0 at 16).
+//    1408 -> 2560, 192 tokens: 102 us = 2.4 TB/s of weights, and 56. Groups
+//    of 64 slots with 6 TMEM stages and 8 activation stages, for few slots per
+//    expert, were no faster (before hidden rows were fp32: 166.6 against 165.5
+//    us for the layer at a mean of 4, 183.0 against 181.0 at 16).
 #include <cuda_fp16.h>
 
 #include <algorithm>
