@@ -879,6 +879,180 @@ MNB_API mnb_status mnb_moe(const void *X, const void *logits, mnb_dtype logits_d
                            mnb_dtype a_dtype, void *workspace, size_t workspace_bytes,
                            mnb_stream_t stream);
 
+/*
+ * The attention block around the projections (page "Qwen3 CPU Inference
+ * Critical Path": GroupQueryAttention with half-split rotary positions,
+ * RotaryEmbedding with its caches of cosines and sines, PagedAttention, and
+ * the fusion of QK layout, rotation and cache; the page names the operators,
+ * the conventions below are this library's).
+ *
+ * mnb_heads describes rows of heads: element d of head h of token t lies at
+ * data + t * token_stride + h * head_stride + d (strides in elements), so the
+ * rows of a fused q, k, v projection are read where they are. HOST struct,
+ * DEVICE pointer inside. Rows of an output do not overlap one another: one of
+ * its strides spans all that the other covers (MNB_ERR_ALIAS).
+ */
+typedef struct {
+  void *data;
+  int64_t token_stride, head_stride;
+  int32_t heads;
+  int32_t reserved; /* 0 */
+} mnb_heads;
+
+/* Rotary positions: tables from mnb_rope_table (or a model's own), fp32
+ * [positions, rot_dim / 2], and which elements of the first rot_dim of a head
+ * are pair i: (i, i + rot_dim / 2), or (2 i, 2 i + 1) with interleaved = 1.
+ * Elements from rot_dim on are not rotated. HOST struct. */
+typedef struct {
+  const float *cos, *sin;
+  int64_t positions;
+  int32_t rot_dim;
+  int32_t interleaved;
+} mnb_rope;
+
+/* A paged cache of keys and values: element d of head h of the token at place
+ * i of page g lies at k + g * k_page_stride + h * k_head_stride +
+ * i * k_token_stride + d (strides in elements), and likewise for v. HOST
+ * struct. page_size: a multiple of 16 (one page of a whole sequence's length
+ * makes a contiguous cache). */
+typedef struct {
+  void *k, *v;
+  int64_t pages;
+  int64_t k_page_stride, k_head_stride, k_token_stride;
+  int64_t v_page_stride, v_head_stride, v_token_stride;
+  int32_t page_size, heads, head_dim;
+  int32_t dtype; /* mnb_dtype */
+} mnb_kv_cache;
+
+/* The sequences of a step, DEVICE arrays in a HOST struct. Sequence b has the
+ * rows starts[b] .. starts[b + 1] of the call's T rows (starts does not
+ * decrease; equal: nothing new), its last one at position lengths[b] - 1: a
+ * length counts the new tokens. Position p is at place p % page_size of page
+ * table[b * table_stride + p / page_size]. The kernels read the arrays when
+ * they run, so a captured graph follows their contents; whatever they hold,
+ * nothing outside the buffers is read or written: a page index outside
+ * 0 .. pages - 1 names no page, positions past table_pages * page_size have
+ * none, rows at or past starts[n] belong to no sequence. */
+typedef struct {
+  const int32_t *starts;  /* [n + 1] */
+  const int32_t *lengths; /* [n] */
+  const int32_t *table;   /* [n, table_pages], rows table_stride apart */
+  int64_t n, table_pages, table_stride;
+} mnb_kv_batch;
+
+/*
+ * Angles per position of the rot_dim / 2 pairs (pure host arithmetic):
+ *   f_i = base^(-2 i / rot_dim)
+ * and, for contexts longer than the model was trained for, with factor > 1:
+ *   original = 0: f_i / factor (positions interpolated);
+ *   original > 0: (1 - r_i) f_i / factor + r_i f_i, by the turns
+ *     n_i = original * f_i / 2 pi that pair i makes within the original
+ *     length: r_i = (n_i - low) / (high - low) kept within 0 .. 1 (the ramp of
+ *     YaRN, "Efficient Context Window Extension of Large Language Models",
+ *     section 3.2).
+ * Errors: MNB_ERR_NULL, MNB_ERR_SHAPE (rot_dim odd, < 2 or > 256; base or
+ * factor not positive and finite; original negative or not finite; with
+ * original > 0, not 0 <= low < high).
+ */
+MNB_API mnb_status mnb_rope_frequencies(int rot_dim, double base, double factor,
+                                        double original, double low, double high, double *out);
+
+/*
+ * Tables of cosines and sines of positions first .. first + n - 1:
+ *   cos[r, i] = magnitude * cos((first + r) * frequencies[i]), sin likewise,
+ * fp32 [n, rot_dim / 2]. frequencies: HOST, rot_dim / 2 doubles. The angle is
+ * kept to 2^-53 of the frequency times the position whatever the position;
+ * results are within 2^-22 of themselves.
+ * Errors: MNB_ERR_NULL, MNB_ERR_SHAPE (rot_dim odd, < 2 or > 256; n < 1 or
+ * first < 0, or first + n past 2^31 - 1; a frequency or the magnitude not
+ * finite), MNB_ERR_ALIGN, MNB_ERR_ALIAS, MNB_ERR_DEVICE, MNB_ERR_CUDA.
+ */
+MNB_API mnb_status mnb_rope_table(const double *frequencies, int rot_dim, int64_t first,
+                                  int64_t n, double magnitude, float *cos, float *sin,
+                                  mnb_stream_t stream);
+
+/*
+ * Norms of queries and keys for each head, with the position rotation in the
+ * same pass: each row x of q (and of k) becomes
+ *   y = x / sqrt(mean(x^2) + eps) * gamma,  then rotated by positions[t],
+ * in fp32, rounded once.
+ *  q, k: T rows each of head_dim elements (k NULL: none), dtype elements.
+ *  gamma_q, gamma_k: fp32 [head_dim], NULL: that norm is left out.
+ *  positions int32 [T]: a position outside 0 .. rope->positions - 1 gives rows
+ *    of zeros. rope (HOST) and positions NULL: no rotation.
+ *  q_out, k_out: as q and k, which they may equal (same pointer and strides:
+ *    in place); no other overlap with an input.
+ * Errors: MNB_ERR_NULL (also k without k_out, rope without positions),
+ * MNB_ERR_SHAPE (T < 1 or past 2^31 - 1, heads < 1, head_dim < 2 or odd,
+ * rot_dim odd, < 2 or > head_dim, negative strides, eps negative or not
+ * finite, heads of an output unlike its input's), MNB_ERR_UNSUPPORTED
+ * (head_dim > 256), MNB_ERR_DTYPE, MNB_ERR_ALIGN (to the elements),
+ * MNB_ERR_ALIAS, MNB_ERR_DEVICE, MNB_ERR_CUDA.
+ */
+MNB_API mnb_status mnb_qk_norm_rope(const mnb_heads *q, const mnb_heads *k, int64_t T,
+                                    int head_dim, mnb_dtype dtype, const float *gamma_q,
+                                    const float *gamma_k, float eps, const mnb_rope *rope,
+                                    const int32_t *positions, const mnb_heads *q_out,
+                                    const mnb_heads *k_out, mnb_stream_t stream);
+
+/*
+ * The new tokens of a step on their way from the projections to the cache:
+ * rows of q and k normed and rotated as by mnb_qk_norm_rope, at the positions
+ * that the batch gives; q into q_out, k and the rows of v (as they are) into
+ * the cache. One launch.
+ *  q, q_out: both NULL: keys and values alone. q_out may equal q.
+ *  k, v: cache->heads heads of cache->head_dim elements of cache->dtype.
+ *  rope NULL: no rotation. Its table has to hold the positions: a row of q or
+ *    k at another position becomes zeros.
+ * A token whose position no page holds appends nothing. Rows that belong to no
+ * sequence leave q_out and the cache as they were, and so does every place of
+ * the cache that no new token has. Two tokens of one place (a page that two
+ * sequences write): one of them, unspecified which, element by element.
+ * Errors: as mnb_qk_norm_rope, and MNB_ERR_SHAPE for page_size not a positive
+ * multiple of 16, pages, n or table_pages < 1, pages, n or table_pages *
+ * page_size past 2^31 - 1, table_stride < table_pages, strides of the cache
+ * below head_dim; MNB_ERR_ALIAS also for a cache that overlaps an input or
+ * whose keys and values start at one address.
+ */
+MNB_API mnb_status mnb_cache_append(const mnb_heads *q, const mnb_heads *k, const mnb_heads *v,
+                                    int64_t T, const float *gamma_q, const float *gamma_k,
+                                    float eps, const mnb_rope *rope, const mnb_kv_cache *cache,
+                                    const mnb_kv_batch *batch, const mnb_heads *q_out,
+                                    mnb_stream_t stream);
+
+/*
+ * Attention of each sequence's new tokens over its pages:
+ *   out[t, h] = sum_j w_j v_j / sum_j w_j,  w_j = exp(scale * q[t, h] . k_j),
+ * over the keys j of key head h / (q->heads / cache->heads) with j <= p, p the
+ * token's position, and j > p - window when window > 0. Keys of a position
+ * that no page holds are not attended. A token that attends no key gets zeros;
+ * rows that belong to no sequence are left as they were.
+ *  q, out: T rows of cache->dtype; q->heads a multiple of cache->heads.
+ *  workspace: mnb_paged_attention_workspace_size bytes of DEVICE memory,
+ *    256-byte aligned; needs no preparation, means nothing afterwards. Calls
+ *    that may overlap on the GPU need one each.
+ * Sums and the softmax are fp32. bf16: weights relative to a running maximum
+ * are rounded to bf16 (2^-9) for the product with the values, not for their
+ * sum. fp32: products from tf32 pairs, within 2^-20 of the terms' magnitudes.
+ * What a masked place holds does not matter, infinities and NaN included. An
+ * infinity or NaN in a key or value that a row does attend makes the row
+ * non-finite (not always as an exact sum would be), and no other.
+ * Results are bitwise reproducible for the same arrays, T and GPU.
+ * Errors: as mnb_cache_append, and MNB_ERR_SHAPE for q->heads not a multiple
+ * of cache->heads, a scale that is not finite, window < 0 or a workspace too
+ * small; MNB_ERR_UNSUPPORTED for head_dim other than 64 and 128;
+ * MNB_ERR_ALIGN for rows of q, out or the cache off 16 bytes (pointers and
+ * strides), or the workspace; MNB_ERR_ALIAS for an output or the workspace
+ * over another buffer.
+ */
+MNB_API size_t mnb_paged_attention_workspace_size(int64_t T, int q_heads,
+                                                  const mnb_kv_cache *cache,
+                                                  const mnb_kv_batch *batch);
+MNB_API mnb_status mnb_paged_attention(const mnb_heads *q, int64_t T, const mnb_kv_cache *cache,
+                                       const mnb_kv_batch *batch, float scale, int64_t window,
+                                       const mnb_heads *out, void *workspace,
+                                       size_t workspace_bytes, mnb_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -47,7 +47,9 @@ EXPORTS = ("mnb_status_string", "mnb_last_error_string", "mnb_version",
            "mnb_graph_run_from_host", "mnb_graph_destroy", "mnb_test_wait_fault",
            "mnb_prepack_experts", "mnb_moe_route_workspace_size", "mnb_moe_route",
            "mnb_matmul_experts_workspace_size", "mnb_matmul_experts",
-           "mnb_moe_workspace_size", "mnb_moe")
+           "mnb_moe_workspace_size", "mnb_moe", "mnb_rope_frequencies", "mnb_rope_table",
+           "mnb_qk_norm_rope", "mnb_cache_append", "mnb_paged_attention_workspace_size",
+           "mnb_paged_attention")
 
 _lock = threading.Lock()
 _lib = None
@@ -99,6 +101,35 @@ class ExpertsC(ctypes.Structure):
                 ("bias", ctypes.c_void_p), ("E", ctypes.c_int64), ("N", ctypes.c_int64),
                 ("K", ctypes.c_int64),
                 ("block_size", ctypes.c_int32), ("scale_dtype", ctypes.c_int32)]
+
+
+class HeadsC(ctypes.Structure):
+    """mnb_heads (include/mnb.h)."""
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("heads", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class RopeC(ctypes.Structure):
+    """mnb_rope (include/mnb.h)."""
+    _fields_ = [("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p),
+                ("positions", ctypes.c_int64), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32)]
+
+
+class KvCacheC(ctypes.Structure):
+    """mnb_kv_cache (include/mnb.h)."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p)] + [
+        (f, ctypes.c_int64) for f in ("pages", "k_page_stride", "k_head_stride",
+                                      "k_token_stride", "v_page_stride", "v_head_stride",
+                                      "v_token_stride")] + [
+        (f, ctypes.c_int32) for f in ("page_size", "heads", "head_dim", "dtype")]
+
+
+class KvBatchC(ctypes.Structure):
+    """mnb_kv_batch (include/mnb.h)."""
+    _fields_ = [(f, ctypes.c_void_p) for f in ("starts", "lengths", "table")] + [
+        (f, ctypes.c_int64) for f in ("n", "table_pages", "table_stride")]
 
 
 class MnbError(RuntimeError):
@@ -224,6 +255,20 @@ def load(build_if_missing: bool = False):
         lib.mnb_moe_workspace_size.restype = sz
         lib.mnb_moe.argtypes = [p, p, i32, i64, i32, i32, e, e, e, p, i32, p, sz, p]
         lib.mnb_moe.restype = i32
+        f64, f32 = ctypes.c_double, ctypes.c_float
+        h, r, c, b = (ctypes.POINTER(t) for t in (HeadsC, RopeC, KvCacheC, KvBatchC))
+        lib.mnb_rope_frequencies.argtypes = [i32, f64, f64, f64, f64, f64, p]
+        lib.mnb_rope_frequencies.restype = i32
+        lib.mnb_rope_table.argtypes = [p, i32, i64, i64, f64, p, p, p]
+        lib.mnb_rope_table.restype = i32
+        lib.mnb_qk_norm_rope.argtypes = [h, h, i64, i32, i32, p, p, f32, r, p, h, h, p]
+        lib.mnb_qk_norm_rope.restype = i32
+        lib.mnb_cache_append.argtypes = [h, h, h, i64, p, p, f32, r, c, b, h, p]
+        lib.mnb_cache_append.restype = i32
+        lib.mnb_paged_attention_workspace_size.argtypes = [i64, i32, c, b]
+        lib.mnb_paged_attention_workspace_size.restype = sz
+        lib.mnb_paged_attention.argtypes = [h, i64, c, b, f32, i64, h, p, sz, p]
+        lib.mnb_paged_attention.restype = i32
         _lib = lib
         return lib
 
@@ -963,4 +1008,257 @@ def mnb_moe(X: torch.Tensor, logits: torch.Tensor, gate: PackedExperts, up: Pack
                            1 if normalize else 0, g, u, d, Y.data_ptr(), code, wp, n, s),
                "mnb_moe")
         return Y
+    return _call_on(dev, stream, call)
+
+
+# ---- attention block --------------------------------------------------------------
+
+class RopeTable(NamedTuple):
+    """Cosines and sines of rotary positions, fp32 [positions, rot_dim / 2]."""
+    cos: torch.Tensor
+    sin: torch.Tensor
+
+
+@dataclass(frozen=True)
+class KvCache:
+    """A paged cache of keys and values, [pages, heads, page_size, head_dim]
+    each, in any layout whose last dimension is contiguous (pages kept token
+    first are a transposed view)."""
+    k: torch.Tensor
+    v: torch.Tensor
+
+    def __getstate__(self):
+        """Copied and pickled without the argument struct (addresses)."""
+        return {n: t for n, t in self.__dict__.items() if n != "_struct"}
+
+
+@dataclass(frozen=True)
+class KvBatch:
+    """The sequences of a step, int32 on the GPU: sequence b has the rows
+    starts[b] .. starts[b + 1], its length with them is lengths[b], and its
+    tokens lie in the pages table[b]. The kernels read them when they run."""
+    starts: torch.Tensor   # [n + 1]
+    lengths: torch.Tensor  # [n]
+    table: torch.Tensor    # [n, pages of the longest sequence]
+
+    def __getstate__(self):
+        """Copied and pickled without the argument struct (addresses)."""
+        return {n: t for n, t in self.__dict__.items() if n != "_struct"}
+
+
+def _heads_struct(name: str, t: torch.Tensor, device, like: torch.Tensor | None = None) -> HeadsC:
+    """mnb_heads of a [T, heads, head_dim] tensor whose last dimension is
+    contiguous."""
+    if t.dim() != 3 or t.device != device or not t.is_cuda:
+        raise ValueError(f"{name} must be a [T, heads, head_dim] tensor on {device}")
+    s = t.stride()
+    if s[2] != 1 and t.shape[2] != 1:
+        raise ValueError(f"{name}'s heads must be contiguous")
+    if like is not None and (t.dtype != like.dtype or t.shape[0] != like.shape[0]
+                             or t.shape[2] != like.shape[2]):
+        raise ValueError(f"{name} must have the rows, head size and dtype of the call's others")
+    return HeadsC(t.data_ptr(), s[0], s[1], t.shape[1], 0)
+
+
+def _cache_struct(c: KvCache, device) -> KvCacheC:
+    """mnb_kv_cache of c, kept with it for as long as its tensors are where
+    they were."""
+    at = (c.k.data_ptr(), c.v.data_ptr())
+    kept = c.__dict__.get("_struct")
+    if kept is None or kept[0] != at:
+        if c.k.dim() != 4 or c.v.shape != c.k.shape or c.v.dtype != c.k.dtype:
+            raise ValueError("k and v must be [pages, heads, page_size, head_dim] tensors of "
+                             "one dtype")
+        if not c.k.is_cuda or c.v.device != c.k.device:
+            raise ValueError("k and v must be on one GPU")
+        if c.k.stride(3) != 1 or c.v.stride(3) != 1:
+            raise ValueError("the rows of k and v must be contiguous")
+        pages, heads, page_size, D = c.k.shape
+        kept = (at, KvCacheC(*at, pages, *c.k.stride()[:3], *c.v.stride()[:3], page_size, heads,
+                             D, _dtype_code(c.k.dtype)))
+        c.__dict__["_struct"] = kept
+    if c.k.device != device:
+        raise ValueError(f"the cache is on {c.k.device}, the call runs on {device}")
+    return kept[1]
+
+
+def _batch_struct(b: KvBatch, device) -> KvBatchC:
+    """mnb_kv_batch of b, kept with it as _cache_struct's."""
+    at = (b.starts.data_ptr(), b.lengths.data_ptr(), b.table.data_ptr())
+    kept = b.__dict__.get("_struct")
+    if kept is None or kept[0] != at:
+        n = b.lengths.shape[0] if b.lengths.dim() == 1 else -1
+        if b.starts.shape != (n + 1,) or b.table.dim() != 2 or b.table.shape[0] != n:
+            raise ValueError("a batch of n sequences has starts [n + 1], lengths [n] and "
+                             "table [n, pages]")
+        for name, t in (("starts", b.starts), ("lengths", b.lengths), ("table", b.table)):
+            if t.dtype != torch.int32 or not t.is_cuda or t.device != b.table.device:
+                raise ValueError(f"{name} must be int32, on the batch's GPU")
+            if t.numel() and t.stride(-1) != 1:
+                raise ValueError(f"{name} must be contiguous")
+        kept = (at, KvBatchC(*at, n, b.table.shape[1],
+                             b.table.stride(0) if n > 1 else b.table.shape[1]))
+        b.__dict__["_struct"] = kept
+    if b.table.device != device:
+        raise ValueError(f"the batch is on {b.table.device}, the call runs on {device}")
+    return kept[1]
+
+
+def _rope_struct(r: RopeTable, interleaved: bool, device) -> RopeC:
+    _on_gpu("cos", r.cos, device)
+    _on_gpu("sin", r.sin, device)
+    if r.cos.dim() != 2 or r.sin.shape != r.cos.shape or not (
+            r.cos.dtype == r.sin.dtype == torch.float32):
+        raise ValueError("cos and sin must be fp32 [positions, rot_dim / 2] tensors")
+    return RopeC(r.cos.data_ptr(), r.sin.data_ptr(), r.cos.shape[0], 2 * r.cos.shape[1],
+                 1 if interleaved else 0)
+
+
+def _gamma(name: str, t: torch.Tensor | None, D: int, device):
+    if t is None:
+        return None
+    _on_gpu(name, t, device)
+    if t.dtype != torch.float32 or t.shape != (D,):
+        raise ValueError(f"{name} must be an fp32 [{D}] tensor")
+    return t.data_ptr()
+
+
+def mnb_rope_frequencies(rot_dim: int, base: float = 1e6, *, factor: float = 1.0,
+                         original: float = 0.0, low: float = 1.0,
+                         high: float = 32.0) -> torch.Tensor:
+    """Angles per position of rot_dim / 2 pairs (float64, on the CPU): plain
+    (factor 1), interpolated by factor, or by parts of the spectrum when the
+    original length is given (include/mnb.h)."""
+    out = torch.empty(max(rot_dim // 2, 0), dtype=torch.float64)
+    _check(load().mnb_rope_frequencies(rot_dim, base, factor, original, low, high,
+                                       out.data_ptr()), "mnb_rope_frequencies")
+    return out
+
+
+def mnb_rope_table(frequencies: torch.Tensor, n: int, *, first: int = 0, magnitude: float = 1.0,
+                   device=None, stream=None) -> RopeTable:
+    """Cosines and sines of the positions first .. first + n - 1, times
+    magnitude, for the frequencies (float64, on the CPU)."""
+    if frequencies.is_cuda or frequencies.dtype != torch.float64 or frequencies.dim() != 1 or (
+            not frequencies.is_contiguous()):
+        raise ValueError("frequencies must be a contiguous float64 vector on the CPU")
+    if device is None:
+        dev = torch.device("cuda", torch.cuda.current_device() if stream is None
+                           else stream.device.index)
+    else:
+        dev = torch.device(device)
+        if dev.index is None:
+            dev = torch.device(dev.type, torch.cuda.current_device())
+    pairs = frequencies.shape[0]
+
+    def call(s):
+        cos, sin = (torch.empty(n, pairs, dtype=torch.float32, device=dev) for _ in range(2))
+        _check(load().mnb_rope_table(frequencies.data_ptr(), 2 * pairs, first, n, magnitude,
+                                     cos.data_ptr(), sin.data_ptr(), s), "mnb_rope_table")
+        return RopeTable(cos, sin)
+    return _call_on(dev, stream, call)
+
+
+def mnb_qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, rope: RopeTable | None,
+                     positions: torch.Tensor | None, *, gamma_q: torch.Tensor | None = None,
+                     gamma_k: torch.Tensor | None = None, eps: float = 1e-6,
+                     interleaved: bool = False, out_q: torch.Tensor | None = None,
+                     out_k: torch.Tensor | None = None, stream=None):
+    """Norms of q [T, heads, head_dim] and k for each head (with a gamma, fp32
+    [head_dim]) and their rotation by positions (int32 [T]), in one pass:
+    (q, k) of the same shapes. out_q and out_k may be q and k. k may be None
+    (and comes back as None); a position outside the table gives zeros."""
+    dev, D = q.device, q.shape[-1]
+    qs = _heads_struct("q", q, dev)
+    ks = None if k is None else _heads_struct("k", k, dev, q)
+    rs = None if rope is None else _rope_struct(rope, interleaved, dev)
+    if positions is not None:
+        _on_gpu("positions", positions, dev)
+        if positions.dtype != torch.int32 or positions.shape != (q.shape[0],):
+            raise ValueError("positions must be an int32 [T] tensor")
+    if k is None and out_k is not None:
+        raise ValueError("out_k without k")
+    gq, gk = _gamma("gamma_q", gamma_q, D, dev), _gamma("gamma_k", gamma_k, D, dev)
+    lib, code = _lib or load(), _dtype_code(q.dtype)
+    given = [_heads_struct(n, t, dev, q) if t is not None else None
+             for n, t in (("out_q", out_q), ("out_k", out_k))]
+
+    def call(s):
+        yq = torch.empty(q.shape, dtype=q.dtype, device=dev) if out_q is None else out_q
+        yk = k
+        if k is not None:
+            yk = torch.empty(k.shape, dtype=k.dtype, device=dev) if out_k is None else out_k
+        oq = given[0] or _heads_struct("out_q", yq, dev)
+        ok = None if k is None else given[1] or _heads_struct("out_k", yk, dev)
+        _check(lib.mnb_qk_norm_rope(qs, ks, q.shape[0], D, code, gq, gk, eps, rs,
+                                    None if positions is None else positions.data_ptr(), oq, ok,
+                                    s), "mnb_qk_norm_rope")
+        return yq, yk
+    return _call_on(dev, stream, call)
+
+
+def mnb_cache_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, cache: KvCache,
+                     batch: KvBatch, rope: RopeTable | None = None, *,
+                     gamma_q: torch.Tensor | None = None, gamma_k: torch.Tensor | None = None,
+                     eps: float = 1e-6, interleaved: bool = False,
+                     out: torch.Tensor | None = None, stream=None) -> torch.Tensor | None:
+    """q and k normed and rotated as by mnb_qk_norm_rope, at the positions of
+    the batch's new tokens; k and v [T, heads, head_dim] go into the cache, q
+    [T, q heads, head_dim] is returned (in out, which may be q). Rows of no
+    sequence are left as they were."""
+    dev, D = k.device, k.shape[-1]
+    if k.dtype != cache.k.dtype or D != cache.k.shape[3] or (
+            k.dim() == 3 and k.shape[1] != cache.k.shape[1]):
+        raise ValueError("k must have the heads, head size and dtype of the cache")
+    ks = _heads_struct("k", k, dev)
+    vs = _heads_struct("v", v, dev, k)
+    qs = None if q is None else _heads_struct("q", q, dev, k)
+    if q is None and out is not None:
+        raise ValueError("out without q")
+    os_ = None if out is None else _heads_struct("out", out, dev, k)
+    rs = None if rope is None else _rope_struct(rope, interleaved, dev)
+    cs, bs = _cache_struct(cache, dev), _batch_struct(batch, dev)
+    gq, gk = _gamma("gamma_q", gamma_q, D, dev), _gamma("gamma_k", gamma_k, D, dev)
+    lib = _lib or load()
+
+    def call(s):
+        y, ys = out, os_
+        if q is not None and out is None:
+            y = torch.empty(q.shape, dtype=q.dtype, device=dev)
+            ys = _heads_struct("out", y, dev)
+        _check(lib.mnb_cache_append(qs, ks, vs, k.shape[0], gq, gk, eps, rs, cs, bs, ys, s),
+               "mnb_cache_append")
+        return y
+    return _call_on(dev, stream, call)
+
+
+def mnb_paged_attention(q: torch.Tensor, cache: KvCache, batch: KvBatch, *,
+                        scale: float | None = None, window: int = 0,
+                        out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Attention of each sequence's new tokens, q [T, q heads, head_dim], over
+    its pages of the cache up to their own positions (and over the last
+    `window` keys alone, when given): [T, q heads, head_dim]. scale is 1 /
+    sqrt(head_dim) unless given. Rows of no sequence are left as they were."""
+    dev = q.device
+    qs = _heads_struct("q", q, dev)
+    if q.dtype != cache.k.dtype or q.shape[2] != cache.k.shape[3]:
+        raise ValueError("q must have the head size and dtype of the cache")
+    os_ = None
+    if out is not None:
+        os_ = _heads_struct("out", out, dev, q)
+    cs, bs = _cache_struct(cache, dev), _batch_struct(batch, dev)
+    lib, T, hq = _lib or load(), q.shape[0], q.shape[1]
+    if scale is None:
+        scale = q.shape[2] ** -0.5
+
+    def call(s):
+        y, ys = out, os_
+        if out is None:
+            y = torch.empty(q.shape, dtype=q.dtype, device=dev)
+            ys = _heads_struct("out", y, dev)
+        n = lib.mnb_paged_attention_workspace_size(T, hq, cs, bs)
+        ws, wp = _workspace(n, dev)
+        _check(lib.mnb_paged_attention(qs, T, cs, bs, scale, window, ys, wp, n, s),
+               "mnb_paged_attention")
+        return y
     return _call_on(dev, stream, call)

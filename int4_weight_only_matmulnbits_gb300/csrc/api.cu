@@ -4,6 +4,7 @@
 // computation.
 #include <atomic>
 #include <algorithm>
+#include <cmath>
 #include <cstdio>
 #include <cstring>
 #include <mutex>
@@ -11,6 +12,7 @@
 #include <vector>
 
 #include "../../include/mnb.h"
+#include "attn.h"
 #include "mnb_common.cuh"
 #include "mnb_launch.h"
 #include "moe.h"
@@ -518,6 +520,185 @@ OpRanges op_ranges(const mnb_chain_op &o, int64_t M, int bs, int a_dtype, int sc
     r.nw[i] = w[i] ? nw[i] : 0;
   }
   return r;
+}
+
+// ---- attention block: checks ----------------------------------------------------
+
+// T rows of heads: pointer, strides, count and, for an output, that no two of
+// its rows overlap.
+mnb_status check_heads(const mnb_heads &h, int64_t T, int64_t D, size_t es, bool output) {
+  if (!h.data) return MNB_ERR_NULL;
+  if (h.heads < 1 || h.reserved != 0 || h.token_stride < 0 || h.head_stride < 0 ||
+      h.token_stride > (int64_t(1) << 40) || h.head_stride > (int64_t(1) << 40))
+    return MNB_ERR_SHAPE;
+  if (!aligned(h.data, es)) return MNB_ERR_ALIGN;
+  if (output) {
+    const bool one_t = T == 1, one_h = h.heads == 1;
+    if ((!one_t && h.token_stride < D) || (!one_h && h.head_stride < D)) return MNB_ERR_ALIAS;
+    if (!one_t && !one_h && h.token_stride < (h.heads - 1) * h.head_stride + D &&
+        h.head_stride < (T - 1) * h.token_stride + D)
+      return MNB_ERR_ALIAS;
+  }
+  return MNB_OK;
+}
+
+// From the first element of T rows of heads to past the last.
+Range heads_range(const mnb_heads &h, int64_t T, int64_t D, size_t es) {
+  return {h.data,
+          size_t((T - 1) * h.token_stride + (h.heads - 1) * h.head_stride + D) * es};
+}
+
+// Whether two sets of rows share bytes. Rows of equal token stride, each
+// token's heads within it (slices of one matrix's rows), are compared within
+// the stride; others by their ends.
+bool heads_overlap(const mnb_heads &a, const mnb_heads &b, int64_t T, int64_t D, size_t es) {
+  const Range ra = heads_range(a, T, D, es), rb = heads_range(b, T, D, es);
+  if (!overlap(ra.p, ra.n, rb.p, rb.n)) return false;
+  const int64_t s = a.token_stride * static_cast<int64_t>(es);
+  const int64_t wa = ((a.heads - 1) * a.head_stride + D) * static_cast<int64_t>(es);
+  const int64_t wb = ((b.heads - 1) * b.head_stride + D) * static_cast<int64_t>(es);
+  if (a.token_stride != b.token_stride || s <= 0 || wa > s || wb > s) return true;
+  int64_t d = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b.data)) -
+              static_cast<int64_t>(reinterpret_cast<uintptr_t>(a.data));
+  d = ((d % s) + s) % s;
+  return d < wa || d + wb > s;
+}
+
+bool same_heads(const mnb_heads &a, const mnb_heads &b, int64_t T) {
+  return a.data == b.data && a.heads == b.heads &&
+         (T == 1 || a.token_stride == b.token_stride) &&
+         (a.heads == 1 || a.head_stride == b.head_stride);
+}
+
+mnb_status check_rows(int64_t T) { return T < 1 || T > kMaxDim ? MNB_ERR_SHAPE : MNB_OK; }
+
+mnb_status check_norm(int64_t D, const float *gq, const float *gk, float eps) {
+  if (D < 2 || D % 2) return MNB_ERR_SHAPE;
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return MNB_ERR_SHAPE;
+  if (!aligned(gq, 4) || !aligned(gk, 4)) return MNB_ERR_ALIGN;
+  if (D > kMaxHeadDim) {
+    std::snprintf(g_last_error, sizeof g_last_error, "head_dim %lld (at most %d)",
+                  (long long)D, kMaxHeadDim);
+    return MNB_ERR_UNSUPPORTED;
+  }
+  return MNB_OK;
+}
+
+mnb_status check_rope(const mnb_rope *r, int64_t D) {
+  if (!r) return MNB_OK;
+  if (!r->cos || !r->sin) return MNB_ERR_NULL;
+  if (r->rot_dim < 2 || r->rot_dim % 2 || r->rot_dim > D || r->positions < 1 ||
+      r->positions > kMaxDim || (r->interleaved != 0 && r->interleaved != 1))
+    return MNB_ERR_SHAPE;
+  if (!aligned(r->cos, 4) || !aligned(r->sin, 4)) return MNB_ERR_ALIGN;
+  return MNB_OK;
+}
+
+mnb_status check_cache(const mnb_kv_cache &c) {
+  if (!c.k || !c.v) return MNB_ERR_NULL;
+  if (!valid_dtype(c.dtype)) return MNB_ERR_DTYPE;
+  if (c.pages < 1 || c.pages > kMaxDim || c.heads < 1 || c.head_dim < 1 || c.page_size < 16 ||
+      c.page_size % 16)
+    return MNB_ERR_SHAPE;
+  for (int64_t s : {c.k_page_stride, c.k_head_stride, c.k_token_stride, c.v_page_stride,
+                    c.v_head_stride, c.v_token_stride})
+    if (s < c.head_dim || s > (int64_t(1) << 40)) return MNB_ERR_SHAPE;
+  const size_t es = dtype_size(c.dtype);
+  if (!aligned(c.k, es) || !aligned(c.v, es)) return MNB_ERR_ALIGN;
+  if (c.k == c.v) return MNB_ERR_ALIAS;
+  return MNB_OK;
+}
+
+mnb_status check_batch(const mnb_kv_batch &b, const mnb_kv_cache &c) {
+  if (!b.starts || !b.lengths || !b.table) return MNB_ERR_NULL;
+  if (b.n < 1 || b.n > kMaxDim - 1 || b.table_pages < 1 ||
+      b.table_pages > kMaxDim / c.page_size || b.table_stride < b.table_pages ||
+      b.table_stride > (int64_t(1) << 40))
+    return MNB_ERR_SHAPE;
+  if (!aligned(b.starts, 4) || !aligned(b.lengths, 4) || !aligned(b.table, 4))
+    return MNB_ERR_ALIGN;
+  return MNB_OK;
+}
+
+Range pages_range(const mnb_kv_cache &c, bool values) {
+  const int64_t ps = values ? c.v_page_stride : c.k_page_stride;
+  const int64_t hs = values ? c.v_head_stride : c.k_head_stride;
+  const int64_t ts = values ? c.v_token_stride : c.k_token_stride;
+  return {values ? c.v : c.k,
+          size_t((c.pages - 1) * ps + (c.heads - 1) * hs + (c.page_size - 1) * ts + c.head_dim) *
+              dtype_size(c.dtype)};
+}
+
+struct BatchRanges {
+  Range r[3];
+  explicit BatchRanges(const mnb_kv_batch &b) {
+    r[0] = {b.starts, size_t(b.n + 1) * 4};
+    r[1] = {b.lengths, size_t(b.n) * 4};
+    r[2] = {b.table, size_t((b.n - 1) * b.table_stride + b.table_pages) * 4};
+  }
+};
+
+Heads heads_view(const mnb_heads *h) {
+  return h ? Heads{h->data, h->token_stride, h->head_stride, h->heads} : Heads{nullptr, 0, 0, 0};
+}
+CacheView cache_view(const mnb_kv_cache &c) {
+  return CacheView{{c.k, c.k_page_stride, c.k_head_stride, c.k_token_stride},
+                   {c.v, c.v_page_stride, c.v_head_stride, c.v_token_stride},
+                   c.pages,
+                   c.page_size,
+                   c.heads,
+                   c.head_dim};
+}
+BatchView batch_view(const mnb_kv_batch &b) {
+  return BatchView{b.starts, b.lengths, b.table, b.table_stride, static_cast<int>(b.n),
+                   static_cast<int>(b.table_pages)};
+}
+
+void set_rope(RopeArgs &a, const float *gq, const float *gk, float eps, const mnb_rope *rope) {
+  a.gq = gq;
+  a.gk = gk;
+  a.eps = eps;
+  if (rope) {
+    a.cos = rope->cos;
+    a.sin = rope->sin;
+    a.positions = rope->positions;
+    a.rot = rope->rot_dim;
+    a.interleaved = rope->interleaved;
+  }
+  a.pdl = g_pdl.load() != 0;
+}
+
+// An output of norms and rotation against its own input (in place, or apart)
+// and the call's other rows.
+mnb_status check_out_rows(const mnb_heads &out, const mnb_heads &own, const mnb_heads *const *ins,
+                          int n_ins, int64_t T, int64_t D, size_t es) {
+  for (int i = 0; i < n_ins; ++i) {
+    if (!ins[i]) continue;
+    if (ins[i] == &own && same_heads(out, own, T)) continue;
+    if (heads_overlap(out, *ins[i], T, D, es)) return MNB_ERR_ALIAS;
+  }
+  return MNB_OK;
+}
+
+mnb_status check_attention(const mnb_kv_cache &c, int q_heads) {
+  if (q_heads < 1 || q_heads % c.heads) return MNB_ERR_SHAPE;
+  if (c.head_dim != 64 && c.head_dim != 128) {
+    std::snprintf(g_last_error, sizeof g_last_error,
+                  "attention takes head_dim 64 or 128, not %d", c.head_dim);
+    return MNB_ERR_UNSUPPORTED;
+  }
+  return MNB_OK;
+}
+
+AttnArgs attn_args(int64_t T, int q_heads, const mnb_kv_cache &c, const mnb_kv_batch &b) {
+  AttnArgs a{};
+  a.f32 = c.dtype == MNB_F32;
+  a.pdl = g_pdl.load() != 0;
+  a.T = T;
+  a.q.n = q_heads;
+  a.c = cache_view(c);
+  a.b = batch_view(b);
+  return a;
 }
 
 }  // namespace
@@ -1575,6 +1756,217 @@ mnb_status mnb_moe(const void *X, const void *logits, mnb_dtype logits_dtype, in
   const cudaError_t e = launch_moe(a, reinterpret_cast<cudaStream_t>(stream));
   if (e == cudaErrorNotSupported) return experts_unsupported(M, top_k, *gate);
   if (e != cudaSuccess) return cuda_fail(e, "mnb_moe");
+  return MNB_OK;
+}
+
+// ---- attention block -----------------------------------------------------------
+
+static_assert(sizeof(mnb_heads) == 32 && sizeof(mnb_rope) == 32 && sizeof(mnb_kv_cache) == 88 &&
+                  sizeof(mnb_kv_batch) == 48,
+              "layout of the attention block's structs");
+
+mnb_status mnb_rope_frequencies(int rot_dim, double base, double factor, double original,
+                                double low, double high, double *out) {
+  if (!out) return MNB_ERR_NULL;
+  if (rot_dim < 2 || rot_dim % 2 || rot_dim > kMaxHeadDim) return MNB_ERR_SHAPE;
+  for (double v : {base, factor})
+    if (!(v > 0) || !std::isfinite(v)) return MNB_ERR_SHAPE;
+  if (!(original >= 0) || !std::isfinite(original)) return MNB_ERR_SHAPE;
+  if (original > 0 && (!(low >= 0) || !(high > low) || !std::isfinite(high)))
+    return MNB_ERR_SHAPE;
+  for (int i = 0; i < rot_dim / 2; ++i) {
+    const double f = std::pow(base, -2.0 * i / rot_dim);
+    double keep = 0.0;
+    if (original > 0)
+      keep = std::min(1.0, std::max(0.0, (original * f / (2.0 * M_PI) - low) / (high - low)));
+    out[i] = (1.0 - keep) * f / factor + keep * f;
+  }
+  return MNB_OK;
+}
+
+mnb_status mnb_rope_table(const double *frequencies, int rot_dim, int64_t first, int64_t n,
+                          double magnitude, float *cos, float *sin, mnb_stream_t stream) {
+  if (!frequencies || !cos || !sin) return MNB_ERR_NULL;
+  if (rot_dim < 2 || rot_dim % 2 || rot_dim > kMaxHeadDim || n < 1 || first < 0 ||
+      n > kMaxDim || first > kMaxDim - n || !std::isfinite(magnitude) ||
+      !std::isfinite(static_cast<float>(magnitude)))
+    return MNB_ERR_SHAPE;
+  for (int i = 0; i < rot_dim / 2; ++i)
+    if (!std::isfinite(frequencies[i])) return MNB_ERR_SHAPE;
+  if (!aligned(cos, 4) || !aligned(sin, 4)) return MNB_ERR_ALIGN;
+  const size_t bytes = size_t(n) * (rot_dim / 2) * 4;
+  if (overlap(cos, bytes, sin, bytes)) return MNB_ERR_ALIAS;
+  const mnb_status st = check_device();
+  if (st != MNB_OK) return st;
+  const RopeTableArgs a{rot_dim / 2, first, n, magnitude, frequencies, cos, sin};
+  const cudaError_t e = launch_rope_table(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "mnb_rope_table");
+  return MNB_OK;
+}
+
+mnb_status mnb_qk_norm_rope(const mnb_heads *q, const mnb_heads *k, int64_t T, int head_dim,
+                            mnb_dtype dtype, const float *gamma_q, const float *gamma_k,
+                            float eps, const mnb_rope *rope, const int32_t *positions,
+                            const mnb_heads *q_out, const mnb_heads *k_out,
+                            mnb_stream_t stream) {
+  if (!q || !q_out || !k != !k_out || !rope != !positions) return MNB_ERR_NULL;
+  if (!valid_dtype(dtype)) return MNB_ERR_DTYPE;
+  const int64_t D = head_dim;
+  const size_t es = dtype_size(dtype);
+  mnb_status st = check_rows(T);
+  if (st == MNB_OK) st = check_norm(D, gamma_q, gamma_k, eps);
+  if (st == MNB_OK) st = check_rope(rope, D);
+  const mnb_heads *rows[] = {q, k, q_out, k_out};
+  for (int i = 0; i < 4; ++i)
+    if (st == MNB_OK && rows[i]) st = check_heads(*rows[i], T, D, es, i >= 2);
+  if (st != MNB_OK) return st;
+  if (q_out->heads != q->heads || (k && k_out->heads != k->heads)) return MNB_ERR_SHAPE;
+  if (!aligned(positions, 4)) return MNB_ERR_ALIGN;
+  const mnb_heads *q_ins[] = {q, k, k_out}, *k_ins[] = {k, q};
+  st = check_out_rows(*q_out, *q, q_ins, 3, T, D, es);
+  if (st == MNB_OK && k) st = check_out_rows(*k_out, *k, k_ins, 2, T, D, es);
+  if (st != MNB_OK) return st;
+  const size_t table = rope ? size_t(rope->positions) * (rope->rot_dim / 2) * 4 : 0;
+  const Range ins[] = {{gamma_q, size_t(D) * 4},        {gamma_k, size_t(D) * 4},
+                       {rope ? rope->cos : nullptr, table}, {rope ? rope->sin : nullptr, table},
+                       {positions, size_t(T) * 4}};
+  for (const mnb_heads *o : {q_out, k_out}) {
+    if (!o) continue;
+    const Range r = heads_range(*o, T, D, es);
+    for (const Range &i : ins)
+      if (overlap(r.p, r.n, i.p, i.n)) return MNB_ERR_ALIAS;
+  }
+  st = check_device();
+  if (st != MNB_OK) return st;
+  RopeArgs a{};
+  a.f32 = dtype == MNB_F32;
+  a.T = T;
+  a.D = head_dim;
+  a.q = heads_view(q);
+  a.k = heads_view(k);
+  a.qo = heads_view(q_out);
+  a.ko = heads_view(k_out);
+  a.pos = positions;
+  set_rope(a, gamma_q, gamma_k, eps, rope);
+  const cudaError_t e = launch_rope(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "mnb_qk_norm_rope");
+  return MNB_OK;
+}
+
+mnb_status mnb_cache_append(const mnb_heads *q, const mnb_heads *k, const mnb_heads *v,
+                            int64_t T, const float *gamma_q, const float *gamma_k, float eps,
+                            const mnb_rope *rope, const mnb_kv_cache *cache,
+                            const mnb_kv_batch *batch, const mnb_heads *q_out,
+                            mnb_stream_t stream) {
+  if (!k || !v || !cache || !batch || !q != !q_out) return MNB_ERR_NULL;
+  mnb_status st = check_rows(T);
+  if (st == MNB_OK) st = check_cache(*cache);
+  if (st == MNB_OK) st = check_batch(*batch, *cache);
+  if (st != MNB_OK) return st;
+  const int64_t D = cache->head_dim;
+  const size_t es = dtype_size(cache->dtype);
+  st = check_norm(D, gamma_q, gamma_k, eps);
+  if (st == MNB_OK) st = check_rope(rope, D);
+  const mnb_heads *rows[] = {q, k, v, q_out};
+  for (int i = 0; i < 4; ++i)
+    if (st == MNB_OK && rows[i]) st = check_heads(*rows[i], T, D, es, i == 3);
+  if (st != MNB_OK) return st;
+  if (k->heads != cache->heads || v->heads != cache->heads || (q && q_out->heads != q->heads))
+    return MNB_ERR_SHAPE;
+  if (q) {
+    const mnb_heads *q_ins[] = {q, k, v};
+    st = check_out_rows(*q_out, *q, q_ins, 3, T, D, es);
+    if (st != MNB_OK) return st;
+  }
+  const size_t table = rope ? size_t(rope->positions) * (rope->rot_dim / 2) * 4 : 0;
+  const BatchRanges br(*batch);
+  const Range none{nullptr, 0};
+  const Range small[] = {{gamma_q, size_t(D) * 4},
+                         {gamma_k, size_t(D) * 4},
+                         {rope ? rope->cos : nullptr, table},
+                         {rope ? rope->sin : nullptr, table},
+                         br.r[0],
+                         br.r[1],
+                         br.r[2]};
+  const Range wide[] = {q ? heads_range(*q, T, D, es) : none, heads_range(*k, T, D, es),
+                        heads_range(*v, T, D, es), q ? heads_range(*q_out, T, D, es) : none};
+  for (const Range &o : {pages_range(*cache, false), pages_range(*cache, true), wide[3]})
+    for (const Range &i : small)
+      if (overlap(o.p, o.n, i.p, i.n)) return MNB_ERR_ALIAS;
+  for (const Range &o : {pages_range(*cache, false), pages_range(*cache, true)})
+    for (const Range &i : wide)
+      if (overlap(o.p, o.n, i.p, i.n)) return MNB_ERR_ALIAS;
+  st = check_device();
+  if (st != MNB_OK) return st;
+  RopeArgs a{};
+  a.f32 = cache->dtype == MNB_F32;
+  a.append = true;
+  a.T = T;
+  a.D = cache->head_dim;
+  a.q = heads_view(q);
+  a.k = heads_view(k);
+  a.v = heads_view(v);
+  a.qo = heads_view(q_out);
+  a.c = cache_view(*cache);
+  a.b = batch_view(*batch);
+  set_rope(a, gamma_q, gamma_k, eps, rope);
+  const cudaError_t e = launch_rope(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "mnb_cache_append");
+  return MNB_OK;
+}
+
+size_t mnb_paged_attention_workspace_size(int64_t T, int q_heads, const mnb_kv_cache *cache,
+                                          const mnb_kv_batch *batch) {
+  if (!cache || !batch || check_rows(T) != MNB_OK || check_cache(*cache) != MNB_OK ||
+      check_batch(*batch, *cache) != MNB_OK || check_attention(*cache, q_heads) != MNB_OK)
+    return 0;
+  return attn_workspace_bytes(attn_args(T, q_heads, *cache, *batch));
+}
+
+mnb_status mnb_paged_attention(const mnb_heads *q, int64_t T, const mnb_kv_cache *cache,
+                               const mnb_kv_batch *batch, float scale, int64_t window,
+                               const mnb_heads *out, void *workspace, size_t workspace_bytes,
+                               mnb_stream_t stream) {
+  if (!q || !cache || !batch || !out) return MNB_ERR_NULL;
+  mnb_status st = check_rows(T);
+  if (st == MNB_OK) st = check_cache(*cache);
+  if (st == MNB_OK) st = check_batch(*batch, *cache);
+  if (st != MNB_OK) return st;
+  const int64_t D = cache->head_dim;
+  const size_t es = dtype_size(cache->dtype);
+  st = check_heads(*q, T, D, es, false);
+  if (st == MNB_OK) st = check_heads(*out, T, D, es, true);
+  if (st == MNB_OK && (!std::isfinite(scale) || window < 0 || out->heads != q->heads))
+    st = MNB_ERR_SHAPE;
+  if (st == MNB_OK) st = check_attention(*cache, q->heads);
+  if (st != MNB_OK) return st;
+  const int64_t lane = 16 / static_cast<int64_t>(es);
+  for (const mnb_heads *h : {q, out})
+    if (!aligned(h->data, 16) || (T > 1 && h->token_stride % lane) ||
+        (h->heads > 1 && h->head_stride % lane))
+      return MNB_ERR_ALIGN;
+  if (!aligned(cache->k, 16) || !aligned(cache->v, 16)) return MNB_ERR_ALIGN;
+  for (int64_t s : {cache->k_page_stride, cache->k_head_stride, cache->k_token_stride,
+                    cache->v_page_stride, cache->v_head_stride, cache->v_token_stride})
+    if (s % lane) return MNB_ERR_ALIGN;
+  AttnArgs a = attn_args(T, q->heads, *cache, *batch);
+  const size_t need = attn_workspace_bytes(a);
+  st = check_workspace(workspace, workspace_bytes, need);
+  if (st != MNB_OK) return st;
+  const BatchRanges br(*batch);
+  const Range outs[] = {heads_range(*out, T, D, es), {workspace, need}};
+  const Range ins[] = {heads_range(*q, T, D, es), pages_range(*cache, false),
+                       pages_range(*cache, true), br.r[0], br.r[1], br.r[2]};
+  st = check_disjoint(outs, 2, ins, 6);
+  if (st == MNB_OK) st = check_device();
+  if (st != MNB_OK) return st;
+  a.q = heads_view(q);
+  a.o = heads_view(out);
+  a.scale = scale;
+  a.window = window;
+  a.ws = static_cast<unsigned char *>(workspace);
+  const cudaError_t e = launch_attn(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "mnb_paged_attention");
   return MNB_OK;
 }
 

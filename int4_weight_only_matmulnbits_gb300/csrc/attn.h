@@ -1,0 +1,115 @@
+// Host-side launch interfaces of the attention block's kernels: rotary tables,
+// norms and rotation of queries and keys, appending to a paged cache and
+// attention over its pages. Arguments arrive here already validated by the C
+// ABI.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "mnb_common.cuh"
+
+namespace mnb {
+
+constexpr int kMaxHeadDim = 256;  // of norms, rotation and appending
+constexpr int kMaxPairs = kMaxHeadDim / 2;
+
+// Rows of heads: element (token, head, d) at token * ts + head * hs + d.
+struct Heads {
+  void *p;
+  int64_t ts, hs;
+  int n;
+};
+
+// Pages of a cache: element (page, head, token in page, d) at
+// page * ps + head * hs + token * ts + d.
+struct Pages {
+  void *p;
+  int64_t ps, hs, ts;
+};
+struct CacheView {
+  Pages k, v;
+  int64_t pages;
+  int page_size, heads, D;
+};
+struct BatchView {
+  const int32_t *starts, *lengths, *table;
+  int64_t table_stride;
+  int n, table_pages;
+};
+
+struct RopeTableArgs {
+  int pairs;
+  int64_t first, n;
+  double magnitude;
+  const double *frequencies;  // HOST
+  float *cos, *sin;
+};
+cudaError_t launch_rope_table(const RopeTableArgs &a, cudaStream_t stream);
+
+struct RopeArgs {
+  bool f32, append, pdl;
+  int64_t T;
+  int D;
+  Heads q, k, v;    // n = 0: none
+  Heads qo, ko;     // ko: not with append
+  const float *gq, *gk;
+  float eps;
+  const float *cos, *sin;  // null: no rotation
+  int64_t positions;
+  int rot, interleaved;
+  const int32_t *pos;  // not with append
+  CacheView c;
+  BatchView b;
+};
+cudaError_t launch_rope(const RopeArgs &a, cudaStream_t stream);
+
+struct AttnArgs {
+  bool f32, pdl;
+  int64_t T;
+  Heads q, o;
+  CacheView c;
+  BatchView b;
+  float scale;
+  int64_t window;  // 0: none
+  unsigned char *ws;
+};
+size_t attn_workspace_bytes(const AttnArgs &a);
+cudaError_t launch_attn(const AttnArgs &a, cudaStream_t stream);
+
+// One sequence of a batch as the attention kernels take it: rows t0 .. t0 + n
+// of the queries, whose row i stands at position len - n + i; keys from lo on
+// (a multiple of 16) are attended by some row.
+struct Seq {
+  int t0, n, len, lo;
+};
+// What the device arrays say, brought within the buffers whatever they hold.
+__device__ __forceinline__ Seq load_seq(const BatchView &b, int i, int T, int cap, int window) {
+  Seq s;
+  const int a = b.starts[i], z = b.starts[i + 1], len = b.lengths[i];
+  s.t0 = min(max(a, 0), T);
+  s.n = max(min(z, T) - s.t0, 0);
+  s.len = min(max(len, 0), cap);
+  s.lo = 0;
+  if (window > 0) s.lo = max(0, s.len - s.n + 1 - window) & ~15;
+  return s;
+}
+
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int block, size_t smem, bool pdl,
+                         cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
+}  // namespace mnb

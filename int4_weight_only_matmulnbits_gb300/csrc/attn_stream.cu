@@ -1,0 +1,744 @@
+// Attention of new tokens over the pages of a cache: the kernel that streams
+// keys and values past 16 query rows at a time (decoding, a few tokens per
+// sequence, fp32).
+//
+//   o_i = sum_j w_ij v_j / sum_j w_ij,  w_ij = exp(scale q_i . k_j),
+// over the keys j <= p_i (and j > p_i - window) of row i's position p_i, with
+// the running maximum and sum of a softmax: one pass over the keys.
+//
+// Rows of a sequence are (token, head of the key head's group), numbered token
+// first; 16 of them, padded, are the rows of the MMAs, so that a key head's
+// keys are read once for its whole group. The keys are cut into blocks of 64,
+// and all blocks of all (sequence, key head, 16 rows) are shared out evenly in
+// one long line: block c of the grid takes the part c of it, wherever that
+// begins and ends. So the split follows the lengths that the device arrays
+// hold at that moment (a captured graph's too), whatever they are. Pieces of a
+// unit that several blocks share are joined by combine_kernel.
+//
+// A block's warps take 16 of a block's 64 keys each, with a ring of
+// asynchronous copies of their own, so that no barrier stands in the loop; the
+// warps' sums are joined at the end of a piece.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <atomic>
+#include <type_traits>
+
+#include "attn.h"
+#include "attn_stream.h"
+#include "mnb_common.cuh"
+#include "mnb_launch.h"
+
+namespace mnb {
+namespace {
+
+constexpr int kWarps = 4, kThreads = kWarps * 32;
+constexpr int kRows = 16;         // query rows of a unit
+constexpr int kWarpKeys = 16;     // keys of a warp's step
+constexpr int kBlockKeys = kWarps * kWarpKeys;
+constexpr int kMinBlocks = 2;     // of the line per block of the grid
+constexpr int kHeader = 8;        // ints of a piece's header
+
+template <int D, bool F32>
+struct Cfg {
+  static constexpr int es = F32 ? 4 : 2;
+  static constexpr int row = D * es;            // bytes of a key
+  static constexpr int step = 2 * kWarpKeys * row;  // keys and values of a warp's step
+  // 96 KB of copies for two blocks on an SM each, 192 KB where a step of 16
+  // keys is too large for that.
+  static constexpr int per_sm = row <= 256 ? 2 : 1;
+  static constexpr int stages = (per_sm == 2 ? 98304 : 196608) / (kWarps * step);
+  static constexpr int ring = kWarps * stages * step;
+  static constexpr int cols = 32;               // columns joined at a time
+  static constexpr int ld = cols + 4;
+  static constexpr int smem = ring + kWarps * kRows * (ld + 2) * 4;
+  static_assert(stages >= 3, "copies in flight");
+};
+
+__device__ __forceinline__ void cp16_or_zero(uint32_t dst, const void *src, bool there) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(there ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ float4 lds4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 "
+      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// x as two tf32 numbers (11 bits each, rounded to nearest): the sum is within
+// 2^-22 of x, and the three products hi hi + hi lo + lo hi within 2^-21 of the
+// product. Infinities and NaN stay in hi (their lo is NaN, which no finite
+// product can have taken in).
+__device__ __forceinline__ void split_tf32(float x, uint32_t &hi, uint32_t &lo) {
+  hi = (__float_as_uint(x) + 0x1000u) & 0xFFFFE000u;
+  lo = __float_as_uint(x - __uint_as_float(hi)) + 0x1000u;
+}
+
+// Bytes 16-byte piece `c` of key `k` lies at in a step's keys or values: pieces
+// are swapped so that no two lanes that read together share a bank. bf16:
+// ldmatrix reads a piece of eight keys. fp32: the lanes g < 2, t read the
+// pieces .. + t of keys g (keys) or the pieces .. + g of keys 2t (values).
+template <int D, bool F32>
+__device__ __forceinline__ int key_at(int k, int c) {
+  return k * Cfg<D, F32>::row + ((F32 ? c ^ ((k & 1) << 2) : c ^ (k & 7)) << 4);
+}
+template <int D, bool F32>
+__device__ __forceinline__ int value_at(int k, int c) {
+  return k * Cfg<D, F32>::row + ((F32 ? c ^ (((k >> 1) & 3) << 1) : c ^ (k & 7)) << 4);
+}
+
+// A unit's place in the line of blocks and what it attends.
+struct Unit {
+  int b, head, tile;      // sequence, key head, 16-row tile
+  int t0, n, len, lo;     // the sequence
+  int blocks;             // of 64 keys from lo on
+  int last;               // position of the tile's last row: no key above it
+};
+
+struct Line {
+  const AttnStreamParams &p;
+  int lane;
+  __device__ __forceinline__ Seq seq(int i) const {
+    return load_seq(p.b, i, p.T, p.cap, p.window);
+  }
+  __device__ __forceinline__ int tiles(const Seq &s) const {
+    return static_cast<int>((int64_t(s.n) * p.G + kRows - 1) / kRows);
+  }
+  static __device__ __forceinline__ int blocks(const Seq &s) {
+    return max(1, (s.len - s.lo + kBlockKeys - 1) / kBlockKeys);
+  }
+  __device__ __forceinline__ int64_t work(int i) const {
+    if (i >= p.b.n) return 0;
+    const Seq s = seq(i);
+    return int64_t(tiles(s)) * p.kv_heads * blocks(s);
+  }
+  // All blocks of the line (every lane takes part; w0: the first 32
+  // sequences').
+  __device__ __forceinline__ int64_t total(int64_t &w0) const {
+    int64_t w = w0 = work(lane);
+    for (int i = lane + 32; i < p.b.n; i += 32) w += work(i);
+#pragma unroll
+    for (int m = 1; m < 32; m *= 2) w += __shfl_xor_sync(0xffffffffu, w, m);
+    return w;
+  }
+  // The sequence that holds block x, and the block's number in it.
+  __device__ __forceinline__ int find(int64_t x, int64_t w0, int64_t &in) const {
+    int64_t before = 0;
+    for (int i0 = 0; i0 < p.b.n; i0 += 32) {
+      const int64_t w = i0 == 0 ? w0 : work(i0 + lane);
+      int64_t up = w;
+#pragma unroll
+      for (int m = 1; m < 32; m *= 2) {
+        const int64_t o = __shfl_up_sync(0xffffffffu, up, m);
+        if (lane >= m) up += o;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, before + up > x);
+      if (past) {
+        const int l = __ffs(past) - 1;
+        in = x - before - __shfl_sync(0xffffffffu, up - w, l);
+        return i0 + l;
+      }
+      before += __shfl_sync(0xffffffffu, up, 31);
+    }
+    in = 0;
+    return p.b.n;
+  }
+  __device__ __forceinline__ void enter(Unit &u, const Seq &s, int unit) const {
+    const int nt = tiles(s);
+    u.head = unit / nt;
+    u.tile = unit - u.head * nt;
+    u.t0 = s.t0;
+    u.n = s.n;
+    u.len = s.len;
+    u.lo = s.lo;
+    u.blocks = blocks(s);
+    u.last = s.len - s.n + min(s.n - 1, (u.tile * kRows + kRows - 1) / p.G);
+  }
+  __device__ __forceinline__ void start(Unit &u, int &kb, int64_t x, int64_t w0) const {
+    int64_t in;
+    u.b = find(x, w0, in);
+    const Seq s = seq(u.b);
+    const int nb = blocks(s);
+    const int unit = static_cast<int>(in / nb);
+    kb = static_cast<int>(in - int64_t(unit) * nb);
+    enter(u, s, unit);
+  }
+  // The unit after u (there is one).
+  __device__ __forceinline__ void next(Unit &u) const {
+    Seq s{u.t0, u.n, u.len, u.lo};
+    int unit = u.head * tiles(s) + u.tile + 1;
+    while (unit >= tiles(s) * p.kv_heads) {
+      unit = 0;
+      s = seq(++u.b);
+    }
+    enter(u, s, unit);
+  }
+};
+
+template <int D, bool F32>
+__global__ void __launch_bounds__(kThreads, Cfg<D, F32>::per_sm)
+    stream_kernel(const __grid_constant__ AttnStreamParams p) {
+  using C = Cfg<D, F32>;
+  using E = typename std::conditional<F32, float, uint16_t>::type;
+  constexpr int kPieces = C::row / 16;            // 16-byte pieces of a key
+  constexpr int kKeysAtOnce = 32 / kPieces > 0 ? 32 / kPieces : 1;
+  constexpr int kSteps = kWarpKeys / kKeysAtOnce;  // copies per lane, keys or values
+  constexpr int kQ = F32 ? D / 2 : D / 4;          // query registers
+  constexpr int kO = D / 8;                        // 8-wide column tiles
+  extern __shared__ __align__(128) unsigned char smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  unsigned char *ring = smem + warp * (C::stages * C::step);
+  const uint32_t ring_u = smem_addr(ring);
+  float *join = reinterpret_cast<float *>(smem + C::ring);  // [warp][row][ld]
+  float *join_m = join + kWarps * kRows * C::ld, *join_l = join_m + kWarps * kRows;
+
+  grid_dependency_wait();
+  grid_dependents_launch();
+
+  const Line line{p, lane};
+  int64_t w0;
+  const int64_t total = line.total(w0);
+  // As many blocks of the grid as have kMinBlocks of the line.
+  const int64_t parts = min(int64_t(gridDim.x), (total + kMinBlocks - 1) / kMinBlocks);
+  int *header = p.headers + blockIdx.x * kHeader;
+  if (int64_t(blockIdx.x) >= parts) {
+    if (threadIdx.x == 0) header[0] = 0;
+    return;
+  }
+  const int64_t x0 = blockIdx.x * total / parts, x1 = (blockIdx.x + 1) * total / parts;
+
+  // ---- copies ---------------------------------------------------------------------
+  Unit fu;
+  int fk, slot = 0;
+  int64_t fx = x0;
+  line.start(fu, fk, x0, w0);
+  Unit u = fu;
+  int kb = fk;
+  // Lane l holds the page of this warp's keys in block page0 + l of the unit.
+  int page0 = 0, pages = -1;
+  auto load_pages = [&](int k0) {
+    page0 = k0;
+    const int j = fu.lo + (k0 + lane) * kBlockKeys + warp * kWarpKeys;
+    const int first = fu.len - fu.n + fu.tile * kRows / p.G;  // the first row's position
+    pages = -1;
+    if (k0 + lane < fu.blocks && j < fu.len && j <= fu.last &&
+        (p.window == 0 || j + kWarpKeys > first - p.window + 1)) {
+      pages = p.b.table[fu.b * p.b.table_stride + j / p.page_size];
+      if (pages < 0 || pages >= p.pages) pages = -1;
+    }
+  };
+  load_pages(fk);
+  // Bit s: stage s holds keys that can be attended.
+  uint32_t held = 0;
+  auto fetch = [&] {
+    if (fx < x1) {
+      if (fk - page0 >= 32) load_pages(fk);
+      const int page = __shfl_sync(0xffffffffu, pages, fk - page0);
+      held &= ~(1u << slot);
+      if (page >= 0) {
+        held |= 1u << slot;
+        const int j = fu.lo + fk * kBlockKeys + warp * kWarpKeys;
+        const int at = j % p.page_size, left = fu.len - j;
+        const int piece = lane % kPieces, first = lane / kPieces;
+        const E *k = static_cast<const E *>(p.k.p) + page * p.k.ps + fu.head * p.k.hs +
+                     (at + first) * p.k.ts + piece * (16 / C::es);
+        const E *v = static_cast<const E *>(p.v.p) + page * p.v.ps + fu.head * p.v.hs +
+                     (at + first) * p.v.ts + piece * (16 / C::es);
+        const uint32_t dst = ring_u + slot * C::step;
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+          const int key = first + i * kKeysAtOnce;
+          cp16_or_zero(dst + key_at<D, F32>(key, piece), k, key < left);
+          k += kKeysAtOnce * p.k.ts;
+        }
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+          const int key = first + i * kKeysAtOnce;
+          cp16_or_zero(dst + C::step / 2 + value_at<D, F32>(key, piece), v, key < left);
+          v += kKeysAtOnce * p.v.ts;
+        }
+      }
+      slot = slot == C::stages - 1 ? 0 : slot + 1;
+      ++fx;
+      if (++fk == fu.blocks && fx < x1) {
+        line.next(fu);
+        fk = 0;
+        load_pages(0);
+      }
+    }
+    cp_commit();
+  };
+  for (int i = 0; i < C::stages - 1; ++i) fetch();
+
+  // ---- the unit's rows ---------------------------------------------------------------
+  uint32_t q[kQ];
+  int pos0 = 0, pos1 = 0;  // positions of the rows g and g + 8 (-1: no row)
+  auto load_rows = [&] {
+    auto row_of = [&](int r, int &pos) -> const E * {
+      const int i = u.tile * kRows + r, tok = i / p.G;
+      if (tok >= u.n) {
+        pos = -1;
+        return nullptr;
+      }
+      pos = max(-1, u.len - u.n + tok);
+      return static_cast<const E *>(p.q.p) + int64_t(u.t0 + tok) * p.q.ts +
+             int64_t(u.head * p.G + i - tok * p.G) * p.q.hs;
+    };
+    const E *a = row_of(g, pos0), *b = row_of(g + 8, pos1);
+    if constexpr (F32) {
+#pragma unroll
+      for (int s = 0; s < D / 16; ++s) {
+        const uint4 z = make_uint4(0, 0, 0, 0);
+        const uint4 x = a ? *reinterpret_cast<const uint4 *>(a + 16 * s + 4 * t) : z;
+        const uint4 y = b ? *reinterpret_cast<const uint4 *>(b + 16 * s + 4 * t) : z;
+        q[8 * s] = x.x; q[8 * s + 1] = x.y; q[8 * s + 2] = x.z; q[8 * s + 3] = x.w;
+        q[8 * s + 4] = y.x; q[8 * s + 5] = y.y; q[8 * s + 6] = y.z; q[8 * s + 7] = y.w;
+      }
+    } else {
+#pragma unroll
+      for (int s = 0; s < D / 16; ++s) {
+        const int c = 16 * s + 2 * t;
+        q[4 * s] = a ? *reinterpret_cast<const uint32_t *>(a + c) : 0u;
+        q[4 * s + 1] = b ? *reinterpret_cast<const uint32_t *>(b + c) : 0u;
+        q[4 * s + 2] = a ? *reinterpret_cast<const uint32_t *>(a + c + 8) : 0u;
+        q[4 * s + 3] = b ? *reinterpret_cast<const uint32_t *>(b + c + 8) : 0u;
+      }
+    }
+  };
+
+  float o[kO][4], m0, m1, l0, l1;
+  auto clear = [&] {
+#pragma unroll
+    for (int i = 0; i < kO; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    m0 = m1 = -INFINITY;
+    l0 = l1 = 0.f;
+  };
+  load_rows();
+  clear();
+  int piece0 = kb, cslot = 0;
+
+  for (int64_t x = x0; x < x1; ++x) {
+    cp_wait<C::stages - 2>();
+    __syncwarp();
+    const bool there = (held >> cslot) & 1;
+    fetch();
+    const uint32_t ks = ring_u + cslot * C::step, vs = ks + C::step / 2;
+    cslot = cslot == C::stages - 1 ? 0 : cslot + 1;
+    const int j0 = u.lo + kb * kBlockKeys + warp * kWarpKeys;
+    const int top = u.last, bottom = u.len - u.n + u.tile * kRows / p.G;
+    if (there) {
+      // ---- scores of 16 rows and 16 keys
+      float s[2][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+      if constexpr (F32) {
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d) {
+          uint32_t ah[2][4], al[2][4];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            split_tf32(__uint_as_float(q[8 * d + 2 * e]), ah[e][0], al[e][0]);
+            split_tf32(__uint_as_float(q[8 * d + 4 + 2 * e]), ah[e][1], al[e][1]);
+            split_tf32(__uint_as_float(q[8 * d + 2 * e + 1]), ah[e][2], al[e][2]);
+            split_tf32(__uint_as_float(q[8 * d + 5 + 2 * e]), ah[e][3], al[e][3]);
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float4 k4 = lds4(ks + key_at<D, F32>(8 * i + g, 4 * d + t));
+            uint32_t h[4], l[4];
+            split_tf32(k4.x, h[0], l[0]);
+            split_tf32(k4.y, h[1], l[1]);
+            split_tf32(k4.z, h[2], l[2]);
+            split_tf32(k4.w, h[3], l[3]);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              mma_tf32(s[i], al[e], h[2 * e], h[2 * e + 1]);
+              mma_tf32(s[i], ah[e], l[2 * e], l[2 * e + 1]);
+              mma_tf32(s[i], ah[e], h[2 * e], h[2 * e + 1]);
+            }
+          }
+        }
+      } else {
+        const int mi = lane >> 3, kr = (mi >> 1) * 8 + (lane & 7);
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d) {
+          uint32_t k4[4];
+          ldsm4(ks + key_at<D, F32>(kr, 2 * d + (mi & 1)), k4);
+          const uint32_t a[4] = {q[4 * d], q[4 * d + 1], q[4 * d + 2], q[4 * d + 3]};
+          mma_bf16_16816(s[0], a, k4[0], k4[1]);
+          mma_bf16_16816(s[1], a, k4[2], k4[3]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[i][e] *= p.scale;
+      // ---- masks, where some row of the tile does not attend some key
+      if (j0 + kWarpKeys - 1 > bottom || (p.window > 0 && j0 <= top - p.window)) {
+        // A masked value that is not finite would still make 0 * inf: such
+        // values become 0 here, and the rows that do attend the key NaN.
+        unsigned bad = 0;
+        for (int i = 0; i < kSteps; ++i) {
+          const int key = lane / kPieces + i * kKeysAtOnce;
+          unsigned char *at = ring + (vs - ring_u) + value_at<D, F32>(key, lane % kPieces);
+          uint4 w = *reinterpret_cast<uint4 *>(at);
+          bool hit = false;
+          auto tidy = [&](uint32_t &r) {
+            if constexpr (F32) {
+              if ((r & 0x7F800000u) == 0x7F800000u) {
+                r = 0;
+                hit = true;
+              }
+            } else {
+              if ((r & 0x7F80u) == 0x7F80u) {
+                r &= 0xFFFF0000u;
+                hit = true;
+              }
+              if ((r & 0x7F800000u) == 0x7F800000u) {
+                r &= 0xFFFFu;
+                hit = true;
+              }
+            }
+          };
+          tidy(w.x);
+          tidy(w.y);
+          tidy(w.z);
+          tidy(w.w);
+          if (hit) {
+            *reinterpret_cast<uint4 *>(at) = w;
+            bad |= 1u << key;
+          }
+        }
+        bad = __reduce_or_sync(0xffffffffu, bad);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int key = 8 * i + 2 * t + (e & 1), j = j0 + key, pos = e < 2 ? pos0 : pos1;
+            if (j > pos || (p.window > 0 && j <= pos - p.window))
+              s[i][e] = -INFINITY;
+            else if ((bad >> key) & 1)
+              s[i][e] = NAN;
+          }
+      }
+      // ---- running maximum and sum
+      float n0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
+      float n1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
+      n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, 1));
+      n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, 1));
+      n0 = fmaxf(m0, fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, 2)));
+      n1 = fmaxf(m1, fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, 2)));
+      const float z0 = n0 == -INFINITY ? 0.f : n0, z1 = n1 == -INFINITY ? 0.f : n1;
+      if (__any_sync(0xffffffffu, n0 != m0 || n1 != m1)) {
+        const float f0 = exp2_fast(m0 - z0), f1 = exp2_fast(m1 - z1);
+        m0 = n0;
+        m1 = n1;
+        l0 *= f0;
+        l1 *= f1;
+#pragma unroll
+        for (int i = 0; i < kO; ++i) {
+          o[i][0] *= f0;
+          o[i][1] *= f0;
+          o[i][2] *= f1;
+          o[i][3] *= f1;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        s[i][0] = exp2_fast(s[i][0] - z0);
+        s[i][1] = exp2_fast(s[i][1] - z0);
+        s[i][2] = exp2_fast(s[i][2] - z1);
+        s[i][3] = exp2_fast(s[i][3] - z1);
+        l0 += s[i][0] + s[i][1];
+        l1 += s[i][2] + s[i][3];
+      }
+      // ---- weights times values
+      if constexpr (F32) {
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+          uint32_t h[4], l[4];
+          split_tf32(s[kk][0], h[0], l[0]);
+          split_tf32(s[kk][2], h[1], l[1]);
+          split_tf32(s[kk][1], h[2], l[2]);
+          split_tf32(s[kk][3], h[3], l[3]);
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) {
+            const float4 v0 = lds4(vs + value_at<D, F32>(8 * kk + 2 * t, 8 * i + g));
+            const float4 v1 = lds4(vs + value_at<D, F32>(8 * kk + 2 * t + 1, 8 * i + g));
+            const float a[4] = {v0.x, v0.y, v0.z, v0.w}, b[4] = {v1.x, v1.y, v1.z, v1.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t ah, al, bh, bl;
+              split_tf32(a[e], ah, al);
+              split_tf32(b[e], bh, bl);
+              mma_tf32(o[4 * i + e], l, ah, bh);
+              mma_tf32(o[4 * i + e], h, al, bl);
+              mma_tf32(o[4 * i + e], h, ah, bh);
+            }
+          }
+        }
+      } else {
+        // Weights are at most 1 and rounded once to bf16, as the values are
+        // held: 2^-9 of each term. Their sum takes them unrounded.
+        const uint32_t a[4] = {bf16_bits(s[0][0]) | (bf16_bits(s[0][1]) << 16),
+                               bf16_bits(s[0][2]) | (bf16_bits(s[0][3]) << 16),
+                               bf16_bits(s[1][0]) | (bf16_bits(s[1][1]) << 16),
+                               bf16_bits(s[1][2]) | (bf16_bits(s[1][3]) << 16)};
+        const int mi = lane >> 3, vr = (mi & 1) * 8 + (lane & 7);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          uint32_t v4[4];
+          ldsm4_t(vs + value_at<D, F32>(vr, 2 * i + (mi >> 1)), v4);
+          mma_bf16_16816(o[2 * i], a, v4[0], v4[1]);
+          mma_bf16_16816(o[2 * i + 1], a, v4[2], v4[3]);
+        }
+      }
+    }
+    __syncwarp();
+    ++kb;
+    if (kb < u.blocks && x + 1 < x1) continue;
+
+    // ---- end of a piece: the warps' sums joined, 32 columns at a time ---------------
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+    if (t == 0) {
+      join_m[warp * kRows + g] = m0;
+      join_m[warp * kRows + g + 8] = m1;
+      join_l[warp * kRows + g] = l0;
+      join_l[warp * kRows + g + 8] = l1;
+    }
+    const bool begins = piece0 == 0, whole = begins && kb == u.blocks;
+    const int64_t piece = int64_t(blockIdx.x) * 2 + (begins ? 1 : 0);
+    float *part = p.parts + piece * (kRows * (D + 2));
+    // A thread's row, and four columns of it.
+    const int row = threadIdx.x >> 3, col = (threadIdx.x & 7) * 4;
+    float f[kWarps], inv = 0.f;
+    const int i = u.tile * kRows + row, tok = i / p.G;
+    E *out = static_cast<E *>(p.o.p) + int64_t(u.t0 + tok) * p.o.ts +
+             int64_t(u.head * p.G + i - tok * p.G) * p.o.hs;
+#pragma unroll
+    for (int c0 = 0; c0 < D; c0 += C::cols) {
+      float *mine = join + warp * kRows * C::ld;
+#pragma unroll
+      for (int c = 0; c < C::cols / 8; ++c) {
+        const float(&x4)[4] = o[c0 / 8 + c];
+        if constexpr (F32) {
+          // Column 2t + e' of tile c is d = 8t + 4e' + c.
+          mine[g * C::ld + 8 * t + c] = x4[0];
+          mine[g * C::ld + 8 * t + 4 + c] = x4[1];
+          mine[(g + 8) * C::ld + 8 * t + c] = x4[2];
+          mine[(g + 8) * C::ld + 8 * t + 4 + c] = x4[3];
+        } else {
+          *reinterpret_cast<float2 *>(mine + g * C::ld + 8 * c + 2 * t) =
+              make_float2(x4[0], x4[1]);
+          *reinterpret_cast<float2 *>(mine + (g + 8) * C::ld + 8 * c + 2 * t) =
+              make_float2(x4[2], x4[3]);
+        }
+      }
+      __syncthreads();
+      if (c0 == 0) {
+        float m = -INFINITY, l = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, join_m[w * kRows + row]);
+        const float z = m == -INFINITY ? 0.f : m;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          f[w] = exp2_fast(join_m[w * kRows + row] - z);
+          l += f[w] * join_l[w * kRows + row];
+        }
+        // No key attended: zeros.
+        inv = m == -INFINITY && l == 0.f ? 0.f : 1.f / l;
+        if (!whole && (threadIdx.x & 7) == 0) {
+          part[kRows * D + row] = m;
+          part[kRows * D + kRows + row] = l;
+        }
+      }
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float4 x4 =
+            *reinterpret_cast<const float4 *>(join + (w * kRows + row) * C::ld + col);
+        a.x += f[w] * x4.x;
+        a.y += f[w] * x4.y;
+        a.z += f[w] * x4.z;
+        a.w += f[w] * x4.w;
+      }
+      if (!whole) {
+        *reinterpret_cast<float4 *>(part + row * D + c0 + col) = a;
+      } else if (tok < u.n) {
+        if constexpr (F32)
+          *reinterpret_cast<float4 *>(out + c0 + col) =
+              make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+        else
+          *reinterpret_cast<uint2 *>(out + c0 + col) =
+              make_uint2(bf16_bits(a.x * inv) | (bf16_bits(a.y * inv) << 16),
+                         bf16_bits(a.z * inv) | (bf16_bits(a.w * inv) << 16));
+      }
+      __syncthreads();
+    }
+    if (x + 1 == x1) {
+      // A unit that begins here and goes on: the blocks after this one that
+      // have a piece of it.
+      if (threadIdx.x == 0) {
+        int more = 0;
+        if (begins && !whole) {
+          const int64_t end = x1 + u.blocks - kb;  // first block of the line past the unit
+          more = static_cast<int>((end * parts - 1) / total) - static_cast<int>(blockIdx.x);
+          // Block c begins at floor(c total / parts): the last c that begins before end.
+          while ((blockIdx.x + more) * total / parts >= end) --more;
+          while ((blockIdx.x + more + 1) * total / parts < end &&
+                 int64_t(blockIdx.x) + more + 1 < parts)
+            ++more;
+        }
+        header[0] = more;
+        header[1] = u.t0;
+        header[2] = u.n;
+        header[3] = u.head;
+        header[4] = u.tile;
+      }
+      break;
+    }
+    line.next(u);
+    kb = piece0 = 0;
+    load_rows();
+    clear();
+  }
+  cp_wait<0>();
+}
+
+// Joins the pieces of a unit: the one that begins at the end of block c's part
+// and the continuations at the start of the parts after it. A warp per row.
+template <int D, bool F32>
+__global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ AttnStreamParams p) {
+  using E = typename std::conditional<F32, float, uint16_t>::type;
+  constexpr int kPer = D / 32;
+  const int lane = threadIdx.x & 31, row = blockIdx.y * 4 + (threadIdx.x >> 5);
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int *h = p.headers + blockIdx.x * kHeader;
+  const int more = h[0];
+  if (more == 0) return;
+  const int t0 = h[1], n = h[2], head = h[3], i = h[4] * kRows + row, tok = i / p.G;
+  if (tok >= n) return;
+  constexpr int64_t kPart = kRows * (D + 2);
+  const float *first = p.parts + (int64_t(blockIdx.x) * 2 + 1) * kPart;
+  const float *rest = p.parts + (int64_t(blockIdx.x) + 1) * 2 * kPart;
+  float m = -INFINITY;
+  for (int c = lane; c <= more; c += 32)
+    m = fmaxf(m, (c == 0 ? first : rest + (c - 1) * 2 * kPart)[kRows * D + row]);
+#pragma unroll
+  for (int s = 1; s < 32; s *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
+  const float z = m == -INFINITY ? 0.f : m;
+  float l = 0.f, a[kPer];
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) a[e] = 0.f;
+#pragma unroll 4
+  for (int c = 0; c <= more; ++c) {
+    const float *x = c == 0 ? first : rest + (c - 1) * 2 * kPart;
+    const float f = exp2_fast(x[kRows * D + row] - z);
+    l += f * x[kRows * D + kRows + row];
+    const float *v = x + row * D + lane * kPer;
+#pragma unroll
+    for (int e = 0; e < kPer; e += 2) {
+      const float2 w = *reinterpret_cast<const float2 *>(v + e);
+      a[e] += f * w.x;
+      a[e + 1] += f * w.y;
+    }
+  }
+  const float inv = m == -INFINITY && l == 0.f ? 0.f : 1.f / l;
+  E *out = static_cast<E *>(p.o.p) + int64_t(t0 + tok) * p.o.ts +
+           int64_t(head * p.G + i - tok * p.G) * p.o.hs + lane * kPer;
+#pragma unroll
+  for (int e = 0; e < kPer; e += 2) {
+    if constexpr (F32)
+      *reinterpret_cast<float2 *>(out + e) = make_float2(a[e] * inv, a[e + 1] * inv);
+    else
+      *reinterpret_cast<uint32_t *>(out + e) =
+          bf16_bits(a[e] * inv) | (bf16_bits(a[e + 1] * inv) << 16);
+  }
+}
+
+int grid_blocks(bool f32, int D) {
+  return std::max(1, sm_count()) * (D * (f32 ? 4 : 2) <= 256 ? 2 : 1);
+}
+
+template <int D, bool F32>
+cudaError_t run(const AttnStreamParams &p, bool pdl, cudaStream_t stream) {
+  using C = Cfg<D, F32>;
+  static std::atomic<unsigned long long> done{0};
+  cudaError_t e = ensure_smem_limit(stream_kernel<D, F32>, C::smem, done);
+  if (e != cudaSuccess) return e;
+  const int grid = grid_blocks(F32, D);
+  e = launch_after(stream_kernel<D, F32>, dim3(grid), kThreads, C::smem, pdl, stream, p);
+  if (e != cudaSuccess) return e;
+  return launch_after(combine_kernel<D, F32>, dim3(grid, kRows / 4), 128, 0, pdl, stream, p);
+}
+
+size_t header_bytes(int grid) { return (size_t(grid) * kHeader * 4 + 255) & ~size_t(255); }
+
+}  // namespace
+
+size_t stream_workspace_bytes(bool f32, int D) {
+  const int grid = grid_blocks(f32, D);
+  return header_bytes(grid) + size_t(grid) * 2 * kRows * (D + 2) * 4;
+}
+
+cudaError_t launch_attn_stream(const AttnArgs &a, cudaStream_t stream) {
+  AttnStreamParams p{};
+  p.q = a.q;
+  p.o = a.o;
+  p.k = a.c.k;
+  p.v = a.c.v;
+  p.pages = static_cast<int>(a.c.pages);
+  p.page_size = a.c.page_size;
+  p.kv_heads = a.c.heads;
+  p.G = a.q.n / a.c.heads;
+  p.b = a.b;
+  p.T = static_cast<int>(a.T);
+  p.cap = static_cast<int>(int64_t(a.b.table_pages) * a.c.page_size);
+  p.window = static_cast<int>(std::min<int64_t>(a.window, p.cap));
+  p.scale = a.scale * 1.44269504088896340736f;  // log2(e): weights are powers of two
+  p.headers = reinterpret_cast<int *>(a.ws);
+  p.parts = reinterpret_cast<float *>(a.ws + header_bytes(grid_blocks(a.f32, a.c.D)));
+  if (a.f32)
+    return a.c.D == 64 ? run<64, true>(p, a.pdl, stream) : run<128, true>(p, a.pdl, stream);
+  return a.c.D == 64 ? run<64, false>(p, a.pdl, stream) : run<128, false>(p, a.pdl, stream);
+}
+
+}  // namespace mnb

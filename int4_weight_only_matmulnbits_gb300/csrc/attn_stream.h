@@ -1,0 +1,23 @@
+// Parameters of the attention kernel that streams keys past a few query rows.
+#pragma once
+
+#include "attn.h"
+
+namespace mnb {
+
+struct AttnStreamParams {
+  Heads q, o;
+  Pages k, v;
+  BatchView b;
+  int pages, page_size, kv_heads, G;  // G: query heads per key head
+  int T, cap;                         // cap: tokens that a row of the table holds
+  int window;                         // 0: none
+  float scale;                        // of the scores, times log2(e)
+  int *headers;                       // of the pieces that end a block's part
+  float *parts;                       // two pieces per block: sums, maxima, sums of weights
+};
+
+size_t stream_workspace_bytes(bool f32, int D);
+cudaError_t launch_attn_stream(const AttnArgs &a, cudaStream_t stream);
+
+}  // namespace mnb
