@@ -1032,8 +1032,9 @@ MNB_API mnb_status mnb_cache_append(const mnb_heads *q, const mnb_heads *k, cons
  *    256-byte aligned; needs no preparation, means nothing afterwards. Calls
  *    that may overlap on the GPU need one each.
  * Sums and the softmax are fp32. bf16: weights relative to a running maximum
- * are rounded to bf16 (2^-9) for the product with the values, not for their
- * sum. fp32: products from tf32 pairs, within 2^-20 of the terms' magnitudes.
+ * are rounded to bf16 (2^-8) for the product with the values, not for their
+ * sum. fp32: products from three bf16 parts of each factor, within 2^-22 of
+ * the terms' magnitudes (magnitudes above 3.38e38 count as infinite).
  * What a masked place holds does not matter, infinities and NaN included. An
  * infinity or NaN in a key or value that a row does attend makes the row
  * non-finite (not always as an exact sum would be), and no other.

@@ -22,6 +22,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <type_traits>
 
 #include "attn.h"
@@ -51,7 +52,9 @@ struct Cfg {
   static constexpr int ring = kWarps * stages * step;
   static constexpr int cols = 32;               // columns joined at a time
   static constexpr int ld = cols + 4;
-  static constexpr int smem = ring + kWarps * kRows * (ld + 2) * 4;
+  static constexpr int joins = kWarps * kRows * (ld + 2) * 4;
+  static constexpr int parts = F32 ? kRows * D * 6 : 0;  // the rows of q in bf16 parts
+  static constexpr int smem = ring + joins + parts;
   static_assert(stages >= 3, "copies in flight");
 };
 
@@ -85,26 +88,35 @@ __device__ __forceinline__ float4 lds4(uint32_t addr) {
                : "memory");
   return v;
 }
-__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 "
-      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
-// x as two tf32 numbers (11 bits each, rounded to nearest): the sum is within
-// 2^-22 of x, and the three products hi hi + hi lo + lo hi within 2^-21 of the
-// product. Infinities and NaN stay in hi (their lo is NaN, which no finite
-// product can have taken in).
-__device__ __forceinline__ void split_tf32(float x, uint32_t &hi, uint32_t &lo) {
-  hi = (__float_as_uint(x) + 0x1000u) & 0xFFFFE000u;
-  lo = __float_as_uint(x - __uint_as_float(hi)) + 0x1000u;
+// Two fp32 numbers as three pairs of bf16 numbers each, 24 bits in all: x =
+// h + m + l to 2^-25 of it. Of the nine products of two such numbers the six
+// largest are taken, so a product is within 2^-23 or so. (tf32 pairs cost as
+// many tensor instructions and keep 21 bits: scores of 30 then move weights by
+// 7e-6.) Infinities, NaN and what is above bf16's largest number become NaN.
+__device__ __forceinline__ void split3(float x, float y, uint32_t &h, uint32_t &m, uint32_t &l) {
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(y), "f"(x));
+  x -= __uint_as_float(h << 16);
+  y -= __uint_as_float(h & 0xFFFF0000u);
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(m) : "f"(y), "f"(x));
+  x -= __uint_as_float(m << 16);
+  y -= __uint_as_float(m & 0xFFFF0000u);
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(l) : "f"(y), "f"(x));
+}
+// d += a b from the parts (0: h, 1: m, 2: l), the smallest products first.
+__device__ __forceinline__ void mma_parts(float (&d)[4], const uint32_t (&a)[3][4],
+                                          const uint32_t (&b0)[3], const uint32_t (&b1)[3]) {
+  mma_bf16_16816(d, a[2], b0[0], b1[0]);
+  mma_bf16_16816(d, a[0], b0[2], b1[2]);
+  mma_bf16_16816(d, a[1], b0[1], b1[1]);
+  mma_bf16_16816(d, a[1], b0[0], b1[0]);
+  mma_bf16_16816(d, a[0], b0[1], b1[1]);
+  mma_bf16_16816(d, a[0], b0[0], b1[0]);
 }
 
 // Bytes 16-byte piece `c` of key `k` lies at in a step's keys or values: pieces
@@ -216,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F32>::per_sm)
   constexpr int kPieces = C::row / 16;            // 16-byte pieces of a key
   constexpr int kKeysAtOnce = 32 / kPieces > 0 ? 32 / kPieces : 1;
   constexpr int kSteps = kWarpKeys / kKeysAtOnce;  // copies per lane, keys or values
-  constexpr int kQ = F32 ? D / 2 : D / 4;          // query registers
+  constexpr int kQ = F32 ? 1 : D / 4;              // query registers
   constexpr int kO = D / 8;                        // 8-wide column tiles
   extern __shared__ __align__(128) unsigned char smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -224,6 +236,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F32>::per_sm)
   const uint32_t ring_u = smem_addr(ring);
   float *join = reinterpret_cast<float *>(smem + C::ring);  // [warp][row][ld]
   float *join_m = join + kWarps * kRows * C::ld, *join_l = join_m + kWarps * kRows;
+  uint4 *qparts = reinterpret_cast<uint4 *>(smem + C::ring + C::joins);  // [d / 16][part][lane]
 
   grid_dependency_wait();
   grid_dependents_launch();
@@ -319,14 +332,23 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F32>::per_sm)
     };
     const E *a = row_of(g, pos0), *b = row_of(g + 8, pos1);
     if constexpr (F32) {
+      // Each warp makes a quarter of the parts, in the order of the MMAs'
+      // registers. The k order within 16 elements is the keys': a lane's are 4t
+      // to 4t + 3.
+      for (int d = warp; d < D / 16; d += kWarps) {
+        const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+        const float4 x = a ? *reinterpret_cast<const float4 *>(a + 16 * d + 4 * t) : z;
+        const float4 y = b ? *reinterpret_cast<const float4 *>(b + 16 * d + 4 * t) : z;
+        uint32_t w[3][4];
+        split3(x.x, x.y, w[0][0], w[1][0], w[2][0]);
+        split3(y.x, y.y, w[0][1], w[1][1], w[2][1]);
+        split3(x.z, x.w, w[0][2], w[1][2], w[2][2]);
+        split3(y.z, y.w, w[0][3], w[1][3], w[2][3]);
 #pragma unroll
-      for (int s = 0; s < D / 16; ++s) {
-        const uint4 z = make_uint4(0, 0, 0, 0);
-        const uint4 x = a ? *reinterpret_cast<const uint4 *>(a + 16 * s + 4 * t) : z;
-        const uint4 y = b ? *reinterpret_cast<const uint4 *>(b + 16 * s + 4 * t) : z;
-        q[8 * s] = x.x; q[8 * s + 1] = x.y; q[8 * s + 2] = x.z; q[8 * s + 3] = x.w;
-        q[8 * s + 4] = y.x; q[8 * s + 5] = y.y; q[8 * s + 6] = y.z; q[8 * s + 7] = y.w;
+        for (int i = 0; i < 3; ++i)
+          qparts[(d * 3 + i) * 32 + lane] = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
       }
+      __syncthreads();
     } else {
 #pragma unroll
       for (int s = 0; s < D / 16; ++s) {
@@ -367,28 +389,22 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F32>::per_sm)
       if constexpr (F32) {
 #pragma unroll
         for (int d = 0; d < D / 16; ++d) {
-          uint32_t ah[2][4], al[2][4];
+          uint32_t a[3][4];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            split_tf32(__uint_as_float(q[8 * d + 2 * e]), ah[e][0], al[e][0]);
-            split_tf32(__uint_as_float(q[8 * d + 4 + 2 * e]), ah[e][1], al[e][1]);
-            split_tf32(__uint_as_float(q[8 * d + 2 * e + 1]), ah[e][2], al[e][2]);
-            split_tf32(__uint_as_float(q[8 * d + 5 + 2 * e]), ah[e][3], al[e][3]);
+          for (int i = 0; i < 3; ++i) {
+            const uint4 w = qparts[(d * 3 + i) * 32 + lane];
+            a[i][0] = w.x;
+            a[i][1] = w.y;
+            a[i][2] = w.z;
+            a[i][3] = w.w;
           }
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const float4 k4 = lds4(ks + key_at<D, F32>(8 * i + g, 4 * d + t));
-            uint32_t h[4], l[4];
-            split_tf32(k4.x, h[0], l[0]);
-            split_tf32(k4.y, h[1], l[1]);
-            split_tf32(k4.z, h[2], l[2]);
-            split_tf32(k4.w, h[3], l[3]);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              mma_tf32(s[i], al[e], h[2 * e], h[2 * e + 1]);
-              mma_tf32(s[i], ah[e], l[2 * e], l[2 * e + 1]);
-              mma_tf32(s[i], ah[e], h[2 * e], h[2 * e + 1]);
-            }
+            uint32_t b0[3], b1[3];
+            split3(k4.x, k4.y, b0[0], b0[1], b0[2]);
+            split3(k4.z, k4.w, b1[0], b1[1], b1[2]);
+            mma_parts(s[i], a, b0, b1);
           }
         }
       } else {
@@ -405,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F32>::per_sm)
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[i][e] *= p.scale;
+        for (int e = 0; e < 4; ++e) s[i][e] = p.negative ? -s[i][e] : s[i][e];
       // ---- masks, where some row of the tile does not attend some key
       if (j0 + kWarpKeys - 1 > bottom || (p.window > 0 && j0 <= top - p.window)) {
         // A masked value that is not finite would still make 0 * inf: such
@@ -455,7 +471,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F32>::per_sm)
               s[i][e] = NAN;
           }
       }
-      // ---- running maximum and sum
+      // ---- running maximum and sum. Differences from the maximum are scaled,
+      // not scores: the rounding of a large score's product with the scale
+      // would move its weight.
       float n0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
       float n1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
       n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, 1));
@@ -464,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F32>::per_sm)
       n1 = fmaxf(m1, fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, 2)));
       const float z0 = n0 == -INFINITY ? 0.f : n0, z1 = n1 == -INFINITY ? 0.f : n1;
       if (__any_sync(0xffffffffu, n0 != m0 || n1 != m1)) {
-        const float f0 = exp2_fast(m0 - z0), f1 = exp2_fast(m1 - z1);
+        const float f0 = exp2_fast((m0 - z0) * p.scale), f1 = exp2_fast((m1 - z1) * p.scale);
         m0 = n0;
         m1 = n1;
         l0 *= f0;
@@ -479,41 +497,43 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F32>::per_sm)
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        s[i][0] = exp2_fast(s[i][0] - z0);
-        s[i][1] = exp2_fast(s[i][1] - z0);
-        s[i][2] = exp2_fast(s[i][2] - z1);
-        s[i][3] = exp2_fast(s[i][3] - z1);
+        s[i][0] = exp2_fast((s[i][0] - z0) * p.scale);
+        s[i][1] = exp2_fast((s[i][1] - z0) * p.scale);
+        s[i][2] = exp2_fast((s[i][2] - z1) * p.scale);
+        s[i][3] = exp2_fast((s[i][3] - z1) * p.scale);
         l0 += s[i][0] + s[i][1];
         l1 += s[i][2] + s[i][3];
       }
       // ---- weights times values
       if constexpr (F32) {
+        uint32_t a[3][4];
+        split3(s[0][0], s[0][1], a[0][0], a[1][0], a[2][0]);
+        split3(s[0][2], s[0][3], a[0][1], a[1][1], a[2][1]);
+        split3(s[1][0], s[1][1], a[0][2], a[1][2], a[2][2]);
+        split3(s[1][2], s[1][3], a[0][3], a[1][3], a[2][3]);
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-          uint32_t h[4], l[4];
-          split_tf32(s[kk][0], h[0], l[0]);
-          split_tf32(s[kk][2], h[1], l[1]);
-          split_tf32(s[kk][1], h[2], l[2]);
-          split_tf32(s[kk][3], h[3], l[3]);
+        for (int i = 0; i < D / 32; ++i) {
+          float v[4][4];
 #pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
-            const float4 v0 = lds4(vs + value_at<D, F32>(8 * kk + 2 * t, 8 * i + g));
-            const float4 v1 = lds4(vs + value_at<D, F32>(8 * kk + 2 * t + 1, 8 * i + g));
-            const float a[4] = {v0.x, v0.y, v0.z, v0.w}, b[4] = {v1.x, v1.y, v1.z, v1.w};
+          for (int k = 0; k < 4; ++k) {
+            const int key = 2 * t + (k & 1) + 8 * (k >> 1);
+            const float4 w = lds4(vs + value_at<D, F32>(key, 8 * i + g));
+            v[k][0] = w.x;
+            v[k][1] = w.y;
+            v[k][2] = w.z;
+            v[k][3] = w.w;
+          }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t ah, al, bh, bl;
-              split_tf32(a[e], ah, al);
-              split_tf32(b[e], bh, bl);
-              mma_tf32(o[4 * i + e], l, ah, bh);
-              mma_tf32(o[4 * i + e], h, al, bl);
-              mma_tf32(o[4 * i + e], h, ah, bh);
-            }
+          for (int e = 0; e < 4; ++e) {
+            uint32_t b0[3], b1[3];
+            split3(v[0][e], v[1][e], b0[0], b0[1], b0[2]);
+            split3(v[2][e], v[3][e], b1[0], b1[1], b1[2]);
+            mma_parts(o[4 * i + e], a, b0, b1);
           }
         }
       } else {
         // Weights are at most 1 and rounded once to bf16, as the values are
-        // held: 2^-9 of each term. Their sum takes them unrounded.
+        // held: 2^-8 of each term. Their sum takes them unrounded.
         const uint32_t a[4] = {bf16_bits(s[0][0]) | (bf16_bits(s[0][1]) << 16),
                                bf16_bits(s[0][2]) | (bf16_bits(s[0][3]) << 16),
                                bf16_bits(s[1][0]) | (bf16_bits(s[1][1]) << 16),
@@ -579,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F32>::per_sm)
         const float z = m == -INFINITY ? 0.f : m;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-          f[w] = exp2_fast(join_m[w * kRows + row] - z);
+          f[w] = exp2_fast((join_m[w * kRows + row] - z) * p.scale);
           l += f[w] * join_l[w * kRows + row];
         }
         // No key attended: zeros.
@@ -671,7 +691,7 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ At
 #pragma unroll 4
   for (int c = 0; c <= more; ++c) {
     const float *x = c == 0 ? first : rest + (c - 1) * 2 * kPart;
-    const float f = exp2_fast(x[kRows * D + row] - z);
+    const float f = exp2_fast((x[kRows * D + row] - z) * p.scale);
     l += f * x[kRows * D + kRows + row];
     const float *v = x + row * D + lane * kPer;
 #pragma unroll
@@ -733,7 +753,11 @@ cudaError_t launch_attn_stream(const AttnArgs &a, cudaStream_t stream) {
   p.T = static_cast<int>(a.T);
   p.cap = static_cast<int>(int64_t(a.b.table_pages) * a.c.page_size);
   p.window = static_cast<int>(std::min<int64_t>(a.window, p.cap));
-  p.scale = a.scale * 1.44269504088896340736f;  // log2(e): weights are powers of two
+  // Weights are powers of two, of (score - maximum) * |scale| log2(e).
+  // (Kept off 0 and infinity: what a masked score, -inf, is multiplied by.)
+  p.scale = static_cast<float>(
+      std::min(std::max(std::fabs(static_cast<double>(a.scale)) * M_LOG2E, 1e-37), 3e38));
+  p.negative = a.scale < 0.f;
   p.headers = reinterpret_cast<int *>(a.ws);
   p.parts = reinterpret_cast<float *>(a.ws + header_bytes(grid_blocks(a.f32, a.c.D)));
   if (a.f32)

@@ -12,7 +12,8 @@ struct AttnStreamParams {
   int pages, page_size, kv_heads, G;  // G: query heads per key head
   int T, cap;                         // cap: tokens that a row of the table holds
   int window;                         // 0: none
-  float scale;                        // of the scores, times log2(e)
+  float scale;                        // |scale| of the scores, times log2(e)
+  int negative;                       // the scale is: scores change their sign
   int *headers;                       // of the pieces that end a block's part
   float *parts;                       // two pieces per block: sums, maxima, sums of weights
 };
