@@ -13,6 +13,7 @@
 
 #include "../../include/mnb.h"
 #include "attn.h"
+#include "attn_tile.h"
 #include "mnb_common.cuh"
 #include "mnb_launch.h"
 #include "moe.h"
@@ -759,8 +760,10 @@ mnb_status mnb_fault_status(unsigned int *fault_bits) {
   if (e == cudaSuccess) e = pair_take_fault(&d);
   unsigned int f = 0;
   if (e == cudaSuccess) e = moe_take_fault(&f);
+  unsigned int g = 0;
+  if (e == cudaSuccess) e = attn_take_fault(&g);
   if (e != cudaSuccess) return cuda_fail(e, "mnb_fault_status");
-  *fault_bits = a | b | c | d | f;
+  *fault_bits = a | b | c | d | f | g;
   return MNB_OK;
 }
 

@@ -1,0 +1,905 @@
+// Attention of many new tokens over the pages of a cache on the tensor cores
+// (tcgen05 / TMEM), bf16, head sizes 64 and 128.
+//
+//   o_i = sum_j w_ij v_j / sum_j w_ij,  w_ij = exp(scale q_i . k_j),
+// one pass over the keys with a running maximum and sum per row.
+//
+// Rows of a sequence are (token, head of the key head's group), token first.
+// A unit is 256 of them, two tiles of 128, times the keys that they attend, in
+// blocks of 128 keys. plan_kernel lists the units of a key head with their
+// blocks; all blocks of all key heads form one line, of which every CTA (one
+// per SM, persistent) takes an equal part: ragged batches, causal prompts and
+// a few rows over a long cache share out alike, whatever the device arrays
+// hold. Pieces of units that several CTAs share are joined by combine_kernel.
+//
+// In a CTA the two tiles take turns: while one tile's softmax runs in its
+// warps (a thread per row), the tensor core works for the other.
+//   S_i = Q_i K^T   128 x 128 fp32 in TMEM, Q and K in shared memory
+//   P_i = weights   bf16, written over S_i, an operand from TMEM
+//   O_i += P_i V    V as it lies in shared memory (keys by rows: the N-major
+//                   form of the B operand)
+// S and O of both tiles fill the 512 columns of TMEM. MMAs execute in the
+// order of their issue, so S of the next block may follow directly on the
+// product that reads P out of the same columns, and the arrival that tells of
+// S tells that O is at rest too: a row's O is rescaled by its own thread, and
+// only when its maximum has grown by 2^8 in weight (weights above 1 up to 2^8
+// do no harm in bf16 or in the fp32 sums).
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+
+#include "attn_tile.h"
+#include "mnb_common.cuh"
+#include "mnb_launch.h"
+#include "umma.cuh"
+
+namespace mnb {
+
+__device__ unsigned int g_fault_attn = 0;
+
+namespace {
+
+constexpr int kTile = 128;                 // rows of an MMA, keys of a block
+constexpr int kUnit = 2 * kTile;           // rows of a unit
+constexpr int kSoftWarps = 8;              // two tiles of four warps
+constexpr int kTmaWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;
+constexpr int kThreads = 32 * (kSoftWarps + 2);
+constexpr int kInfo = 8;                   // blocks whose key masks are kept
+constexpr int kTmemCols = 512;
+constexpr int kHeader = 8;                 // ints
+constexpr float kGrow = 8.f;               // rescale from 2^8 on
+
+template <int D>
+struct Cfg {
+  static constexpr int tile = kTile * D * 2;       // bytes of 128 rows of q, k or v
+  static constexpr int half = kTile * 128;         // bytes of their 64 columns
+  static constexpr int stages = D == 128 ? 5 : 10;
+  static constexpr int off_ring = 2 * tile;
+  static constexpr int off_info = off_ring + stages * tile;
+  static constexpr int off_bar = off_info + kInfo * 32;
+  static constexpr int total = off_bar + 512;
+};
+static_assert(Cfg<128>::total + 1024 <= 227 * 1024, "shared memory");
+
+struct Info {       // of a block of keys
+  uint32_t pages;   // bit g: keys 16 g .. 16 g + 15 have a page
+  uint32_t pad[3];
+  uint32_t bad[4];  // keys whose values are not finite
+};
+static_assert(sizeof(Info) == 32, "");
+
+// Bounded wait that sleeps in the hardware for up to 50 us at a time: a warp
+// that polls takes issue slots from the softmax. At most about a second.
+__device__ __forceinline__ bool mbar_sleep(uint64_t *bar, uint32_t parity) {
+  for (uint32_t i = 0; i < 20000u; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(50000u)
+        : "memory");
+    if (ok) return true;
+  }
+  return false;
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok));
+  return ok != 0;
+}
+__device__ __forceinline__ void tma_load_4d(void *dst, const void *tmap, int x, int y, int z,
+                                            int w, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
+      : "memory");
+}
+// D fp32, A and B bf16, M = 128; B's rows are its N (n_major: its K) index.
+__host__ __device__ constexpr uint32_t idesc_bf16(int n, bool b_n_major) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (b_n_major ? 1u << 16 : 0u) |
+         (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(kTile >> 4) << 24);
+}
+__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void umma_commit(uint64_t *bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+          smem_addr(bar))
+      : "memory");
+}
+// V's descriptor: rows of 64 columns (128 bytes, swizzled), one per key; groups
+// of 8 keys lie 1024 bytes apart (stride offset), the halves of 64 columns
+// `half` bytes apart (leading offset).
+__device__ __forceinline__ uint64_t smem_desc_rows(uint32_t addr, uint32_t half) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((addr & 0x3FFFF) >> 4);
+  d |= static_cast<uint64_t>(half >> 4) << 16;
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+// 128 consecutive fp32 columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld128(uint32_t taddr, float (&v)[128]) {
+  uint32_t r[128];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x128.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+      "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+      "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63, "
+      "%64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, "
+      "%80, %81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95, "
+      "%96, %97, %98, %99, %100, %101, %102, %103, %104, %105, %106, %107, %108, %109, %110, %111, "
+      "%112, %113, %114, %115, %116, %117, %118, %119, %120, %121, %122, %123, %124, %125, %126, %127}, [%128];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+        "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+        "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63]),
+        "=r"(r[64]), "=r"(r[65]), "=r"(r[66]), "=r"(r[67]), "=r"(r[68]), "=r"(r[69]), "=r"(r[70]), "=r"(r[71]),
+        "=r"(r[72]), "=r"(r[73]), "=r"(r[74]), "=r"(r[75]), "=r"(r[76]), "=r"(r[77]), "=r"(r[78]), "=r"(r[79]),
+        "=r"(r[80]), "=r"(r[81]), "=r"(r[82]), "=r"(r[83]), "=r"(r[84]), "=r"(r[85]), "=r"(r[86]), "=r"(r[87]),
+        "=r"(r[88]), "=r"(r[89]), "=r"(r[90]), "=r"(r[91]), "=r"(r[92]), "=r"(r[93]), "=r"(r[94]), "=r"(r[95]),
+        "=r"(r[96]), "=r"(r[97]), "=r"(r[98]), "=r"(r[99]), "=r"(r[100]), "=r"(r[101]), "=r"(r[102]), "=r"(r[103]),
+        "=r"(r[104]), "=r"(r[105]), "=r"(r[106]), "=r"(r[107]), "=r"(r[108]), "=r"(r[109]), "=r"(r[110]), "=r"(r[111]),
+        "=r"(r[112]), "=r"(r[113]), "=r"(r[114]), "=r"(r[115]), "=r"(r[116]), "=r"(r[117]), "=r"(r[118]), "=r"(r[119]),
+        "=r"(r[120]), "=r"(r[121]), "=r"(r[122]), "=r"(r[123]), "=r"(r[124]), "=r"(r[125]), "=r"(r[126]), "=r"(r[127])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 128; ++i) v[i] = __uint_as_float(r[i]);
+}
+// 32 consecutive 32-bit columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
+      :
+      : "r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+        "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+        "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) {
+  uint32_t r[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(v[i]);
+  tmem_st32(taddr, r);
+}
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// ---- the line of blocks -------------------------------------------------------------
+
+struct Unit {
+  int t0, n, len, tile;  // rows tile * 256 .. of a sequence's n tokens from row t0 on
+  int block0, blocks;    // of keys
+  int b;                 // the sequence
+};
+
+__device__ __forceinline__ int units_of(const Seq &s, int G) {
+  return static_cast<int>((int64_t(s.n) * G + kUnit - 1) / kUnit);
+}
+__device__ __forceinline__ int first_pos(const Unit &u, int G) {
+  return u.len - u.n + static_cast<int>(int64_t(u.tile) * kUnit / G);
+}
+__device__ __forceinline__ int last_pos(const Unit &u, int G) {
+  return u.len - u.n +
+         static_cast<int>(min(int64_t(u.n) - 1, (int64_t(u.tile) * kUnit + kUnit - 1) / G));
+}
+
+// Inclusive sums over the block's threads.
+template <typename I>
+__device__ __forceinline__ I block_scan(I v, I *sums, int tid) {
+  const int lane = tid & 31, warp = tid >> 5;
+#pragma unroll
+  for (int m = 1; m < 32; m *= 2) {
+    const I o = __shfl_up_sync(0xffffffffu, v, m);
+    if (lane >= m) v += o;
+  }
+  __syncthreads();
+  if (lane == 31) sums[warp] = v;
+  __syncthreads();
+  if (warp == 0) {
+    I w = sums[lane];
+#pragma unroll
+    for (int m = 1; m < 32; m *= 2) {
+      const I o = __shfl_up_sync(0xffffffffu, w, m);
+      if (lane >= m) w += o;
+    }
+    sums[lane] = w;
+  }
+  __syncthreads();
+  return warp ? v + sums[warp - 1] : v;
+}
+
+// Lists the units of a key head and where in the line each begins: one block,
+// a warp per sequence. Latency-bound.
+constexpr int kPlanThreads = 1024;
+__global__ void __launch_bounds__(kPlanThreads)
+    plan_kernel(const __grid_constant__ AttnTileParams p) {
+  __shared__ int64_t sums[32];
+  __shared__ int offset[kPlanThreads];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  grid_dependency_wait();
+  grid_dependents_launch();
+  int base = 0;
+  for (int b0 = 0; b0 < p.b.n; b0 += kPlanThreads) {
+    int mine = 0;
+    if (b0 + tid < p.b.n) mine = units_of(load_seq(p.b, b0 + tid, p.T, p.cap, p.window), p.G);
+    const int upto = static_cast<int>(block_scan<int64_t>(mine, sums, tid));
+    offset[tid] = base + upto - mine;
+    base += static_cast<int>(sums[31]);
+    __syncthreads();
+    for (int i = warp; i < min(kPlanThreads, p.b.n - b0); i += 32) {
+      const Seq s = load_seq(p.b, b0 + i, p.T, p.cap, p.window);
+      const int n = units_of(s, p.G);
+      for (int t = lane; t < n; t += 32) {
+        Unit u{s.t0, s.n, s.len, t, 0, 0, b0 + i};
+        if (p.window > 0) u.block0 = max(0, first_pos(u, p.G) - p.window + 1) / kTile;
+        u.blocks = max(1, (last_pos(u, p.G) + kTile) / kTile - u.block0);
+        p.units[2 * (offset[i] + t)] = make_int4(u.t0, u.n, u.len, u.tile);
+        p.units[2 * (offset[i] + t) + 1] = make_int4(u.block0, u.blocks, u.b, 0);
+      }
+    }
+    __syncthreads();
+  }
+  int64_t at = 0;
+  for (int u0 = 0; u0 < base; u0 += kPlanThreads) {
+    const int64_t mine = u0 + tid < base ? p.units[2 * (u0 + tid) + 1].y : 0;
+    const int64_t upto = block_scan<int64_t>(mine, sums, tid);
+    if (u0 + tid < base) p.first[u0 + tid] = at + upto - mine;
+    at += sums[31];
+    __syncthreads();
+  }
+  if (tid == 0) {
+    p.first[base] = at;
+    p.line[0] = at;
+    p.line[1] = base;
+  }
+}
+
+// A CTA's part of the line, piece by piece.
+struct Walk {
+  const AttnTileParams &p;
+  int64_t x, x1, total;
+  int parts, n_units, unit, head, k0, k1;
+  Unit u;
+  __device__ __forceinline__ explicit Walk(const AttnTileParams &p_) : p(p_) {}
+  __device__ __forceinline__ void load() {
+    const int4 a = p.units[2 * unit], b = p.units[2 * unit + 1];
+    u = Unit{a.x, a.y, a.z, a.w, b.x, b.y, b.z};
+    k1 = static_cast<int>(min(int64_t(u.blocks), x1 - x + k0));
+  }
+  // Whole warps; false: nothing for this CTA.
+  __device__ __forceinline__ bool start(int lane) {
+    const int64_t per = p.line[0];
+    n_units = static_cast<int>(p.line[1]);
+    total = per * p.kv_heads;
+    parts = static_cast<int>(min(int64_t(gridDim.x), total));
+    if (static_cast<int>(blockIdx.x) >= parts) return false;
+    x = blockIdx.x * total / parts;
+    x1 = (blockIdx.x + 1) * total / parts;
+    head = static_cast<int>(x / per);
+    const int64_t in = x - head * per;
+    int lo = 0, hi = n_units;
+    while (hi - lo > 1) {
+      const int step = (hi - lo + 31) / 32, i = lo + (lane + 1) * step;
+      const int k = __popc(__ballot_sync(0xffffffffu, i < hi && p.first[i] <= in));
+      lo += k * step;
+      hi = min(hi, lo + step);
+    }
+    unit = lo;
+    k0 = static_cast<int>(in - p.first[unit]);
+    load();
+    return true;
+  }
+  __device__ __forceinline__ bool next() {
+    x += k1 - k0;
+    if (x >= x1) return false;
+    k0 = 0;
+    if (++unit == n_units) {
+      unit = 0;
+      ++head;
+    }
+    load();
+    return true;
+  }
+  __device__ __forceinline__ bool two() const {
+    return int64_t(u.n) * p.G > int64_t(u.tile) * kUnit + kTile;
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    tile_kernel(const __grid_constant__ AttnTileParams p) {
+  using C = Cfg<D>;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+  Info *infos = reinterpret_cast<Info *>(smem + C::off_info);
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::off_bar);
+  uint64_t *empty = full + C::stages;
+  uint64_t *known = empty + C::stages;  // a block's info is there
+  uint64_t *sfull = known + kInfo;      // per tile
+  uint64_t *pfull = sfull + 2;
+  uint64_t *qfull = pfull + 2;
+  uint64_t *ofull = qfull + 2;
+  uint64_t *scanned = ofull + 2;        // a tile's warps have looked over the values
+  uint64_t *done = scanned + 2;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
+  static_assert((2 * C::stages + kInfo + 11) * 8 + 4 <= 512, "barriers");
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int i = 0; i < C::stages; ++i) {
+      mbar_init(full + i, 1);
+      mbar_init(empty + i, 1);
+    }
+    for (int i = 0; i < kInfo; ++i) mbar_init(known + i, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(sfull + i, 1);
+      mbar_init(pfull + i, 4);
+      mbar_init(qfull + i, 4);
+      mbar_init(ofull + i, 1);
+      mbar_init(scanned + i, 4);
+    }
+    mbar_init(done, 1);
+    fence_barrier_init();
+  }
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_addr(tmem_slot)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  grid_dependency_wait();
+  grid_dependents_launch();
+  Walk w(p);
+  const bool any = w.start(lane);
+  int *header = p.headers + blockIdx.x * kHeader;
+  if (!any) {
+    if (tid == 0) header[0] = 0;
+  } else if (warp == kTmaWarp) {
+    // ---- keys and values ----------------------------------------------------------
+    const int nbox = kTile / p.box;  // copies of 64 columns: nbox for each half
+    const int box = lane % nbox, col = lane / nbox;
+    const bool copies = lane < nbox * (D / 64);
+    int tiles = 0, blocks = 0;
+    bool ok = true;
+    do {
+      const int last = last_pos(w.u, p.G), end = min(w.u.len, p.cap);
+      // Lane g < 8: the page of the keys 16 g on of the next block.
+      auto page_of = [&](int kb) {
+        const int j = (w.u.block0 + kb) * kTile + (lane & 7) * 16;
+        int page = -1;
+        if (j < end && j <= last) page = p.b.table[w.u.b * p.b.table_stride + j / p.page_size];
+        return page >= 0 && page < p.pages ? page : -1;
+      };
+      int page = page_of(w.k0);
+      for (int kb = w.k0; kb < w.k1; ++kb, ++blocks) {
+        const int now = page;
+        if (kb + 1 < w.k1) page = page_of(kb + 1);
+        const uint32_t bits = __ballot_sync(0xffffffffu, now >= 0 && lane < 8);
+        const int mine = __shfl_sync(0xffffffffu, now, box * (p.box / 16) & 7);
+        const int at = ((w.u.block0 + kb) * kTile + box * p.box) % p.page_size;
+        for (int v = 0; v < 2; ++v, ++tiles) {
+          const int s = tiles % C::stages;
+          if (tiles >= C::stages) {
+            ok = __all_sync(0xffffffffu, mbar_sleep(empty + s, (tiles / C::stages - 1) & 1));
+            if (!ok) break;
+          }
+          if (v == 0 && lane == 0) {
+            // (A free stage for these keys means that the block eight before
+            // them is done with.)
+            Info &f = infos[blocks % kInfo];
+            f.pages = bits;
+            f.bad[0] = f.bad[1] = f.bad[2] = f.bad[3] = 0;
+            mbar_arrive(known + blocks % kInfo);
+          }
+          if (lane == 0) mbar_arrive_expect_tx(full + s, C::tile);
+          __syncwarp();
+          if (copies)
+            tma_load_4d(smem + C::off_ring + s * C::tile + col * C::half + box * p.box * 128,
+                        v ? &p.tv : &p.tk, col * 64, at, w.head, mine, full + s);
+          __syncwarp();
+        }
+        if (!ok) break;
+      }
+    } while (ok && w.next());
+    if (!ok) {
+      if (lane == 0) record_fault(&g_fault_attn, kFaultAttnWait);
+      // Given up: the copies in flight land before the CTA leaves.
+      for (int i = max(0, tiles - C::stages); i < tiles; ++i)
+        mbar_sleep(full + i % C::stages, (i / C::stages) & 1);
+    }
+  } else if (warp == kMmaWarp) {
+    // ---- MMAs: the whole warp goes round, one elected lane issues --------------------
+    constexpr uint32_t kQk = idesc_bf16(kTile, false), kPv = idesc_bf16(D, true);
+    const uint64_t q_desc = smem_desc_sw128(smem_addr(smem));
+    const uint64_t k_desc = smem_desc_sw128(smem_addr(smem + C::off_ring));
+    const uint64_t v_desc = smem_desc_rows(smem_addr(smem + C::off_ring), C::half);
+    int tiles = 0, units0 = 0, units1 = 0, blocks0 = 0, blocks1 = 0;
+    bool ok = true;
+    auto wait = [&](uint64_t *bar, int parity) {
+      ok = ok && __all_sync(0xffffffffu, mbar_sleep(bar, parity & 1));
+    };
+    auto wait_tile = [&](int t) { wait(full + t % C::stages, t / C::stages); };
+    auto scores = [&](int i, int t, bool release) {  // S_i = Q_i K(t)^T
+      tc_fence_after();
+      if (ok && elect_one()) {
+        const uint64_t a = q_desc + i * (C::tile >> 4);
+        const uint64_t b = k_desc + (t % C::stages) * (C::tile >> 4);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint64_t step = (k / 4) * (C::half >> 4) + (k % 4) * 2;
+          umma_ss(tmem + i * kTile, a + step, b + step, kQk, k > 0);
+        }
+        umma_commit(sfull + i);
+        if (release) umma_commit(empty + t % C::stages);
+      }
+      __syncwarp();
+    };
+    auto values = [&](int i, int t, bool fresh, bool release) {  // O_i += P_i V(t)
+      tc_fence_after();
+      if (ok && elect_one()) {
+        const uint64_t b = v_desc + (t % C::stages) * (C::tile >> 4);
+#pragma unroll
+        for (int k = 0; k < kTile / 16; ++k)
+          umma_ts(tmem + 2 * kTile + i * kTile, tmem + i * kTile + k * 8, b + k * (2048 >> 4),
+                  kPv, !fresh || k > 0);
+        if (release) umma_commit(empty + t % C::stages);
+      }
+      __syncwarp();
+    };
+    do {
+      const bool two = w.two();
+      wait(qfull, units0++);
+      wait_tile(tiles);
+      scores(0, tiles, !two);
+      if (two) {
+        wait(qfull + 1, units1++);
+        scores(1, tiles, true);
+      }
+      for (int kb = w.k0; kb < w.k1; ++kb, tiles += 2) {
+        const bool more = kb + 1 < w.k1, fresh = kb == w.k0;
+        wait_tile(tiles + 1);
+        wait(pfull, blocks0++);
+        values(0, tiles + 1, fresh, !two);
+        if (more) {
+          wait_tile(tiles + 2);
+          scores(0, tiles + 2, !two);
+        } else if (ok && elect_one()) {
+          umma_commit(ofull);
+        }
+        __syncwarp();
+        if (two) {
+          wait(pfull + 1, blocks1++);
+          values(1, tiles + 1, fresh, true);
+          if (more)
+            scores(1, tiles + 2, true);
+          else if (ok && elect_one())
+            umma_commit(ofull + 1);
+          __syncwarp();
+        }
+        if (!ok) break;
+      }
+    } while (ok && w.next());
+    // Every MMA issued is complete before the tensor memory is released.
+    if (elect_one()) umma_commit(done);
+    __syncwarp();
+    if (!__all_sync(0xffffffffu, mbar_sleep(done, 0)) || !ok)
+      if (lane == 0) record_fault(&g_fault_attn, kFaultAttnWait);
+  } else {
+    // ---- softmax: a thread per row --------------------------------------------------
+    const int i = warp >> 2, r = (warp & 3) * 32 + lane;  // tile, row in it
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lanes + i * kTile, to = tmem + lanes + 2 * kTile + i * kTile;
+    int blocks = 0, mine = 0, units = 0, scans = 0;  // of the CTA; of this tile
+    bool ok = true, live;
+    int pos, row;
+    auto load_q = [&] {
+      // 16-byte piece c of row r lies at c ^ (r & 7) of the row's 128 bytes.
+      row = i * kTile + r;
+      const int64_t at = int64_t(w.u.tile) * kUnit + row;
+      const int tok = static_cast<int>(at / p.G);
+      live = at < int64_t(w.u.n) * p.G;
+      pos = live ? w.u.len - w.u.n + tok : -1;
+      const uint4 *src = reinterpret_cast<const uint4 *>(
+          static_cast<const uint16_t *>(p.q.p) + int64_t(w.u.t0 + tok) * p.q.ts +
+          (w.head * p.G + (at - int64_t(tok) * p.G)) * p.q.hs);
+      unsigned char *dst = smem + i * C::tile + r * 128;
+      const uint32_t flip = p.negative ? 0x80008000u : 0u;
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
+        uint4 v = live ? src[c] : make_uint4(0, 0, 0, 0);
+        v.x ^= flip;
+        v.y ^= flip;
+        v.z ^= flip;
+        v.w ^= flip;
+        *reinterpret_cast<uint4 *>(dst + (c / 8) * C::half + (((c % 8) ^ (r & 7)) << 4)) = v;
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(qfull + i);
+    };
+    do {
+      if (i == 1 && !w.two()) {
+        blocks += w.k1 - w.k0;
+        continue;
+      }
+      load_q();
+      const int top = last_pos(w.u, p.G), bottom = first_pos(w.u, p.G);
+      float m = -INFINITY, mc = 0.f, l = 0.f;  // maximum (of scores), times the scale; sum
+      for (int kb = w.k0; kb < w.k1 && ok; ++kb, ++blocks, ++mine) {
+        // (In this order: a tile that was left out of units is blocks ahead.)
+        ok = mbar_sleep(sfull + i, mine & 1) &&
+             mbar_sleep(known + blocks % kInfo, (blocks / kInfo) & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        float s[128];
+        tmem_ld128(ts, s);
+        Info &f = infos[blocks % kInfo];
+        const int j0 = (w.u.block0 + kb) * kTile;
+        const uint32_t have = f.pages;
+        // Masks, where some row of the unit does not attend some key (both
+        // tiles alike: they share what is done to the values).
+        if (have != 0xFFu || j0 + kTile - 1 > bottom ||
+            (p.window > 0 && j0 <= top - p.window)) {
+          // A masked value that is not finite would still make 0 * inf: such
+          // values become 0 here, and the rows that do attend the key NaN.
+          const int t = 2 * blocks + 1;
+          ok = __all_sync(0xffffffffu, mbar_sleep(full + t % C::stages, (t / C::stages) & 1));
+          unsigned char *v = smem + C::off_ring + (t % C::stages) * C::tile;
+          for (int c = tid & 127; ok && c < C::tile / 16; c += 128) {
+            uint4 x = *reinterpret_cast<const uint4 *>(v + c * 16);
+            auto over = [](uint32_t y) { return (y & 0x7F807F80u) + 0x00800080u; };
+            if ((over(x.x) | over(x.y) | over(x.z) | over(x.w)) & 0x80008000u) {
+              const int key = (c / 8) % kTile;
+              atomicOr(&f.bad[key >> 5], 1u << (key & 31));
+              __threadfence_block();
+              auto tidy = [&](uint32_t &y) {
+                if ((y & 0x7F80u) == 0x7F80u) y &= 0xFFFF0000u;
+                if ((y & 0x7F800000u) == 0x7F800000u) y &= 0xFFFFu;
+              };
+              tidy(x.x);
+              tidy(x.y);
+              tidy(x.z);
+              tidy(x.w);
+              *reinterpret_cast<uint4 *>(v + c * 16) = x;
+            }
+          }
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(scanned + i);
+          ok = __all_sync(0xffffffffu, ok && mbar_sleep(scanned + i, scans++ & 1));
+          if (!ok) break;
+          const volatile uint32_t *bad = f.bad;
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const uint32_t b = bad[g];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const int c = 32 * g + e, j = j0 + c;
+              const bool on = j <= pos && ((have >> (c >> 4)) & 1) &&
+                              (p.window == 0 || j > pos - p.window);
+              s[c] = on ? ((b >> e) & 1 ? NAN : s[c]) : -INFINITY;
+            }
+          }
+        }
+        float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int c = 4; c < 128; c += 4)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[c + e]);
+        const float top_s = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        const float new_m = fmaxf(m, top_s), new_mc = new_m == -INFINITY ? 0.f : new_m * p.scale;
+        // (Not for the difference of an infinity with itself.)
+        const bool grown = new_m > m && !(new_mc - mc <= kGrow && m != -INFINITY);
+        if (__any_sync(0xffffffffu, grown)) {
+          const float fac = m == -INFINITY ? 0.f : exp2_fast(grown ? mc - new_mc : 0.f);
+          if (grown) {
+            m = new_m;
+            mc = new_mc;
+          }
+          l *= fac;
+          if (kb > w.k0) {
+#pragma unroll
+            for (int c = 0; c < D; c += 32) {
+              float o[32];
+              tmem_ld32(to + c, o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] *= fac;
+              tmem_st32(to + c, o);
+            }
+          }
+        }
+        // Weights, rounded to bf16 (2^-8) for the product with the values; their
+        // sum takes them unrounded.
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c0 = 0; c0 < 128; c0 += 64) {
+          uint32_t x[32];
+#pragma unroll
+          for (int c = 0; c < 64; c += 2) {
+            const float a = exp2_fast(fmaf(s[c0 + c], p.scale, -mc));
+            const float b = exp2_fast(fmaf(s[c0 + c + 1], p.scale, -mc));
+            sum[c & 2] += a;
+            sum[(c & 2) + 1] += b;
+            x[c / 2] = f32x2_to_bf16x2(a, b);
+          }
+          tmem_st32(ts + c0 / 2, x);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(pfull + i);
+      }
+      if (ok) ok = mbar_sleep(ofull + i, units++ & 1);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      // ---- end of a piece
+      const bool whole = w.k0 == 0 && w.k1 == w.u.blocks;
+      if (whole) {
+        const int64_t at = int64_t(w.u.tile) * kUnit + row;
+        const int tok = static_cast<int>(at / p.G);
+        uint16_t *out = static_cast<uint16_t *>(p.o.p) + int64_t(w.u.t0 + tok) * p.o.ts +
+                        (w.head * p.G + (at - int64_t(tok) * p.G)) * p.o.hs;
+        const float inv = m == -INFINITY && l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+        for (int c = 0; c < D; c += 32) {
+          float o[32];
+          tmem_ld32(to + c, o);
+          if (live) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8)
+              *reinterpret_cast<uint4 *>(out + c + e) = make_uint4(
+                  f32x2_to_bf16x2(o[e] * inv, o[e + 1] * inv),
+                  f32x2_to_bf16x2(o[e + 2] * inv, o[e + 3] * inv),
+                  f32x2_to_bf16x2(o[e + 4] * inv, o[e + 5] * inv),
+                  f32x2_to_bf16x2(o[e + 6] * inv, o[e + 7] * inv));
+          }
+        }
+      } else {
+        float *part = p.parts + (int64_t(blockIdx.x) * 2 + (w.k0 == 0)) * (kUnit * (D + 2));
+#pragma unroll
+        for (int c = 0; c < D; c += 32) {
+          float o[32];
+          tmem_ld32(to + c, o);
+          if (live) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<float4 *>(part + row * D + c + e) =
+                  make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          }
+        }
+        part[kUnit * D + row] = m;
+        part[kUnit * D + kUnit + row] = l;
+      }
+      tc_fence_before();
+    } while (w.next());
+    if (!ok && lane == 0) record_fault(&g_fault_attn, kFaultAttnWait);
+  }
+  if (any && warp == kTmaWarp && lane == 0) {
+    // A unit that begins in this part and goes on past it: the CTAs after this
+    // one that have a piece of it. (After a wait that ran out the results mean
+    // nothing.)
+    int more = 0;
+    if (w.k0 == 0 && w.k1 < w.u.blocks) {
+      const int64_t end = w.x1 + w.u.blocks - w.k1;
+      more = static_cast<int>((end * w.parts - 1) / w.total) - static_cast<int>(blockIdx.x);
+      while ((blockIdx.x + more) * w.total / w.parts >= end) --more;
+      while (int64_t(blockIdx.x) + more + 1 < w.parts &&
+             (blockIdx.x + more + 1) * w.total / w.parts < end)
+        ++more;
+    }
+    header[0] = more;
+    header[1] = w.u.t0;
+    header[2] = w.u.n;
+    header[3] = w.head;
+    header[4] = w.u.tile;
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                 "r"(kTmemCols)
+                 : "memory");
+  }
+}
+
+// Joins the pieces of a unit: the one that begins at the end of CTA c's part
+// and the continuations at the start of the parts after it. A warp per row.
+template <int D>
+__global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ AttnTileParams p) {
+  constexpr int kPer = D / 32;
+  const int lane = threadIdx.x & 31;
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int *h = p.headers + blockIdx.x * kHeader;
+  const int more = h[0];
+  if (more == 0) return;
+  const int t0 = h[1], n = h[2], head = h[3], tile = h[4];
+  for (int row = blockIdx.y * 8 + (threadIdx.x >> 5); row < kUnit; row += gridDim.y * 8) {
+    const int64_t i = int64_t(tile) * kUnit + row;
+    if (i >= int64_t(n) * p.G) return;
+    const int tok = static_cast<int>(i / p.G);
+    constexpr int64_t kPart = kUnit * (D + 2);
+    const float *first = p.parts + (int64_t(blockIdx.x) * 2 + 1) * kPart;
+    const float *rest = p.parts + (int64_t(blockIdx.x) + 1) * 2 * kPart;
+    float m = -INFINITY;
+    for (int c = lane; c <= more; c += 32)
+      m = fmaxf(m, (c == 0 ? first : rest + (c - 1) * 2 * kPart)[kUnit * D + row]);
+#pragma unroll
+    for (int s = 1; s < 32; s *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
+    const float z = m == -INFINITY ? 0.f : m;
+    float l = 0.f, a[kPer];
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) a[e] = 0.f;
+#pragma unroll 4
+    for (int c = 0; c <= more; ++c) {
+      const float *x = c == 0 ? first : rest + (c - 1) * 2 * kPart;
+      const float f = exp2_fast((x[kUnit * D + row] - z) * p.scale);
+      l += f * x[kUnit * D + kUnit + row];
+      const float *v = x + row * D + lane * kPer;
+#pragma unroll
+      for (int e = 0; e < kPer; e += 2) {
+        const float2 y = *reinterpret_cast<const float2 *>(v + e);
+        a[e] += f * y.x;
+        a[e + 1] += f * y.y;
+      }
+    }
+    const float inv = m == -INFINITY && l == 0.f ? 0.f : 1.f / l;
+    uint16_t *out = static_cast<uint16_t *>(p.o.p) + int64_t(t0 + tok) * p.o.ts +
+                    (head * p.G + (i - int64_t(tok) * p.G)) * p.o.hs + lane * kPer;
+#pragma unroll
+    for (int e = 0; e < kPer; e += 2)
+      *reinterpret_cast<uint32_t *>(out + e) = f32x2_to_bf16x2(a[e] * inv, a[e + 1] * inv);
+  }
+}
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+struct Space {
+  int64_t *line, *first;
+  int4 *units;
+  int *headers;
+  float *parts;
+  size_t bytes;
+};
+Space space(unsigned char *ws, const AttnArgs &a) {
+  const int64_t G = a.q.n / a.c.heads;
+  const int64_t most = a.T * G / kUnit + std::min<int64_t>(a.b.n, a.T) + 1;
+  const size_t ctas = std::max(1, sm_count());
+  Space s{};
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    unsigned char *p = ws + at;
+    at += align256(n);
+    return p;
+  };
+  s.line = reinterpret_cast<int64_t *>(take(16));
+  s.headers = reinterpret_cast<int *>(take(ctas * kHeader * 4));
+  s.first = reinterpret_cast<int64_t *>(take(size_t(most + 1) * 8));
+  s.units = reinterpret_cast<int4 *>(take(size_t(most) * 32));
+  s.parts = reinterpret_cast<float *>(take(ctas * 2 * kUnit * (a.c.D + 2) * 4));
+  s.bytes = at;
+  return s;
+}
+
+template <int D>
+cudaError_t run(const AttnTileParams &p, bool pdl, cudaStream_t stream) {
+  constexpr int kSmem = Cfg<D>::total + 1024;
+  static std::atomic<unsigned long long> done{0};
+  cudaError_t e = ensure_smem_limit(tile_kernel<D>, kSmem, done);
+  if (e != cudaSuccess) return e;
+  const int ctas = std::max(1, sm_count());
+  e = launch_after(plan_kernel, dim3(1), kPlanThreads, 0, pdl, stream, p);
+  if (e == cudaSuccess)
+    e = launch_after(tile_kernel<D>, dim3(ctas), kThreads, kSmem, pdl, stream, p);
+  if (e == cudaSuccess)
+    e = launch_after(combine_kernel<D>, dim3(ctas, kUnit / 16), 256, 0, pdl, stream, p);
+  return e;
+}
+
+}  // namespace
+
+bool tile_path(const AttnArgs &a) {
+  if (a.f32) return false;
+  // What a tensor map can describe.
+  for (int64_t s : {a.c.k.ps, a.c.k.hs, a.c.k.ts, a.c.v.ps, a.c.v.hs, a.c.v.ts})
+    if (s * 2 >= int64_t(1) << 40) return false;
+  const int64_t G = a.q.n / a.c.heads;
+  return a.T * G > 16 * std::min<int64_t>(a.b.n, a.T);
+}
+
+size_t tile_workspace_bytes(const AttnArgs &a) { return space(nullptr, a).bytes; }
+
+cudaError_t launch_attn_tile(const AttnArgs &a, cudaStream_t stream) {
+  AttnTileParams p{};
+  p.box = 128;
+  while (a.c.page_size % p.box) p.box /= 2;
+  for (int v = 0; v < 2; ++v) {
+    const Pages &pg = v ? a.c.v : a.c.k;
+    const uint64_t dims[4] = {uint64_t(a.c.D), uint64_t(a.c.page_size), uint64_t(a.c.heads),
+                              uint64_t(a.c.pages)};
+    const uint64_t strides[3] = {uint64_t(pg.ts) * 2, uint64_t(pg.hs) * 2, uint64_t(pg.ps) * 2};
+    const uint32_t box[4] = {64, uint32_t(p.box), 1, 1};
+    const cudaError_t e = make_tmap(v ? &p.tv : &p.tk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, pg.p,
+                                    dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (e != cudaSuccess) return e;
+  }
+  p.q = a.q;
+  p.o = a.o;
+  p.b = a.b;
+  p.pages = static_cast<int>(a.c.pages);
+  p.page_size = a.c.page_size;
+  p.kv_heads = a.c.heads;
+  p.G = a.q.n / a.c.heads;
+  p.T = static_cast<int>(a.T);
+  p.cap = static_cast<int>(int64_t(a.b.table_pages) * a.c.page_size);
+  p.window = static_cast<int>(std::min<int64_t>(a.window, p.cap));
+  p.scale = static_cast<float>(
+      std::min(std::max(std::fabs(static_cast<double>(a.scale)) * M_LOG2E, 1e-37), 3e38));
+  p.negative = a.scale < 0.f;
+  const Space s = space(a.ws, a);
+  p.line = s.line;
+  p.first = s.first;
+  p.units = s.units;
+  p.headers = s.headers;
+  p.parts = s.parts;
+  return a.c.D == 64 ? run<64>(p, a.pdl, stream) : run<128>(p, a.pdl, stream);
+}
+
+cudaError_t attn_take_fault(unsigned int *out) {
+  cudaError_t e = cudaMemcpyFromSymbol(out, g_fault_attn, sizeof(unsigned int));
+  if (e != cudaSuccess) return e;
+  const unsigned int zero = 0;
+  return cudaMemcpyToSymbol(g_fault_attn, &zero, sizeof zero);
+}
+
+}  // namespace mnb

@@ -238,5 +238,6 @@ constexpr unsigned int kFaultGemvWait = 1u;
 constexpr unsigned int kFaultGemmWait = 2u;
 constexpr unsigned int kFaultChainWait = 4u;
 constexpr unsigned int kFaultMoeWait = 8u;
+constexpr unsigned int kFaultAttnWait = 16u;
 
 }  // namespace mnb
