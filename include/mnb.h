@@ -1040,8 +1040,8 @@ MNB_API mnb_status mnb_cache_append(const mnb_heads *q, const mnb_heads *k, cons
  * non-finite (not always as an exact sum would be), and no other.
  * Results are bitwise reproducible for the same arrays, T and GPU.
  * Errors: as mnb_cache_append, and MNB_ERR_SHAPE for q->heads not a multiple
- * of cache->heads, a scale that is not finite, window < 0 or a workspace too
- * small; MNB_ERR_UNSUPPORTED for head_dim other than 64 and 128;
+ * of cache->heads, T * (q->heads / cache->heads) near 2^31, a scale that is not
+ * finite, window < 0 or a workspace too small; MNB_ERR_UNSUPPORTED for head_dim other than 64 and 128;
  * MNB_ERR_ALIGN for rows of q, out or the cache off 16 bytes (pointers and
  * strides), or the workspace; MNB_ERR_ALIAS for an output or the workspace
  * over another buffer.

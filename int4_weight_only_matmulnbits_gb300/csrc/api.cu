@@ -681,8 +681,10 @@ mnb_status check_out_rows(const mnb_heads &out, const mnb_heads &own, const mnb_
   return MNB_OK;
 }
 
-mnb_status check_attention(const mnb_kv_cache &c, int q_heads) {
+mnb_status check_attention(const mnb_kv_cache &c, int64_t T, int q_heads) {
   if (q_heads < 1 || q_heads % c.heads) return MNB_ERR_SHAPE;
+  // Rows of a key head, padded to whole units, are counted in 32 bits.
+  if (T > (kMaxDim - 1024) / (q_heads / c.heads)) return MNB_ERR_SHAPE;
   if (c.head_dim != 64 && c.head_dim != 128) {
     std::snprintf(g_last_error, sizeof g_last_error,
                   "attention takes head_dim 64 or 128, not %d", c.head_dim);
@@ -1921,7 +1923,7 @@ mnb_status mnb_cache_append(const mnb_heads *q, const mnb_heads *k, const mnb_he
 size_t mnb_paged_attention_workspace_size(int64_t T, int q_heads, const mnb_kv_cache *cache,
                                           const mnb_kv_batch *batch) {
   if (!cache || !batch || check_rows(T) != MNB_OK || check_cache(*cache) != MNB_OK ||
-      check_batch(*batch, *cache) != MNB_OK || check_attention(*cache, q_heads) != MNB_OK)
+      check_batch(*batch, *cache) != MNB_OK || check_attention(*cache, T, q_heads) != MNB_OK)
     return 0;
   return attn_workspace_bytes(attn_args(T, q_heads, *cache, *batch));
 }
@@ -1941,7 +1943,7 @@ mnb_status mnb_paged_attention(const mnb_heads *q, int64_t T, const mnb_kv_cache
   if (st == MNB_OK) st = check_heads(*out, T, D, es, true);
   if (st == MNB_OK && (!std::isfinite(scale) || window < 0 || out->heads != q->heads))
     st = MNB_ERR_SHAPE;
-  if (st == MNB_OK) st = check_attention(*cache, q->heads);
+  if (st == MNB_OK) st = check_attention(*cache, T, q->heads);
   if (st != MNB_OK) return st;
   const int64_t lane = 16 / static_cast<int64_t>(es);
   for (const mnb_heads *h : {q, out})

@@ -45,7 +45,10 @@ constexpr int kTile = 128;                 // rows of an MMA, keys of a block
 constexpr int kUnit = 2 * kTile;           // rows of a unit
 constexpr int kSoftWarps = 8;              // two tiles of four warps
 constexpr int kTmaWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;
-constexpr int kThreads = 32 * (kSoftWarps + 2);
+constexpr int kThreads = 32 * (kSoftWarps + 4);  // a third group of four, two of them idle
+// Registers: of the 3 x 168 a lane that the launch has, the softmax takes more.
+constexpr int kSoftRegs = 216, kOtherRegs = 72;
+static_assert(2 * kSoftRegs + kOtherRegs <= 3 * 168, "within the launch's registers");
 constexpr int kInfo = 8;                   // blocks whose key masks are kept
 constexpr int kTmemCols = 512;
 constexpr int kHeader = 8;                 // ints
@@ -92,6 +95,11 @@ __device__ __forceinline__ bool elect_one() {
       "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok));
   return ok != 0;
+}
+__device__ __forceinline__ void cp16_or_zero(uint32_t dst, const void *src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(there ? 16 : 0)
+               : "memory");
 }
 __device__ __forceinline__ void tma_load_4d(void *dst, const void *tmap, int x, int y, int z,
                                             int w, uint64_t *bar) {
@@ -140,40 +148,28 @@ __device__ __forceinline__ uint64_t smem_desc_rows(uint32_t addr, uint32_t half)
   d |= static_cast<uint64_t>(2) << 61;
   return d;
 }
-// 128 consecutive fp32 columns of this thread's TMEM lane.
-__device__ __forceinline__ void tmem_ld128(uint32_t taddr, float (&v)[128]) {
-  uint32_t r[128];
+// 32 consecutive fp32 columns of this thread's TMEM lane, without waiting for
+// them; and the wait, which hands the registers on.
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, float (&v)[32]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x128.b32 "
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
       "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
-      "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
-      "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63, "
-      "%64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, "
-      "%80, %81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95, "
-      "%96, %97, %98, %99, %100, %101, %102, %103, %104, %105, %106, %107, %108, %109, %110, %111, "
-      "%112, %113, %114, %115, %116, %117, %118, %119, %120, %121, %122, %123, %124, %125, %126, %127}, [%128];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
-        "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
-        "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
-        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
-        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63]),
-        "=r"(r[64]), "=r"(r[65]), "=r"(r[66]), "=r"(r[67]), "=r"(r[68]), "=r"(r[69]), "=r"(r[70]), "=r"(r[71]),
-        "=r"(r[72]), "=r"(r[73]), "=r"(r[74]), "=r"(r[75]), "=r"(r[76]), "=r"(r[77]), "=r"(r[78]), "=r"(r[79]),
-        "=r"(r[80]), "=r"(r[81]), "=r"(r[82]), "=r"(r[83]), "=r"(r[84]), "=r"(r[85]), "=r"(r[86]), "=r"(r[87]),
-        "=r"(r[88]), "=r"(r[89]), "=r"(r[90]), "=r"(r[91]), "=r"(r[92]), "=r"(r[93]), "=r"(r[94]), "=r"(r[95]),
-        "=r"(r[96]), "=r"(r[97]), "=r"(r[98]), "=r"(r[99]), "=r"(r[100]), "=r"(r[101]), "=r"(r[102]), "=r"(r[103]),
-        "=r"(r[104]), "=r"(r[105]), "=r"(r[106]), "=r"(r[107]), "=r"(r[108]), "=r"(r[109]), "=r"(r[110]), "=r"(r[111]),
-        "=r"(r[112]), "=r"(r[113]), "=r"(r[114]), "=r"(r[115]), "=r"(r[116]), "=r"(r[117]), "=r"(r[118]), "=r"(r[119]),
-        "=r"(r[120]), "=r"(r[121]), "=r"(r[122]), "=r"(r[123]), "=r"(r[124]), "=r"(r[125]), "=r"(r[126]), "=r"(r[127])
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+        "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
+        "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
+        "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
       : "r"(taddr)
       : "memory");
-#pragma unroll
-  for (int i = 0; i < 128; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_ld_wait(float (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]),
+                 "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]),
+                 "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31])
+               :
+               : "memory");
 }
 // 32 consecutive 32-bit columns of this thread's TMEM lane.
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
@@ -195,8 +191,37 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) 
   for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(v[i]);
   tmem_st32(taddr, r);
 }
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
+      :
+      : "r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+// Two fp32 numbers at a time.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t r, float &a, float &b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
@@ -213,14 +238,13 @@ struct Unit {
 };
 
 __device__ __forceinline__ int units_of(const Seq &s, int G) {
-  return static_cast<int>((int64_t(s.n) * G + kUnit - 1) / kUnit);
+  return (s.n * G + kUnit - 1) / kUnit;
 }
 __device__ __forceinline__ int first_pos(const Unit &u, int G) {
-  return u.len - u.n + static_cast<int>(int64_t(u.tile) * kUnit / G);
+  return u.len - u.n + u.tile * kUnit / G;
 }
 __device__ __forceinline__ int last_pos(const Unit &u, int G) {
-  return u.len - u.n +
-         static_cast<int>(min(int64_t(u.n) - 1, (int64_t(u.tile) * kUnit + kUnit - 1) / G));
+  return u.len - u.n + min(u.n - 1, (u.tile * kUnit + kUnit - 1) / G);
 }
 
 // Inclusive sums over the block's threads.
@@ -294,17 +318,21 @@ __global__ void __launch_bounds__(kPlanThreads)
   }
 }
 
-// A CTA's part of the line, piece by piece.
+// A CTA's part of the line, piece by piece; the unit after the present one is
+// loaded ahead.
 struct Walk {
   const AttnTileParams &p;
   int64_t x, x1, total;
   int parts, n_units, unit, head, k0, k1;
-  Unit u;
+  Unit u, after;
   __device__ __forceinline__ explicit Walk(const AttnTileParams &p_) : p(p_) {}
-  __device__ __forceinline__ void load() {
-    const int4 a = p.units[2 * unit], b = p.units[2 * unit + 1];
-    u = Unit{a.x, a.y, a.z, a.w, b.x, b.y, b.z};
+  __device__ __forceinline__ Unit load(int i) const {
+    const int4 a = p.units[2 * i], b = p.units[2 * i + 1];
+    return Unit{a.x, a.y, a.z, a.w, b.x, b.y, b.z};
+  }
+  __device__ __forceinline__ void enter() {
     k1 = static_cast<int>(min(int64_t(u.blocks), x1 - x + k0));
+    if (more()) after = load(unit + 1 == n_units ? 0 : unit + 1);
   }
   // Whole warps; false: nothing for this CTA.
   __device__ __forceinline__ bool start(int lane) {
@@ -326,22 +354,26 @@ struct Walk {
     }
     unit = lo;
     k0 = static_cast<int>(in - p.first[unit]);
-    load();
+    u = load(unit);
+    enter();
     return true;
   }
+  // Another piece follows.
+  __device__ __forceinline__ bool more() const { return x + (k1 - k0) < x1; }
+  __device__ __forceinline__ int next_head() const { return unit + 1 == n_units ? head + 1 : head; }
   __device__ __forceinline__ bool next() {
+    if (!more()) return false;
     x += k1 - k0;
-    if (x >= x1) return false;
     k0 = 0;
-    if (++unit == n_units) {
-      unit = 0;
-      ++head;
-    }
-    load();
+    head = next_head();
+    unit = unit + 1 == n_units ? 0 : unit + 1;
+    u = after;
+    enter();
     return true;
   }
-  __device__ __forceinline__ bool two() const {
-    return int64_t(u.n) * p.G > int64_t(u.tile) * kUnit + kTile;
+  // The unit has rows in its second tile.
+  __device__ __forceinline__ bool two(const Unit &v) const {
+    return v.n * p.G > v.tile * kUnit + kTile;
   }
 };
 
@@ -360,9 +392,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *qfull = pfull + 2;
   uint64_t *ofull = qfull + 2;
   uint64_t *scanned = ofull + 2;        // a tile's warps have looked over the values
-  uint64_t *done = scanned + 2;
+  uint64_t *phalf = scanned + 2;        // the weights of the first 64 keys
+  uint64_t *done = phalf + 2;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
-  static_assert((2 * C::stages + kInfo + 11) * 8 + 4 <= 512, "barriers");
+  static_assert((2 * C::stages + kInfo + 13) * 8 + 4 <= 512, "barriers");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
@@ -373,6 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kInfo; ++i) mbar_init(known + i, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(sfull + i, 1);
+      mbar_init(phalf + i, 4);
       mbar_init(pfull + i, 4);
       mbar_init(qfull + i, 4);
       mbar_init(ofull + i, 1);
@@ -398,330 +432,433 @@ __global__ void __launch_bounds__(kThreads, 1)
   Walk w(p);
   const bool any = w.start(lane);
   int *header = p.headers + blockIdx.x * kHeader;
-  if (!any) {
-    if (tid == 0) header[0] = 0;
-  } else if (warp == kTmaWarp) {
-    // ---- keys and values ----------------------------------------------------------
-    const int nbox = kTile / p.box;  // copies of 64 columns: nbox for each half
-    const int box = lane % nbox, col = lane / nbox;
-    const bool copies = lane < nbox * (D / 64);
-    int tiles = 0, blocks = 0;
-    bool ok = true;
-    do {
-      const int last = last_pos(w.u, p.G), end = min(w.u.len, p.cap);
-      // Lane g < 8: the page of the keys 16 g on of the next block.
-      auto page_of = [&](int kb) {
-        const int j = (w.u.block0 + kb) * kTile + (lane & 7) * 16;
-        int page = -1;
-        if (j < end && j <= last) page = p.b.table[w.u.b * p.b.table_stride + j / p.page_size];
-        return page >= 0 && page < p.pages ? page : -1;
+  if (!any && tid == 0) header[0] = 0;
+  if (warp >= kSoftWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (any && warp == kTmaWarp) {
+      // ---- keys and values ----------------------------------------------------------
+      const int nbox = kTile / p.box;  // copies of 64 columns: nbox for each half
+      const int box = lane % nbox, col = lane / nbox;
+      const bool copies = lane < nbox * (D / 64);
+      int tiles = 0, blocks = 0;
+      bool ok = true;
+      do {
+        const int last = last_pos(w.u, p.G), end = min(w.u.len, p.cap);
+        // Lane g < 8: the page of the keys 16 g on of the next block.
+        auto page_of = [&](int kb) {
+          const int j = (w.u.block0 + kb) * kTile + (lane & 7) * 16;
+          int page = -1;
+          if (j < end && j <= last) page = p.b.table[w.u.b * p.b.table_stride + j / p.page_size];
+          return page >= 0 && page < p.pages ? page : -1;
+        };
+        int page = page_of(w.k0);
+        for (int kb = w.k0; kb < w.k1; ++kb, ++blocks) {
+          const int now = page;
+          if (kb + 1 < w.k1) page = page_of(kb + 1);
+          const uint32_t bits = __ballot_sync(0xffffffffu, now >= 0 && lane < 8);
+          const int mine = __shfl_sync(0xffffffffu, now, box * (p.box / 16) & 7);
+          const int at = ((w.u.block0 + kb) * kTile + box * p.box) % p.page_size;
+          for (int v = 0; v < 2; ++v, ++tiles) {
+            const int s = tiles % C::stages;
+            if (tiles >= C::stages) {
+              ok = __all_sync(0xffffffffu, mbar_sleep(empty + s, (tiles / C::stages - 1) & 1));
+              if (!ok) break;
+            }
+            if (v == 0 && lane == 0) {
+              // (A free stage for these keys means that the block eight before
+              // them is done with.)
+              Info &f = infos[blocks % kInfo];
+              f.pages = bits;
+              f.bad[0] = f.bad[1] = f.bad[2] = f.bad[3] = 0;
+              mbar_arrive(known + blocks % kInfo);
+            }
+            if (lane == 0) mbar_arrive_expect_tx(full + s, C::tile);
+            __syncwarp();
+            if (copies)
+              tma_load_4d(smem + C::off_ring + s * C::tile + col * C::half + box * p.box * 128,
+                          v ? &p.tv : &p.tk, col * 64, at, w.head, mine, full + s);
+            __syncwarp();
+          }
+          if (!ok) break;
+        }
+      } while (ok && w.next());
+      if (!ok) {
+        if (lane == 0) record_fault(&g_fault_attn, kFaultAttnWait);
+        // Given up: the copies in flight land before the CTA leaves.
+        for (int i = max(0, tiles - C::stages); i < tiles; ++i)
+          mbar_sleep(full + i % C::stages, (i / C::stages) & 1);
+      }
+    } else if (any && warp == kMmaWarp) {
+      // ---- MMAs: the whole warp goes round, one elected lane issues ------------------
+      // What decides the way and the operands is taken from lane 0, so that it
+      // stays in uniform registers: moving it there for each MMA took as long
+      // as an MMA and a half.
+      auto uniform = [](uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); };
+      const uint32_t tm = uniform(tmem);
+      // A negative scale: Q counts negated.
+      const uint32_t qk = idesc_bf16(kTile, false) | (p.negative ? 1u << 13 : 0u);
+      constexpr uint32_t kPv = idesc_bf16(D, true);
+      const uint64_t q_desc = smem_desc_sw128(smem_addr(smem));
+      const uint64_t k_desc = smem_desc_sw128(smem_addr(smem + C::off_ring));
+      const uint64_t v_desc = smem_desc_rows(smem_addr(smem + C::off_ring), C::half);
+      int next = 0, phase = 0, units0 = 0, units1 = 0, blocks0 = 0, blocks1 = 0;
+      bool ok = true;
+      auto wait = [&](uint64_t *bar, int parity) {
+        ok = __all_sync(0xffffffffu, ok && mbar_sleep(bar, parity & 1));
       };
-      int page = page_of(w.k0);
-      for (int kb = w.k0; kb < w.k1; ++kb, ++blocks) {
-        const int now = page;
-        if (kb + 1 < w.k1) page = page_of(kb + 1);
-        const uint32_t bits = __ballot_sync(0xffffffffu, now >= 0 && lane < 8);
-        const int mine = __shfl_sync(0xffffffffu, now, box * (p.box / 16) & 7);
-        const int at = ((w.u.block0 + kb) * kTile + box * p.box) % p.page_size;
-        for (int v = 0; v < 2; ++v, ++tiles) {
-          const int s = tiles % C::stages;
-          if (tiles >= C::stages) {
-            ok = __all_sync(0xffffffffu, mbar_sleep(empty + s, (tiles / C::stages - 1) & 1));
-            if (!ok) break;
-          }
-          if (v == 0 && lane == 0) {
-            // (A free stage for these keys means that the block eight before
-            // them is done with.)
-            Info &f = infos[blocks % kInfo];
-            f.pages = bits;
-            f.bad[0] = f.bad[1] = f.bad[2] = f.bad[3] = 0;
-            mbar_arrive(known + blocks % kInfo);
-          }
-          if (lane == 0) mbar_arrive_expect_tx(full + s, C::tile);
-          __syncwarp();
-          if (copies)
-            tma_load_4d(smem + C::off_ring + s * C::tile + col * C::half + box * p.box * 128,
-                        v ? &p.tv : &p.tk, col * 64, at, w.head, mine, full + s);
-          __syncwarp();
+      auto take = [&] {  // the stage of the next tile of keys or values
+        wait(full + next, phase);
+        const int s = next;
+        if (++next == C::stages) {
+          next = 0;
+          phase ^= 1;
         }
-        if (!ok) break;
-      }
-    } while (ok && w.next());
-    if (!ok) {
-      if (lane == 0) record_fault(&g_fault_attn, kFaultAttnWait);
-      // Given up: the copies in flight land before the CTA leaves.
-      for (int i = max(0, tiles - C::stages); i < tiles; ++i)
-        mbar_sleep(full + i % C::stages, (i / C::stages) & 1);
-    }
-  } else if (warp == kMmaWarp) {
-    // ---- MMAs: the whole warp goes round, one elected lane issues --------------------
-    constexpr uint32_t kQk = idesc_bf16(kTile, false), kPv = idesc_bf16(D, true);
-    const uint64_t q_desc = smem_desc_sw128(smem_addr(smem));
-    const uint64_t k_desc = smem_desc_sw128(smem_addr(smem + C::off_ring));
-    const uint64_t v_desc = smem_desc_rows(smem_addr(smem + C::off_ring), C::half);
-    int tiles = 0, units0 = 0, units1 = 0, blocks0 = 0, blocks1 = 0;
-    bool ok = true;
-    auto wait = [&](uint64_t *bar, int parity) {
-      ok = ok && __all_sync(0xffffffffu, mbar_sleep(bar, parity & 1));
-    };
-    auto wait_tile = [&](int t) { wait(full + t % C::stages, t / C::stages); };
-    auto scores = [&](int i, int t, bool release) {  // S_i = Q_i K(t)^T
-      tc_fence_after();
-      if (ok && elect_one()) {
-        const uint64_t a = q_desc + i * (C::tile >> 4);
-        const uint64_t b = k_desc + (t % C::stages) * (C::tile >> 4);
+        return s;
+      };
+      auto scores = [&](int i, int s, bool release) {  // S_i = Q_i K^T
+        tc_fence_after();
+        const uint64_t a = q_desc + i * (C::tile >> 4), b = k_desc + s * (C::tile >> 4);
+        if (ok && elect_one()) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint64_t step = (k / 4) * (C::half >> 4) + (k % 4) * 2;
-          umma_ss(tmem + i * kTile, a + step, b + step, kQk, k > 0);
-        }
-        umma_commit(sfull + i);
-        if (release) umma_commit(empty + t % C::stages);
-      }
-      __syncwarp();
-    };
-    auto values = [&](int i, int t, bool fresh, bool release) {  // O_i += P_i V(t)
-      tc_fence_after();
-      if (ok && elect_one()) {
-        const uint64_t b = v_desc + (t % C::stages) * (C::tile >> 4);
-#pragma unroll
-        for (int k = 0; k < kTile / 16; ++k)
-          umma_ts(tmem + 2 * kTile + i * kTile, tmem + i * kTile + k * 8, b + k * (2048 >> 4),
-                  kPv, !fresh || k > 0);
-        if (release) umma_commit(empty + t % C::stages);
-      }
-      __syncwarp();
-    };
-    do {
-      const bool two = w.two();
-      wait(qfull, units0++);
-      wait_tile(tiles);
-      scores(0, tiles, !two);
-      if (two) {
-        wait(qfull + 1, units1++);
-        scores(1, tiles, true);
-      }
-      for (int kb = w.k0; kb < w.k1; ++kb, tiles += 2) {
-        const bool more = kb + 1 < w.k1, fresh = kb == w.k0;
-        wait_tile(tiles + 1);
-        wait(pfull, blocks0++);
-        values(0, tiles + 1, fresh, !two);
-        if (more) {
-          wait_tile(tiles + 2);
-          scores(0, tiles + 2, !two);
-        } else if (ok && elect_one()) {
-          umma_commit(ofull);
+          for (int k = 0; k < D / 16; ++k) {
+            const uint64_t step = (k / 4) * (C::half >> 4) + (k % 4) * 2;
+            umma_ss(tm + i * kTile, a + step, b + step, qk, k > 0);
+          }
+          umma_commit(sfull + i);
+          if (release) umma_commit(empty + s);
         }
         __syncwarp();
-        if (two) {
-          wait(pfull + 1, blocks1++);
-          values(1, tiles + 1, fresh, true);
-          if (more)
-            scores(1, tiles + 2, true);
-          else if (ok && elect_one())
-            umma_commit(ofull + 1);
-          __syncwarp();
-        }
-        if (!ok) break;
-      }
-    } while (ok && w.next());
-    // Every MMA issued is complete before the tensor memory is released.
-    if (elect_one()) umma_commit(done);
-    __syncwarp();
-    if (!__all_sync(0xffffffffu, mbar_sleep(done, 0)) || !ok)
-      if (lane == 0) record_fault(&g_fault_attn, kFaultAttnWait);
-  } else {
-    // ---- softmax: a thread per row --------------------------------------------------
-    const int i = warp >> 2, r = (warp & 3) * 32 + lane;  // tile, row in it
-    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + lanes + i * kTile, to = tmem + lanes + 2 * kTile + i * kTile;
-    int blocks = 0, mine = 0, units = 0, scans = 0;  // of the CTA; of this tile
-    bool ok = true, live;
-    int pos, row;
-    auto load_q = [&] {
-      // 16-byte piece c of row r lies at c ^ (r & 7) of the row's 128 bytes.
-      row = i * kTile + r;
-      const int64_t at = int64_t(w.u.tile) * kUnit + row;
-      const int tok = static_cast<int>(at / p.G);
-      live = at < int64_t(w.u.n) * p.G;
-      pos = live ? w.u.len - w.u.n + tok : -1;
-      const uint4 *src = reinterpret_cast<const uint4 *>(
-          static_cast<const uint16_t *>(p.q.p) + int64_t(w.u.t0 + tok) * p.q.ts +
-          (w.head * p.G + (at - int64_t(tok) * p.G)) * p.q.hs);
-      unsigned char *dst = smem + i * C::tile + r * 128;
-      const uint32_t flip = p.negative ? 0x80008000u : 0u;
+      };
+      // O_i += P_i V, for the tile's block n; the first half of the keys while the
+      // weights of the second are made.
+      auto values = [&](int i, int s, int n, bool fresh, bool release) {
+        wait(phalf + i, n);
+        tc_fence_after();
+        const uint64_t b = v_desc + s * (C::tile >> 4);
+        if (ok && elect_one()) {
+          umma_ts(tm + 2 * kTile + i * kTile, tm + i * kTile, b, kPv, !fresh);
 #pragma unroll
-      for (int c = 0; c < D / 8; ++c) {
-        uint4 v = live ? src[c] : make_uint4(0, 0, 0, 0);
-        v.x ^= flip;
-        v.y ^= flip;
-        v.z ^= flip;
-        v.w ^= flip;
-        *reinterpret_cast<uint4 *>(dst + (c / 8) * C::half + (((c % 8) ^ (r & 7)) << 4)) = v;
-      }
-      fence_async_smem();
+          for (int k = 1; k < kTile / 32; ++k)
+            umma_ts(tm + 2 * kTile + i * kTile, tm + i * kTile + k * 8, b + k * (2048 >> 4), kPv, 1);
+        }
+        __syncwarp();
+        wait(pfull + i, n);
+        tc_fence_after();
+        if (ok && elect_one()) {
+#pragma unroll
+          for (int k = kTile / 32; k < kTile / 16; ++k)
+            umma_ts(tm + 2 * kTile + i * kTile, tm + i * kTile + k * 8, b + k * (2048 >> 4), kPv, 1);
+          if (release) umma_commit(empty + s);
+        }
+        __syncwarp();
+      };
+      bool again;
+      do {
+        const bool two = uniform(w.two(w.u));
+        const int n = uniform(w.k1 - w.k0);
+        again = uniform(w.next());
+        wait(qfull, units0++);
+        int ks = take();
+        scores(0, ks, !two);
+        if (two) {
+          wait(qfull + 1, units1++);
+          scores(1, ks, true);
+        }
+        for (int kb = 0; kb < n && ok; ++kb) {
+          const bool more = kb + 1 < n;
+          const int vs = take();
+          values(0, vs, blocks0++, kb == 0, !two);
+          if (more) {
+            ks = take();
+            scores(0, ks, !two);
+          } else {
+            if (ok && elect_one()) umma_commit(ofull);
+            __syncwarp();
+          }
+          if (two) {
+            values(1, vs, blocks1++, kb == 0, true);
+            if (more) {
+              scores(1, ks, true);
+            } else {
+              if (ok && elect_one()) umma_commit(ofull + 1);
+              __syncwarp();
+            }
+          }
+        }
+      } while (ok && again);
+      // Every MMA issued is complete before the tensor memory is released.
+      if (elect_one()) umma_commit(done);
       __syncwarp();
-      if (lane == 0) mbar_arrive(qfull + i);
-    };
-    do {
-      if (i == 1 && !w.two()) {
-        blocks += w.k1 - w.k0;
-        continue;
-      }
-      load_q();
-      const int top = last_pos(w.u, p.G), bottom = first_pos(w.u, p.G);
-      float m = -INFINITY, mc = 0.f, l = 0.f;  // maximum (of scores), times the scale; sum
-      for (int kb = w.k0; kb < w.k1 && ok; ++kb, ++blocks, ++mine) {
-        // (In this order: a tile that was left out of units is blocks ahead.)
-        ok = mbar_sleep(sfull + i, mine & 1) &&
-             mbar_sleep(known + blocks % kInfo, (blocks / kInfo) & 1);
+      if (!__all_sync(0xffffffffu, mbar_sleep(done, 0)) || !ok)
+        if (lane == 0) record_fault(&g_fault_attn, kFaultAttnWait);
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+    if (any) {
+      // ---- softmax: a thread per row ------------------------------------------------
+      const int i = warp >> 2, r = (warp & 3) * 32 + lane;  // tile, row in it
+      const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+      const uint32_t ts = tmem + lanes + i * kTile, to = tmem + lanes + 2 * kTile + i * kTile;
+      int blocks = 0, mine = 0, units = 0, scans = 0;  // of the CTA; of this tile
+      bool ok = true, started = false;  // started: the unit's rows are on their way
+      const int row = i * kTile + r;  // in the unit
+      // Starts the copies of a unit's row into this tile's place, and tells the
+      // MMAs when they are there. 16-byte piece c of row r lies at c ^ (r & 7) of
+      // the row's 128 bytes.
+      auto fetch_q = [&](const Unit &u, int head) {
+        const int at = u.tile * kUnit + row, tok = at / p.G;
+        const bool live = at < u.n * p.G;
+        const uint16_t *src = static_cast<const uint16_t *>(p.q.p);
+        if (live)
+          src += int64_t(u.t0 + tok) * p.q.ts + int64_t(head * p.G + at - tok * p.G) * p.q.hs;
+        const uint32_t dst = smem_addr(smem + i * C::tile + r * 128);
+#pragma unroll 4
+        for (int c = 0; c < D / 8; ++c)
+          cp16_or_zero(dst + (c / 8) * C::half + (((c % 8) ^ (r & 7)) << 4), src + (live ? c * 8 : 0),
+                       live);
+      };
+      auto pass_q = [&] {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(qfull + i);
+      };
+      do {
+        if (i == 1 && !w.two(w.u)) {
+          blocks += w.k1 - w.k0;
+          continue;
+        }
+        if (!started) {  // else they came with the unit before
+          fetch_q(w.u, w.head);
+          pass_q();
+        }
+        const int at = w.u.tile * kUnit + row, tok = at / p.G;
+        const bool live = at < w.u.n * p.G;
+        const int pos = live ? w.u.len - w.u.n + tok : -1;
+        const int top = last_pos(w.u, p.G), bottom = first_pos(w.u, p.G);
+        float m = -INFINITY, mc = 0.f, l = 0.f;  // maximum (of scores), times the scale; sum
+        for (int kb = w.k0; kb < w.k1 && ok; ++kb, ++blocks, ++mine) {
+          // (In this order: a tile that was left out of units is blocks ahead.)
+          ok = mbar_sleep(sfull + i, mine & 1) &&
+               mbar_sleep(known + blocks % kInfo, (blocks / kInfo) & 1);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
+          // S of the last block is there: Q's place is free for the next unit.
+          const bool ahead = kb + 1 == w.k1 && w.more() && (i == 0 || w.two(w.after));
+          if (ahead) fetch_q(w.after, w.next_head());
+          Info &f = infos[blocks % kInfo];
+          const int j0 = (w.u.block0 + kb) * kTile;
+          const uint32_t have = f.pages;
+          // Masks, where some row of the unit does not attend some key (both
+          // tiles alike: they share what is done to the values).
+          const bool masked = have != 0xFFu || j0 + kTile - 1 > bottom ||
+                              (p.window > 0 && j0 <= top - p.window);
+          if (masked) {
+            // A masked value that is not finite would still make 0 * inf: such
+            // values become 0 here, and the rows that do attend the key NaN.
+            const int t = 2 * blocks + 1;
+            ok = __all_sync(0xffffffffu, mbar_sleep(full + t % C::stages, (t / C::stages) & 1));
+            unsigned char *v = smem + C::off_ring + (t % C::stages) * C::tile;
+            auto over = [](uint32_t y) { return (y & 0x7F807F80u) + 0x00800080u; };
+#pragma unroll 1
+            for (int c = tid & 127; ok && c < C::tile / 16; c += 512) {
+              uint4 x[4];
+              uint32_t hit[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                x[e] = *reinterpret_cast<const uint4 *>(v + (c + e * 128) * 16);
+                hit[e] = (over(x[e].x) | over(x[e].y) | over(x[e].z) | over(x[e].w)) & 0x80008000u;
+              }
+              if (!(hit[0] | hit[1] | hit[2] | hit[3])) continue;
+#pragma unroll 1
+              for (int e = 0; e < 4; ++e) {
+                uint16_t *at = reinterpret_cast<uint16_t *>(v + (c + e * 128) * 16);
+                const int key = ((c + e * 128) / 8) % kTile;
+#pragma unroll 1
+                for (int h = 0; h < 8; ++h) {
+                  if ((at[h] & 0x7F80u) != 0x7F80u) continue;
+                  atomicOr(&f.bad[key >> 5], 1u << (key & 31));
+                  __threadfence_block();  // known before it is gone
+                  at[h] = 0;
+                }
+              }
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(scanned + i);
+            ok = __all_sync(0xffffffffu, ok && mbar_sleep(scanned + i, scans++ & 1));
+            if (!ok) break;
+            // (Through tensor memory and back, in a loop: this way is taken for a
+            // block or two of a unit, and as straight code it took longer to fetch
+            // than to run.)
+#pragma unroll 1
+            for (int c0 = 0; c0 < kTile; c0 += 32) {
+              float x[32];
+              tmem_ld32(ts + c0, x);
+              const uint32_t bad = *static_cast<const volatile uint32_t *>(&f.bad[c0 / 32]);
+              const int to = pos - j0 - c0, from = p.window > 0 ? to - p.window + 1 : 0;
+              // Bit e: the row attends column c0 + e.
+              uint32_t on = to < 0 ? 0u : to >= 31 ? ~0u : (2u << to) - 1u;
+              on &= from <= 0 ? ~0u : from >= 32 ? 0u : ~0u << from;
+              on &= ((have >> (c0 / 16)) & 1 ? 0xFFFFu : 0u) |
+                    ((have >> (c0 / 16)) & 2 ? 0xFFFF0000u : 0u);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) x[e] = on & (1u << e) ? x[e] : -INFINITY;
+              if (__any_sync(0xffffffffu, bad & on))
+#pragma unroll
+                for (int e = 0; e < 32; ++e) x[e] = bad & on & (1u << e) ? NAN : x[e];
+              tmem_st32(ts + c0, x);
+            }
+            tmem_st_wait();
+          }
+          float s0[32], s1[32], s2[32], s3[32];  // the scores, 32 columns each
+          tmem_ld32_async(ts, s0);
+          tmem_ld32_async(ts + 32, s1);
+          tmem_ld32_async(ts + 64, s2);
+          tmem_ld32_async(ts + 96, s3);
+          tmem_ld_wait(s0);
+          tmem_ld_wait(s1);
+          tmem_ld_wait(s2);
+          tmem_ld_wait(s3);
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          auto maxima = [&](const float (&v)[32]) {
+#pragma unroll
+            for (int c = 0; c < 32; c += 8)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) mx[e] = fmaxf(fmaxf(mx[e], v[c + e]), v[c + 4 + e]);
+          };
+          maxima(s0);
+          maxima(s1);
+          maxima(s2);
+          maxima(s3);
+          const float top_s = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          const float new_m = fmaxf(m, top_s), new_mc = new_m == -INFINITY ? 0.f : new_m * p.scale;
+          // (Not for the difference of an infinity with itself.)
+          const bool grown = new_m > m && !(new_mc - mc <= kGrow && m != -INFINITY);
+          if (__any_sync(0xffffffffu, grown)) {
+            const float fac = m == -INFINITY ? 0.f : exp2_fast(grown ? mc - new_mc : 0.f);
+            if (grown) {
+              m = new_m;
+              mc = new_mc;
+            }
+            l *= fac;
+            if (kb > w.k0) {
+#pragma unroll 1
+              for (int c = 0; c < D; c += 32) {
+                float o[32];
+                tmem_ld32(to + c, o);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] *= fac;
+                tmem_st32(to + c, o);
+              }
+            }
+          }
+          // Weights, rounded to bf16 (2^-8) for the product with the values; their
+          // sum takes them unrounded.
+          uint64_t sum[2] = {0, 0};
+          const uint64_t scale2 = pack2(p.scale, p.scale), mc2 = pack2(-mc, -mc);
+          auto weights = [&](int c0, const float (&v)[32]) {
+            uint32_t x[16];
+#pragma unroll
+            for (int c = 0; c < 32; c += 2) {
+              float a, b;
+              unpack2(fma2(pack2(v[c], v[c + 1]), scale2, mc2), a, b);
+              a = exp2_fast(a);
+              b = exp2_fast(b);
+              sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], pack2(a, b));
+              x[c / 2] = f32x2_to_bf16x2(a, b);
+            }
+            tmem_st16(ts + c0 / 2, x);
+          };
+          weights(0, s0);
+          weights(32, s1);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(phalf + i);
+          weights(64, s2);
+          weights(96, s3);
+          float la, lb;
+          unpack2(add2(sum[0], sum[1]), la, lb);
+          l += la + lb;
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(pfull + i);
+          started = ahead;
+          if (ahead) pass_q();
+        }
+        if (ok) ok = mbar_sleep(ofull + i, units++ & 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-        float s[128];
-        tmem_ld128(ts, s);
-        Info &f = infos[blocks % kInfo];
-        const int j0 = (w.u.block0 + kb) * kTile;
-        const uint32_t have = f.pages;
-        // Masks, where some row of the unit does not attend some key (both
-        // tiles alike: they share what is done to the values).
-        if (have != 0xFFu || j0 + kTile - 1 > bottom ||
-            (p.window > 0 && j0 <= top - p.window)) {
-          // A masked value that is not finite would still make 0 * inf: such
-          // values become 0 here, and the rows that do attend the key NaN.
-          const int t = 2 * blocks + 1;
-          ok = __all_sync(0xffffffffu, mbar_sleep(full + t % C::stages, (t / C::stages) & 1));
-          unsigned char *v = smem + C::off_ring + (t % C::stages) * C::tile;
-          for (int c = tid & 127; ok && c < C::tile / 16; c += 128) {
-            uint4 x = *reinterpret_cast<const uint4 *>(v + c * 16);
-            auto over = [](uint32_t y) { return (y & 0x7F807F80u) + 0x00800080u; };
-            if ((over(x.x) | over(x.y) | over(x.z) | over(x.w)) & 0x80008000u) {
-              const int key = (c / 8) % kTile;
-              atomicOr(&f.bad[key >> 5], 1u << (key & 31));
-              __threadfence_block();
-              auto tidy = [&](uint32_t &y) {
-                if ((y & 0x7F80u) == 0x7F80u) y &= 0xFFFF0000u;
-                if ((y & 0x7F800000u) == 0x7F800000u) y &= 0xFFFFu;
-              };
-              tidy(x.x);
-              tidy(x.y);
-              tidy(x.z);
-              tidy(x.w);
-              *reinterpret_cast<uint4 *>(v + c * 16) = x;
+        // ---- end of a piece
+        const bool whole = w.k0 == 0 && w.k1 == w.u.blocks;
+        if (whole) {
+          // Four lanes exchange 16-byte pieces of their rows, so that a store
+          // covers 64 bytes of each row that it touches: with 16 of each, the
+          // stores of a unit took as long as two blocks of keys.
+          const uint64_t mine_at =
+              live ? reinterpret_cast<uint64_t>(static_cast<uint16_t *>(p.o.p) +
+                                                int64_t(w.u.t0 + tok) * p.o.ts +
+                                                int64_t(w.head * p.G + at - tok * p.G) * p.o.hs)
+                   : 0;
+          uint64_t rows[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            rows[e] = __shfl_sync(0xffffffffu, mine_at, (lane & ~3) + e);
+          const float inv = m == -INFINITY && l == 0.f ? 0.f : 1.f / l;
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            float o[32];
+            tmem_ld32(to + c, o);
+            uint32_t x[16];  // four pieces
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] = f32x2_to_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv);
+#pragma unroll
+            for (int bit = 1; bit < 4; bit *= 2) {
+              // Piece a with the bit clear and a + bit change places across lanes.
+              const bool up = lane & bit;
+#pragma unroll
+              for (int a = 0; a < 4; ++a) {
+                if (a & bit) continue;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  uint32_t &lo = x[a * 4 + e], &hi = x[(a + bit) * 4 + e];
+                  const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? lo : hi, bit);
+                  if (up)
+                    lo = got;
+                  else
+                    hi = got;
+                }
+              }
             }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (rows[e])
+                *reinterpret_cast<uint4 *>(rows[e] + (c + (lane & 3) * 8) * 2) =
+                    make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
           }
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(scanned + i);
-          ok = __all_sync(0xffffffffu, ok && mbar_sleep(scanned + i, scans++ & 1));
-          if (!ok) break;
-          const volatile uint32_t *bad = f.bad;
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const uint32_t b = bad[g];
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const int c = 32 * g + e, j = j0 + c;
-              const bool on = j <= pos && ((have >> (c >> 4)) & 1) &&
-                              (p.window == 0 || j > pos - p.window);
-              s[c] = on ? ((b >> e) & 1 ? NAN : s[c]) : -INFINITY;
-            }
-          }
-        }
-        float mx[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-        for (int c = 4; c < 128; c += 4)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[c + e]);
-        const float top_s = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        const float new_m = fmaxf(m, top_s), new_mc = new_m == -INFINITY ? 0.f : new_m * p.scale;
-        // (Not for the difference of an infinity with itself.)
-        const bool grown = new_m > m && !(new_mc - mc <= kGrow && m != -INFINITY);
-        if (__any_sync(0xffffffffu, grown)) {
-          const float fac = m == -INFINITY ? 0.f : exp2_fast(grown ? mc - new_mc : 0.f);
-          if (grown) {
-            m = new_m;
-            mc = new_mc;
-          }
-          l *= fac;
-          if (kb > w.k0) {
-#pragma unroll
-            for (int c = 0; c < D; c += 32) {
-              float o[32];
-              tmem_ld32(to + c, o);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] *= fac;
-              tmem_st32(to + c, o);
-            }
-          }
-        }
-        // Weights, rounded to bf16 (2^-8) for the product with the values; their
-        // sum takes them unrounded.
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int c0 = 0; c0 < 128; c0 += 64) {
-          uint32_t x[32];
-#pragma unroll
-          for (int c = 0; c < 64; c += 2) {
-            const float a = exp2_fast(fmaf(s[c0 + c], p.scale, -mc));
-            const float b = exp2_fast(fmaf(s[c0 + c + 1], p.scale, -mc));
-            sum[c & 2] += a;
-            sum[(c & 2) + 1] += b;
-            x[c / 2] = f32x2_to_bf16x2(a, b);
-          }
-          tmem_st32(ts + c0 / 2, x);
-        }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(pfull + i);
-      }
-      if (ok) ok = mbar_sleep(ofull + i, units++ & 1);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      tc_fence_after();
-      // ---- end of a piece
-      const bool whole = w.k0 == 0 && w.k1 == w.u.blocks;
-      if (whole) {
-        const int64_t at = int64_t(w.u.tile) * kUnit + row;
-        const int tok = static_cast<int>(at / p.G);
-        uint16_t *out = static_cast<uint16_t *>(p.o.p) + int64_t(w.u.t0 + tok) * p.o.ts +
-                        (w.head * p.G + (at - int64_t(tok) * p.G)) * p.o.hs;
-        const float inv = m == -INFINITY && l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-        for (int c = 0; c < D; c += 32) {
-          float o[32];
-          tmem_ld32(to + c, o);
-          if (live) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 8)
-              *reinterpret_cast<uint4 *>(out + c + e) = make_uint4(
-                  f32x2_to_bf16x2(o[e] * inv, o[e + 1] * inv),
-                  f32x2_to_bf16x2(o[e + 2] * inv, o[e + 3] * inv),
-                  f32x2_to_bf16x2(o[e + 4] * inv, o[e + 5] * inv),
-                  f32x2_to_bf16x2(o[e + 6] * inv, o[e + 7] * inv));
-          }
-        }
-      } else {
-        float *part = p.parts + (int64_t(blockIdx.x) * 2 + (w.k0 == 0)) * (kUnit * (D + 2));
-#pragma unroll
-        for (int c = 0; c < D; c += 32) {
-          float o[32];
-          tmem_ld32(to + c, o);
-          if (live) {
+        } else {
+          // Four columns of all rows, the next four, ..: lanes write side by side.
+          float *part = p.parts + (int64_t(blockIdx.x) * 2 + (w.k0 == 0)) * (kUnit * (D + 2));
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            float o[32];
+            tmem_ld32(to + c, o);
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<float4 *>(part + row * D + c + e) =
+              *reinterpret_cast<float4 *>(part + (c + e) * kUnit + row * 4) =
                   make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
           }
+          part[kUnit * D + row] = m;
+          part[kUnit * D + kUnit + row] = l;
         }
-        part[kUnit * D + row] = m;
-        part[kUnit * D + kUnit + row] = l;
-      }
-      tc_fence_before();
-    } while (w.next());
-    if (!ok && lane == 0) record_fault(&g_fault_attn, kFaultAttnWait);
+        tc_fence_before();
+      } while (w.next());
+      if (!ok && lane == 0) record_fault(&g_fault_attn, kFaultAttnWait);
+    }
   }
   if (any && warp == kTmaWarp && lane == 0) {
     // A unit that begins in this part and goes on past it: the CTAs after this
@@ -753,52 +890,80 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the pieces of a unit: the one that begins at the end of CTA c's part
-// and the continuations at the start of the parts after it. A warp per row.
+// and the continuations at the start of the parts after it. A block per 32
+// rows: a lane per row, a warp per four columns at a time.
 template <int D>
 __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ AttnTileParams p) {
-  constexpr int kPer = D / 32;
-  const int lane = threadIdx.x & 31;
+  constexpr int64_t kPart = kUnit * (D + 2);
+  constexpr int kLd = D / 2 + 2;             // words of a row of the result
+  constexpr int kMany = 64;                  // pieces at a time
+  __shared__ float fac[kMany][32], top[8][32];
+  __shared__ uint32_t out_s[32 * kLd];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   grid_dependency_wait();
   grid_dependents_launch();
   const int *h = p.headers + blockIdx.x * kHeader;
   const int more = h[0];
   if (more == 0) return;
   const int t0 = h[1], n = h[2], head = h[3], tile = h[4];
-  for (int row = blockIdx.y * 8 + (threadIdx.x >> 5); row < kUnit; row += gridDim.y * 8) {
-    const int64_t i = int64_t(tile) * kUnit + row;
-    if (i >= int64_t(n) * p.G) return;
-    const int tok = static_cast<int>(i / p.G);
-    constexpr int64_t kPart = kUnit * (D + 2);
-    const float *first = p.parts + (int64_t(blockIdx.x) * 2 + 1) * kPart;
-    const float *rest = p.parts + (int64_t(blockIdx.x) + 1) * 2 * kPart;
-    float m = -INFINITY;
-    for (int c = lane; c <= more; c += 32)
-      m = fmaxf(m, (c == 0 ? first : rest + (c - 1) * 2 * kPart)[kUnit * D + row]);
+  const int row0 = blockIdx.y * 32, row = row0 + lane;
+  if (tile * kUnit + row0 >= n * p.G) return;
+  const float *first = p.parts + (int64_t(blockIdx.x) * 2 + 1) * kPart;
+  const float *rest = p.parts + (int64_t(blockIdx.x) + 1) * 2 * kPart;
+  auto piece = [&](int c) { return c == 0 ? first : rest + (c - 1) * 2 * kPart; };
+  // (Rows of a second tile that the unit does not have hold anything.)
+  const bool live = tile * kUnit + row < n * p.G;
+  float m = -INFINITY;
+  for (int c = warp; c <= more; c += 8)
+    if (live) m = fmaxf(m, piece(c)[kUnit * D + row]);
+  top[warp][lane] = m;
+  __syncthreads();
 #pragma unroll
-    for (int s = 1; s < 32; s *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
-    const float z = m == -INFINITY ? 0.f : m;
-    float l = 0.f, a[kPer];
+  for (int w = 0; w < 8; ++w) m = fmaxf(m, top[w][lane]);
+  const float z = m == -INFINITY ? 0.f : m;
+  float l = 0.f;
+  float4 a[D / 32];
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) a[e] = 0.f;
-#pragma unroll 4
-    for (int c = 0; c <= more; ++c) {
-      const float *x = c == 0 ? first : rest + (c - 1) * 2 * kPart;
-      const float f = exp2_fast((x[kUnit * D + row] - z) * p.scale);
-      l += f * x[kUnit * D + kUnit + row];
-      const float *v = x + row * D + lane * kPer;
+  for (int e = 0; e < D / 32; ++e) a[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c0 = 0; c0 <= more; c0 += kMany) {
+    const int cn = min(kMany, more + 1 - c0);
+    __syncthreads();
+    for (int c = warp; c < cn; c += 8)
+      fac[c][lane] = live ? exp2_fast((piece(c0 + c)[kUnit * D + row] - z) * p.scale) : 0.f;
+    __syncthreads();
+#pragma unroll 2
+    for (int c = 0; c < cn; ++c) {
+      const float *x = piece(c0 + c);
+      const float f = fac[c][lane];
+      if (live) {
+        l += f * x[kUnit * D + kUnit + row];
 #pragma unroll
-      for (int e = 0; e < kPer; e += 2) {
-        const float2 y = *reinterpret_cast<const float2 *>(v + e);
-        a[e] += f * y.x;
-        a[e + 1] += f * y.y;
+        for (int e = 0; e < D / 32; ++e) {
+          const float4 y = *reinterpret_cast<const float4 *>(x + (e * 8 + warp) * 4 * kUnit + row * 4);
+          a[e].x += f * y.x;
+          a[e].y += f * y.y;
+          a[e].z += f * y.z;
+          a[e].w += f * y.w;
+        }
       }
     }
-    const float inv = m == -INFINITY && l == 0.f ? 0.f : 1.f / l;
-    uint16_t *out = static_cast<uint16_t *>(p.o.p) + int64_t(t0 + tok) * p.o.ts +
-                    (head * p.G + (i - int64_t(tok) * p.G)) * p.o.hs + lane * kPer;
+  }
+  const float inv = m == -INFINITY && l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-    for (int e = 0; e < kPer; e += 2)
-      *reinterpret_cast<uint32_t *>(out + e) = f32x2_to_bf16x2(a[e] * inv, a[e + 1] * inv);
+  for (int e = 0; e < D / 32; ++e) {
+    uint32_t *y = out_s + lane * kLd + (e * 8 + warp) * 2;
+    y[0] = f32x2_to_bf16x2(a[e].x * inv, a[e].y * inv);
+    y[1] = f32x2_to_bf16x2(a[e].z * inv, a[e].w * inv);
+  }
+  __syncthreads();
+  for (int r = warp; r < 32; r += 8) {
+    const int at = tile * kUnit + row0 + r, tok = at / p.G;
+    if (at >= n * p.G) break;
+    uint32_t *out = reinterpret_cast<uint32_t *>(
+        static_cast<uint16_t *>(p.o.p) + int64_t(t0 + tok) * p.o.ts +
+        int64_t(head * p.G + at - tok * p.G) * p.o.hs);
+#pragma unroll
+    for (int c = lane; c < D / 2; c += 32) out[c] = out_s[r * kLd + c];
   }
 }
 
@@ -842,7 +1007,7 @@ cudaError_t run(const AttnTileParams &p, bool pdl, cudaStream_t stream) {
   if (e == cudaSuccess)
     e = launch_after(tile_kernel<D>, dim3(ctas), kThreads, kSmem, pdl, stream, p);
   if (e == cudaSuccess)
-    e = launch_after(combine_kernel<D>, dim3(ctas, kUnit / 16), 256, 0, pdl, stream, p);
+    e = launch_after(combine_kernel<D>, dim3(ctas, kUnit / 32), 256, 0, pdl, stream, p);
   return e;
 }
 
