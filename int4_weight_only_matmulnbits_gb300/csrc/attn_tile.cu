@@ -45,11 +45,12 @@ constexpr int kTile = 128;                 // rows of an MMA, keys of a block
 constexpr int kUnit = 2 * kTile;           // rows of a unit
 constexpr int kSoftWarps = 8;              // two tiles of four warps
 constexpr int kTmaWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;
-constexpr int kThreads = 32 * (kSoftWarps + 4);  // a third group of four, two of them idle
+constexpr int kScanWarp = kSoftWarps + 2, kScanWarps = 2;
+constexpr int kThreads = 32 * (kSoftWarps + 4);
 // Registers: of the 3 x 168 a lane that the launch has, the softmax takes more.
 constexpr int kSoftRegs = 216, kOtherRegs = 72;
 static_assert(2 * kSoftRegs + kOtherRegs <= 3 * 168, "within the launch's registers");
-constexpr int kInfo = 8;                   // blocks whose key masks are kept
+constexpr int kInfo = 8;                   // blocks whose masks are kept, masked ones in flight
 constexpr int kTmemCols = 512;
 constexpr int kHeader = 8;                 // ints
 constexpr float kGrow = 8.f;               // rescale from 2^8 on
@@ -61,15 +62,17 @@ struct Cfg {
   static constexpr int stages = D == 128 ? 5 : 10;
   static constexpr int off_ring = 2 * tile;
   static constexpr int off_info = off_ring + stages * tile;
-  static constexpr int off_bar = off_info + kInfo * 32;
-  static constexpr int total = off_bar + 512;
+  static constexpr int off_todo = off_info + kInfo * 32;  // of masked blocks: tile, or -1
+  static constexpr int off_bar = off_todo + kInfo * 4;
+  static constexpr int total = off_bar + 640;
 };
 static_assert(Cfg<128>::total + 1024 <= 227 * 1024, "shared memory");
 
 struct Info {       // of a block of keys
   uint32_t pages;   // bit g: keys 16 g .. 16 g + 15 have a page
-  uint32_t pad[3];
-  uint32_t bad[4];  // keys whose values are not finite
+  int scan;         // masked: the how-manieth masked block it is, else -1
+  uint32_t pad[2];
+  uint32_t bad[4];  // masked: keys whose values are not finite
 };
 static_assert(sizeof(Info) == 32, "");
 
@@ -391,11 +394,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *pfull = sfull + 2;
   uint64_t *qfull = pfull + 2;
   uint64_t *ofull = qfull + 2;
-  uint64_t *scanned = ofull + 2;        // a tile's warps have looked over the values
-  uint64_t *phalf = scanned + 2;        // the weights of the first 64 keys
-  uint64_t *done = phalf + 2;
+  uint64_t *phalf = ofull + 2;          // the weights of the first 64 keys
+  uint64_t *toscan = phalf + 2;         // a masked block's values are to be looked over
+  uint64_t *scanned = toscan + kInfo;   // and have been
+  uint64_t *done = scanned + kInfo;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
-  static_assert((2 * C::stages + kInfo + 13) * 8 + 4 <= 512, "barriers");
+  static_assert((2 * C::stages + 3 * kInfo + 11) * 8 + 4 <= 640, "barriers");
+  int *todo = reinterpret_cast<int *>(smem + C::off_todo);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
@@ -403,14 +408,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(full + i, 1);
       mbar_init(empty + i, 1);
     }
-    for (int i = 0; i < kInfo; ++i) mbar_init(known + i, 1);
+    for (int i = 0; i < kInfo; ++i) {
+      mbar_init(known + i, 1);
+      mbar_init(toscan + i, 1);
+      mbar_init(scanned + i, kScanWarps);
+    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(sfull + i, 1);
       mbar_init(phalf + i, 4);
       mbar_init(pfull + i, 4);
       mbar_init(qfull + i, 4);
       mbar_init(ofull + i, 1);
-      mbar_init(scanned + i, 4);
     }
     mbar_init(done, 1);
     fence_barrier_init();
@@ -440,9 +448,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int nbox = kTile / p.box;  // copies of 64 columns: nbox for each half
       const int box = lane % nbox, col = lane / nbox;
       const bool copies = lane < nbox * (D / 64);
-      int tiles = 0, blocks = 0;
+      int tiles = 0, blocks = 0, scans = 0;
       bool ok = true;
       do {
+        const int bottom = first_pos(w.u, p.G);
         const int last = last_pos(w.u, p.G), end = min(w.u.len, p.cap);
         // Lane g < 8: the page of the keys 16 g on of the next block.
         auto page_of = [&](int kb) {
@@ -457,7 +466,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (kb + 1 < w.k1) page = page_of(kb + 1);
           const uint32_t bits = __ballot_sync(0xffffffffu, now >= 0 && lane < 8);
           const int mine = __shfl_sync(0xffffffffu, now, box * (p.box / 16) & 7);
-          const int at = ((w.u.block0 + kb) * kTile + box * p.box) % p.page_size;
+          const int j0 = (w.u.block0 + kb) * kTile, at = (j0 + box * p.box) % p.page_size;
+          // Masks are needed where some row of the unit does not attend some key
+          // (both tiles alike: they share what is done to the values).
+          const bool masked = bits != 0xFFu || j0 + kTile - 1 > bottom ||
+                              (p.window > 0 && j0 <= last - p.window);
           for (int v = 0; v < 2; ++v, ++tiles) {
             const int s = tiles % C::stages;
             if (tiles >= C::stages) {
@@ -469,9 +482,16 @@ __global__ void __launch_bounds__(kThreads, 1)
               // them is done with.)
               Info &f = infos[blocks % kInfo];
               f.pages = bits;
+              f.scan = masked ? scans : -1;
               f.bad[0] = f.bad[1] = f.bad[2] = f.bad[3] = 0;
               mbar_arrive(known + blocks % kInfo);
+              if (masked) {
+                // (As many masked blocks are never in flight.)
+                todo[scans % kInfo] = blocks;
+                mbar_arrive(toscan + scans % kInfo);
+              }
             }
+            if (v == 0 && masked) ++scans;
             if (lane == 0) mbar_arrive_expect_tx(full + s, C::tile);
             __syncwarp();
             if (copies)
@@ -482,6 +502,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
         }
       } while (ok && w.next());
+      if (lane == 0) {
+        todo[scans % kInfo] = -1;
+        mbar_arrive(toscan + scans % kInfo);
+      }
       if (!ok) {
         if (lane == 0) record_fault(&g_fault_attn, kFaultAttnWait);
         // Given up: the copies in flight land before the CTA leaves.
@@ -591,6 +615,46 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (!__all_sync(0xffffffffu, mbar_sleep(done, 0)) || !ok)
         if (lane == 0) record_fault(&g_fault_attn, kFaultAttnWait);
+    } else if (any) {
+      // ---- values of masked blocks ----------------------------------------------------
+      // A masked value that is not finite would still make 0 * inf: such values
+      // become 0 here, before the weights' product with them, and their keys are
+      // noted: the rows that do attend one get NaN.
+      auto over = [](uint32_t y) { return (y & 0x7F807F80u) + 0x00800080u; };
+      bool ok = true;
+      for (int n = 0; ok; ++n) {
+        ok = __all_sync(0xffffffffu, mbar_sleep(toscan + n % kInfo, (n / kInfo) & 1));
+        const int block = ok ? todo[n % kInfo] : -1, t = 2 * block + 1;
+        if (block < 0) break;
+        ok = __all_sync(0xffffffffu, mbar_sleep(full + t % C::stages, (t / C::stages) & 1));
+        if (!ok) break;
+        unsigned char *v = smem + C::off_ring + (t % C::stages) * C::tile;
+        uint32_t *bad = infos[block % kInfo].bad;
+        constexpr int kStep = 32 * kScanWarps;
+#pragma unroll 1
+        for (int c = (warp - kScanWarp) * 32 + lane; c < C::tile / 16; c += 8 * kStep) {
+          uint32_t hit = 0;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(v + (c + e * kStep) * 16);
+            hit |= over(x.x) | over(x.y) | over(x.z) | over(x.w);
+          }
+          if (!(hit & 0x80008000u)) continue;
+#pragma unroll 1
+          for (int e = 0; e < 64; ++e) {
+            const int at = c + (e / 8) * kStep;
+            uint16_t *x = reinterpret_cast<uint16_t *>(v + at * 16) + e % 8;
+            if ((*x & 0x7F80u) != 0x7F80u) continue;
+            *x = 0;
+            const int key = (at / 8) % kTile;
+            atomicOr(bad + (key >> 5), 1u << (key & 31));
+          }
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(scanned + n % kInfo);
+      }
+      if (!ok && lane == 0) record_fault(&g_fault_attn, kFaultAttnWait);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
@@ -599,23 +663,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int i = warp >> 2, r = (warp & 3) * 32 + lane;  // tile, row in it
       const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
       const uint32_t ts = tmem + lanes + i * kTile, to = tmem + lanes + 2 * kTile + i * kTile;
-      int blocks = 0, mine = 0, units = 0, scans = 0;  // of the CTA; of this tile
+      int blocks = 0, mine = 0, units = 0;  // of the CTA; of this tile
       bool ok = true, started = false;  // started: the unit's rows are on their way
       const int row = i * kTile + r;  // in the unit
-      // Starts the copies of a unit's row into this tile's place, and tells the
-      // MMAs when they are there. 16-byte piece c of row r lies at c ^ (r & 7) of
-      // the row's 128 bytes.
+      // Starts the copies of a unit's rows into this tile's place, lanes side by
+      // side along a row, and tells the MMAs when they are there. 16-byte piece c
+      // of row r lies at c ^ (r & 7) of the row's 128 bytes.
       auto fetch_q = [&](const Unit &u, int head) {
         const int at = u.tile * kUnit + row, tok = at / p.G;
-        const bool live = at < u.n * p.G;
         const uint16_t *src = static_cast<const uint16_t *>(p.q.p);
-        if (live)
-          src += int64_t(u.t0 + tok) * p.q.ts + int64_t(head * p.G + at - tok * p.G) * p.q.hs;
-        const uint32_t dst = smem_addr(smem + i * C::tile + r * 128);
+        const uint64_t mine_at =
+            at < u.n * p.G
+                ? reinterpret_cast<uint64_t>(src + int64_t(u.t0 + tok) * p.q.ts +
+                                             int64_t(head * p.G + at - tok * p.G) * p.q.hs)
+                : 0;
+        constexpr int kPieces = D / 8, kAtOnce = 32 / kPieces;  // pieces of a row; rows
+        const int c = lane % kPieces;
 #pragma unroll 4
-        for (int c = 0; c < D / 8; ++c)
-          cp16_or_zero(dst + (c / 8) * C::half + (((c % 8) ^ (r & 7)) << 4), src + (live ? c * 8 : 0),
-                       live);
+        for (int e = 0; e < 32; e += kAtOnce) {
+          const int from = e + lane / kPieces, rr = (warp & 3) * 32 + from;
+          const uint64_t x = __shfl_sync(0xffffffffu, mine_at, from);
+          cp16_or_zero(smem_addr(smem + i * C::tile + (c / 8) * C::half + rr * 128 +
+                                 (((c % 8) ^ (rr & 7)) << 4)),
+                       x ? reinterpret_cast<const uint16_t *>(x) + c * 8 : src, x != 0);
+        }
       };
       auto pass_q = [&] {
         asm volatile("cp.async.wait_all;" ::: "memory");
@@ -635,7 +706,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int at = w.u.tile * kUnit + row, tok = at / p.G;
         const bool live = at < w.u.n * p.G;
         const int pos = live ? w.u.len - w.u.n + tok : -1;
-        const int top = last_pos(w.u, p.G), bottom = first_pos(w.u, p.G);
         float m = -INFINITY, mc = 0.f, l = 0.f;  // maximum (of scores), times the scale; sum
         for (int kb = w.k0; kb < w.k1 && ok; ++kb, ++blocks, ++mine) {
           // (In this order: a tile that was left out of units is blocks ahead.)
@@ -650,44 +720,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           Info &f = infos[blocks % kInfo];
           const int j0 = (w.u.block0 + kb) * kTile;
           const uint32_t have = f.pages;
-          // Masks, where some row of the unit does not attend some key (both
-          // tiles alike: they share what is done to the values).
-          const bool masked = have != 0xFFu || j0 + kTile - 1 > bottom ||
-                              (p.window > 0 && j0 <= top - p.window);
-          if (masked) {
-            // A masked value that is not finite would still make 0 * inf: such
-            // values become 0 here, and the rows that do attend the key NaN.
-            const int t = 2 * blocks + 1;
-            ok = __all_sync(0xffffffffu, mbar_sleep(full + t % C::stages, (t / C::stages) & 1));
-            unsigned char *v = smem + C::off_ring + (t % C::stages) * C::tile;
-            auto over = [](uint32_t y) { return (y & 0x7F807F80u) + 0x00800080u; };
-#pragma unroll 1
-            for (int c = tid & 127; ok && c < C::tile / 16; c += 512) {
-              uint4 x[4];
-              uint32_t hit[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                x[e] = *reinterpret_cast<const uint4 *>(v + (c + e * 128) * 16);
-                hit[e] = (over(x[e].x) | over(x[e].y) | over(x[e].z) | over(x[e].w)) & 0x80008000u;
-              }
-              if (!(hit[0] | hit[1] | hit[2] | hit[3])) continue;
-#pragma unroll 1
-              for (int e = 0; e < 4; ++e) {
-                uint16_t *at = reinterpret_cast<uint16_t *>(v + (c + e * 128) * 16);
-                const int key = ((c + e * 128) / 8) % kTile;
-#pragma unroll 1
-                for (int h = 0; h < 8; ++h) {
-                  if ((at[h] & 0x7F80u) != 0x7F80u) continue;
-                  atomicOr(&f.bad[key >> 5], 1u << (key & 31));
-                  __threadfence_block();  // known before it is gone
-                  at[h] = 0;
-                }
-              }
-            }
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(scanned + i);
-            ok = __all_sync(0xffffffffu, ok && mbar_sleep(scanned + i, scans++ & 1));
+          const int scan = f.scan;
+          if (scan >= 0) {
+            ok = __all_sync(0xffffffffu,
+                            mbar_sleep(scanned + scan % kInfo, (scan / kInfo) & 1));
             if (!ok) break;
             // (Through tensor memory and back, in a loop: this way is taken for a
             // block or two of a unit, and as straight code it took longer to fetch
