@@ -51,6 +51,7 @@ constexpr int kThreads = 32 * (kSoftWarps + 4);
 constexpr int kSoftRegs = 216, kOtherRegs = 72;
 static_assert(2 * kSoftRegs + kOtherRegs <= 3 * 168, "within the launch's registers");
 constexpr int kInfo = 8;                   // blocks whose masks are kept, masked ones in flight
+constexpr int kPieces = 8;                 // pieces of units that are known ahead
 constexpr int kTmemCols = 512;
 constexpr int kHeader = 8;                 // ints
 constexpr float kGrow = 8.f;               // rescale from 2^8 on
@@ -63,8 +64,9 @@ struct Cfg {
   static constexpr int off_ring = 2 * tile;
   static constexpr int off_info = off_ring + stages * tile;
   static constexpr int off_todo = off_info + kInfo * 32;  // of masked blocks: tile, or -1
-  static constexpr int off_bar = off_todo + kInfo * 4;
-  static constexpr int total = off_bar + 640;
+  static constexpr int off_pieces = off_todo + kInfo * 4;
+  static constexpr int off_bar = off_pieces + kPieces * 48;
+  static constexpr int total = off_bar + 768;
 };
 static_assert(Cfg<128>::total + 1024 <= 227 * 1024, "shared memory");
 
@@ -380,6 +382,15 @@ struct Walk {
   }
 };
 
+// A piece as the copying warp hands it to the others.
+struct Piece {
+  int t0, n, len, tile, block0, blocks, head, k0, k1;
+  int more;  // another one follows
+  int none;  // this CTA has no part of the line
+  int pad;
+};
+static_assert(sizeof(Piece) == 48, "");
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     tile_kernel(const __grid_constant__ AttnTileParams p) {
@@ -397,10 +408,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *phalf = ofull + 2;          // the weights of the first 64 keys
   uint64_t *toscan = phalf + 2;         // a masked block's values are to be looked over
   uint64_t *scanned = toscan + kInfo;   // and have been
-  uint64_t *done = scanned + kInfo;
+  uint64_t *listed = scanned + kInfo;   // a piece is there
+  uint64_t *taken = listed + kPieces;   // and has been read by every warp it concerns
+  uint64_t *qfree = taken + kPieces;    // per tile: its rows have been used
+  uint64_t *done = qfree + 2;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
-  static_assert((2 * C::stages + 3 * kInfo + 11) * 8 + 4 <= 640, "barriers");
+  static_assert((2 * C::stages + 3 * kInfo + 2 * kPieces + 13) * 8 + 4 <= 768, "barriers");
   int *todo = reinterpret_cast<int *>(smem + C::off_todo);
+  Piece *pieces = reinterpret_cast<Piece *>(smem + C::off_pieces);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
@@ -413,11 +428,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(toscan + i, 1);
       mbar_init(scanned + i, kScanWarps);
     }
+    for (int i = 0; i < kPieces; ++i) {
+      mbar_init(listed + i, 1);
+      mbar_init(taken + i, kSoftWarps + 1);
+    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(sfull + i, 1);
       mbar_init(phalf + i, 4);
       mbar_init(pfull + i, 4);
-      mbar_init(qfull + i, 4);
+      mbar_init(qfull + i, p.q_tma ? 1 : 4);
+      mbar_init(qfree + i, 1);
       mbar_init(ofull + i, 1);
     }
     mbar_init(done, 1);
@@ -437,20 +457,42 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   grid_dependency_wait();
   grid_dependents_launch();
-  Walk w(p);
-  const bool any = w.start(lane);
-  int *header = p.headers + blockIdx.x * kHeader;
-  if (!any && tid == 0) header[0] = 0;
+  // The pieces, as every warp but the copying ones takes them: copied to
+  // registers, so that the place is free again at once.
+  auto take_piece = [&](int n, bool &ok) {
+    ok = __all_sync(0xffffffffu, mbar_sleep(listed + n % kPieces, (n / kPieces) & 1));
+    const Piece pc = pieces[n % kPieces];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(taken + n % kPieces);
+    return pc;
+  };
   if (warp >= kSoftWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (any && warp == kTmaWarp) {
+    if (warp == kTmaWarp) {
       // ---- keys and values ----------------------------------------------------------
       const int nbox = kTile / p.box;  // copies of 64 columns: nbox for each half
       const int box = lane % nbox, col = lane / nbox;
       const bool copies = lane < nbox * (D / 64);
-      int tiles = 0, blocks = 0, scans = 0;
+      Walk w(p);
+      const bool any = w.start(lane);
+      int tiles = 0, blocks = 0, scans = 0, listing = 0, uses[2] = {0, 0};
       bool ok = true;
-      do {
+      if (!any && lane == 0) {
+        pieces[0].none = 1;
+        mbar_arrive(listed);
+      }
+      if (any) do {
+        const int ps = listing % kPieces;
+        if (listing >= kPieces)
+          ok = __all_sync(0xffffffffu, mbar_sleep(taken + ps, (listing / kPieces - 1) & 1));
+        if (!ok) break;
+        const bool two = w.two(w.u);
+        if (lane == 0) {
+          pieces[ps] = Piece{w.u.t0,     w.u.n,  w.u.len, w.u.tile, w.u.block0, w.u.blocks,
+                             w.head,     w.k0,   w.k1,    w.more(), 0,          0};
+          mbar_arrive(listed + ps);
+        }
+        ++listing;
         const int bottom = first_pos(w.u, p.G);
         const int last = last_pos(w.u, p.G), end = min(w.u.len, p.cap);
         // Lane g < 8: the page of the keys 16 g on of the next block.
@@ -498,6 +540,20 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_load_4d(smem + C::off_ring + s * C::tile + col * C::half + box * p.box * 128,
                           v ? &p.tv : &p.tk, col * 64, at, w.head, mine, full + s);
             __syncwarp();
+            // The unit's rows follow its first keys, as each tile's place is free.
+            if (v == 0 && kb == w.k0 && p.q_tma)
+              for (int i = 0; i < 1 + two; ++i) {
+                if (uses[i]++ > 0)
+                  ok = __all_sync(0xffffffffu, mbar_sleep(qfree + i, (uses[i] - 2) & 1));
+                if (!ok) break;
+                if (lane == 0) mbar_arrive_expect_tx(qfull + i, C::tile);
+                __syncwarp();
+                if (lane < D / 64)
+                  tma_load_3d(smem + i * C::tile + lane * C::half, &p.tq, lane * 64, w.head * p.G,
+                              w.u.t0 + (w.u.tile * kUnit + i * kTile) / p.G, qfull + i);
+                __syncwarp();
+              }
+            if (!ok) break;
           }
           if (!ok) break;
         }
@@ -511,8 +567,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Given up: the copies in flight land before the CTA leaves.
         for (int i = max(0, tiles - C::stages); i < tiles; ++i)
           mbar_sleep(full + i % C::stages, (i / C::stages) & 1);
+        for (int i = 0; i < 2 && p.q_tma; ++i)
+          if (uses[i] > 0) mbar_sleep(qfull + i, (uses[i] - 1) & 1);
       }
-    } else if (any && warp == kMmaWarp) {
+      if (lane == 0) {
+        // A unit that begins in this part and goes on past it: the CTAs after
+        // this one that have a piece of it. (After a wait that ran out the
+        // results mean nothing.)
+        int *header = p.headers + blockIdx.x * kHeader;
+        int more = 0;
+        if (any && w.k0 == 0 && w.k1 < w.u.blocks) {
+          const int64_t end = w.x1 + w.u.blocks - w.k1;
+          more = static_cast<int>((end * w.parts - 1) / w.total) - static_cast<int>(blockIdx.x);
+          while ((blockIdx.x + more) * w.total / w.parts >= end) --more;
+          while (int64_t(blockIdx.x) + more + 1 < w.parts &&
+                 (blockIdx.x + more + 1) * w.total / w.parts < end)
+            ++more;
+          header[1] = w.u.t0;
+          header[2] = w.u.n;
+          header[3] = w.head;
+          header[4] = w.u.tile;
+        }
+        header[0] = more;
+      }
+    } else if (warp == kMmaWarp) {
       // ---- MMAs: the whole warp goes round, one elected lane issues ------------------
       // What decides the way and the operands is taken from lane 0, so that it
       // stays in uniform registers: moving it there for each MMA took as long
@@ -539,7 +617,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return s;
       };
-      auto scores = [&](int i, int s, bool release) {  // S_i = Q_i K^T
+      // S_i = Q_i K^T; last: of the unit.
+      auto scores = [&](int i, int s, bool last, bool release) {
         tc_fence_after();
         const uint64_t a = q_desc + i * (C::tile >> 4), b = k_desc + s * (C::tile >> 4);
         if (ok && elect_one()) {
@@ -549,6 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             umma_ss(tm + i * kTile, a + step, b + step, qk, k > 0);
           }
           umma_commit(sfull + i);
+          if (last) umma_commit(qfree + i);
           if (release) umma_commit(empty + s);
         }
         __syncwarp();
@@ -576,17 +656,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       };
-      bool again;
-      do {
-        const bool two = uniform(w.two(w.u));
-        const int n = uniform(w.k1 - w.k0);
-        again = uniform(w.next());
+      for (int pn = 0; ok; ++pn) {
+        const Piece pc = take_piece(pn, ok);
+        const bool two = uniform(pc.n * p.G > pc.tile * kUnit + kTile);
+        const int n = uniform(pc.k1 - pc.k0);
+        if (!ok || uniform(pc.none)) break;
         wait(qfull, units0++);
         int ks = take();
-        scores(0, ks, !two);
+        scores(0, ks, n == 1, !two);
         if (two) {
           wait(qfull + 1, units1++);
-          scores(1, ks, true);
+          scores(1, ks, n == 1, true);
         }
         for (int kb = 0; kb < n && ok; ++kb) {
           const bool more = kb + 1 < n;
@@ -594,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           values(0, vs, blocks0++, kb == 0, !two);
           if (more) {
             ks = take();
-            scores(0, ks, !two);
+            scores(0, ks, kb + 2 == n, !two);
           } else {
             if (ok && elect_one()) umma_commit(ofull);
             __syncwarp();
@@ -602,20 +682,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (two) {
             values(1, vs, blocks1++, kb == 0, true);
             if (more) {
-              scores(1, ks, true);
+              scores(1, ks, kb + 2 == n, true);
             } else {
               if (ok && elect_one()) umma_commit(ofull + 1);
               __syncwarp();
             }
           }
         }
-      } while (ok && again);
+        if (!uniform(pc.more)) break;
+      }
       // Every MMA issued is complete before the tensor memory is released.
       if (elect_one()) umma_commit(done);
       __syncwarp();
       if (!__all_sync(0xffffffffu, mbar_sleep(done, 0)) || !ok)
         if (lane == 0) record_fault(&g_fault_attn, kFaultAttnWait);
-    } else if (any) {
+    } else {
       // ---- values of masked blocks ----------------------------------------------------
       // A masked value that is not finite would still make 0 * inf: such values
       // become 0 here, before the weights' product with them, and their keys are
@@ -658,24 +739,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
-    if (any) {
+    {
       // ---- softmax: a thread per row ------------------------------------------------
       const int i = warp >> 2, r = (warp & 3) * 32 + lane;  // tile, row in it
       const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
       const uint32_t ts = tmem + lanes + i * kTile, to = tmem + lanes + 2 * kTile + i * kTile;
       int blocks = 0, mine = 0, units = 0;  // of the CTA; of this tile
-      bool ok = true, started = false;  // started: the unit's rows are on their way
+      bool ok = true;
       const int row = i * kTile + r;  // in the unit
-      // Starts the copies of a unit's rows into this tile's place, lanes side by
-      // side along a row, and tells the MMAs when they are there. 16-byte piece c
-      // of row r lies at c ^ (r & 7) of the row's 128 bytes.
-      auto fetch_q = [&](const Unit &u, int head) {
-        const int at = u.tile * kUnit + row, tok = at / p.G;
+      // The unit's rows, where no tensor map describes them: lanes side by side
+      // along a row. 16-byte piece c of row r lies at c ^ (r & 7) of the row's 128
+      // bytes.
+      auto load_q = [&](const Piece &u, int at, int tok) {
         const uint16_t *src = static_cast<const uint16_t *>(p.q.p);
         const uint64_t mine_at =
             at < u.n * p.G
                 ? reinterpret_cast<uint64_t>(src + int64_t(u.t0 + tok) * p.q.ts +
-                                             int64_t(head * p.G + at - tok * p.G) * p.q.hs)
+                                             int64_t(u.head * p.G + at - tok * p.G) * p.q.hs)
                 : 0;
         constexpr int kPieces = D / 8, kAtOnce = 32 / kPieces;  // pieces of a row; rows
         const int c = lane % kPieces;
@@ -687,51 +767,44 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  (((c % 8) ^ (rr & 7)) << 4)),
                        x ? reinterpret_cast<const uint16_t *>(x) + c * 8 : src, x != 0);
         }
-      };
-      auto pass_q = [&] {
         asm volatile("cp.async.wait_all;" ::: "memory");
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(qfull + i);
       };
-      do {
-        if (i == 1 && !w.two(w.u)) {
-          blocks += w.k1 - w.k0;
+      for (int pn = 0; ok; ++pn) {
+        const Piece pc = take_piece(pn, ok);
+        if (!ok || pc.none) break;
+        if (i == 1 && pc.n * p.G <= pc.tile * kUnit + kTile) {  // no rows in this tile
+          blocks += pc.k1 - pc.k0;
+          if (!pc.more) break;
           continue;
         }
-        if (!started) {  // else they came with the unit before
-          fetch_q(w.u, w.head);
-          pass_q();
-        }
-        const int at = w.u.tile * kUnit + row, tok = at / p.G;
-        const bool live = at < w.u.n * p.G;
-        const int pos = live ? w.u.len - w.u.n + tok : -1;
+        const int at = pc.tile * kUnit + row, tok = at / p.G;
+        const bool live = at < pc.n * p.G;
+        const int pos = live ? pc.len - pc.n + tok : -1;
+        if (!p.q_tma) load_q(pc, at, tok);
         float m = -INFINITY, mc = 0.f, l = 0.f;  // maximum (of scores), times the scale; sum
-        for (int kb = w.k0; kb < w.k1 && ok; ++kb, ++blocks, ++mine) {
+        for (int kb = pc.k0; kb < pc.k1 && ok; ++kb, ++blocks, ++mine) {
           // (In this order: a tile that was left out of units is blocks ahead.)
           ok = mbar_sleep(sfull + i, mine & 1) &&
                mbar_sleep(known + blocks % kInfo, (blocks / kInfo) & 1);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
-          // S of the last block is there: Q's place is free for the next unit.
-          const bool ahead = kb + 1 == w.k1 && w.more() && (i == 0 || w.two(w.after));
-          if (ahead) fetch_q(w.after, w.next_head());
           Info &f = infos[blocks % kInfo];
-          const int j0 = (w.u.block0 + kb) * kTile;
+          const int j0 = (pc.block0 + kb) * kTile;
           const uint32_t have = f.pages;
           const int scan = f.scan;
           if (scan >= 0) {
             ok = __all_sync(0xffffffffu,
                             mbar_sleep(scanned + scan % kInfo, (scan / kInfo) & 1));
             if (!ok) break;
-            // (Through tensor memory and back, in a loop: this way is taken for a
+            // Through tensor memory and back, in a loop: this way is taken for a
             // block or two of a unit, and as straight code it took longer to fetch
-            // than to run.)
+            // than to run.
 #pragma unroll 1
             for (int c0 = 0; c0 < kTile; c0 += 32) {
-              float x[32];
-              tmem_ld32(ts + c0, x);
               const uint32_t bad = *static_cast<const volatile uint32_t *>(&f.bad[c0 / 32]);
               const int to = pos - j0 - c0, from = p.window > 0 ? to - p.window + 1 : 0;
               // Bit e: the row attends column c0 + e.
@@ -739,11 +812,19 @@ __global__ void __launch_bounds__(kThreads, 1)
               on &= from <= 0 ? ~0u : from >= 32 ? 0u : ~0u << from;
               on &= ((have >> (c0 / 16)) & 1 ? 0xFFFFu : 0u) |
                     ((have >> (c0 / 16)) & 2 ? 0xFFFF0000u : 0u);
+              if (__all_sync(0xffffffffu, on == ~0u && bad == 0)) continue;
+              float x[32];
+              if (__any_sync(0xffffffffu, on)) {
+                tmem_ld32(ts + c0, x);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) x[e] = on & (1u << e) ? x[e] : -INFINITY;
-              if (__any_sync(0xffffffffu, bad & on))
+                for (int e = 0; e < 32; ++e) x[e] = on & (1u << e) ? x[e] : -INFINITY;
+                if (__any_sync(0xffffffffu, bad & on))
 #pragma unroll
-                for (int e = 0; e < 32; ++e) x[e] = bad & on & (1u << e) ? NAN : x[e];
+                  for (int e = 0; e < 32; ++e) x[e] = bad & on & (1u << e) ? NAN : x[e];
+              } else {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) x[e] = -INFINITY;
+              }
               tmem_st32(ts + c0, x);
             }
             tmem_st_wait();
@@ -779,7 +860,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               mc = new_mc;
             }
             l *= fac;
-            if (kb > w.k0) {
+            if (kb > pc.k0) {
 #pragma unroll 1
               for (int c = 0; c < D; c += 32) {
                 float o[32];
@@ -822,23 +903,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(pfull + i);
-          started = ahead;
-          if (ahead) pass_q();
         }
         if (ok) ok = mbar_sleep(ofull + i, units++ & 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
         // ---- end of a piece
-        const bool whole = w.k0 == 0 && w.k1 == w.u.blocks;
+        const bool whole = pc.k0 == 0 && pc.k1 == pc.blocks;
         if (whole) {
           // Four lanes exchange 16-byte pieces of their rows, so that a store
           // covers 64 bytes of each row that it touches: with 16 of each, the
           // stores of a unit took as long as two blocks of keys.
           const uint64_t mine_at =
               live ? reinterpret_cast<uint64_t>(static_cast<uint16_t *>(p.o.p) +
-                                                int64_t(w.u.t0 + tok) * p.o.ts +
-                                                int64_t(w.head * p.G + at - tok * p.G) * p.o.hs)
+                                                int64_t(pc.t0 + tok) * p.o.ts +
+                                                int64_t(pc.head * p.G + at - tok * p.G) * p.o.hs)
                    : 0;
           uint64_t rows[4];
 #pragma unroll
@@ -878,7 +957,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         } else {
           // Four columns of all rows, the next four, ..: lanes write side by side.
-          float *part = p.parts + (int64_t(blockIdx.x) * 2 + (w.k0 == 0)) * (kUnit * (D + 2));
+          float *part = p.parts + (int64_t(blockIdx.x) * 2 + (pc.k0 == 0)) * (kUnit * (D + 2));
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
             float o[32];
@@ -892,28 +971,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           part[kUnit * D + kUnit + row] = l;
         }
         tc_fence_before();
-      } while (w.next());
+        if (!pc.more) break;
+      }
       if (!ok && lane == 0) record_fault(&g_fault_attn, kFaultAttnWait);
     }
-  }
-  if (any && warp == kTmaWarp && lane == 0) {
-    // A unit that begins in this part and goes on past it: the CTAs after this
-    // one that have a piece of it. (After a wait that ran out the results mean
-    // nothing.)
-    int more = 0;
-    if (w.k0 == 0 && w.k1 < w.u.blocks) {
-      const int64_t end = w.x1 + w.u.blocks - w.k1;
-      more = static_cast<int>((end * w.parts - 1) / w.total) - static_cast<int>(blockIdx.x);
-      while ((blockIdx.x + more) * w.total / w.parts >= end) --more;
-      while (int64_t(blockIdx.x) + more + 1 < w.parts &&
-             (blockIdx.x + more + 1) * w.total / w.parts < end)
-        ++more;
-    }
-    header[0] = more;
-    header[1] = w.u.t0;
-    header[2] = w.u.n;
-    header[3] = w.head;
-    header[4] = w.u.tile;
   }
   tc_fence_before();
   __syncthreads();
@@ -1072,6 +1133,19 @@ cudaError_t launch_attn_tile(const AttnArgs &a, cudaStream_t stream) {
     const uint32_t box[4] = {64, uint32_t(p.box), 1, 1};
     const cudaError_t e = make_tmap(v ? &p.tv : &p.tk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, pg.p,
                                     dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (e != cudaSuccess) return e;
+  }
+  // Rows by TMA where 128 of them are whole tokens, and the strides can be told.
+  const int group = a.q.n / a.c.heads;
+  const int64_t hs = a.q.n > 1 ? a.q.hs : a.c.D, ts = a.T > 1 ? a.q.ts : a.c.D;
+  p.q_tma = kTile % group == 0 && hs > 0 && ts > 0 && hs * 2 < (int64_t(1) << 40) &&
+            ts * 2 < (int64_t(1) << 40);
+  if (p.q_tma) {
+    const uint64_t dims[3] = {uint64_t(a.c.D), uint64_t(a.q.n), uint64_t(a.T)};
+    const uint64_t strides[2] = {uint64_t(hs) * 2, uint64_t(ts) * 2};
+    const uint32_t box[3] = {64, uint32_t(group), uint32_t(kTile / group)};
+    const cudaError_t e = make_tmap(&p.tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.q.p, dims,
+                                    strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
     if (e != cudaSuccess) return e;
   }
   p.q = a.q;

@@ -8,13 +8,14 @@
 namespace mnb {
 
 struct AttnTileParams {
-  CUtensorMap tk, tv;  // pages: head size / 64 halves of `box` tokens
+  CUtensorMap tk, tv;  // pages: 64 columns of `box` tokens
+  CUtensorMap tq;      // rows of q: 64 columns of 128 rows (q_tma)
   Heads q, o;
   BatchView b;
   int pages, page_size, box, kv_heads, G;
   int T, cap, window;
   float scale;    // |scale| times log2(e)
-  int negative;
+  int negative, q_tma;
   int64_t *line;  // [0]: blocks of a key head, [1]: units
   int64_t *first; // [units + 1]: first block of each unit, within a key head
   int4 *units;    // [2 units]: t0, n, len, tile; first block of keys, blocks
