@@ -663,54 +663,88 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F32>::per_sm)
 }
 
 // Joins the pieces of a unit: the one that begins at the end of block c's part
-// and the continuations at the start of the parts after it. A warp per row.
+// and the continuations at the start of the parts after it. Four rows at a
+// time, four warps for each row, which take every fourth piece: loads of all
+// pieces are in flight together, since the latency of three loads after one
+// another (header, maxima, sums) is what this kernel costs.
+constexpr int kJoinWarps = 16;
 template <int D, bool F32>
-__global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ AttnStreamParams p) {
+__global__ void __launch_bounds__(kJoinWarps * 32)
+    combine_kernel(const __grid_constant__ AttnStreamParams p) {
   using E = typename std::conditional<F32, float, uint16_t>::type;
   constexpr int kPer = D / 32;
-  const int lane = threadIdx.x & 31, row = blockIdx.y * 4 + (threadIdx.x >> 5);
+  constexpr int64_t kPart = kRows * (D + 2);
+  __shared__ float sums[kJoinWarps][D + 1];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, share = warp >> 2;
   grid_dependency_wait();
   grid_dependents_launch();
   const int *h = p.headers + blockIdx.x * kHeader;
   const int more = h[0];
   if (more == 0) return;
-  const int t0 = h[1], n = h[2], head = h[3], i = h[4] * kRows + row, tok = i / p.G;
-  if (tok >= n) return;
-  constexpr int64_t kPart = kRows * (D + 2);
+  const int t0 = h[1], n = h[2], head = h[3], tile = h[4];
   const float *first = p.parts + (int64_t(blockIdx.x) * 2 + 1) * kPart;
   const float *rest = p.parts + (int64_t(blockIdx.x) + 1) * 2 * kPart;
-  float m = -INFINITY;
-  for (int c = lane; c <= more; c += 32)
-    m = fmaxf(m, (c == 0 ? first : rest + (c - 1) * 2 * kPart)[kRows * D + row]);
+  auto piece = [&](int c) { return c == 0 ? first : rest + (c - 1) * 2 * kPart; };
+  for (int r0 = 0; r0 < kRows; r0 += 4) {
+    const int row = r0 + (warp & 3), i = tile * kRows + row, tok = i / p.G;
+    if ((tile * kRows + r0) / p.G >= n) return;
+    float m = -INFINITY;
+    for (int c = lane; c <= more; c += 32) m = fmaxf(m, piece(c)[kRows * D + row]);
 #pragma unroll
-  for (int s = 1; s < 32; s *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
-  const float z = m == -INFINITY ? 0.f : m;
-  float l = 0.f, a[kPer];
+    for (int s = 1; s < 32; s *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
+    const float z = m == -INFINITY ? 0.f : m;
+    float l = 0.f, a[kPer];
 #pragma unroll
-  for (int e = 0; e < kPer; ++e) a[e] = 0.f;
-#pragma unroll 4
-  for (int c = 0; c <= more; ++c) {
-    const float *x = c == 0 ? first : rest + (c - 1) * 2 * kPart;
-    const float f = exp2_fast((x[kRows * D + row] - z) * p.scale);
-    l += f * x[kRows * D + kRows + row];
-    const float *v = x + row * D + lane * kPer;
+    for (int e = 0; e < kPer; ++e) a[e] = 0.f;
+    // Lane j of a share has the factor of its piece 4 j + share of 128.
+    for (int c0 = 0; c0 <= more; c0 += 128) {
+      const int mine = c0 + 4 * lane + share;
+      float f = 0.f;
+      if (mine <= more) {
+        f = exp2_fast((piece(mine)[kRows * D + row] - z) * p.scale);
+        l += f * piece(mine)[kRows * D + kRows + row];
+      }
+      const int here = min(32, (more - c0 - share + 4) / 4);
+#pragma unroll 8
+      for (int j = 0; j < here; ++j) {
+        const float g = __shfl_sync(0xffffffffu, f, j);
+        const float *v = piece(c0 + 4 * j + share) + row * D + lane * kPer;
+#pragma unroll
+        for (int e = 0; e < kPer; e += 2) {
+          const float2 w = *reinterpret_cast<const float2 *>(v + e);
+          a[e] += g * w.x;
+          a[e + 1] += g * w.y;
+        }
+      }
+    }
+#pragma unroll
+    for (int s = 1; s < 32; s *= 2) l += __shfl_xor_sync(0xffffffffu, l, s);
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) sums[warp][lane * kPer + e] = a[e];
+    if (lane == 0) sums[warp][D] = l;
+    __syncthreads();
+    if (share != 0 || tok >= n) continue;
+    l = 0.f;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) a[e] = 0.f;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      l += sums[4 * s + warp][D];
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) a[e] += sums[4 * s + warp][lane * kPer + e];
+    }
+    const float inv = m == -INFINITY && l == 0.f ? 0.f : 1.f / l;
+    E *out = static_cast<E *>(p.o.p) + int64_t(t0 + tok) * p.o.ts +
+             int64_t(head * p.G + i - tok * p.G) * p.o.hs + lane * kPer;
 #pragma unroll
     for (int e = 0; e < kPer; e += 2) {
-      const float2 w = *reinterpret_cast<const float2 *>(v + e);
-      a[e] += f * w.x;
-      a[e + 1] += f * w.y;
+      if constexpr (F32)
+        *reinterpret_cast<float2 *>(out + e) = make_float2(a[e] * inv, a[e + 1] * inv);
+      else
+        *reinterpret_cast<uint32_t *>(out + e) =
+            bf16_bits(a[e] * inv) | (bf16_bits(a[e + 1] * inv) << 16);
     }
-  }
-  const float inv = m == -INFINITY && l == 0.f ? 0.f : 1.f / l;
-  E *out = static_cast<E *>(p.o.p) + int64_t(t0 + tok) * p.o.ts +
-           int64_t(head * p.G + i - tok * p.G) * p.o.hs + lane * kPer;
-#pragma unroll
-  for (int e = 0; e < kPer; e += 2) {
-    if constexpr (F32)
-      *reinterpret_cast<float2 *>(out + e) = make_float2(a[e] * inv, a[e + 1] * inv);
-    else
-      *reinterpret_cast<uint32_t *>(out + e) =
-          bf16_bits(a[e] * inv) | (bf16_bits(a[e + 1] * inv) << 16);
   }
 }
 
@@ -727,7 +761,8 @@ cudaError_t run(const AttnStreamParams &p, bool pdl, cudaStream_t stream) {
   const int grid = grid_blocks(F32, D);
   e = launch_after(stream_kernel<D, F32>, dim3(grid), kThreads, C::smem, pdl, stream, p);
   if (e != cudaSuccess) return e;
-  return launch_after(combine_kernel<D, F32>, dim3(grid, kRows / 4), 128, 0, pdl, stream, p);
+  return launch_after(combine_kernel<D, F32>, dim3(grid), kJoinWarps * 32, 0, pdl,
+                      stream, p);
 }
 
 size_t header_bytes(int grid) { return (size_t(grid) * kHeader * 4 + 255) & ~size_t(255); }

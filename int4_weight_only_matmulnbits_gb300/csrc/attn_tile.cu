@@ -405,15 +405,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *pfull = sfull + 2;
   uint64_t *qfull = pfull + 2;
   uint64_t *ofull = qfull + 2;
-  uint64_t *phalf = ofull + 2;          // the weights of the first 64 keys
-  uint64_t *toscan = phalf + 2;         // a masked block's values are to be looked over
+  uint64_t *toscan = ofull + 2;         // a masked block's values are to be looked over
   uint64_t *scanned = toscan + kInfo;   // and have been
   uint64_t *listed = scanned + kInfo;   // a piece is there
   uint64_t *taken = listed + kPieces;   // and has been read by every warp it concerns
   uint64_t *qfree = taken + kPieces;    // per tile: its rows have been used
   uint64_t *done = qfree + 2;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
-  static_assert((2 * C::stages + 3 * kInfo + 2 * kPieces + 13) * 8 + 4 <= 768, "barriers");
+  static_assert((2 * C::stages + 3 * kInfo + 2 * kPieces + 11) * 8 + 4 <= 768, "barriers");
   int *todo = reinterpret_cast<int *>(smem + C::off_todo);
   Piece *pieces = reinterpret_cast<Piece *>(smem + C::off_pieces);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -434,7 +433,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(sfull + i, 1);
-      mbar_init(phalf + i, 4);
       mbar_init(pfull + i, 4);
       mbar_init(qfull + i, p.q_tma ? 1 : 4);
       mbar_init(qfree + i, 1);
@@ -617,44 +615,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return s;
       };
-      // S_i = Q_i K^T; last: of the unit.
+      // Issued by the elected lane. S_i = Q_i K^T; last: of the unit.
       auto scores = [&](int i, int s, bool last, bool release) {
-        tc_fence_after();
         const uint64_t a = q_desc + i * (C::tile >> 4), b = k_desc + s * (C::tile >> 4);
-        if (ok && elect_one()) {
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint64_t step = (k / 4) * (C::half >> 4) + (k % 4) * 2;
-            umma_ss(tm + i * kTile, a + step, b + step, qk, k > 0);
-          }
-          umma_commit(sfull + i);
-          if (last) umma_commit(qfree + i);
-          if (release) umma_commit(empty + s);
+#pragma unroll 1
+        for (int k = 0; k < D / 16; ++k) {
+          const uint64_t step = (k / 4) * (C::half >> 4) + (k % 4) * 2;
+          umma_ss(tm + i * kTile, a + step, b + step, qk, k > 0);
         }
-        __syncwarp();
+        umma_commit(sfull + i);
+        if (last) umma_commit(qfree + i);
+        if (release) umma_commit(empty + s);
       };
-      // O_i += P_i V, for the tile's block n; the first half of the keys while the
-      // weights of the second are made.
-      auto values = [&](int i, int s, int n, bool fresh, bool release) {
-        wait(phalf + i, n);
-        tc_fence_after();
+      // O_i += P_i V.
+      auto values = [&](int i, int s, bool fresh, bool release) {
         const uint64_t b = v_desc + s * (C::tile >> 4);
-        if (ok && elect_one()) {
-          umma_ts(tm + 2 * kTile + i * kTile, tm + i * kTile, b, kPv, !fresh);
+        umma_ts(tm + 2 * kTile + i * kTile, tm + i * kTile, b, kPv, !fresh);
 #pragma unroll
-          for (int k = 1; k < kTile / 32; ++k)
-            umma_ts(tm + 2 * kTile + i * kTile, tm + i * kTile + k * 8, b + k * (2048 >> 4), kPv, 1);
-        }
-        __syncwarp();
-        wait(pfull + i, n);
-        tc_fence_after();
-        if (ok && elect_one()) {
-#pragma unroll
-          for (int k = kTile / 32; k < kTile / 16; ++k)
-            umma_ts(tm + 2 * kTile + i * kTile, tm + i * kTile + k * 8, b + k * (2048 >> 4), kPv, 1);
-          if (release) umma_commit(empty + s);
-        }
-        __syncwarp();
+        for (int k = 1; k < kTile / 16; ++k)
+          umma_ts(tm + 2 * kTile + i * kTile, tm + i * kTile + k * 8, b + k * (2048 >> 4), kPv, 1);
+        if (release) umma_commit(empty + s);
       };
       for (int pn = 0; ok; ++pn) {
         const Piece pc = take_piece(pn, ok);
@@ -663,31 +643,41 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok || uniform(pc.none)) break;
         wait(qfull, units0++);
         int ks = take();
-        scores(0, ks, n == 1, !two);
+        tc_fence_after();
+        if (ok && elect_one()) scores(0, ks, n == 1, !two);
+        __syncwarp();
         if (two) {
           wait(qfull + 1, units1++);
-          scores(1, ks, n == 1, true);
+          tc_fence_after();
+          if (ok && elect_one()) scores(1, ks, n == 1, true);
+          __syncwarp();
         }
+        // What a block needs besides the weights is waited for ahead of them.
         for (int kb = 0; kb < n && ok; ++kb) {
-          const bool more = kb + 1 < n;
+          const bool more = kb + 1 < n, last = kb + 2 == n;
           const int vs = take();
-          values(0, vs, blocks0++, kb == 0, !two);
-          if (more) {
-            ks = take();
-            scores(0, ks, kb + 2 == n, !two);
-          } else {
-            if (ok && elect_one()) umma_commit(ofull);
-            __syncwarp();
+          if (more) ks = take();
+          wait(pfull, blocks0++);
+          tc_fence_after();
+          if (ok && elect_one()) {
+            values(0, vs, kb == 0, !two);
+            if (more)
+              scores(0, ks, last, !two);
+            else
+              umma_commit(ofull);
           }
-          if (two) {
-            values(1, vs, blocks1++, kb == 0, true);
-            if (more) {
-              scores(1, ks, kb + 2 == n, true);
-            } else {
-              if (ok && elect_one()) umma_commit(ofull + 1);
-              __syncwarp();
-            }
+          __syncwarp();
+          if (!two) continue;
+          wait(pfull + 1, blocks1++);
+          tc_fence_after();
+          if (ok && elect_one()) {
+            values(1, vs, kb == 0, true);
+            if (more)
+              scores(1, ks, last, true);
+            else
+              umma_commit(ofull + 1);
           }
+          __syncwarp();
         }
         if (!uniform(pc.more)) break;
       }
@@ -890,10 +880,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           };
           weights(0, s0);
           weights(32, s1);
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(phalf + i);
           weights(64, s2);
           weights(96, s3);
           float la, lb;
