@@ -3,7 +3,9 @@
 Each translation unit compiles in parallel to an object under ``_build/``;
 the objects link into ``libmnb.so`` next to this file, with the CUDA runtime
 linked statically so the library does not depend on which runtime another
-package in the process loaded.
+package in the process loaded. Beside it goes ``_mnb_py.so``, the part of the
+Python binding that is written against the CPython C API; it calls
+``libmnb.so`` (found next to it) and holds no computation.
 """
 from __future__ import annotations
 
@@ -11,12 +13,15 @@ import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OBJ_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libmnb.so")
+PY_SRC = os.path.join(CSRC, "py_attn.cpp")
+PY_PATH = os.path.join(PKG, "_mnb_py.so")
 HEADER = os.path.join(ROOT, "include", "mnb.h")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -79,6 +84,23 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
         if res.returncode != 0:
             raise RuntimeError(f"link failed:\n{res.stdout}{res.stderr}")
         os.replace(tmp, LIB_PATH)
+
+    # Python.h's version is part of what the module is built for: another
+    # interpreter's is stale.
+    stamp = os.path.join(OBJ_DIR, "_mnb_py.abi")
+    abi = sysconfig.get_config_var("SOABI") or ""
+    old = open(stamp).read() if os.path.exists(stamp) else None
+    if force or old != abi or _stale(PY_PATH, [PY_SRC, HEADER]):
+        tmp = PY_PATH + f".tmp{os.getpid()}"
+        cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC",
+               "-fvisibility=hidden", "-I" + sysconfig.get_paths()["include"], PY_SRC, "-o", tmp,
+               "-L" + PKG, "-l:libmnb.so", "-Wl,-rpath,$ORIGIN"]
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError(f"g++ failed for {PY_SRC}:\n{res.stdout}{res.stderr}")
+        os.replace(tmp, PY_PATH)
+        with open(stamp, "w") as f:
+            f.write(abi)
     return LIB_PATH
 
 

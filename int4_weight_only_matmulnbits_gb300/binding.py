@@ -8,6 +8,8 @@ immediately; there is no fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import threading
 from dataclasses import dataclass
@@ -1027,10 +1029,6 @@ class KvCache:
     k: torch.Tensor
     v: torch.Tensor
 
-    def __getstate__(self):
-        """Copied and pickled without the argument struct (addresses)."""
-        return {n: t for n, t in self.__dict__.items() if n != "_struct"}
-
 
 @dataclass(frozen=True)
 class KvBatch:
@@ -1041,86 +1039,33 @@ class KvBatch:
     lengths: torch.Tensor  # [n]
     table: torch.Tensor    # [n, pages of the longest sequence]
 
-    def __getstate__(self):
-        """Copied and pickled without the argument struct (addresses)."""
-        return {n: t for n, t in self.__dict__.items() if n != "_struct"}
+
+_native_mod = None
 
 
-def _heads_struct(name: str, t: torch.Tensor, device, like: torch.Tensor | None = None) -> HeadsC:
-    """mnb_heads of a [T, heads, head_dim] tensor whose last dimension is
-    contiguous."""
-    if t.dim() != 3 or t.device != device or not t.is_cuda:
-        raise ValueError(f"{name} must be a [T, heads, head_dim] tensor on {device}")
-    s = t.stride()
-    if s[2] != 1 and t.shape[2] != 1:
-        raise ValueError(f"{name}'s heads must be contiguous")
-    if like is not None and (t.dtype != like.dtype or t.shape[0] != like.shape[0]
-                             or t.shape[2] != like.shape[2]):
-        raise ValueError(f"{name} must have the rows, head size and dtype of the call's others")
-    return HeadsC(t.data_ptr(), s[0], s[1], t.shape[1], 0)
+def _native():
+    """The marshalling of the calls below (csrc/py_attn.cpp), set up once."""
+    global _native_mod
+    if _native_mod is None:
+        load()
+        path = _build.PY_PATH
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it with "
+                               "`python -c 'import __graft_entry__ as g; g.build()'`")
+        loader = importlib.machinery.ExtensionFileLoader("_mnb_py", path)
+        mod = importlib.util.module_from_spec(
+            importlib.util.spec_from_file_location("_mnb_py", path, loader=loader))
+        loader.exec_module(mod)
+        mod.setup(torch, _check)
+        _native_mod = mod
+    return _native_mod
 
 
-def _cache_struct(c: KvCache, device) -> KvCacheC:
-    """mnb_kv_cache of c, kept with it for as long as its tensors are where
-    they were."""
-    at = (c.k.data_ptr(), c.v.data_ptr())
-    kept = c.__dict__.get("_struct")
-    if kept is None or kept[0] != at:
-        if c.k.dim() != 4 or c.v.shape != c.k.shape or c.v.dtype != c.k.dtype:
-            raise ValueError("k and v must be [pages, heads, page_size, head_dim] tensors of "
-                             "one dtype")
-        if not c.k.is_cuda or c.v.device != c.k.device:
-            raise ValueError("k and v must be on one GPU")
-        if c.k.stride(3) != 1 or c.v.stride(3) != 1:
-            raise ValueError("the rows of k and v must be contiguous")
-        pages, heads, page_size, D = c.k.shape
-        kept = (at, KvCacheC(*at, pages, *c.k.stride()[:3], *c.v.stride()[:3], page_size, heads,
-                             D, _dtype_code(c.k.dtype)))
-        c.__dict__["_struct"] = kept
-    if c.k.device != device:
-        raise ValueError(f"the cache is on {c.k.device}, the call runs on {device}")
-    return kept[1]
-
-
-def _batch_struct(b: KvBatch, device) -> KvBatchC:
-    """mnb_kv_batch of b, kept with it as _cache_struct's."""
-    at = (b.starts.data_ptr(), b.lengths.data_ptr(), b.table.data_ptr())
-    kept = b.__dict__.get("_struct")
-    if kept is None or kept[0] != at:
-        n = b.lengths.shape[0] if b.lengths.dim() == 1 else -1
-        if b.starts.shape != (n + 1,) or b.table.dim() != 2 or b.table.shape[0] != n:
-            raise ValueError("a batch of n sequences has starts [n + 1], lengths [n] and "
-                             "table [n, pages]")
-        for name, t in (("starts", b.starts), ("lengths", b.lengths), ("table", b.table)):
-            if t.dtype != torch.int32 or not t.is_cuda or t.device != b.table.device:
-                raise ValueError(f"{name} must be int32, on the batch's GPU")
-            if t.numel() and t.stride(-1) != 1:
-                raise ValueError(f"{name} must be contiguous")
-        kept = (at, KvBatchC(*at, n, b.table.shape[1],
-                             b.table.stride(0) if n > 1 else b.table.shape[1]))
-        b.__dict__["_struct"] = kept
-    if b.table.device != device:
-        raise ValueError(f"the batch is on {b.table.device}, the call runs on {device}")
-    return kept[1]
-
-
-def _rope_struct(r: RopeTable, interleaved: bool, device) -> RopeC:
-    _on_gpu("cos", r.cos, device)
-    _on_gpu("sin", r.sin, device)
-    if r.cos.dim() != 2 or r.sin.shape != r.cos.shape or not (
-            r.cos.dtype == r.sin.dtype == torch.float32):
-        raise ValueError("cos and sin must be fp32 [positions, rot_dim / 2] tensors")
-    return RopeC(r.cos.data_ptr(), r.sin.data_ptr(), r.cos.shape[0], 2 * r.cos.shape[1],
-                 1 if interleaved else 0)
-
-
-def _gamma(name: str, t: torch.Tensor | None, D: int, device):
-    if t is None:
-        return None
-    _on_gpu(name, t, device)
-    if t.dtype != torch.float32 or t.shape != (D,):
-        raise ValueError(f"{name} must be an fp32 [{D}] tensor")
-    return t.data_ptr()
+def _elsewhere(t: torch.Tensor, stream, fn, *args):
+    """fn(*args) on t's device, which is not the current one, or on `stream`."""
+    if not t.is_cuda:
+        raise ValueError("the call's tensors must be on a GPU")
+    return _call_on(t.device, stream, lambda _: fn(*args))
 
 
 def mnb_rope_frequencies(rot_dim: int, base: float = 1e6, *, factor: float = 1.0,
@@ -1168,33 +1113,13 @@ def mnb_qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, rope: RopeTable | 
     [head_dim]) and their rotation by positions (int32 [T]), in one pass:
     (q, k) of the same shapes. out_q and out_k may be q and k. k may be None
     (and comes back as None); a position outside the table gives zeros."""
-    dev, D = q.device, q.shape[-1]
-    qs = _heads_struct("q", q, dev)
-    ks = None if k is None else _heads_struct("k", k, dev, q)
-    rs = None if rope is None else _rope_struct(rope, interleaved, dev)
-    if positions is not None:
-        _on_gpu("positions", positions, dev)
-        if positions.dtype != torch.int32 or positions.shape != (q.shape[0],):
-            raise ValueError("positions must be an int32 [T] tensor")
-    if k is None and out_k is not None:
-        raise ValueError("out_k without k")
-    gq, gk = _gamma("gamma_q", gamma_q, D, dev), _gamma("gamma_k", gamma_k, D, dev)
-    lib, code = _lib or load(), _dtype_code(q.dtype)
-    given = [_heads_struct(n, t, dev, q) if t is not None else None
-             for n, t in (("out_q", out_q), ("out_k", out_k))]
-
-    def call(s):
-        yq = torch.empty(q.shape, dtype=q.dtype, device=dev) if out_q is None else out_q
-        yk = k
-        if k is not None:
-            yk = torch.empty(k.shape, dtype=k.dtype, device=dev) if out_k is None else out_k
-        oq = given[0] or _heads_struct("out_q", yq, dev)
-        ok = None if k is None else given[1] or _heads_struct("out_k", yk, dev)
-        _check(lib.mnb_qk_norm_rope(qs, ks, q.shape[0], D, code, gq, gk, eps, rs,
-                                    None if positions is None else positions.data_ptr(), oq, ok,
-                                    s), "mnb_qk_norm_rope")
-        return yq, yk
-    return _call_on(dev, stream, call)
+    fn = (_native_mod or _native()).qk_norm_rope
+    args = (q, k, rope, positions, gamma_q, gamma_k, eps, interleaved, out_q, out_k)
+    if stream is None:
+        y = fn(*args)
+        if y is not NotImplemented:
+            return y
+    return _elsewhere(q, stream, fn, *args)
 
 
 def mnb_cache_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, cache: KvCache,
@@ -1206,30 +1131,13 @@ def mnb_cache_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, c
     the batch's new tokens; k and v [T, heads, head_dim] go into the cache, q
     [T, q heads, head_dim] is returned (in out, which may be q). Rows of no
     sequence are left as they were."""
-    dev, D = k.device, k.shape[-1]
-    if k.dtype != cache.k.dtype or D != cache.k.shape[3] or (
-            k.dim() == 3 and k.shape[1] != cache.k.shape[1]):
-        raise ValueError("k must have the heads, head size and dtype of the cache")
-    ks = _heads_struct("k", k, dev)
-    vs = _heads_struct("v", v, dev, k)
-    qs = None if q is None else _heads_struct("q", q, dev, k)
-    if q is None and out is not None:
-        raise ValueError("out without q")
-    os_ = None if out is None else _heads_struct("out", out, dev, k)
-    rs = None if rope is None else _rope_struct(rope, interleaved, dev)
-    cs, bs = _cache_struct(cache, dev), _batch_struct(batch, dev)
-    gq, gk = _gamma("gamma_q", gamma_q, D, dev), _gamma("gamma_k", gamma_k, D, dev)
-    lib = _lib or load()
-
-    def call(s):
-        y, ys = out, os_
-        if q is not None and out is None:
-            y = torch.empty(q.shape, dtype=q.dtype, device=dev)
-            ys = _heads_struct("out", y, dev)
-        _check(lib.mnb_cache_append(qs, ks, vs, k.shape[0], gq, gk, eps, rs, cs, bs, ys, s),
-               "mnb_cache_append")
-        return y
-    return _call_on(dev, stream, call)
+    fn = (_native_mod or _native()).cache_append
+    args = (q, k, v, cache, batch, rope, gamma_q, gamma_k, eps, interleaved, out)
+    if stream is None:
+        y = fn(*args)
+        if y is not NotImplemented:
+            return y
+    return _elsewhere(k, stream, fn, *args)
 
 
 def mnb_paged_attention(q: torch.Tensor, cache: KvCache, batch: KvBatch, *,
@@ -1239,26 +1147,10 @@ def mnb_paged_attention(q: torch.Tensor, cache: KvCache, batch: KvBatch, *,
     its pages of the cache up to their own positions (and over the last
     `window` keys alone, when given): [T, q heads, head_dim]. scale is 1 /
     sqrt(head_dim) unless given. Rows of no sequence are left as they were."""
-    dev = q.device
-    qs = _heads_struct("q", q, dev)
-    if q.dtype != cache.k.dtype or q.shape[2] != cache.k.shape[3]:
-        raise ValueError("q must have the head size and dtype of the cache")
-    os_ = None
-    if out is not None:
-        os_ = _heads_struct("out", out, dev, q)
-    cs, bs = _cache_struct(cache, dev), _batch_struct(batch, dev)
-    lib, T, hq = _lib or load(), q.shape[0], q.shape[1]
-    if scale is None:
-        scale = q.shape[2] ** -0.5
-
-    def call(s):
-        y, ys = out, os_
-        if out is None:
-            y = torch.empty(q.shape, dtype=q.dtype, device=dev)
-            ys = _heads_struct("out", y, dev)
-        n = lib.mnb_paged_attention_workspace_size(T, hq, cs, bs)
-        ws, wp = _workspace(n, dev)
-        _check(lib.mnb_paged_attention(qs, T, cs, bs, scale, window, ys, wp, n, s),
-               "mnb_paged_attention")
-        return y
-    return _call_on(dev, stream, call)
+    fn = (_native_mod or _native()).paged_attention
+    args = (q, cache, batch, scale, window, out)
+    if stream is None:
+        y = fn(*args)
+        if y is not NotImplemented:
+            return y
+    return _elsewhere(q, stream, fn, *args)

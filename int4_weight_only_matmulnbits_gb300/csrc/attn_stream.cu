@@ -37,7 +37,7 @@ constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kRows = 16;         // query rows of a unit
 constexpr int kWarpKeys = 16;     // keys of a warp's step
 constexpr int kBlockKeys = kWarps * kWarpKeys;
-constexpr int kMinBlocks = 2;     // of the line per block of the grid
+constexpr int kMinBlocks = 1;     // of the line per block of the grid
 constexpr int kHeader = 8;        // ints of a piece's header
 
 template <int D, bool F32>
