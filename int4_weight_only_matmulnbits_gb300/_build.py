@@ -4,16 +4,18 @@ Each translation unit compiles in parallel to an object under ``_build/``;
 the objects link into ``libmnb.so`` next to this file, with the CUDA runtime
 linked statically so the library does not depend on which runtime another
 package in the process loaded. Beside it goes ``_mnb_py.so``, the part of the
-Python binding that is written against the CPython C API; it calls
+Python binding that reads tensors through torch's C++ interface; it calls
 ``libmnb.so`` (found next to it) and holds no computation.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
 import sysconfig
+import zlib
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -52,6 +54,41 @@ def _stale(target: str, deps: list[str]) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _gxx() -> str:
+    return shutil.which("g++") or "g++"
+
+
+def _torch_dir() -> str:
+    """Where torch is installed, without importing it."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.origin:
+        raise RuntimeError("torch not found: the Python binding is built against it")
+    return os.path.dirname(spec.origin)
+
+
+def _compile_py(force: bool) -> str:
+    """The object of the Python binding's native part. The interpreter and the
+    torch that it is compiled for are part of its name: another's is stale."""
+    torch_dir = _torch_dir()
+    with open(os.path.join(torch_dir, "version.py")) as f:
+        made_for = (sysconfig.get_config_var("SOABI") or "") + torch_dir + f.read()
+    obj = os.path.join(OBJ_DIR, f"py_attn.{zlib.crc32(made_for.encode()):08x}.o")
+    if not force and not _stale(obj, [PY_SRC, HEADER]):
+        return obj
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    include = os.path.join(torch_dir, "include")
+    tmp = f"{obj}.tmp{os.getpid()}"
+    cmd = [_gxx(), "-O2", "-std=c++20", "-fPIC", "-fvisibility=hidden", "-w",
+           "-isystem", include, "-isystem", os.path.join(include, "torch/csrc/api/include"),
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(cuda, "include"),
+           "-c", PY_SRC, "-o", tmp]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed for {PY_SRC}:\n{res.stdout}{res.stderr}")
+    os.replace(tmp, obj)
+    return obj
+
+
 def build_library(force: bool = False, verbose: bool = False) -> str:
     """Compile (if stale) and return the path of libmnb.so."""
     os.makedirs(OBJ_DIR, exist_ok=True)
@@ -75,7 +112,9 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+        py = ex.submit(_compile_py, force)
         list(ex.map(compile_one, zip(srcs, objs)))
+        py_obj = py.result()
 
     if force or _stale(LIB_PATH, objs):
         tmp = LIB_PATH + f".tmp{os.getpid()}"
@@ -85,22 +124,16 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"link failed:\n{res.stdout}{res.stderr}")
         os.replace(tmp, LIB_PATH)
 
-    # Python.h's version is part of what the module is built for: another
-    # interpreter's is stale.
-    stamp = os.path.join(OBJ_DIR, "_mnb_py.abi")
-    abi = sysconfig.get_config_var("SOABI") or ""
-    old = open(stamp).read() if os.path.exists(stamp) else None
-    if force or old != abi or _stale(PY_PATH, [PY_SRC, HEADER]):
+    if force or _stale(PY_PATH, [py_obj]):
+        torch_lib = os.path.join(_torch_dir(), "lib")
         tmp = PY_PATH + f".tmp{os.getpid()}"
-        cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC",
-               "-fvisibility=hidden", "-I" + sysconfig.get_paths()["include"], PY_SRC, "-o", tmp,
-               "-L" + PKG, "-l:libmnb.so", "-Wl,-rpath,$ORIGIN"]
+        cmd = [_gxx(), "-shared", "-o", tmp, py_obj, "-L" + PKG, "-l:libmnb.so", "-L" + torch_lib,
+               "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10",
+               "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + torch_lib]
         res = subprocess.run(cmd, capture_output=True, text=True)
         if res.returncode != 0:
-            raise RuntimeError(f"g++ failed for {PY_SRC}:\n{res.stdout}{res.stderr}")
+            raise RuntimeError(f"link failed:\n{res.stdout}{res.stderr}")
         os.replace(tmp, PY_PATH)
-        with open(stamp, "w") as f:
-            f.write(abi)
     return LIB_PATH
 
 

@@ -1056,7 +1056,7 @@ def _native():
         mod = importlib.util.module_from_spec(
             importlib.util.spec_from_file_location("_mnb_py", path, loader=loader))
         loader.exec_module(mod)
-        mod.setup(torch, _check)
+        mod.setup(_check)
         _native_mod = mod
     return _native_mod
 
@@ -1084,24 +1084,21 @@ def mnb_rope_table(frequencies: torch.Tensor, n: int, *, first: int = 0, magnitu
                    device=None, stream=None) -> RopeTable:
     """Cosines and sines of the positions first .. first + n - 1, times
     magnitude, for the frequencies (float64, on the CPU)."""
-    if frequencies.is_cuda or frequencies.dtype != torch.float64 or frequencies.dim() != 1 or (
-            not frequencies.is_contiguous()):
+    if frequencies.is_cuda or frequencies.dtype != torch.float64:
         raise ValueError("frequencies must be a contiguous float64 vector on the CPU")
-    if device is None:
-        dev = torch.device("cuda", torch.cuda.current_device() if stream is None
-                           else stream.device.index)
-    else:
+    if device is not None:
         dev = torch.device(device)
-        if dev.index is None:
-            dev = torch.device(dev.type, torch.cuda.current_device())
-    pairs = frequencies.shape[0]
-
-    def call(s):
-        cos, sin = (torch.empty(n, pairs, dtype=torch.float32, device=dev) for _ in range(2))
-        _check(load().mnb_rope_table(frequencies.data_ptr(), 2 * pairs, first, n, magnitude,
-                                     cos.data_ptr(), sin.data_ptr(), s), "mnb_rope_table")
-        return RopeTable(cos, sin)
-    return _call_on(dev, stream, call)
+    else:
+        dev = torch.device("cuda") if stream is None else stream.device
+    if dev.type != "cuda":
+        raise ValueError("the tables are made on a GPU")
+    here = torch.cuda.current_device()
+    index = here if dev.index is None else dev.index
+    fn = (_native_mod or _native()).rope_table
+    if stream is None and index == here:
+        return RopeTable(*fn(frequencies, n, first, magnitude, index))
+    return _call_on(torch.device("cuda", index), stream,
+                    lambda _: RopeTable(*fn(frequencies, n, first, magnitude, index)))
 
 
 def mnb_qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, rope: RopeTable | None,

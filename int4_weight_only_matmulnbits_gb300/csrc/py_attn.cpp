@@ -1,15 +1,20 @@
-// Argument marshalling of the attention block's calls for the Python binding
-// (CPython C API): tensors are described by their own methods, checked, and
-// handed to the C ABI. These calls run a few microseconds on the GPU in a
-// decode step; the same marshalling through ctypes took 20 to 30 on the host,
-// here it takes 5 to 9.
+// Argument marshalling of the attention block's calls for the Python binding:
+// tensors are read through torch's C++ interface, checked, and handed to the C
+// ABI; outputs and workspaces are torch's. These calls run a few microseconds
+// on the GPU in a decode step: through ctypes they took 20 to 30 on the host,
+// and much of that was a dozen small Python calls into torch for each.
 //
 // Every function works on the current device and its current stream, and
 // returns NotImplemented for tensors of another device; the Python functions
 // around them (binding.py) then change over, and hold the documentation.
 #define PY_SSIZE_T_CLEAN
-#include <Python.h>
+#include <torch/csrc/autograd/python_variable.h>
 
+#include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAStream.h>
+
+#include <cmath>
 #include <cstdarg>
 #include <cstdint>
 
@@ -17,10 +22,8 @@
 
 namespace {
 
-// Names and objects of torch, looked up when the module is set up.
-PyObject *s_data_ptr, *s_stride, *s_shape, *s_dtype, *s_get_device, *s_new_empty, *s_cos, *s_sin,
-    *s_k, *s_v, *s_starts, *s_lengths, *s_table;
-PyObject *t_f32, *t_bf16, *t_i32, *t_u8, *raw_stream, *current_device, *check_status, *kw_u8;
+PyObject *s_cos, *s_sin, *s_k, *s_v, *s_starts, *s_lengths, *s_table;  // interned names
+PyObject *check_status;
 
 struct Ref {  // an owned reference
   PyObject *p;
@@ -48,50 +51,28 @@ struct Tensor {
   long device = -1;
   int dims = 0;
   int64_t shape[4] = {}, stride[4] = {};
-  PyObject *dtype = nullptr;  // (torch's dtypes live as long as torch)
+  at::ScalarType dtype = at::kByte;
 };
 
-bool call_long(PyObject *o, PyObject *name, int64_t &v) {
-  Ref r(PyObject_CallMethodNoArgs(o, name));
-  if (!r.p) return false;
-  v = static_cast<int64_t>(PyLong_AsUnsignedLongLongMask(r.p));
-  return !PyErr_Occurred();
-}
-
-bool ints_of(PyObject *t, int64_t (&out)[4], int &n) {
-  if (!PyTuple_Check(t)) return refuse("not a tensor");
-  const Py_ssize_t k = PyTuple_GET_SIZE(t);
-  n = static_cast<int>(k);
-  for (Py_ssize_t i = 0; i < k && i < 4; ++i) {
-    out[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(t, i));
-    if (out[i] == -1 && PyErr_Occurred()) return false;
-  }
-  return true;
-}
-
 bool describe(PyObject *o, const char *name, Tensor &t) {
-  Ref shape(PyObject_GetAttr(o, s_shape));
-  if (!shape.p) {
-    PyErr_Clear();
-    return refuse("%s must be a tensor", name);
+  if (!THPVariable_Check(o)) return refuse("%s must be a tensor", name);
+  const at::Tensor &x = THPVariable_Unpack(o);
+  if (!x.defined() || x.layout() != at::kStrided) return refuse("%s must be a dense tensor", name);
+  t.dims = static_cast<int>(x.dim());
+  for (int i = 0; i < t.dims && i < 4; ++i) {
+    t.shape[i] = x.size(i);
+    t.stride[i] = x.stride(i);
   }
-  Ref stride(PyObject_CallMethodNoArgs(o, s_stride)), dtype(PyObject_GetAttr(o, s_dtype));
-  if (!stride.p || !dtype.p) return false;
-  int n = 0;
-  int64_t at = 0, dev = 0;
-  if (!ints_of(shape.p, t.shape, t.dims) || !ints_of(stride.p, t.stride, n) ||
-      !call_long(o, s_data_ptr, at) || !call_long(o, s_get_device, dev))
-    return false;
-  t.ptr = static_cast<uint64_t>(at);
-  t.device = static_cast<long>(dev);
-  t.dtype = dtype.p;
+  t.ptr = reinterpret_cast<uint64_t>(x.const_data_ptr());
+  t.device = x.is_cuda() ? x.get_device() : -1;
+  t.dtype = x.scalar_type();
   return true;
 }
 
-int dtype_code(PyObject *d) {
-  if (d == t_f32) return MNB_F32;
-  if (d == t_bf16) return MNB_BF16;
-  PyErr_Format(PyExc_TypeError, "unsupported dtype %R: fp32 or bf16", d);
+int dtype_code(at::ScalarType d) {
+  if (d == at::kFloat) return MNB_F32;
+  if (d == at::kBFloat16) return MNB_BF16;
+  PyErr_Format(PyExc_TypeError, "unsupported dtype %s: fp32 or bf16", c10::toString(d));
   return -1;
 }
 
@@ -132,26 +113,17 @@ bool rows_of(PyObject *o, const char *name, long device, const Rows *like, Rows 
   return true;
 }
 
-// An output: the caller's tensor, or a new one of `like`'s shape.
-PyObject *output(PyObject *given, PyObject *like, const char *name, const Rows &in, Rows &r) {
-  Ref made;
-  if (given == Py_None) {
-    Ref shape(PyObject_GetAttr(like, s_shape));
-    if (!shape.p) return nullptr;
-    made.p = PyObject_CallMethodOneArg(like, s_new_empty, shape.p);
-    if (!made.p) return nullptr;
-    int64_t at = 0;
-    if (!call_long(made.p, s_data_ptr, at)) return nullptr;
-    r.t = in.t;
-    r.t.ptr = static_cast<uint64_t>(at);
-    r.h = mnb_heads{reinterpret_cast<void *>(at), in.t.shape[1] * in.t.shape[2], in.t.shape[2],
-                    in.h.heads, 0};
-  } else {
-    Py_INCREF(given);
-    made.p = given;
-    if (!rows_of(given, name, in.t.device, &in, r)) return nullptr;
-  }
-  return made.take();
+// An output: the caller's tensor, or a new one of the input's shape.
+PyObject *output(PyObject *given, const char *name, const Rows &in, Rows &r) {
+  if (given != Py_None) return rows_of(given, name, in.t.device, &in, r) ? Py_NewRef(given) : nullptr;
+  const at::Tensor y =
+      at::empty({in.t.shape[0], in.t.shape[1], in.t.shape[2]},
+                at::TensorOptions().dtype(in.t.dtype).device(at::kCUDA, in.t.device));
+  r.t = in.t;
+  r.t.ptr = reinterpret_cast<uint64_t>(y.mutable_data_ptr());
+  r.h = mnb_heads{reinterpret_cast<void *>(r.t.ptr), in.t.shape[1] * in.t.shape[2], in.t.shape[2],
+                  in.h.heads, 0};
+  return THPVariable_Wrap(y);
 }
 
 bool gamma_of(PyObject *o, const char *name, int64_t D, long device, const float *&p) {
@@ -159,7 +131,7 @@ bool gamma_of(PyObject *o, const char *name, int64_t D, long device, const float
   if (o == Py_None) return true;
   Tensor t;
   if (!describe(o, name, t) || !on_device(t, name, device)) return false;
-  if (t.dtype != t_f32 || t.dims != 1 || t.shape[0] != D || !contiguous(t))
+  if (t.dtype != at::kFloat || t.dims != 1 || t.shape[0] != D || !contiguous(t))
     return refuse("%s must be a contiguous fp32 [%lld] tensor", name, (long long)D);
   p = reinterpret_cast<const float *>(t.ptr);
   return true;
@@ -173,7 +145,7 @@ bool rope_of(PyObject *o, int interleaved, long device, mnb_rope &r) {
       !on_device(ts, "sin", device))
     return false;
   if (tc.dims != 2 || ts.dims != 2 || tc.shape[0] != ts.shape[0] || tc.shape[1] != ts.shape[1] ||
-      tc.dtype != t_f32 || ts.dtype != t_f32 || !contiguous(tc) || !contiguous(ts))
+      tc.dtype != at::kFloat || ts.dtype != at::kFloat || !contiguous(tc) || !contiguous(ts))
     return refuse("cos and sin must be contiguous fp32 [positions, rot_dim / 2] tensors");
   if (tc.shape[1] > (1 << 20)) return refuse("cos and sin are too wide");
   r = mnb_rope{reinterpret_cast<const float *>(tc.ptr), reinterpret_cast<const float *>(ts.ptr),
@@ -229,7 +201,7 @@ bool batch_of(PyObject *o, long device, mnb_kv_batch &b) {
   const char *names[] = {"starts", "lengths", "table"};
   for (int i = 0; i < 3; ++i) {
     if (!on_device(*all[i], names[i], device)) return false;
-    if (all[i]->dtype != t_i32) return refuse("%s must be int32", names[i]);
+    if (all[i]->dtype != at::kInt) return refuse("%s must be int32", names[i]);
     const int last = all[i]->dims - 1;
     if (all[i]->stride[last] != 1 && all[i]->shape[last] > 1)
       return refuse("%s must be contiguous", names[i]);
@@ -243,27 +215,10 @@ bool batch_of(PyObject *o, long device, mnb_kv_batch &b) {
   return true;
 }
 
-// 1: `device` is the current one, 0: another is, -1: an error.
-int is_current(long device) {
-  Ref d(PyObject_CallNoArgs(current_device));
-  if (!d.p) return -1;
-  const long now = PyLong_AsLong(d.p);
-  return PyErr_Occurred() ? -1 : now == device;
-}
-#define MNB_CURRENT_OR_RETURN(device)                     \
-  do {                                                    \
-    const int here_ = is_current(device);                 \
-    if (here_ < 0) return nullptr;                        \
-    if (here_ == 0) return Py_NewRef(Py_NotImplemented);  \
-  } while (0)
-
-bool stream_of(long device, mnb_stream_t &s) {
-  Ref d(PyLong_FromLong(device));
-  if (!d.p) return false;
-  Ref r(PyObject_CallOneArg(raw_stream, d.p));
-  if (!r.p) return false;
-  s = reinterpret_cast<mnb_stream_t>(PyLong_AsUnsignedLongLongMask(r.p));
-  return !PyErr_Occurred();
+bool is_current(long device) { return c10::cuda::current_device() == device; }
+mnb_stream_t stream_of(long device) {
+  return reinterpret_cast<mnb_stream_t>(
+      c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(device)).stream());
 }
 
 bool status_ok(mnb_status st, const char *where) {
@@ -279,7 +234,7 @@ PyObject *qk_norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
   Rows q, k, oq, ok;
   if (!rows_of(a[0], "q", -1, nullptr, q)) return nullptr;
   const long dev = q.t.device;
-  MNB_CURRENT_OR_RETURN(dev);
+  if (!is_current(dev)) return Py_NewRef(Py_NotImplemented);
   const bool has_k = a[1] != Py_None;
   if (has_k && !rows_of(a[1], "k", dev, &q, k)) return nullptr;
   mnb_rope rope;
@@ -291,7 +246,7 @@ PyObject *qk_norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
   if (a[3] != Py_None) {
     Tensor t;
     if (!describe(a[3], "positions", t) || !on_device(t, "positions", dev)) return nullptr;
-    if (t.dtype != t_i32 || t.dims != 1 || t.shape[0] != q.t.shape[0] || !contiguous(t))
+    if (t.dtype != at::kInt || t.dims != 1 || t.shape[0] != q.t.shape[0] || !contiguous(t))
       return refuse("positions must be a contiguous int32 [T] tensor"), nullptr;
     pos = reinterpret_cast<const int32_t *>(t.ptr);
   }
@@ -303,17 +258,16 @@ PyObject *qk_norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
   const int code = dtype_code(q.t.dtype);
   if (code < 0) return nullptr;
   if (q.t.shape[2] > INT32_MAX) return refuse("q's heads are too long"), nullptr;
-  Ref yq(output(a[8], a[0], "out_q", q, oq));
+  Ref yq(output(a[8], "out_q", q, oq));
   if (!yq.p) return nullptr;
   Ref yk;
   if (has_k) {
-    yk.p = output(a[9], a[1], "out_k", k, ok);
+    yk.p = output(a[9], "out_k", k, ok);
     if (!yk.p) return nullptr;
   } else {
     yk.p = Py_NewRef(Py_None);
   }
-  mnb_stream_t s;
-  if (!stream_of(dev, s)) return nullptr;
+  const mnb_stream_t s = stream_of(dev);
   if (!status_ok(mnb_qk_norm_rope(&q.h, has_k ? &k.h : nullptr, q.t.shape[0],
                                   static_cast<int>(q.t.shape[2]), static_cast<mnb_dtype>(code),
                                   gq, gk, static_cast<float>(eps),
@@ -333,7 +287,7 @@ PyObject *cache_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
   mnb_rope rope;
   if (!rows_of(a[1], "k", -1, nullptr, k)) return nullptr;
   const long dev = k.t.device;
-  MNB_CURRENT_OR_RETURN(dev);
+  if (!is_current(dev)) return Py_NewRef(Py_NotImplemented);
   if (!rows_of(a[2], "v", dev, &k, v) || !cache_of(a[3], dev, c)) return nullptr;
   if (k.t.dtype != c.k.dtype || k.t.shape[2] != c.k.shape[3] || k.t.shape[1] != c.k.shape[1])
     return refuse("k must have the heads, head size and dtype of the cache"), nullptr;
@@ -351,13 +305,12 @@ PyObject *cache_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return nullptr;
   Ref y;
   if (has_q) {
-    y.p = output(a[10], a[0], "out", q, oq);
+    y.p = output(a[10], "out", q, oq);
     if (!y.p) return nullptr;
   } else {
     y.p = Py_NewRef(Py_None);
   }
-  mnb_stream_t s;
-  if (!stream_of(dev, s)) return nullptr;
+  const mnb_stream_t s = stream_of(dev);
   if (!status_ok(mnb_cache_append(has_q ? &q.h : nullptr, &k.h, &v.h, k.t.shape[0], gq, gk,
                                   static_cast<float>(eps), a[5] == Py_None ? nullptr : &rope,
                                   &c.c, &b, has_q ? &oq.h : nullptr, s),
@@ -374,69 +327,88 @@ PyObject *paged_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
   mnb_kv_batch b;
   if (!rows_of(a[0], "q", -1, nullptr, q)) return nullptr;
   const long dev = q.t.device;
-  MNB_CURRENT_OR_RETURN(dev);
+  if (!is_current(dev)) return Py_NewRef(Py_NotImplemented);
   if (!cache_of(a[1], dev, c)) return nullptr;
   if (q.t.dtype != c.k.dtype || q.t.shape[2] != c.k.shape[3])
     return refuse("q must have the head size and dtype of the cache"), nullptr;
   if (!batch_of(a[2], dev, b)) return nullptr;
-  double scale = 1.0 / __builtin_sqrt(static_cast<double>(q.t.shape[2]));
+  double scale = 1.0 / std::sqrt(static_cast<double>(q.t.shape[2]));
   if (a[3] != Py_None) {
     scale = PyFloat_AsDouble(a[3]);
     if (scale == -1.0 && PyErr_Occurred()) return nullptr;
   }
   const long long window = PyLong_AsLongLong(a[4]);
   if (window == -1 && PyErr_Occurred()) return nullptr;
-  Ref y(output(a[5], a[0], "out", q, o));
+  Ref y(output(a[5], "out", q, o));
   if (!y.p) return nullptr;
   // The workspace is freed on return to torch's allocator, which hands the
   // memory out again on the same stream only, after the call's kernels.
   const size_t need =
       mnb_paged_attention_workspace_size(q.t.shape[0], q.h.heads, &c.c, &b);
-  Ref ws;
-  int64_t at = 0;
-  if (need) {
-    Ref size(PyLong_FromSize_t(need));
-    Ref fn(PyObject_GetAttr(a[0], s_new_empty));
-    if (!size.p || !fn.p) return nullptr;
-    PyObject *args[] = {size.p, t_u8};
-    ws.p = PyObject_Vectorcall(fn.p, args, 1, kw_u8);
-    if (!ws.p || !call_long(ws.p, s_data_ptr, at)) return nullptr;
-  }
-  mnb_stream_t s;
-  if (!stream_of(dev, s)) return nullptr;
+  at::Tensor ws;
+  if (need)
+    ws = at::empty({static_cast<int64_t>(need)},
+                   at::TensorOptions().dtype(at::kByte).device(at::kCUDA, dev));
+  const mnb_stream_t s = stream_of(dev);
   if (!status_ok(mnb_paged_attention(&q.h, q.t.shape[0], &c.c, &b, static_cast<float>(scale),
-                                     window, &o.h, reinterpret_cast<void *>(at), need, s),
+                                     window, &o.h, need ? ws.mutable_data_ptr() : nullptr, need, s),
                  "mnb_paged_attention"))
     return nullptr;
   return y.take();
 }
 
-// setup(torch, check): torch's module, and the binding's function that raises
-// for a status.
-PyObject *setup(PyObject *, PyObject *args) {
-  PyObject *torch, *check;
-  if (!PyArg_ParseTuple(args, "OO", &torch, &check)) return nullptr;
-  struct {
-    PyObject **to;
-    const char *name;
-  } const dtypes[] = {{&t_f32, "float32"}, {&t_bf16, "bfloat16"}, {&t_i32, "int32"},
-                      {&t_u8, "uint8"}};
-  for (const auto &d : dtypes)
-    if (!(*d.to = PyObject_GetAttrString(torch, d.name))) return nullptr;
-  Ref c(PyObject_GetAttrString(torch, "_C"));
-  if (!c.p || !(raw_stream = PyObject_GetAttrString(c.p, "_cuda_getCurrentRawStream")) ||
-      !(current_device = PyObject_GetAttrString(c.p, "_cuda_getDevice")))
+// frequencies, n, first, magnitude, device
+PyObject *rope_table(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  if (n != 5) return PyErr_Format(PyExc_TypeError, "5 arguments, not %zd", n);
+  Tensor f;
+  if (!describe(a[0], "frequencies", f)) return nullptr;
+  if (f.device >= 0 || f.dtype != at::kDouble || f.dims != 1 || !contiguous(f) ||
+      !THPVariable_Unpack(a[0]).is_cpu())
+    return refuse("frequencies must be a contiguous float64 vector on the CPU"), nullptr;
+  const long long rows = PyLong_AsLongLong(a[1]), first = PyLong_AsLongLong(a[2]);
+  const double magnitude = PyFloat_AsDouble(a[3]);
+  const long dev = PyLong_AsLong(a[4]);
+  if (PyErr_Occurred()) return nullptr;
+  if (!is_current(dev)) return Py_NewRef(Py_NotImplemented);
+  const int64_t pairs = f.shape[0];
+  if (rows < 0 || pairs > (1 << 20)) return refuse("n must not be negative"), nullptr;
+  const auto options = at::TensorOptions().dtype(at::kFloat).device(at::kCUDA, dev);
+  const at::Tensor c = at::empty({rows, pairs}, options), s = at::empty({rows, pairs}, options);
+  if (!status_ok(mnb_rope_table(reinterpret_cast<const double *>(f.ptr),
+                                static_cast<int>(2 * pairs), first, rows, magnitude,
+                                static_cast<float *>(c.mutable_data_ptr()),
+                                static_cast<float *>(s.mutable_data_ptr()), stream_of(dev)),
+                 "mnb_rope_table"))
     return nullptr;
-  check_status = Py_NewRef(check);
+  Ref pc(THPVariable_Wrap(c)), ps(THPVariable_Wrap(s));
+  if (!pc.p || !ps.p) return nullptr;
+  return PyTuple_Pack(2, pc.p, ps.p);
+}
+
+// Torch's exceptions (out of memory, a device's error) as Python's.
+template <PyObject *(*F)(PyObject *, PyObject *const *, Py_ssize_t)>
+PyObject *guarded(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  return F(self, a, n);
+  END_HANDLE_TH_ERRORS
+}
+
+// setup(check): the binding's function that raises for a status.
+PyObject *setup(PyObject *, PyObject *check) {
+  Py_XSETREF(check_status, Py_NewRef(check));
   Py_RETURN_NONE;
 }
 
-PyMethodDef methods[] = {
-    {"setup", setup, METH_VARARGS, nullptr},
-    {"qk_norm_rope", reinterpret_cast<PyCFunction>(qk_norm_rope), METH_FASTCALL, nullptr},
-    {"cache_append", reinterpret_cast<PyCFunction>(cache_append), METH_FASTCALL, nullptr},
-    {"paged_attention", reinterpret_cast<PyCFunction>(paged_attention), METH_FASTCALL, nullptr},
-    {nullptr, nullptr, 0, nullptr}};
+template <PyObject *(*F)(PyObject *, PyObject *const *, Py_ssize_t)>
+PyMethodDef method(const char *name) {
+  return {name, reinterpret_cast<PyCFunction>(guarded<F>), METH_FASTCALL, nullptr};
+}
+PyMethodDef methods[] = {{"setup", setup, METH_O, nullptr},
+                         method<rope_table>("rope_table"),
+                         method<qk_norm_rope>("qk_norm_rope"),
+                         method<cache_append>("cache_append"),
+                         method<paged_attention>("paged_attention"),
+                         {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_mnb_py", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 
@@ -446,13 +418,10 @@ PyMODINIT_FUNC PyInit__mnb_py() {
   struct {
     PyObject **to;
     const char *name;
-  } const names[] = {{&s_data_ptr, "data_ptr"}, {&s_stride, "stride"},   {&s_shape, "shape"},
-                     {&s_dtype, "dtype"},       {&s_get_device, "get_device"},
-                     {&s_new_empty, "new_empty"}, {&s_cos, "cos"},       {&s_sin, "sin"},
-                     {&s_k, "k"},               {&s_v, "v"},             {&s_starts, "starts"},
-                     {&s_lengths, "lengths"},   {&s_table, "table"}};
+  } const names[] = {{&s_cos, "cos"},       {&s_sin, "sin"},         {&s_k, "k"},
+                     {&s_v, "v"},           {&s_starts, "starts"},   {&s_lengths, "lengths"},
+                     {&s_table, "table"}};
   for (const auto &s : names)
     if (!(*s.to = PyUnicode_InternFromString(s.name))) return nullptr;
-  if (!(kw_u8 = Py_BuildValue("(s)", "dtype"))) return nullptr;
   return PyModule_Create(&module);
 }

@@ -26,8 +26,10 @@ namespace {
 // An angle p f is held in turns as a 64-bit fraction: p times the fraction of
 // f / 2 pi, modulo 2^64, is exact but for the rounding of f / 2 pi to 2^-64,
 // at any position, with one integer product. The nearest quarter turn is
-// taken off in integers too, so what sincospi gets, at most 1/4, has all of
-// its 24 bits however near a zero of the cosine the angle lies.
+// taken off in integers too; the rest, at most pi / 4, keeps all of its 24
+// bits however near a zero of the cosine the angle lies, and goes through the
+// Taylor series of sine (to x^9) and cosine (to x^10), which end below 2^-28
+// there. Bound by the writes: 8 bytes for some 40 instructions.
 struct TableParams {
   uint64_t turns[kMaxPairs];
   int pairs;
@@ -38,37 +40,53 @@ struct TableParams {
 
 __device__ __forceinline__ void table_entry(uint64_t turns, float mag, float mag_lo, float &c,
                                             float &s) {
-  const uint64_t quarter = (turns + (uint64_t(1) << 61)) >> 62;  // 0 .. 3 (4 as 0)
-  const int64_t rest = static_cast<int64_t>(turns - (quarter << 62));
-  float x, y;
-  sincospif(static_cast<float>(rest) * 0x1p-63f, &y, &x);
+  const uint32_t top = static_cast<uint32_t>(turns >> 32) + (1u << 29);
+  const uint32_t quarter = top >> 30;  // 0 .. 3 (4 as 0)
+  // The rest's high word, signed, and low word: 2^-64 turns.
+  const int32_t hi = static_cast<int32_t>((top & 0x3FFFFFFFu) - (1u << 29));
+  const float lo = static_cast<float>(static_cast<uint32_t>(turns));
+  const float x = fmaf(static_cast<float>(hi), 0x1p32f, lo) * 0x1.921fb6p-62f;  // 2 pi 2^-64
+  const float x2 = x * x;
+  float p = fmaf(x2, 1.f / 362880.f, -1.f / 5040.f);
+  p = fmaf(x2, p, 1.f / 120.f);
+  p = fmaf(x2, p, -1.f / 6.f);
+  float y = fmaf(x * x2, p, x);
+  float q = fmaf(x2, -1.f / 3628800.f, 1.f / 40320.f);
+  q = fmaf(x2, q, -1.f / 720.f);
+  q = fmaf(x2, q, 1.f / 24.f);
+  q = fmaf(x2, q, -0.5f);
+  float z = fmaf(x2, q, 1.f);
   if (quarter & 1) {
-    const float t = x;
-    x = -y;
+    const float t = z;
+    z = -y;
     y = t;
   }
-  if (quarter & 2) {
-    x = -x;
-    y = -y;
-  }
-  c = fmaf(x, mag, x * mag_lo);
+  const uint32_t flip = (quarter & 2) << 30;
+  z = __uint_as_float(__float_as_uint(z) ^ flip);
+  y = __uint_as_float(__float_as_uint(y) ^ flip);
+  c = fmaf(z, mag, z * mag_lo);
   s = fmaf(y, mag, y * mag_lo);
 }
 
-// A thread per V neighbouring pairs of a position.
+// A thread keeps V neighbouring pairs and takes every at_once-th position of its
+// block's.
+constexpr int kTableRows = 64;  // positions of a block: 128 leave too few blocks for 40960
 template <int V>
 __global__ void __launch_bounds__(256) table_kernel(const __grid_constant__ TableParams p) {
-  const int per = p.pairs / V;
-  const int64_t total = p.n * per;
-  for (int64_t i = blockIdx.x * int64_t(256) + threadIdx.x; i < total;
-       i += gridDim.x * int64_t(256)) {
-    const int64_t row = i / per;
-    const int j = static_cast<int>(i - row * per) * V;
-    const uint64_t at = static_cast<uint64_t>(p.first + row);
+  const int per = p.pairs / V, at_once = 256 / per;
+  const int j = threadIdx.x % per * V, r0 = threadIdx.x / per;
+  if (r0 >= at_once) return;
+  uint64_t turns[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) turns[e] = p.turns[j + e];
+  const int64_t row0 = blockIdx.x * int64_t(kTableRows);
+  const int rows = static_cast<int>(min(int64_t(kTableRows), p.n - row0));
+  for (int r = r0; r < rows; r += at_once) {
+    const uint64_t at = static_cast<uint64_t>(p.first + row0 + r);
     float c[V], s[V];
 #pragma unroll
-    for (int e = 0; e < V; ++e) table_entry(at * p.turns[j + e], p.mag, p.mag_lo, c[e], s[e]);
-    float *pc = p.cos + row * p.pairs + j, *ps = p.sin + row * p.pairs + j;
+    for (int e = 0; e < V; ++e) table_entry(at * turns[e], p.mag, p.mag_lo, c[e], s[e]);
+    float *pc = p.cos + (row0 + r) * p.pairs + j, *ps = p.sin + (row0 + r) * p.pairs + j;
     if constexpr (V == 4) {
       *reinterpret_cast<float4 *>(pc) = make_float4(c[0], c[1], c[2], c[3]);
       *reinterpret_cast<float4 *>(ps) = make_float4(s[0], s[1], s[2], s[3]);
@@ -84,8 +102,8 @@ __global__ void __launch_bounds__(256) table_kernel(const __grid_constant__ Tabl
 
 // ---- norms, rotation, cache -----------------------------------------------------
 
-// The sequence that holds row t (-1: none), by a search of 32 places a step;
-// every lane of the warp takes part.
+// The last sequence that begins at or before row t, by a search of 32 places a
+// step; every lane of the warp takes part, with one t.
 __device__ __forceinline__ int seq_of(const BatchView &b, int t, int lane) {
   int lo = 0, hi = b.n;
   while (hi - lo > 1) {
@@ -95,26 +113,30 @@ __device__ __forceinline__ int seq_of(const BatchView &b, int t, int lane) {
     lo += k * step;
     hi = min(hi, lo + step);
   }
-  return b.starts[lo] <= t && t < b.starts[lo + 1] ? lo : -1;
+  return lo;
 }
 
-// Where row t goes: its position (negative: none), and its place in the cache.
+// Where row t goes: its position, and its place in the cache.
 struct Place {
   int64_t pos;
   int64_t page;  // -1: no page holds it
   int at;
 };
+// False: the row belongs to no sequence. Whole warps; t0: the warp's first row.
 template <bool APPEND>
-__device__ __forceinline__ bool place_of(const RopeArgs &a, int64_t t, int lane, Place &pl) {
+__device__ __forceinline__ bool place_of(const RopeArgs &a, int64_t t, int64_t t0, int lane,
+                                         Place &pl) {
   pl.page = -1;
   pl.at = 0;
   if (!APPEND) {
-    pl.pos = a.pos ? a.pos[t] : -1;
-    return true;
+    pl.pos = a.pos ? a.pos[min(t, a.T - 1)] : -1;
+    return t < a.T;
   }
-  const int s = seq_of(a.b, static_cast<int>(t), lane);
-  if (s < 0) return false;
-  pl.pos = int64_t(a.b.lengths[s]) - (a.b.starts[s + 1] - t);
+  int s = seq_of(a.b, static_cast<int>(t0), lane);
+  int end = a.b.starts[s + 1];
+  while (end <= t && s + 1 < a.b.n) end = a.b.starts[++s + 1];
+  if (t >= a.T || t >= end || t < a.b.starts[s]) return false;
+  pl.pos = int64_t(a.b.lengths[s]) - (end - t);
   if (pl.pos >= 0 && pl.pos < int64_t(a.b.table_pages) * a.c.page_size) {
     const int i = static_cast<int>(pl.pos) / a.c.page_size;
     pl.at = static_cast<int>(pl.pos) - i * a.c.page_size;
@@ -164,58 +186,71 @@ __device__ __forceinline__ void load_floats(const float *p, float (&v)[N]) {
   }
 }
 
-// One block per token; LANES lanes per head row, each with two 16-byte pieces
-// that hold whole pairs: pieces s and s + rot/2 of the half-split layout (2s
-// and 2s + 1 interleaved, and past the rotated part), so that nothing but the
-// sum of squares crosses lanes. Cosines and sines are read once per lane and
-// used for each of its heads. Bound by memory: every row is read and written
-// once; the tables, shared by a token's heads, add rot * 4 bytes to it.
-template <bool F32, int LANES, bool APPEND>
-__global__ void __launch_bounds__(512) rope_kernel(const __grid_constant__ RopeArgs a) {
+// LANES lanes per head row, each with two 16-byte pieces that hold whole pairs:
+// pieces s and s + rot/2 of the half-split layout (2s and 2s + 1 interleaved,
+// and past the rotated part), so that nothing but the sum of squares crosses
+// lanes. A group of lanes takes R heads of a token: their loads, which wait for
+// no position, go first, all together, and its cosines and sines serve all of
+// them. Bound by memory: every row is read and written once; the tables,
+// shared by a token's heads, add rot * 4 bytes to it.
+template <bool F32, int LANES, int R, bool APPEND>
+__global__ void __launch_bounds__(128, R > 1 ? 6 : 8) rope_kernel(const __grid_constant__ RopeArgs a) {
   using V = Vec<F32>;
   constexpr int N = V::N;
   using E = typename std::conditional<F32, float, uint16_t>::type;
   const int lane = threadIdx.x & 31, s = threadIdx.x % LANES;
-  const int groups = blockDim.x / LANES;
   grid_dependency_wait();
   grid_dependents_launch();
-  const int64_t t = blockIdx.x;
-  Place pl;
-  if (!place_of<APPEND>(a, t, lane, pl)) return;
+  const int rows = a.q.n + a.k.n + a.v.n, per = (rows + R - 1) / R;  // groups per token
+  const int64_t g0 = (blockIdx.x * int64_t(128) + (threadIdx.x & ~31)) / LANES;
+  const int64_t t0 = g0 / per;
+  // The warp's groups are neighbours: same token, or the next ones.
+  const int in = static_cast<int>(g0 - t0 * per) + lane / LANES;
+  const int64_t t = t0 + in / per;
+  const int h0 = (in - in / per * per) * R;
   const int pairs = a.rot / 2, slots = a.D / (2 * N), turning = a.rot / (2 * N);
-  const bool mine = s < slots, turned = a.cos != nullptr && s < turning;
-  const bool known = a.cos == nullptr || (pl.pos >= 0 && pl.pos < a.positions);
+  const bool mine = s < slots && t < a.T;
   const int o0 = s < turning && !a.interleaved ? s * N : s * 2 * N;
   const int o1 = s < turning && !a.interleaved ? pairs + s * N : s * 2 * N + N;
-  float c[N], sn[N];
-  if (turned && known) {
-    load_floats<N>(a.cos + pl.pos * pairs + s * N, c);
-    load_floats<N>(a.sin + pl.pos * pairs + s * N, sn);
-  }
-  const int rows = a.q.n + a.k.n + a.v.n;
-  // Whole warps go round together: the sum of squares crosses their lanes.
-  for (int h0 = threadIdx.x / 32 * (32 / LANES); h0 < rows; h0 += groups) {
-    const int h = h0 + lane / LANES;
-    const bool live = mine && h < rows;
+  uint4 r0[R], r1[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int h = h0 + i;
+    r0[i] = r1[i] = make_uint4(0, 0, 0, 0);
+    if (!mine || h >= rows) continue;
     const int kind = h < a.q.n ? 0 : h < a.q.n + a.k.n ? 1 : 2;
     const int hh = kind == 0 ? h : kind == 1 ? h - a.q.n : h - a.q.n - a.k.n;
     const Heads &src = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
-    uint4 r0 = make_uint4(0, 0, 0, 0), r1 = r0;
-    if (live) {
-      const E *x = static_cast<const E *>(src.p) + t * src.ts + hh * src.hs;
-      r0 = *reinterpret_cast<const uint4 *>(x + o0);
-      r1 = *reinterpret_cast<const uint4 *>(x + o1);
-    }
+    const E *x = static_cast<const E *>(src.p) + t * src.ts + hh * src.hs;
+    r0[i] = *reinterpret_cast<const uint4 *>(x + o0);
+    r1[i] = *reinterpret_cast<const uint4 *>(x + o1);
+  }
+  Place pl;
+  const bool there = place_of<APPEND>(a, t, t0, lane, pl);
+  const bool turned = a.cos != nullptr && s < turning;
+  const bool known = a.cos == nullptr || (pl.pos >= 0 && pl.pos < a.positions);
+  float c[N], sn[N];
+  if (there && turned && known) {
+    load_floats<N>(a.cos + pl.pos * pairs + s * N, c);
+    load_floats<N>(a.sin + pl.pos * pairs + s * N, sn);
+  }
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int h = h0 + i;
+    const int kind = h < a.q.n ? 0 : h < a.q.n + a.k.n ? 1 : 2;
+    const int hh = kind == 0 ? h : kind == 1 ? h - a.q.n : h - a.q.n - a.k.n;
     const float *gamma = kind == 0 ? a.gq : kind == 1 ? a.gk : nullptr;
     float v0[N], v1[N];
-    V::widen(r0, v0);
-    V::widen(r1, v1);
+    V::widen(r0[i], v0);
+    V::widen(r1[i], v1);
     float sum = 0.f;
+    if (a.gq || a.gk) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) sum += v0[i] * v0[i] + v1[i] * v1[i];
+      for (int e = 0; e < N; ++e) sum += v0[e] * v0[e] + v1[e] * v1[e];
 #pragma unroll
-    for (int m = 1; m < LANES; m *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-    if (!live) continue;
+      for (int m = 1; m < LANES; m *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+    }
+    if (!mine || !there || h >= rows) continue;
     E *y;
     if (kind == 0) {
       y = static_cast<E *>(a.qo.p) + t * a.qo.ts + hh * a.qo.hs;
@@ -232,38 +267,38 @@ __global__ void __launch_bounds__(512) rope_kernel(const __grid_constant__ RopeA
         float g[N];
         load_floats<N>(gamma + o0, g);
 #pragma unroll
-        for (int i = 0; i < N; ++i) v0[i] = v0[i] * f * g[i];
+        for (int e = 0; e < N; ++e) v0[e] = v0[e] * f * g[e];
         load_floats<N>(gamma + o1, g);
 #pragma unroll
-        for (int i = 0; i < N; ++i) v1[i] = v1[i] * f * g[i];
+        for (int e = 0; e < N; ++e) v1[e] = v1[e] * f * g[e];
       }
       if (turned && known) {
         if (!a.interleaved) {
 #pragma unroll
-          for (int i = 0; i < N; ++i) {
-            const float p = v0[i], q = v1[i];
-            v0[i] = p * c[i] - q * sn[i];
-            v1[i] = q * c[i] + p * sn[i];
+          for (int e = 0; e < N; ++e) {
+            const float p = v0[e], q = v1[e];
+            v0[e] = p * c[e] - q * sn[e];
+            v1[e] = q * c[e] + p * sn[e];
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < N; i += 2) {
-            const float p = v0[i], q = v0[i + 1], u = v1[i], w = v1[i + 1];
-            v0[i] = p * c[i / 2] - q * sn[i / 2];
-            v0[i + 1] = q * c[i / 2] + p * sn[i / 2];
-            v1[i] = u * c[(N + i) / 2] - w * sn[(N + i) / 2];
-            v1[i + 1] = w * c[(N + i) / 2] + u * sn[(N + i) / 2];
+          for (int e = 0; e < N; e += 2) {
+            const float p = v0[e], q = v0[e + 1], u = v1[e], w = v1[e + 1];
+            v0[e] = p * c[e / 2] - q * sn[e / 2];
+            v0[e + 1] = q * c[e / 2] + p * sn[e / 2];
+            v1[e] = u * c[(N + e) / 2] - w * sn[(N + e) / 2];
+            v1[e + 1] = w * c[(N + e) / 2] + u * sn[(N + e) / 2];
           }
         }
       }
       if (gamma || a.cos) {
-        r0 = V::narrow(v0);
-        r1 = V::narrow(v1);
+        r0[i] = V::narrow(v0);
+        r1[i] = V::narrow(v1);
       }
-      if (!known) r0 = r1 = make_uint4(0, 0, 0, 0);
+      if (!known) r0[i] = r1[i] = make_uint4(0, 0, 0, 0);
     }
-    *reinterpret_cast<uint4 *>(y + o0) = r0;
-    *reinterpret_cast<uint4 *>(y + o1) = r1;
+    *reinterpret_cast<uint4 *>(y + o0) = r0[i];
+    *reinterpret_cast<uint4 *>(y + o1) = r1[i];
   }
 }
 
@@ -281,7 +316,7 @@ __global__ void __launch_bounds__(kPlainWarps * 32)
   grid_dependents_launch();
   const int64_t t = blockIdx.x;
   Place pl;
-  if (!place_of<APPEND>(a, t, lane, pl)) return;
+  if (!place_of<APPEND>(a, t, t, lane, pl)) return;
   const int pairs = a.rot / 2;
   const bool known = a.cos == nullptr || (pl.pos >= 0 && pl.pos < a.positions);
   auto put = [](E *p, float v) {
@@ -361,19 +396,24 @@ cudaError_t run_rope(const RopeArgs &a, cudaStream_t stream) {
                            : vec_heads(a.ko, es)) &&
                    vec_floats(a.gq) && vec_floats(a.gk) && vec_floats(a.cos) &&
                    vec_floats(a.sin);
-  const dim3 grid(static_cast<unsigned>(a.T));
   if (!vec)
-    return launch_after(rope_plain_kernel<F32, APPEND>, grid, kPlainWarps * 32, 0, a.pdl, stream,
-                        a);
+    return launch_after(rope_plain_kernel<F32, APPEND>, dim3(static_cast<unsigned>(a.T)),
+                        kPlainWarps * 32, 0, a.pdl, stream, a);
   const int slots = a.D / (2 * N), rows = a.q.n + a.k.n + a.v.n;
   const int lanes = slots <= 4 ? 4 : slots <= 8 ? 8 : slots <= 16 ? 16 : 32;
-  const int threads = static_cast<int>(
-      std::min<int64_t>(512, ceil_div(int64_t(rows) * lanes, 32) * 32));
-  auto *kernel = lanes == 4    ? rope_kernel<F32, 4, APPEND>
-                 : lanes == 8  ? rope_kernel<F32, 8, APPEND>
-                 : lanes == 16 ? rope_kernel<F32, 16, APPEND>
-                               : rope_kernel<F32, 32, APPEND>;
-  return launch_after(kernel, grid, threads, 0, a.pdl, stream, a);
+  // Four heads a group once that still fills the GPU's threads; below, a head a
+  // group is sooner done.
+  const bool many = a.T * rows * lanes >= int64_t(4) * 2048 * std::max(1, sm_count());
+  const int64_t groups = a.T * ceil_div(rows, many ? 4 : 1);
+  const int64_t blocks = ceil_div(groups * lanes, 128);
+  if (blocks > (int64_t(1) << 31) - 1) return cudaErrorInvalidValue;
+  void (*const kernels[2][4])(RopeArgs) = {
+      {rope_kernel<F32, 4, 1, APPEND>, rope_kernel<F32, 8, 1, APPEND>,
+       rope_kernel<F32, 16, 1, APPEND>, rope_kernel<F32, 32, 1, APPEND>},
+      {rope_kernel<F32, 4, 4, APPEND>, rope_kernel<F32, 8, 4, APPEND>,
+       rope_kernel<F32, 16, 4, APPEND>, rope_kernel<F32, 32, 4, APPEND>}};
+  auto *kernel = kernels[many][lanes == 4 ? 0 : lanes == 8 ? 1 : lanes == 16 ? 2 : 3];
+  return launch_after(kernel, dim3(static_cast<unsigned>(blocks)), 128, 0, a.pdl, stream, a);
 }
 
 }  // namespace
@@ -383,11 +423,9 @@ cudaError_t launch_rope_table(const RopeTableArgs &a, cudaStream_t stream) {
   for (int i = 0; i < a.pairs; ++i) {
     // The fraction of a turn that a position adds, rounded to 2^-64 (a double
     // keeps 53 bits of it).
-    double f = a.frequencies[i] / (2.0 * M_PI);
+    double f = a.frequencies[i] * (0.5 / M_PI);
     f -= std::floor(f);
-    const double hi = std::floor(std::ldexp(f, 32));
-    const double lo = std::ldexp(f, 64) - std::ldexp(hi, 32);
-    p.turns[i] = (static_cast<uint64_t>(hi) << 32) + static_cast<uint64_t>(lo);
+    p.turns[i] = f < 1.0 ? static_cast<uint64_t>(f * 0x1p64) : 0;  // (1 - 2^-60 may round to 1)
   }
   p.pairs = a.pairs;
   p.first = a.first;
@@ -397,8 +435,7 @@ cudaError_t launch_rope_table(const RopeTableArgs &a, cudaStream_t stream) {
   p.cos = a.cos;
   p.sin = a.sin;
   const bool four = a.pairs % 4 == 0 && vec_floats(a.cos) && vec_floats(a.sin);
-  const int64_t blocks = ceil_div(a.n * (four ? a.pairs / 4 : a.pairs), 256);
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(blocks, 1 << 20));
+  const unsigned grid = static_cast<unsigned>(ceil_div(a.n, kTableRows));
   if (four)
     table_kernel<4><<<grid, 256, 0, stream>>>(p);
   else
