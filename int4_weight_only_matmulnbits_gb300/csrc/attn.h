@@ -78,6 +78,52 @@ struct AttnArgs {
 size_t attn_workspace_bytes(const AttnArgs &a);
 cudaError_t launch_attn(const AttnArgs &a, cudaStream_t stream);
 
+// Division of 0 <= x < 2^31 by a number known at the launch: a product and a
+// shift, where the compiler's division takes some 40 instructions.
+struct FastDiv {
+  uint32_t mul, shift, d;
+  FastDiv() = default;
+  explicit FastDiv(uint32_t by) : d(by) {
+    shift = 0;
+    while ((uint64_t(1) << shift) < by) ++shift;  // 2^(shift - 1) < by <= 2^shift
+    // ceil(2^(31 + shift) / by) fits 32 bits, and its excess over the quotient,
+    // below 1, adds less than x / 2^(31 + shift) < 1 / by to x / by.
+    mul = static_cast<uint32_t>(((uint64_t(1) << (31 + shift)) + by - 1) / by);
+  }
+  __device__ __forceinline__ int div(int x) const {
+    return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(x)) * mul) >>
+                            (31 + shift));
+  }
+};
+
+// `total` blocks of a line shared out over `parts` CTAs: the first total %
+// parts of them take one more.
+struct Share {
+  int64_t q;
+  int r;
+  __device__ __forceinline__ Share(int64_t total, int parts) {
+    if (total < (int64_t(1) << 31)) {  // (64-bit divisions take a microsecond)
+      const uint32_t n = static_cast<uint32_t>(total), d = static_cast<uint32_t>(parts);
+      q = n / d;
+      r = static_cast<int>(n - static_cast<uint32_t>(q) * d);
+    } else {
+      q = total / parts;
+      r = static_cast<int>(total - q * parts);
+    }
+  }
+  __device__ __forceinline__ int64_t first(int c) const { return c * q + min(c, r); }
+  // The CTA that has block x.
+  __device__ __forceinline__ int owner(int64_t x) const {
+    const int64_t head = r * (q + 1);
+    return static_cast<int>(x < head ? div(x, q + 1) : r + div(x - head, q));
+  }
+  static __device__ __forceinline__ int64_t div(int64_t a, int64_t b) {
+    if ((a | b) < (int64_t(1) << 31))
+      return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+  }
+};
+
 // One sequence of a batch as the attention kernels take it: rows t0 .. t0 + n
 // of the queries, whose row i stands at position len - n + i; keys from lo on
 // (a multiple of 16) are attended by some row.

@@ -50,9 +50,8 @@ struct Cfg {
   static constexpr int per_sm = row <= 256 ? 2 : 1;
   static constexpr int stages = (per_sm == 2 ? 98304 : 196608) / (kWarps * step);
   static constexpr int ring = kWarps * stages * step;
-  static constexpr int cols = 32;               // columns joined at a time
-  static constexpr int ld = cols + 4;
-  static constexpr int joins = kWarps * kRows * (ld + 2) * 4;
+  static constexpr int ld = D + 4;              // joined: four rows at a time
+  static constexpr int joins = (kWarps * 4 * ld + 2 * kWarps * kRows) * 4;
   static constexpr int parts = F32 ? kRows * D * 6 : 0;  // the rows of q in bf16 parts
   static constexpr int smem = ring + joins + parts;
   static_assert(stages >= 3, "copies in flight");
@@ -147,30 +146,35 @@ struct Line {
     return load_seq(p.b, i, p.T, p.cap, p.window);
   }
   __device__ __forceinline__ int tiles(const Seq &s) const {
-    return static_cast<int>((int64_t(s.n) * p.G + kRows - 1) / kRows);
+    return (s.n * static_cast<int>(p.G.d) + kRows - 1) / kRows;
   }
   static __device__ __forceinline__ int blocks(const Seq &s) {
     return max(1, (s.len - s.lo + kBlockKeys - 1) / kBlockKeys);
   }
-  __device__ __forceinline__ int64_t work(int i) const {
-    if (i >= p.b.n) return 0;
-    const Seq s = seq(i);
+  __device__ __forceinline__ int64_t work(const Seq &s) const {
     return int64_t(tiles(s)) * p.kv_heads * blocks(s);
   }
-  // All blocks of the line (every lane takes part; w0: the first 32
-  // sequences').
-  __device__ __forceinline__ int64_t total(int64_t &w0) const {
-    int64_t w = w0 = work(lane);
-    for (int i = lane + 32; i < p.b.n; i += 32) w += work(i);
+  // All blocks of the line; every lane takes part, and keeps one of the first 32
+  // sequences in s0.
+  __device__ __forceinline__ int64_t total(Seq &s0) const {
+    s0 = Seq{0, 0, 0, 0};
+    if (lane < p.b.n) s0 = seq(lane);
+    int64_t w = work(s0);
+    for (int i = lane + 32; i < p.b.n; i += 32) w += work(seq(i));
 #pragma unroll
     for (int m = 1; m < 32; m *= 2) w += __shfl_xor_sync(0xffffffffu, w, m);
     return w;
   }
-  // The sequence that holds block x, and the block's number in it.
-  __device__ __forceinline__ int find(int64_t x, int64_t w0, int64_t &in) const {
+  // The unit that holds block x of the line, and the block's number in it.
+  __device__ __forceinline__ void start(Unit &u, int &kb, int64_t x, const Seq &s0) const {
     int64_t before = 0;
     for (int i0 = 0; i0 < p.b.n; i0 += 32) {
-      const int64_t w = i0 == 0 ? w0 : work(i0 + lane);
+      Seq s{0, 0, 0, 0};
+      if (i0 == 0)
+        s = s0;
+      else if (i0 + lane < p.b.n)
+        s = seq(i0 + lane);
+      const int64_t w = work(s);
       int64_t up = w;
 #pragma unroll
       for (int m = 1; m < 32; m *= 2) {
@@ -178,35 +182,31 @@ struct Line {
         if (lane >= m) up += o;
       }
       const unsigned past = __ballot_sync(0xffffffffu, before + up > x);
-      if (past) {
+      if (past) {  // (some lane of some round has it: x is below the total)
         const int l = __ffs(past) - 1;
-        in = x - before - __shfl_sync(0xffffffffu, up - w, l);
-        return i0 + l;
+        const int64_t in = x - before - __shfl_sync(0xffffffffu, up - w, l);
+        s = Seq{__shfl_sync(0xffffffffu, s.t0, l), __shfl_sync(0xffffffffu, s.n, l),
+                __shfl_sync(0xffffffffu, s.len, l), __shfl_sync(0xffffffffu, s.lo, l)};
+        u.b = i0 + l;
+        const int nb = blocks(s);
+        const int unit = static_cast<int>(Share::div(in, nb));
+        kb = static_cast<int>(in - int64_t(unit) * nb);
+        enter(u, s, unit);
+        return;
       }
       before += __shfl_sync(0xffffffffu, up, 31);
     }
-    in = 0;
-    return p.b.n;
   }
   __device__ __forceinline__ void enter(Unit &u, const Seq &s, int unit) const {
     const int nt = tiles(s);
-    u.head = unit / nt;
+    u.head = nt == 1 ? unit : unit / nt;
     u.tile = unit - u.head * nt;
     u.t0 = s.t0;
     u.n = s.n;
     u.len = s.len;
     u.lo = s.lo;
     u.blocks = blocks(s);
-    u.last = s.len - s.n + min(s.n - 1, (u.tile * kRows + kRows - 1) / p.G);
-  }
-  __device__ __forceinline__ void start(Unit &u, int &kb, int64_t x, int64_t w0) const {
-    int64_t in;
-    u.b = find(x, w0, in);
-    const Seq s = seq(u.b);
-    const int nb = blocks(s);
-    const int unit = static_cast<int>(in / nb);
-    kb = static_cast<int>(in - int64_t(unit) * nb);
-    enter(u, s, unit);
+    u.last = s.len - s.n + min(s.n - 1, p.G.div(u.tile * kRows + kRows - 1));
   }
   // The unit after u (there is one).
   __device__ __forceinline__ void next(Unit &u) const {
@@ -234,30 +234,32 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F32>::per_sm)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   unsigned char *ring = smem + warp * (C::stages * C::step);
   const uint32_t ring_u = smem_addr(ring);
-  float *join = reinterpret_cast<float *>(smem + C::ring);  // [warp][row][ld]
-  float *join_m = join + kWarps * kRows * C::ld, *join_l = join_m + kWarps * kRows;
+  float *join = reinterpret_cast<float *>(smem + C::ring);  // [warp][4 rows][ld]
+  float *join_m = join + kWarps * 4 * C::ld, *join_l = join_m + kWarps * kRows;
   uint4 *qparts = reinterpret_cast<uint4 *>(smem + C::ring + C::joins);  // [d / 16][part][lane]
 
   grid_dependency_wait();
   grid_dependents_launch();
 
   const Line line{p, lane};
-  int64_t w0;
-  const int64_t total = line.total(w0);
+  Seq s0;
+  const int64_t total = line.total(s0);
   // As many blocks of the grid as have kMinBlocks of the line.
-  const int64_t parts = min(int64_t(gridDim.x), (total + kMinBlocks - 1) / kMinBlocks);
+  const int parts =
+      static_cast<int>(min(int64_t(gridDim.x), (total + kMinBlocks - 1) / kMinBlocks));
   int *header = p.headers + blockIdx.x * kHeader;
-  if (int64_t(blockIdx.x) >= parts) {
+  if (static_cast<int>(blockIdx.x) >= parts) {
     if (threadIdx.x == 0) header[0] = 0;
     return;
   }
-  const int64_t x0 = blockIdx.x * total / parts, x1 = (blockIdx.x + 1) * total / parts;
+  const Share share(total, parts);
+  const int64_t x0 = share.first(blockIdx.x), x1 = share.first(blockIdx.x + 1);
 
   // ---- copies ---------------------------------------------------------------------
   Unit fu;
   int fk, slot = 0;
   int64_t fx = x0;
-  line.start(fu, fk, x0, w0);
+  line.start(fu, fk, x0, s0);
   Unit u = fu;
   int kb = fk;
   // Lane l holds the page of this warp's keys in block page0 + l of the unit.
@@ -265,11 +267,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F32>::per_sm)
   auto load_pages = [&](int k0) {
     page0 = k0;
     const int j = fu.lo + (k0 + lane) * kBlockKeys + warp * kWarpKeys;
-    const int first = fu.len - fu.n + fu.tile * kRows / p.G;  // the first row's position
+    const int first = fu.len - fu.n + p.G.div(fu.tile * kRows);  // the first row's position
     pages = -1;
     if (k0 + lane < fu.blocks && j < fu.len && j <= fu.last &&
         (p.window == 0 || j + kWarpKeys > first - p.window + 1)) {
-      pages = p.b.table[fu.b * p.b.table_stride + j / p.page_size];
+      pages = p.b.table[fu.b * p.b.table_stride + p.page_size.div(j)];
       if (pages < 0 || pages >= p.pages) pages = -1;
     }
   };
@@ -284,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F32>::per_sm)
       if (page >= 0) {
         held |= 1u << slot;
         const int j = fu.lo + fk * kBlockKeys + warp * kWarpKeys;
-        const int at = j % p.page_size, left = fu.len - j;
+        const int at = j - p.page_size.div(j) * p.page_size.d, left = fu.len - j;
         const int piece = lane % kPieces, first = lane / kPieces;
         const E *k = static_cast<const E *>(p.k.p) + page * p.k.ps + fu.head * p.k.hs +
                      (at + first) * p.k.ts + piece * (16 / C::es);
@@ -314,21 +316,19 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F32>::per_sm)
     }
     cp_commit();
   };
-  for (int i = 0; i < C::stages - 1; ++i) fetch();
-
   // ---- the unit's rows ---------------------------------------------------------------
   uint32_t q[kQ];
   int pos0 = 0, pos1 = 0;  // positions of the rows g and g + 8 (-1: no row)
   auto load_rows = [&] {
     auto row_of = [&](int r, int &pos) -> const E * {
-      const int i = u.tile * kRows + r, tok = i / p.G;
+      const int i = u.tile * kRows + r, tok = p.G.div(i);
       if (tok >= u.n) {
         pos = -1;
         return nullptr;
       }
       pos = max(-1, u.len - u.n + tok);
       return static_cast<const E *>(p.q.p) + int64_t(u.t0 + tok) * p.q.ts +
-             int64_t(u.head * p.G + i - tok * p.G) * p.q.hs;
+             int64_t((u.head - tok) * static_cast<int>(p.G.d) + i) * p.q.hs;
     };
     const E *a = row_of(g, pos0), *b = row_of(g + 8, pos1);
     if constexpr (F32) {
@@ -368,7 +368,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F32>::per_sm)
     m0 = m1 = -INFINITY;
     l0 = l1 = 0.f;
   };
+  // (Their loads are under way while the first pages are looked up.)
   load_rows();
+  for (int i = 0; i < C::stages - 1; ++i) fetch();
   clear();
   int piece0 = kb, cslot = 0;
 
@@ -380,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F32>::per_sm)
     const uint32_t ks = ring_u + cslot * C::step, vs = ks + C::step / 2;
     cslot = cslot == C::stages - 1 ? 0 : cslot + 1;
     const int j0 = u.lo + kb * kBlockKeys + warp * kWarpKeys;
-    const int top = u.last, bottom = u.len - u.n + u.tile * kRows / p.G;
+    const int top = u.last, bottom = u.len - u.n + p.G.div(u.tile * kRows);
     if (there) {
       // ---- scores of 16 rows and 16 keys
       float s[2][4];
@@ -552,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F32>::per_sm)
     ++kb;
     if (kb < u.blocks && x + 1 < x1) continue;
 
-    // ---- end of a piece: the warps' sums joined, 32 columns at a time ---------------
+    // ---- end of a piece: the warps' sums joined, four rows at a time ---------------
     l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
     l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
     l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
@@ -566,34 +568,31 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F32>::per_sm)
     const bool begins = piece0 == 0, whole = begins && kb == u.blocks;
     const int64_t piece = int64_t(blockIdx.x) * 2 + (begins ? 1 : 0);
     float *part = p.parts + piece * (kRows * (D + 2));
-    // A thread's row, and four columns of it.
-    const int row = threadIdx.x >> 3, col = (threadIdx.x & 7) * 4;
-    float f[kWarps], inv = 0.f;
-    const int i = u.tile * kRows + row, tok = i / p.G;
-    E *out = static_cast<E *>(p.o.p) + int64_t(u.t0 + tok) * p.o.ts +
-             int64_t(u.head * p.G + i - tok * p.G) * p.o.hs;
+    const int live = min(kRows, u.n * static_cast<int>(p.G.d) - u.tile * kRows);
 #pragma unroll
-    for (int c0 = 0; c0 < D; c0 += C::cols) {
-      float *mine = join + warp * kRows * C::ld;
+    for (int half = 0; half < 2; ++half) {
+#pragma unroll 1
+      for (int quad = 0; quad < 8; quad += 4) {
+        if (8 * half + quad >= live) break;
+        if ((g & 4) == quad) {
+          float *mine = join + (warp * 4 + (g & 3)) * C::ld;
 #pragma unroll
-      for (int c = 0; c < C::cols / 8; ++c) {
-        const float(&x4)[4] = o[c0 / 8 + c];
-        if constexpr (F32) {
-          // Column 2t + e' of tile c is d = 8t + 4e' + c.
-          mine[g * C::ld + 8 * t + c] = x4[0];
-          mine[g * C::ld + 8 * t + 4 + c] = x4[1];
-          mine[(g + 8) * C::ld + 8 * t + c] = x4[2];
-          mine[(g + 8) * C::ld + 8 * t + 4 + c] = x4[3];
-        } else {
-          *reinterpret_cast<float2 *>(mine + g * C::ld + 8 * c + 2 * t) =
-              make_float2(x4[0], x4[1]);
-          *reinterpret_cast<float2 *>(mine + (g + 8) * C::ld + 8 * c + 2 * t) =
-              make_float2(x4[2], x4[3]);
+          for (int c = 0; c < kO; ++c) {
+            if constexpr (F32) {
+              // Column 2t + e of tile 4 i + c is d = 32 i + 8 t + 4 e + c.
+              mine[c / 4 * 32 + 8 * t + (c & 3)] = o[c][2 * half];
+              mine[c / 4 * 32 + 8 * t + 4 + (c & 3)] = o[c][2 * half + 1];
+            } else {
+              *reinterpret_cast<float2 *>(mine + 8 * c + 2 * t) =
+                  make_float2(o[c][2 * half], o[c][2 * half + 1]);
+            }
+          }
         }
-      }
-      __syncthreads();
-      if (c0 == 0) {
-        float m = -INFINITY, l = 0.f;
+        __syncthreads();
+        // A warp per row, kPer columns a lane.
+        constexpr int kPer = D / 32;
+        const int row = 8 * half + quad + warp;
+        float m = -INFINITY, l = 0.f, f[kWarps];
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) m = fmaxf(m, join_m[w * kRows + row]);
         const float z = m == -INFINITY ? 0.f : m;
@@ -602,35 +601,44 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F32>::per_sm)
           f[w] = exp2_fast((join_m[w * kRows + row] - z) * p.scale);
           l += f[w] * join_l[w * kRows + row];
         }
-        // No key attended: zeros.
-        inv = m == -INFINITY && l == 0.f ? 0.f : 1.f / l;
-        if (!whole && (threadIdx.x & 7) == 0) {
-          part[kRows * D + row] = m;
-          part[kRows * D + kRows + row] = l;
-        }
-      }
-      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+        float a[kPer];
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float4 x4 =
-            *reinterpret_cast<const float4 *>(join + (w * kRows + row) * C::ld + col);
-        a.x += f[w] * x4.x;
-        a.y += f[w] * x4.y;
-        a.z += f[w] * x4.z;
-        a.w += f[w] * x4.w;
+        for (int e = 0; e < kPer; ++e) a[e] = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w)
+#pragma unroll
+          for (int e = 0; e < kPer; e += 2) {
+            const float2 v = *reinterpret_cast<const float2 *>(join + (w * 4 + warp) * C::ld +
+                                                               lane * kPer + e);
+            a[e] += f[w] * v.x;
+            a[e + 1] += f[w] * v.y;
+          }
+        if (!whole) {
+#pragma unroll
+          for (int e = 0; e < kPer; e += 2)
+            *reinterpret_cast<float2 *>(part + row * D + lane * kPer + e) =
+                make_float2(a[e], a[e + 1]);
+          if (lane == 0) {
+            part[kRows * D + row] = m;
+            part[kRows * D + kRows + row] = l;
+          }
+        } else if (row < live) {
+          const int i = u.tile * kRows + row, tok = p.G.div(i);
+          E *out = static_cast<E *>(p.o.p) + int64_t(u.t0 + tok) * p.o.ts +
+                   int64_t((u.head - tok) * static_cast<int>(p.G.d) + i) * p.o.hs + lane * kPer;
+          // No key attended: zeros.
+          const float inv = m == -INFINITY && l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+          for (int e = 0; e < kPer; e += 2) {
+            if constexpr (F32)
+              *reinterpret_cast<float2 *>(out + e) = make_float2(a[e] * inv, a[e + 1] * inv);
+            else
+              *reinterpret_cast<uint32_t *>(out + e) =
+                  bf16_bits(a[e] * inv) | (bf16_bits(a[e + 1] * inv) << 16);
+          }
+        }
+        __syncthreads();
       }
-      if (!whole) {
-        *reinterpret_cast<float4 *>(part + row * D + c0 + col) = a;
-      } else if (tok < u.n) {
-        if constexpr (F32)
-          *reinterpret_cast<float4 *>(out + c0 + col) =
-              make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
-        else
-          *reinterpret_cast<uint2 *>(out + c0 + col) =
-              make_uint2(bf16_bits(a.x * inv) | (bf16_bits(a.y * inv) << 16),
-                         bf16_bits(a.z * inv) | (bf16_bits(a.w * inv) << 16));
-      }
-      __syncthreads();
     }
     if (x + 1 == x1) {
       // A unit that begins here and goes on: the blocks after this one that
@@ -639,12 +647,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F32>::per_sm)
         int more = 0;
         if (begins && !whole) {
           const int64_t end = x1 + u.blocks - kb;  // first block of the line past the unit
-          more = static_cast<int>((end * parts - 1) / total) - static_cast<int>(blockIdx.x);
-          // Block c begins at floor(c total / parts): the last c that begins before end.
-          while ((blockIdx.x + more) * total / parts >= end) --more;
-          while ((blockIdx.x + more + 1) * total / parts < end &&
-                 int64_t(blockIdx.x) + more + 1 < parts)
-            ++more;
+          more = share.owner(end - 1) - static_cast<int>(blockIdx.x);
         }
         header[0] = more;
         header[1] = u.t0;
@@ -663,88 +666,61 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F32>::per_sm)
 }
 
 // Joins the pieces of a unit: the one that begins at the end of block c's part
-// and the continuations at the start of the parts after it. Four rows at a
-// time, four warps for each row, which take every fourth piece: loads of all
-// pieces are in flight together, since the latency of three loads after one
-// another (header, maxima, sums) is what this kernel costs.
-constexpr int kJoinWarps = 16;
+// and the continuations at the start of the parts after it. A thread per
+// column of a row, the loads of 32 pieces in flight together, lane c with the
+// maximum and the sum of weights of piece c. Bound by latency (a launch, the
+// header, the pieces: each the best part of a microsecond), so the code is kept
+// short as well: fetching it is part of that.
+constexpr int kJoinThreads = 512;
 template <int D, bool F32>
-__global__ void __launch_bounds__(kJoinWarps * 32)
+__global__ void __launch_bounds__(kJoinThreads)
     combine_kernel(const __grid_constant__ AttnStreamParams p) {
   using E = typename std::conditional<F32, float, uint16_t>::type;
-  constexpr int kPer = D / 32;
   constexpr int64_t kPart = kRows * (D + 2);
-  __shared__ float sums[kJoinWarps][D + 1];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, share = warp >> 2;
+  const int lane = threadIdx.x & 31, d = threadIdx.x % D;
   grid_dependency_wait();
   grid_dependents_launch();
   const int *h = p.headers + blockIdx.x * kHeader;
   const int more = h[0];
   if (more == 0) return;
   const int t0 = h[1], n = h[2], head = h[3], tile = h[4];
-  const float *first = p.parts + (int64_t(blockIdx.x) * 2 + 1) * kPart;
-  const float *rest = p.parts + (int64_t(blockIdx.x) + 1) * 2 * kPart;
-  auto piece = [&](int c) { return c == 0 ? first : rest + (c - 1) * 2 * kPart; };
-  for (int r0 = 0; r0 < kRows; r0 += 4) {
-    const int row = r0 + (warp & 3), i = tile * kRows + row, tok = i / p.G;
-    if ((tile * kRows + r0) / p.G >= n) return;
-    float m = -INFINITY;
-    for (int c = lane; c <= more; c += 32) m = fmaxf(m, piece(c)[kRows * D + row]);
+  // Piece 0, and pieces 1, 2, .. two apart from the next block's on.
+  const float *parts = p.parts + int64_t(blockIdx.x) * 2 * kPart;
+  auto piece = [&](int c) { return parts + (c == 0 ? kPart : c * 2 * kPart); };
+#pragma unroll 1
+  for (int row = threadIdx.x / D; row < kRows; row += kJoinThreads / D) {
+    const int i = tile * kRows + row, tok = p.G.div(i);
+    if (tok >= n) return;
+    float m = -INFINITY, l = 0.f, a = 0.f;
+#pragma unroll 1
+    for (int c0 = 0; c0 <= more; c0 += 32) {
+      const bool there = c0 + lane <= more;
+      const float *x = piece(there ? c0 + lane : 0) + kRows * D + row;
+      const float mc = there ? x[0] : -INFINITY, lc = there ? x[kRows] : 0.f;
+      float v[32];
 #pragma unroll
-    for (int s = 1; s < 32; s *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
-    const float z = m == -INFINITY ? 0.f : m;
-    float l = 0.f, a[kPer];
+      for (int c = 0; c < 32; ++c) v[c] = c0 + c <= more ? piece(c0 + c)[row * D + d] : 0.f;
+      float top = mc;
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) a[e] = 0.f;
-    // Lane j of a share has the factor of its piece 4 j + share of 128.
-    for (int c0 = 0; c0 <= more; c0 += 128) {
-      const int mine = c0 + 4 * lane + share;
-      float f = 0.f;
-      if (mine <= more) {
-        f = exp2_fast((piece(mine)[kRows * D + row] - z) * p.scale);
-        l += f * piece(mine)[kRows * D + kRows + row];
-      }
-      const int here = min(32, (more - c0 - share + 4) / 4);
-#pragma unroll 8
-      for (int j = 0; j < here; ++j) {
-        const float g = __shfl_sync(0xffffffffu, f, j);
-        const float *v = piece(c0 + 4 * j + share) + row * D + lane * kPer;
+      for (int s = 1; s < 32; s *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+      top = fmaxf(top, m);
+      const float z = top == -INFINITY ? 0.f : top;
+      const float old = exp2_fast((m - z) * p.scale), f = exp2_fast((mc - z) * p.scale);
+      m = top;
+      a *= old;
+      l = l * old + f * lc;
 #pragma unroll
-        for (int e = 0; e < kPer; e += 2) {
-          const float2 w = *reinterpret_cast<const float2 *>(v + e);
-          a[e] += g * w.x;
-          a[e + 1] += g * w.y;
-        }
-      }
+      for (int c = 0; c < 32; ++c) a += __shfl_sync(0xffffffffu, f, c) * v[c];
     }
 #pragma unroll
     for (int s = 1; s < 32; s *= 2) l += __shfl_xor_sync(0xffffffffu, l, s);
-    __syncthreads();
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) sums[warp][lane * kPer + e] = a[e];
-    if (lane == 0) sums[warp][D] = l;
-    __syncthreads();
-    if (share != 0 || tok >= n) continue;
-    l = 0.f;
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) a[e] = 0.f;
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      l += sums[4 * s + warp][D];
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) a[e] += sums[4 * s + warp][lane * kPer + e];
-    }
-    const float inv = m == -INFINITY && l == 0.f ? 0.f : 1.f / l;
+    a *= m == -INFINITY && l == 0.f ? 0.f : 1.f / l;
     E *out = static_cast<E *>(p.o.p) + int64_t(t0 + tok) * p.o.ts +
-             int64_t(head * p.G + i - tok * p.G) * p.o.hs + lane * kPer;
-#pragma unroll
-    for (int e = 0; e < kPer; e += 2) {
-      if constexpr (F32)
-        *reinterpret_cast<float2 *>(out + e) = make_float2(a[e] * inv, a[e + 1] * inv);
-      else
-        *reinterpret_cast<uint32_t *>(out + e) =
-            bf16_bits(a[e] * inv) | (bf16_bits(a[e + 1] * inv) << 16);
-    }
+             int64_t((head - tok) * static_cast<int>(p.G.d) + i) * p.o.hs + d;
+    if constexpr (F32)
+      *out = a;
+    else
+      *out = static_cast<uint16_t>(bf16_bits(a));
   }
 }
 
@@ -761,7 +737,7 @@ cudaError_t run(const AttnStreamParams &p, bool pdl, cudaStream_t stream) {
   const int grid = grid_blocks(F32, D);
   e = launch_after(stream_kernel<D, F32>, dim3(grid), kThreads, C::smem, pdl, stream, p);
   if (e != cudaSuccess) return e;
-  return launch_after(combine_kernel<D, F32>, dim3(grid), kJoinWarps * 32, 0, pdl,
+  return launch_after(combine_kernel<D, F32>, dim3(grid), kJoinThreads, 0, pdl,
                       stream, p);
 }
 
@@ -781,9 +757,9 @@ cudaError_t launch_attn_stream(const AttnArgs &a, cudaStream_t stream) {
   p.k = a.c.k;
   p.v = a.c.v;
   p.pages = static_cast<int>(a.c.pages);
-  p.page_size = a.c.page_size;
+  p.page_size = FastDiv(a.c.page_size);
   p.kv_heads = a.c.heads;
-  p.G = a.q.n / a.c.heads;
+  p.G = FastDiv(a.q.n / a.c.heads);
   p.b = a.b;
   p.T = static_cast<int>(a.T);
   p.cap = static_cast<int>(int64_t(a.b.table_pages) * a.c.page_size);

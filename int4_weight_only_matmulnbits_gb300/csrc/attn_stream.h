@@ -9,7 +9,8 @@ struct AttnStreamParams {
   Heads q, o;
   Pages k, v;
   BatchView b;
-  int pages, page_size, kv_heads, G;  // G: query heads per key head
+  int pages, kv_heads;
+  FastDiv page_size, G;               // G: query heads per key head
   int T, cap;                         // cap: tokens that a row of the table holds
   int window;                         // 0: none
   float scale;                        // |scale| of the scores, times log2(e)
