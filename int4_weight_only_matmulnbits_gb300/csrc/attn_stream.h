@@ -15,6 +15,7 @@ struct AttnStreamParams {
   int window;                         // 0: none
   float scale;                        // |scale| of the scores, times log2(e)
   int negative;                       // the scale is: scores change their sign
+  int cluster;                        // blocks of a cluster (one unit each), where they are used
   int *headers;                       // of the pieces that end a block's part
   float *parts;                       // two pieces per block: sums, maxima, sums of weights
 };
