@@ -6,7 +6,7 @@
 namespace mnb {
 
 size_t attn_workspace_bytes(const AttnArgs &a) {
-  return tile_path(a) ? tile_workspace_bytes(a) : stream_workspace_bytes(a.f32, a.c.D);
+  return tile_path(a) ? tile_workspace_bytes(a) : stream_workspace_bytes(a.c.D);
 }
 
 cudaError_t launch_attn(const AttnArgs &a, cudaStream_t stream) {

@@ -40,27 +40,30 @@ namespace mnb {
 namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
-constexpr int kRows = 16;         // query rows of a unit
-constexpr int kWarpKeys = 16;     // keys of a warp's step
-constexpr int kBlockKeys = kWarps * kWarpKeys;
 constexpr int kMinBlocks = 1;     // of the line per block of the grid
 constexpr int kHeader = 8;        // ints of a piece's header
 constexpr int kMaxCluster = 16;   // blocks of a cluster
 
-template <int D, bool F32>
+// ROWS query rows per unit: 16 on the tensor cores, 4 (fp32) on the FMA units.
+template <int D, bool F32, int ROWS>
 struct Cfg {
+  static constexpr bool few = ROWS == 4;
+  static constexpr int rows = ROWS;
+  static constexpr int keys = few ? 8 : 16;     // of a warp's step
+  static constexpr int block = kWarps * keys;   // of a block's step
   static constexpr int es = F32 ? 4 : 2;
   static constexpr int row = D * es;            // bytes of a key
-  static constexpr int step = 2 * kWarpKeys * row;  // keys and values of a warp's step
-  // 96 KB of copies for two blocks on an SM each, 192 KB where a step of 16
-  // keys is too large for that.
-  static constexpr int per_sm = row <= 256 ? 2 : 1;
+  static constexpr int step = 2 * keys * row;   // keys and values of a warp's step
+  // 96 KB of copies for two blocks on an SM each, 192 KB where three steps are
+  // too large for that.
+  static constexpr int per_sm = step * kWarps * 3 <= 98304 ? 2 : 1;
   static constexpr int stages = (per_sm == 2 ? 98304 : 196608) / (kWarps * step);
   static constexpr int ring = kWarps * stages * step;
   static constexpr int ld = D + 4;              // joined: four rows at a time
-  static constexpr int joins = (kWarps * 4 * ld + 2 * kWarps * kRows) * 4;
-  static constexpr int parts = F32 ? kRows * D * 6 : 0;  // the rows of q in bf16 parts
-  static constexpr int smem = ring + joins + parts;
+  static constexpr int joins = (kWarps * 4 * ld + 2 * kWarps * rows) * 4;
+  // fp32: the rows of q in bf16 parts, or a step's weights of each warp.
+  static constexpr int extra = few ? kWarps * keys * 16 : F32 ? rows * D * 6 : 0;
+  static constexpr int smem = ring + joins + extra;
   static_assert(stages >= 3, "copies in flight");
 };
 
@@ -131,11 +134,11 @@ __device__ __forceinline__ void mma_parts(float (&d)[4], const uint32_t (&a)[3][
 // pieces .. + t of keys g (keys) or the pieces .. + g of keys 2t (values).
 template <int D, bool F32>
 __device__ __forceinline__ int key_at(int k, int c) {
-  return k * Cfg<D, F32>::row + ((F32 ? c ^ ((k & 1) << 2) : c ^ (k & 7)) << 4);
+  return k * (D * (F32 ? 4 : 2)) + ((F32 ? c ^ ((k & 1) << 2) : c ^ (k & 7)) << 4);
 }
 template <int D, bool F32>
 __device__ __forceinline__ int value_at(int k, int c) {
-  return k * Cfg<D, F32>::row + ((F32 ? c ^ (((k >> 1) & 3) << 1) : c ^ (k & 7)) << 4);
+  return k * (D * (F32 ? 4 : 2)) + ((F32 ? c ^ (((k >> 1) & 3) << 1) : c ^ (k & 7)) << 4);
 }
 
 // A unit's place in the line of blocks and what it attends.
@@ -146,6 +149,7 @@ struct Unit {
   int last;               // position of the tile's last row: no key above it
 };
 
+template <typename C>
 struct Line {
   const AttnStreamParams &p;
   int lane;
@@ -153,10 +157,10 @@ struct Line {
     return load_seq(p.b, i, p.T, p.cap, p.window);
   }
   __device__ __forceinline__ int tiles(const Seq &s) const {
-    return (s.n * static_cast<int>(p.G.d) + kRows - 1) / kRows;
+    return (s.n * static_cast<int>(p.G.d) + C::rows - 1) / C::rows;
   }
   static __device__ __forceinline__ int blocks(const Seq &s) {
-    return max(1, (s.len - s.lo + kBlockKeys - 1) / kBlockKeys);
+    return max(1, (s.len - s.lo + C::block - 1) / C::block);
   }
   __device__ __forceinline__ int64_t work(const Seq &s) const {
     return int64_t(tiles(s)) * p.kv_heads * blocks(s);
@@ -233,7 +237,7 @@ struct Line {
     u.len = s.len;
     u.lo = s.lo;
     u.blocks = blocks(s);
-    u.last = s.len - s.n + min(s.n - 1, p.G.div(u.tile * kRows + kRows - 1));
+    u.last = s.len - s.n + min(s.n - 1, p.G.div(u.tile * C::rows + C::rows - 1));
   }
   // The unit after u (there is one).
   __device__ __forceinline__ void next(Unit &u) const {
@@ -247,16 +251,18 @@ struct Line {
   }
 };
 
-template <int D, bool F32, bool CLUSTER>
-__global__ void __launch_bounds__(kThreads, Cfg<D, F32>::per_sm)
+template <int D, bool F32, int ROWS, bool CLUSTER>
+__global__ void __launch_bounds__(kThreads, Cfg<D, F32, ROWS>::per_sm)
     stream_kernel(const __grid_constant__ AttnStreamParams p) {
-  using C = Cfg<D, F32>;
+  using C = Cfg<D, F32, ROWS>;
   using E = typename std::conditional<F32, float, uint16_t>::type;
+  constexpr int kRows = ROWS, kWarpKeys = C::keys, kBlockKeys = C::block;
   constexpr int kPieces = C::row / 16;            // 16-byte pieces of a key
   constexpr int kKeysAtOnce = 32 / kPieces > 0 ? 32 / kPieces : 1;
   constexpr int kSteps = kWarpKeys / kKeysAtOnce;  // copies per lane, keys or values
   constexpr int kQ = F32 ? 1 : D / 4;              // query registers
-  constexpr int kO = D / 8;                        // 8-wide column tiles
+  constexpr int kO = C::few ? 1 : D / 8;           // 8-wide column tiles
+  constexpr int kPer = D / 32;                     // columns of a lane, joining (few: all along)
   extern __shared__ __align__(128) unsigned char smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   unsigned char *ring = smem + warp * (C::stages * C::step);
@@ -264,11 +270,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F32>::per_sm)
   float *join = reinterpret_cast<float *>(smem + C::ring);  // [warp][4 rows][ld]
   float *join_m = join + kWarps * 4 * C::ld, *join_l = join_m + kWarps * kRows;
   uint4 *qparts = reinterpret_cast<uint4 *>(smem + C::ring + C::joins);  // [d / 16][part][lane]
+  float4 *weights_s = reinterpret_cast<float4 *>(smem + C::ring + C::joins) + warp * kWarpKeys;
 
   grid_dependency_wait();
   grid_dependents_launch();
 
-  const Line line{p, lane};
+  const Line<C> line{p, lane};
   Unit fu;
   int fk, slot = 0, rank = 0;
   int64_t x0, x1, total = 0;
@@ -357,7 +364,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F32>::per_sm)
   };
   // ---- the unit's rows ---------------------------------------------------------------
   uint32_t q[kQ];
-  int pos0 = 0, pos1 = 0;  // positions of the rows g and g + 8 (-1: no row)
+  float4 qf[C::few ? 4 : 1][C::few ? kPer : 1];
+  int pos0 = 0, pos1 = 0;  // positions of the rows g and g + 8, few: lane & 3 (-1: no row)
   auto load_rows = [&] {
     auto row_of = [&](int r, int &pos) -> const E * {
       const int i = u.tile * kRows + r, tok = p.G.div(i);
@@ -369,6 +377,20 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F32>::per_sm)
       return static_cast<const E *>(p.q.p) + int64_t(u.t0 + tok) * p.q.ts +
              int64_t((u.head - tok) * static_cast<int>(p.G.d) + i) * p.q.hs;
     };
+    if constexpr (C::few) {
+      // Lane `sub` of eight has the pieces sub, sub + 8, .. of all four rows.
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        int pos;
+        const E *a = row_of(r, pos);
+        if (r == (lane & 3)) pos0 = pos;
+#pragma unroll
+        for (int c = 0; c < kPer; ++c)
+          qf[r][c] = a ? *reinterpret_cast<const float4 *>(a + 4 * ((lane & 7) + 8 * c))
+                       : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      return;
+    }
     const E *a = row_of(g, pos0), *b = row_of(g + 8, pos1);
     if constexpr (F32) {
       // Each warp makes a quarter of the parts, in the order of the MMAs'
@@ -401,11 +423,56 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F32>::per_sm)
   };
 
   float o[kO][4], m0, m1, l0, l1;
+  float acc[C::few ? 4 : 1][kPer];  // few: four rows of a lane's columns
   auto clear = [&] {
+#pragma unroll
+    for (int r = 0; r < (C::few ? 4 : 1); ++r)
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) acc[r][e] = 0.f;
 #pragma unroll
     for (int i = 0; i < kO; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
     m0 = m1 = -INFINITY;
     l0 = l1 = 0.f;
+  };
+  // A masked value that is not finite would still make 0 * inf: such values of a
+  // step become 0, and the rows that do attend their keys (returned) NaN.
+  auto tidy_values = [&](uint32_t vs) {
+    unsigned bad = 0;
+#pragma unroll 2
+    for (int i = 0; i < kSteps; ++i) {
+      const int key = lane / kPieces + i * kKeysAtOnce;
+      unsigned char *at = ring + (vs - ring_u) + value_at<D, F32>(key, lane % kPieces);
+      uint4 w = *reinterpret_cast<uint4 *>(at);
+      bool hit = false;
+      auto tidy = [&](uint32_t &r) {
+        if constexpr (F32) {
+          if ((r & 0x7F800000u) == 0x7F800000u) {
+            r = 0;
+            hit = true;
+          }
+        } else {
+          if ((r & 0x7F80u) == 0x7F80u) {
+            r &= 0xFFFF0000u;
+            hit = true;
+          }
+          if ((r & 0x7F800000u) == 0x7F800000u) {
+            r &= 0xFFFFu;
+            hit = true;
+          }
+        }
+      };
+      tidy(w.x);
+      tidy(w.y);
+      tidy(w.z);
+      tidy(w.w);
+      if (hit) {
+        *reinterpret_cast<uint4 *>(at) = w;
+        bad |= 1u << key;
+      }
+    }
+    bad = __reduce_or_sync(0xffffffffu, bad);
+    __syncwarp();
+    return bad;
   };
   // (Their loads are under way while the first pages are looked up.)
   load_rows();
@@ -423,7 +490,94 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F32>::per_sm)
       cslot = cslot == C::stages - 1 ? 0 : cslot + 1;
       const int j0 = u.lo + kb * kBlockKeys + warp * kWarpKeys;
       const int top = u.last, bottom = u.len - u.n + p.G.div(u.tile * kRows);
-      if (there) {
+      const bool masked = j0 + kWarpKeys - 1 > bottom || (p.window > 0 && j0 <= top - p.window);
+      if constexpr (C::few) {
+        if (there) {
+          // Eight lanes per key, four keys at a time: a lane's pieces of a key
+          // times those of the four rows; then the lanes add up by halves, so that
+          // lane `lane` has the score of row lane & 3 and key 4 (lane >> 2 & 1) +
+          // (lane >> 3).
+          float s[2][4];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+#pragma unroll
+            for (int c = 0; c < kPer; ++c) {
+              const float4 k4 = lds4(ks + key_at<D, F32>(4 * i + (lane >> 3), (lane & 7) + 8 * c));
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+                s[i][r] += qf[r][c].x * k4.x + qf[r][c].y * k4.y + qf[r][c].z * k4.z +
+                           qf[r][c].w * k4.w;
+            }
+          }
+          float u4[4], u2[2];
+          const bool b2 = lane & 4, b1 = lane & 2, b0 = lane & 1;
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            u4[r] = (b2 ? s[1][r] : s[0][r]) +
+                    __shfl_xor_sync(0xffffffffu, b2 ? s[0][r] : s[1][r], 4);
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+            u2[r] = (b1 ? u4[2 + r] : u4[r]) +
+                    __shfl_xor_sync(0xffffffffu, b1 ? u4[r] : u4[2 + r], 2);
+          float sc = (b0 ? u2[1] : u2[0]) + __shfl_xor_sync(0xffffffffu, b0 ? u2[0] : u2[1], 1);
+          if (p.negative) sc = -sc;
+          const int key = 4 * ((lane >> 2) & 1) + (lane >> 3), j = j0 + key;
+          if (masked) {
+            const unsigned bad = tidy_values(vs);
+            if (j > pos0 || (p.window > 0 && j <= pos0 - p.window))
+              sc = -INFINITY;
+            else if ((bad >> key) & 1)
+              sc = NAN;
+          }
+          float n0 = sc;
+#pragma unroll
+          for (int k = 4; k < 32; k *= 2) n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, k));
+          n0 = fmaxf(m0, n0);
+          const float z0 = n0 == -INFINITY ? 0.f : n0;
+          if (__any_sync(0xffffffffu, n0 != m0)) {
+            const float f0 = exp2_fast((m0 - z0) * p.scale);
+            m0 = n0;
+            l0 *= f0;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const float f = __shfl_sync(0xffffffffu, f0, r);
+#pragma unroll
+              for (int e = 0; e < kPer; ++e) acc[r][e] *= f;
+            }
+          }
+          const float w = exp2_fast((sc - z0) * p.scale);
+          l0 += w;
+          reinterpret_cast<float *>(weights_s + key)[lane & 3] = w;
+          __syncwarp();
+          // A lane's columns of every key's values, times the four rows' weights.
+#pragma unroll
+          for (int k = 0; k < kWarpKeys; ++k) {
+            const float4 w4 = weights_s[k];
+            float v[kPer];
+            const uint32_t at = vs + value_at<D, F32>(k, lane * kPer / 4) + lane * kPer % 4 * 4;
+            if constexpr (kPer == 4) {
+              const float4 x = lds4(at);
+              v[0] = x.x;
+              v[1] = x.y;
+              v[2] = x.z;
+              v[3] = x.w;
+            } else {
+              asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];"
+                           : "=f"(v[0]), "=f"(v[1])
+                           : "r"(at)
+                           : "memory");
+            }
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) {
+              acc[0][e] += w4.x * v[e];
+              acc[1][e] += w4.y * v[e];
+              acc[2][e] += w4.z * v[e];
+              acc[3][e] += w4.w * v[e];
+            }
+          }
+        }
+      } else if (there) {
         // ---- scores of 16 rows and 16 keys
         float s[2][4];
 #pragma unroll
@@ -465,43 +619,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F32>::per_sm)
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[i][e] = p.negative ? -s[i][e] : s[i][e];
         // ---- masks, where some row of the tile does not attend some key
-        if (j0 + kWarpKeys - 1 > bottom || (p.window > 0 && j0 <= top - p.window)) {
-          // A masked value that is not finite would still make 0 * inf: such
-          // values become 0 here, and the rows that do attend the key NaN.
-          unsigned bad = 0;
-          for (int i = 0; i < kSteps; ++i) {
-            const int key = lane / kPieces + i * kKeysAtOnce;
-            unsigned char *at = ring + (vs - ring_u) + value_at<D, F32>(key, lane % kPieces);
-            uint4 w = *reinterpret_cast<uint4 *>(at);
-            bool hit = false;
-            auto tidy = [&](uint32_t &r) {
-              if constexpr (F32) {
-                if ((r & 0x7F800000u) == 0x7F800000u) {
-                  r = 0;
-                  hit = true;
-                }
-              } else {
-                if ((r & 0x7F80u) == 0x7F80u) {
-                  r &= 0xFFFF0000u;
-                  hit = true;
-                }
-                if ((r & 0x7F800000u) == 0x7F800000u) {
-                  r &= 0xFFFFu;
-                  hit = true;
-                }
-              }
-            };
-            tidy(w.x);
-            tidy(w.y);
-            tidy(w.z);
-            tidy(w.w);
-            if (hit) {
-              *reinterpret_cast<uint4 *>(at) = w;
-              bad |= 1u << key;
-            }
-          }
-          bad = __reduce_or_sync(0xffffffffu, bad);
-          __syncwarp();
+        if (masked) {
+          const unsigned bad = tidy_values(vs);
 #pragma unroll
           for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -597,15 +716,24 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F32>::per_sm)
     }
 
     // ---- end of a piece: the warps' sums joined, four rows at a time ---------------
-    l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
-    l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
-    if (t == 0) {
-      join_m[warp * kRows + g] = m0;
-      join_m[warp * kRows + g + 8] = m1;
-      join_l[warp * kRows + g] = l0;
-      join_l[warp * kRows + g + 8] = l1;
+    if constexpr (C::few) {
+#pragma unroll
+      for (int k = 4; k < 32; k *= 2) l0 += __shfl_xor_sync(0xffffffffu, l0, k);
+      if (lane < 4) {
+        join_m[warp * kRows + lane] = m0;
+        join_l[warp * kRows + lane] = l0;
+      }
+    } else {
+      l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+      l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+      l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+      l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+      if (t == 0) {
+        join_m[warp * kRows + g] = m0;
+        join_m[warp * kRows + g + 8] = m1;
+        join_l[warp * kRows + g] = l0;
+        join_l[warp * kRows + g + 8] = l1;
+      }
     }
     const bool begins = piece0 == 0, whole = begins && kb == u.blocks;
     const int64_t piece = int64_t(blockIdx.x) * 2 + (begins ? 1 : 0);
@@ -617,11 +745,17 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F32>::per_sm)
     }
     const int live = min(kRows, u.n * static_cast<int>(p.G.d) - u.tile * kRows);
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
+    for (int half = 0; half < (C::few ? 1 : 2); ++half) {
 #pragma unroll 1
-      for (int quad = 0; quad < 8; quad += 4) {
+      for (int quad = 0; quad < (C::few ? 4 : 8); quad += 4) {
         if (8 * half + quad >= live) break;
-        if ((g & 4) == quad) {
+        if constexpr (C::few) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int e = 0; e < kPer; ++e)
+              join[(warp * 4 + r) * C::ld + lane * kPer + e] = acc[r][e];
+        } else if ((g & 4) == quad) {
           float *mine = join + (warp * 4 + (g & 3)) * C::ld;
 #pragma unroll
           for (int c = 0; c < kO; ++c) {
@@ -637,7 +771,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F32>::per_sm)
         }
         __syncthreads();
         // A warp per row, kPer columns a lane.
-        constexpr int kPer = D / 32;
         const int row = 8 * half + quad + warp;
         float m = -INFINITY, l = 0.f, f[kWarps];
 #pragma unroll
@@ -759,10 +892,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F32>::per_sm)
 // header, the pieces: each the best part of a microsecond), so the code is kept
 // short as well: fetching it is part of that.
 constexpr int kJoinThreads = 512;
-template <int D, bool F32>
+template <int D, bool F32, int ROWS>
 __global__ void __launch_bounds__(kJoinThreads)
     combine_kernel(const __grid_constant__ AttnStreamParams p) {
   using E = typename std::conditional<F32, float, uint16_t>::type;
+  constexpr int kRows = ROWS;
   constexpr int64_t kPart = kRows * (D + 2);
   const int lane = threadIdx.x & 31, d = threadIdx.x % D;
   grid_dependency_wait();
@@ -811,9 +945,8 @@ __global__ void __launch_bounds__(kJoinThreads)
   }
 }
 
-int grid_blocks(bool f32, int D) {
-  return std::max(1, sm_count()) * (D * (f32 ? 4 : 2) <= 256 ? 2 : 1);
-}
+// Blocks of the grid, at most two on an SM.
+int grid_blocks(int per_sm) { return std::max(1, sm_count()) * per_sm; }
 
 // Clusters of `kernel` that the current device holds at once (asked once per
 // device; 0: none, or the question failed).
@@ -833,9 +966,10 @@ int clusters_at_once(Kernel kernel, const cudaLaunchConfig_t &cfg, std::atomic<i
   return n;
 }
 
-template <int D, bool F32>
+template <int D, bool F32, int ROWS>
 cudaError_t run(const AttnStreamParams &p, bool pdl, cudaStream_t stream) {
-  using C = Cfg<D, F32>;
+  using C = Cfg<D, F32, ROWS>;
+  constexpr int kRows = ROWS;
   // The most units that T rows of n sequences make.
   const int64_t few = std::min<int64_t>(p.b.n, p.T);
   const int64_t units =
@@ -848,7 +982,7 @@ cudaError_t run(const AttnStreamParams &p, bool pdl, cudaStream_t stream) {
     const double bytes = 2.0 * p.cap * p.kv_heads * C::row;
     const double rate = std::min(6500.0, 45.0 * p.kv_heads * size);
     if (bytes * 1e-3 * (1 / rate - 1 / 6500.0) > 4.3) continue;
-    auto *kernel = stream_kernel<D, F32, true>;
+    auto *kernel = stream_kernel<D, F32, ROWS, true>;
     static std::atomic<unsigned long long> done{0};
     static std::atomic<int> known[2][64];
     cudaError_t e = ensure_smem_limit(kernel, C::smem, done);
@@ -873,23 +1007,23 @@ cudaError_t run(const AttnStreamParams &p, bool pdl, cudaStream_t stream) {
     q.cluster = size;
     return cudaLaunchKernelEx(&cfg, kernel, q);
   }
-  auto *kernel = stream_kernel<D, F32, false>;
+  auto *kernel = stream_kernel<D, F32, ROWS, false>;
   static std::atomic<unsigned long long> done{0};
   cudaError_t e = ensure_smem_limit(kernel, C::smem, done);
   if (e != cudaSuccess) return e;
-  const int grid = grid_blocks(F32, D);
+  const int grid = grid_blocks(C::per_sm);
   e = launch_after(kernel, dim3(grid), kThreads, C::smem, pdl, stream, p);
   if (e != cudaSuccess) return e;
-  return launch_after(combine_kernel<D, F32>, dim3(grid), kJoinThreads, 0, pdl, stream, p);
+  return launch_after(combine_kernel<D, F32, ROWS>, dim3(grid), kJoinThreads, 0, pdl, stream, p);
 }
 
 size_t header_bytes(int grid) { return (size_t(grid) * kHeader * 4 + 255) & ~size_t(255); }
 
 }  // namespace
 
-size_t stream_workspace_bytes(bool f32, int D) {
-  const int grid = grid_blocks(f32, D);
-  return header_bytes(grid) + size_t(grid) * 2 * kRows * (D + 2) * 4;
+size_t stream_workspace_bytes(int D) {
+  const int grid = grid_blocks(2);
+  return header_bytes(grid) + size_t(grid) * 2 * 16 * (D + 2) * 4;
 }
 
 cudaError_t launch_attn_stream(const AttnArgs &a, cudaStream_t stream) {
@@ -912,10 +1046,19 @@ cudaError_t launch_attn_stream(const AttnArgs &a, cudaStream_t stream) {
       std::min(std::max(std::fabs(static_cast<double>(a.scale)) * M_LOG2E, 1e-37), 3e38));
   p.negative = a.scale < 0.f;
   p.headers = reinterpret_cast<int *>(a.ws);
-  p.parts = reinterpret_cast<float *>(a.ws + header_bytes(grid_blocks(a.f32, a.c.D)));
-  if (a.f32)
-    return a.c.D == 64 ? run<64, true>(p, a.pdl, stream) : run<128, true>(p, a.pdl, stream);
-  return a.c.D == 64 ? run<64, false>(p, a.pdl, stream) : run<128, false>(p, a.pdl, stream);
+  p.parts = reinterpret_cast<float *>(a.ws + header_bytes(grid_blocks(2)));
+  const bool wide = a.c.D == 128;
+  if (!a.f32)
+    return wide ? run<128, false, 16>(p, a.pdl, stream) : run<64, false, 16>(p, a.pdl, stream);
+  // Four rows a sequence or fewer: fp32 products on the FMA units, some 340
+  // instructions for 8 keys, where bf16 parts take 500 for the tensor cores,
+  // whose other rows would be empty, and half of the shared memory. Measured
+  // with 2 query heads per key head, 8 of those (us, FMA / tensor cores): one
+  // sequence of 2049 tokens, 2 rows 9.5 / 14.3, 8 rows 12.3 / 14.6, 16 rows of
+  // 8000 37 / 32; 16 sequences of 2049, 4 rows each 48 / 66, 8 rows 72 / 68.
+  if (a.T * p.G.d <= std::max<int64_t>(8, 4 * std::min<int64_t>(a.b.n, a.T)))
+    return wide ? run<128, true, 4>(p, a.pdl, stream) : run<64, true, 4>(p, a.pdl, stream);
+  return wide ? run<128, true, 16>(p, a.pdl, stream) : run<64, true, 16>(p, a.pdl, stream);
 }
 
 }  // namespace mnb

@@ -20,7 +20,7 @@ struct AttnStreamParams {
   float *parts;                       // two pieces per block: sums, maxima, sums of weights
 };
 
-size_t stream_workspace_bytes(bool f32, int D);
+size_t stream_workspace_bytes(int D);
 cudaError_t launch_attn_stream(const AttnArgs &a, cudaStream_t stream);
 
 }  // namespace mnb

@@ -278,26 +278,28 @@ __device__ __forceinline__ I block_scan(I v, I *sums, int tid) {
 }
 
 // Lists the units of a key head and where in the line each begins: one block,
-// a warp per sequence. Latency-bound.
+// a warp per sequence. Latency-bound. (Sequences that overlap, which `starts`
+// must not describe, could make more units than there is room for: those past
+// it are left out.)
 constexpr int kPlanThreads = 1024;
 __global__ void __launch_bounds__(kPlanThreads)
     plan_kernel(const __grid_constant__ AttnTileParams p) {
   __shared__ int64_t sums[32];
-  __shared__ int offset[kPlanThreads];
+  __shared__ int64_t offset[kPlanThreads];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   grid_dependency_wait();
   grid_dependents_launch();
-  int base = 0;
+  int64_t base = 0;
   for (int b0 = 0; b0 < p.b.n; b0 += kPlanThreads) {
     int mine = 0;
     if (b0 + tid < p.b.n) mine = units_of(load_seq(p.b, b0 + tid, p.T, p.cap, p.window), p.G);
-    const int upto = static_cast<int>(block_scan<int64_t>(mine, sums, tid));
+    const int64_t upto = block_scan<int64_t>(mine, sums, tid);
     offset[tid] = base + upto - mine;
-    base += static_cast<int>(sums[31]);
+    base += sums[31];
     __syncthreads();
     for (int i = warp; i < min(kPlanThreads, p.b.n - b0); i += 32) {
       const Seq s = load_seq(p.b, b0 + i, p.T, p.cap, p.window);
-      const int n = units_of(s, p.G);
+      const int64_t n = min(int64_t(units_of(s, p.G)), p.most - offset[i]);
       for (int t = lane; t < n; t += 32) {
         Unit u{s.t0, s.n, s.len, t, 0, 0, b0 + i};
         if (p.window > 0) u.block0 = max(0, first_pos(u, p.G) - p.window + 1) / kTile;
@@ -308,8 +310,9 @@ __global__ void __launch_bounds__(kPlanThreads)
     }
     __syncthreads();
   }
+  base = min(base, p.most);
   int64_t at = 0;
-  for (int u0 = 0; u0 < base; u0 += kPlanThreads) {
+  for (int64_t u0 = 0; u0 < base; u0 += kPlanThreads) {
     const int64_t mine = u0 + tid < base ? p.units[2 * (u0 + tid) + 1].y : 0;
     const int64_t upto = block_scan<int64_t>(mine, sums, tid);
     if (u0 + tid < base) p.first[u0 + tid] = at + upto - mine;
@@ -1052,6 +1055,12 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ At
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
+// The most units that T rows of n sequences make.
+int64_t most_units(const AttnArgs &a) {
+  const int64_t G = a.q.n / a.c.heads, few = std::min<int64_t>(a.b.n, a.T);
+  return (a.T * G + (kUnit - 1) * few) / kUnit;
+}
+
 struct Space {
   int64_t *line, *first;
   int4 *units;
@@ -1060,8 +1069,7 @@ struct Space {
   size_t bytes;
 };
 Space space(unsigned char *ws, const AttnArgs &a) {
-  const int64_t G = a.q.n / a.c.heads;
-  const int64_t most = a.T * G / kUnit + std::min<int64_t>(a.b.n, a.T) + 1;
+  const int64_t most = most_units(a);
   const size_t ctas = std::max(1, sm_count());
   Space s{};
   size_t at = 0;
@@ -1101,8 +1109,14 @@ bool tile_path(const AttnArgs &a) {
   // What a tensor map can describe.
   for (int64_t s : {a.c.k.ps, a.c.k.hs, a.c.k.ts, a.c.v.ps, a.c.v.hs, a.c.v.ts})
     if (s * 2 >= int64_t(1) << 40) return false;
+  // The streaming kernel reads a sequence's keys for every 16 rows, this one for
+  // every 256, at some 12 us more for its plan and its joins. Measured with 4
+  // query heads per key head, 8 of those (us, streaming / this): one sequence of
+  // 2000 tokens, 64 rows 11 / 23, 128 rows 24 / 25; of 16000, 48 rows 36 / 38,
+  // 64 rows 44 / 38; 16 sequences of 2000, 16 rows each 38 / 43, 20 rows 45 / 44;
+  // of 16000, 16 rows 172 / 217, 20 rows 319 / 218.
   const int64_t G = a.q.n / a.c.heads;
-  return a.T * G > 16 * std::min<int64_t>(a.b.n, a.T);
+  return a.T * G > std::max<int64_t>(64, 16 * std::min<int64_t>(a.b.n, a.T));
 }
 
 size_t tile_workspace_bytes(const AttnArgs &a) { return space(nullptr, a).bytes; }
@@ -1151,6 +1165,7 @@ cudaError_t launch_attn_tile(const AttnArgs &a, cudaStream_t stream) {
   p.line = s.line;
   p.first = s.first;
   p.units = s.units;
+  p.most = most_units(a);
   p.headers = s.headers;
   p.parts = s.parts;
   return a.c.D == 64 ? run<64>(p, a.pdl, stream) : run<128>(p, a.pdl, stream);

@@ -18,7 +18,8 @@ struct AttnTileParams {
   int negative, q_tma;
   int64_t *line;  // [0]: blocks of a key head, [1]: units
   int64_t *first; // [units + 1]: first block of each unit, within a key head
-  int4 *units;    // [2 units]: t0, n, len, tile; first block of keys, blocks
+  int4 *units;    // [2 units]: t0, n, len, tile; first block of keys, blocks, sequence
+  int64_t most;   // units that there is room for
   int *headers;
   float *parts;
 };

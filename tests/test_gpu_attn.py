@@ -21,6 +21,12 @@ def dev():
     return torch.device("cuda:0")
 
 
+@pytest.fixture(autouse=True)
+def no_wait_ran_out(dev):
+    yield
+    assert mnb.mnb_fault_status() == 0
+
+
 def within(got, want, bound):
     got = got.double().cpu()
     assert torch.isfinite(got).all(), "not finite"
@@ -134,6 +140,41 @@ def test_one_of_a_kind(dev):
     assert torch.equal(yq, q)
     want, mag = ref.norm_rotate(k.cpu(), gamma, 1e-6, None, None, pos, False)
     within(yk, want, ref.norm_rotate_bound(want, mag, 64, F32, True))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("inter,norm", [(False, True), (True, False)])
+def test_many_rows_equal_few(dev, inter, norm, dtype):
+    """Thousands of rows (several heads a group of lanes) bit for bit as the same rows in small
+    calls, for odd counts of heads."""
+    g = torch.Generator().manual_seed(7)
+    T, hq, hk, D = 4801, 29, 7, 128
+    qkv = torch.randn(T, hq + 2 * hk, D, generator=g).to(dtype).to(dev)
+    q, k, v = qkv[:, :hq], qkv[:, hq:hq + hk], qkv[:, hq + hk:]
+    r = mnb.RopeTable(*(t.to(dev) for t in tables(4900, 64)))
+    pos = torch.randint(0, 4900, (T,), generator=g, dtype=torch.int32).to(dev)
+    gamma = torch.rand(D, generator=g).to(dev) if norm else None
+    kw = dict(gamma_q=gamma, gamma_k=gamma, interleaved=inter)
+    yq, yk = mnb.mnb_qk_norm_rope(q, k, r, pos, **kw)
+    # Three sequences, the second one with nothing new, 40 rows behind the last.
+    starts, lens = [0, 4000, 4000, T - 40], [4000, 5, 861]
+    ps = 256
+    _, table, pages, _ = make_batch(g, [4000, 0, 761], lens, ps)
+    cache = make_cache(g, pages, hk, ps, D, dtype)
+    k0, v0 = cache.k.clone(), cache.v.clone()
+    out = torch.full_like(yq, 7.0)
+    mnb.mnb_cache_append(q, k, v, cache, on_gpu(starts, lens, table), r, out=out, **kw)
+    assert torch.all(out[T - 40:] == 7.0)
+    for a in range(0, T, 1000):
+        zq, zk = mnb.mnb_qk_norm_rope(q[a:a + 50], k[a:a + 50], r, pos[a:a + 50], **kw)
+        assert torch.equal(zq, yq[a:a + 50]) and torch.equal(zk, yk[a:a + 50])
+    where = torch.tensor([p for _, p, _, _ in ref.places(starts, lens, table, ps, pages, T)],
+                         dtype=torch.int32).to(dev)
+    zq, zk = mnb.mnb_qk_norm_rope(q[:T - 40], k[:T - 40], r, where, **kw)
+    assert torch.equal(out[:T - 40], zq)
+    for t, _, page, at in ref.places(starts, lens, table, ps, pages, T):
+        k0[page, :, at], v0[page, :, at] = zk[t], v[t]
+    assert torch.equal(cache.k, k0) and torch.equal(cache.v, v0)
 
 
 def test_rows_of_zeros_and_a_row_of_nan(dev):
@@ -290,6 +331,10 @@ CASES = [
     ([7, 0, 3], [50, 0, 3], 15, 3, 48), ([5], [200], 7, 1, 256), ([16, 33], [16, 95], 6, 2, 64),
     ([1, 1], [4000, 5], 16, 1, 16), ([3], [130], 40, 2, 128), ([100], [100], 4, 2, 16),
     ([65, 1, 140], [321, 77, 140], 8, 2, 32), ([257], [300], 5, 1, 16), ([300], [1000], 2, 1, 1024),
+    # One sequence and few, of few rows: clusters of 16 and 8 blocks, and more units than fit them.
+    ([8], [200], 16, 8, 16), ([4], [1030], 30, 15, 16), ([1, 1, 1], [700, 16, 90], 12, 4, 16),
+    ([2], [333], 8, 1, 16), ([1], [2500], 64, 32, 16), ([0, 1], [5, 999], 8, 8, 64),
+    ([16], [900], 4, 1, 16), ([17], [900], 4, 1, 16), ([2], [64], 4, 2, 16), ([3], [640], 4, 2, 16),
 ]
 
 
@@ -380,6 +425,49 @@ def test_pages_that_do_not_exist_and_empty_rows(dev, n, dtype):
     want, bound = ref.attend(q.cpu(), cache.k.cpu(), cache.v.cpu(), starts, lens, table, D ** -0.5,
                              5)
     within(y, want, bound)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n", [1, 40])
+def test_arrays_that_make_no_sense(dev, n, dtype):
+    """Starts that decrease, overlap or lie outside, lengths of any size, pages of any number: some
+    result or other, nothing outside the buffers."""
+    g = torch.Generator().manual_seed(28)
+    B, T, ps = 9, 3 * n, 16
+    cache = make_cache(g, 6, 2, ps, 64, dtype)
+    q = rows(g, T, 4, 64, dtype)
+    for starts in ([0, T] * 5, [T, 0] * 5, [-5, T + 99] * 5, [2 ** 31 - 1, -2 ** 31] * 5):
+        lens = [int(x) for x in torch.randint(-50, 200, (B,), generator=g)]
+        lens[3], lens[4] = 2 ** 31 - 1, -2 ** 31
+        table = torch.randint(-3, 9, (B, 5), generator=g, dtype=torch.int32)
+        table[0, 0], table[1, 1] = 2 ** 31 - 1, -2 ** 31
+        for window in (0, 7):
+            guard = torch.full((T + 8, 4, 64), 7.0, dtype=dtype, device=dev)
+            batch = on_gpu(starts, lens, table)
+            mnb.mnb_paged_attention(q, cache, batch, window=window, out=guard[4:T + 4])
+            mnb.mnb_cache_append(None, rows(g, T, 2, 64, dtype), rows(g, T, 2, 64, dtype), cache,
+                                 batch)
+            assert torch.all(guard[:4] == 7.0) and torch.all(guard[T + 4:] == 7.0)
+
+
+def test_broadcast_queries(dev):
+    """Queries without a stride of their own between heads or tokens (expanded views)."""
+    g = torch.Generator().manual_seed(29)
+    for n in (1, 90):
+        starts, table, pages, T = make_batch(g, [n], [200], 16)
+        cache = make_cache(g, pages, 2, 16, 64, BF16)
+        one = torch.randn(T, 1, 64, generator=g).to(BF16).to(dev).expand(T, 4, 64)
+        tok = torch.randn(1, 4, 64, generator=g).to(BF16).to(dev).expand(T, 4, 64)
+        for q in (one, tok):
+            batch = on_gpu(starts, [200], table)
+            assert torch.equal(mnb.mnb_paged_attention(q, cache, batch),
+                               mnb.mnb_paged_attention(q.contiguous(), cache, batch))
+
+
+def test_more_sequences_than_a_round_of_the_plan(dev):
+    g = torch.Generator().manual_seed(30)
+    lens = [5 + i % 3 for i in range(1100)]
+    attend(g, [5 if i % 7 else 0 for i in range(1100)], lens, 4, 1, 64, 16, BF16)
 
 
 def test_lengths_past_the_table(dev):
