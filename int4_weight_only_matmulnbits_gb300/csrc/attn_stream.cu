@@ -117,15 +117,22 @@ __device__ __forceinline__ void split3(float x, float y, uint32_t &h, uint32_t &
   y -= __uint_as_float(m & 0xFFFF0000u);
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(l) : "f"(y), "f"(x));
 }
-// d += a b from the parts (0: h, 1: m, 2: l), the smallest products first.
+// d += a b from the parts (0: h, 1: m, 2: l), the smallest products first. The
+// tensor cores cut off what they add up, relative to the sum so far: the
+// products of 16 terms begin a sum of their own, which is added to d with
+// rounding. (Added up in d itself, they lost three times as much as fp32 sums
+// with rounding do.)
 __device__ __forceinline__ void mma_parts(float (&d)[4], const uint32_t (&a)[3][4],
                                           const uint32_t (&b0)[3], const uint32_t (&b1)[3]) {
-  mma_bf16_16816(d, a[2], b0[0], b1[0]);
-  mma_bf16_16816(d, a[0], b0[2], b1[2]);
-  mma_bf16_16816(d, a[1], b0[1], b1[1]);
-  mma_bf16_16816(d, a[1], b0[0], b1[0]);
-  mma_bf16_16816(d, a[0], b0[1], b1[1]);
-  mma_bf16_16816(d, a[0], b0[0], b1[0]);
+  float t[4];
+  mma_bf16_16816_zero(t, a[2], b0[0], b1[0]);
+  mma_bf16_16816(t, a[0], b0[2], b1[2]);
+  mma_bf16_16816(t, a[1], b0[1], b1[1]);
+  mma_bf16_16816(t, a[1], b0[0], b1[0]);
+  mma_bf16_16816(t, a[0], b0[1], b1[1]);
+  mma_bf16_16816(t, a[0], b0[0], b1[0]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) d[i] += t[i];
 }
 
 // Bytes 16-byte piece `c` of key `k` lies at in a step's keys or values: pieces
