@@ -1084,21 +1084,16 @@ def mnb_rope_table(frequencies: torch.Tensor, n: int, *, first: int = 0, magnitu
                    device=None, stream=None) -> RopeTable:
     """Cosines and sines of the positions first .. first + n - 1, times
     magnitude, for the frequencies (float64, on the CPU)."""
-    if frequencies.is_cuda or frequencies.dtype != torch.float64:
-        raise ValueError("frequencies must be a contiguous float64 vector on the CPU")
-    if device is not None:
-        dev = torch.device(device)
-    else:
-        dev = torch.device("cuda") if stream is None else stream.device
+    fn = (_native_mod or _native()).rope_table
+    if device is None and stream is None:  # the current device
+        return RopeTable(*fn(frequencies, n, first, magnitude, -1))
+    dev = torch.device(device) if device is not None else stream.device
     if dev.type != "cuda":
         raise ValueError("the tables are made on a GPU")
-    here = torch.cuda.current_device()
-    index = here if dev.index is None else dev.index
-    fn = (_native_mod or _native()).rope_table
-    if stream is None and index == here:
-        return RopeTable(*fn(frequencies, n, first, magnitude, index))
-    return _call_on(torch.device("cuda", index), stream,
-                    lambda _: RopeTable(*fn(frequencies, n, first, magnitude, index)))
+    if dev.index is None:
+        dev = torch.device("cuda", torch.cuda.current_device())
+    return _call_on(dev, stream,
+                    lambda _: RopeTable(*fn(frequencies, n, first, magnitude, dev.index)))
 
 
 def mnb_qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, rope: RopeTable | None,

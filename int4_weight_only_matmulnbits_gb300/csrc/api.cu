@@ -1803,7 +1803,8 @@ mnb_status mnb_rope_table(const double *frequencies, int rot_dim, int64_t first,
   if (overlap(cos, bytes, sin, bytes)) return MNB_ERR_ALIAS;
   const mnb_status st = check_device();
   if (st != MNB_OK) return st;
-  const RopeTableArgs a{rot_dim / 2, first, n, magnitude, frequencies, cos, sin};
+  const RopeTableArgs a{rot_dim / 2, first, n, magnitude, frequencies, cos, sin,
+                        g_pdl.load() != 0};
   const cudaError_t e = launch_rope_table(a, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "mnb_rope_table");
   return MNB_OK;

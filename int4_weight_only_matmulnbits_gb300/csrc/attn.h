@@ -45,6 +45,7 @@ struct RopeTableArgs {
   double magnitude;
   const double *frequencies;  // HOST
   float *cos, *sin;
+  bool pdl;
 };
 cudaError_t launch_rope_table(const RopeTableArgs &a, cudaStream_t stream);
 

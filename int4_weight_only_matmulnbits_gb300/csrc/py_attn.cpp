@@ -357,7 +357,7 @@ PyObject *paged_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return y.take();
 }
 
-// frequencies, n, first, magnitude, device
+// frequencies, n, first, magnitude, device (-1: the current one)
 PyObject *rope_table(PyObject *, PyObject *const *a, Py_ssize_t n) {
   if (n != 5) return PyErr_Format(PyExc_TypeError, "5 arguments, not %zd", n);
   Tensor f;
@@ -367,8 +367,9 @@ PyObject *rope_table(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return refuse("frequencies must be a contiguous float64 vector on the CPU"), nullptr;
   const long long rows = PyLong_AsLongLong(a[1]), first = PyLong_AsLongLong(a[2]);
   const double magnitude = PyFloat_AsDouble(a[3]);
-  const long dev = PyLong_AsLong(a[4]);
+  long dev = PyLong_AsLong(a[4]);
   if (PyErr_Occurred()) return nullptr;
+  if (dev < 0) dev = c10::cuda::current_device();
   if (!is_current(dev)) return Py_NewRef(Py_NotImplemented);
   const int64_t pairs = f.shape[0];
   if (rows < 0 || pairs > (1 << 20)) return refuse("n must not be negative"), nullptr;

@@ -79,6 +79,8 @@ __global__ void __launch_bounds__(256) table_kernel(const __grid_constant__ Tabl
   uint64_t turns[V];
 #pragma unroll
   for (int e = 0; e < V; ++e) turns[e] = p.turns[j + e];
+  grid_dependency_wait();
+  grid_dependents_launch();
   const int64_t row0 = blockIdx.x * int64_t(kTableRows);
   const int rows = static_cast<int>(min(int64_t(kTableRows), p.n - row0));
   for (int r = r0; r < rows; r += at_once) {
@@ -169,7 +171,7 @@ struct Vec {  // 16 bytes of a row
       if constexpr (F32)
         w[i] = __float_as_uint(v[i]);
       else
-        w[i] = bf16_bits(v[2 * i]) | (bf16_bits(v[2 * i + 1]) << 16);
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(v[2 * i + 1]), "f"(v[2 * i]));
     return make_uint4(w[0], w[1], w[2], w[3]);
   }
 };
@@ -193,8 +195,9 @@ __device__ __forceinline__ void load_floats(const float *p, float (&v)[N]) {
 // no position, go first, all together, and its cosines and sines serve all of
 // them. Bound by memory: every row is read and written once; the tables,
 // shared by a token's heads, add rot * 4 bytes to it.
+constexpr int kRopeThreads = 64;
 template <bool F32, int LANES, int R, bool APPEND>
-__global__ void __launch_bounds__(128, R > 1 ? 6 : 8) rope_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, R > 1 ? 12 : 16) rope_kernel(const __grid_constant__ RopeArgs a) {
   using V = Vec<F32>;
   constexpr int N = V::N;
   using E = typename std::conditional<F32, float, uint16_t>::type;
@@ -202,7 +205,7 @@ __global__ void __launch_bounds__(128, R > 1 ? 6 : 8) rope_kernel(const __grid_c
   grid_dependency_wait();
   grid_dependents_launch();
   const int rows = a.q.n + a.k.n + a.v.n, per = (rows + R - 1) / R;  // groups per token
-  const int64_t g0 = (blockIdx.x * int64_t(128) + (threadIdx.x & ~31)) / LANES;
+  const int64_t g0 = (blockIdx.x * int64_t(kRopeThreads) + (threadIdx.x & ~31)) / LANES;
   const int64_t t0 = g0 / per;
   // The warp's groups are neighbours: same token, or the next ones.
   const int in = static_cast<int>(g0 - t0 * per) + lane / LANES;
@@ -405,7 +408,7 @@ cudaError_t run_rope(const RopeArgs &a, cudaStream_t stream) {
   // group is sooner done.
   const bool many = a.T * rows * lanes >= int64_t(4) * 2048 * std::max(1, sm_count());
   const int64_t groups = a.T * ceil_div(rows, many ? 4 : 1);
-  const int64_t blocks = ceil_div(groups * lanes, 128);
+  const int64_t blocks = ceil_div(groups * lanes, kRopeThreads);
   if (blocks > (int64_t(1) << 31) - 1) return cudaErrorInvalidValue;
   void (*const kernels[2][4])(RopeArgs) = {
       {rope_kernel<F32, 4, 1, APPEND>, rope_kernel<F32, 8, 1, APPEND>,
@@ -413,7 +416,7 @@ cudaError_t run_rope(const RopeArgs &a, cudaStream_t stream) {
       {rope_kernel<F32, 4, 4, APPEND>, rope_kernel<F32, 8, 4, APPEND>,
        rope_kernel<F32, 16, 4, APPEND>, rope_kernel<F32, 32, 4, APPEND>}};
   auto *kernel = kernels[many][lanes == 4 ? 0 : lanes == 8 ? 1 : lanes == 16 ? 2 : 3];
-  return launch_after(kernel, dim3(static_cast<unsigned>(blocks)), 128, 0, a.pdl, stream, a);
+  return launch_after(kernel, dim3(static_cast<unsigned>(blocks)), kRopeThreads, 0, a.pdl, stream, a);
 }
 
 }  // namespace
@@ -436,11 +439,8 @@ cudaError_t launch_rope_table(const RopeTableArgs &a, cudaStream_t stream) {
   p.sin = a.sin;
   const bool four = a.pairs % 4 == 0 && vec_floats(a.cos) && vec_floats(a.sin);
   const unsigned grid = static_cast<unsigned>(ceil_div(a.n, kTableRows));
-  if (four)
-    table_kernel<4><<<grid, 256, 0, stream>>>(p);
-  else
-    table_kernel<1><<<grid, 256, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_after(four ? table_kernel<4> : table_kernel<1>, dim3(grid), 256, 0, a.pdl, stream,
+                      p);
 }
 
 cudaError_t launch_rope(const RopeArgs &a, cudaStream_t stream) {
