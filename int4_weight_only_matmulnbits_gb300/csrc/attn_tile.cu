@@ -55,6 +55,9 @@ constexpr int kPieces = 8;                 // pieces of units that are known ahe
 constexpr int kTmemCols = 512;
 constexpr int kHeader = 8;                 // ints
 constexpr float kGrow = 8.f;               // rescale from 2^8 on
+// A unit counts for as many blocks more than it has: its masked block, results
+// and first scores stand for some 6000 cycles, a block in full swing for 2650.
+constexpr int kUnitCost = 2;
 
 template <int D>
 struct Cfg {
@@ -313,7 +316,8 @@ __global__ void __launch_bounds__(kPlanThreads)
   base = min(base, p.most);
   int64_t at = 0;
   for (int64_t u0 = 0; u0 < base; u0 += kPlanThreads) {
-    const int64_t mine = u0 + tid < base ? p.units[2 * (u0 + tid) + 1].y : 0;
+    const int64_t mine =
+        u0 + tid < base ? p.units[2 * (u0 + tid) + 1].y + int64_t(kUnitCost) : 0;
     const int64_t upto = block_scan<int64_t>(mine, sums, tid);
     if (u0 + tid < base) p.first[u0 + tid] = at + upto - mine;
     at += sums[31];
@@ -327,10 +331,11 @@ __global__ void __launch_bounds__(kPlanThreads)
 }
 
 // A CTA's part of the line, piece by piece; the unit after the present one is
-// loaded ahead.
+// loaded ahead. A unit's own cost stands before its blocks: block k is at
+// kUnitCost + k, and who has that place has the block.
 struct Walk {
   const AttnTileParams &p;
-  int64_t x, x1, total;
+  int64_t at, x1, total;  // at: the unit's place in the line
   int parts, n_units, unit, head, k0, k1;
   Unit u, after;
   __device__ __forceinline__ explicit Walk(const AttnTileParams &p_) : p(p_) {}
@@ -338,9 +343,13 @@ struct Walk {
     const int4 a = p.units[2 * i], b = p.units[2 * i + 1];
     return Unit{a.x, a.y, a.z, a.w, b.x, b.y, b.z};
   }
+  // Blocks of the unit at `from` that lie before place x.
+  __device__ __forceinline__ int before(int64_t x, int64_t from, const Unit &v) const {
+    return static_cast<int>(max(int64_t(0), min(int64_t(v.blocks), x - from - kUnitCost)));
+  }
   __device__ __forceinline__ void enter() {
-    k1 = static_cast<int>(min(int64_t(u.blocks), x1 - x + k0));
-    if (more()) after = load(unit + 1 == n_units ? 0 : unit + 1);
+    k1 = before(x1, at, u);
+    if (at + u.blocks + kUnitCost < x1) after = load(unit + 1 == n_units ? 0 : unit + 1);
   }
   // Whole warps; false: nothing for this CTA.
   __device__ __forceinline__ bool start(int lane) {
@@ -349,10 +358,10 @@ struct Walk {
     total = per * p.kv_heads;
     parts = static_cast<int>(min(int64_t(gridDim.x), total));
     if (static_cast<int>(blockIdx.x) >= parts) return false;
-    x = blockIdx.x * total / parts;
+    const int64_t x0 = blockIdx.x * total / parts;
     x1 = (blockIdx.x + 1) * total / parts;
-    head = static_cast<int>(x / per);
-    const int64_t in = x - head * per;
+    head = static_cast<int>(x0 / per);
+    const int64_t in = x0 - head * per;
     int lo = 0, hi = n_units;
     while (hi - lo > 1) {
       const int step = (hi - lo + 31) / 32, i = lo + (lane + 1) * step;
@@ -361,23 +370,36 @@ struct Walk {
       hi = min(hi, lo + step);
     }
     unit = lo;
-    k0 = static_cast<int>(in - p.first[unit]);
+    at = head * per + p.first[unit];
     u = load(unit);
+    k0 = before(x0, at, u);
     enter();
-    return true;
+    return k0 < k1 || next();
   }
   // Another piece follows.
-  __device__ __forceinline__ bool more() const { return x + (k1 - k0) < x1; }
-  __device__ __forceinline__ int next_head() const { return unit + 1 == n_units ? head + 1 : head; }
+  __device__ __forceinline__ bool more() const {
+    return at + u.blocks + 2 * kUnitCost < x1;
+  }
   __device__ __forceinline__ bool next() {
     if (!more()) return false;
-    x += k1 - k0;
+    at += u.blocks + kUnitCost;
     k0 = 0;
-    head = next_head();
-    unit = unit + 1 == n_units ? 0 : unit + 1;
+    if (++unit == n_units) {
+      unit = 0;
+      ++head;
+    }
     u = after;
     enter();
     return true;
+  }
+  // The CTAs after this one that have a piece of the unit that ends this part.
+  __device__ __forceinline__ int others() const {
+    if (k0 > 0 || k1 == u.blocks) return 0;
+    const int64_t last = at + kUnitCost + u.blocks - 1;  // the last block's place
+    int64_t c = ((last + 1) * parts - 1) / total;
+    while (c * total / parts > last) --c;
+    while (c + 1 < parts && (c + 1) * total / parts <= last) ++c;
+    return static_cast<int>(c) - static_cast<int>(blockIdx.x);
   }
   // The unit has rows in its second tile.
   __device__ __forceinline__ bool two(const Unit &v) const {
@@ -576,14 +598,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // this one that have a piece of it. (After a wait that ran out the
         // results mean nothing.)
         int *header = p.headers + blockIdx.x * kHeader;
-        int more = 0;
-        if (any && w.k0 == 0 && w.k1 < w.u.blocks) {
-          const int64_t end = w.x1 + w.u.blocks - w.k1;
-          more = static_cast<int>((end * w.parts - 1) / w.total) - static_cast<int>(blockIdx.x);
-          while ((blockIdx.x + more) * w.total / w.parts >= end) --more;
-          while (int64_t(blockIdx.x) + more + 1 < w.parts &&
-                 (blockIdx.x + more + 1) * w.total / w.parts < end)
-            ++more;
+        const int more = any ? w.others() : 0;
+        if (more > 0) {
           header[1] = w.u.t0;
           header[2] = w.u.n;
           header[3] = w.head;
