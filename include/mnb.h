@@ -1009,8 +1009,8 @@ MNB_API mnb_status mnb_qk_norm_rope(const mnb_heads *q, const mnb_heads *k, int6
  * the cache that no new token has. Two tokens of one place (a page that two
  * sequences write): one of them, unspecified which, element by element.
  * Errors: as mnb_qk_norm_rope, and MNB_ERR_SHAPE for page_size not a positive
- * multiple of 16, pages, n or table_pages < 1, pages, n or table_pages *
- * page_size past 2^31 - 1, table_stride < table_pages, strides of the cache
+ * multiple of 16, pages, n or table_pages < 1, pages or n past 2^31 - 1,
+ * table_pages * page_size past 2^31 - 1025, table_stride < table_pages, strides of the cache
  * below head_dim; MNB_ERR_ALIAS also for a cache that overlaps an input or
  * whose keys and values start at one address.
  */
@@ -1035,9 +1035,10 @@ MNB_API mnb_status mnb_cache_append(const mnb_heads *q, const mnb_heads *k, cons
  * are rounded to bf16 (2^-8) for the product with the values, not for their
  * sum. fp32: products from three bf16 parts of each factor, within 2^-22 of
  * the terms' magnitudes (magnitudes above 3.38e38 count as infinite).
- * What a masked place holds does not matter, infinities and NaN included. An
- * infinity or NaN in a key or value that a row does attend makes the row
- * non-finite (not always as an exact sum would be), and no other.
+ * What a masked place holds does not matter, infinities and NaN included. In a
+ * key or value that a row does attend they reach that row's outputs (not always
+ * as an exact sum would have them; a score of -inf counts as a masked one), and
+ * no other row's.
  * Results are bitwise reproducible for the same arrays, T and GPU.
  * Errors: as mnb_cache_append, and MNB_ERR_SHAPE for q->heads not a multiple
  * of cache->heads, T * (q->heads / cache->heads) near 2^31, a scale that is not

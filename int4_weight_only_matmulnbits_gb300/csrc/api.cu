@@ -613,7 +613,7 @@ mnb_status check_cache(const mnb_kv_cache &c) {
 mnb_status check_batch(const mnb_kv_batch &b, const mnb_kv_cache &c) {
   if (!b.starts || !b.lengths || !b.table) return MNB_ERR_NULL;
   if (b.n < 1 || b.n > kMaxDim - 1 || b.table_pages < 1 ||
-      b.table_pages > kMaxDim / c.page_size || b.table_stride < b.table_pages ||
+      b.table_pages > kMaxPositions / c.page_size || b.table_stride < b.table_pages ||
       b.table_stride > (int64_t(1) << 40))
     return MNB_ERR_SHAPE;
   if (!aligned(b.starts, 4) || !aligned(b.lengths, 4) || !aligned(b.table, 4))

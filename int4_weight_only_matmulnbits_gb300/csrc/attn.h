@@ -127,19 +127,25 @@ struct Share {
 
 // One sequence of a batch as the attention kernels take it: rows t0 .. t0 + n
 // of the queries, whose row i stands at position len - n + i; keys from lo on
-// (a multiple of 16) are attended by some row.
+// (a multiple of 16) are attended by some row, of those that the table holds.
 struct Seq {
   int t0, n, len, lo;
 };
+constexpr int kMaxPositions = 2147483647 - 1024;  // block ends stay within an int
+// A window as the kernels take it (0: none): none reaches further than positions.
+inline int window_of(int64_t window) {
+  return window < kMaxPositions ? static_cast<int>(window) : 0;
+}
 // What the device arrays say, brought within the buffers whatever they hold.
-__device__ __forceinline__ Seq load_seq(const BatchView &b, int i, int T, int cap, int window) {
+__device__ __forceinline__ Seq load_seq(const BatchView &b, int i, int T, int window) {
   Seq s;
   const int a = b.starts[i], z = b.starts[i + 1], len = b.lengths[i];
   s.t0 = min(max(a, 0), T);
   s.n = max(min(z, T) - s.t0, 0);
-  s.len = min(max(len, 0), cap);
+  s.len = min(max(len, 0), kMaxPositions);
   s.lo = 0;
-  if (window > 0) s.lo = max(0, s.len - s.n + 1 - window) & ~15;
+  if (window > 0)
+    s.lo = static_cast<int>(max(int64_t(0), int64_t(s.len) - s.n + 1 - window)) & ~15;
   return s;
 }
 

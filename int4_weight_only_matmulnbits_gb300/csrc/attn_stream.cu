@@ -161,13 +161,13 @@ struct Line {
   const AttnStreamParams &p;
   int lane;
   __device__ __forceinline__ Seq seq(int i) const {
-    return load_seq(p.b, i, p.T, p.cap, p.window);
+    return load_seq(p.b, i, p.T, p.window);
   }
   __device__ __forceinline__ int tiles(const Seq &s) const {
     return (s.n * static_cast<int>(p.G.d) + C::rows - 1) / C::rows;
   }
-  static __device__ __forceinline__ int blocks(const Seq &s) {
-    return max(1, (s.len - s.lo + C::block - 1) / C::block);
+  __device__ __forceinline__ int blocks(const Seq &s) const {
+    return max(1, (min(s.len, p.cap) - s.lo + C::block - 1) / C::block);
   }
   __device__ __forceinline__ int64_t work(const Seq &s) const {
     return int64_t(tiles(s)) * p.kv_heads * blocks(s);
@@ -244,7 +244,7 @@ struct Line {
     u.len = s.len;
     u.lo = s.lo;
     u.blocks = blocks(s);
-    u.last = s.len - s.n + min(s.n - 1, p.G.div(u.tile * C::rows + C::rows - 1));
+    u.last = max(s.len - s.n + min(s.n - 1, p.G.div(u.tile * C::rows + C::rows - 1)), -1);
   }
   // The unit after u (there is one).
   __device__ __forceinline__ void next(Unit &u) const {
@@ -319,10 +319,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F32, ROWS>::per_sm)
   int page0 = 0, pages = -1;
   auto load_pages = [&](int k0) {
     page0 = k0;
-    const int j = fu.lo + (k0 + lane) * kBlockKeys + warp * kWarpKeys;
-    const int first = fu.len - fu.n + p.G.div(fu.tile * kRows);  // the first row's position
+    const int j = fu.lo + min(k0 + lane, fu.blocks) * kBlockKeys + warp * kWarpKeys;
+    // The position of the first row that has one.
+    const int first = max(fu.len - fu.n + p.G.div(fu.tile * kRows), 0);
     pages = -1;
-    if (k0 + lane < fu.blocks && j < fu.len && j <= fu.last &&
+    if (k0 + lane < fu.blocks && j < min(fu.len, p.cap) && j <= fu.last &&
         (p.window == 0 || j + kWarpKeys > first - p.window + 1)) {
       pages = p.b.table[fu.b * p.b.table_stride + p.page_size.div(j)];
       if (pages < 0 || pages >= p.pages) pages = -1;
@@ -339,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F32, ROWS>::per_sm)
       if (page >= 0) {
         held |= 1u << slot;
         const int j = fu.lo + fk * kBlockKeys + warp * kWarpKeys;
-        const int at = j - p.page_size.div(j) * p.page_size.d, left = fu.len - j;
+        const int at = j - p.page_size.div(j) * p.page_size.d, left = min(fu.len, p.cap) - j;
         const int piece = lane % kPieces, first = lane / kPieces;
         const E *k = static_cast<const E *>(p.k.p) + page * p.k.ps + fu.head * p.k.hs +
                      (at + first) * p.k.ts + piece * (16 / C::es);
@@ -1046,7 +1047,7 @@ cudaError_t launch_attn_stream(const AttnArgs &a, cudaStream_t stream) {
   p.b = a.b;
   p.T = static_cast<int>(a.T);
   p.cap = static_cast<int>(int64_t(a.b.table_pages) * a.c.page_size);
-  p.window = static_cast<int>(std::min<int64_t>(a.window, p.cap));
+  p.window = window_of(a.window);
   // Weights are powers of two, of (score - maximum) * |scale| log2(e).
   // (Kept off 0 and infinity: what a masked score, -inf, is multiplied by.)
   p.scale = static_cast<float>(

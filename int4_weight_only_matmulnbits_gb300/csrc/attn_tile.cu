@@ -295,18 +295,19 @@ __global__ void __launch_bounds__(kPlanThreads)
   int64_t base = 0;
   for (int b0 = 0; b0 < p.b.n; b0 += kPlanThreads) {
     int mine = 0;
-    if (b0 + tid < p.b.n) mine = units_of(load_seq(p.b, b0 + tid, p.T, p.cap, p.window), p.G);
+    if (b0 + tid < p.b.n) mine = units_of(load_seq(p.b, b0 + tid, p.T, p.window), p.G);
     const int64_t upto = block_scan<int64_t>(mine, sums, tid);
     offset[tid] = base + upto - mine;
     base += sums[31];
     __syncthreads();
     for (int i = warp; i < min(kPlanThreads, p.b.n - b0); i += 32) {
-      const Seq s = load_seq(p.b, b0 + i, p.T, p.cap, p.window);
+      const Seq s = load_seq(p.b, b0 + i, p.T, p.window);
       const int64_t n = min(int64_t(units_of(s, p.G)), p.most - offset[i]);
       for (int t = lane; t < n; t += 32) {
         Unit u{s.t0, s.n, s.len, t, 0, 0, b0 + i};
-        if (p.window > 0) u.block0 = max(0, first_pos(u, p.G) - p.window + 1) / kTile;
-        u.blocks = max(1, (last_pos(u, p.G) + kTile) / kTile - u.block0);
+        if (p.window > 0)
+          u.block0 = min(max(0, max(0, first_pos(u, p.G)) - p.window + 1), p.cap) / kTile;
+        u.blocks = max(1, (min(last_pos(u, p.G), p.cap - 1) + kTile) / kTile - u.block0);
         p.units[2 * (offset[i] + t)] = make_int4(u.t0, u.n, u.len, u.tile);
         p.units[2 * (offset[i] + t) + 1] = make_int4(u.block0, u.blocks, u.b, 0);
       }
@@ -517,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ++listing;
         const int bottom = first_pos(w.u, p.G);
-        const int last = last_pos(w.u, p.G), end = min(w.u.len, p.cap);
+        const int last = max(last_pos(w.u, p.G), -1), end = min(w.u.len, p.cap);
         // Lane g < 8: the page of the keys 16 g on of the next block.
         auto page_of = [&](int kb) {
           const int j = (w.u.block0 + kb) * kTile + (lane & 7) * 16;
@@ -791,7 +792,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const int at = pc.tile * kUnit + row, tok = at / p.G;
         const bool live = at < pc.n * p.G;
-        const int pos = live ? pc.len - pc.n + tok : -1;
+        const int pos = live ? max(pc.len - pc.n + tok, -1) : -1;
         if (!p.q_tma) load_q(pc, at, tok);
         float m = -INFINITY, mc = 0.f, l = 0.f;  // maximum (of scores), times the scale; sum
         for (int kb = pc.k0; kb < pc.k1 && ok; ++kb, ++blocks, ++mine) {
@@ -1173,7 +1174,7 @@ cudaError_t launch_attn_tile(const AttnArgs &a, cudaStream_t stream) {
   p.G = a.q.n / a.c.heads;
   p.T = static_cast<int>(a.T);
   p.cap = static_cast<int>(int64_t(a.b.table_pages) * a.c.page_size);
-  p.window = static_cast<int>(std::min<int64_t>(a.window, p.cap));
+  p.window = window_of(a.window);
   p.scale = static_cast<float>(
       std::min(std::max(std::fabs(static_cast<double>(a.scale)) * M_LOG2E, 1e-37), 3e38));
   p.negative = a.scale < 0.f;

@@ -476,11 +476,48 @@ def test_lengths_past_the_table(dev):
     starts, table, pages, T = make_batch(g, [2, 1], [64, 64], 16)
     cache = make_cache(g, pages, 2, 16, 64, BF16)
     q = rows(g, T, 2, 64, BF16)
-    y = mnb.mnb_paged_attention(q, cache, on_gpu(starts, [64, 2 ** 31 - 1], table))
-    want, bound = ref.attend(q.cpu()[:2], cache.k.cpu(), cache.v.cpu(), [0, 2], [64], table[:1],
-                             64 ** -0.5)
-    within(y[:2], want, bound)
-    assert torch.isfinite(y.float()).all()
+    for long in (2 ** 31 - 1, 70, 65):
+        y = mnb.mnb_paged_attention(q, cache, on_gpu(starts, [64, long], table))
+        want, bound = ref.attend(q.cpu(), cache.k.cpu(), cache.v.cpu(), starts, [64, long], table,
+                                 64 ** -0.5)
+        within(y, want, bound)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n,window", [(5, 0), (5, 20), (5, 1000), (90, 0), (90, 30), (90, 300)])
+def test_positions_past_the_table(dev, n, window, dtype):
+    """Rows whose own positions lie past the table's pages attend the keys that it does hold, as
+    far as their windows reach them."""
+    g = torch.Generator().manual_seed(31)
+    lens = [150, 2 ** 30, 128 + n // 2]
+    _, table, pages, T = make_batch(g, [n] * 3, [128] * 3, 16)
+    cache = make_cache(g, pages, 2, 16, 64, dtype)
+    q, starts = rows(g, T, 4, 64, dtype), [0, n, 2 * n, 3 * n]
+    y = mnb.mnb_paged_attention(q, cache, on_gpu(starts, lens, table), window=window)
+    want, bound = ref.attend(q.cpu(), cache.k.cpu(), cache.v.cpu(), starts, lens, table, 64 ** -0.5,
+                             window)
+    within(y, want, bound)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("window", [2 ** 30, 2 ** 31 - 1026, 2 ** 31 - 1, 2 ** 31, 2 ** 63 - 1])
+def test_windows_past_every_position(dev, window, dtype):
+    """The largest windows, with rows that stand before the first position (they attend nothing)."""
+    g = torch.Generator().manual_seed(33)
+    for news, lens in ([3, 1, 90], [1, 50, 60]), ([2000], [7]):
+        attend(g, news, lens, 4, 2, 64, 16, dtype, window=window)
+
+
+def test_tables_that_are_slices_of_wider_ones(dev):
+    g = torch.Generator().manual_seed(32)
+    starts, table, pages, T = make_batch(g, [1, 70], [90, 100], 16, width=9)
+    cache = make_cache(g, pages, 2, 16, 64, BF16)
+    q, batch = rows(g, T, 4, 64, BF16), on_gpu(starts, [90, 100], table)
+    wide = torch.full((2, 40), -1, dtype=torch.int32, device=dev)
+    wide[:, 3:12] = batch.table
+    part = mnb.KvBatch(batch.starts, batch.lengths, wide[:, 3:12])
+    assert torch.equal(mnb.mnb_paged_attention(q, cache, batch),
+                       mnb.mnb_paged_attention(q, cache, part))
 
 
 @pytest.mark.parametrize("n", [1, 80])
