@@ -551,13 +551,17 @@ __global__ void __launch_bounds__(kThreads, 1)
               f.scan = masked ? scans : -1;
               f.bad[0] = f.bad[1] = f.bad[2] = f.bad[3] = 0;
               mbar_arrive(known + blocks % kInfo);
-              if (masked) {
-                // (As many masked blocks are never in flight.)
+            }
+            if (v == 1 && masked) {
+              // Not before this stage is free: until then its barrier may be a phase
+              // behind, and the parity that the values are waited for by taken for the
+              // one before it. (As many masked blocks are never in flight.)
+              if (lane == 0) {
                 todo[scans % kInfo] = blocks;
                 mbar_arrive(toscan + scans % kInfo);
               }
+              ++scans;
             }
-            if (v == 0 && masked) ++scans;
             if (lane == 0) mbar_arrive_expect_tx(full + s, C::tile);
             __syncwarp();
             if (copies)

@@ -499,6 +499,20 @@ def test_positions_past_the_table(dev, n, window, dtype):
     within(y, want, bound)
 
 
+@pytest.mark.parametrize("hq,D", [(16, 128), (24, 128), (8, 64)])
+def test_what_shared_memory_held_before(dev, hq, D):
+    """Masked blocks that are a CTA's first, after a kernel that leaves NaN all over the SMs."""
+    g = torch.Generator().manual_seed(34)
+    news, lens = [7, 708, 9, 5, 1, 2, 1, 0, 57], [7, 908, 4312, 2428, 11, 2, 10, 90, 57]
+    starts, table, pages, T = make_batch(g, news, lens, 64)
+    cache = make_cache(g, pages, 8, 64, D, BF16)
+    q, batch = rows(g, T, hq, D, BF16), on_gpu(starts, lens, table)
+    want, bound = ref.attend(q.cpu(), cache.k.cpu(), cache.v.cpu(), starts, lens, table, D ** -0.5)
+    for _ in range(6):
+        torch.full((1 << 26,), math.nan, device=dev)
+        within(mnb.mnb_paged_attention(q, cache, batch), want, bound)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("window", [2 ** 30, 2 ** 31 - 1026, 2 ** 31 - 1, 2 ** 31, 2 ** 63 - 1])
 def test_windows_past_every_position(dev, window, dtype):
