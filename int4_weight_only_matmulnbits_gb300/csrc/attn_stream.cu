@@ -9,7 +9,8 @@
 // Rows of a sequence are (token, head of the key head's group), numbered token
 // first; 16 of them, padded, are the rows of the MMAs, so that a key head's
 // keys are read once for its whole group. The keys are cut into blocks of 64,
-// and all blocks of all (sequence, key head, 16 rows) are shared out evenly in
+// and all blocks of all (sequence, key head, 16 rows), of those keys that a window
+// reaches from the rows, are shared out evenly in
 // one long line: block c of the grid takes the part c of it, wherever that
 // begins and ends. So the split follows the lengths that the device arrays
 // hold at that moment (a captured graph's too), whatever they are. Pieces of a
@@ -22,7 +23,7 @@
 // Few units (a single sequence's decode step): a cluster of 8 or 16 blocks takes
 // a unit, an equal share of its keys each, and joins the sums through
 // distributed shared memory: one launch instead of two. Decoding one sequence
-// of 4097 tokens (8 key heads of 128, bf16) takes 8.4 us this way and 12.7 with
+// of 4097 tokens (8 key heads of 128, bf16) takes 9.0 us this way and 12.7 with
 // the line and its joining kernel.
 #include <cuda_bf16.h>
 
@@ -40,7 +41,7 @@ namespace mnb {
 namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
-constexpr int kMinBlocks = 1;     // of the line per block of the grid
+constexpr int kSplit = 12;        // a block of the grid has sqrt(unit / kSplit) blocks at least
 constexpr int kHeader = 8;        // ints of a piece's header
 constexpr int kMaxCluster = 16;   // blocks of a cluster
 
@@ -166,19 +167,27 @@ struct Line {
   __device__ __forceinline__ int tiles(const Seq &s) const {
     return (s.n * static_cast<int>(p.G.d) + C::rows - 1) / C::rows;
   }
+  // Of each unit: those of the sequence, or those that a window spans.
   __device__ __forceinline__ int blocks(const Seq &s) const {
-    return max(1, (min(s.len, p.cap) - s.lo + C::block - 1) / C::block);
+    const int all = max(1, (min(s.len, p.cap) - s.lo + C::block - 1) / C::block);
+    return min(all, p.span);
   }
   __device__ __forceinline__ int64_t work(const Seq &s) const {
     return int64_t(tiles(s)) * p.kv_heads * blocks(s);
   }
-  // All blocks of the line; every lane takes part, and keeps one of the first 32
-  // sequences in s0.
-  __device__ __forceinline__ int64_t total(Seq &s0) const {
+  // All blocks of the line, and of the longest unit; every lane takes part, and
+  // keeps one of the first 32 sequences in s0.
+  __device__ __forceinline__ int64_t total(Seq &s0, int &longest) const {
     s0 = Seq{0, 0, 0, 0};
     if (lane < p.b.n) s0 = seq(lane);
     int64_t w = work(s0);
-    for (int i = lane + 32; i < p.b.n; i += 32) w += work(seq(i));
+    longest = s0.n > 0 ? blocks(s0) : 0;
+    for (int i = lane + 32; i < p.b.n; i += 32) {
+      const Seq s = seq(i);
+      w += work(s);
+      if (s.n > 0) longest = max(longest, blocks(s));
+    }
+    longest = __reduce_max_sync(0xffffffffu, longest);
 #pragma unroll
     for (int m = 1; m < 32; m *= 2) w += __shfl_xor_sync(0xffffffffu, w, m);
     return w;
@@ -209,7 +218,7 @@ struct Line {
         const int nb = blocks(s);
         const int unit = static_cast<int>(Share::div(in, nb));
         kb = static_cast<int>(in - int64_t(unit) * nb);
-        enter(u, s, unit);
+        enter(u, s, unit, nb);
         return;
       }
       before += __shfl_sync(0xffffffffu, up, 31);
@@ -232,29 +241,32 @@ struct Line {
     s = Seq{__shfl_sync(0xffffffffu, s.t0, l), __shfl_sync(0xffffffffu, s.n, l),
             __shfl_sync(0xffffffffu, s.len, l), __shfl_sync(0xffffffffu, s.lo, l)};
     u.b = l;
-    enter(u, s, unit - __shfl_sync(0xffffffffu, up - w, l));
+    enter(u, s, unit - __shfl_sync(0xffffffffu, up - w, l), blocks(s));
     return true;
   }
-  __device__ __forceinline__ void enter(Unit &u, const Seq &s, int unit) const {
+  __device__ __forceinline__ void enter(Unit &u, const Seq &s, int unit, int nb) const {
     const int nt = tiles(s);
     u.head = nt == 1 ? unit : unit / nt;
     u.tile = unit - u.head * nt;
     u.t0 = s.t0;
     u.n = s.n;
     u.len = s.len;
-    u.lo = s.lo;
-    u.blocks = blocks(s);
+    u.blocks = nb;
+    u.lo = 0;
+    if (p.window > 0)
+      u.lo = max(0, max(0, s.len - s.n + p.G.div(u.tile * C::rows)) - p.window + 1) & ~15;
     u.last = max(s.len - s.n + min(s.n - 1, p.G.div(u.tile * C::rows + C::rows - 1)), -1);
   }
   // The unit after u (there is one).
   __device__ __forceinline__ void next(Unit &u) const {
-    Seq s{u.t0, u.n, u.len, u.lo};
-    int unit = u.head * tiles(s) + u.tile + 1;
+    Seq s{u.t0, u.n, u.len, 0};
+    int unit = u.head * tiles(s) + u.tile + 1, nb = u.blocks;
     while (unit >= tiles(s) * p.kv_heads) {
       unit = 0;
       s = seq(++u.b);
+      nb = blocks(s);
     }
-    enter(u, s, unit);
+    enter(u, s, unit, nb);
   }
 };
 
@@ -296,15 +308,20 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F32, ROWS>::per_sm)
     x1 = share.first(rank + 1);
   } else {
     Seq s0;
-    total = line.total(s0);
-    // As many blocks of the grid as have kMinBlocks of the line.
+    int longest;
+    total = line.total(s0, longest);
+    // Of a long unit the pieces take as long to join as to make when a block of the
+    // grid has sqrt(unit / kSplit) blocks of the line (16 rows over 16000 keys: 16 us,
+    // 30 with a block each, joined by one block; over 2000 9 either way).
+    const int least = max(1, static_cast<int>(sqrtf(longest * (1.f / kSplit)) + 0.5f));
     const int parts =
-        static_cast<int>(min(int64_t(gridDim.x), (total + kMinBlocks - 1) / kMinBlocks));
+        static_cast<int>(min(int64_t(gridDim.x), (total + least - 1) / least));
     header = p.headers + blockIdx.x * kHeader;
     if (static_cast<int>(blockIdx.x) >= parts) {
       if (threadIdx.x == 0) header[0] = 0;
       return;
     }
+    if (threadIdx.x == 0) header[5] = parts;  // for this thread, at the end
     const Share share(total, parts);
     x0 = share.first(blockIdx.x);
     x1 = share.first(blockIdx.x + 1);
@@ -872,10 +889,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F32, ROWS>::per_sm)
       if (threadIdx.x == 0) {
         int more = 0;
         if (begins && !whole) {
-          const int parts =
-              static_cast<int>(min(int64_t(gridDim.x), (total + kMinBlocks - 1) / kMinBlocks));
           const int64_t end = x1 + u.blocks - kb;  // first block of the line past the unit
-          more = Share(total, parts).owner(end - 1) - static_cast<int>(blockIdx.x);
+          more = Share(total, header[5]).owner(end - 1) - static_cast<int>(blockIdx.x);
         }
         header[0] = more;
         header[1] = u.t0;
@@ -894,12 +909,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F32, ROWS>::per_sm)
 }
 
 // Joins the pieces of a unit: the one that begins at the end of block c's part
-// and the continuations at the start of the parts after it. A thread per
-// column of a row, the loads of 32 pieces in flight together, lane c with the
+// and the continuations at the start of the parts after it. Four rows a block
+// (a lone unit's pieces are too many for one SM to read: 33 us for 400 of 16 rows,
+// 17 so, with fewer pieces), a thread per column of a row, the loads of 32 pieces in flight together, lane c with the
 // maximum and the sum of weights of piece c. Bound by latency (a launch, the
 // header, the pieces: each the best part of a microsecond), so the code is kept
 // short as well: fetching it is part of that.
-constexpr int kJoinThreads = 512;
+constexpr int kJoinThreads = 512, kJoinBlocks = 4;
 template <int D, bool F32, int ROWS>
 __global__ void __launch_bounds__(kJoinThreads)
     combine_kernel(const __grid_constant__ AttnStreamParams p) {
@@ -917,7 +933,8 @@ __global__ void __launch_bounds__(kJoinThreads)
   const float *parts = p.parts + int64_t(blockIdx.x) * 2 * kPart;
   auto piece = [&](int c) { return parts + (c == 0 ? kPart : c * 2 * kPart); };
 #pragma unroll 1
-  for (int row = threadIdx.x / D; row < kRows; row += kJoinThreads / D) {
+  for (int row = blockIdx.y * (kJoinThreads / D) + threadIdx.x / D; row < kRows;
+       row += gridDim.y * (kJoinThreads / D)) {
     const int i = tile * kRows + row, tok = p.G.div(i);
     if (tok >= n) return;
     float m = -INFINITY, l = 0.f, a = 0.f;
@@ -975,9 +992,14 @@ int clusters_at_once(Kernel kernel, const cudaLaunchConfig_t &cfg, std::atomic<i
 }
 
 template <int D, bool F32, int ROWS>
-cudaError_t run(const AttnStreamParams &p, bool pdl, cudaStream_t stream) {
+cudaError_t run(AttnStreamParams p, bool pdl, cudaStream_t stream) {
   using C = Cfg<D, F32, ROWS>;
   constexpr int kRows = ROWS;
+  p.span = kMaxPositions;
+  // From a multiple of 16 at or below the first row's window to the last row.
+  if (p.window > 0)
+    p.span = static_cast<int>(
+        (int64_t(p.window) + (kRows - 1) / p.G.d + 1 + 15 + C::block - 1) / C::block);
   // The most units that T rows of n sequences make.
   const int64_t few = std::min<int64_t>(p.b.n, p.T);
   const int64_t units =
@@ -987,7 +1009,7 @@ cudaError_t run(const AttnStreamParams &p, bool pdl, cudaStream_t stream) {
     // units' blocks, some 45 GB/s each, where the line reads at 6500. The line
     // takes 4.3 us more of launch and joining. (The table's width stands for the
     // lengths, which the host does not know.)
-    const double bytes = 2.0 * p.cap * p.kv_heads * C::row;
+    const double bytes = 2.0 * std::min<double>(p.cap, double(p.span) * C::block) * p.kv_heads * C::row;
     const double rate = std::min(6500.0, 45.0 * p.kv_heads * size);
     if (bytes * 1e-3 * (1 / rate - 1 / 6500.0) > 4.3) continue;
     auto *kernel = stream_kernel<D, F32, ROWS, true>;
@@ -1022,7 +1044,8 @@ cudaError_t run(const AttnStreamParams &p, bool pdl, cudaStream_t stream) {
   const int grid = grid_blocks(C::per_sm);
   e = launch_after(kernel, dim3(grid), kThreads, C::smem, pdl, stream, p);
   if (e != cudaSuccess) return e;
-  return launch_after(combine_kernel<D, F32, ROWS>, dim3(grid), kJoinThreads, 0, pdl, stream, p);
+  return launch_after(combine_kernel<D, F32, ROWS>, dim3(grid, kJoinBlocks), kJoinThreads, 0, pdl,
+                      stream, p);
 }
 
 size_t header_bytes(int grid) { return (size_t(grid) * kHeader * 4 + 255) & ~size_t(255); }

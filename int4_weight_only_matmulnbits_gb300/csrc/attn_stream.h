@@ -13,6 +13,7 @@ struct AttnStreamParams {
   FastDiv page_size, G;               // G: query heads per key head
   int T, cap;                         // cap: tokens that a row of the table holds
   int window;                         // 0: none
+  int span;                           // blocks of keys that the rows of a unit reach in a window
   float scale;                        // |scale| of the scores, times log2(e)
   int negative;                       // the scale is: scores change their sign
   int cluster;                        // blocks of a cluster (one unit each), where they are used

@@ -315,10 +315,15 @@ __global__ void __launch_bounds__(kPlanThreads)
     __syncthreads();
   }
   base = min(base, p.most);
+  __shared__ int longest;  // unit's blocks
+  if (tid == 0) longest = 0;
+  __syncthreads();
   int64_t at = 0;
   for (int64_t u0 = 0; u0 < base; u0 += kPlanThreads) {
-    const int64_t mine =
-        u0 + tid < base ? p.units[2 * (u0 + tid) + 1].y + int64_t(kUnitCost) : 0;
+    const int blocks = u0 + tid < base ? p.units[2 * (u0 + tid) + 1].y : 0;
+    const int64_t mine = u0 + tid < base ? blocks + int64_t(kUnitCost) : 0;
+    const int most = __reduce_max_sync(0xffffffffu, blocks);
+    if (lane == 0) atomicMax(&longest, most);
     const int64_t upto = block_scan<int64_t>(mine, sums, tid);
     if (u0 + tid < base) p.first[u0 + tid] = at + upto - mine;
     at += sums[31];
@@ -328,8 +333,11 @@ __global__ void __launch_bounds__(kPlanThreads)
     p.first[base] = at;
     p.line[0] = at;
     p.line[1] = base;
+    p.line[2] = longest;
   }
 }
+
+constexpr int kSplit = 3;  // a CTA has sqrt(longest unit / kSplit) places at least
 
 // A CTA's part of the line, piece by piece; the unit after the present one is
 // loaded ahead. A unit's own cost stands before its blocks: block k is at
@@ -357,7 +365,12 @@ struct Walk {
     const int64_t per = p.line[0];
     n_units = static_cast<int>(p.line[1]);
     total = per * p.kv_heads;
-    parts = static_cast<int>(min(int64_t(gridDim.x), total));
+    // Of a long unit the pieces take as long to join as to make when a CTA has
+    // sqrt(unit / kSplit) blocks (128 rows over 16000 keys: 30 us, 69 with a place of
+    // the line each; over 2000 18 and 20).
+    const int least =
+        max(1, static_cast<int>(sqrtf(static_cast<float>(p.line[2]) / kSplit) + 0.5f));
+    parts = static_cast<int>(min(int64_t(gridDim.x), (total + least - 1) / least));
     if (static_cast<int>(blockIdx.x) >= parts) return false;
     const int64_t x0 = blockIdx.x * total / parts;
     x1 = (blockIdx.x + 1) * total / parts;
@@ -1021,6 +1034,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ At
   // (Rows of a second tile that the unit does not have hold anything.)
   const bool live = tile * kUnit + row < n * p.G;
   float m = -INFINITY;
+#pragma unroll 8
   for (int c = warp; c <= more; c += 8)
     if (live) m = fmaxf(m, piece(c)[kUnit * D + row]);
   top[warp][lane] = m;
@@ -1035,6 +1049,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ At
   for (int c0 = 0; c0 <= more; c0 += kMany) {
     const int cn = min(kMany, more + 1 - c0);
     __syncthreads();
+#pragma unroll 8
     for (int c = warp; c < cn; c += 8)
       fac[c][lane] = live ? exp2_fast((piece(c0 + c)[kUnit * D + row] - z) * p.scale) : 0.f;
     __syncthreads();
@@ -1099,7 +1114,7 @@ Space space(unsigned char *ws, const AttnArgs &a) {
     at += align256(n);
     return p;
   };
-  s.line = reinterpret_cast<int64_t *>(take(16));
+  s.line = reinterpret_cast<int64_t *>(take(24));
   s.headers = reinterpret_cast<int *>(take(ctas * kHeader * 4));
   s.first = reinterpret_cast<int64_t *>(take(size_t(most + 1) * 8));
   s.units = reinterpret_cast<int4 *>(take(size_t(most) * 32));
@@ -1131,13 +1146,15 @@ bool tile_path(const AttnArgs &a) {
   for (int64_t s : {a.c.k.ps, a.c.k.hs, a.c.k.ts, a.c.v.ps, a.c.v.hs, a.c.v.ts})
     if (s * 2 >= int64_t(1) << 40) return false;
   // The streaming kernel reads a sequence's keys for every 16 rows, this one for
-  // every 256, at some 12 us more for its plan and its joins. Measured with 4
-  // query heads per key head, 8 of those (us, streaming / this): one sequence of
-  // 2000 tokens, 64 rows 11 / 23, 128 rows 24 / 25; of 16000, 48 rows 36 / 38,
-  // 64 rows 44 / 38; 16 sequences of 2000, 16 rows each 38 / 43, 20 rows 45 / 44;
-  // of 16000, 16 rows 172 / 217, 20 rows 319 / 218.
+  // every 256, at some 12 us more for its plan and its joins: enough rows a
+  // sequence, and enough of all heads, are what that takes. Measured with 4 query
+  // heads per key head (us, streaming / this): one sequence of 2000 tokens, 512
+  // rows of all heads 10 / 21, 1024 rows 20 / 22 (19 with 8 key heads); of 16000,
+  // 256 rows 25 / 31, 512 rows 36 / 34; 16 sequences of 2000, 16 rows each of 8
+  // key heads 38 / 43, 20 rows 45 / 44; of 16000, 16 rows 172 / 217, 20 rows 319 /
+  // 218; 16 of 16000, 32 rows each of one key head 39 / 42, of two 80 / 60.
   const int64_t G = a.q.n / a.c.heads;
-  return a.T * G > std::max<int64_t>(64, 16 * std::min<int64_t>(a.b.n, a.T));
+  return a.T * G > 16 * std::min<int64_t>(a.b.n, a.T) && a.T * a.q.n > 512;
 }
 
 size_t tile_workspace_bytes(const AttnArgs &a) { return space(nullptr, a).bytes; }

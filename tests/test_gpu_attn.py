@@ -499,6 +499,15 @@ def test_positions_past_the_table(dev, n, window, dtype):
     within(y, want, bound)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("news,lens,hq,window", [([1], [9001], 4, 0), ([16], [6007], 4, 0),
+                                                 ([7, 4, 2, 9], [135, 24, 9000, 700], 5, 0),
+                                                 ([150], [5003], 4, 0), ([150], [5003], 4, 900)])
+def test_lone_long_sequences_over_one_key_head(dev, news, lens, hq, window, dtype):
+    g = torch.Generator().manual_seed(35)
+    attend(g, news, lens, hq, 1, 128, 32, dtype, window=window)
+
+
 @pytest.mark.parametrize("hq,D", [(16, 128), (24, 128), (8, 64)])
 def test_what_shared_memory_held_before(dev, hq, D):
     """Masked blocks that are a CTA's first, after a kernel that leaves NaN all over the SMs."""
