@@ -136,6 +136,11 @@ constexpr int kMaxPositions = 2147483647 - 1024;  // block ends stay within an i
 inline int window_of(int64_t window) {
   return window < kMaxPositions ? static_cast<int>(window) : 0;
 }
+// The first key, rounded down to a multiple of 16, that some of the rows attends.
+__device__ __forceinline__ int first_key(int n, int len, int window) {
+  if (window == 0) return 0;
+  return static_cast<int>(max(int64_t(0), int64_t(len) - n + 1 - window)) & ~15;
+}
 // What the device arrays say, brought within the buffers whatever they hold.
 __device__ __forceinline__ Seq load_seq(const BatchView &b, int i, int T, int window) {
   Seq s;
@@ -143,9 +148,7 @@ __device__ __forceinline__ Seq load_seq(const BatchView &b, int i, int T, int wi
   s.t0 = min(max(a, 0), T);
   s.n = max(min(z, T) - s.t0, 0);
   s.len = min(max(len, 0), kMaxPositions);
-  s.lo = 0;
-  if (window > 0)
-    s.lo = static_cast<int>(max(int64_t(0), int64_t(s.len) - s.n + 1 - window)) & ~15;
+  s.lo = first_key(s.n, s.len, window);
   return s;
 }
 
