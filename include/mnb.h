@@ -928,7 +928,9 @@ typedef struct {
  * rows starts[b] .. starts[b + 1] of the call's T rows (starts does not
  * decrease; equal: nothing new), its last one at position lengths[b] - 1: a
  * length counts the new tokens. Position p is at place p % page_size of page
- * table[b * table_stride + p / page_size]. The kernels read the arrays when
+ * table[b * table_stride + p / page_size]. Starts may go on past T (a call of a
+ * step's first rows): rows keep the positions that they have in the whole step.
+ * Attention takes a length above 2^31 - 1025 as that. The kernels read the arrays when
  * they run, so a captured graph follows their contents; whatever they hold,
  * nothing outside the buffers is read or written: a page index outside
  * 0 .. pages - 1 names no page, positions past table_pages * page_size have

@@ -144,10 +144,13 @@ __device__ __forceinline__ int first_key(int n, int len, int window) {
 // What the device arrays say, brought within the buffers whatever they hold.
 __device__ __forceinline__ Seq load_seq(const BatchView &b, int i, int T, int window) {
   Seq s;
-  const int a = b.starts[i], z = b.starts[i + 1], len = b.lengths[i];
+  const int a = b.starts[i], z = b.starts[i + 1];
+  // The length up to the last row that is here: those past the call's T rows are
+  // not, and the ones before them keep their positions.
+  const int64_t len = b.lengths[i] - max(int64_t(z) - T, int64_t(0));
   s.t0 = min(max(a, 0), T);
   s.n = max(min(z, T) - s.t0, 0);
-  s.len = min(max(len, 0), kMaxPositions);
+  s.len = static_cast<int>(min(max(len, int64_t(0)), int64_t(kMaxPositions)));
   s.lo = first_key(s.n, s.len, window);
   return s;
 }

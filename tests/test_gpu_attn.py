@@ -715,3 +715,29 @@ def test_without_programmatic_launch(dev):
         attend(g, [1, 50], [100, 60], 4, 2, 64, 16, BF16)
     finally:
         mnb.mnb_set_programmatic_launch(True)
+
+
+# ---- calls that a plain step does not make -------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("window", [0, 20])
+@pytest.mark.parametrize("news,lens,T", [
+    ([1, 6], [40, 100], 4), ([3, 20, 9], [50, 21, 70], 5), ([2] * 40 + [7], [30] * 40 + [90], 83),
+    ([3, 200, 90], [50, 300, 700], 260), ([300], [1000], 150), ([150, 9, 100], [150, 60, 100], 152)])
+def test_the_first_rows_of_a_step(dev, news, lens, T, window, dtype):
+    """A call of the first T rows of a step whose starts go on past them: every row is placed as in
+    the whole step, by appending and by attention alike."""
+    g = torch.Generator().manual_seed(T + window)
+    hq, H, D, ps = 8, 2, 64, 16
+    starts, table, pages, whole = make_batch(g, news, lens, ps)
+    assert T < whole
+    q, k, v = (rows(g, whole, n, D, dtype) for n in (hq, H, H))
+    cache, batch = make_cache(g, pages, H, ps, D, dtype), on_gpu(starts, lens, table)
+    k0, v0 = cache.k.clone(), cache.v.clone()
+    y = mnb.mnb_paged_attention(q[:T], cache, batch, window=window)
+    want, bound = ref.attend(q.cpu(), k0.cpu(), v0.cpu(), starts, lens, table, D ** -0.5, window)
+    within(y, want[:T], bound[:T])
+    mnb.mnb_cache_append(None, k[:T], v[:T], cache, batch)
+    for t, _, page, at in ref.places(starts, lens, table, ps, pages, T):
+        k0[page, :, at], v0[page, :, at] = k[t], v[t]
+    assert torch.equal(cache.k, k0) and torch.equal(cache.v, v0)
