@@ -962,9 +962,10 @@ MNB_API mnb_status mnb_rope_frequencies(int rot_dim, double base, double factor,
 /*
  * Tables of cosines and sines of positions first .. first + n - 1:
  *   cos[r, i] = magnitude * cos((first + r) * frequencies[i]), sin likewise,
- * fp32 [n, rot_dim / 2]. frequencies: HOST, rot_dim / 2 doubles. The angle is
- * kept to 2^-53 of the frequency times the position whatever the position;
- * results are within 2^-22 of themselves.
+ * fp32 [n, rot_dim / 2]. frequencies: HOST, rot_dim / 2 doubles of either sign.
+ * The angle is kept to 2^-52 of itself and 2^-65 of a turn for each position,
+ * whatever the position (the latter is past 2^-22 of an angle for frequencies
+ * below 2^-40 alone); but for that, results are within 2^-22 of themselves.
  * Errors: MNB_ERR_NULL, MNB_ERR_SHAPE (rot_dim odd, < 2 or > 256; n < 1 or
  * first < 0, or first + n past 2^31 - 1; a frequency or the magnitude not
  * finite), MNB_ERR_ALIGN, MNB_ERR_ALIAS, MNB_ERR_DEVICE, MNB_ERR_CUDA.

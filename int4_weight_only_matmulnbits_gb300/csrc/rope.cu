@@ -26,9 +26,10 @@ namespace {
 // An angle p f is held in turns as a 64-bit fraction: p times the fraction of
 // f / 2 pi, modulo 2^64, is exact but for the rounding of f / 2 pi to 2^-64,
 // at any position, with one integer product. The nearest quarter turn is
-// taken off in integers too; the rest, at most pi / 4, keeps all of its 24
-// bits however near a zero of the cosine the angle lies, and goes through the
-// Taylor series of sine (to x^9) and cosine (to x^10), which end below 2^-28
+// taken off in integers too; the rest, at most pi / 4, is split at its nearest
+// multiple of 2^-32 turns, so that it keeps all of its 24 bits however near a
+// zero of the sine or cosine the angle lies, on either side, and goes through
+// the Taylor series of sine (to x^9) and cosine (to x^10), which end below 2^-28
 // there. Bound by the writes: 8 bytes for some 40 instructions.
 struct TableParams {
   uint64_t turns[kMaxPairs];
@@ -40,11 +41,12 @@ struct TableParams {
 
 __device__ __forceinline__ void table_entry(uint64_t turns, float mag, float mag_lo, float &c,
                                             float &s) {
-  const uint32_t top = static_cast<uint32_t>(turns >> 32) + (1u << 29);
+  // In 2^-32 turns, to the nearest, from an eighth of a turn below.
+  const uint32_t top = static_cast<uint32_t>((turns + 0x2000000080000000ull) >> 32);
   const uint32_t quarter = top >> 30;  // 0 .. 3 (4 as 0)
-  // The rest's high word, signed, and low word: 2^-64 turns.
+  // The rest's high part, and the signed low one: 2^-64 turns.
   const int32_t hi = static_cast<int32_t>((top & 0x3FFFFFFFu) - (1u << 29));
-  const float lo = static_cast<float>(static_cast<uint32_t>(turns));
+  const float lo = static_cast<float>(static_cast<int32_t>(turns));
   const float x = fmaf(static_cast<float>(hi), 0x1p32f, lo) * 0x1.921fb6p-62f;  // 2 pi 2^-64
   const float x2 = x * x;
   float p = fmaf(x2, 1.f / 362880.f, -1.f / 5040.f);
@@ -425,10 +427,11 @@ cudaError_t launch_rope_table(const RopeTableArgs &a, cudaStream_t stream) {
   TableParams p{};
   for (int i = 0; i < a.pairs; ++i) {
     // The fraction of a turn that a position adds, rounded to 2^-64 (a double
-    // keeps 53 bits of it).
-    double f = a.frequencies[i] * (0.5 / M_PI);
+    // keeps 53 bits of it), and its complement where it is negative.
+    double f = std::fabs(a.frequencies[i]) * (0.5 / M_PI);
     f -= std::floor(f);
-    p.turns[i] = f < 1.0 ? static_cast<uint64_t>(f * 0x1p64) : 0;  // (1 - 2^-60 may round to 1)
+    p.turns[i] = static_cast<uint64_t>(f * 0x1p64 + 0.5);
+    if (a.frequencies[i] < 0) p.turns[i] = 0 - p.turns[i];
   }
   p.pairs = a.pairs;
   p.first = a.first;

@@ -741,3 +741,18 @@ def test_the_first_rows_of_a_step(dev, news, lens, T, window, dtype):
     for t, _, page, at in ref.places(starts, lens, table, ps, pages, T):
         k0[page, :, at], v0[page, :, at] = k[t], v[t]
     assert torch.equal(cache.k, k0) and torch.equal(cache.v, v0)
+
+
+@pytest.mark.parametrize("f,n,first", [(-1e-11, 3000, 0), (-7e-11, 3000, 0), (1e-13, 3000, 0),
+                                       (-1e-13, 500, 2 ** 31 - 1000), (-1e-9, 500, 1 << 20),
+                                       (3e-17, 500, 2 ** 30), (-0.7, 2000, 0)])
+def test_tables_of_small_and_negative_frequencies(dev, f, n, first):
+    """Relative to themselves but for what the angle is off: 2^-52 of it (two products of doubles),
+    and 2^-65 of a turn for each position."""
+    t = mnb.mnb_rope_table(torch.tensor([f], dtype=torch.float64), n, first=first, device=dev)
+    p = torch.arange(first, first + n, dtype=torch.float64)[:, None]
+    a = p * f
+    slack = 2.0 ** -52 * a.abs() + p * (2 * math.pi * 2.0 ** -65)
+    slack += 2.0 ** -53 * a.abs()  # the reference's product
+    within(t.cos, torch.cos(a), 2.0 ** -22 * torch.cos(a).abs() + slack + 1e-45)
+    within(t.sin, torch.sin(a), 2.0 ** -22 * torch.sin(a).abs() + slack + 1e-45)
