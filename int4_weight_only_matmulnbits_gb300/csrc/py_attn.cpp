@@ -7,6 +7,9 @@
 // Every function works on the current device and its current stream, and
 // returns NotImplemented for tensors of another device; the Python functions
 // around them (binding.py) then change over, and hold the documentation.
+// Arguments are read with the interpreter held; allocations and launches, which
+// may wait for the GPU or the driver, run without it, so that the process's other
+// Python threads go on.
 #define PY_SSIZE_T_CLEAN
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -38,6 +41,14 @@ struct Ref {  // an owned reference
   }
 };
 
+struct Released {  // the interpreter, for the scope's length
+  PyThreadState *state = PyEval_SaveThread();
+  Released() = default;
+  Released(const Released &) = delete;
+  Released &operator=(const Released &) = delete;
+  ~Released() { PyEval_RestoreThread(state); }
+};
+
 bool refuse(const char *format, ...) {
   va_list ap;
   va_start(ap, format);
@@ -47,6 +58,7 @@ bool refuse(const char *format, ...) {
 }
 
 struct Tensor {
+  at::Tensor keep;  // the memory stays while the interpreter is released
   uint64_t ptr = 0;
   long device = -1;
   int dims = 0;
@@ -58,6 +70,7 @@ bool describe(PyObject *o, const char *name, Tensor &t) {
   if (!THPVariable_Check(o)) return refuse("%s must be a tensor", name);
   const at::Tensor &x = THPVariable_Unpack(o);
   if (!x.defined() || x.layout() != at::kStrided) return refuse("%s must be a dense tensor", name);
+  t.keep = x;
   t.dims = static_cast<int>(x.dim());
   for (int i = 0; i < t.dims && i < 4; ++i) {
     t.shape[i] = x.size(i);
@@ -113,34 +126,43 @@ bool rows_of(PyObject *o, const char *name, long device, const Rows *like, Rows 
   return true;
 }
 
-// An output: the caller's tensor, or a new one of the input's shape.
-PyObject *output(PyObject *given, const char *name, const Rows &in, Rows &r) {
-  if (given != Py_None) return rows_of(given, name, in.t.device, &in, r) ? Py_NewRef(given) : nullptr;
-  const at::Tensor y =
-      at::empty({in.t.shape[0], in.t.shape[1], in.t.shape[2]},
-                at::TensorOptions().dtype(in.t.dtype).device(at::kCUDA, in.t.device));
-  r.t = in.t;
-  r.t.ptr = reinterpret_cast<uint64_t>(y.mutable_data_ptr());
-  r.h = mnb_heads{reinterpret_cast<void *>(r.t.ptr), in.t.shape[1] * in.t.shape[2], in.t.shape[2],
+// An output: the caller's tensor, or (made) a new one of the input's shape.
+bool output_of(PyObject *given, const char *name, const Rows &in, Rows &r) {
+  return given == Py_None || rows_of(given, name, in.t.device, &in, r);
+}
+void make_output(PyObject *given, const Rows &in, Rows &r) {
+  if (given != Py_None) return;
+  r.t.keep = at::empty({in.t.shape[0], in.t.shape[1], in.t.shape[2]},
+                       at::TensorOptions().dtype(in.t.dtype).device(at::kCUDA, in.t.device));
+  r.h = mnb_heads{r.t.keep.mutable_data_ptr(), in.t.shape[1] * in.t.shape[2], in.t.shape[2],
                   in.h.heads, 0};
-  return THPVariable_Wrap(y);
+}
+PyObject *result(PyObject *given, const Rows &r) {
+  return given != Py_None ? Py_NewRef(given) : THPVariable_Wrap(r.t.keep);
 }
 
-bool gamma_of(PyObject *o, const char *name, int64_t D, long device, const float *&p) {
-  p = nullptr;
-  if (o == Py_None) return true;
+struct Gamma {
   Tensor t;
+  const float *p = nullptr;
+};
+bool gamma_of(PyObject *o, const char *name, int64_t D, long device, Gamma &out) {
+  if (o == Py_None) return true;
+  Tensor &t = out.t;
   if (!describe(o, name, t) || !on_device(t, name, device)) return false;
   if (t.dtype != at::kFloat || t.dims != 1 || t.shape[0] != D || !contiguous(t))
     return refuse("%s must be a contiguous fp32 [%lld] tensor", name, (long long)D);
-  p = reinterpret_cast<const float *>(t.ptr);
+  out.p = reinterpret_cast<const float *>(t.ptr);
   return true;
 }
 
-bool rope_of(PyObject *o, int interleaved, long device, mnb_rope &r) {
+struct Rope {
+  Tensor cos, sin;
+  mnb_rope r;
+};
+bool rope_of(PyObject *o, int interleaved, long device, Rope &out) {
   Ref c(PyObject_GetAttr(o, s_cos)), s(PyObject_GetAttr(o, s_sin));
   if (!c.p || !s.p) return false;
-  Tensor tc, ts;
+  Tensor &tc = out.cos, &ts = out.sin;
   if (!describe(c.p, "cos", tc) || !describe(s.p, "sin", ts) || !on_device(tc, "cos", device) ||
       !on_device(ts, "sin", device))
     return false;
@@ -148,20 +170,20 @@ bool rope_of(PyObject *o, int interleaved, long device, mnb_rope &r) {
       tc.dtype != at::kFloat || ts.dtype != at::kFloat || !contiguous(tc) || !contiguous(ts))
     return refuse("cos and sin must be contiguous fp32 [positions, rot_dim / 2] tensors");
   if (tc.shape[1] > (1 << 20)) return refuse("cos and sin are too wide");
-  r = mnb_rope{reinterpret_cast<const float *>(tc.ptr), reinterpret_cast<const float *>(ts.ptr),
-               tc.shape[0], static_cast<int32_t>(2 * tc.shape[1]), interleaved ? 1 : 0};
+  out.r = mnb_rope{reinterpret_cast<const float *>(tc.ptr),
+                   reinterpret_cast<const float *>(ts.ptr), tc.shape[0],
+                   static_cast<int32_t>(2 * tc.shape[1]), interleaved ? 1 : 0};
   return true;
 }
 
 struct Cache {
-  Tensor k;
+  Tensor k, v;
   mnb_kv_cache c;
 };
 bool cache_of(PyObject *o, long device, Cache &out) {
   Ref k(PyObject_GetAttr(o, s_k)), v(PyObject_GetAttr(o, s_v));
   if (!k.p || !v.p) return false;
-  Tensor tv;
-  Tensor &tk = out.k;
+  Tensor &tk = out.k, &tv = out.v;
   if (!describe(k.p, "the cache's k", tk) || !describe(v.p, "the cache's v", tv)) return false;
   if (tk.dims != 4 || tv.dims != 4 || tk.dtype != tv.dtype || tk.shape[0] != tv.shape[0] ||
       tk.shape[1] != tv.shape[1] || tk.shape[2] != tv.shape[2] || tk.shape[3] != tv.shape[3])
@@ -186,11 +208,15 @@ bool cache_of(PyObject *o, long device, Cache &out) {
   return true;
 }
 
-bool batch_of(PyObject *o, long device, mnb_kv_batch &b) {
+struct Batch {
+  Tensor starts, lengths, table;
+  mnb_kv_batch b;
+};
+bool batch_of(PyObject *o, long device, Batch &out) {
   Ref s(PyObject_GetAttr(o, s_starts)), l(PyObject_GetAttr(o, s_lengths)),
       t(PyObject_GetAttr(o, s_table));
   if (!s.p || !l.p || !t.p) return false;
-  Tensor ts, tl, tt;
+  Tensor &ts = out.starts, &tl = out.lengths, &tt = out.table;
   if (!describe(s.p, "starts", ts) || !describe(l.p, "lengths", tl) ||
       !describe(t.p, "table", tt))
     return false;
@@ -206,12 +232,12 @@ bool batch_of(PyObject *o, long device, mnb_kv_batch &b) {
     if (all[i]->stride[last] != 1 && all[i]->shape[last] > 1)
       return refuse("%s must be contiguous", names[i]);
   }
-  b = mnb_kv_batch{reinterpret_cast<const int32_t *>(ts.ptr),
-                   reinterpret_cast<const int32_t *>(tl.ptr),
-                   reinterpret_cast<const int32_t *>(tt.ptr),
-                   tl.shape[0],
-                   tt.shape[1],
-                   tl.shape[0] > 1 ? tt.stride[0] : tt.shape[1]};
+  out.b = mnb_kv_batch{reinterpret_cast<const int32_t *>(ts.ptr),
+                       reinterpret_cast<const int32_t *>(tl.ptr),
+                       reinterpret_cast<const int32_t *>(tt.ptr),
+                       tl.shape[0],
+                       tt.shape[1],
+                       tl.shape[0] > 1 ? tt.stride[0] : tt.shape[1]};
   return true;
 }
 
@@ -237,45 +263,42 @@ PyObject *qk_norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
   if (!is_current(dev)) return Py_NewRef(Py_NotImplemented);
   const bool has_k = a[1] != Py_None;
   if (has_k && !rows_of(a[1], "k", dev, &q, k)) return nullptr;
-  mnb_rope rope;
+  Rope rope;
   const double eps = PyFloat_AsDouble(a[6]);
   const int inter = PyObject_IsTrue(a[7]);
   if ((eps == -1.0 && PyErr_Occurred()) || inter < 0) return nullptr;
   if (a[2] != Py_None && !rope_of(a[2], inter, dev, rope)) return nullptr;
+  Tensor t;
   const int32_t *pos = nullptr;
   if (a[3] != Py_None) {
-    Tensor t;
     if (!describe(a[3], "positions", t) || !on_device(t, "positions", dev)) return nullptr;
     if (t.dtype != at::kInt || t.dims != 1 || t.shape[0] != q.t.shape[0] || !contiguous(t))
       return refuse("positions must be a contiguous int32 [T] tensor"), nullptr;
     pos = reinterpret_cast<const int32_t *>(t.ptr);
   }
   if (!has_k && a[9] != Py_None) return refuse("out_k without k"), nullptr;
-  const float *gq, *gk;
+  Gamma gq, gk;
   if (!gamma_of(a[4], "gamma_q", q.t.shape[2], dev, gq) ||
       !gamma_of(a[5], "gamma_k", q.t.shape[2], dev, gk))
     return nullptr;
   const int code = dtype_code(q.t.dtype);
   if (code < 0) return nullptr;
   if (q.t.shape[2] > INT32_MAX) return refuse("q's heads are too long"), nullptr;
-  Ref yq(output(a[8], "out_q", q, oq));
-  if (!yq.p) return nullptr;
-  Ref yk;
-  if (has_k) {
-    yk.p = output(a[9], "out_k", k, ok);
-    if (!yk.p) return nullptr;
-  } else {
-    yk.p = Py_NewRef(Py_None);
-  }
-  const mnb_stream_t s = stream_of(dev);
-  if (!status_ok(mnb_qk_norm_rope(&q.h, has_k ? &k.h : nullptr, q.t.shape[0],
-                                  static_cast<int>(q.t.shape[2]), static_cast<mnb_dtype>(code),
-                                  gq, gk, static_cast<float>(eps),
-                                  a[2] == Py_None ? nullptr : &rope, pos, &oq.h,
-                                  has_k ? &ok.h : nullptr, s),
-                 "mnb_qk_norm_rope"))
+  if (!output_of(a[8], "out_q", q, oq) || (has_k && !output_of(a[9], "out_k", k, ok)))
     return nullptr;
-  return PyTuple_Pack(2, yq.p, yk.p);
+  mnb_status st;
+  {
+    const Released released;
+    make_output(a[8], q, oq);
+    if (has_k) make_output(a[9], k, ok);
+    st = mnb_qk_norm_rope(&q.h, has_k ? &k.h : nullptr, q.t.shape[0],
+                          static_cast<int>(q.t.shape[2]), static_cast<mnb_dtype>(code), gq.p, gk.p,
+                          static_cast<float>(eps), a[2] == Py_None ? nullptr : &rope.r, pos, &oq.h,
+                          has_k ? &ok.h : nullptr, stream_of(dev));
+  }
+  if (!status_ok(st, "mnb_qk_norm_rope")) return nullptr;
+  Ref yq(result(a[8], oq)), yk(has_k ? result(a[9], ok) : Py_NewRef(Py_None));
+  return yq.p && yk.p ? PyTuple_Pack(2, yq.p, yk.p) : nullptr;
 }
 
 // q, k, v, cache, batch, rope, gamma_q, gamma_k, eps, interleaved, out
@@ -283,8 +306,8 @@ PyObject *cache_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
   if (n != 11) return PyErr_Format(PyExc_TypeError, "11 arguments, not %zd", n);
   Rows q, k, v, oq;
   Cache c;
-  mnb_kv_batch b;
-  mnb_rope rope;
+  Batch b;
+  Rope rope;
   if (!rows_of(a[1], "k", -1, nullptr, k)) return nullptr;
   const long dev = k.t.device;
   if (!is_current(dev)) return Py_NewRef(Py_NotImplemented);
@@ -299,24 +322,21 @@ PyObject *cache_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
   if ((eps == -1.0 && PyErr_Occurred()) || inter < 0) return nullptr;
   if (!batch_of(a[4], dev, b) || (a[5] != Py_None && !rope_of(a[5], inter, dev, rope)))
     return nullptr;
-  const float *gq, *gk;
+  Gamma gq, gk;
   if (!gamma_of(a[6], "gamma_q", k.t.shape[2], dev, gq) ||
-      !gamma_of(a[7], "gamma_k", k.t.shape[2], dev, gk))
+      !gamma_of(a[7], "gamma_k", k.t.shape[2], dev, gk) ||
+      (has_q && !output_of(a[10], "out", q, oq)))
     return nullptr;
-  Ref y;
-  if (has_q) {
-    y.p = output(a[10], "out", q, oq);
-    if (!y.p) return nullptr;
-  } else {
-    y.p = Py_NewRef(Py_None);
+  mnb_status st;
+  {
+    const Released released;
+    if (has_q) make_output(a[10], q, oq);
+    st = mnb_cache_append(has_q ? &q.h : nullptr, &k.h, &v.h, k.t.shape[0], gq.p, gk.p,
+                          static_cast<float>(eps), a[5] == Py_None ? nullptr : &rope.r, &c.c, &b.b,
+                          has_q ? &oq.h : nullptr, stream_of(dev));
   }
-  const mnb_stream_t s = stream_of(dev);
-  if (!status_ok(mnb_cache_append(has_q ? &q.h : nullptr, &k.h, &v.h, k.t.shape[0], gq, gk,
-                                  static_cast<float>(eps), a[5] == Py_None ? nullptr : &rope,
-                                  &c.c, &b, has_q ? &oq.h : nullptr, s),
-                 "mnb_cache_append"))
-    return nullptr;
-  return y.take();
+  if (!status_ok(st, "mnb_cache_append")) return nullptr;
+  return has_q ? result(a[10], oq) : Py_NewRef(Py_None);
 }
 
 // q, cache, batch, scale (None: 1 / sqrt(head_dim)), window, out
@@ -324,7 +344,7 @@ PyObject *paged_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
   if (n != 6) return PyErr_Format(PyExc_TypeError, "6 arguments, not %zd", n);
   Rows q, o;
   Cache c;
-  mnb_kv_batch b;
+  Batch b;
   if (!rows_of(a[0], "q", -1, nullptr, q)) return nullptr;
   const long dev = q.t.device;
   if (!is_current(dev)) return Py_NewRef(Py_NotImplemented);
@@ -339,22 +359,24 @@ PyObject *paged_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
   }
   const long long window = PyLong_AsLongLong(a[4]);
   if (window == -1 && PyErr_Occurred()) return nullptr;
-  Ref y(output(a[5], "out", q, o));
-  if (!y.p) return nullptr;
-  // The workspace is freed on return to torch's allocator, which hands the
-  // memory out again on the same stream only, after the call's kernels.
-  const size_t need =
-      mnb_paged_attention_workspace_size(q.t.shape[0], q.h.heads, &c.c, &b);
-  at::Tensor ws;
-  if (need)
-    ws = at::empty({static_cast<int64_t>(need)},
-                   at::TensorOptions().dtype(at::kByte).device(at::kCUDA, dev));
-  const mnb_stream_t s = stream_of(dev);
-  if (!status_ok(mnb_paged_attention(&q.h, q.t.shape[0], &c.c, &b, static_cast<float>(scale),
-                                     window, &o.h, need ? ws.mutable_data_ptr() : nullptr, need, s),
-                 "mnb_paged_attention"))
-    return nullptr;
-  return y.take();
+  if (!output_of(a[5], "out", q, o)) return nullptr;
+  mnb_status st;
+  {
+    const Released released;
+    make_output(a[5], q, o);
+    // The workspace is freed to torch's allocator after the call, which hands the
+    // memory out again on the same stream only, after the call's kernels.
+    const size_t need =
+        mnb_paged_attention_workspace_size(q.t.shape[0], q.h.heads, &c.c, &b.b);
+    at::Tensor ws;
+    if (need)
+      ws = at::empty({static_cast<int64_t>(need)},
+                     at::TensorOptions().dtype(at::kByte).device(at::kCUDA, dev));
+    st = mnb_paged_attention(&q.h, q.t.shape[0], &c.c, &b.b, static_cast<float>(scale), window,
+                             &o.h, need ? ws.mutable_data_ptr() : nullptr, need, stream_of(dev));
+  }
+  if (!status_ok(st, "mnb_paged_attention")) return nullptr;
+  return result(a[5], o);
 }
 
 // frequencies, n, first, magnitude, device (-1: the current one)
@@ -373,14 +395,18 @@ PyObject *rope_table(PyObject *, PyObject *const *a, Py_ssize_t n) {
   if (!is_current(dev)) return Py_NewRef(Py_NotImplemented);
   const int64_t pairs = f.shape[0];
   if (rows < 0 || pairs > (1 << 20)) return refuse("n must not be negative"), nullptr;
-  const auto options = at::TensorOptions().dtype(at::kFloat).device(at::kCUDA, dev);
-  const at::Tensor c = at::empty({rows, pairs}, options), s = at::empty({rows, pairs}, options);
-  if (!status_ok(mnb_rope_table(reinterpret_cast<const double *>(f.ptr),
-                                static_cast<int>(2 * pairs), first, rows, magnitude,
-                                static_cast<float *>(c.mutable_data_ptr()),
-                                static_cast<float *>(s.mutable_data_ptr()), stream_of(dev)),
-                 "mnb_rope_table"))
-    return nullptr;
+  at::Tensor c, s;
+  mnb_status st;
+  {
+    const Released released;
+    const auto options = at::TensorOptions().dtype(at::kFloat).device(at::kCUDA, dev);
+    c = at::empty({rows, pairs}, options);
+    s = at::empty({rows, pairs}, options);
+    st = mnb_rope_table(reinterpret_cast<const double *>(f.ptr), static_cast<int>(2 * pairs), first,
+                        rows, magnitude, static_cast<float *>(c.mutable_data_ptr()),
+                        static_cast<float *>(s.mutable_data_ptr()), stream_of(dev));
+  }
+  if (!status_ok(st, "mnb_rope_table")) return nullptr;
   Ref pc(THPVariable_Wrap(c)), ps(THPVariable_Wrap(s));
   if (!pc.p || !ps.p) return nullptr;
   return PyTuple_Pack(2, pc.p, ps.p);

@@ -756,3 +756,45 @@ def test_tables_of_small_and_negative_frequencies(dev, f, n, first):
     slack += 2.0 ** -53 * a.abs()  # the reference's product
     within(t.cos, torch.cos(a), 2.0 ** -22 * torch.cos(a).abs() + slack + 1e-45)
     within(t.sin, torch.sin(a), 2.0 ** -22 * torch.sin(a).abs() + slack + 1e-45)
+
+
+def test_other_threads_run_while_a_call_waits(dev):
+    """A launch that finds the stream's queue full blocks until the GPU catches up; the process's
+    other Python threads go on meanwhile. (The stream is held by a host function that sleeps.)"""
+    import ctypes
+    import threading
+    import time
+    hold = 0.5
+    driver = ctypes.CDLL("libcuda.so.1")
+    sleep = ctypes.cast(ctypes.CDLL(None).usleep, ctypes.c_void_p)
+    q = torch.zeros(1, 1, 64, dtype=BF16, device=dev)
+    y = torch.empty_like(q)
+    gamma = torch.ones(64, device=dev)
+    call = lambda: mnb.mnb_qk_norm_rope(q, None, None, None, gamma_q=gamma, out_q=y)  # noqa: E731
+    call()
+    torch.cuda.synchronize()
+    beats, stop = [], threading.Event()
+
+    def beat():
+        while not stop.is_set():
+            beats.append(time.perf_counter())
+            time.sleep(0.002)
+    other = threading.Thread(target=beat)
+    other.start()
+    try:
+        stream = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        assert driver.cuLaunchHostFunc(stream, sleep, ctypes.c_void_p(int(hold * 1e6))) == 0
+        start = at = time.perf_counter()
+        longest = 0.0
+        while at - start < hold:
+            call()
+            now = time.perf_counter()
+            longest, at = max(longest, now - at), now
+    finally:
+        stop.set()
+        other.join()
+        torch.cuda.synchronize()
+    assert longest > hold / 2, "no call had to wait"
+    beats = [b for b in beats if start <= b <= at]
+    gaps = [b - a for a, b in zip([start] + beats, beats + [at])]
+    assert max(gaps) < hold / 4, f"the other thread stood still for {max(gaps):.3f} s"
