@@ -5,7 +5,8 @@ the objects link into ``libmnb.so`` next to this file, with the CUDA runtime
 linked statically so the library does not depend on which runtime another
 package in the process loaded. Beside it goes ``_mnb_py.so``, the part of the
 Python binding that reads tensors through torch's C++ interface; it calls
-``libmnb.so`` (found next to it) and holds no computation.
+``libmnb.so`` (found next to it) and holds no computation. ``libmnb.so`` needs
+nvcc alone: it is linked first, and without torch it is all that is built.
 """
 from __future__ import annotations
 
@@ -58,18 +59,15 @@ def _gxx() -> str:
     return shutil.which("g++") or "g++"
 
 
-def _torch_dir() -> str:
-    """Where torch is installed, without importing it."""
+def _torch_dir() -> str | None:
+    """Where torch is installed, without importing it; None: it is not."""
     spec = importlib.util.find_spec("torch")
-    if spec is None or not spec.origin:
-        raise RuntimeError("torch not found: the Python binding is built against it")
-    return os.path.dirname(spec.origin)
+    return os.path.dirname(spec.origin) if spec is not None and spec.origin else None
 
 
-def _compile_py(force: bool) -> str:
+def _compile_py(torch_dir: str, force: bool) -> str:
     """The object of the Python binding's native part. The interpreter and the
     torch that it is compiled for are part of its name: another's is stale."""
-    torch_dir = _torch_dir()
     with open(os.path.join(torch_dir, "version.py")) as f:
         made_for = (sysconfig.get_config_var("SOABI") or "") + torch_dir + f.read()
     obj = os.path.join(OBJ_DIR, f"py_attn.{zlib.crc32(made_for.encode()):08x}.o")
@@ -90,7 +88,8 @@ def _compile_py(force: bool) -> str:
 
 
 def build_library(force: bool = False, verbose: bool = False) -> str:
-    """Compile (if stale) and return the path of libmnb.so."""
+    """Compile (if stale) and return the path of libmnb.so. What fails in the
+    Python binding's native part is raised once libmnb.so is there."""
     os.makedirs(OBJ_DIR, exist_ok=True)
     nvcc = _nvcc()
     headers = _deps()
@@ -111,10 +110,10 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
         os.replace(tmp, obj)
         return obj
 
+    torch_dir = _torch_dir()
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
-        py = ex.submit(_compile_py, force)
+        py = ex.submit(_compile_py, torch_dir, force) if torch_dir else None
         list(ex.map(compile_one, zip(srcs, objs)))
-        py_obj = py.result()
 
     if force or _stale(LIB_PATH, objs):
         tmp = LIB_PATH + f".tmp{os.getpid()}"
@@ -124,8 +123,11 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"link failed:\n{res.stdout}{res.stderr}")
         os.replace(tmp, LIB_PATH)
 
+    if py is None:
+        return LIB_PATH
+    py_obj = py.result()
     if force or _stale(PY_PATH, [py_obj]):
-        torch_lib = os.path.join(_torch_dir(), "lib")
+        torch_lib = os.path.join(torch_dir, "lib")
         tmp = PY_PATH + f".tmp{os.getpid()}"
         cmd = [_gxx(), "-shared", "-o", tmp, py_obj, "-L" + PKG, "-l:libmnb.so", "-L" + torch_lib,
                "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10",
