@@ -3,9 +3,10 @@
 Each translation unit compiles in parallel to an object under ``_build/``;
 the objects link into ``libmnb.so`` next to this file, with the CUDA runtime
 linked statically so the library does not depend on which runtime another
-package in the process loaded. Beside it goes ``_mnb_py.so``, the part of the
-Python binding that reads tensors through torch's C++ interface; it calls
-``libmnb.so`` (found next to it) and holds no computation. ``libmnb.so`` needs
+package in the process loaded. Beside it goes ``_mnb_py.<key>.so``, the part of
+the Python binding that reads tensors through torch's C++ interface; it calls
+``libmnb.so`` (found next to it) and holds no computation. The key stands for the
+interpreter and the torch that it was made for. ``libmnb.so`` needs
 nvcc alone: it is linked first, and without torch it is all that is built.
 """
 from __future__ import annotations
@@ -24,7 +25,6 @@ CSRC = os.path.join(PKG, "csrc")
 OBJ_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libmnb.so")
 PY_SRC = os.path.join(CSRC, "py_attn.cpp")
-PY_PATH = os.path.join(PKG, "_mnb_py.so")
 HEADER = os.path.join(ROOT, "include", "mnb.h")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -65,12 +65,26 @@ def _torch_dir() -> str | None:
     return os.path.dirname(spec.origin) if spec is not None and spec.origin else None
 
 
-def _compile_py(torch_dir: str, force: bool) -> str:
-    """The object of the Python binding's native part. The interpreter and the
-    torch that it is compiled for are part of its name: another's is stale."""
+def _py_key(torch_dir: str) -> str:
+    """The interpreter and the torch that the Python binding's native part is
+    compiled for and linked to, in the names of its object and module: no other
+    process finds them."""
     with open(os.path.join(torch_dir, "version.py")) as f:
         made_for = (sysconfig.get_config_var("SOABI") or "") + torch_dir + f.read()
-    obj = os.path.join(OBJ_DIR, f"py_attn.{zlib.crc32(made_for.encode()):08x}.o")
+    return f"{zlib.crc32(made_for.encode()):08x}"
+
+
+def py_path() -> str:
+    """The module of this process's interpreter and torch."""
+    torch_dir = _torch_dir()
+    if torch_dir is None:
+        raise RuntimeError("torch not found: the Python binding is built against it")
+    return os.path.join(os.path.dirname(LIB_PATH), f"_mnb_py.{_py_key(torch_dir)}.so")
+
+
+def _compile_py(torch_dir: str, force: bool) -> str:
+    """The object of the Python binding's native part."""
+    obj = os.path.join(OBJ_DIR, f"py_attn.{_py_key(torch_dir)}.o")
     if not force and not _stale(obj, [PY_SRC, HEADER]):
         return obj
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
@@ -125,17 +139,17 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
 
     if py is None:
         return LIB_PATH
-    py_obj = py.result()
-    if force or _stale(PY_PATH, [py_obj]):
+    py_obj, py_so = py.result(), py_path()
+    if force or _stale(py_so, [py_obj]):
         torch_lib = os.path.join(torch_dir, "lib")
-        tmp = PY_PATH + f".tmp{os.getpid()}"
+        tmp = py_so + f".tmp{os.getpid()}"
         cmd = [_gxx(), "-shared", "-o", tmp, py_obj, "-L" + PKG, "-l:libmnb.so", "-L" + torch_lib,
                "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10",
                "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + torch_lib]
         res = subprocess.run(cmd, capture_output=True, text=True)
         if res.returncode != 0:
             raise RuntimeError(f"link failed:\n{res.stdout}{res.stderr}")
-        os.replace(tmp, PY_PATH)
+        os.replace(tmp, py_so)
     return LIB_PATH
 
 

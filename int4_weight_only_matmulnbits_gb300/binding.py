@@ -1048,7 +1048,7 @@ def _native():
     global _native_mod
     if _native_mod is None:
         load()
-        path = _build.PY_PATH
+        path = _build.py_path()
         if not os.path.exists(path):
             raise RuntimeError(f"{path} is missing: build it with "
                                "`python -c 'import __graft_entry__ as g; g.build()'`")

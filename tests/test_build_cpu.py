@@ -65,3 +65,22 @@ def test_the_library_is_linked_whatever_becomes_of_the_binding(compilers):
     made = compilers.build()
     assert len(made) == 2 and made[0].startswith("py_attn.") and made[1].startswith("_mnb_py")
     assert compilers.build() == []
+
+
+def test_each_torch_has_a_module_of_its_own(compilers, monkeypatch, tmp_path):
+    """Built for one torch, then another, then the first again: what the binding would load is made
+    for the torch of the process each time, and newer than its object."""
+    for turn, version in enumerate(("1", "2", "1", "2")):
+        torch_dir = tmp_path / f"torch{version}"
+        torch_dir.mkdir(exist_ok=True)
+        (torch_dir / "version.py").write_text(f"version = {version!r}\n")
+        monkeypatch.setattr(_build, "_torch_dir", lambda: str(torch_dir))
+        made = compilers.build()
+        with open(_build.py_path()) as f:
+            command = f.read()
+        obj = [w for w in command.split() if "py_attn." in w][0]
+        with open(obj) as f:
+            assert str(torch_dir) in command and str(torch_dir) in f.read()
+        assert os.path.getmtime(_build.py_path()) > os.path.getmtime(obj)
+        assert [n for n in made if "py" in n] == (
+            [os.path.basename(obj), os.path.basename(_build.py_path())] if turn < 2 else [])
