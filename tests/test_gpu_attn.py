@@ -798,3 +798,134 @@ def test_other_threads_run_while_a_call_waits(dev):
     beats = [b for b in beats if start <= b <= at]
     gaps = [b - a for a, b in zip([start] + beats, beats + [at])]
     assert max(gaps) < hold / 4, f"the other thread stood still for {max(gaps):.3f} s"
+
+
+FINE, FINER = 2.0 ** -9, 2.0 ** -18  # 1 + FINE + FINER: each bf16 part of it holds one of the three
+
+
+def one_sequence_per_row(q, k, v, scale):
+    """Attention of q [n, heads, D], each row a sequence of its own over k, v [n or 1, keys, D] of
+    one key head."""
+    n, L, D = q.shape[0], k.shape[1], q.shape[2]
+    ps = -(-L // 16) * 16
+    pad = lambda x: torch.nn.functional.pad(x, (0, 0, 0, ps - L))[:, None].cuda()  # noqa: E731
+    table = torch.arange(n, dtype=torch.int32)[:, None] if k.shape[0] == n else torch.zeros(
+        n, 1, dtype=torch.int32)
+    return mnb.mnb_paged_attention(q.cuda(), mnb.KvCache(pad(k), pad(v)),
+                                   on_gpu(list(range(n + 1)), [L] * n, table), scale=scale)
+
+
+@pytest.mark.parametrize("G", [1, 4, 16])
+@pytest.mark.parametrize("D", [64, 128])
+def test_the_low_bits_of_fp32_keys(dev, D, G):
+    """Two keys whose scores differ by bits past the 16th alone, in some of the elements, blown up
+    by the scale: row t, which holds element t alone, sees them as 1 apart where they differ. All
+    products and sums are exact in 24 bits."""
+    g = torch.Generator().manual_seed(D + G)
+    bit = torch.randint(0, 2, (D,), generator=g).float()
+    k = torch.full((1, 2, D), 1 + FINE)
+    k[0, 0] += bit * FINER
+    q = torch.eye(D)[:, None].expand(D, G, D).contiguous()
+    v = torch.tensor([1.0, 0.0])[None, :, None].expand(1, 2, D).contiguous()
+    y = one_sequence_per_row(q, k, v, 1 / FINER).double().cpu()
+    want = torch.sigmoid(bit.double())
+    # The exponential to 2^-21, the roundings of weight, sum, quotient and product.
+    assert ((y - want[:, None, None]).abs() <= 2.0 ** -20).all()
+
+
+@pytest.mark.parametrize("G", [1, 4, 16])
+@pytest.mark.parametrize("D", [64, 128])
+def test_the_low_bits_of_fp32_queries(dev, D, G):
+    """The same with the low bits in the rows: element t has them, element t + 1 does not; one key
+    takes the even elements, the other the odd ones."""
+    t = torch.arange(D)
+    q = torch.zeros(D, G, D)
+    q[t, :, t], q[t, :, (t + 1) % D] = 1 + FINE + FINER, 1 + FINE
+    even = (t % 2 == 0).float()
+    k = torch.stack((even, 1 - even))[None]
+    v = torch.tensor([1.0, 0.0])[None, :, None].expand(1, 2, D).contiguous()
+    y = one_sequence_per_row(q, k, v, 1 / FINER).double().cpu()
+    want = torch.sigmoid(torch.where(t % 2 == 0, 1.0, -1.0).double())
+    assert ((y - want[:, None, None]).abs() <= 2.0 ** -20).all()
+
+
+@pytest.mark.parametrize("G", [1, 4, 16])
+@pytest.mark.parametrize("D", [64, 128])
+def test_products_of_the_middle_bits(dev, D, G):
+    """(1 + 2^-9)^2 against 1 + 2^-8: the product of both factors' second parts is what differs."""
+    t = torch.arange(D)
+    q = torch.zeros(D, G, D)
+    q[t, :, t], q[t, :, (t + 1) % D] = 1 + FINE, 1.0
+    k = torch.zeros(D, 2, D)
+    k[t, 0, t], k[t, 1, (t + 1) % D] = 1 + FINE, 1 + 2 * FINE
+    v = torch.tensor([1.0, 0.0])[None, :, None].expand(D, 2, D).contiguous()
+    y = one_sequence_per_row(q, k, v, 1 / FINER).double().cpu()
+    assert ((y - torch.sigmoid(torch.tensor(1.0).double())).abs() <= 2.0 ** -20).all()
+
+
+@pytest.mark.parametrize("G", [1, 4, 16])
+@pytest.mark.parametrize("D", [64, 128])
+def test_the_low_bits_of_fp32_values(dev, D, G):
+    """One key attended with weight 1, at every place of a step in turn (the others' scores are
+    200 below): its value comes back, 24 bits of it."""
+    g = torch.Generator().manual_seed(D * G)
+    n = 64
+    q = torch.zeros(n, G, D)
+    q[..., 0] = 1.0
+    k, v = torch.zeros(n, n, D), torch.randn(n, n, D, generator=g)
+    k[..., 0] = -200.0
+    i = torch.arange(n)
+    k[i, i, 0] = 0.0
+    y = one_sequence_per_row(q, k, v, 1.0).double().cpu()
+    want = v[i, i].double()[:, None].expand(n, G, D)
+    # Three parts to 2^-25 and their sum to 2^-23; e^-200 counts for nothing in 24 bits.
+    assert ((y - want).abs() <= 2.0 ** -22 * want.abs()).all()
+
+
+@pytest.mark.parametrize("G", [1, 4, 16])
+@pytest.mark.parametrize("D", [64, 128])
+def test_the_low_bits_of_fp32_weights(dev, D, G):
+    """Weights 1 and 1 - 2^-9 - 2^-18 of opposite values, at every pair of neighbouring places of a
+    step: what is left of the sum is their difference, 2^-18 of which are the weight's third part."""
+    n = 64
+    w = 1 - FINE - FINER
+    q = torch.zeros(n, G, D)
+    q[..., 0] = 1.0
+    k, v = torch.zeros(n, n, D), torch.zeros(n, n, D)
+    k[..., 0] = -200.0
+    i = torch.arange(n)
+    k[i, i, 0], k[i, (i + 1) % n, 0] = 0.0, math.log(w)
+    v[i, i], v[i, (i + 1) % n] = 1.0, -1.0
+    y = one_sequence_per_row(q, k, v, 1.0).double().cpu()
+    want = (1 - w) / (1 + w)
+    # The exponential to 2^-21, over a sum of 2; without the third part it would be 2^-19 off.
+    assert ((y - want).abs() <= 2.0 ** -21).all()
+
+
+@pytest.mark.parametrize("news,lens,hq,H,D", [
+    ([1], [2049], 16, 8, 128), ([4], [300], 2, 2, 64), ([1] * 12, [900] * 12, 8, 2, 128),
+    ([16], [16], 4, 2, 64), ([40], [1000], 4, 2, 128), ([130], [130], 8, 1, 64),
+    ([33, 60], [700, 2000], 6, 2, 128)])
+@pytest.mark.parametrize("spread", [1.0, 4.0])
+def test_fp32_attention_is_as_exact_as_fp32_arithmetic(dev, news, lens, hq, H, D, spread):
+    """The error's mean square against 64 bits, beside that of the same attention in elementary fp32
+    operations. Three bf16 parts a factor come out at up to 1.4 times the plain error when the
+    kernel's arithmetic is followed on the CPU, two parts at 20 times and more."""
+    g = torch.Generator().manual_seed(len(news) + D)
+    starts, table, pages, T = make_batch(g, news, lens, 16)
+    cache = make_cache(g, pages, H, 16, D, F32)
+    q = rows(g, T, hq, D, F32, spread=spread)
+    y = mnb.mnb_paged_attention(q, cache, on_gpu(starts, lens, table)).cpu()
+    want, _ = ref.attend(q.cpu(), cache.k.cpu(), cache.v.cpu(), starts, lens, table, D ** -0.5)
+    plain = torch.empty_like(y)
+    for b, L in enumerate(lens):
+        g_ = table[b].long()
+        k, v = (x.cpu()[g_].transpose(1, 2).reshape(-1, H, D)[:L].repeat_interleave(hq // H, 1)
+                for x in (cache.k, cache.v))
+        for t in range(starts[b], starts[b + 1]):
+            p = L - (starts[b + 1] - t) + 1
+            s = (q[t].cpu()[None] * k[:p]).sum(-1) * D ** -0.5
+            w = torch.exp(s - s.amax(0))
+            plain[t] = (w[..., None] * v[:p]).sum(0) / w.sum(0)[:, None]
+    rms = lambda x: (x.double() - want).pow(2).mean().sqrt().item()  # noqa: E731
+    assert rms(y) <= 4 * rms(plain), f"{rms(y):.3g}, plain fp32 {rms(plain):.3g}"
