@@ -929,3 +929,41 @@ def test_fp32_attention_is_as_exact_as_fp32_arithmetic(dev, news, lens, hq, H, D
             plain[t] = (w[..., None] * v[:p]).sum(0) / w.sum(0)[:, None]
     rms = lambda x: (x.double() - want).pow(2).mean().sqrt().item()  # noqa: E731
     assert rms(y) <= 4 * rms(plain), f"{rms(y):.3g}, plain fp32 {rms(plain):.3g}"
+
+
+@pytest.mark.parametrize("hq,D", [(16, 128), (24, 128), (8, 64)])
+def test_what_the_kernel_itself_left_in_shared_memory(dev, hq, D):
+    """Masked blocks that are a CTA's first, after the same kernel has filled every stage of every
+    SM's ring with the NaN of another cache."""
+    g = torch.Generator().manual_seed(34)
+    news, lens = [7, 708, 9, 5, 1, 2, 1, 0, 57], [7, 908, 4312, 2428, 11, 2, 10, 90, 57]
+    starts, table, pages, T = make_batch(g, news, lens, 64)
+    cache = make_cache(g, pages, 8, 64, D, BF16)
+    q, batch = rows(g, T, hq, D, BF16), on_gpu(starts, lens, table)
+    want, bound = ref.attend(q.cpu(), cache.k.cpu(), cache.v.cpu(), starts, lens, table, D ** -0.5)
+    # 4000 tokens of 8 key heads: each CTA takes more blocks of keys than its ring holds.
+    starts2, table2, pages2, T2 = make_batch(g, [4000], [4000], 64)
+    nan = make_cache(g, pages2, 8, 64, D, BF16, fill=NAN)
+    q2, batch2 = rows(g, T2, hq, D, BF16), on_gpu(starts2, [4000], table2)
+    for _ in range(6):
+        assert mnb.mnb_paged_attention(q2, nan, batch2).isnan().all()
+        within(mnb.mnb_paged_attention(q, cache, batch), want, bound)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("window", [1, 16, 100, 700])
+def test_many_sequences_over_a_window(dev, window, dtype):
+    """More sequences and units than clusters take, a few tokens each."""
+    g = torch.Generator().manual_seed(window + 40)
+    lens = [int(x) for x in torch.randint(3, 900, (45,), generator=g)]
+    attend(g, [1 + i % 3 for i in range(45)], lens, 8, 2, 128, 16, dtype, window=window, dirty=True)
+
+
+@pytest.mark.parametrize("window", [0, 50])
+@pytest.mark.parametrize("chunk,L", [(100, 700), (150, 150)])
+def test_a_chunk_among_many_decoding_sequences(dev, chunk, L, window):
+    """So many sequences that the chunk goes through the kernel for few rows as well."""
+    g = torch.Generator().manual_seed(chunk)
+    lens = [int(x) for x in torch.randint(1, 400, (63,), generator=g)]
+    attend(g, [1] * 40 + [chunk] + [1] * 23, lens[:40] + [L] + lens[40:], 4, 2, 128, 16, BF16,
+           window=window, dirty=True)
