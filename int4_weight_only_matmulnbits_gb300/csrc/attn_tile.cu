@@ -97,6 +97,17 @@ __device__ __forceinline__ bool mbar_sleep(uint64_t *bar, uint32_t parity) {
   }
   return false;
 }
+// The same for what a whole run of blocks may stand before: the next masked block,
+// or the next unit for a tile that the present one leaves out. 2^31 keys are 2^24
+// blocks at 1.4 us, 23 s; the copying warp says when it has given up.
+__device__ __forceinline__ bool mbar_sleep_long(uint64_t *bar, uint32_t parity,
+                                                const volatile int *given_up) {
+  for (int i = 0; i < 40; ++i) {
+    if (mbar_sleep(bar, parity)) return true;
+    if (*given_up) return false;
+  }
+  return false;
+}
 __device__ __forceinline__ bool elect_one() {
   uint32_t ok;
   asm volatile(
@@ -451,7 +462,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *qfree = taken + kPieces;    // per tile: its rows have been used
   uint64_t *done = qfree + 2;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
-  static_assert((2 * C::stages + 3 * kInfo + 2 * kPieces + 11) * 8 + 4 <= 768, "barriers");
+  volatile int *given_up = reinterpret_cast<int *>(tmem_slot + 1);  // the copying warp has
+  static_assert((2 * C::stages + 3 * kInfo + 2 * kPieces + 11) * 8 + 8 <= 768, "barriers");
   int *todo = reinterpret_cast<int *>(smem + C::off_todo);
   Piece *pieces = reinterpret_cast<Piece *>(smem + C::off_pieces);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -478,6 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(ofull + i, 1);
     }
     mbar_init(done, 1);
+    *given_up = 0;
     fence_barrier_init();
   }
   if (warp == kMmaWarp) {
@@ -497,7 +510,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // The pieces, as every warp but the copying ones takes them: copied to
   // registers, so that the place is free again at once.
   auto take_piece = [&](int n, bool &ok) {
-    ok = __all_sync(0xffffffffu, mbar_sleep(listed + n % kPieces, (n / kPieces) & 1));
+    ok = __all_sync(0xffffffffu,
+                    mbar_sleep_long(listed + n % kPieces, (n / kPieces) & 1, given_up));
     const Piece pc = pieces[n % kPieces];
     __syncwarp();
     if (lane == 0) mbar_arrive(taken + n % kPieces);
@@ -604,7 +618,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(toscan + scans % kInfo);
       }
       if (!ok) {
-        if (lane == 0) record_fault(&g_fault_attn, kFaultAttnWait);
+        if (lane == 0) {
+          *given_up = 1;
+          record_fault(&g_fault_attn, kFaultAttnWait);
+        }
         // Given up: the copies in flight land before the CTA leaves.
         for (int i = max(0, tiles - C::stages); i < tiles; ++i)
           mbar_sleep(full + i % C::stages, (i / C::stages) & 1);
@@ -731,7 +748,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto over = [](uint32_t y) { return (y & 0x7F807F80u) + 0x00800080u; };
       bool ok = true;
       for (int n = 0; ok; ++n) {
-        ok = __all_sync(0xffffffffu, mbar_sleep(toscan + n % kInfo, (n / kInfo) & 1));
+        ok = __all_sync(0xffffffffu,
+                        mbar_sleep_long(toscan + n % kInfo, (n / kInfo) & 1, given_up));
         const int block = ok ? todo[n % kInfo] : -1, t = 2 * block + 1;
         if (block < 0) break;
         ok = __all_sync(0xffffffffu, mbar_sleep(full + t % C::stages, (t / C::stages) & 1));

@@ -967,3 +967,38 @@ def test_a_chunk_among_many_decoding_sequences(dev, chunk, L, window):
     lens = [int(x) for x in torch.randint(1, 400, (63,), generator=g)]
     attend(g, [1] * 40 + [chunk] + [1] * 23, lens[:40] + [L] + lens[40:], 4, 2, 128, 16, BF16,
            window=window, dirty=True)
+
+
+@pytest.mark.parametrize("n,new", [(1, 4864), (160, 16)])
+def test_runs_of_blocks_longer_than_a_wait(dev, n, new):
+    """154 M positions (pages that repeat), so that a CTA of the tensor-core kernel goes through
+    blocks without a mask, or with one tile alone, for more than the second after which other waits
+    give up. Four keys of a page take all the weight (the others' underflows to 0)."""
+    g = torch.Generator().manual_seed(41)
+    hq, D, ps, repeats = 8, 128, 1 << 16, 2344
+    L = repeats * ps - 40000
+    hot = torch.tensor([70, 20001, 30011, 65535])
+    u = torch.randn(D, generator=g)
+    u /= u.norm()
+    k = torch.zeros(1, 1, ps, D)
+    k[0, 0, hot] = u * 40
+    q = (u * 34 + 0.3 * torch.randn(n * new, hq, D, generator=g)).to(BF16).to(dev)
+    cache = mnb.KvCache(k.to(BF16).to(dev), torch.randn(k.shape, generator=g).to(BF16).to(dev))
+    starts = list(range(0, n * new + 1, new))
+    y = mnb.mnb_paged_attention(q, cache, on_gpu(starts, [L] * n,
+                                                 torch.zeros(n, repeats, dtype=torch.int32)))
+    assert mnb.mnb_fault_status() == 0
+    keys, values = (x[0, 0, hot.to(dev)].double().cpu() for x in (cache.k, cache.v))
+    for t in torch.randint(0, n * new, (40,), generator=g).tolist():
+        p = L - (new - t % new)
+        times = (p + 1) // ps + (hot <= p % ps).double() * ((p + 1) % ps > 0)
+        qt = q[t].double().cpu()
+        s = qt @ keys.T * D ** -0.5
+        assert (s > 105).all()  # e^-105 is below the smallest number
+        w = times * torch.exp(s - s.amax(-1, keepdim=True))
+        w /= w.sum(-1, keepdim=True)
+        want, spread = w @ values, w @ values.abs()
+        # As ref.attend counts them, with an addition for each time that a key counts.
+        dw = (D + 8) * 2.0 ** -23 * (qt.abs() @ keys.abs().T).amax() * D ** -0.5 + 2.0 ** -20
+        rel = 2 * dw + ref.BF16_U + (4 * repeats + 16) * 2.0 ** -23
+        within(y[t], want, rel * (spread + want.abs()) + ref.BF16_U * want.abs() + 1e-30)
