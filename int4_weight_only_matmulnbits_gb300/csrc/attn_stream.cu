@@ -753,8 +753,24 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F32, ROWS>::per_sm)
           for (int i = 0; i < D / 16; ++i) {
             uint32_t v4[4];
             ldsm4_t(vs + value_at<D, F32>(vr, 2 * i + (mi >> 1)), v4);
-            mma_bf16_16816(o[2 * i], a, v4[0], v4[1]);
-            mma_bf16_16816(o[2 * i + 1], a, v4[2], v4[3]);
+            if constexpr (CLUSTER) {
+              mma_bf16_16816(o[2 * i], a, v4[0], v4[1]);
+              mma_bf16_16816(o[2 * i + 1], a, v4[2], v4[3]);
+            } else {
+              // A sum of 16 terms of its own, added with rounding: the tensor cores
+              // cut off what they add, relative to the sum so far, and 4 M keys of
+              // equal weight in one block came out 0.4 % low. (A cluster's warps have
+              // 4096 steps at most, some 2^-12, and one sequence of 4097 tokens takes
+              // 0.3 us less without.)
+              float x[2][4];
+              mma_bf16_16816_zero(x[0], a, v4[0], v4[1]);
+              mma_bf16_16816_zero(x[1], a, v4[2], v4[3]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                o[2 * i][e] += x[0][e];
+                o[2 * i + 1][e] += x[1][e];
+              }
+            }
           }
         }
       }
@@ -1037,6 +1053,8 @@ cudaError_t run(AttnStreamParams p, bool pdl, cudaStream_t stream) {
     const double bytes = 2.0 * std::min<double>(p.cap, double(p.span) * C::block) * p.kv_heads * C::row;
     const double rate = std::min(6500.0, 45.0 * p.kv_heads * size);
     if (bytes * 1e-3 * (1 / rate - 1 / 6500.0) > 4.3) continue;
+    // Sums of the tensor cores stay short (see the product with the values).
+    if (std::min<double>(p.cap, double(p.span) * C::block) > 4096.0 * C::block * size) continue;
     auto *kernel = stream_kernel<D, F32, ROWS, true>;
     static std::atomic<unsigned long long> done{0};
     static std::atomic<int> known[2][64];

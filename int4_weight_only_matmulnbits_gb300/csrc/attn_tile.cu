@@ -58,6 +58,13 @@ constexpr float kGrow = 8.f;               // rescale from 2^8 on
 // A unit counts for as many blocks more than it has: its masked block, results
 // and first scores stand for some 6000 cycles, a block in full swing for 2650.
 constexpr int kUnitCost = 2;
+// Blocks whose products are added up in tensor memory. The tensor cores cut off
+// what they add, relative to the sum so far: 1 M keys of equal weight in one run
+// came out 0.37 % low, 4 M 2.2 %. So after a run a row's O goes to its thread's
+// place in global memory, added there with rounding: at most 4096 additions of the
+// tensor cores stand in a row, some 2^-12. (Runs past 65536 keys alone; a unit's
+// 131 KB there and back are some 3 us of 700.)
+constexpr int kRun = 512;
 
 template <int D>
 struct Cfg {
@@ -714,7 +721,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           wait(pfull, blocks0++);
           tc_fence_after();
           if (ok && elect_one()) {
-            values(0, vs, kb == 0, !two);
+            values(0, vs, kb % kRun == 0, !two);
             if (more)
               scores(0, ks, last, !two);
             else
@@ -725,7 +732,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           wait(pfull + 1, blocks1++);
           tc_fence_after();
           if (ok && elect_one()) {
-            values(1, vs, kb == 0, true);
+            values(1, vs, kb % kRun == 0, true);
             if (more)
               scores(1, ks, last, true);
             else
@@ -817,6 +824,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(qfull + i);
       };
+      // The row's place among a piece's results: four columns of all rows, the next
+      // four, ..: lanes lie side by side.
+      auto part_of = [&](const Piece &u) {
+        return p.parts + (int64_t(blockIdx.x) * 2 + (u.k0 == 0)) * (kUnit * (D + 2)) + row * 4;
+      };
       for (int pn = 0; ok; ++pn) {
         const Piece pc = take_piece(pn, ok);
         if (!ok || pc.none) break;
@@ -830,120 +842,146 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int pos = live ? max(pc.len - pc.n + tok, -1) : -1;
         if (!p.q_tma) load_q(pc, at, tok);
         float m = -INFINITY, mc = 0.f, l = 0.f;  // maximum (of scores), times the scale; sum
-        for (int kb = pc.k0; kb < pc.k1 && ok; ++kb, ++blocks, ++mine) {
-          // (In this order: a tile that was left out of units is blocks ahead.)
-          ok = mbar_sleep(sfull + i, mine & 1) &&
-               mbar_sleep(known + blocks % kInfo, (blocks / kInfo) & 1);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          tc_fence_after();
-          Info &f = infos[blocks % kInfo];
-          const int j0 = (pc.block0 + kb) * kTile;
-          const uint32_t have = f.pages;
-          const int scan = f.scan;
-          if (scan >= 0) {
-            ok = __all_sync(0xffffffffu,
-                            mbar_sleep(scanned + scan % kInfo, (scan / kInfo) & 1));
+        float part_mc = 0.f;  // mc when O was last added to part (-inf: nothing attended)
+        for (int run = pc.k0; run < pc.k1 && ok; run += kRun) {
+          if (run > pc.k0) {
+            // (The next scores tell that O is at rest.)
+            ok = __all_sync(0xffffffffu, mbar_sleep(sfull + i, mine & 1));
             if (!ok) break;
-            // Through tensor memory and back, in a loop: this way is taken for a
-            // block or two of a unit, and as straight code it took longer to fetch
-            // than to run.
+            tc_fence_after();
+            const bool add = run - pc.k0 > kRun;
+            const float fac = exp2_fast(part_mc - mc);
+            part_mc = m == -INFINITY ? -INFINITY : mc;
+            float *part = part_of(pc);
 #pragma unroll 1
-            for (int c0 = 0; c0 < kTile; c0 += 32) {
-              const uint32_t bad = *static_cast<const volatile uint32_t *>(&f.bad[c0 / 32]);
-              const int to = pos - j0 - c0, from = p.window > 0 ? to - p.window + 1 : 0;
-              // Bit e: the row attends column c0 + e.
-              uint32_t on = to < 0 ? 0u : to >= 31 ? ~0u : (2u << to) - 1u;
-              on &= from <= 0 ? ~0u : from >= 32 ? 0u : ~0u << from;
-              on &= ((have >> (c0 / 16)) & 1 ? 0xFFFFu : 0u) |
-                    ((have >> (c0 / 16)) & 2 ? 0xFFFF0000u : 0u);
-              if (__all_sync(0xffffffffu, on == ~0u && bad == 0)) continue;
-              float x[32];
-              if (__any_sync(0xffffffffu, on)) {
-                tmem_ld32(ts + c0, x);
+            for (int c = 0; c < D; c += 32) {
+              float o[32];
+              tmem_ld32(to + c, o);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) x[e] = on & (1u << e) ? x[e] : -INFINITY;
-                if (__any_sync(0xffffffffu, bad & on))
-#pragma unroll
-                  for (int e = 0; e < 32; ++e) x[e] = bad & on & (1u << e) ? NAN : x[e];
-              } else {
-#pragma unroll
-                for (int e = 0; e < 32; ++e) x[e] = -INFINITY;
+              for (int e = 0; e < 32; e += 4) {
+                float4 *x = reinterpret_cast<float4 *>(part + (c + e) * kUnit);
+                const float4 y = add ? *x : make_float4(0.f, 0.f, 0.f, 0.f);
+                *x = make_float4(fmaf(fac, y.x, o[e]), fmaf(fac, y.y, o[e + 1]),
+                                 fmaf(fac, y.z, o[e + 2]), fmaf(fac, y.w, o[e + 3]));
               }
-              tmem_st32(ts + c0, x);
             }
+          }
+          const int end = min(run + kRun, pc.k1);
+          for (int kb = run; kb < end && ok; ++kb, ++blocks, ++mine) {
+            // (In this order: a tile that was left out of units is blocks ahead.)
+            ok = mbar_sleep(sfull + i, mine & 1) &&
+                 mbar_sleep(known + blocks % kInfo, (blocks / kInfo) & 1);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            Info &f = infos[blocks % kInfo];
+            const int j0 = (pc.block0 + kb) * kTile;
+            const uint32_t have = f.pages;
+            const int scan = f.scan;
+            if (scan >= 0) {
+              ok = __all_sync(0xffffffffu,
+                              mbar_sleep(scanned + scan % kInfo, (scan / kInfo) & 1));
+              if (!ok) break;
+              // Through tensor memory and back, in a loop: this way is taken for a
+              // block or two of a unit, and as straight code it took longer to fetch
+              // than to run.
+#pragma unroll 1
+              for (int c0 = 0; c0 < kTile; c0 += 32) {
+                const uint32_t bad = *static_cast<const volatile uint32_t *>(&f.bad[c0 / 32]);
+                const int to = pos - j0 - c0, from = p.window > 0 ? to - p.window + 1 : 0;
+                // Bit e: the row attends column c0 + e.
+                uint32_t on = to < 0 ? 0u : to >= 31 ? ~0u : (2u << to) - 1u;
+                on &= from <= 0 ? ~0u : from >= 32 ? 0u : ~0u << from;
+                on &= ((have >> (c0 / 16)) & 1 ? 0xFFFFu : 0u) |
+                      ((have >> (c0 / 16)) & 2 ? 0xFFFF0000u : 0u);
+                if (__all_sync(0xffffffffu, on == ~0u && bad == 0)) continue;
+                float x[32];
+                if (__any_sync(0xffffffffu, on)) {
+                  tmem_ld32(ts + c0, x);
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) x[e] = on & (1u << e) ? x[e] : -INFINITY;
+                  if (__any_sync(0xffffffffu, bad & on))
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) x[e] = bad & on & (1u << e) ? NAN : x[e];
+                } else {
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) x[e] = -INFINITY;
+                }
+                tmem_st32(ts + c0, x);
+              }
+              tmem_st_wait();
+            }
+            float s0[32], s1[32], s2[32], s3[32];  // the scores, 32 columns each
+            tmem_ld32_async(ts, s0);
+            tmem_ld32_async(ts + 32, s1);
+            tmem_ld32_async(ts + 64, s2);
+            tmem_ld32_async(ts + 96, s3);
+            tmem_ld_wait(s0);
+            tmem_ld_wait(s1);
+            tmem_ld_wait(s2);
+            tmem_ld_wait(s3);
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            auto maxima = [&](const float (&v)[32]) {
+#pragma unroll
+              for (int c = 0; c < 32; c += 8)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mx[e] = fmaxf(fmaxf(mx[e], v[c + e]), v[c + 4 + e]);
+            };
+            maxima(s0);
+            maxima(s1);
+            maxima(s2);
+            maxima(s3);
+            const float top_s = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            const float new_m = fmaxf(m, top_s), new_mc = new_m == -INFINITY ? 0.f : new_m * p.scale;
+            // (Not for the difference of an infinity with itself.)
+            const bool grown = new_m > m && !(new_mc - mc <= kGrow && m != -INFINITY);
+            if (__any_sync(0xffffffffu, grown)) {
+              const float fac = m == -INFINITY ? 0.f : exp2_fast(grown ? mc - new_mc : 0.f);
+              if (grown) {
+                m = new_m;
+                mc = new_mc;
+              }
+              l *= fac;
+              if (kb > run) {
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                  float o[32];
+                  tmem_ld32(to + c, o);
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) o[e] *= fac;
+                  tmem_st32(to + c, o);
+                }
+              }
+            }
+            // Weights, rounded to bf16 (2^-8) for the product with the values; their
+            // sum takes them unrounded.
+            uint64_t sum[2] = {0, 0};
+            const uint64_t scale2 = pack2(p.scale, p.scale), mc2 = pack2(-mc, -mc);
+            auto weights = [&](int c0, const float (&v)[32]) {
+              uint32_t x[16];
+#pragma unroll
+              for (int c = 0; c < 32; c += 2) {
+                float a, b;
+                unpack2(fma2(pack2(v[c], v[c + 1]), scale2, mc2), a, b);
+                a = exp2_fast(a);
+                b = exp2_fast(b);
+                sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], pack2(a, b));
+                x[c / 2] = f32x2_to_bf16x2(a, b);
+              }
+              tmem_st16(ts + c0 / 2, x);
+            };
+            weights(0, s0);
+            weights(32, s1);
+            weights(64, s2);
+            weights(96, s3);
+            float la, lb;
+            unpack2(add2(sum[0], sum[1]), la, lb);
+            l += la + lb;
             tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(pfull + i);
           }
-          float s0[32], s1[32], s2[32], s3[32];  // the scores, 32 columns each
-          tmem_ld32_async(ts, s0);
-          tmem_ld32_async(ts + 32, s1);
-          tmem_ld32_async(ts + 64, s2);
-          tmem_ld32_async(ts + 96, s3);
-          tmem_ld_wait(s0);
-          tmem_ld_wait(s1);
-          tmem_ld_wait(s2);
-          tmem_ld_wait(s3);
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          auto maxima = [&](const float (&v)[32]) {
-#pragma unroll
-            for (int c = 0; c < 32; c += 8)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) mx[e] = fmaxf(fmaxf(mx[e], v[c + e]), v[c + 4 + e]);
-          };
-          maxima(s0);
-          maxima(s1);
-          maxima(s2);
-          maxima(s3);
-          const float top_s = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          const float new_m = fmaxf(m, top_s), new_mc = new_m == -INFINITY ? 0.f : new_m * p.scale;
-          // (Not for the difference of an infinity with itself.)
-          const bool grown = new_m > m && !(new_mc - mc <= kGrow && m != -INFINITY);
-          if (__any_sync(0xffffffffu, grown)) {
-            const float fac = m == -INFINITY ? 0.f : exp2_fast(grown ? mc - new_mc : 0.f);
-            if (grown) {
-              m = new_m;
-              mc = new_mc;
-            }
-            l *= fac;
-            if (kb > pc.k0) {
-#pragma unroll 1
-              for (int c = 0; c < D; c += 32) {
-                float o[32];
-                tmem_ld32(to + c, o);
-#pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] *= fac;
-                tmem_st32(to + c, o);
-              }
-            }
-          }
-          // Weights, rounded to bf16 (2^-8) for the product with the values; their
-          // sum takes them unrounded.
-          uint64_t sum[2] = {0, 0};
-          const uint64_t scale2 = pack2(p.scale, p.scale), mc2 = pack2(-mc, -mc);
-          auto weights = [&](int c0, const float (&v)[32]) {
-            uint32_t x[16];
-#pragma unroll
-            for (int c = 0; c < 32; c += 2) {
-              float a, b;
-              unpack2(fma2(pack2(v[c], v[c + 1]), scale2, mc2), a, b);
-              a = exp2_fast(a);
-              b = exp2_fast(b);
-              sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], pack2(a, b));
-              x[c / 2] = f32x2_to_bf16x2(a, b);
-            }
-            tmem_st16(ts + c0 / 2, x);
-          };
-          weights(0, s0);
-          weights(32, s1);
-          weights(64, s2);
-          weights(96, s3);
-          float la, lb;
-          unpack2(add2(sum[0], sum[1]), la, lb);
-          l += la + lb;
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(pfull + i);
         }
         if (ok) ok = mbar_sleep(ofull + i, units++ & 1);
         ok = __all_sync(0xffffffffu, ok);
@@ -951,6 +989,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         // ---- end of a piece
         const bool whole = pc.k0 == 0 && pc.k1 == pc.blocks;
+        if (pc.k1 - pc.k0 > kRun) {  // the earlier runs' sums, added to the last one's
+          const float fac = exp2_fast(part_mc - mc);
+          const float *part = part_of(pc);
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            float o[32];
+            tmem_ld32(to + c, o);
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              const float4 y = *reinterpret_cast<const float4 *>(part + (c + e) * kUnit);
+              o[e] = fmaf(fac, y.x, o[e]);
+              o[e + 1] = fmaf(fac, y.y, o[e + 1]);
+              o[e + 2] = fmaf(fac, y.z, o[e + 2]);
+              o[e + 3] = fmaf(fac, y.w, o[e + 3]);
+            }
+            tmem_st32(to + c, o);
+          }
+          tmem_st_wait();
+        }
         if (whole) {
           // Four lanes exchange 16-byte pieces of their rows, so that a store
           // covers 64 bytes of each row that it touches: with 16 of each, the
@@ -997,19 +1054,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
           }
         } else {
-          // Four columns of all rows, the next four, ..: lanes write side by side.
-          float *part = p.parts + (int64_t(blockIdx.x) * 2 + (pc.k0 == 0)) * (kUnit * (D + 2));
+          float *part = part_of(pc);
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
             float o[32];
             tmem_ld32(to + c, o);
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<float4 *>(part + (c + e) * kUnit + row * 4) =
+              *reinterpret_cast<float4 *>(part + (c + e) * kUnit) =
                   make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
           }
-          part[kUnit * D + row] = m;
-          part[kUnit * D + kUnit + row] = l;
+          float *sums = part + kUnit * D - row * 3;
+          sums[0] = m;
+          sums[kUnit] = l;
         }
         tc_fence_before();
         if (!pc.more) break;

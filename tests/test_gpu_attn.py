@@ -1002,3 +1002,20 @@ def test_runs_of_blocks_longer_than_a_wait(dev, n, new):
         dw = (D + 8) * 2.0 ** -23 * (qt.abs() @ keys.abs().T).amax() * D ** -0.5 + 2.0 ** -20
         rel = 2 * dw + ref.BF16_U + (4 * repeats + 16) * 2.0 ** -23
         within(y[t], want, rel * (spread + want.abs()) + ref.BF16_U * want.abs() + 1e-30)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n,new,repeats", [(1, 4864, 16), (1, 4864, 64), (304, 1, 64)])
+def test_sums_of_millions_of_keys(dev, n, new, repeats, D):
+    """The mean of ones over 1 M and 4 M keys (pages that repeat), on the tensor-core kernel and, a
+    row a sequence, on the streaming one: 1, unless the sums lose half of bf16's step below it,
+    2^-9. (Weights are rounded to bf16, 2^-9 either way, which a million of them average out.)"""
+    g = torch.Generator().manual_seed(42)
+    hq, ps = 8, 1 << 16
+    cache = mnb.KvCache(*(x.to(BF16).to(dev) for x in (torch.randn(1, 1, ps, D, generator=g),
+                                                       torch.ones(1, 1, ps, D))))
+    q = (0.2 * torch.randn(n * new, hq, D, generator=g)).to(BF16).to(dev)
+    batch = on_gpu(list(range(0, n * new + 1, new)), [repeats * ps] * n,
+                   torch.zeros(n, repeats, dtype=torch.int32))
+    y = mnb.mnb_paged_attention(q, cache, batch)
+    assert torch.all(y == 1), f"{y.float().min().item()} .. {y.float().max().item()}"
