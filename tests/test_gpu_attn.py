@@ -1019,3 +1019,39 @@ def test_sums_of_millions_of_keys(dev, n, new, repeats, D):
                    torch.zeros(n, repeats, dtype=torch.int32))
     y = mnb.mnb_paged_attention(q, cache, batch)
     assert torch.all(y == 1), f"{y.float().min().item()} .. {y.float().max().item()}"
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("window", [0, 150_000])
+def test_sums_put_aside_between_runs(dev, window, D):
+    """Runs of 512 blocks and more whose maxima keep growing, in units that CTAs share: 210 000 keys
+    that get longer, shuffled pages, some of which are missing."""
+    g = torch.Generator().manual_seed(43)
+    hq, ps, L, T = 8, 64, 210_000, 5000
+    pages = -(-L // ps)
+    table = torch.randperm(pages, generator=g).to(torch.int32)[None].clone()
+    table[0, 100:120], table[0, 2000] = -1, pages
+    k, v = (torch.randn(pages * ps, D, generator=g) for _ in range(2))
+    k *= torch.linspace(0.1, 2.5, pages * ps)[:, None]
+    there = ((table[0] >= 0) & (table[0] < pages)).repeat_interleave(ps)[:L].to(dev)
+    k, v = k.to(BF16).to(dev), v.to(BF16).to(dev)  # by position
+    cache = make_cache(g, pages, 1, ps, D, BF16, fill=NAN)
+    for x, y in ((cache.k, k), (cache.v, v)):
+        for i, page in enumerate(table[0].tolist()):
+            if 0 <= page < pages:
+                x[page, 0] = y[i * ps:(i + 1) * ps]
+    q = rows(g, T, hq, D, BF16)
+    y = mnb.mnb_paged_attention(q, cache, on_gpu([0, T], [L], table), window=window)
+    for t in [0, 1, T - 1] + torch.randint(0, T, (25,), generator=g).tolist():
+        p = L - T + t
+        j = torch.arange(L, device=dev)
+        on = there & (j <= p) & ((j > p - window) if window else True)
+        kd, vd, qt = k[:L][on].double(), v[:L][on].double(), q[t].double()
+        s = qt @ kd.T * D ** -0.5
+        w = torch.softmax(s, -1)
+        want, spread = w @ vd, w @ vd.abs()
+        # As ref.attend counts them; 2^-11 for what additions cut off.
+        ds = (D + 8) * 2.0 ** -23 * (qt.abs() @ kd.abs().T).amax(-1) * D ** -0.5
+        rel = 2 * (ds + 2.0 ** -21 + 3 * ref.F32_U) + ref.BF16_U + 2.0 ** -11
+        bound = rel[:, None] * (spread + want.abs())
+        within(y[t], want.cpu(), (bound + ref.BF16_U * (want.abs() + bound)).cpu())
