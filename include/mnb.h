@@ -952,6 +952,15 @@ typedef struct {
  *     length: r_i = (n_i - low) / (high - low) kept within 0 .. 1 (the ramp of
  *     YaRN, "Efficient Context Window Extension of Large Language Models",
  *     section 3.2).
+ * That ramp is linear in the turns. Much published model code ramps over the
+ * pair's index instead, with the same settings (its beta_fast is high, its
+ * beta_slow low): r_i = (b - i) / (b - a) kept within 0 .. 1, with
+ *   a = floor(d(high)), b = ceil(d(low)),
+ *   d(n) = rot_dim ln(original / (2 pi n)) / (2 ln base).
+ * These are other positions: for rot_dim 128, base 1e6, original 32768, factor 4,
+ * low 1 and high 32, 16 of the 64 pairs differ by more than 1 %, pair 32 the most
+ * (0.352 of the plain frequency here, 0.603 there). A model made with them needs
+ * them: mnb_rope_table takes any frequencies.
  * Errors: MNB_ERR_NULL, MNB_ERR_SHAPE (rot_dim odd, < 2 or > 256; base or
  * factor not positive and finite; original negative or not finite; with
  * original > 0, not 0 <= low < high).

@@ -1073,7 +1073,9 @@ def mnb_rope_frequencies(rot_dim: int, base: float = 1e6, *, factor: float = 1.0
                          high: float = 32.0) -> torch.Tensor:
     """Angles per position of rot_dim / 2 pairs (float64, on the CPU): plain
     (factor 1), interpolated by factor, or by parts of the spectrum when the
-    original length is given (include/mnb.h)."""
+    original length is given. The parts are told apart by a ramp over the turns
+    that a pair makes, not over its index: models made with the latter need
+    their own frequencies (formulas in include/mnb.h)."""
     out = torch.empty(max(rot_dim // 2, 0), dtype=torch.float64)
     _check(load().mnb_rope_frequencies(rot_dim, base, factor, original, low, high,
                                        out.data_ptr()), "mnb_rope_frequencies")

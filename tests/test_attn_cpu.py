@@ -245,3 +245,21 @@ def test_binding_refuses_what_it_cannot_describe():
         mnb.mnb_rope_table(torch.zeros(3), 10)     # not float64
     with pytest.raises(ValueError):
         mnb.mnb_paged_attention(t, mnb.KvCache(t, t), mnb.KvBatch(t, t, t))
+
+
+def test_frequencies_by_parts_ramp_over_the_turns_and_not_over_the_index():
+    """What the header says of the other ramp in use, with its formulas: a caller who needs it can
+    tell that these are not its frequencies."""
+    rot, base, original, factor, low, high = 128, 1e6, 32768.0, 4.0, 1.0, 32.0
+    plain = mnb.mnb_rope_frequencies(rot, base)
+    here = mnb.mnb_rope_frequencies(rot, base, factor=factor, original=original, low=low, high=high)
+    d = lambda n: rot * math.log(original / (2 * math.pi * n)) / (2 * math.log(base))  # noqa: E731
+    first, last = math.floor(d(high)), math.ceil(d(low))
+    r = ((last - torch.arange(rot // 2, dtype=torch.float64)) / (last - first)).clamp(0, 1)
+    there = (1 - r) * plain / factor + r * plain
+    apart = (here / there - 1).abs()
+    assert int((apart > 0.01).sum()) == 16 and int(apart.argmax()) == 32
+    assert abs(float(here[32] / plain[32]) - 0.352) < 5e-4
+    assert abs(float(there[32] / plain[32]) - 0.603) < 5e-4
+    assert torch.equal(here[:first + 1], plain[:first + 1])
+    assert torch.equal(here[last:], plain[last:] / factor)
