@@ -1046,8 +1046,9 @@ MNB_API mnb_status mnb_cache_append(const mnb_heads *q, const mnb_heads *k, cons
  * Sums and the softmax are fp32. bf16: weights relative to a running maximum
  * are rounded to bf16 (2^-8) for the product with the values, not for their
  * sum; what the tensor cores cut off in adding up stays below 2^-11 of the terms'
- * magnitudes, however many keys there are. fp32: products from three bf16 parts of each factor, within 2^-22 of
- * the terms' magnitudes (magnitudes above 3.38e38 count as infinite).
+ * magnitudes, however many keys there are. fp32: products from three bf16 parts of
+ * each factor, within 2^-22 of the terms' magnitudes (magnitudes above 3.38e38
+ * count as infinite).
  * What a masked place holds does not matter, infinities and NaN included. In a
  * key or value that a row does attend they reach that row's outputs (not always
  * as an exact sum would have them; a score of -inf counts as a masked one), and

@@ -105,7 +105,9 @@ __device__ __forceinline__ float exp2_fast(float x) {
 }
 
 // Two fp32 numbers as three pairs of bf16 numbers each, 24 bits in all: x =
-// h + m + l to 2^-25 of it. Of the nine products of two such numbers the six
+// h + m + l to 2^-25 of it (Henry, Tang, Heinecke, "Leveraging the bfloat16
+// Artificial Intelligence Datatype For Higher-Precision Computations", 2019). Of
+// the nine products of two such numbers the six
 // largest are taken, so a product is within 2^-23 or so. (tf32 pairs cost as
 // many tensor instructions and keep 21 bits: scores of 30 then move weights by
 // 7e-6.) Infinities, NaN and what is above bf16's largest number become NaN.
@@ -742,8 +744,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, F32, ROWS>::per_sm)
             }
           }
         } else {
-          // Weights are at most 1 and rounded once to bf16, as the values are
-          // held: 2^-8 of each term. Their sum takes them unrounded.
+          // Weights are at most 1 and rounded once to bf16, the type of the values
+          // that they are multiplied by (an MMA takes one type; a second part of the
+          // weights would be a second MMA): 2^-8 of each term, and errors of 0.0017
+          // against 64 bits where fp32 weights have 0.00165, results rounded to bf16.
+          // Their sum takes them unrounded.
           const uint32_t a[4] = {bf16_bits(s[0][0]) | (bf16_bits(s[0][1]) << 16),
                                  bf16_bits(s[0][2]) | (bf16_bits(s[0][3]) << 16),
                                  bf16_bits(s[1][0]) | (bf16_bits(s[1][1]) << 16),
@@ -1049,7 +1054,8 @@ cudaError_t run(AttnStreamParams p, bool pdl, cudaStream_t stream) {
     // Clusters cannot share a long sequence out over all SMs: it has its own
     // units' blocks, some 45 GB/s each, where the line reads at 6500. The line
     // takes 4.3 us more of launch and joining. (The table's width stands for the
-    // lengths, which the host does not know.)
+    // lengths, which the host does not know: with tables wider than some 53000 tokens,
+    // 8 key heads of 128, a short sequence takes the line too.)
     const double bytes = 2.0 * std::min<double>(p.cap, double(p.span) * C::block) * p.kv_heads * C::row;
     const double rate = std::min(6500.0, 45.0 * p.kv_heads * size);
     if (bytes * 1e-3 * (1 / rate - 1 / 6500.0) > 4.3) continue;

@@ -30,7 +30,10 @@ namespace {
 // multiple of 2^-32 turns, so that it keeps all of its 24 bits however near a
 // zero of the sine or cosine the angle lies, on either side, and goes through
 // the Taylor series of sine (to x^9) and cosine (to x^10), which end below 2^-28
-// there. Bound by the writes: 8 bytes for some 40 instructions.
+// there; in fp32, which leaves an error of 3 to 4e-8 where 64-bit results rounded
+// once have 2 to 3e-8, at a fraction of the work. Bound by the writes (8 bytes an
+// entry) and issue slots (some 40 instructions) alike: 147457 x 64 entries, 15.5
+// us, are 11.3 of the one and about 10 of the other.
 struct TableParams {
   uint64_t turns[kMaxPairs];
   int pairs;
@@ -196,7 +199,9 @@ __device__ __forceinline__ void load_floats(const float *p, float (&v)[N]) {
 // lanes. A group of lanes takes R heads of a token: their loads, which wait for
 // no position, go first, all together, and its cosines and sines serve all of
 // them. Bound by memory: every row is read and written once; the tables,
-// shared by a token's heads, add rot * 4 bytes to it.
+// shared by a token's heads, add rot * 4 bytes to it. Blocks on an SM (12 with four
+// heads a group, 16 with one) count for more than registers: at the 80 and 64 that
+// they leave a thread, the bf16 instances spill 76 to 84 bytes and 4 (fp32: none).
 constexpr int kRopeThreads = 64;
 template <bool F32, int LANES, int R, bool APPEND>
 __global__ void __launch_bounds__(kRopeThreads, R > 1 ? 12 : 16) rope_kernel(const __grid_constant__ RopeArgs a) {
