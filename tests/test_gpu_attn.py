@@ -1055,3 +1055,37 @@ def test_sums_put_aside_between_runs(dev, window, D):
         rel = 2 * (ds + 2.0 ** -21 + 3 * ref.F32_U) + ref.BF16_U + 2.0 ** -11
         bound = rel[:, None] * (spread + want.abs())
         within(y[t], want.cpu(), (bound + ref.BF16_U * (want.abs() + bound)).cpu())
+
+
+def test_calls_from_several_threads(dev):
+    """Threads with streams of their own, whose calls overlap on the host and on the GPU: every
+    result as alone."""
+    import threading
+    jobs = []
+    for i, (news, lens, dtype) in enumerate([([1, 1], [900, 70], BF16), ([130, 3], [300, 40], BF16),
+                                             ([1] * 40, [50] * 40, BF16), ([9], [700], F32)]):
+        g = torch.Generator().manual_seed(50 + i)
+        starts, table, pages, T = make_batch(g, news, lens, 16)
+        cache = make_cache(g, pages, 2, 16, 128, dtype)
+        q, batch = rows(g, T, 8, 128, dtype), on_gpu(starts, lens, table)
+        gamma = torch.rand(128, generator=g).to(dev)
+
+        def step(q=q, cache=cache, batch=batch, gamma=gamma):
+            y, _ = mnb.mnb_qk_norm_rope(q, None, None, None, gamma_q=gamma)
+            return mnb.mnb_paged_attention(y, cache, batch)
+        jobs.append((step, step(), torch.cuda.Stream(), []))
+    torch.cuda.synchronize()
+
+    def work(step, stream, out):
+        with torch.cuda.stream(stream):
+            for _ in range(100):
+                out.append(step())
+    threads = [threading.Thread(target=work, args=(step, stream, out))
+               for step, _, stream, out in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for _, alone, _, out in jobs:
+        assert len(out) == 100 and all(torch.equal(y, alone) for y in out)
