@@ -1960,10 +1960,15 @@ mnb_status mnb_paged_attention(const mnb_heads *q, int64_t T, const mnb_kv_cache
   st = check_workspace(workspace, workspace_bytes, need);
   if (st != MNB_OK) return st;
   const BatchRanges br(*batch);
+  const Range rows = heads_range(*q, T, D, es);
   const Range outs[] = {heads_range(*out, T, D, es), {workspace, need}};
-  const Range ins[] = {heads_range(*q, T, D, es), pages_range(*cache, false),
-                       pages_range(*cache, true), br.r[0], br.r[1], br.r[2]};
-  st = check_disjoint(outs, 2, ins, 6);
+  const Range ins[] = {pages_range(*cache, false), pages_range(*cache, true), br.r[0], br.r[1],
+                       br.r[2]};
+  st = check_disjoint(outs, 2, ins, 5);
+  // (The rows of q and out may be slices of one matrix's.)
+  if (st == MNB_OK &&
+      (heads_overlap(*q, *out, T, D, es) || overlap(workspace, need, rows.p, rows.n)))
+    st = MNB_ERR_ALIAS;
   if (st == MNB_OK) st = check_device();
   if (st != MNB_OK) return st;
   a.q = heads_view(q);

@@ -263,3 +263,16 @@ def test_frequencies_by_parts_ramp_over_the_turns_and_not_over_the_index():
     assert abs(float(there[32] / plain[32]) - 0.603) < 5e-4
     assert torch.equal(here[:first + 1], plain[:first + 1])
     assert torch.equal(here[last:], plain[last:] / factor)
+
+
+def test_attention_between_slices_of_one_matrix(lib):
+    """Rows of q and of the result side by side in one matrix: apart, although their ends interleave;
+    not so where they share an element, or the workspace lies among the rows of q."""
+    row = 8 * 64
+    q, o = heads(Q, 4, ts=row), heads(Q + 4 * 128, 4, ts=row)
+    assert attention(lib, q=q, o=o) in (b.MNB_ERR_DEVICE, b.MNB_ERR_CUDA)
+    assert attention(lib, q=o, o=q) in (b.MNB_ERR_DEVICE, b.MNB_ERR_CUDA)
+    assert attention(lib, q=q, o=heads(Q + 4 * 128 - 16, 4, ts=row)) == b.MNB_ERR_ALIAS
+    assert attention(lib, q=q, o=heads(Q + 5 * 128, 4, ts=row)) == b.MNB_ERR_ALIAS  # the next row's
+    assert attention(lib, q=q, ws=Q + 256) == b.MNB_ERR_ALIAS
+    assert attention(lib, q=q, o=q) == b.MNB_ERR_ALIAS

@@ -1089,3 +1089,19 @@ def test_calls_from_several_threads(dev):
     torch.cuda.synchronize()
     for _, alone, _, out in jobs:
         assert len(out) == 100 and all(torch.equal(y, alone) for y in out)
+
+
+@pytest.mark.parametrize("news,lens", [([1], [300]), ([1] * 40, [90] * 40), ([150], [200])])
+def test_results_beside_the_queries(dev, news, lens):
+    """q and out as slices of one matrix's rows."""
+    g = torch.Generator().manual_seed(44)
+    starts, table, pages, T = make_batch(g, news, lens, 16)
+    cache, batch = make_cache(g, pages, 2, 16, 128, BF16), on_gpu(starts, lens, table)
+    both = torch.full((T, 18, 128), 7.0, dtype=BF16, device=dev)
+    both[:, 1:9] = rows(g, T, 8, 128, BF16)
+    q, out = both[:, 1:9], both[:, 9:17]
+    want = mnb.mnb_paged_attention(q.contiguous(), cache, batch)
+    before = q.clone()
+    assert mnb.mnb_paged_attention(q, cache, batch, out=out) is out
+    assert torch.equal(out, want) and torch.equal(q, before)
+    assert torch.all(both[:, 0] == 7.0) and torch.all(both[:, 17] == 7.0)
