@@ -1059,8 +1059,9 @@ cudaError_t run(AttnStreamParams p, bool pdl, cudaStream_t stream) {
     const double bytes = 2.0 * std::min<double>(p.cap, double(p.span) * C::block) * p.kv_heads * C::row;
     const double rate = std::min(6500.0, 45.0 * p.kv_heads * size);
     if (bytes * 1e-3 * (1 / rate - 1 / 6500.0) > 4.3) continue;
-    // Sums of the tensor cores stay short (see the product with the values).
-    if (std::min<double>(p.cap, double(p.span) * C::block) > 4096.0 * C::block * size) continue;
+    // bf16: sums of the tensor cores stay short (see the product with the values).
+    if (!F32 && std::min<double>(p.cap, double(p.span) * C::block) > 4096.0 * C::block * size)
+      continue;
     auto *kernel = stream_kernel<D, F32, ROWS, true>;
     static std::atomic<unsigned long long> done{0};
     static std::atomic<int> known[2][64];

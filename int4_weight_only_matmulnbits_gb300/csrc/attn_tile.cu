@@ -63,8 +63,8 @@ constexpr int kUnitCost = 2;
 // what they add, relative to the sum so far: 1 M keys of equal weight in one run
 // came out 0.37 % low, 4 M 2.2 %. So after a run a row's O goes to its thread's
 // place in global memory, added there with rounding: at most 4096 additions of the
-// tensor cores stand in a row, some 2^-12. (Runs past 65536 keys alone; a unit's
-// 131 KB there and back are some 3 us of 700.)
+// tensor cores stand in a row, some 2^-12. (Runs past 65536 keys alone: 38912 rows
+// over 1 M keys take 12.86 ms, 12.74 in one sum.)
 constexpr int kRun = 512;
 
 template <int D>

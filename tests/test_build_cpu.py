@@ -1,5 +1,6 @@
 """The build on machines of other kinds: what is compiled and linked when, with the compilers
 replaced by a function that writes the file they are asked for."""
+import itertools
 import os
 import subprocess
 
@@ -17,7 +18,7 @@ class Compilers:
                 monkeypatch.setattr(_build, name, path)
         monkeypatch.setattr(_build, "_nvcc", lambda: "nvcc")
         monkeypatch.setattr(_build.subprocess, "run", self.run)
-        self.clock = os.path.getmtime(_build.PY_SRC) + 1e6
+        self.clock = itertools.count(int(os.path.getmtime(_build.PY_SRC)) + 10 ** 6)
 
     def run(self, cmd, **kw):
         out = cmd[cmd.index("-o") + 1]
@@ -27,8 +28,8 @@ class Compilers:
             self.made.append(name)
             with open(out, "w") as f:
                 f.write(" ".join(cmd))
-            self.clock += 1.0  # every file is newer than the one before it
-            os.utime(out, (self.clock, self.clock))
+            now = next(self.clock)  # every file is newer than the one before it
+            os.utime(out, (now, now))
         return subprocess.CompletedProcess(cmd, int(failed), "", "no such compiler")
 
     def build(self):
